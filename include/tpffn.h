@@ -61,7 +61,9 @@ enum {
   TP_ERR_UNSUPPORTED = 2,  /* valid request this build does not implement   */
   TP_ERR_CUDA = 3,         /* a CUDA call or kernel launch failed           */
   TP_ERR_TIMEOUT = 4,      /* a device-side bounded wait expired            */
-  TP_ERR_ALIGN = 5         /* pointer not 16-byte aligned                    */
+  TP_ERR_ALIGN = 5,        /* pointer not 16-byte aligned                    */
+  TP_ERR_BATCH = 6         /* a cache batch's device arrays held a page,
+                              offset or length that is out of range          */
 };
 
 /* Activation between the two matrices. */
@@ -352,6 +354,114 @@ TPFFN_API int tp_attn_core_bwd(const tp_attn_plan* plan, int64_t B, int64_t S, c
 /* Diagnostics of attention calls, as their tp_ffn_* counterparts. */
 TPFFN_API int tp_attn_kernel_times(const tp_attn_plan* plan, int max, const char** names, float* ms);
 TPFFN_API int tp_attn_last_launch_count(const tp_attn_plan* plan);
+
+/* --------------------------------------------- attention with a key/value cache
+ *
+ * Serving: the keys and values of earlier tokens stay in a cache of pages, and
+ * each call brings the new tokens of a batch of sequences (one per sequence
+ * while text is generated, a few when proposed tokens are verified, a whole
+ * prompt or a chunk of one at first).
+ *
+ * Cache: `k` and `v`, each [n_pages][n_kv_heads][page_size][head_dim] bf16.
+ * page_size is a power of two from 8 to 1024.
+ * Batch (device arrays of int32):
+ *   cu_tokens  [n_seqs + 1]  sequence b's new tokens are the rows
+ *              cu_tokens[b] .. cu_tokens[b + 1] - 1 of every [n_tokens][...]
+ *              buffer; ascending from 0.  Rows behind cu_tokens[n_seqs] are
+ *              nobody's (padding): they are not read and left as they were.
+ *   kv_len     [n_seqs]  keys of the sequence with the new tokens, whose
+ *              positions are the last ones: kv_len[b] - q .. kv_len[b] - 1
+ *   page_table [n_seqs][max_pages]  key j lies in page page_table[b][j /
+ *              page_size], slot j % page_size.  Entries behind the last key
+ *              are not read.
+ * max_new (a host number) bounds the new tokens of any one sequence; n_tokens
+ * and max_new decide on the launches, so a captured graph serves every batch
+ * within them.  A sequence may have no new tokens, and no keys.
+ * What the device arrays hold is brought into range before it is used: a page
+ * outside the cache is neither written nor read (its keys count as zeros),
+ * a row or length outside its bounds is cut; what is computed for such a
+ * sequence is unspecified, nothing else is touched, and
+ * tp_attn_kv_last_device_error reports TP_ERR_BATCH.  Pages of two sequences
+ * may coincide where only one or neither of them appends.
+ */
+typedef struct tp_kv_cache {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int64_t page_size;
+} tp_kv_cache;
+
+typedef struct tp_kv_batch {
+  int64_t n_seqs, n_tokens, max_new, max_pages;
+  const int32_t* cu_tokens;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+} tp_kv_batch;
+
+/* Rotation of queries and keys by position: with theta_j = t * inv_freq[j]
+ * (formed in 64 bits) for a token at position t, the pair (x, y) of columns
+ * (j, j + rotary_dim/2), or (2j, 2j + 1) when interleaved, becomes
+ * ((x cos - y sin) * scale, (y cos + x sin) * scale), j < rotary_dim/2; the
+ * other columns pass.  inv_freq: device fp32 [rotary_dim/2]; rotary_dim: a
+ * multiple of 16 up to head_dim, 0 for no rotation (inv_freq may be NULL). */
+typedef struct tp_kv_rotation {
+  const float* inv_freq;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float scale;
+} tp_kv_rotation;
+
+/* Workspace of one call (queried on the device that runs it): `call` is
+ * TP_KV_APPEND, TP_KV_ATTEND or TP_KV_DECODE; shared_len and flags as for the
+ * call (0 where it has none).  0 for arguments that the call would refuse.
+ * Calls that may run at the same time need workspaces of their own. */
+enum { TP_KV_APPEND = 0, TP_KV_ATTEND = 1, TP_KV_DECODE = 2 };
+TPFFN_API size_t tp_attn_kv_workspace_bytes(const tp_attn_plan* plan, const tp_kv_batch* batch, int64_t page_size,
+                                            int64_t shared_len, int call, int flags);
+
+/* Append: from the packed projections qkv [n_tokens][qkv_width] of the new
+ * tokens, stores the rotated keys and the values in their pages and writes
+ * the rotated queries to q [n_tokens][H*hd] (head h in columns
+ * [h*hd, (h+1)*hd)).  rotation NULL: none.  A token whose position is
+ * negative (more new tokens than kv_len) has no place: its q row is zero and
+ * nothing is stored.  One launch; flags: TP_FLAG_SYNC, TP_FLAG_TIMING.
+ * Errors: TP_ERR_INVALID (NULL, sizes, workspace too small, rotary_dim),
+ * TP_ERR_UNSUPPORTED (page_size; n_tokens or n_seqs above 2^24),
+ * TP_ERR_ALIGN.  n_tokens or n_seqs 0: TP_OK, no work. */
+TPFFN_API int tp_attn_kv_append(const tp_attn_plan* plan, const tp_kv_cache* cache, const tp_kv_batch* batch,
+                                const tp_kv_rotation* rotation, const void* qkv, void* q, void* workspace,
+                                size_t workspace_bytes, int flags, tp_stream_t stream);
+
+/* Attention of q [n_tokens][H*hd] over the cache: new token i of sequence b
+ * (position t) sees keys 0 .. t (causal plans) or all kv_len[b] keys.
+ * o [n_tokens][H*hd]; lse [n_tokens][H] fp32 or NULL: log2 of
+ * sum_j 2^(s_ij log2 e), as in tp_attn_core_fwd.  A row that sees no key gets
+ * o = 0 and lse = -inf.  Cached keys and values that a row does not see must
+ * still be finite where they belong to its sequence; slots behind kv_len may
+ * hold anything.
+ * shared_len > 0: the first shared_len keys of all sequences are the same
+ * (their page table rows name the same pages, or pages of the same contents,
+ * there); they are attended to once for the rows of all sequences together,
+ * read through the table row of the longest sequence.  The result is that
+ * of shared_len = 0 up to rounding.  0 <= shared_len <= max_pages * page_size.
+ * Results do not change from run to run.  Errors as tp_attn_kv_append. */
+TPFFN_API int tp_attn_paged_fwd(const tp_attn_plan* plan, const tp_kv_cache* cache, const tp_kv_batch* batch,
+                                int64_t shared_len, const void* q, void* o, float* lse, void* workspace,
+                                size_t workspace_bytes, int flags, tp_stream_t stream);
+
+/* The sublayer's serving pass: y [n_tokens][d] from x [n_tokens][d] --
+ * q/k/v projections, tp_attn_kv_append, tp_attn_paged_fwd and the row-sharded
+ * output projection with its ordered shard-sum (flags: TP_SUM_* as in
+ * tp_attn_fwd).  Rows of y behind cu_tokens[n_seqs] are unspecified. */
+TPFFN_API int tp_attn_decode_fwd(const tp_attn_plan* plan, const tp_kv_cache* cache, const tp_kv_batch* batch,
+                                 const tp_kv_rotation* rotation, int64_t shared_len, const void* x,
+                                 const void* wqkv, const void* wo_packed, void* y, void* workspace,
+                                 size_t workspace_bytes, int flags, tp_stream_t stream);
+
+/* Wait for the stream, then read what the last of these calls on this
+ * workspace reported: TP_OK, TP_ERR_BATCH, TP_ERR_TIMEOUT or TP_ERR_CUDA.
+ * Only after a call that enqueued work. */
+TPFFN_API int tp_attn_kv_last_device_error(const tp_attn_plan* plan, const void* workspace, tp_stream_t stream);
 
 /* ------------------------------------------------ forward without allocation */
 

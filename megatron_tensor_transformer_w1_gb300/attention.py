@@ -8,6 +8,7 @@ in libtpffn.so ("7.9 Tensor and pipeline parallelism (TP, PP)", §2.2
     wqkv, wo = attn.pack(Wq, Wk, Wv, Wo)
     y, saved = attn.forward(x, B, S, wqkv, wo)
     g = attn.backward(x, B, S, wqkv, wo, saved, dy)   # dx, dwqkv, dwo
+    y = attn.decode(x, cache, batch, wqkv, wo)        # serving, over a kv_cache.PagedKVCache
 """
 from __future__ import annotations
 
@@ -93,6 +94,15 @@ class TensorParallelAttention:
         abi.check(abi.tp_attn_bwd(self.plan, B, S, x, wqkv, wo, saved, dy, dx, dwqkv, dwo, ws, ws.numel(), flags,
                                   self._stream()), "tp_attn_bwd")
         return dict(dx=dx, dwqkv=dwqkv, dwo=dwo)
+
+    def decode(self, x, cache, batch, wqkv, wo, shared_len=0, fused=False, overlap=False, flags=0):
+        """Serving pass over a PagedKVCache of this sublayer: projects the new tokens
+        x [n_tokens, d] of a batch, appends their keys and values, attends to the
+        cache and projects the head outputs: y [n_tokens, d]."""
+        if cache.attn is not self:
+            raise ValueError("the cache belongs to another attention sublayer")
+        flags |= (abi.TP_SUM_FUSED if fused else 0) | (abi.TP_SUM_OVERLAP if overlap else 0)
+        return cache.decode(x, batch, wqkv, wo, shared_len, flags=flags)
 
     def core_forward(self, qkv, B, S, flags=0):
         o = torch.empty(B * S, self.H * self.hd, dtype=torch.bfloat16, device=self.device)

@@ -23,6 +23,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <initializer_list>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <string>
@@ -394,6 +395,7 @@ const char* tp_ffn_status_string(int status) {
     case TP_ERR_CUDA: return "TP_ERR_CUDA: CUDA call or kernel launch failed";
     case TP_ERR_TIMEOUT: return "TP_ERR_TIMEOUT: a device-side bounded wait expired";
     case TP_ERR_ALIGN: return "TP_ERR_ALIGN: pointer or stride not 16-byte aligned";
+    case TP_ERR_BATCH: return "TP_ERR_BATCH: a cache batch held a page, offset or length that is out of range";
     default: return "unknown status";
   }
 }
@@ -1128,6 +1130,31 @@ AttnSpec attn_spec(const tp_attn_plan* a, int64_t B, int64_t S) {
   return sp;
 }
 
+// q, k, v of every shard: one GEMM over the shard-major packed weight.
+// wo_ws: the W_O forward's workspace, whose last-wave region is free until
+// that GEMM runs.
+int qkv_proj(const tp_attn_plan* a, int64_t n, const void* x, const void* wqkv, void* qkv, char* wo_ws, int flags,
+             LaunchCtx& ctx) {
+  GemmSpec g;
+  g.name = "qkv_proj";
+  g.M = n;
+  g.N = a->W;
+  g.K = a->d;
+  g.A = kmajor(x, a->d, n, 1, a->d, n * a->d, 0, 0);
+  g.B = kmajor(wqkv, a->d, a->W, 1, a->d, a->W * a->d, 0, 0);
+  g.epi = EPI_OUT;
+  g.out = qkv;
+  g.out_rs = a->W;
+  g.n_store = a->W;
+  g.out_bf16 = 1;
+  const WsLayout WL = ws_layout(a->wo, n, flags);
+  if (WL.has_tail) {
+    g.tail_ws = reinterpret_cast<float*>(wo_ws + WL.tail);
+    g.tail_ws_bytes = WL.tail_bytes;
+  }
+  return run_gemm(a->wo, g, ctx);
+}
+
 int attn_check(const tp_attn_plan* a, int64_t B, int64_t S, size_t ws_bytes, const void* workspace, int flags,
                std::initializer_list<const void*> ptrs) {
   if (!a || B < 0 || S < 0 || !workspace) return TP_ERR_INVALID;
@@ -1246,28 +1273,7 @@ int tp_attn_fwd(const tp_attn_plan* a, int64_t B, int64_t S, const void* x, cons
   const AttnWs L = attn_ws(a, B, S, flags);
   char* sv = static_cast<char*>(saved);
   char* ws = static_cast<char*>(workspace);
-  // q, k, v of every shard: one GEMM over the shard-major packed weight
-  GemmSpec g;
-  g.name = "qkv_proj";
-  g.M = n;
-  g.N = a->W;
-  g.K = a->d;
-  g.A = kmajor(x, a->d, n, 1, a->d, n * a->d, 0, 0);
-  g.B = kmajor(wqkv, a->d, a->W, 1, a->d, a->W * a->d, 0, 0);
-  g.epi = EPI_OUT;
-  g.out = sv + SV.qkv;
-  g.out_rs = a->W;
-  g.n_store = a->W;
-  g.out_bf16 = 1;
-  {
-    // the W_O forward's last-wave region is free until that GEMM runs
-    const WsLayout WL = ws_layout(a->wo, n, flags);
-    if (WL.has_tail) {
-      g.tail_ws = reinterpret_cast<float*>(ws + L.wo + WL.tail);
-      g.tail_ws_bytes = WL.tail_bytes;
-    }
-  }
-  rc = run_gemm(a->wo, g, ctx);
+  rc = qkv_proj(a, n, x, wqkv, sv + SV.qkv, ws + L.wo, flags, ctx);
   if (!rc) {
     AttnSpec sp = attn_spec(a, B, S);
     sp.qkv = sv + SV.qkv;
@@ -1425,5 +1431,215 @@ int tp_attn_kernel_times(const tp_attn_plan* a, int max, const char** names, flo
 }
 
 int tp_attn_last_launch_count(const tp_attn_plan* a) { return a ? a->wo->last_launches : -1; }
+
+// --------------------------------------------- attention with a key/value cache
+namespace {
+constexpr int64_t kMaxKvTokens = int64_t(1) << 24;
+
+// Sizes of a batch that the launches go by; the device arrays are the kernels'
+// to check.  page_size, max_pages and shared_len bound one another.
+int kv_sizes(const tp_attn_plan* a, const tp_kv_batch* b, int64_t page_size, int64_t shared_len, KvSpec& sp) {
+  if (!a || !b || b->n_seqs < 0 || b->n_tokens < 0 || shared_len < 0 || page_size < 1) return TP_ERR_INVALID;
+  if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1))) return TP_ERR_UNSUPPORTED;
+  if (b->n_seqs > kMaxKvTokens || b->n_tokens > kMaxKvTokens) return TP_ERR_UNSUPPORTED;
+  if (b->n_seqs > 0 && b->n_tokens > 0 && (b->max_new < 1 || b->max_pages < 1)) return TP_ERR_INVALID;
+  if (b->max_pages > (int64_t(1) << 27)) return TP_ERR_UNSUPPORTED;
+  if (b->n_tokens * (a->H / a->Hkv) > INT32_MAX || b->n_seqs * a->Hkv > INT32_MAX) return TP_ERR_UNSUPPORTED;
+  sp.H = a->H;
+  sp.Hkv = a->Hkv;
+  sp.T_p = a->T_p;
+  sp.causal = a->causal;
+  sp.max_pages = b->max_pages;
+  sp.page_size = static_cast<int>(page_size);
+  sp.n_seqs = static_cast<int>(b->n_seqs);
+  sp.n_tokens = static_cast<int>(b->n_tokens);
+  sp.max_new = static_cast<int>(b->max_new < b->n_tokens ? b->max_new : b->n_tokens);
+  sp.cu = b->cu_tokens;
+  sp.kv_len = b->kv_len;
+  sp.table = b->page_table;
+  if (b->n_seqs > 0 && b->n_tokens > 0 && shared_len > kv_cap(sp)) return TP_ERR_INVALID;
+  sp.shared_len = static_cast<int>(shared_len);
+  return TP_OK;
+}
+
+bool aligned4(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0; }
+
+int kv_spec(const tp_attn_plan* a, const tp_kv_cache* c, const tp_kv_batch* b, int64_t shared_len, KvSpec& sp) {
+  if (!c) return TP_ERR_INVALID;
+  int rc = kv_sizes(a, b, c->page_size, shared_len, sp);
+  if (rc || sp.n_tokens == 0 || sp.n_seqs == 0) return rc;
+  if (!c->k || !c->v || c->n_pages < 1 || !b->cu_tokens || !b->kv_len || !b->page_table) return TP_ERR_INVALID;
+  if (c->n_pages > INT32_MAX) return TP_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(b->cu_tokens) || !aligned4(b->kv_len) ||
+      !aligned4(b->page_table))
+    return TP_ERR_ALIGN;
+  sp.k = c->k;
+  sp.v = c->v;
+  sp.n_pages = c->n_pages;
+  return TP_OK;
+}
+
+int kv_rotation(const tp_attn_plan* a, const tp_kv_rotation* r, KvRotation& out) {
+  if (!r || r->rotary_dim == 0) return TP_OK;
+  if (r->rotary_dim < 0 || r->rotary_dim > a->hd || r->rotary_dim % 16 || !r->inv_freq) return TP_ERR_INVALID;
+  if (!aligned4(r->inv_freq)) return TP_ERR_ALIGN;
+  out.inv_freq = r->inv_freq;
+  out.rotary_dim = r->rotary_dim;
+  out.interleaved = r->interleaved ? 1 : 0;
+  out.scale = r->scale;
+  return TP_OK;
+}
+
+int kv_pointers(void* workspace, size_t have, size_t need, std::initializer_list<const void*> ptrs) {
+  if (!workspace || have < need) return TP_ERR_INVALID;
+  for (const void* q : ptrs) {
+    if (!q) return TP_ERR_INVALID;
+    if (!aligned16(q)) return TP_ERR_ALIGN;
+  }
+  return aligned16(workspace) ? TP_OK : TP_ERR_ALIGN;
+}
+
+void kv_ctx(const tp_attn_plan* a, void* workspace, int flags, cudaStream_t stream, LaunchCtx& ctx) {
+  // no error word to clear: every block writes its own status word
+  ctx.stream = stream;
+  ctx.err = static_cast<int*>(workspace);
+  ctx.num_sms = num_sms_current();
+  ctx.timing = (flags & TP_FLAG_TIMING) != 0;
+  if (ctx.timing) {
+    a->wo->timing_stream = stream;
+    ctx.before = timing_before;
+    ctx.after = timing_after;
+    ctx.user = a->wo;
+  }
+}
+
+int kv_finish(const tp_attn_plan* a, LaunchCtx& ctx, int rc, int flags, void* workspace) {
+  a->wo->last_launches = ctx.launches;
+  if (rc != TP_OK) return rc;
+  if (cudaPeekAtLastError() != cudaSuccess) return TP_ERR_CUDA;
+  if (flags & TP_FLAG_SYNC)
+    return tp_attn_kv_last_device_error(a, workspace, reinterpret_cast<tp_stream_t>(ctx.stream));
+  return TP_OK;
+}
+
+struct DecodeWs {
+  size_t attend = 0, wo = 0, qkv = 0, q = 0, c = 0, total = 0;
+};
+DecodeWs decode_ws(const tp_attn_plan* a, const KvSpec& sp, int flags) {
+  DecodeWs L;
+  const size_t n = static_cast<size_t>(sp.n_tokens);
+  size_t off = align_up(kKvHeaderBytes);
+  L.attend = off;
+  off += align_up(kv_attend_scratch_bytes(sp, num_sms_current()));
+  L.wo = off;
+  off += align_up(ws_layout(a->wo, sp.n_tokens, flags).total);
+  L.qkv = off;
+  off += align_up(n * a->W * 2);
+  L.q = off;
+  off += align_up(n * a->H * a->hd * 2);
+  L.c = off;
+  off += align_up(n * a->H * a->hd * 2);
+  L.total = off;
+  return L;
+}
+}  // namespace
+
+size_t tp_attn_kv_workspace_bytes(const tp_attn_plan* a, const tp_kv_batch* batch, int64_t page_size,
+                                  int64_t shared_len, int call, int flags) {
+  KvSpec sp;
+  if (kv_sizes(a, batch, page_size, shared_len, sp)) return 0;
+  switch (call) {
+    case TP_KV_APPEND: return align_up(kKvHeaderBytes);
+    case TP_KV_ATTEND: return align_up(kKvHeaderBytes) + kv_attend_scratch_bytes(sp, num_sms_current());
+    case TP_KV_DECODE: return decode_ws(a, sp, flags).total;
+    default: return 0;
+  }
+}
+
+int tp_attn_kv_append(const tp_attn_plan* a, const tp_kv_cache* cache, const tp_kv_batch* batch,
+                      const tp_kv_rotation* rotation, const void* qkv, void* q, void* workspace,
+                      size_t workspace_bytes, int flags, tp_stream_t stream) {
+  KvSpec sp;
+  KvRotation rot;
+  int rc = kv_spec(a, cache, batch, 0, sp);
+  if (!rc) rc = kv_rotation(a, rotation, rot);
+  if (rc) return rc;
+  if (sp.n_tokens == 0 || sp.n_seqs == 0) {
+    a->wo->last_launches = 0;
+    return TP_OK;
+  }
+  if ((rc = kv_pointers(workspace, workspace_bytes, align_up(kKvHeaderBytes), {qkv, q}))) return rc;
+  LaunchCtx ctx;
+  kv_ctx(a, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
+  rc = launch_kv_append(sp, rot, qkv, q, static_cast<int*>(workspace), true, ctx);
+  return kv_finish(a, ctx, rc, flags, workspace);
+}
+
+int tp_attn_paged_fwd(const tp_attn_plan* a, const tp_kv_cache* cache, const tp_kv_batch* batch, int64_t shared_len,
+                      const void* q, void* o, float* lse, void* workspace, size_t workspace_bytes, int flags,
+                      tp_stream_t stream) {
+  KvSpec sp;
+  int rc = kv_spec(a, cache, batch, shared_len, sp);
+  if (rc) return rc;
+  if (sp.n_tokens == 0 || sp.n_seqs == 0) {
+    a->wo->last_launches = 0;
+    return TP_OK;
+  }
+  const size_t head = align_up(kKvHeaderBytes);
+  const int sms = num_sms_current();
+  if ((rc = kv_pointers(workspace, workspace_bytes, head + kv_attend_scratch_bytes(sp, sms), {q, o}))) return rc;
+  if (!aligned4(lse)) return TP_ERR_ALIGN;
+  LaunchCtx ctx;
+  kv_ctx(a, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
+  rc = launch_kv_attend(sp, q, o, lse, static_cast<int*>(workspace), true, static_cast<char*>(workspace) + head, ctx);
+  return kv_finish(a, ctx, rc, flags, workspace);
+}
+
+int tp_attn_decode_fwd(const tp_attn_plan* a, const tp_kv_cache* cache, const tp_kv_batch* batch,
+                       const tp_kv_rotation* rotation, int64_t shared_len, const void* x, const void* wqkv,
+                       const void* wo_packed, void* y, void* workspace, size_t workspace_bytes, int flags,
+                       tp_stream_t stream) {
+  KvSpec sp;
+  KvRotation rot;
+  int rc = kv_spec(a, cache, batch, shared_len, sp);
+  if (!rc) rc = kv_rotation(a, rotation, rot);
+  if (rc) return rc;
+  if ((flags & TP_SUM_FUSED) && (flags & TP_SUM_OVERLAP)) return TP_ERR_INVALID;
+  if (sp.n_tokens == 0 || sp.n_seqs == 0) {
+    a->wo->last_launches = 0;
+    return TP_OK;
+  }
+  const DecodeWs L = decode_ws(a, sp, flags);
+  if ((rc = kv_pointers(workspace, workspace_bytes, L.total, {x, wqkv, wo_packed, y}))) return rc;
+  LaunchCtx ctx;
+  rc = make_ctx(a->wo, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
+  if (rc) return rc;
+  const int64_t n = sp.n_tokens;
+  char* ws = static_cast<char*>(workspace);
+  rc = qkv_proj(a, n, x, wqkv, ws + L.qkv, ws + L.wo, flags, ctx);
+  if (!rc) rc = launch_kv_append(sp, rot, ws + L.qkv, ws + L.q, static_cast<int*>(workspace), false, ctx);
+  if (!rc)
+    rc = launch_kv_attend(sp, ws + L.q, ws + L.c, nullptr, static_cast<int*>(workspace), false, ws + L.attend, ctx);
+  if (!rc)
+    rc = fwd_impl(a->wo, n, ws + L.c, nullptr, wo_packed, nullptr, nullptr, y, nullptr, nullptr, ws + L.wo, flags,
+                  ctx, nullptr);
+  return kv_finish(a, ctx, rc, flags, workspace);
+}
+
+int tp_attn_kv_last_device_error(const tp_attn_plan* a, const void* workspace, tp_stream_t stream) {
+  if (!a || !workspace) return TP_ERR_INVALID;
+  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return TP_ERR_CUDA;
+  std::unique_ptr<int[]> words(new (std::nothrow) int[kKvHeaderBytes / sizeof(int)]);
+  if (!words) return TP_ERR_INVALID;
+  if (cudaMemcpy(words.get(), workspace, kKvHeaderBytes, cudaMemcpyDeviceToHost) != cudaSuccess) return TP_ERR_CUDA;
+  int all = words[0];
+  for (int part = 0; part < 2; ++part) {
+    const int n = words[1 + part] < kKvStatusWords ? words[1 + part] : kKvStatusWords;
+    for (int i = 0; i < n; ++i) all |= words[kKvHeaderWords + part * kKvStatusWords + i];
+  }
+  if (all & DEV_ERR_TIMEOUT) return TP_ERR_TIMEOUT;
+  if (all & DEV_ERR_BATCH) return TP_ERR_BATCH;
+  return all ? TP_ERR_CUDA : TP_OK;
+}
 
 }  // extern "C"

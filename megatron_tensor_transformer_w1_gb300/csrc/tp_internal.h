@@ -101,6 +101,7 @@ struct RowSlices {
 
 // Device error bits.
 constexpr int DEV_ERR_TIMEOUT = 1;
+constexpr int DEV_ERR_BATCH = 2;  // a page, offset or length of a cache batch is out of range
 
 // tensor-core GEMM (tp_gemm_tc.cu). Returns 0 or a TP_ERR_* code.
 int launch_tc_gemm(const GemmSpec& s, LaunchCtx& ctx);
@@ -201,5 +202,39 @@ int launch_attn_bwd(const AttnSpec& a, LaunchCtx& ctx);
 // (unpack = 1 reverses it).
 int launch_pack_qkv(const void* Wq, const void* Wk, const void* Wv, void* packed, int T_p, int64_t sq, int64_t sk,
                     int64_t d, int unpack, cudaStream_t st);
+
+// Serving operators over a paged key/value cache (tp_kv.cu): pages
+// [n_pages][Hkv][page_size][128] of keys and of values (bf16), a page table
+// row per sequence, the new tokens of sequence b in rows cu[b] .. cu[b+1]-1,
+// kv_len[b] keys with the new ones.
+struct KvSpec {
+  int H = 0, Hkv = 0, T_p = 1, causal = 1;
+  void *k = nullptr, *v = nullptr;
+  int64_t n_pages = 0, max_pages = 0;
+  int page_size = 0;
+  int n_seqs = 0, n_tokens = 0, max_new = 0;
+  int shared_len = 0;   // leading keys that all sequences have in the same pages
+  const int *cu = nullptr, *kv_len = nullptr, *table = nullptr;
+};
+struct KvRotation {
+  const float* inv_freq = nullptr;
+  float scale = 1.f;
+  int rotary_dim = 0, interleaved = 0;
+};
+// Status words, one per block, written by every block (so that no call has to
+// clear them): kKvStatusWords for the append, as many for the attention, after
+// kKvHeaderWords words {error word of the GEMMs, blocks of the append, blocks
+// of the attention}.
+constexpr int kKvHeaderWords = 64, kKvStatusWords = 2048;
+constexpr size_t kKvHeaderBytes = (kKvHeaderWords + 2 * kKvStatusWords) * sizeof(int);
+// Keys that a row of the page table can hold.
+int kv_cap(const KvSpec& a);
+// `header`: kKvHeaderBytes; `alone`: not part of a call that keeps the other
+// words of the header.
+int launch_kv_append(const KvSpec& a, const KvRotation& r, const void* qkv, void* q, int* header, bool alone,
+                     LaunchCtx& ctx);
+size_t kv_attend_scratch_bytes(const KvSpec& a, int num_sms);
+int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* header, bool alone, void* scratch,
+                     LaunchCtx& ctx);
 
 }  // namespace tpffn

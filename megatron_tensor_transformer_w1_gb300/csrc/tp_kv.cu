@@ -1,0 +1,1021 @@
+// tp_kv.cu -- the serving operators of the head-sharded attention sublayer:
+// appending the new tokens' keys and values to a paged cache, with the
+// rotation by position, and attention of few query rows over that cache.
+//
+// Sequence b of a batch has new tokens in rows cu[b] .. cu[b+1] - 1 and
+// kv_len[b] keys, the new tokens' included; key j lies in page
+// page_table[b][j / page_size], slot j % page_size.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "tc_ptx.cuh"
+#include "tp_internal.h"
+#include "tp_kv.cuh"
+#include "tpffn.h"
+
+namespace tpffn {
+namespace kv {
+using tc::grid_dep_launch;
+using tc::grid_dep_wait;
+using tc::pack_bf16x2;
+using tc::smem_u32;
+
+// ================================================================ append
+// A token at position t turns the pairs (x_j, y_j) of each of its query and
+// key heads by the angle t * inv_freq[j]:
+//   x' = (x cos - y sin) scale,  y' = (y cos + x sin) scale,
+// pairs (j, j + r/2) or, interleaved, (2j, 2j + 1), for the first r columns.
+// The angle is formed in turns in 64 bits and reduced to (-1/2, 1/2] turn
+// before it is rounded to 32 (a float product t * f loses the angle of far
+// positions), once per token and pair: all heads of the token share it.
+// Bound by memory: every element is read once and written once.
+struct AppendParams {
+  Batch b;
+  const __nv_bfloat16* qkv;
+  __nv_bfloat16* q;
+  const float* inv_freq;
+  float scale;
+  int rot, interleaved;
+  int hq_per, hk_per;  // query / key heads per shard
+  int* header;         // see kKvHeaderBytes
+  int alone;
+};
+
+__device__ __forceinline__ float2 unpack_bf16x2(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+
+__device__ __forceinline__ void turn_pair(uint32_t& wa, uint32_t& wb, const float2* cs) {
+  // two pairs: the low and the high halves of the two words
+  const float2 a = unpack_bf16x2(wa), b = unpack_bf16x2(wb);
+  const float2 c0 = cs[0], c1 = cs[1];
+  wa = pack_bf16x2(a.x * c0.x - b.x * c0.y, a.y * c1.x - b.y * c1.y);
+  wb = pack_bf16x2(b.x * c0.x + a.x * c0.y, b.y * c1.x + a.y * c1.y);
+}
+
+constexpr int APPEND_THREADS = 256;
+
+__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendParams p) {
+  __shared__ float2 cs[HD / 2];
+  __shared__ int s_err;
+  if (threadIdx.x == 0) s_err = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  const Batch& B = p.b;
+  const int per = p.hq_per + 2 * p.hk_per, heads = B.H + 2 * B.Hkv;
+  const int half = p.rot / 16;  // 16-byte chunks of half the rotated columns
+  int err = 0;
+  for (int row = blockIdx.x; row < B.n_tokens; row += gridDim.x) {
+    const int b = find_seq_warp(B.cu, B.B, row);
+    if (b >= B.B || B.cu[b] > row || B.cu[b] < 0) continue;  // no sequence's row: left as it is
+    const int pos = B.kv_len[b] - (B.cu[b + 1] - row);
+    long long page = -1;
+    if (pos >= 0 && pos < B.cap) {
+      page = B.table[static_cast<long long>(b) * B.max_pages + (pos >> B.page_shift)];
+      if (page >= B.n_pages) page = -1;
+    }
+    if (page < 0 || B.cu[b + 1] > B.n_tokens) err = DEV_ERR_BATCH;
+    __syncthreads();  // the previous token's angles have been read
+    if (threadIdx.x < p.rot / 2) {
+      const double turns = static_cast<double>(pos) * static_cast<double>(p.inv_freq[threadIdx.x]) *
+                           0.15915494309189533577;  // 1 / (2 pi)
+      float s, c;
+      sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+      cs[threadIdx.x] = make_float2(c * p.scale, s * p.scale);
+    }
+    __syncthreads();
+    const uint4* src = reinterpret_cast<const uint4*>(p.qkv + static_cast<long long>(row) * heads * HD);
+    const int slot = pos & ((1 << B.page_shift) - 1);
+    // 8 units of two 16-byte chunks per head: the two chunks of 8 pairs
+    // (first half, second half), or two neighbours
+    for (int u = threadIdx.x; u < heads * 8; u += APPEND_THREADS) {
+      const int hh = u >> 3, k = u & 7;
+      const int t = hh / per, w = hh - t * per;
+      int ca = 2 * k, cb = 2 * k + 1;
+      const bool turned = w < p.hq_per + p.hk_per;
+      if (!p.interleaved) {
+        if (k < half) {
+          ca = k;
+          cb = k + half;
+        } else {
+          ca = 2 * k;  // 2 half + 2 (k - half): the columns past the rotated ones
+          cb = ca + 1;
+        }
+      }
+      uint4 a = src[hh * 16 + ca], c = src[hh * 16 + cb];
+      if (turned) {
+        if (p.interleaved) {
+          if (ca * 8 < p.rot) {
+            uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
+            uint32_t* wc = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = unpack_bf16x2(wa[i]), y = unpack_bf16x2(wc[i]);
+              const float2 f = cs[ca * 4 + i], g = cs[cb * 4 + i];
+              wa[i] = pack_bf16x2(x.x * f.x - x.y * f.y, x.y * f.x + x.x * f.y);
+              wc[i] = pack_bf16x2(y.x * g.x - y.y * g.y, y.y * g.x + y.x * g.y);
+            }
+          }
+        } else if (k < half) {
+          turn_pair(a.x, c.x, cs + 8 * k);
+          turn_pair(a.y, c.y, cs + 8 * k + 2);
+          turn_pair(a.z, c.z, cs + 8 * k + 4);
+          turn_pair(a.w, c.w, cs + 8 * k + 6);
+        }
+      }
+      __nv_bfloat16* dst;
+      if (w < p.hq_per) {
+        dst = p.q + (static_cast<long long>(row) * B.H + t * p.hq_per + w) * HD;
+        if (pos < 0) a = c = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        if (page < 0) continue;
+        const bool is_k = w < p.hq_per + p.hk_per;
+        const int h = t * p.hk_per + (is_k ? w - p.hq_per : w - p.hq_per - p.hk_per);
+        dst = (is_k ? B.k : B.v) + ((((page * B.Hkv + h) << B.page_shift) + slot) * HD);
+      }
+      reinterpret_cast<uint4*>(dst)[ca] = a;
+      reinterpret_cast<uint4*>(dst)[cb] = c;
+    }
+  }
+  if (err) atomicOr(&s_err, err);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.header[kKvHeaderWords + blockIdx.x] = s_err;
+    if (blockIdx.x == 0) {
+      p.header[1] = gridDim.x;
+      if (p.alone) p.header[0] = p.header[2] = 0;
+    }
+  }
+}
+
+// ================================================================ few rows
+// Attention of at most 16 WR query rows per item over the cache.  An item is
+// a key/value head of a sequence, its rows the sequence's new tokens times
+// the G query heads of the group (so K and V are read once for the group);
+// or, for the shared keys, a key/value head with the rows of every sequence.
+// Its floor is the one read of K and V from memory, 512 bytes per key.
+//
+// Work is cut in tiles of 64 keys and every block takes the same number of
+// consecutive tiles of the whole batch, however the lengths differ; a block
+// starts and ends inside an item, and the parts of an item (its running
+// maximum, sum and unnormalised output) are joined by kv_combine_kernel.
+//
+// One block: 4 warps, three stages of a tile's K and V (32 KB) filled by
+// 16-byte asynchronous copies, so that two blocks per SM keep some 128 KB in
+// flight.  4 / WR key groups of warps: a warp takes 16 query rows and 16 WR
+// keys of a tile with its own running maximum and sum (no exchange per
+// tile); the groups meet at the end of a segment.  The products are m16n8k16
+// matrix instructions on registers: with at most 64 rows to a key they take
+// less time than the bytes do, and the 128-row tensor-memory products would
+// be mostly empty.
+template <int WR>
+struct Few {
+  static constexpr int WK = 4 / WR;           // key groups
+  static constexpr int ROWS = 16 * WR;
+  static constexpr int NB = WR;               // 16-key blocks of a warp per tile
+  static constexpr int STAGES = WR == 4 ? 2 : 3;
+  static constexpr int KV_BYTES = KT * HD * 2;
+  static constexpr int Q_BYTES = ROWS * HD * 2;
+  static constexpr int STAGE = 2 * KV_BYTES + Q_BYTES;
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+};
+
+struct FewParams {
+  Batch b;
+  const __nv_bfloat16* q;  // [n_tokens][H * HD]
+  __nv_bfloat16* o;        // [n_tokens][H * HD]
+  float* lse;              // [n_tokens][H] or null
+  float* part_o;           // [slots][rows][HD]
+  float2* part_ml;         // [slots][rows]
+  long long* sched;        // [B + 1] tiles per key/value head before sequence b
+  int rows;                // rows of a slot
+  float scale_log2;
+  int* status;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16-byte chunk c of row r of a tile with 256-byte rows: eight rows' chunks
+// of one column fall into different banks
+__device__ __forceinline__ uint32_t tile_chunk(uint32_t tile, int r, int c) {
+  return tile + static_cast<uint32_t>(r * 256 + ((c ^ (r & 7)) << 4));
+}
+
+// Where a block's copies stand: sequence, head, tile of the item.
+struct Cursor {
+  int b, h, t, t0, nt;  // tile t of [0, nt) holds the keys from (t0 + t) * KT on
+  Seq s;
+};
+
+// Prefix items: all sequences' rows as one, over the shared keys.
+template <bool PREFIX>
+__device__ __forceinline__ int tiles_of(const Batch& p, const Seq& s, int& t0) {
+  t0 = PREFIX ? 0 : p.shared / KT;
+  const int lo = PREFIX ? 0 : p.shared;
+  return (s.qn > 0 && s.kv > lo) ? (s.kv + KT - 1) / KT - t0 : 0;
+}
+
+struct Sched {
+  long long total;   // tiles of all items
+  long long blocks;  // blocks that get any: min(gridDim.x, total)
+  int table_row;     // whose page table leads to the shared pages
+};
+
+// Sums the tiles of all sequences, finds the block's first tile and, in
+// block 0, leaves the prefix sums for the combine kernel.  128 threads.
+template <bool PREFIX>
+__device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Cursor& c, long long& first,
+                                          long long& last, int* err) {
+  __shared__ long long sums[128];
+  __shared__ int s_best[128], s_len[128];
+  __shared__ int s_b;
+  __shared__ long long s_before;
+  const int tid = threadIdx.x;
+  Sched S{};
+  if constexpr (PREFIX) {
+    // the longest sequence's table covers the shared pages if any does
+    int best = 0, len = -1;
+    for (int b = tid; b < p.B; b += 128) {
+      const int l = min(max(p.kv_len[b], 0), p.cap);
+      if (l > len) { len = l; best = b; }
+    }
+    s_best[tid] = best;
+    s_len[tid] = len;
+    __syncthreads();
+    for (int d = 64; d; d >>= 1) {
+      if (tid < d) {
+        const int ol = s_len[tid + d], ob = s_best[tid + d];
+        if (ol > s_len[tid] || (ol == s_len[tid] && ob < s_best[tid])) { s_len[tid] = ol; s_best[tid] = ob; }
+      }
+      __syncthreads();
+    }
+    S.table_row = s_best[0];
+    c.s.q0 = 0;
+    c.s.qn = min(max(p.cu[p.B], 0), p.n_tokens);
+    c.s.kv = min(p.shared, s_len[0]);
+    c.nt = tiles_of<true>(p, c.s, c.t0);
+    S.total = static_cast<long long>(c.nt) * p.Hkv;
+    if (blockIdx.x == 0 && tid == 0) {
+      sched[0] = 0;
+      sched[1] = c.nt;
+    }
+    c.b = 0;
+    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
+    if (blockIdx.x >= S.blocks) { first = last = 0; return S; }
+    first = first_tile(blockIdx.x, S.total, S.blocks);
+    last = first_tile(blockIdx.x + 1, S.total, S.blocks);
+    c.h = static_cast<int>(first / c.nt);
+    c.t = static_cast<int>(first - static_cast<long long>(c.h) * c.nt);
+    return S;
+  } else {
+    const int per = (p.B + 127) / 128;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      int t0;
+      const Seq s = load_seq(p, b);
+      *err |= s.err;
+      sum += tiles_of<false>(p, s, t0);
+    }
+    sums[tid] = sum;
+    __syncthreads();
+    for (int d = 1; d < 128; d <<= 1) {
+      const long long add = tid >= d ? sums[tid - d] : 0;
+      __syncthreads();
+      sums[tid] += add;
+      __syncthreads();
+    }
+    const long long before = sums[tid] - sum;
+    S.total = sums[127] * p.Hkv;
+    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
+    if (blockIdx.x == 0) {
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        int t0;
+        sched[b] = at;
+        at += tiles_of<false>(p, load_seq(p, b), t0);
+      }
+      if (tid == 127) sched[p.B] = sums[127];
+    }
+    if (blockIdx.x >= S.blocks) { first = last = 0; return S; }
+    first = first_tile(blockIdx.x, S.total, S.blocks);
+    last = first_tile(blockIdx.x + 1, S.total, S.blocks);
+    if (first >= before * p.Hkv && first < (before + sum) * p.Hkv) {
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        int t0;
+        const int nt = tiles_of<false>(p, load_seq(p, b), t0);
+        if (first < (at + nt) * p.Hkv) {
+          s_b = b;
+          s_before = at;
+          break;
+        }
+        at += nt;
+      }
+    }
+    __syncthreads();
+    c.b = s_b;
+    c.s = load_seq(p, c.b);
+    c.nt = tiles_of<false>(p, c.s, c.t0);
+    const long long in = first - s_before * p.Hkv;
+    c.h = static_cast<int>(in / c.nt);
+    c.t = static_cast<int>(in - static_cast<long long>(c.h) * c.nt);
+    return S;
+  }
+}
+
+// The next tile; past an item's end the next head, past the last head the
+// next sequence that has tiles (the caller knows that there is one).
+template <bool PREFIX>
+__device__ __forceinline__ void advance(const Batch& p, Cursor& c) {
+  if (++c.t < c.nt) return;
+  c.t = 0;
+  if (++c.h < p.Hkv) return;
+  c.h = 0;
+  if constexpr (!PREFIX) {
+    do {
+      ++c.b;
+      c.s = load_seq(p, c.b);
+      c.nt = tiles_of<false>(p, c.s, c.t0);
+    } while (c.nt == 0);
+  }
+}
+
+template <int WR, bool PREFIX>
+__global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
+  using F = Few<WR>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  __shared__ float2 s_ml[4][16];
+  __shared__ Cursor s_cur[F::STAGES];
+  __shared__ int s_err;
+  const Batch& B = p.b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rg = warp / F::WK, kg = warp % F::WK;
+  if (tid == 0) s_err = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  int err = 0;
+  Cursor c;
+  long long tile, last;
+  const Sched S = schedule<PREFIX>(B, p.sched, c, tile, last, &err);
+  __syncthreads();
+  if (tile >= last) {
+    if (err) atomicOr(&s_err, err);
+    __syncthreads();
+    if (tid == 0) p.status[blockIdx.x] = s_err;
+    return;
+  }
+  const int n_tiles = static_cast<int>(last - tile);
+
+  // page of 8-key group `lane` (< 8) of the cursor's tile, or -1
+  auto page_of_group = [&](const Cursor& x) -> int {
+    if (lane >= 8) return -1;
+    const int key = (x.t0 + x.t) * KT + lane * 8;
+    if (key >= x.s.kv) return -1;
+    const int row = PREFIX ? S.table_row : x.b;
+    const int page = B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
+    if (page < 0 || page >= B.n_pages) {
+      err = DEV_ERR_BATCH;
+      return -1;
+    }
+    return page;
+  };
+  auto issue = [&](int stage, const Cursor& x, int group_page, bool new_item) {
+    const uint32_t ks = smem_u32(smem + stage * F::STAGE), vs = ks + F::KV_BYTES, qs = vs + F::KV_BYTES;
+    const int ch = tid & 15, r0 = tid >> 4;
+    const int lo = PREFIX ? 0 : B.shared;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 8 * i, key = (x.t0 + x.t) * KT + r;
+      const int page = __shfl_sync(0xffffffffu, group_page, i);
+      const bool ok = page >= 0 && key >= lo && key < x.s.kv;
+      const long long off =
+          ok ? ((((static_cast<long long>(page) * B.Hkv + x.h) << B.page_shift) +
+                 (key & ((1 << B.page_shift) - 1))) * HD + ch * 8)
+             : 0;
+      cp_async16(tile_chunk(ks, r, ch), B.k + off, ok);
+      cp_async16(tile_chunk(vs, r, ch), B.v + off, ok);
+    }
+    if (new_item) {
+      const int rows = x.s.qn * B.G;
+#pragma unroll
+      for (int i = 0; i < 2 * WR; ++i) {
+        const int r = r0 + 8 * i;
+        const bool ok = r < rows;
+        const int tok = ok ? r / B.G : 0, g = ok ? r - tok * B.G : 0;
+        const long long off =
+            ok ? (static_cast<long long>(x.s.q0 + tok) * B.H + x.h * B.G + g) * HD + ch * 8 : 0;
+        cp_async16(tile_chunk(qs, r, ch), p.q + off, ok);
+      }
+    }
+    if (tid == 0) s_cur[stage] = x;
+  };
+
+  int issued = 0;
+  int group_page = page_of_group(c);
+#pragma unroll
+  for (int s = 0; s < F::STAGES - 1; ++s) {
+    if (issued < n_tiles) {
+      issue(s, c, group_page, issued == 0 || c.t == 0);
+      if (++issued < n_tiles) {
+        advance<PREFIX>(B, c);
+        group_page = page_of_group(c);
+      }
+    }
+    cp_async_commit();
+  }
+
+  float o[16][4];
+  float m[2], l[2];
+  uint32_t qf[8][4];
+  int limit[2] = {0, 0};
+  bool fresh = true;      // the next tile starts a segment
+  int seg_t = 0;          // its first tile within the item
+  for (int i = 0; i < n_tiles; ++i) {
+    const int stage = i % F::STAGES;
+    cp_async_wait<F::STAGES - 2>();
+    __syncthreads();  // tile i has landed for everybody; tile i - 1 has been used by everybody
+    const Cursor x = s_cur[stage];
+    if (issued < n_tiles) {
+      issue((i + F::STAGES - 1) % F::STAGES, c, group_page, c.t == 0);
+      if (++issued < n_tiles) {
+        advance<PREFIX>(B, c);
+        group_page = page_of_group(c);
+      }
+    }
+    cp_async_commit();
+
+    const uint32_t ks = smem_u32(smem + stage * F::STAGE), vs = ks + F::KV_BYTES, qs = vs + F::KV_BYTES;
+    const int rows = x.s.qn * B.G;
+    if (fresh) {
+      seg_t = x.t;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        ldsm4(qf[k], tile_chunk(qs, rg * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)));
+      // how many of the sequence's keys this thread's two rows see
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = rg * 16 + (lane >> 2) + 8 * e;
+        limit[e] = 0;
+        if (r < rows) {
+          const int tok = r / B.G;
+          if (PREFIX) {
+            const int b = find_seq(B.cu, B.B, tok);
+            if (b < B.B) {
+              const Seq s = load_seq(B, b);
+              if (tok >= s.q0 && tok < s.q0 + s.qn) limit[e] = min(s.visible(tok - s.q0, B.causal), x.s.kv);
+            }
+          } else {
+            limit[e] = x.s.visible(tok, B.causal);
+          }
+        }
+      }
+      fresh = false;
+    }
+    if (rg * 16 < rows) {
+      const int key0 = kg * 16 * F::NB;  // this warp's keys of the tile
+      const int base = (x.t0 + x.t) * KT + key0;
+      const int lo = PREFIX ? 0 : B.shared;
+      float s[F::NB][2][4];
+#pragma unroll
+      for (int nb = 0; nb < F::NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nb][0][e] = s[nb][1][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t kf[4];
+          ldsm4(kf, tile_chunk(ks, key0 + nb * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+          mma16816(s[nb][0], qf[k], kf[0], kf[1]);
+          mma16816(s[nb][1], qf[k], kf[2], kf[3]);
+        }
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nb = 0; nb < F::NB; ++nb)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = base + nb * 16 + n * 8 + (lane & 3) * 2 + (e & 1);
+            if (key < lo || key >= limit[e >> 1]) s[nb][n][e] = -INFINITY;
+            mx[e >> 1] = fmaxf(mx[e >> 1], s[nb][n][e]);
+          }
+      float alpha[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2)) * p.scale_log2;
+        // the maximum moves only when it grew by more than 2^8
+        alpha[e] = 1.f;
+        if (mx[e] > m[e] + 8.f || m[e] == -INFINITY) {
+          if (mx[e] > m[e]) {
+            alpha[e] = ex2(m[e] - mx[e]);
+            m[e] = mx[e];
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] *= alpha[e >> 1];
+        l[0] *= alpha[0];
+        l[1] *= alpha[1];
+      }
+      const float nm[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
+#pragma unroll
+      for (int nb = 0; nb < F::NB; ++nb) {
+        uint32_t pf[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float e4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            e4[e] = ex2(fmaf(s[nb][n][e], p.scale_log2, nm[e >> 1]));
+            l[e >> 1] += e4[e];
+          }
+          // the probabilities are rounded to bf16 for the second product, as
+          // its operand has to be; their sum is taken before that
+          pf[2 * n] = pack_bf16x2(e4[0], e4[1]);
+          pf[2 * n + 1] = pack_bf16x2(e4[2], e4[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t vf[4];
+          ldsm4t(vf, tile_chunk(vs, key0 + nb * 16 + (lane & 15), 2 * j + (lane >> 4)));
+          mma16816(o[2 * j], pf, vf[0], vf[1]);
+          mma16816(o[2 * j + 1], pf, vf[2], vf[3]);
+        }
+      }
+    }
+    if (x.t + 1 < x.nt && i + 1 < n_tiles) continue;
+
+    // ---- end of a segment: the key groups of the rows meet
+    fresh = true;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if ((lane & 3) == 0) s_ml[warp][(lane >> 2) + 8 * e] = make_float2(m[e], l[e]);
+    }
+    __syncthreads();  // everybody is done with this tile's K and V: they become the meeting place
+    float* meet = reinterpret_cast<float*>(smem + stage * F::STAGE);  // [4 warps][16 rows][HD]
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int col = j * 8 + (lane & 3) * 2, r = lane >> 2;
+      // rows are shifted against each other so that a store's eight rows use different banks
+      *reinterpret_cast<float2*>(meet + (warp * 16 + r) * HD + ((col + 8 * (r & 7)) & 127)) =
+          make_float2(o[j][0], o[j][1]);
+      *reinterpret_cast<float2*>(meet + (warp * 16 + r + 8) * HD + ((col + 8 * (r & 7)) & 127)) =
+          make_float2(o[j][2], o[j][3]);
+    }
+    __syncthreads();
+    const bool whole = !PREFIX && B.shared == 0 && seg_t == 0 && x.t + 1 == x.nt;
+    const long long slot = static_cast<long long>(x.b) * B.Hkv + x.h + blockIdx.x;
+#pragma unroll
+    for (int a = 0; a < WR; ++a) {
+      const int r16 = tid >> 3, r = a * 16 + r16;
+      if (r < rows) {
+        float mr = -INFINITY, lr = 0.f, f[F::WK];
+#pragma unroll
+        for (int g = 0; g < F::WK; ++g) mr = fmaxf(mr, s_ml[a * F::WK + g][r16].x);
+#pragma unroll
+        for (int g = 0; g < F::WK; ++g) {
+          const float2 ml = s_ml[a * F::WK + g][r16];
+          f[g] = mr == -INFINITY ? 0.f : ex2(ml.x - mr);
+          lr += ml.y * f[g];
+        }
+        const int tok = x.s.q0 + r / B.G, head = x.h * B.G + r % B.G;
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int col = (tid & 7) * 4 + 32 * k;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int g = 0; g < F::WK; ++g) {
+            const float4 w = *reinterpret_cast<const float4*>(
+                meet + ((a * F::WK + g) * 16 + r16) * HD + ((col + 8 * (r16 & 7)) & 127));
+            v.x += w.x * f[g];
+            v.y += w.y * f[g];
+            v.z += w.z * f[g];
+            v.w += w.w * f[g];
+          }
+          if (whole) {
+            uint2 w;
+            w.x = pack_bf16x2(v.x * inv, v.y * inv);
+            w.y = pack_bf16x2(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2*>(p.o + (static_cast<long long>(tok) * B.H + head) * HD + col) = w;
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (slot * p.rows + r) * HD + col) = v;
+          }
+        }
+        if ((tid & 7) == 0) {
+          if (!whole)
+            p.part_ml[slot * p.rows + r] = make_float2(mr, lr);
+          else if (p.lse)
+            p.lse[static_cast<long long>(tok) * B.H + head] = lr > 0.f ? mr + log2f(lr) : -INFINITY;
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  if (err) atomicOr(&s_err, err);
+  __syncthreads();
+  if (tid == 0) p.status[blockIdx.x] = s_err;
+}
+
+// ================================================================ combine
+// Joins the parts of a row: with (m_i, l_i, O_i) the running maximum, sum and
+// unnormalised output of part i, m = max m_i, l = sum l_i 2^(m_i - m),
+// o = sum O_i 2^(m_i - m) / l, always in the order of the parts, so that a
+// result does not change from run to run.  A row without any key gets zeros.
+// Bound by latency: the parts lie in L2.  A warp per row; rows cut into many
+// parts (a long sequence on many blocks) are taken by all eight warps.
+struct PartSrc {
+  const float* o = nullptr;
+  const float2* ml = nullptr;
+  const long long* sched = nullptr;
+  int rows = 0, grid = 0;
+};
+struct CombineParams {
+  Batch b;
+  PartSrc own, shared;   // shared.o null: no shared keys
+  __nv_bfloat16* o;
+  float* lse;
+  int rows_per_block;    // 1 or 8
+  int many;              // more parts than this: all warps
+  int* header;           // see kKvHeaderBytes
+  int alone, status_words;
+};
+
+struct RowParts {
+  long long own0, sh0;   // first slots
+  int n_own, n;          // parts of the sequence's own keys, parts in all
+  int r_own, r_sh;       // the row within the slots
+  int tok, head;
+  bool direct;           // already written, or nobody's row
+};
+
+__device__ __forceinline__ RowParts row_parts(const CombineParams& p, long long row) {
+  const Batch& B = p.b;
+  RowParts R{};
+  R.direct = true;
+  if (row >= static_cast<long long>(B.n_tokens) * B.H) return R;
+  R.tok = static_cast<int>(row / B.H);
+  R.head = static_cast<int>(row - static_cast<long long>(R.tok) * B.H);
+  const int b = find_seq_warp(B.cu, B.B, R.tok);
+  if (b >= B.B) return R;
+  const Seq s = load_seq(B, b);
+  if (R.tok < s.q0 || R.tok >= s.q0 + s.qn) return R;
+  const int h = R.head / B.G, g = R.head - h * B.G;
+  const long long before = p.own.sched[b], nt = p.own.sched[b + 1] - before;
+  if (nt > 0) {
+    const long long T = p.own.sched[B.B] * B.Hkv, C = T < p.own.grid ? T : p.own.grid;
+    const long long t0 = before * B.Hkv + h * nt;
+    const long long c0 = block_of_tile(t0, T, C), c1 = block_of_tile(t0 + nt - 1, T, C);
+    R.own0 = static_cast<long long>(b) * B.Hkv + h + c0;
+    R.n_own = static_cast<int>(c1 - c0) + 1;
+    R.r_own = (R.tok - s.q0) * B.G + g;
+  }
+  R.n = R.n_own;
+  if (p.shared.o) {
+    const long long snt = p.shared.sched[1];
+    if (snt > 0) {
+      const long long T = snt * B.Hkv, C = T < p.shared.grid ? T : p.shared.grid;
+      const long long c0 = block_of_tile(h * snt, T, C), c1 = block_of_tile((h + 1) * snt - 1, T, C);
+      R.sh0 = h + c0;
+      R.n += static_cast<int>(c1 - c0) + 1;
+      R.r_sh = R.tok * B.G + g;
+    }
+  }
+  R.direct = !p.shared.o && R.n == 1;
+  return R;
+}
+
+__device__ __forceinline__ float2 part_ml(const CombineParams& p, const RowParts& R, int i) {
+  return i < R.n_own ? p.own.ml[(R.own0 + i) * p.own.rows + R.r_own]
+                     : p.shared.ml[(R.sh0 + i - R.n_own) * p.shared.rows + R.r_sh];
+}
+__device__ __forceinline__ float4 part_o(const CombineParams& p, const RowParts& R, int i) {
+  const float* base = i < R.n_own ? p.own.o + ((R.own0 + i) * p.own.rows + R.r_own) * HD
+                                  : p.shared.o + ((R.sh0 + i - R.n_own) * p.shared.rows + R.r_sh) * HD;
+  return reinterpret_cast<const float4*>(base)[threadIdx.x & 31];
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+// parts first, first + step, ... of a row: sum of O_i 2^(m_i - m)
+__device__ __forceinline__ float4 sum_parts(const CombineParams& p, const RowParts& R, float m, int first, int step) {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = first; i < R.n; i += step) {
+    const float f = ex2(part_ml(p, R, i).x - m);
+    const float4 v = part_o(p, R, i);
+    a.x += f * v.x;
+    a.y += f * v.y;
+    a.z += f * v.z;
+    a.w += f * v.w;
+  }
+  return a;
+}
+__device__ __forceinline__ void write_row(const CombineParams& p, const RowParts& R, float4 a, float m, float l) {
+  const int lane = threadIdx.x & 31;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const long long row = static_cast<long long>(R.tok) * p.b.H + R.head;
+  uint2 w;
+  w.x = pack_bf16x2(a.x * inv, a.y * inv);
+  w.y = pack_bf16x2(a.z * inv, a.w * inv);
+  reinterpret_cast<uint2*>(p.o + row * HD)[lane] = w;
+  if (p.lse && lane == 0) p.lse[row] = l > 0.f ? m + log2f(l) : -INFINITY;
+}
+
+__global__ void __launch_bounds__(256) kv_combine_kernel(const CombineParams p) {
+  __shared__ float4 s_acc[8][32];
+  __shared__ int s_many[8];
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.header[2] = p.status_words;
+    if (p.alone) p.header[0] = p.header[1] = 0;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row0 = static_cast<long long>(blockIdx.x) * p.rows_per_block;
+  if (warp < p.rows_per_block) {
+    const RowParts R = row_parts(p, row0 + warp);
+    const bool many = R.n > p.many;
+    if (lane == 0) s_many[warp] = many && !R.direct;
+    if (!R.direct && !many) {
+      const float2 ml = lane < R.n ? part_ml(p, R, lane) : make_float2(-INFINITY, 0.f);
+      const float m = warp_max(ml.x);
+      const float l = m == -INFINITY ? 0.f : warp_sum(ml.y * ex2(ml.x - m));
+      const float4 a = m == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : sum_parts(p, R, m, 0, 1);
+      write_row(p, R, a, m, l);
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < p.rows_per_block; ++k) {
+    if (!s_many[k]) continue;
+    const RowParts R = row_parts(p, row0 + k);
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < R.n; i += 32) m = fmaxf(m, part_ml(p, R, i).x);
+    m = warp_max(m);
+    if (m != -INFINITY) {
+      for (int i = lane; i < R.n; i += 32) {
+        const float2 ml = part_ml(p, R, i);
+        l += ml.y * ex2(ml.x - m);
+      }
+      l = warp_sum(l);
+      s_acc[warp][lane] = sum_parts(p, R, m, warp, 8);
+    } else {
+      s_acc[warp][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float4 a = s_acc[0][lane];
+      for (int w = 1; w < 8; ++w) {
+        const float4 v = s_acc[w][lane];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+      write_row(p, R, a, m, l);
+    }
+    __syncthreads();
+  }
+}
+
+// ================================================================ host
+// Launch as a programmatic dependent of the stream's previous kernel.
+template <typename P>
+void launch_dep(void (*kern)(P), int grid, int block, int smem, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <typename K>
+int set_smem_once(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TP_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done.load() & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return TP_ERR_CUDA;
+    done.fetch_or(bit);
+  }
+  return TP_OK;
+}
+
+Batch make_batch(const KvSpec& a) {
+  Batch b{};
+  b.k = static_cast<__nv_bfloat16*>(a.k);
+  b.v = static_cast<__nv_bfloat16*>(a.v);
+  b.n_pages = a.n_pages;
+  b.max_pages = a.max_pages;
+  while ((1 << b.page_shift) < a.page_size) ++b.page_shift;
+  b.B = a.n_seqs;
+  b.n_tokens = a.n_tokens;
+  b.max_new = a.max_new;
+  b.H = a.H;
+  b.Hkv = a.Hkv;
+  b.G = a.H / a.Hkv;
+  b.causal = a.causal;
+  b.cap = kv_cap(a);
+  b.shared = a.shared_len;
+  b.cu = a.cu;
+  b.kv_len = a.kv_len;
+  b.table = a.table;
+  return b;
+}
+
+int few_blocks(int num_sms) { return 2 * num_sms; }
+
+template <int WR, bool PREFIX>
+int launch_few_inst(const FewParams& p, LaunchCtx& ctx, const char* name) {
+  static std::atomic<uint64_t> done{0};
+  if (int rc = set_smem_once(kv_few_kernel<WR, PREFIX>, Few<WR>::SMEM, done)) return rc;
+  if (ctx.before) ctx.before(ctx.user, name, ctx.stream);
+  launch_dep(kv_few_kernel<WR, PREFIX>, few_blocks(ctx.num_sms), 128, Few<WR>::SMEM, ctx.stream, p);
+  if (ctx.after) ctx.after(ctx.user, ctx.stream);
+  ctx.launches++;
+  return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+template <bool PREFIX>
+int launch_few(const FewParams& p, LaunchCtx& ctx, const char* name) {
+  if (p.rows <= 16) return launch_few_inst<1, PREFIX>(p, ctx, name);
+  if (p.rows <= 32) return launch_few_inst<2, PREFIX>(p, ctx, name);
+  return launch_few_inst<4, PREFIX>(p, ctx, name);
+}
+
+}  // namespace kv
+
+int kv_cap(const KvSpec& a) {
+  const long long keys = static_cast<long long>(a.max_pages) * a.page_size;
+  return keys < (1 << 30) ? static_cast<int>(keys) : (1 << 30);
+}
+
+int launch_kv_append(const KvSpec& a, const KvRotation& r, const void* qkv, void* q, int* header, bool alone,
+                     LaunchCtx& ctx) {
+  kv::AppendParams p{};
+  p.b = kv::make_batch(a);
+  p.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  p.q = static_cast<__nv_bfloat16*>(q);
+  p.inv_freq = r.inv_freq;
+  p.scale = r.scale;
+  p.rot = r.rotary_dim;
+  p.interleaved = r.interleaved;
+  p.hq_per = a.H / a.T_p;
+  p.hk_per = a.Hkv / a.T_p;
+  p.header = header;
+  p.alone = alone;
+  const int most = 8 * ctx.num_sms < kKvStatusWords ? 8 * ctx.num_sms : kKvStatusWords;
+  if (ctx.before) ctx.before(ctx.user, "kv_append", ctx.stream);
+  kv::launch_dep(kv::kv_append_kernel, a.n_tokens < most ? a.n_tokens : most, kv::APPEND_THREADS, 0, ctx.stream, p);
+  if (ctx.after) ctx.after(ctx.user, ctx.stream);
+  ctx.launches++;
+  return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+namespace {
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+// The attention's scratch: for the own keys and for the shared ones the
+// tiles' prefix sums and the parts.
+struct AttendLayout {
+  size_t sched = 0, own_o = 0, own_ml = 0, sh_sched = 0, sh_o = 0, sh_ml = 0, total = 0;
+  int own_rows = 0, sh_rows = 0;
+};
+AttendLayout attend_layout(const KvSpec& a, int num_sms) {
+  AttendLayout L;
+  const int64_t G = a.H / a.Hkv, blocks = kv::few_blocks(num_sms);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.own_rows = static_cast<int>(a.max_new * G);
+  L.sched = take((static_cast<size_t>(a.n_seqs) + 1) * 8);
+  const size_t own = (static_cast<size_t>(a.n_seqs) * a.Hkv + blocks) * L.own_rows;
+  L.own_o = take(own * kv::HD * 4);
+  L.own_ml = take(own * 8);
+  if (a.shared_len > 0) {
+    L.sh_rows = static_cast<int>(a.n_tokens * G);
+    L.sh_sched = take(2 * 8);
+    const size_t sh = (static_cast<size_t>(a.Hkv) + blocks) * L.sh_rows;
+    L.sh_o = take(sh * kv::HD * 4);
+    L.sh_ml = take(sh * 8);
+  }
+  L.total = off;
+  return L;
+}
+}  // namespace
+
+size_t kv_attend_scratch_bytes(const KvSpec& a, int num_sms) { return attend_layout(a, num_sms).total; }
+
+int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* header, bool alone, void* scratch,
+                     LaunchCtx& ctx) {
+  const AttendLayout L = attend_layout(a, ctx.num_sms);
+  if (L.own_rows > 64 || L.sh_rows > 64) return TP_ERR_UNSUPPORTED;
+  char* ws = static_cast<char*>(scratch);
+  const int blocks = kv::few_blocks(ctx.num_sms);
+  int* status = header + kKvHeaderWords + kKvStatusWords;
+  kv::CombineParams c{};
+  kv::FewParams p{};
+  p.b = kv::make_batch(a);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kv::HD)));
+  int rc = TP_OK;
+  if (a.shared_len > 0) {
+    p.part_o = reinterpret_cast<float*>(ws + L.sh_o);
+    p.part_ml = reinterpret_cast<float2*>(ws + L.sh_ml);
+    p.sched = reinterpret_cast<long long*>(ws + L.sh_sched);
+    p.rows = L.sh_rows;
+    p.status = status + c.status_words;
+    c.status_words += blocks;
+    c.shared = {p.part_o, p.part_ml, p.sched, p.rows, blocks};
+    if ((rc = kv::launch_few<true>(p, ctx, "kv_attend_shared"))) return rc;
+  }
+  p.part_o = reinterpret_cast<float*>(ws + L.own_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.own_ml);
+  p.sched = reinterpret_cast<long long*>(ws + L.sched);
+  p.rows = L.own_rows;
+  p.status = status + c.status_words;
+  c.status_words += blocks;
+  c.own = {p.part_o, p.part_ml, p.sched, p.rows, blocks};
+  if ((rc = kv::launch_few<false>(p, ctx, "kv_attend_own"))) return rc;
+  c.b = p.b;
+  c.o = p.o;
+  c.lse = lse;
+  c.header = header;
+  c.alone = alone;
+  // few rows: a block for each, so that a long sequence's many parts are
+  // read by all of its warps
+  const long long rows = static_cast<long long>(a.n_tokens) * a.H;
+  c.rows_per_block = rows <= 4ll * ctx.num_sms ? 1 : 8;
+  c.many = c.rows_per_block == 1 ? 4 : 32;
+  if (ctx.before) ctx.before(ctx.user, "kv_combine", ctx.stream);
+  kv::launch_dep(kv::kv_combine_kernel, static_cast<int>((rows + c.rows_per_block - 1) / c.rows_per_block), 256, 0,
+                 ctx.stream, c);
+  if (ctx.after) ctx.after(ctx.user, ctx.stream);
+  ctx.launches++;
+  return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+}  // namespace tpffn

@@ -1,0 +1,148 @@
+"""The attention sublayer's paged key/value cache over the C ABI (tp_attn_kv_*
+and tp_attn_paged_fwd of include/tpffn.h).
+
+PyTorch allocates the device buffers and supplies the stream; every step runs
+in libtpffn.so.
+
+    attn = TensorParallelAttention(d=4096, n_heads=32, n_kv_heads=8, head_dim=128, T_p=8)
+    cache = PagedKVCache(attn, n_pages=4096, page_size=64, inv_freq=inv_freq)
+    batch = cache.batch(cu_tokens, kv_len, page_table, n_tokens=n, max_new=1)
+    q = cache.append(qkv, batch)                      # keys and values stored, q rotated
+    o = cache.attend(q, batch, shared_len=0)          # [n, H * 128]
+    y = attn.decode(x, cache, batch, wqkv, wo)        # both, between the projections
+
+A call takes its workspace from PyTorch's allocator on the current stream, so
+calls on different streams, and graphs that were captured apart, do not share
+one.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import tpffn as abi
+
+
+class KVBatch:
+    """Device arrays that describe a batch of sequences (see tp_kv_batch).
+
+    The tensors are used where they lie: their contents may change from step to
+    step (a replayed graph reads them anew) as long as n_tokens and max_new
+    still bound them."""
+
+    def __init__(self, cu_tokens, kv_len, page_table, n_tokens, max_new):
+        for name, t, dims in (("cu_tokens", cu_tokens, 1), ("kv_len", kv_len, 1), ("page_table", page_table, 2)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous int32 tensor of {dims} dimension(s) is needed")
+        if cu_tokens.numel() != kv_len.numel() + 1 or page_table.shape[0] != kv_len.numel():
+            raise ValueError("cu_tokens has one entry more than kv_len, page_table a row for each")
+        if len({cu_tokens.device, kv_len.device, page_table.device}) != 1:
+            raise ValueError("the batch's tensors lie on different devices")
+        n_tokens, max_new = int(n_tokens), int(max_new)
+        if n_tokens < 0 or max_new < 0:
+            raise ValueError("n_tokens and max_new are not negative")
+        self.cu_tokens, self.kv_len, self.page_table = cu_tokens, kv_len, page_table
+        self.n_seqs, self.n_tokens, self.max_new = kv_len.numel(), n_tokens, max_new
+        self.device = kv_len.device
+        self.abi = abi.KvBatch(self.n_seqs, n_tokens, max_new, page_table.shape[1], cu_tokens.data_ptr(),
+                               kv_len.data_ptr(), page_table.data_ptr())
+
+
+class PagedKVCache:
+    """Pages of keys and values of one attention sublayer, [n_pages, n_kv_heads,
+    page_size, 128] each in bf16, and the rotation of its queries and keys.
+
+    inv_freq: float32 [rotary_dim / 2] on the device, or None for no rotation;
+    k, v: existing pages (zeros are allocated otherwise)."""
+
+    def __init__(self, attn, n_pages, page_size, k=None, v=None, inv_freq=None, interleaved=False, rotary_scale=1.0):
+        shape = (int(n_pages), attn.Hkv, int(page_size), attn.hd)
+        self.attn, self.n_pages, self.page_size = attn, shape[0], shape[2]
+        self.device = attn.device if attn.device.index is not None else torch.device(
+            attn.device.type, torch.cuda.current_device())
+        if n_pages < 1 or page_size < 8 or page_size > 1024 or page_size & (page_size - 1):
+            raise ValueError("n_pages is at least 1, page_size a power of two from 8 to 1024")
+        pages = []
+        for name, t in (("k", k), ("v", v)):
+            if t is None:
+                t = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+            self._check(name, t, torch.bfloat16, shape)
+            pages.append(t)
+        self.k, self.v = pages
+        self.inv_freq = inv_freq
+        self._abi = abi.KvCache(self.k.data_ptr(), self.v.data_ptr(), shape[0], shape[2])
+        self._rot = None
+        if inv_freq is not None:
+            if inv_freq.dim() != 1 or inv_freq.numel() % 8 or not 8 <= inv_freq.numel() <= attn.hd // 2:
+                raise ValueError("inv_freq has rotary_dim / 2 entries: a multiple of 8 up to half the head width")
+            self._check("inv_freq", inv_freq, torch.float32, inv_freq.shape)
+            self._rot = abi.KvRotation(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)),
+                                       float(rotary_scale))
+        self._last = None  # workspace of the last call, for last_device_error
+
+    def _check(self, name, t, dtype, shape):
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device} is "
+                             f"needed, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _out(self, name, t, dtype, shape):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        self._check(name, t, dtype, shape)
+        return t
+
+    def _call(self, batch, shared_len, call, flags):
+        """Workspace and stream of one call."""
+        if batch.device != self.device:
+            raise ValueError(f"the batch lies on {batch.device}, the cache on {self.device}")
+        need = abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call, flags)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+        self._last = ws if batch.n_tokens and batch.n_seqs else None
+        return ws, torch.cuda.current_stream(self.device)
+
+    def batch(self, cu_tokens, kv_len, page_table, n_tokens, max_new):
+        return KVBatch(cu_tokens, kv_len, page_table, n_tokens, max_new)
+
+    def append(self, qkv, batch, q=None, flags=0):
+        """Stores the new tokens' keys (rotated) and values; returns the rotated
+        queries [n_tokens, H * 128] (in `q` if given)."""
+        a, n = self.attn, batch.n_tokens
+        with torch.cuda.device(self.device):
+            self._check("qkv", qkv, torch.bfloat16, (n, a.info["qkv_width"]))
+            q = self._out("q", q, torch.bfloat16, (n, a.H * a.hd))
+            ws, st = self._call(batch, 0, abi.TP_KV_APPEND, flags)
+            abi.check(abi.tp_attn_kv_append(a.plan, self._abi, batch.abi, self._rot, qkv, q, ws, ws.numel(), flags,
+                                            st), "tp_attn_kv_append")
+        return q
+
+    def attend(self, q, batch, shared_len=0, lse=False, out=None, flags=0):
+        """Attention of q [n_tokens, H * 128] over the cache: o, or (o, lse) with
+        the rows' log2-sum-exp [n_tokens, H] if `lse`."""
+        a, n = self.attn, batch.n_tokens
+        with torch.cuda.device(self.device):
+            self._check("q", q, torch.bfloat16, (n, a.H * a.hd))
+            o = self._out("out", out, torch.bfloat16, (n, a.H * a.hd))
+            rows = torch.empty(n, a.H, dtype=torch.float32, device=self.device) if lse else None
+            ws, st = self._call(batch, shared_len, abi.TP_KV_ATTEND, flags)
+            abi.check(abi.tp_attn_paged_fwd(a.plan, self._abi, batch.abi, shared_len, q, o, rows, ws, ws.numel(),
+                                            flags, st), "tp_attn_paged_fwd")
+        return (o, rows) if lse else o
+
+    def decode(self, x, batch, wqkv, wo, shared_len=0, out=None, flags=0):
+        """The sublayer's serving pass, y [n_tokens, d] (TensorParallelAttention.decode)."""
+        a, n = self.attn, batch.n_tokens
+        with torch.cuda.device(self.device):
+            self._check("x", x, torch.bfloat16, (n, a.d))
+            y = self._out("out", out, torch.bfloat16, (n, a.d))
+            ws, st = self._call(batch, shared_len, abi.TP_KV_DECODE, flags)
+            abi.check(abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
+                                             ws.numel(), flags, st), "tp_attn_decode_fwd")
+        return y
+
+    def last_device_error(self):
+        """Waits for the current stream and returns the status that the last call
+        on this cache left on the device (TP_OK, TP_ERR_BATCH, ...)."""
+        if self._last is None:
+            return abi.TP_OK
+        with torch.cuda.device(self.device):
+            return abi.tp_attn_kv_last_device_error(self.attn.plan, self._last,
+                                                    torch.cuda.current_stream(self.device))

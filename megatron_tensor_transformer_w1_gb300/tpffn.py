@@ -14,12 +14,13 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtpffn.so")
 
-TP_OK, TP_ERR_INVALID, TP_ERR_UNSUPPORTED, TP_ERR_CUDA, TP_ERR_TIMEOUT, TP_ERR_ALIGN = range(6)
+TP_OK, TP_ERR_INVALID, TP_ERR_UNSUPPORTED, TP_ERR_CUDA, TP_ERR_TIMEOUT, TP_ERR_ALIGN, TP_ERR_BATCH = range(7)
 TP_ACT_NONE, TP_ACT_GELU_TANH, TP_ACT_SWIGLU = 0, 1, 2
 TP_F32, TP_BF16 = 0, 1
 TP_PACK_COLUMNS, TP_PACK_ROWS = 0, 1
 TP_SUM_STANDALONE, TP_SUM_FUSED, TP_FLAG_SYNC, TP_FLAG_TIMING, TP_SUM_OVERLAP = 0, 1, 2, 4, 8
 TP_FLAG_DEBUG_SKIP_LOAD = 1 << 16
+TP_KV_APPEND, TP_KV_ATTEND, TP_KV_DECODE = 0, 1, 2
 
 ABI_FUNCTIONS = (
     "tp_ffn_plan_create", "tp_attn_out_plan_create", "tp_ffn_plan_destroy", "tp_ffn_plan_info",
@@ -32,6 +33,8 @@ ABI_FUNCTIONS = (
     "tp_attn_shard_weights", "tp_attn_unshard_weights", "tp_attn_saved_bytes", "tp_attn_saved_offsets",
     "tp_attn_workspace_bytes", "tp_attn_fwd", "tp_attn_bwd", "tp_attn_core_fwd", "tp_attn_core_bwd",
     "tp_attn_kernel_times", "tp_attn_last_launch_count",
+    "tp_attn_kv_workspace_bytes", "tp_attn_kv_append", "tp_attn_paged_fwd", "tp_attn_decode_fwd",
+    "tp_attn_kv_last_device_error",
 )
 TPFFN_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -51,6 +54,25 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+
+
+
+class KvCache(ctypes.Structure):
+    """tp_kv_cache"""
+    _fields_ = [("k", _P), ("v", _P), ("n_pages", _I64), ("page_size", _I64)]
+
+
+class KvBatch(ctypes.Structure):
+    """tp_kv_batch"""
+    _fields_ = [("n_seqs", _I64), ("n_tokens", _I64), ("max_new", _I64), ("max_pages", _I64), ("cu_tokens", _P),
+                ("kv_len", _P), ("page_table", _P)]
+
+
+class KvRotation(ctypes.Structure):
+    """tp_kv_rotation"""
+    _fields_ = [("inv_freq", _P), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
 
 _SIGS = {
     "tp_ffn_plan_create": (_INT, [ctypes.POINTER(_P), _I64, _I64, _INT, _INT, _INT]),
@@ -91,6 +113,11 @@ _SIGS = {
     "tp_attn_core_bwd": (_INT, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _INT, _P]),
     "tp_attn_kernel_times": (_INT, [_P, _INT, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float)]),
     "tp_attn_last_launch_count": (_INT, [_P]),
+    "tp_attn_kv_workspace_bytes": (_SZ, [_P, _P, _I64, _I64, _INT, _INT]),
+    "tp_attn_kv_append": (_INT, [_P, _P, _P, _P, _P, _P, _P, _SZ, _INT, _P]),
+    "tp_attn_paged_fwd": (_INT, [_P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _INT, _P]),
+    "tp_attn_decode_fwd": (_INT, [_P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _SZ, _INT, _P]),
+    "tp_attn_kv_last_device_error": (_INT, [_P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -319,6 +346,37 @@ def tp_attn_kernel_times(plan, max_records=64):
 
 def tp_attn_last_launch_count(plan):
     return _lib.tp_attn_last_launch_count(plan)
+
+
+# ------------------------------------------------------------ key/value cache
+def _ref(s):
+    """The address of a KvCache, KvBatch or KvRotation (or None)."""
+    return None if s is None else ctypes.addressof(s)
+
+
+def tp_attn_kv_workspace_bytes(plan, batch, page_size, shared_len, call, flags=0):
+    return _lib.tp_attn_kv_workspace_bytes(plan, _ref(batch), page_size, shared_len, call, flags)
+
+
+def tp_attn_kv_append(plan, cache, batch, rotation, qkv, q, workspace, workspace_bytes, flags=0, stream=None):
+    return _lib.tp_attn_kv_append(plan, _ref(cache), _ref(batch), _ref(rotation), _ptr(qkv), _ptr(q),
+                                  _ptr(workspace), workspace_bytes, flags, _stream(stream))
+
+
+def tp_attn_paged_fwd(plan, cache, batch, shared_len, q, o, lse, workspace, workspace_bytes, flags=0, stream=None):
+    return _lib.tp_attn_paged_fwd(plan, _ref(cache), _ref(batch), shared_len, _ptr(q), _ptr(o), _ptr(lse),
+                                  _ptr(workspace), workspace_bytes, flags, _stream(stream))
+
+
+def tp_attn_decode_fwd(plan, cache, batch, rotation, shared_len, x, wqkv, wo_packed, y, workspace, workspace_bytes,
+                       flags=0, stream=None):
+    return _lib.tp_attn_decode_fwd(plan, _ref(cache), _ref(batch), _ref(rotation), shared_len, _ptr(x), _ptr(wqkv),
+                                   _ptr(wo_packed), _ptr(y), _ptr(workspace), workspace_bytes, flags,
+                                   _stream(stream))
+
+
+def tp_attn_kv_last_device_error(plan, workspace, stream=None):
+    return _lib.tp_attn_kv_last_device_error(plan, _ptr(workspace), _stream(stream))
 
 
 def check(status, where=""):

@@ -1,0 +1,370 @@
+"""Serving operators of the attention sublayer against plain 64-bit forms:
+appending to the paged cache with the rotation by position, and attention over
+the cache with and without a shared prefix.
+
+Tolerances.  A rounding to bf16 is off by at most 2^-8 of the value.
+ * Append, unrotated columns and values: equal.  Rotated ones: 2^-8 |ref| for
+   the output's rounding, plus the 32-bit error of x cos - y sin: sine and
+   cosine are within 2^-22 (an angle reduced to half a turn and rounded to 24
+   bits is off by 2 pi 2^-26 < 2^-23, the functions by less than 2^-23), two
+   products and a sum add 2^-23, so 2^-20 (|x| + |y|) covers it four times.
+ * Attention: the rounding of o (2^-8 |o|), the rounding of each probability
+   before the second product (2^-8 sum p |v|), and the scores' error d: 128
+   products summed in 32 bits are off by at most 2^7 2^-24 sum |q k|, which
+   changes p by a factor within exp(2 d); likewise the sum over L keys in 32
+   bits, L 2^-24, both relative to sum p |v|.  (1 + 2^-8) covers products of
+   these.  In root mean square the roundings of single probabilities average:
+   the relative error stays below 2^-8.
+ * lse: d log2 e from the scores and 2^-22 (|lse| + L 2^-2) from 32-bit sums.
+"""
+import math
+
+import pytest
+import torch
+
+from tests import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+HD = 128
+U = 2.0 ** -8
+
+
+def _modules():
+    from megatron_tensor_transformer_w1_gb300 import tpffn as abi
+    from megatron_tensor_transformer_w1_gb300.attention import TensorParallelAttention
+    from megatron_tensor_transformer_w1_gb300.kv_cache import KVBatch, PagedKVCache
+    return abi, TensorParallelAttention, KVBatch, PagedKVCache
+
+
+def _cache(s, H, T, causal=True, **kw):
+    _, Attention, _, Cache = _modules()
+    Hkv, page = s["k"].shape[1], s["k"].shape[2]
+    attn = Attention(256, H, Hkv, HD, T, causal=causal)
+    cache = Cache(attn, s["n_pages"], page, k=s["k"], v=s["v"], **kw)
+    return cache, cache.batch(s["cu"], s["kv_len"], s["table"], n_tokens=s["n"], max_new=s["max_new"])
+
+
+def _q(n, H, seed, scale=1.5):
+    g = torch.Generator(device="cuda").manual_seed(1000 + seed)
+    return (torch.randn(n, H * HD, generator=g, device="cuda") * scale).to(torch.bfloat16)
+
+
+def check_attend(s, q, H, o, lse, causal=True):
+    rows = s["cu"][-1].item()
+    want, want_lse, a, rough = ref.attend(s, q[:rows], H, causal)
+    longest = max(s["lens"])
+    d = 2.0 ** -17 * rough
+    wide = lambda t: t.repeat_interleave(HD, 1)
+    tol = (1 + U) * (U * want.abs() + a * (U + 2 * wide(d) + longest * 2.0 ** -24)) + 1e-30
+    err = (o[:rows].double() - want).abs()
+    assert torch.isfinite(o[:rows]).all()
+    assert (err <= tol).all(), f"largest error over its bound: {(err / tol).max().item():.2f}"
+    rms = want.square().mean().sqrt()
+    assert err.square().mean().sqrt() <= U * rms + 1e-30, (err.square().mean().sqrt() / rms).item()
+    if lse is not None:
+        none = want_lse == -math.inf
+        assert torch.equal(none, lse[:rows] == -math.inf)
+        lim = d * math.log2(math.e) + 2.0 ** -22 * (want_lse.abs() + longest / 4)
+        assert ((lse[:rows].double() - want_lse).abs()[~none] <= lim[~none]).all()
+        assert (o[:rows].view(rows, H, HD)[none] == 0).all()
+
+
+ATTEND = [  # new, ctx, H, Hkv, T, page, shared, causal
+    ([1], [0], 4, 4, 2, 16, 0, True),                                  # one key
+    ([1], [511], 8, 2, 2, 16, 0, True),
+    ([1, 1, 1], [63, 64, 65], 4, 1, 1, 64, 0, True),                   # around a tile's end
+    ([1] * 5, [0, 1, 7, 8, 1000], 16, 2, 2, 8, 0, True),               # around a page's end
+    ([1, 0, 3, 0, 2], [30, 50, 129, 0, 0], 4, 2, 2, 32, 0, True),      # sequences without new tokens
+    ([2, 5, 1], [100, 0, 333], 8, 8, 4, 128, 0, True),
+    ([4, 4], [700, 3], 32, 2, 2, 256, 0, True),                        # 64 rows to a key head
+    ([3, 1], [77, 2050], 25, 5, 5, 16, 0, True),                       # groups of five
+    ([2, 3], [200, 90], 10, 1, 1, 1024, 0, True),                      # groups of ten, long pages
+    ([2, 3], [200, 90], 4, 2, 1, 16, 0, False),
+    ([1] * 3, [5, 40, 1], 8, 2, 2, 16, 256, True),                     # a shared prefix of whole pages
+    ([1, 2, 1, 0], [5, 0, 130, 9], 4, 2, 2, 16, 100, True),            # that ends inside a page and a tile
+    ([3, 1], [0, 0], 8, 4, 4, 64, 1030, True),                         # no own context behind it
+    ([2, 1], [300, 10], 8, 2, 2, 32, 70, False),
+    ([1] * 40, [i * 3 for i in range(40)], 2, 2, 2, 8, 512, True),     # 40 rows against the prefix
+    ([1] * 131, [(i * 37) % 300 for i in range(131)], 2, 1, 1, 16, 0, True),  # more sequences than threads
+]
+
+
+@pytest.mark.parametrize("new,ctx,H,Hkv,T,page,shared,causal", ATTEND)
+def test_attend(new, ctx, H, Hkv, T, page, shared, causal):
+    s = ref.make_batch(new, ctx, Hkv, page, shared, spare_rows=2, seed=len(new) + page)
+    cache, batch = _cache(s, H, T, causal)
+    q = _q(s["n"], H, page)
+    out = torch.full((s["n"], H * HD), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, lse = cache.attend(q, batch, shared_len=shared, lse=True, out=out)
+    assert cache.last_device_error() == 0
+    check_attend(s, q, H, o, lse, causal)
+    assert (o[-2:] == 7.0).all()  # rows behind the last sequence stay as they were
+    again, _ = cache.attend(q, batch, shared_len=shared, lse=True)
+    rows = s["cu"][-1].item()
+    assert torch.equal(o[:rows], again[:rows])
+    if shared:  # the same keys, each sequence on its own
+        check_attend(s, q, H, cache.attend(q, batch), None, causal)
+
+
+def test_attend_rows_that_see_nothing():
+    """More new tokens than keys (the first rows see none), and no keys at all."""
+    s = ref.make_batch([3, 2, 4], [40, 0, 0], 2, 16, seed=5)
+    s["lens"] = [43, 0, 2]
+    s["kv_len"].copy_(torch.tensor(s["lens"]))
+    cache, batch = _cache(s, 8, 2)
+    q = _q(s["n"], 8, 1)
+    o, lse = cache.attend(q, batch, lse=True)
+    assert cache.last_device_error() == 0
+    check_attend(s, q, 8, o, lse)
+    # behind a prefix that is longer than some sequences
+    s = ref.make_batch([2, 1, 1], [9, 5, 60], 2, 16, shared=96, seed=6)
+    s["lens"] = [107, 40, 0]
+    s["kv_len"].copy_(torch.tensor(s["lens"]))
+    cache, batch = _cache(s, 8, 2)
+    q = _q(s["n"], 8, 2)
+    o, lse = cache.attend(q, batch, shared_len=96, lse=True)
+    check_attend(s, q, 8, o, lse)
+
+
+def test_attend_long_sequence_among_short_ones():
+    """One sequence takes most of the blocks: its rows are joined from many parts."""
+    s = ref.make_batch([1, 1, 1, 1], [40000, 3, 17, 0], 1, 64, seed=9)
+    cache, batch = _cache(s, 4, 1)
+    q = _q(s["n"], 4, 3)
+    check_attend(s, q, 4, *cache.attend(q, batch, lse=True))
+    s = ref.make_batch([1] * 200, [20000] + [2] * 199, 1, 64, seed=10)
+    cache, batch = _cache(s, 8, 1)
+    q = _q(s["n"], 8, 4)
+    check_attend(s, q, 8, *cache.attend(q, batch, lse=True))
+
+
+def test_attend_sharp_scores():
+    """Scores in the hundreds, rising along the keys: the running maximum moves often."""
+    s = ref.make_batch([1, 2], [900, 2000], 2, 16, seed=11)
+    s["k"].mul_(torch.linspace(0.1, 6, s["k"].shape[0], device="cuda").to(torch.bfloat16)[:, None, None, None])
+    cache, batch = _cache(s, 4, 2)
+    q = _q(s["n"], 4, 5, scale=6.0)
+    check_attend(s, q, 4, *cache.attend(q, batch, lse=True))
+
+
+APPEND = [  # new, ctx, H, Hkv, T, page, rotary, interleaved, scale
+    ([1], [0], 4, 4, 4, 16, 128, False, 1.0),
+    ([1], [1000], 32, 8, 8, 64, 128, False, 1.0),
+    ([1, 0, 7, 2], [5, 9, 15, 16], 8, 2, 2, 8, 64, True, 1.0),
+    ([33, 1], [0, 70000], 4, 1, 1, 32, 96, False, 1.25),
+    ([5, 3], [100000, 2], 10, 2, 1, 16, 16, True, 0.5),
+    ([9, 40], [3, 0], 25, 5, 5, 128, 128, True, 1.0),
+    ([2, 2], [3, 6], 4, 2, 2, 1024, 0, False, 1.0),
+    ([1] * 70, list(range(70)), 2, 2, 1, 8, 32, False, 1.0),
+    ([700, 1300], [12, 1], 4, 2, 2, 64, 128, False, 1.0),              # more rows than blocks
+]
+
+
+@pytest.mark.parametrize("new,ctx,H,Hkv,T,page,rotary,interleaved,scale", APPEND)
+def test_append(new, ctx, H, Hkv, T, page, rotary, interleaved, scale):
+    s = ref.make_batch(new, ctx, Hkv, page, spare_rows=1, seed=3, junk=3.0)
+    freq = 10000.0 ** (-torch.arange(rotary // 2, device="cuda") * 2 / max(rotary, 1)) if rotary else None
+    cache, batch = _cache(s, H, T, inv_freq=freq, interleaved=interleaved, rotary_scale=scale)
+    g = torch.Generator(device="cuda").manual_seed(17)
+    qkv = torch.randn(s["n"], (H + 2 * Hkv) * HD, generator=g, device="cuda").to(torch.bfloat16)
+    k0, v0 = s["k"].clone(), s["v"].clone()
+    q = cache.append(qkv, batch, q=torch.full((s["n"], H * HD), 5.0, dtype=torch.bfloat16, device="cuda"))
+    assert cache.last_device_error() == 0
+    assert (q[-1] == 5.0).all()
+    rows = s["cu"][-1].item()
+    pos = ref.positions(s)
+    x, k, v = (t.double() for t in ref.split_qkv(qkv[:rows], H, Hkv, T))
+    for got, inp in ((q[:rows].view(rows, H, HD), x), (None, k)):
+        want, size = ref.rotate(inp, pos, freq, interleaved, scale)
+        if got is None:  # where the keys were stored
+            seq = torch.bucketize(torch.arange(rows, device="cuda"), s["cu"][1:].long(), right=True)
+            pages = s["table"][seq, pos // page].long()
+            got = s["k"][pages, :, pos % page]
+            assert torch.equal(s["v"][pages, :, pos % page].double(), v)
+            k0[pages, :, pos % page] = got
+            v0[pages, :, pos % page] = s["v"][pages, :, pos % page]
+        assert torch.equal(got[..., rotary:].double(), want[..., rotary:])
+        tol = (1 + U) * (U * want.abs() + 2.0 ** -20 * size)
+        assert ((got.double() - want).abs() <= tol).all()
+    assert torch.equal(k0, s["k"]) and torch.equal(v0, s["v"])  # nothing else was written
+
+
+def test_append_tokens_without_a_place():
+    """More new tokens than kv_len: those at negative positions are not stored, their q is zero."""
+    s = ref.make_batch([4], [6], 2, 16, seed=1, junk=0.0)
+    s["kv_len"].fill_(2)
+    cache, batch = _cache(s, 4, 1)
+    qkv = torch.ones(4, 8 * HD, dtype=torch.bfloat16, device="cuda")
+    k0 = s["k"].clone()
+    q = cache.append(qkv, batch)
+    assert (q[:2] == 0).all() and (q[2:] == 1).all()
+    page = s["table"][0, 0].item()
+    k0[page, :, :2] = 1
+    assert torch.equal(k0, s["k"])
+    assert cache.last_device_error() == _modules()[0].TP_ERR_BATCH
+
+
+def test_bad_batches_are_reported_and_touch_nothing_else():
+    """Pages outside the cache and lengths outside the table: reported, the other
+    sequences' results as ever."""
+    abi = _modules()[0]
+    s = ref.make_batch([1, 1, 1], [100, 60, 200], 2, 16, seed=21)
+    cache, batch = _cache(s, 4, 2)
+    q = _q(s["n"], 4, 6)
+    good = cache.attend(q, batch)
+    assert cache.last_device_error() == abi.TP_OK
+    keep = s["table"].clone()
+    for bad in (-1, s["n_pages"], 2 ** 31 - 1, -2 ** 31):
+        s["table"][1, 2] = bad
+        o = cache.attend(q, batch)
+        assert cache.last_device_error() == abi.TP_ERR_BATCH
+        assert torch.equal(o[0], good[0]) and torch.equal(o[2], good[2]) and torch.isfinite(o).all()
+        k0, v0 = s["k"].clone(), s["v"].clone()
+        s["table"][1, 3] = bad
+        cache.append(torch.ones(3, 8 * HD, dtype=torch.bfloat16, device="cuda"), batch)
+        assert cache.last_device_error() == abi.TP_ERR_BATCH
+        changed = (s["k"] != k0).flatten(1).any(1) & ~s["k"].isnan().flatten(1).any(1)
+        assert not changed[[p for p in range(s["n_pages"]) if p not in keep[[0, 2]].flatten().tolist()]].any()
+        s["k"].copy_(k0)
+        s["v"].copy_(v0)
+        s["table"].copy_(keep)
+    for name, at, bad in (("kv_len", 1, 10 ** 9), ("kv_len", 1, -5), ("cu", 3, 10 ** 6), ("cu", 1, -3)):
+        was = s[name][at].item()
+        s[name][at] = bad
+        o = cache.attend(q, batch)
+        assert cache.last_device_error() == abi.TP_ERR_BATCH, name
+        s[name][at] = was
+    assert torch.equal(cache.attend(q, batch), good)
+    assert cache.last_device_error() == abi.TP_OK
+
+
+def _step(cache, batch, qkv, shared=0):
+    q = cache.append(qkv, batch)
+    return cache.attend(q, batch, shared_len=shared, lse=True)
+
+
+def test_append_then_attend_over_several_steps():
+    """A prompt, then single tokens, page after page: each step's rows against the
+    64-bit form on what the cache then holds."""
+    Hkv, H, T, page = 2, 8, 2, 8
+    full = ref.make_batch([30, 11, 4], [0, 0, 0], Hkv, page, seed=31)
+    freq = 10000.0 ** (-torch.arange(64, device="cuda") / 64)
+    s = dict(full, lens=[9, 3, 0], new=[9, 3, 0])
+    cache, _ = _cache(s, H, T, inv_freq=freq)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for step in range(8):
+        cu = [0] + torch.tensor(s["new"]).cumsum(0).tolist()
+        n = cu[-1]
+        batch = cache.batch(torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                            torch.tensor(s["lens"], dtype=torch.int32, device="cuda"), s["table"], n, max(s["new"]))
+        qkv = torch.randn(n, (H + 2 * Hkv) * HD, generator=g, device="cuda").to(torch.bfloat16)
+        q = cache.append(qkv, batch)
+        o, lse = cache.attend(q, batch, lse=True)
+        assert cache.last_device_error() == 0
+        check_attend(dict(s, cu=batch.cu_tokens), q, H, o, lse)
+        s["new"] = [3, 1, 0 if step < 4 else 1]
+        s["lens"] = [a + b for a, b in zip(s["lens"], s["new"])]
+
+
+def test_two_streams_and_a_graph():
+    """Calls on two streams at once, and a captured step replayed on changed contents."""
+    s = ref.make_batch([1] * 6, [300, 20, 999, 0, 64, 128], 2, 16, shared=64, seed=41)
+    cache, batch = _cache(s, 16, 2, inv_freq=10000.0 ** (-torch.arange(32, device="cuda") / 32))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = [torch.randn(s["n"], 20 * HD, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    eager = []
+    for x in qkv:
+        o, lse = _step(cache, batch, x, 64)
+        eager.append((o.clone(), lse.clone()))
+    qs = [cache.append(x, batch).clone() for x in qkv]
+    cache.append(qkv[0], batch)
+    torch.cuda.synchronize()
+    one = [cache.attend(q, batch, shared_len=64) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for st, q, out in zip(streams, qs, got):
+            with torch.cuda.stream(st):
+                out.append(cache.attend(q, batch, shared_len=64))
+    torch.cuda.synchronize()
+    for out, want in zip(got, one):
+        assert all(torch.equal(o, want) for o in out)
+    graphs, held = [], []
+    x = qkv[0].clone()
+    for _ in range(2):  # two graphs of the same calls
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held.append(_step(cache, batch, x, 64))
+        graphs.append(graph)
+    for i in (1, 2, 0):
+        x.copy_(qkv[i])
+        for graph, (o, lse) in zip(graphs, held):
+            o.fill_(9)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, eager[i][0]) and torch.equal(lse, eager[i][1])
+
+
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("new,ctx,shared", [([1] * 5, [3, 50, 0, 7, 200], 48), ([2, 1, 5], [16, 90, 0], 0)])
+def test_decode_is_the_composition(new, ctx, shared, fused):
+    """TensorParallelAttention.decode against its parts called one by one, and the
+    parts' projections against 64 bits."""
+    abi, Attention, _, Cache = _modules()
+    H, Hkv, T, d, page = 8, 2, 2, 512, 16
+    s = ref.make_batch(new, ctx, Hkv, page, shared, seed=51)
+    attn = Attention(d, H, Hkv, HD, T)
+    freq = 10000.0 ** (-torch.arange(64, device="cuda") / 64)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w = lambda *sh: (torch.randn(*sh, generator=g, device="cuda") / math.sqrt(sh[1])).to(torch.bfloat16)
+    Wq, Wk, Wv, Wo = w(H * HD, d), w(Hkv * HD, d), w(Hkv * HD, d), w(d, H * HD)
+    wqkv, wo = attn.pack(Wq, Wk, Wv, Wo)
+    x = torch.randn(s["n"], d, generator=g, device="cuda").to(torch.bfloat16)
+    pages = []
+    for _ in range(2):
+        cache = Cache(attn, s["n_pages"], page, k=s["k"].clone(), v=s["v"].clone(), inv_freq=freq)
+        pages.append((cache, cache.batch(s["cu"], s["kv_len"], s["table"], s["n"], s["max_new"])))
+    (c0, b0), (c1, b1) = pages
+    y = attn.decode(x, c0, b0, wqkv, wo, shared_len=shared, fused=fused)
+    assert c0.last_device_error() == abi.TP_OK
+    # the parts: x is rounded to bf16 after the q/k/v projection
+    z = torch.cat([x.double() @ W.double().T for W in (Wq, Wk, Wv)], 1)
+    order = []
+    for t in range(T):
+        for first, heads in ((0, H), (H, Hkv), (H + Hkv, Hkv)):
+            order += range((first + t * heads // T) * HD, (first + (t + 1) * heads // T) * HD)
+    qkv = z[:, order].to(torch.bfloat16).contiguous()
+    q = c1.append(qkv, b1)
+    o = c1.attend(q, b1, shared_len=shared)
+    want = o.double() @ Wo.double().T
+    # the two paths round q, k, v alike but where the 32-bit product falls on the
+    # other side of a rounding border; both outputs are rounded once: in root mean
+    # square both stay below 2^-8 each
+    rel = ((y.double() - want).square().mean() / want.square().mean()).sqrt()
+    assert rel <= 2 * U, rel.item()
+    new_k = (c0.k.double() - c1.k.double()).nan_to_num().abs()
+    assert (new_k <= 2 * U * c1.k.double().nan_to_num().abs() + 2.0 ** -16).all()
+
+
+def test_decode_matches_the_training_forward():
+    """Without rotation, a whole sequence through decode is the causal forward."""
+    abi, Attention, _, Cache = _modules()
+    H, Hkv, T, d = 4, 2, 2, 256
+    attn = Attention(d, H, Hkv, HD, T)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    w = lambda *sh: (torch.randn(*sh, generator=g, device="cuda") / math.sqrt(sh[1])).to(torch.bfloat16)
+    wqkv, wo = attn.pack(w(H * HD, d), w(Hkv * HD, d), w(Hkv * HD, d), w(d, H * HD))
+    S = 24
+    x = torch.randn(S, d, generator=g, device="cuda").to(torch.bfloat16)
+    y, _ = attn.forward(x, 1, S, wqkv, wo)
+    cache = Cache(attn, 4, 16)
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    got = [attn.decode(x[:7].contiguous(), cache, cache.batch(i32(0, 7), i32(7), table, 7, 7), wqkv, wo)]
+    for t in range(7, S):
+        got.append(attn.decode(x[t:t + 1].contiguous(), cache, cache.batch(i32(0, 1), i32(t + 1), table, 1, 1),
+                               wqkv, wo))
+    rel = ((torch.cat(got).double() - y.double()).square().mean() / y.double().square().mean()).sqrt()
+    assert rel <= 2 * U, rel.item()  # each side rounds its probabilities and outputs, 2^-8 in root mean square
