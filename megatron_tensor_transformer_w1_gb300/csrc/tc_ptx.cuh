@@ -192,11 +192,103 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 2^x by the SFU instruction (ex2.approx, flush-to-zero): a few ulp, far
+// below the bf16 rounding the probabilities get next; 2^-inf = 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tcgen05.mma with the A operand in tensor memory: for kind::f16 each 32-bit
+// TMEM cell of a lane holds two consecutive K elements of that row (the
+// lower K index in the low half), so one K = 16 step spans 8 columns.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled tile (version 1, SBO 1024).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// K-major operand: `rows` rows x 128 K-columns held as two 64-column boxes of
+// rows*128 bytes; K step ks covers columns [16 ks, 16 ks + 16).
+__device__ __forceinline__ uint64_t kdesc(uint32_t tile, int rows, int ks) {
+  return sw128_desc(tile + static_cast<uint32_t>((ks >> 2) * rows * 128 + (ks & 3) * 32), 16);
+}
+// MN-major operand: `krows` rows along K, 128 M/N columns held as two boxes
+// of krows*128 bytes; K step ks covers rows [16 ks, 16 ks + 16).
+__device__ __forceinline__ uint64_t mndesc(uint32_t tile, int krows, int ks) {
+  return sw128_desc(tile + static_cast<uint32_t>(ks * 2048), static_cast<uint32_t>(krows * 128));
+}
+// Instruction descriptor, kind::f16, M = 128, bf16 x bf16 -> fp32.
+__host__ __device__ constexpr uint32_t idesc(int N, int amn, int bmn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(amn) << 15) |
+         (static_cast<uint32_t>(bmn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+// Address of 16-byte chunk col8 (= column / 8) of row r of a thread-written
+// K-major swizzled tile of `rows` rows (the layout TMA's 128-byte swizzle
+// gives: chunk index XOR row mod 8 inside each 1024-byte group of 8 rows).
+__device__ __forceinline__ uint32_t sw_chunk(uint32_t tile, int rows, int r, int col8) {
+  return tile + static_cast<uint32_t>((col8 >> 3) * rows * 128 + r * 128 + (((col8 & 7) ^ (r & 7)) << 4));
+}
+
+struct Waiter {
+  volatile int* abort_flag;
+  int* err;
+  unsigned long long timeout_ns;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    return wait_bounded_raw(bar, parity, abort_flag, err, timeout_ns, true);
+  }
+  // drain wait: ignores the abort flag
+  __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
+    wait_bounded_raw(bar, parity, abort_flag, err, timeout_ns, false);
+  }
+  // warp-uniform wait of the softmax warps
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    const bool ok = wait_bounded_raw(bar, parity, abort_flag, err, timeout_ns, true);
+    return __all_sync(0xffffffffu, ok) != 0;
+  }
+};
+
 // Host: 3-D bf16 tensor map {dims[0] (contiguous), dims[1], dims[2]} with
 // the given byte strides of dims 1 and 2, 128-byte swizzle and zero fill out
 // of bounds.  Returns 0 or a TP_ERR_* code.
 int encode_map_3d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[3], const uint64_t strides_bytes[2],
                        const uint32_t box[3]);
+// The same in four dimensions.
+int encode_map_4d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[4], const uint64_t strides_bytes[3],
+                       const uint32_t box[4]);
 
 }  // namespace tc
 }  // namespace tpffn

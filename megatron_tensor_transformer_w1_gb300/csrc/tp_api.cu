@@ -1444,7 +1444,7 @@ int kv_sizes(const tp_attn_plan* a, const tp_kv_batch* b, int64_t page_size, int
   if (b->n_seqs > kMaxKvTokens || b->n_tokens > kMaxKvTokens) return TP_ERR_UNSUPPORTED;
   if (b->n_seqs > 0 && b->n_tokens > 0 && (b->max_new < 1 || b->max_pages < 1)) return TP_ERR_INVALID;
   if (b->max_pages > (int64_t(1) << 27)) return TP_ERR_UNSUPPORTED;
-  if (b->n_tokens * (a->H / a->Hkv) > INT32_MAX || b->n_seqs * a->Hkv > INT32_MAX) return TP_ERR_UNSUPPORTED;
+  if (b->n_tokens * a->H > INT32_MAX / 2 || b->n_seqs * a->Hkv > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
   sp.H = a->H;
   sp.Hkv = a->Hkv;
   sp.T_p = a->T_p;

@@ -23,6 +23,7 @@ namespace tpffn {
 namespace kv {
 using tc::grid_dep_launch;
 using tc::grid_dep_wait;
+using tc::ex2;
 using tc::pack_bf16x2;
 using tc::smem_u32;
 
@@ -186,19 +187,6 @@ struct Few {
   static constexpr int SMEM = STAGES * STAGE + 1024;
 };
 
-struct FewParams {
-  Batch b;
-  const __nv_bfloat16* q;  // [n_tokens][H * HD]
-  __nv_bfloat16* o;        // [n_tokens][H * HD]
-  float* lse;              // [n_tokens][H] or null
-  float* part_o;           // [slots][rows][HD]
-  float2* part_ml;         // [slots][rows]
-  long long* sched;        // [B + 1] tiles per key/value head before sequence b
-  int rows;                // rows of a slot
-  float scale_log2;
-  int* status;
-};
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -233,149 +221,10 @@ __device__ __forceinline__ uint32_t tile_chunk(uint32_t tile, int r, int c) {
   return tile + static_cast<uint32_t>(r * 256 + ((c ^ (r & 7)) << 4));
 }
 
-// Where a block's copies stand: sequence, head, tile of the item.
-struct Cursor {
-  int b, h, t, t0, nt;  // tile t of [0, nt) holds the keys from (t0 + t) * KT on
-  Seq s;
-};
-
-// Prefix items: all sequences' rows as one, over the shared keys.
-template <bool PREFIX>
-__device__ __forceinline__ int tiles_of(const Batch& p, const Seq& s, int& t0) {
-  t0 = PREFIX ? 0 : p.shared / KT;
-  const int lo = PREFIX ? 0 : p.shared;
-  return (s.qn > 0 && s.kv > lo) ? (s.kv + KT - 1) / KT - t0 : 0;
-}
-
-struct Sched {
-  long long total;   // tiles of all items
-  long long blocks;  // blocks that get any: min(gridDim.x, total)
-  int table_row;     // whose page table leads to the shared pages
-};
-
-// Sums the tiles of all sequences, finds the block's first tile and, in
-// block 0, leaves the prefix sums for the combine kernel.  128 threads.
-template <bool PREFIX>
-__device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Cursor& c, long long& first,
-                                          long long& last, int* err) {
-  __shared__ long long sums[128];
-  __shared__ int s_best[128], s_len[128];
-  __shared__ int s_b;
-  __shared__ long long s_before;
-  const int tid = threadIdx.x;
-  Sched S{};
-  if constexpr (PREFIX) {
-    // the longest sequence's table covers the shared pages if any does
-    int best = 0, len = -1;
-    for (int b = tid; b < p.B; b += 128) {
-      const int l = min(max(p.kv_len[b], 0), p.cap);
-      if (l > len) { len = l; best = b; }
-    }
-    s_best[tid] = best;
-    s_len[tid] = len;
-    __syncthreads();
-    for (int d = 64; d; d >>= 1) {
-      if (tid < d) {
-        const int ol = s_len[tid + d], ob = s_best[tid + d];
-        if (ol > s_len[tid] || (ol == s_len[tid] && ob < s_best[tid])) { s_len[tid] = ol; s_best[tid] = ob; }
-      }
-      __syncthreads();
-    }
-    S.table_row = s_best[0];
-    c.s.q0 = 0;
-    c.s.qn = min(max(p.cu[p.B], 0), p.n_tokens);
-    c.s.kv = min(p.shared, s_len[0]);
-    c.nt = tiles_of<true>(p, c.s, c.t0);
-    S.total = static_cast<long long>(c.nt) * p.Hkv;
-    if (blockIdx.x == 0 && tid == 0) {
-      sched[0] = 0;
-      sched[1] = c.nt;
-    }
-    c.b = 0;
-    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
-    if (blockIdx.x >= S.blocks) { first = last = 0; return S; }
-    first = first_tile(blockIdx.x, S.total, S.blocks);
-    last = first_tile(blockIdx.x + 1, S.total, S.blocks);
-    c.h = static_cast<int>(first / c.nt);
-    c.t = static_cast<int>(first - static_cast<long long>(c.h) * c.nt);
-    return S;
-  } else {
-    const int per = (p.B + 127) / 128;
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      int t0;
-      const Seq s = load_seq(p, b);
-      *err |= s.err;
-      sum += tiles_of<false>(p, s, t0);
-    }
-    sums[tid] = sum;
-    __syncthreads();
-    for (int d = 1; d < 128; d <<= 1) {
-      const long long add = tid >= d ? sums[tid - d] : 0;
-      __syncthreads();
-      sums[tid] += add;
-      __syncthreads();
-    }
-    const long long before = sums[tid] - sum;
-    S.total = sums[127] * p.Hkv;
-    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
-    if (blockIdx.x == 0) {
-      long long at = before;
-      for (int b = b0; b < b1; ++b) {
-        int t0;
-        sched[b] = at;
-        at += tiles_of<false>(p, load_seq(p, b), t0);
-      }
-      if (tid == 127) sched[p.B] = sums[127];
-    }
-    if (blockIdx.x >= S.blocks) { first = last = 0; return S; }
-    first = first_tile(blockIdx.x, S.total, S.blocks);
-    last = first_tile(blockIdx.x + 1, S.total, S.blocks);
-    if (first >= before * p.Hkv && first < (before + sum) * p.Hkv) {
-      long long at = before;
-      for (int b = b0; b < b1; ++b) {
-        int t0;
-        const int nt = tiles_of<false>(p, load_seq(p, b), t0);
-        if (first < (at + nt) * p.Hkv) {
-          s_b = b;
-          s_before = at;
-          break;
-        }
-        at += nt;
-      }
-    }
-    __syncthreads();
-    c.b = s_b;
-    c.s = load_seq(p, c.b);
-    c.nt = tiles_of<false>(p, c.s, c.t0);
-    const long long in = first - s_before * p.Hkv;
-    c.h = static_cast<int>(in / c.nt);
-    c.t = static_cast<int>(in - static_cast<long long>(c.h) * c.nt);
-    return S;
-  }
-}
-
-// The next tile; past an item's end the next head, past the last head the
-// next sequence that has tiles (the caller knows that there is one).
-template <bool PREFIX>
-__device__ __forceinline__ void advance(const Batch& p, Cursor& c) {
-  if (++c.t < c.nt) return;
-  c.t = 0;
-  if (++c.h < p.Hkv) return;
-  c.h = 0;
-  if constexpr (!PREFIX) {
-    do {
-      ++c.b;
-      c.s = load_seq(p, c.b);
-      c.nt = tiles_of<false>(p, c.s, c.t0);
-    } while (c.nt == 0);
-  }
-}
-
 template <int WR, bool PREFIX>
-__global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ AttendParams p) {
   using F = Few<WR>;
+  using C = Cut<PREFIX, KT, 0>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   __shared__ float2 s_ml[4][16];
@@ -389,21 +238,20 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
   grid_dep_launch();
   int err = 0;
   Cursor c;
-  long long tile, last;
-  const Sched S = schedule<PREFIX>(B, p.sched, c, tile, last, &err);
+  const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem), c, &err);
   __syncthreads();
-  if (tile >= last) {
+  const int n_tiles = S.n_tiles, t0 = C::t0(B), lo = C::first_key(B);
+  if (n_tiles == 0) {
     if (err) atomicOr(&s_err, err);
     __syncthreads();
     if (tid == 0) p.status[blockIdx.x] = s_err;
     return;
   }
-  const int n_tiles = static_cast<int>(last - tile);
 
   // page of 8-key group `lane` (< 8) of the cursor's tile, or -1
   auto page_of_group = [&](const Cursor& x) -> int {
     if (lane >= 8) return -1;
-    const int key = (x.t0 + x.t) * KT + lane * 8;
+    const int key = (t0 + x.t) * KT + lane * 8;
     if (key >= x.s.kv) return -1;
     const int row = PREFIX ? S.table_row : x.b;
     const int page = B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
@@ -416,10 +264,9 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
   auto issue = [&](int stage, const Cursor& x, int group_page, bool new_item) {
     const uint32_t ks = smem_u32(smem + stage * F::STAGE), vs = ks + F::KV_BYTES, qs = vs + F::KV_BYTES;
     const int ch = tid & 15, r0 = tid >> 4;
-    const int lo = PREFIX ? 0 : B.shared;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = r0 + 8 * i, key = (x.t0 + x.t) * KT + r;
+      const int r = r0 + 8 * i, key = (t0 + x.t) * KT + r;
       const int page = __shfl_sync(0xffffffffu, group_page, i);
       const bool ok = page >= 0 && key >= lo && key < x.s.kv;
       const long long off =
@@ -451,7 +298,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
     if (issued < n_tiles) {
       issue(s, c, group_page, issued == 0 || c.t == 0);
       if (++issued < n_tiles) {
-        advance<PREFIX>(B, c);
+        advance<C, PREFIX>(B, c);
         group_page = page_of_group(c);
       }
     }
@@ -462,8 +309,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
   float m[2], l[2];
   uint32_t qf[8][4];
   int limit[2] = {0, 0};
-  bool fresh = true;      // the next tile starts a segment
-  int seg_t = 0;          // its first tile within the item
+  bool fresh = true;         // the next tile starts a segment
+  int seg_t = 0, seg_i = 0;  // its first tile within the item, and of the block's
   for (int i = 0; i < n_tiles; ++i) {
     const int stage = i % F::STAGES;
     cp_async_wait<F::STAGES - 2>();
@@ -472,7 +319,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
     if (issued < n_tiles) {
       issue((i + F::STAGES - 1) % F::STAGES, c, group_page, c.t == 0);
       if (++issued < n_tiles) {
-        advance<PREFIX>(B, c);
+        advance<C, PREFIX>(B, c);
         group_page = page_of_group(c);
       }
     }
@@ -482,6 +329,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
     const int rows = x.s.qn * B.G;
     if (fresh) {
       seg_t = x.t;
+      seg_i = i;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
 #pragma unroll
@@ -513,8 +361,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
     }
     if (rg * 16 < rows) {
       const int key0 = kg * 16 * F::NB;  // this warp's keys of the tile
-      const int base = (x.t0 + x.t) * KT + key0;
-      const int lo = PREFIX ? 0 : B.shared;
+      const int base = (t0 + x.t) * KT + key0;
       float s[F::NB][2][4];
 #pragma unroll
       for (int nb = 0; nb < F::NB; ++nb) {
@@ -609,8 +456,9 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
           make_float2(o[j][2], o[j][3]);
     }
     __syncthreads();
-    const bool whole = !PREFIX && B.shared == 0 && seg_t == 0 && x.t + 1 == x.nt;
-    const long long slot = static_cast<long long>(x.b) * B.Hkv + x.h + blockIdx.x;
+    const bool whole = seg_t == 0 && x.t + 1 == x.nt;
+    const bool direct = whole && !PREFIX && B.shared == 0;
+    const long long slot = (2ll * blockIdx.x + (seg_i ? 1 : 0)) * p.part.slot_rows;
 #pragma unroll
     for (int a = 0; a < WR; ++a) {
       const int r16 = tid >> 3, r = a * 16 + r16;
@@ -625,6 +473,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
           lr += ml.y * f[g];
         }
         const int tok = x.s.q0 + r / B.G, head = x.h * B.G + r % B.G;
+        const long long row = static_cast<long long>(tok) * B.H + head;
+        float* part_o = whole ? p.part.row_o + row * HD : p.part.slot_o + (slot + r) * HD;
         const float inv = lr > 0.f ? 1.f / lr : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -639,20 +489,20 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
             v.z += w.z * f[g];
             v.w += w.w * f[g];
           }
-          if (whole) {
+          if (direct) {
             uint2 w;
             w.x = pack_bf16x2(v.x * inv, v.y * inv);
             w.y = pack_bf16x2(v.z * inv, v.w * inv);
-            *reinterpret_cast<uint2*>(p.o + (static_cast<long long>(tok) * B.H + head) * HD + col) = w;
+            *reinterpret_cast<uint2*>(p.o + row * HD + col) = w;
           } else {
-            *reinterpret_cast<float4*>(p.part_o + (slot * p.rows + r) * HD + col) = v;
+            *reinterpret_cast<float4*>(part_o + col) = v;
           }
         }
         if ((tid & 7) == 0) {
-          if (!whole)
-            p.part_ml[slot * p.rows + r] = make_float2(mr, lr);
+          if (!direct)
+            (whole ? p.part.row_ml[row] : p.part.slot_ml[slot + r]) = make_float2(mr, lr);
           else if (p.lse)
-            p.lse[static_cast<long long>(tok) * B.H + head] = lr > 0.f ? mr + log2f(lr) : -INFINITY;
+            p.lse[row] = lr > 0.f ? mr + log2f(lr) : -INFINITY;
         }
       }
     }
@@ -668,78 +518,56 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const FewParams p) {
 // unnormalised output of part i, m = max m_i, l = sum l_i 2^(m_i - m),
 // o = sum O_i 2^(m_i - m) / l, always in the order of the parts, so that a
 // result does not change from run to run.  A row without any key gets zeros.
-// Bound by latency: the parts lie in L2.  A warp per row; rows cut into many
-// parts (a long sequence on many blocks) are taken by all eight warps.
-struct PartSrc {
-  const float* o = nullptr;
-  const float2* ml = nullptr;
-  const long long* sched = nullptr;
-  int rows = 0, grid = 0;
-};
+// Bound by latency: the parts lie in L2.  A block takes an item's rows, a
+// few of them at a time; where there are few rows in all, several warps share
+// one, so that the many parts of a long sequence are read at once.
 struct CombineParams {
   Batch b;
-  PartSrc own, shared;   // shared.o null: no shared keys
+  Parts own, shared;     // shared.sched null: no shared keys
   __nv_bfloat16* o;
   float* lse;
-  int rows_per_block;    // 1 or 8
-  int many;              // more parts than this: all warps
+  int rows_per_block;    // 1, 2, 4 or 8
   int* header;           // see kKvHeaderBytes
   int alone, status_words;
 };
 
-struct RowParts {
-  long long own0, sh0;   // first slots
-  int n_own, n;          // parts of the sequence's own keys, parts in all
-  int r_own, r_sh;       // the row within the slots
-  int tok, head;
-  bool direct;           // already written, or nobody's row
+// The parts of an item's rows: block c's slot of rows for c of [c0, c1], or
+// the rows' own places.
+struct ItemParts {
+  int n = 0;
+  long long c0 = 0;
+  int second = 0;        // the first part lies in its block's second slot
+  __device__ __forceinline__ void set(const Parts& P, long long start, long long nt, long long total) {
+    const long long C = total < P.grid ? total : P.grid;
+    c0 = block_of_tile(start, total, C);
+    n = static_cast<int>(block_of_tile(start + nt - 1, total, C) - c0) + 1;
+    second = start != first_tile(c0, total, C);
+  }
+  __device__ __forceinline__ long long slot(const Parts& P, int i, int r) const {
+    return (2 * (c0 + i) + (i == 0 ? second : 0)) * P.slot_rows + r;
+  }
+};
+struct Row {
+  ItemParts own, sh;
+  int r_own, r_sh;
+  long long at;  // token * H + head
+  __device__ __forceinline__ int n() const { return own.n + sh.n; }
+  __device__ __forceinline__ float2 ml(const CombineParams& p, int i) const {
+    const bool mine = i < own.n;
+    const Parts& P = mine ? p.own : p.shared;
+    const ItemParts& I = mine ? own : sh;
+    return I.n == 1 ? P.row_ml[at] : P.slot_ml[I.slot(P, mine ? i : i - own.n, mine ? r_own : r_sh)];
+  }
+  __device__ __forceinline__ float4 o(const CombineParams& p, int i, int lane) const {
+    const bool mine = i < own.n;
+    const Parts& P = mine ? p.own : p.shared;
+    const ItemParts& I = mine ? own : sh;
+    const float* base =
+        I.n == 1 ? P.row_o + at * HD : P.slot_o + I.slot(P, mine ? i : i - own.n, mine ? r_own : r_sh) * HD;
+    return reinterpret_cast<const float4*>(base)[lane];
+  }
 };
 
-__device__ __forceinline__ RowParts row_parts(const CombineParams& p, long long row) {
-  const Batch& B = p.b;
-  RowParts R{};
-  R.direct = true;
-  if (row >= static_cast<long long>(B.n_tokens) * B.H) return R;
-  R.tok = static_cast<int>(row / B.H);
-  R.head = static_cast<int>(row - static_cast<long long>(R.tok) * B.H);
-  const int b = find_seq_warp(B.cu, B.B, R.tok);
-  if (b >= B.B) return R;
-  const Seq s = load_seq(B, b);
-  if (R.tok < s.q0 || R.tok >= s.q0 + s.qn) return R;
-  const int h = R.head / B.G, g = R.head - h * B.G;
-  const long long before = p.own.sched[b], nt = p.own.sched[b + 1] - before;
-  if (nt > 0) {
-    const long long T = p.own.sched[B.B] * B.Hkv, C = T < p.own.grid ? T : p.own.grid;
-    const long long t0 = before * B.Hkv + h * nt;
-    const long long c0 = block_of_tile(t0, T, C), c1 = block_of_tile(t0 + nt - 1, T, C);
-    R.own0 = static_cast<long long>(b) * B.Hkv + h + c0;
-    R.n_own = static_cast<int>(c1 - c0) + 1;
-    R.r_own = (R.tok - s.q0) * B.G + g;
-  }
-  R.n = R.n_own;
-  if (p.shared.o) {
-    const long long snt = p.shared.sched[1];
-    if (snt > 0) {
-      const long long T = snt * B.Hkv, C = T < p.shared.grid ? T : p.shared.grid;
-      const long long c0 = block_of_tile(h * snt, T, C), c1 = block_of_tile((h + 1) * snt - 1, T, C);
-      R.sh0 = h + c0;
-      R.n += static_cast<int>(c1 - c0) + 1;
-      R.r_sh = R.tok * B.G + g;
-    }
-  }
-  R.direct = !p.shared.o && R.n == 1;
-  return R;
-}
-
-__device__ __forceinline__ float2 part_ml(const CombineParams& p, const RowParts& R, int i) {
-  return i < R.n_own ? p.own.ml[(R.own0 + i) * p.own.rows + R.r_own]
-                     : p.shared.ml[(R.sh0 + i - R.n_own) * p.shared.rows + R.r_sh];
-}
-__device__ __forceinline__ float4 part_o(const CombineParams& p, const RowParts& R, int i) {
-  const float* base = i < R.n_own ? p.own.o + ((R.own0 + i) * p.own.rows + R.r_own) * HD
-                                  : p.shared.o + ((R.sh0 + i - R.n_own) * p.shared.rows + R.r_sh) * HD;
-  return reinterpret_cast<const float4*>(base)[threadIdx.x & 31];
-}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
@@ -750,117 +578,113 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-// parts first, first + step, ... of a row: sum of O_i 2^(m_i - m)
-__device__ __forceinline__ float4 sum_parts(const CombineParams& p, const RowParts& R, float m, int first, int step) {
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = first; i < R.n; i += step) {
-    const float f = ex2(part_ml(p, R, i).x - m);
-    const float4 v = part_o(p, R, i);
-    a.x += f * v.x;
-    a.y += f * v.y;
-    a.z += f * v.z;
-    a.w += f * v.w;
-  }
-  return a;
-}
-__device__ __forceinline__ void write_row(const CombineParams& p, const RowParts& R, float4 a, float m, float l) {
-  const int lane = threadIdx.x & 31;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const long long row = static_cast<long long>(R.tok) * p.b.H + R.head;
-  uint2 w;
-  w.x = pack_bf16x2(a.x * inv, a.y * inv);
-  w.y = pack_bf16x2(a.z * inv, a.w * inv);
-  reinterpret_cast<uint2*>(p.o + row * HD)[lane] = w;
-  if (p.lse && lane == 0) p.lse[row] = l > 0.f ? m + log2f(l) : -INFINITY;
-}
 
-__global__ void __launch_bounds__(256) kv_combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__ CombineParams p) {
   __shared__ float4 s_acc[8][32];
-  __shared__ int s_many[8];
   grid_dep_wait();
   grid_dep_launch();
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  const Batch& B = p.b;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     p.header[2] = p.status_words;
     if (p.alone) p.header[0] = p.header[1] = 0;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row0 = static_cast<long long>(blockIdx.x) * p.rows_per_block;
-  if (warp < p.rows_per_block) {
-    const RowParts R = row_parts(p, row0 + warp);
-    const bool many = R.n > p.many;
-    if (lane == 0) s_many[warp] = many && !R.direct;
-    if (!R.direct && !many) {
-      const float2 ml = lane < R.n ? part_ml(p, R, lane) : make_float2(-INFINITY, 0.f);
-      const float m = warp_max(ml.x);
-      const float l = m == -INFINITY ? 0.f : warp_sum(ml.y * ex2(ml.x - m));
-      const float4 a = m == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : sum_parts(p, R, m, 0, 1);
-      write_row(p, R, a, m, l);
+  // the item: a sequence, a key/value head and, of the many-rows kernel, a
+  // row tile (sequence b's row tiles start at cu[b] G / RT + b)
+  const int h = blockIdx.x % B.Hkv, u = blockIdx.x / B.Hkv;
+  int b = u, rt = 0;
+  if (p.own.rt) {
+    int lo = 0, hi = B.B;
+    auto first = [&](int x) {
+      return min(max(B.cu[x], 0), B.n_tokens) * static_cast<long long>(B.G) / p.own.rt + x;
+    };
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first(mid) <= u) lo = mid; else hi = mid;
     }
+    b = lo;
+    rt = static_cast<int>(u - first(b));
   }
-  __syncthreads();
-  for (int k = 0; k < p.rows_per_block; ++k) {
-    if (!s_many[k]) continue;
-    const RowParts R = row_parts(p, row0 + k);
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < R.n; i += 32) m = fmaxf(m, part_ml(p, R, i).x);
+  const Seq s = load_seq(B, b);
+  const int rows = min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
+  const int row0 = blockIdx.y * p.rows_per_block;
+  if (row0 >= rows) return;
+  Row R{};
+  {
+    const long long before = p.own.sched[b], per_head = p.own.sched[b + 1] - before;
+    long long nt = per_head, pre = 0;
+    if (p.own.rt) {
+      using C = Cut<false, 128, RT_MANY>;
+      nt = C::tiles(B, s, rt);
+      int sum = 0;
+      for (int i = lane; i < rt; i += 32) sum += C::tiles(B, s, i);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      pre = sum;
+    }
+    if (nt > 0) R.own.set(p.own, before * B.Hkv + h * per_head + pre, nt, p.own.sched[B.B] * B.Hkv);
+  }
+  if (!p.shared.sched && R.own.n == 1) return;  // written by the block that had it whole
+  const int per_row = 8 / p.rows_per_block;     // warps
+  const int wr = warp / per_row, wp = warp - wr * per_row;
+  const int r = row0 + wr;
+  const bool live = r < rows;
+  float m = -INFINITY, l = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    const int item_row = rt * p.own.rt + r, tok = s.q0 + item_row / B.G, g = item_row % B.G;
+    R.r_own = r;
+    R.at = static_cast<long long>(tok) * B.H + h * B.G + g;
+    if (p.shared.sched) {
+      const long long nt = p.shared.sched[0], n_rt = p.shared.sched[1];
+      if (nt > 0) {
+        const int all = tok * B.G + g, srt = p.shared.rt ? all / p.shared.rt : 0;
+        R.r_sh = all - srt * p.shared.rt;
+        R.sh.set(p.shared, (h * n_rt + srt) * nt, nt, nt * n_rt * B.Hkv);
+      }
+    }
+    const int n = R.n();
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, R.ml(p, i).x);
     m = warp_max(m);
     if (m != -INFINITY) {
-      for (int i = lane; i < R.n; i += 32) {
-        const float2 ml = part_ml(p, R, i);
+      for (int i = lane; i < n; i += 32) {
+        const float2 ml = R.ml(p, i);
         l += ml.y * ex2(ml.x - m);
       }
       l = warp_sum(l);
-      s_acc[warp][lane] = sum_parts(p, R, m, warp, 8);
-    } else {
-      s_acc[warp][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      float4 a = s_acc[0][lane];
-      for (int w = 1; w < 8; ++w) {
-        const float4 v = s_acc[w][lane];
-        a.x += v.x;
-        a.y += v.y;
-        a.z += v.z;
-        a.w += v.w;
+#pragma unroll 4
+      for (int i = wp; i < n; i += per_row) {
+        const float f = ex2(R.ml(p, i).x - m);
+        const float4 v = R.o(p, i, lane);
+        a.x += f * v.x;
+        a.y += f * v.y;
+        a.z += f * v.z;
+        a.w += f * v.w;
       }
-      write_row(p, R, a, m, l);
     }
-    __syncthreads();
   }
+  if (per_row > 1) {
+    s_acc[warp][lane] = a;
+    __syncthreads();
+    if (wp) return;
+    for (int w = 1; w < per_row; ++w) {
+      const float4 v = s_acc[warp + w][lane];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+  }
+  if (!live) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint2 w;
+  w.x = pack_bf16x2(a.x * inv, a.y * inv);
+  w.y = pack_bf16x2(a.z * inv, a.w * inv);
+  reinterpret_cast<uint2*>(p.o + R.at * HD)[lane] = w;
+  if (p.lse && lane == 0) p.lse[R.at] = l > 0.f ? m + log2f(l) : -INFINITY;
 }
 
 // ================================================================ host
-// Launch as a programmatic dependent of the stream's previous kernel.
-template <typename P>
-void launch_dep(void (*kern)(P), int grid, int block, int smem, cudaStream_t stream, const P& p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(block));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-template <typename K>
-int set_smem_once(K kern, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return TP_ERR_CUDA;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(done.load() & bit)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-      return TP_ERR_CUDA;
-    done.fetch_or(bit);
-  }
-  return TP_OK;
-}
-
 Batch make_batch(const KvSpec& a) {
   Batch b{};
   b.k = static_cast<__nv_bfloat16*>(a.k);
@@ -886,19 +710,19 @@ Batch make_batch(const KvSpec& a) {
 int few_blocks(int num_sms) { return 2 * num_sms; }
 
 template <int WR, bool PREFIX>
-int launch_few_inst(const FewParams& p, LaunchCtx& ctx, const char* name) {
+int launch_few_inst(const AttendParams& p, LaunchCtx& ctx, const char* name) {
   static std::atomic<uint64_t> done{0};
   if (int rc = set_smem_once(kv_few_kernel<WR, PREFIX>, Few<WR>::SMEM, done)) return rc;
   if (ctx.before) ctx.before(ctx.user, name, ctx.stream);
-  launch_dep(kv_few_kernel<WR, PREFIX>, few_blocks(ctx.num_sms), 128, Few<WR>::SMEM, ctx.stream, p);
+  launch_dep(kv_few_kernel<WR, PREFIX>, dim3(p.part.grid), 128, Few<WR>::SMEM, ctx.stream, p);
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
   return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 template <bool PREFIX>
-int launch_few(const FewParams& p, LaunchCtx& ctx, const char* name) {
-  if (p.rows <= 16) return launch_few_inst<1, PREFIX>(p, ctx, name);
-  if (p.rows <= 32) return launch_few_inst<2, PREFIX>(p, ctx, name);
+int launch_few(const AttendParams& p, LaunchCtx& ctx, const char* name) {
+  if (p.part.slot_rows <= 16) return launch_few_inst<1, PREFIX>(p, ctx, name);
+  if (p.part.slot_rows <= 32) return launch_few_inst<2, PREFIX>(p, ctx, name);
   return launch_few_inst<4, PREFIX>(p, ctx, name);
 }
 
@@ -925,7 +749,7 @@ int launch_kv_append(const KvSpec& a, const KvRotation& r, const void* qkv, void
   p.alone = alone;
   const int most = 8 * ctx.num_sms < kKvStatusWords ? 8 * ctx.num_sms : kKvStatusWords;
   if (ctx.before) ctx.before(ctx.user, "kv_append", ctx.stream);
-  kv::launch_dep(kv::kv_append_kernel, a.n_tokens < most ? a.n_tokens : most, kv::APPEND_THREADS, 0, ctx.stream, p);
+  kv::launch_dep(kv::kv_append_kernel, dim3(a.n_tokens < most ? a.n_tokens : most), kv::APPEND_THREADS, 0, ctx.stream, p);
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
   return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
@@ -933,86 +757,93 @@ int launch_kv_append(const KvSpec& a, const KvRotation& r, const void* qkv, void
 
 namespace {
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-// The attention's scratch: for the own keys and for the shared ones the
-// tiles' prefix sums and the parts.
-struct AttendLayout {
-  size_t sched = 0, own_o = 0, own_ml = 0, sh_sched = 0, sh_o = 0, sh_ml = 0, total = 0;
-  int own_rows = 0, sh_rows = 0;
+
+// How a call's attention is launched, and its scratch.
+constexpr int kFewRows = 64;  // at most so many rows to a key/value head: the few-rows kernel
+struct AttendPlan {
+  bool share = false;
+  kv::Parts own, shared;      // the pointers as offsets from the scratch's start
+  int items = 0, item_rows = 0;
+  size_t bytes = 0;
 };
-AttendLayout attend_layout(const KvSpec& a, int num_sms) {
-  AttendLayout L;
-  const int64_t G = a.H / a.Hkv, blocks = kv::few_blocks(num_sms);
+AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
+  AttendPlan P;
+  const int64_t G = a.H / a.Hkv, rows = static_cast<int64_t>(a.n_tokens) * a.H;
   size_t off = 0;
   auto take = [&](size_t bytes) {
-    const size_t at = off;
+    char* at = ws + off;
     off += align256(bytes);
     return at;
   };
-  L.own_rows = static_cast<int>(a.max_new * G);
-  L.sched = take((static_cast<size_t>(a.n_seqs) + 1) * 8);
-  const size_t own = (static_cast<size_t>(a.n_seqs) * a.Hkv + blocks) * L.own_rows;
-  L.own_o = take(own * kv::HD * 4);
-  L.own_ml = take(own * 8);
-  if (a.shared_len > 0) {
-    L.sh_rows = static_cast<int>(a.n_tokens * G);
-    L.sh_sched = take(2 * 8);
-    const size_t sh = (static_cast<size_t>(a.Hkv) + blocks) * L.sh_rows;
-    L.sh_o = take(sh * kv::HD * 4);
-    L.sh_ml = take(sh * 8);
-  }
-  L.total = off;
-  return L;
+  auto part = [&](kv::Parts& p, int64_t item_rows, size_t sched) {
+    const bool many = item_rows > kFewRows;
+    p.rt = many ? kv::RT_MANY : 0;
+    p.slot_rows = static_cast<int>(many ? kv::RT_MANY : item_rows);
+    p.grid = many ? num_sms : kv::few_blocks(num_sms);
+    const size_t slots = 2 * static_cast<size_t>(p.grid) * p.slot_rows;
+    p.sched = reinterpret_cast<long long*>(take(sched * 8));
+    p.slot_o = reinterpret_cast<float*>(take(slots * kv::HD * 4));
+    p.slot_ml = reinterpret_cast<float2*>(take(slots * 8));
+    if (P.share) {
+      p.row_o = reinterpret_cast<float*>(take(rows * kv::HD * 4));
+      p.row_ml = reinterpret_cast<float2*>(take(rows * 8));
+    }
+  };
+  // One sequence shares with nobody; and where the sequences bring many rows
+  // each, their products bound the time, not the reads of the shared keys, and
+  // the parts to be joined would only cost.
+  P.share = a.shared_len > 0 && a.n_seqs > 1 && a.n_tokens * G <= static_cast<int64_t>(kFewRows) * a.n_seqs;
+  part(P.own, a.max_new * G, static_cast<size_t>(a.n_seqs) + 1);
+  if (P.share) part(P.shared, a.n_tokens * G, 2);
+  const int64_t units = P.own.rt ? a.n_tokens * G / kv::RT_MANY + a.n_seqs : a.n_seqs;
+  P.items = static_cast<int>(units * a.Hkv);
+  P.item_rows = P.own.slot_rows;
+  P.bytes = off;
+  return P;
 }
 }  // namespace
 
-size_t kv_attend_scratch_bytes(const KvSpec& a, int num_sms) { return attend_layout(a, num_sms).total; }
+size_t kv_attend_scratch_bytes(const KvSpec& a, int num_sms) { return attend_plan(a, num_sms, nullptr).bytes; }
 
 int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* header, bool alone, void* scratch,
                      LaunchCtx& ctx) {
-  const AttendLayout L = attend_layout(a, ctx.num_sms);
-  if (L.own_rows > 64 || L.sh_rows > 64) return TP_ERR_UNSUPPORTED;
-  char* ws = static_cast<char*>(scratch);
-  const int blocks = kv::few_blocks(ctx.num_sms);
+  const AttendPlan P = attend_plan(a, ctx.num_sms, static_cast<char*>(scratch));
   int* status = header + kKvHeaderWords + kKvStatusWords;
   kv::CombineParams c{};
-  kv::FewParams p{};
+  kv::AttendParams p{};
   p.b = kv::make_batch(a);
+  if (!P.share) p.b.shared = 0;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kv::HD)));
+  p.timeout_ns = ctx.timeout_ns;
   int rc = TP_OK;
-  if (a.shared_len > 0) {
-    p.part_o = reinterpret_cast<float*>(ws + L.sh_o);
-    p.part_ml = reinterpret_cast<float2*>(ws + L.sh_ml);
-    p.sched = reinterpret_cast<long long*>(ws + L.sh_sched);
-    p.rows = L.sh_rows;
-    p.status = status + c.status_words;
-    c.status_words += blocks;
-    c.shared = {p.part_o, p.part_ml, p.sched, p.rows, blocks};
-    if ((rc = kv::launch_few<true>(p, ctx, "kv_attend_shared"))) return rc;
+  if (P.share) {
+    p.part = c.shared = P.shared;
+    p.status = status;
+    c.status_words += P.shared.grid;
+    rc = P.shared.rt ? kv::launch_many(p, true, ctx, "kv_attend_shared_many")
+                     : kv::launch_few<true>(p, ctx, "kv_attend_shared_few");
+    if (rc) return rc;
   }
-  p.part_o = reinterpret_cast<float*>(ws + L.own_o);
-  p.part_ml = reinterpret_cast<float2*>(ws + L.own_ml);
-  p.sched = reinterpret_cast<long long*>(ws + L.sched);
-  p.rows = L.own_rows;
+  p.part = c.own = P.own;
   p.status = status + c.status_words;
-  c.status_words += blocks;
-  c.own = {p.part_o, p.part_ml, p.sched, p.rows, blocks};
-  if ((rc = kv::launch_few<false>(p, ctx, "kv_attend_own"))) return rc;
+  c.status_words += P.own.grid;
+  rc = P.own.rt ? kv::launch_many(p, false, ctx, "kv_attend_many") : kv::launch_few<false>(p, ctx, "kv_attend_few");
+  if (rc) return rc;
   c.b = p.b;
   c.o = p.o;
   c.lse = lse;
   c.header = header;
   c.alone = alone;
-  // few rows: a block for each, so that a long sequence's many parts are
-  // read by all of its warps
-  const long long rows = static_cast<long long>(a.n_tokens) * a.H;
-  c.rows_per_block = rows <= 4ll * ctx.num_sms ? 1 : 8;
-  c.many = c.rows_per_block == 1 ? 4 : 32;
+  c.rows_per_block = 8;
+  while (c.rows_per_block > 1 &&
+         static_cast<int64_t>(P.items) * ((P.item_rows + c.rows_per_block - 1) / c.rows_per_block) < ctx.num_sms)
+    c.rows_per_block /= 2;
   if (ctx.before) ctx.before(ctx.user, "kv_combine", ctx.stream);
-  kv::launch_dep(kv::kv_combine_kernel, static_cast<int>((rows + c.rows_per_block - 1) / c.rows_per_block), 256, 0,
-                 ctx.stream, c);
+  kv::launch_dep(kv::kv_combine_kernel,
+                 dim3(P.items, (P.item_rows + c.rows_per_block - 1) / c.rows_per_block), 256, 0, ctx.stream, c);
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
   return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;

@@ -4,9 +4,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "tp_internal.h"
+#include "tpffn.h"
 
 namespace tpffn {
 namespace kv {
@@ -80,19 +82,245 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int row) {
   return lo;
 }
 
-// 2^x by the SFU instruction; 2^-inf = 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Work is a list of tiles, in the order of the items they belong to.  Block c
-// of C takes the tiles [c T / C, (c + 1) T / C); a run of tiles of one item
-// in one block is a segment.
+// Work is a list of tiles of KTILE keys, in the order of the items they belong
+// to: sequence by sequence, its key/value heads, their row tiles of RT rows
+// (RT = 0: all rows of the item in one).  The rows of a sequence and a key/value
+// head are its new tokens times the G query heads of the group, row r being
+// token r / G, head h G + r % G.  Prefix items (PREFIX) take the rows of all
+// sequences together against the shared keys.
+//
+// Block c of C takes the tiles [c T / C, (c + 1) T / C), whatever items they
+// belong to; a run of tiles of one item in one block is a segment.  Every
+// block gets the same number of tiles however the lengths differ.
 __host__ __device__ __forceinline__ long long first_tile(long long c, long long T, long long C) { return c * T / C; }
 __host__ __device__ __forceinline__ long long block_of_tile(long long t, long long T, long long C) {
   return ((t + 1) * C - 1) / T;
+}
+
+template <bool PREFIX, int KTILE, int RT>
+struct Cut {
+  static __device__ __forceinline__ int row_tiles(const Batch& p, const Seq& s) {
+    const int rows = s.qn * p.G;
+    return RT ? (rows + RT - 1) / (RT ? RT : 1) : (rows > 0);
+  }
+  static __device__ __forceinline__ int first_key(const Batch& p) { return PREFIX ? 0 : p.shared; }
+  static __device__ __forceinline__ int t0(const Batch& p) { return first_key(p) / KTILE; }
+  // tiles of one row tile: up to the last key that any of its rows sees
+  static __device__ __forceinline__ int tiles(const Batch& p, const Seq& s, int rt) {
+    int hi = s.kv;
+    if (RT && !PREFIX) {
+      const int tok = min((rt * RT + RT - 1) / p.G, s.qn - 1);
+      hi = s.visible(tok, p.causal);
+    }
+    return (s.qn > 0 && hi > first_key(p)) ? (hi + KTILE - 1) / KTILE - t0(p) : 0;
+  }
+  static __device__ __forceinline__ long long tiles_per_head(const Batch& p, const Seq& s) {
+    const int n = row_tiles(p, s);
+    if (!RT || PREFIX) return static_cast<long long>(n) * tiles(p, s, 0);
+    long long sum = 0;
+    for (int rt = 0; rt < n; ++rt) sum += tiles(p, s, rt);
+    return sum;
+  }
+};
+
+// Where a block stands in the list: tile t of the nt of a row tile.
+struct Cursor {
+  int b, h, rt, t, nt;
+  Seq s;
+};
+
+// The next tile; past an item's end the next one that has tiles (the caller
+// knows that there is one).
+template <typename C, bool PREFIX>
+__device__ __forceinline__ void advance(const Batch& p, Cursor& c) {
+  if (++c.t < c.nt) return;
+  c.t = 0;
+  do {
+    if (++c.rt >= C::row_tiles(p, c.s)) {
+      c.rt = 0;
+      if (++c.h >= p.Hkv) {
+        c.h = 0;
+        if constexpr (!PREFIX) c.s = load_seq(p, ++c.b);
+      }
+    }
+    c.nt = C::tiles(p, c.s, c.rt);
+  } while (c.nt == 0);
+}
+
+struct SchedScratch {
+  long long sums[128];
+  int best[128], len[128];
+  Cursor start;
+};
+struct Sched {
+  int n_tiles;    // of this block
+  int table_row;  // whose page table leads to the shared pages
+};
+
+// Called by every thread of a block (at least 128): sums the tiles of all
+// sequences, finds the block's first tile and, in block 0, leaves the prefix
+// sums for the combine kernel: `sched` [B + 1] tiles per key/value head before
+// sequence b, or for prefix items {tiles of a row tile, row tiles}.
+template <typename C, bool PREFIX>
+__device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, SchedScratch* w, Cursor& c, int* err) {
+  const int tid = threadIdx.x;
+  Sched S{0, 0};
+  if constexpr (PREFIX) {
+    // the longest sequence's table covers the shared pages if any does
+    if (tid < 128) {
+      int best = 0, len = -1;
+      for (int b = tid; b < p.B; b += 128) {
+        const int l = min(max(p.kv_len[b], 0), p.cap);
+        if (l > len) { len = l; best = b; }
+      }
+      w->best[tid] = best;
+      w->len[tid] = len;
+    }
+    __syncthreads();
+    for (int d = 64; d; d >>= 1) {
+      if (tid < d) {
+        const int ol = w->len[tid + d], ob = w->best[tid + d];
+        if (ol > w->len[tid] || (ol == w->len[tid] && ob < w->best[tid])) { w->len[tid] = ol; w->best[tid] = ob; }
+      }
+      __syncthreads();
+    }
+    S.table_row = w->best[0];
+    c.b = 0;
+    c.s.q0 = 0;
+    c.s.qn = min(max(p.cu[p.B], 0), p.n_tokens);
+    c.s.kv = min(p.shared, w->len[0]);
+    c.s.err = 0;
+    const int n_rt = C::row_tiles(p, c.s);
+    c.nt = C::tiles(p, c.s, 0);
+    const long long total = static_cast<long long>(n_rt) * c.nt * p.Hkv;
+    if (blockIdx.x == 0 && tid == 0) {
+      sched[0] = c.nt;
+      sched[1] = n_rt;
+    }
+    const long long blocks = total < gridDim.x ? total : gridDim.x;
+    if (blockIdx.x >= blocks) return S;
+    const long long first = first_tile(blockIdx.x, total, blocks);
+    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, total, blocks) - first);
+    const long long item = first / c.nt;
+    c.t = static_cast<int>(first - item * c.nt);
+    c.h = static_cast<int>(item / n_rt);
+    c.rt = static_cast<int>(item - static_cast<long long>(c.h) * n_rt);
+  } else {
+    const int per = (p.B + 127) / 128;
+    const int b0 = min(tid * per, p.B), b1 = tid < 128 ? min(b0 + per, p.B) : b0;
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load_seq(p, b);
+      *err |= s.err;
+      sum += C::tiles_per_head(p, s);
+    }
+    if (tid < 128) w->sums[tid] = sum;
+    __syncthreads();
+    for (int d = 1; d < 128; d <<= 1) {
+      const long long add = tid < 128 && tid >= d ? w->sums[tid - d] : 0;
+      __syncthreads();
+      if (tid < 128) w->sums[tid] += add;
+      __syncthreads();
+    }
+    const long long total = w->sums[127] * p.Hkv;
+    const long long blocks = total < gridDim.x ? total : gridDim.x;
+    const long long before = tid < 128 ? w->sums[tid] - sum : 0;
+    if (blockIdx.x == 0 && tid < 128) {
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        sched[b] = at;
+        at += C::tiles_per_head(p, load_seq(p, b));
+      }
+      if (tid == 127) sched[p.B] = w->sums[127];
+    }
+    if (blockIdx.x >= blocks) return S;
+    const long long first = first_tile(blockIdx.x, total, blocks);
+    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, total, blocks) - first);
+    if (tid < 128 && first >= before * p.Hkv && first < (before + sum) * p.Hkv) {
+      long long at = first - before * p.Hkv;
+      for (int b = b0; b < b1; ++b) {
+        Cursor x;
+        x.b = b;
+        x.s = load_seq(p, b);
+        const long long per_head = C::tiles_per_head(p, x.s);
+        if (at < per_head * p.Hkv) {
+          x.h = static_cast<int>(at / per_head);
+          at -= x.h * per_head;
+          for (x.rt = 0;; ++x.rt) {
+            x.nt = C::tiles(p, x.s, x.rt);
+            if (at < x.nt) break;
+            at -= x.nt;
+          }
+          x.t = static_cast<int>(at);
+          w->start = x;
+          break;
+        }
+        at -= per_head * p.Hkv;
+      }
+    }
+    __syncthreads();
+    c = w->start;
+  }
+  return S;
+}
+
+// What a segment leaves for the combine kernel: the running maximum (in log2
+// units) and sum of each row, and its unnormalised output in 32 bits.  A
+// segment that is a whole item goes to its rows' own places ([token][head],
+// used only where other keys are still to be joined), the others, of which a
+// block has at most two, its first and its last, to the block's two slots.
+struct Parts {
+  float* slot_o = nullptr;    // [2 blocks][slot_rows][HD]
+  float2* slot_ml = nullptr;  // [2 blocks][slot_rows]
+  float* row_o = nullptr;     // [n_tokens * H][HD]
+  float2* row_ml = nullptr;
+  long long* sched = nullptr;
+  int slot_rows = 0, grid = 0, rt = 0;  // rt: rows of a row tile, 0: all
+};
+
+struct AttendParams {
+  Batch b;
+  const __nv_bfloat16* q;  // [n_tokens][H * HD]
+  __nv_bfloat16* o;        // [n_tokens][H * HD]
+  float* lse;              // [n_tokens][H] or null
+  Parts part;
+  float scale_log2;
+  int* status;             // a word per block
+  unsigned long long timeout_ns;
+};
+
+constexpr int RT_MANY = 256;  // rows of an item of the many-rows kernel
+// The many-rows kernel (tp_kv_tc.cu).
+int launch_many(const AttendParams& p, bool prefix, LaunchCtx& ctx, const char* name);
+
+// Launch as a programmatic dependent of the stream's previous kernel.
+template <typename... KArgs, typename... Args>
+void launch_dep(void (*kern)(KArgs...), dim3 grid, int block, int smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Whether a kernel's shared-memory limit has been raised on the current device.
+template <typename K>
+int set_smem_once(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TP_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done.load() & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return TP_ERR_CUDA;
+    done.fetch_or(bit);
+  }
+  return TP_OK;
 }
 
 }  // namespace kv

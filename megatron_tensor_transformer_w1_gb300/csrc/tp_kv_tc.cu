@@ -1,0 +1,499 @@
+// tp_kv_tc.cu -- attention of many query rows over the paged key/value cache:
+// prompts and chunks of prompts, and the rows of a whole batch against the
+// keys that its sequences share.
+//
+// An item is a key/value head with 256 of a sequence's rows (new tokens times
+// the G query heads of the group; of all sequences' rows for the shared
+// keys), in two tiles of 128; its keys come in tiles of 128.  One persistent
+// block per SM takes an equal share of the batch's key tiles (see Cut in
+// tp_kv.cuh) and leaves the parts of items that it shares with its
+// neighbours to kv_combine_kernel.
+//
+// With R rows a key/value head does 2 R products per byte of K and V, so from
+// some 128 rows on the tensor cores bound the time, not the memory: 4 x 128^3
+// products a step of two row tiles, 2048 cycles at 4096 a cycle.  The two
+// row tiles take turns: while one tile's scores go through the softmax, the
+// products of the other run.  A block has
+//  * warp 0: copies K and V tiles by TMA, page by page (box: 64 columns by a
+//    page, or 128 keys of a longer one), into a ring of four 32 KB slots;
+//  * warp 1: one lane issues tcgen05.mma.  Per row tile t: S_t = Q_t K^T into
+//    tensor memory, then O_t += P_t V with P_t, in bf16, over the S_t it came
+//    from.  Products run in the order of issue, so S_t of the next key tile,
+//    issued behind O_t += P_t V, finds P_t read, and when it is done that sum
+//    is too;
+//  * warp 2: gathers the query rows of the next item into the swizzled
+//    layout of the products;
+//  * warps 4-7 and 8-11: the softmax of row tiles 0 and 1, a row per thread,
+//    with a maximum that moves only when it grew by more than 2^8, so that
+//    O_t is rarely rescaled; they write the rows out at the end of a segment.
+// Values of slots behind a sequence's last key may be anything, also NaN, and
+// 0 x NaN would spoil a row: the rows of V behind the last key are zeroed up
+// to the 16 that a product step takes, and the steps behind are left out.
+//
+// Every wait is bounded (status word and block-wide abort flag; copies and
+// products in flight are drained and tensor memory freed).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "tc_ptx.cuh"
+#include "tp_internal.h"
+#include "tp_kv.cuh"
+#include "tpffn.h"
+
+namespace tpffn {
+namespace kv {
+using namespace tc;
+
+constexpr int BK = 128;                 // keys of a tile
+constexpr int TILE_BYTES = 128 * HD * 2;
+constexpr int SLOTS = 4;                // K and V tiles in flight
+constexpr int MANY_THREADS = 384;
+constexpr int M_Q = 0;                             // two row tiles
+constexpr int M_RING = M_Q + 2 * TILE_BYTES;
+constexpr int M_OUT = M_RING + SLOTS * TILE_BYTES; // 4 KB per softmax warp
+constexpr int M_BAR = M_OUT + 8 * 4096;
+constexpr int M_SMEM = M_BAR + 512 + 1024;
+static_assert(M_SMEM <= 232448, "shared memory per block");
+static_assert(sizeof(SchedScratch) <= 8 * 4096, "the schedule's scratch lies where the output is staged");
+
+template <bool PREFIX>
+using Many = Cut<PREFIX, BK, RT_MANY>;
+
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* tm, uint64_t* bar, int col, int slot,
+                                              int head, int page) {
+  tma_load_4d(dst, tm, bar, col, slot, head, page);
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+template <bool PREFIX>
+__global__ void __launch_bounds__(MANY_THREADS, 1)
+    kv_many_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const __grid_constant__ AttendParams p) {
+  using C = Many<PREFIX>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + M_BAR);
+  uint64_t* full = bar;         // [SLOTS] a K or V tile has landed
+  uint64_t* empty = bar + 4;    // [SLOTS] its products are done
+  uint64_t* q_full = bar + 8;   // [2]
+  uint64_t* q_empty = bar + 10; // [2] the item's last S_t is done
+  uint64_t* s_full = bar + 12;  // [2]
+  uint64_t* p_full = bar + 14;  // [2] P_t written (a warp each)
+  uint64_t* o_full = bar + 16;  // [2] the segment's last O_t is done
+  uint64_t* drain = bar + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 19);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 19) + 1;
+  const Batch& B = p.b;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* status = p.status + blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 32);
+      mbar_init(&q_empty[t], 1);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  grid_dep_wait();
+  grid_dep_launch();
+  if (threadIdx.x == 0) *status = 0;
+  int err = 0;
+  Cursor c;
+  const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem + M_OUT), c, &err);
+  tc_fence_before();
+  __syncthreads();  // (also: the status word is clear, the scratch has been read)
+  tc_fence_after();
+  if (err) atomicOr(status, err);
+  const uint32_t tmem = *tmem_slot;  // S_0, S_1 at columns 0 and 128, O_0, O_1 at 256 and 384
+  const Waiter W{abort_flag, status, p.timeout_ns};
+  const int N = S.n_tiles, t0 = C::t0(B), lo = C::first_key(B);
+  auto ring = [&](uint32_t i) { return smem + M_RING + (i & (SLOTS - 1)) * TILE_BYTES; };
+  auto rows_of = [&](const Cursor& x) { return x.s.qn * B.G - x.rt * RT_MANY; };  // > 128: both row tiles
+
+  if (warp == 0) {
+    // ------------------------------------------------ copies: K_0, V_0, K_1, V_1, ...
+    const int page_keys = 1 << B.page_shift, box = page_keys < BK ? page_keys : BK;
+    const int groups = BK / box;  // at most 16
+    int last_phase[SLOTS] = {-1, -1, -1, -1};
+    bool ok = true;
+    for (int n = 0; n < N && ok; ++n) {
+      const int base = (t0 + c.t) * BK;
+      const int live = min(groups, (c.s.kv - base + box - 1) / box);  // groups that hold keys
+      int page = static_cast<int>(B.n_pages);  // past the end: the copy fills with zeros
+      const int key = base + lane * box;
+      if (lane < live) {
+        const int row = PREFIX ? S.table_row : c.b;
+        const int at = B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
+        if (at >= 0 && at < B.n_pages)
+          page = at;
+        else
+          atomicOr(status, DEV_ERR_BATCH);
+      }
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t i = 2u * n + kv;
+        const int slot = i & (SLOTS - 1);
+        const uint32_t ph = (i / SLOTS) & 1u;
+        if (!W.warp(&empty[slot], ph ^ 1u)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(live * box) * HD * 2);
+        __syncwarp();
+        last_phase[slot] = static_cast<int>(ph);
+        if (lane < live) {
+          uint8_t* dst = ring(i) + lane * box * 128;
+          const CUtensorMap* tm = kv ? &tv : &tk;
+          const int at = key & (page_keys - 1);
+          tma_load_page(dst, tm, &full[slot], 0, at, c.h, page);
+          tma_load_page(dst + TILE_BYTES / 2, tm, &full[slot], 64, at, c.h, page);
+        }
+      }
+      if (n + 1 < N) advance<C, PREFIX>(B, c);
+    }
+    // every issued copy lands before the block may exit
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i)
+      if (last_phase[i] >= 0) W.drain(&full[i], static_cast<uint32_t>(last_phase[i]));
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ products
+    if (lane == 0 && N > 0) {
+      constexpr uint32_t ID_S = idesc(128, 0, 0);   // S = Q K^T
+      constexpr uint32_t ID_PV = idesc(128, 0, 1);  // O += P V (V: N = hd contiguous)
+      uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+      bool ok = true;
+      // S_t of tile x (the n-th of this block)
+      auto issue_s = [&](int t, const Cursor& x, int n, bool new_seg, bool seg_ends) -> bool {
+        if (new_seg) {
+          if (!W(&q_full[t], q_uses[t] & 1u)) return false;
+          ++q_uses[t];
+        }
+        tc_fence_after();
+        const uint32_t qa = smem_u32(smem + M_Q + t * TILE_BYTES), ka = smem_u32(ring(2u * n));
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          umma_bf16(tmem + t * 128, kdesc(qa, 128, ks), kdesc(ka, 128, ks), ID_S, ks > 0 ? 1u : 0u);
+        umma_commit(&s_full[t]);
+        if (seg_ends) umma_commit(&q_empty[t]);
+        return true;
+      };
+      auto wait_tile = [&](uint32_t i) { return W(&full[i & (SLOTS - 1)], (i / SLOTS) & 1u); };
+      auto ends = [&](const Cursor& x, int n) { return x.t + 1 == x.nt || n + 1 == N; };
+      bool two = rows_of(c) > 128;
+      ok = wait_tile(0) && issue_s(0, c, 0, true, ends(c, 0)) && (!two || issue_s(1, c, 0, true, ends(c, 0)));
+      if (ok) umma_commit(&empty[0]);
+      bool first = true;
+      for (int n = 0; n < N && ok; ++n) {
+        const int base = (t0 + c.t) * BK;
+        const int steps = (min(BK, c.s.kv - base) + 15) / 16;
+        const bool last = ends(c, n), more = n + 1 < N;
+        Cursor x = c;
+        if (more) advance<C, PREFIX>(B, x);
+        const bool two_next = more && rows_of(x) > 128;
+        ok = wait_tile(2u * n + 1) && (!more || wait_tile(2u * n + 2));
+        if (!ok) break;
+        const uint32_t va = smem_u32(ring(2u * n + 1));
+        auto issue_pv = [&](int t) -> bool {
+          if (!W(&p_full[t], p_uses[t] & 1u)) return false;
+          ++p_uses[t];
+          tc_fence_after();
+          for (int ks = 0; ks < steps; ++ks)
+            umma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, mndesc(va, 128, ks), ID_PV,
+                         (!first || ks > 0) ? 1u : 0u);
+          if (last) umma_commit(&o_full[t]);
+          return true;
+        };
+        if (!last) {
+          ok = issue_pv(0) && issue_s(0, x, n + 1, false, ends(x, n + 1));
+          if (ok && two) ok = issue_pv(1) && issue_s(1, x, n + 1, false, ends(x, n + 1));
+        } else {
+          // the next item's S waits for its rows: behind both tiles' products
+          ok = issue_pv(0) && (!two || issue_pv(1));
+          if (ok && more)
+            ok = issue_s(0, x, n + 1, true, ends(x, n + 1)) && (!two_next || issue_s(1, x, n + 1, true, ends(x, n + 1)));
+        }
+        if (!ok) break;
+        umma_commit(&empty[(2u * n + 1) & (SLOTS - 1)]);
+        if (more) umma_commit(&empty[(2u * n + 2) & (SLOTS - 1)]);
+        first = last;
+        c = x;
+        two = two_next;
+      }
+      umma_commit(drain);  // all issued products complete before tensor memory is released
+      W.drain(drain, 0u);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ query rows of each segment
+    uint32_t uses[2] = {0, 0};
+    bool ok = true, fresh = true;
+    for (int n = 0; n < N && ok; ++n) {
+      if (fresh) {
+        const int rows = rows_of(c);
+        for (int t = 0; t < 2 && rows > t * 128; ++t) {
+          if (!W.warp(&q_empty[t], (uses[t] & 1u) ^ 1u)) { ok = false; break; }
+          ++uses[t];
+          const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
+          // 16 lanes to a row: two rows of 256 bytes a time
+          for (int r = lane >> 4; r < 128; r += 2) {
+            const int item_row = c.rt * RT_MANY + t * 128 + r;
+            const bool valid = t * 128 + r < rows;
+            const int tok = valid ? item_row / B.G : 0, g = valid ? item_row - tok * B.G : 0;
+            const long long off =
+                valid ? (static_cast<long long>(c.s.q0 + tok) * B.H + c.h * B.G + g) * HD + (lane & 15) * 8 : 0;
+            cp_async16z(sw_chunk(qs, 128, r, lane & 15), p.q + off, valid);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          mbar_arrive(&q_full[t]);
+        }
+      }
+      fresh = c.t + 1 == c.nt;
+      if (n + 1 < N) advance<C, PREFIX>(B, c);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------ softmax of row tile t
+    const int t = (warp - 4) >> 2, quarter = warp & 3;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t sbuf = smem_u32(smem + M_OUT + (warp - 4) * 4096);
+    uint32_t s_uses = 0, o_uses = 0;
+    bool fresh = true;
+    int seg_t = 0, seg_n = 0, limit = 0;
+    int at = -1;  // token * H + head of this thread's row, -1: none
+    float m = -INFINITY, l = 0.f;
+    for (int n = 0; n < N; ++n) {
+      const int rows = rows_of(c);
+      const bool last = c.t + 1 == c.nt || n + 1 == N;
+      if (rows > t * 128) {
+        if (fresh) {
+          seg_t = c.t;
+          seg_n = n;
+          m = -INFINITY;
+          l = 0.f;
+          limit = 0;
+          at = -1;
+          const int r = t * 128 + quarter * 32 + lane;
+          if (r < rows) {
+            const int item_row = c.rt * RT_MANY + r, tok = item_row / B.G;
+            at = (c.s.q0 + tok) * B.H + c.h * B.G + (item_row - tok * B.G);
+            if (PREFIX) {
+              const int b = find_seq(B.cu, B.B, tok);
+              if (b < B.B) {
+                const Seq s = load_seq(B, b);
+                if (tok >= s.q0 && tok < s.q0 + s.qn) limit = min(s.visible(tok - s.q0, B.causal), c.s.kv);
+              }
+            } else {
+              limit = c.s.visible(tok, B.causal);
+            }
+          }
+        }
+        if (!W.warp(&s_full[t], s_uses & 1u)) break;
+        ++s_uses;
+        tc_fence_after();
+        uint32_t r[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tmem_ld32(tl + t * 128 + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * k]));
+        tmem_wait_ld();
+        const int base = (t0 + c.t) * BK;
+        if (__any_sync(0xffffffffu, base < lo || base + BK > limit)) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            r[k] = (base + k >= lo && base + k < limit) ? r[k] : __float_as_uint(-INFINITY);
+        }
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = __uint_as_float(r[k]);
+#pragma unroll
+        for (int k = 8; k < 128; ++k) m8[k & 7] = fmaxf(m8[k & 7], __uint_as_float(r[k]));
+        const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (m == -INFINITY) {
+          m = mx;  // the first key that this row sees: O_t and l are still zero
+        } else if (mx > m + 8.f) {
+          alpha = ex2(m - mx);
+          m = mx;
+          rescale = true;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          // O_t holds the sum up to the tile before: S_t was issued behind it
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tmem_ld32(tl + 256 + t * 128 + k * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tl + 256 + t * 128 + k * 32, o);
+          }
+          tmem_wait_st();
+        }
+        const float neg_m = m == -INFINITY ? 0.f : -m;  // no key yet: every p is 0
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float e0 = ex2(fmaf(__uint_as_float(r[64 * half + 2 * k]), p.scale_log2, neg_m));
+            const float e1 = ex2(fmaf(__uint_as_float(r[64 * half + 2 * k + 1]), p.scale_log2, neg_m));
+            l4[k & 3] += e0 + e1;
+            // rounded to bf16 for the second product; the sum is taken before
+            pk[k] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(tl + t * 128 + half * 32, pk);
+        }
+        tmem_wait_st();
+        l = l * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+        const int keys = min(BK, c.s.kv - base);  // of the sequence; V behind them may be anything
+        if (t == 0 && (keys & 15)) {
+          const uint32_t i = 2u * n + 1;
+          if (!W.warp(&full[i & (SLOTS - 1)], (i / SLOTS) & 1u)) break;
+          const uint32_t vs = smem_u32(ring(i));
+          const int tid = threadIdx.x - 128, bad = 16 - (keys & 15);
+          for (int k = tid; k < bad * 16; k += 128) st_shared_v4(sw_chunk(vs, 128, keys + (k >> 4), k & 15), 0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        arrive_warp(&p_full[t]);
+        if (last) {
+          // ---- the segment's rows: to o, to their own places, or to a slot
+          if (!W.warp(&o_full[t], o_uses & 1u)) break;
+          ++o_uses;
+          tc_fence_after();
+          const bool whole = seg_t == 0 && c.t + 1 == c.nt;
+          const bool direct = whole && !PREFIX && B.shared == 0;
+          const long long slot = (2ll * blockIdx.x + (seg_n ? 1 : 0)) * p.part.slot_rows + t * 128 + quarter * 32;
+          if (direct) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t o[32];
+                tmem_ld32(tl + 256 + t * 128 + k * 64 + half * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                  st_shared_v4(sbuf + lane * 128 + (((4 * half + i) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                }
+              }
+              __syncwarp();
+              // eight lanes write 128 bytes of a row, four rows at a time
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+                const uint4 v = ld_shared_v4(sbuf + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                const int row = __shfl_sync(0xffffffffu, at, rr);
+                if (row >= 0) reinterpret_cast<uint4*>(p.o + static_cast<long long>(row) * HD + k * 64)[ch] = v;
+              }
+              __syncwarp();
+            }
+            if (at >= 0 && p.lse) p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              uint32_t o[32];
+              tmem_ld32(tl + 256 + t * 128 + k * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                st_shared_v4(sbuf + lane * 128 + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
+                             o[4 * i + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+                const uint4 v = ld_shared_v4(sbuf + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                const int row = __shfl_sync(0xffffffffu, at, rr);
+                float* dst = whole ? p.part.row_o + static_cast<long long>(row) * HD : p.part.slot_o + (slot + rr) * HD;
+                if (row >= 0) reinterpret_cast<uint4*>(dst + k * 32)[ch] = v;
+              }
+              __syncwarp();
+            }
+            if (at >= 0) (whole ? p.part.row_ml[at] : p.part.slot_ml[slot + lane]) = make_float2(m, l);
+          }
+          tc_fence_before();
+        }
+      }
+      fresh = last;
+      if (n + 1 < N) advance<C, PREFIX>(B, c);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+namespace {
+int map_pages(CUtensorMap* m, const void* ptr, const Batch& b) {
+  const uint64_t page = 1ull << b.page_shift;
+  const uint64_t dims[4] = {HD, page, static_cast<uint64_t>(b.Hkv), static_cast<uint64_t>(b.n_pages)};
+  const uint64_t str[3] = {HD * 2, page * HD * 2, page * HD * 2 * static_cast<uint64_t>(b.Hkv)};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(page < BK ? page : BK), 1, 1};
+  return encode_map_4d_bf16(m, ptr, dims, str, box);
+}
+
+template <bool PREFIX>
+int launch_many_inst(const AttendParams& p, LaunchCtx& ctx, const char* name) {
+  CUtensorMap tk, tv;
+  int rc;
+  if ((rc = map_pages(&tk, p.b.k, p.b)) || (rc = map_pages(&tv, p.b.v, p.b))) return rc;
+  static std::atomic<uint64_t> done{0};
+  if ((rc = set_smem_once(kv_many_kernel<PREFIX>, M_SMEM, done))) return rc;
+  if (ctx.before) ctx.before(ctx.user, name, ctx.stream);
+  launch_dep(kv_many_kernel<PREFIX>, dim3(p.part.grid), MANY_THREADS, M_SMEM, ctx.stream, tk, tv, p);
+  if (ctx.after) ctx.after(ctx.user, ctx.stream);
+  ctx.launches++;
+  return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+}  // namespace
+
+int launch_many(const AttendParams& p, bool prefix, LaunchCtx& ctx, const char* name) {
+  return prefix ? launch_many_inst<true>(p, ctx, name) : launch_many_inst<false>(p, ctx, name);
+}
+
+}  // namespace kv
+}  // namespace tpffn

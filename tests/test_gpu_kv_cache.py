@@ -107,6 +107,73 @@ def test_attend(new, ctx, H, Hkv, T, page, shared, causal):
         check_attend(s, q, H, cache.attend(q, batch), None, causal)
 
 
+MANY = [  # more than 64 rows to a key head: the tensor-memory kernel
+    ([65], [0], 1, 1, 1, 16, 0, True),                                 # just more; only own keys
+    ([17], [100], 4, 1, 1, 8, 0, True),
+    ([128], [128], 2, 2, 1, 64, 0, True),                              # whole tiles
+    ([129, 1, 257], [0, 300, 127], 4, 2, 2, 16, 0, True),              # around the tiles' ends, a single token among them
+    ([300], [1000], 8, 2, 2, 128, 0, True),
+    ([40, 0, 3, 90], [7, 500, 0, 129], 5, 1, 1, 32, 0, True),          # groups of five across row tiles
+    ([200, 13], [50, 900], 4, 4, 4, 1024, 0, True),
+    ([100, 30], [77, 260], 8, 2, 2, 256, 0, False),
+    ([700, 100], [3000, 0], 8, 2, 2, 64, 0, True),                     # items cut between blocks
+    ([1] * 40, [i * 3 for i in range(40)], 4, 2, 2, 8, 512, True),     # a shared prefix for 80 rows
+    ([1] * 70, [(i * 29) % 200 for i in range(70)], 16, 2, 2, 16, 1000, True),  # 560 rows, ends inside a page
+    ([2] * 33, [5] * 33, 8, 8, 4, 128, 129, False),
+    ([90, 1, 1, 1, 1, 1, 1, 1, 1], [3] * 9, 4, 2, 2, 16, 300, True),   # a prompt among single tokens
+    ([100, 80], [30, 40], 8, 2, 2, 32, 640, True),                     # prompts behind a prefix
+]
+
+
+@pytest.mark.parametrize("new,ctx,H,Hkv,T,page,shared,causal", MANY)
+def test_attend_many_rows(new, ctx, H, Hkv, T, page, shared, causal):
+    test_attend(new, ctx, H, Hkv, T, page, shared, causal)
+
+
+def test_attend_many_rows_that_see_nothing():
+    """A prompt cut off by kv_len: its first rows see no key, whole row tiles among them."""
+    s = ref.make_batch([600, 70, 80], [0, 0, 10], 1, 16, seed=15)
+    s["lens"] = [40, 0, 90]
+    s["kv_len"].copy_(torch.tensor(s["lens"]))
+    cache, batch = _cache(s, 2, 1)
+    q = _q(s["n"], 2, 7)
+    o, lse = cache.attend(q, batch, lse=True)
+    assert cache.last_device_error() == 0
+    check_attend(s, q, 2, o, lse)
+
+
+def test_attend_many_rows_sharp_scores():
+    s = ref.make_batch([150, 70], [900, 2000], 2, 16, seed=12)
+    s["k"].mul_(torch.linspace(0.1, 6, s["k"].shape[0], device="cuda").to(torch.bfloat16)[:, None, None, None])
+    cache, batch = _cache(s, 4, 2)
+    q = _q(s["n"], 4, 5, scale=6.0)
+    check_attend(s, q, 4, *cache.attend(q, batch, lse=True))
+
+
+def test_many_rows_bad_batches():
+    abi = _modules()[0]
+    s = ref.make_batch([80, 70, 90], [100, 60, 200], 2, 16, seed=22)
+    cache, batch = _cache(s, 4, 2)
+    q = _q(s["n"], 4, 6)
+    good = cache.attend(q, batch)
+    assert cache.last_device_error() == abi.TP_OK
+    keep = s["table"].clone()
+    for bad in (-1, s["n_pages"], 2 ** 31 - 1, -2 ** 31):
+        s["table"][1, 2] = bad
+        o = cache.attend(q, batch)
+        assert cache.last_device_error() == abi.TP_ERR_BATCH
+        assert torch.equal(o[:80], good[:80]) and torch.equal(o[150:], good[150:]) and torch.isfinite(o).all()
+        s["table"].copy_(keep)
+    for name, at, bad in (("kv_len", 1, -5), ("cu", 3, 10 ** 6), ("cu", 1, -3)):
+        was = s[name][at].item()
+        s[name][at] = bad
+        cache.attend(q, batch)
+        assert cache.last_device_error() == abi.TP_ERR_BATCH, name
+        s[name][at] = was
+    assert torch.equal(cache.attend(q, batch), good)
+    assert cache.last_device_error() == abi.TP_OK
+
+
 def test_attend_rows_that_see_nothing():
     """More new tokens than keys (the first rows see none), and no keys at all."""
     s = ref.make_batch([3, 2, 4], [40, 0, 0], 2, 16, seed=5)
