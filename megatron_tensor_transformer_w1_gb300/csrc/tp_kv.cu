@@ -242,6 +242,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   __syncthreads();
   const int n_tiles = S.n_tiles, t0 = C::t0(B), lo = C::first_key(B);
   if (n_tiles == 0) {
+    if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, 0);
+    if (tid == 0 && p.part.split) p.part.split[blockIdx.x] = Split{};
     if (err) atomicOr(&s_err, err);
     __syncthreads();
     if (tid == 0) p.status[blockIdx.x] = s_err;
@@ -346,7 +348,9 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
         limit[e] = 0;
         if (r < rows) {
           const int tok = r / B.G;
-          if (PREFIX) {
+          if (PREFIX && S.all_see) {
+            limit[e] = x.s.kv;
+          } else if (PREFIX) {
             const int b = find_seq(B.cu, B.B, tok);
             if (b < B.B) {
               const Seq s = load_seq(B, b);
@@ -438,6 +442,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
 
     // ---- end of a segment: the key groups of the rows meet
     fresh = true;
+    if (tid == 0 && i + 1 == n_tiles && p.part.split)
+      p.part.split[blockIdx.x] = split_of(B, S, x, seg_t, seg_i > 0);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -508,6 +514,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     }
   }
   cp_async_wait<0>();
+  if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, 0);
   if (err) atomicOr(&s_err, err);
   __syncthreads();
   if (tid == 0) p.status[blockIdx.x] = s_err;
@@ -518,53 +525,34 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
 // unnormalised output of part i, m = max m_i, l = sum l_i 2^(m_i - m),
 // o = sum O_i 2^(m_i - m) / l, always in the order of the parts, so that a
 // result does not change from run to run.  A row without any key gets zeros.
-// Bound by latency: the parts lie in L2.  A block takes an item's rows, a
-// few of them at a time; where there are few rows in all, several warps share
-// one, so that the many parts of a long sequence are read at once.
+// Bound by latency: the parts lie in L2.  Several warps share a row where
+// there are few rows in all, so that the many parts of a long sequence are
+// read at once.
 struct CombineParams {
   Batch b;
-  Parts own, shared;     // shared.sched null: no shared keys
+  Parts own, shared;
   __nv_bfloat16* o;
   float* lse;
-  int rows_per_block;    // 1, 2, 4 or 8
+  int rows_per_pass;     // of a block's eight warps: 1, 2, 4 or 8
   int* header;           // see kKvHeaderBytes
   int alone, status_words;
 };
 
-// The parts of an item's rows: block c's slot of rows for c of [c0, c1], or
-// the rows' own places.
+// The parts of an item's rows: block c's slot of rows for c of [c0, c0 + n),
+// or, n = 1, the rows' own places.
 struct ItemParts {
   int n = 0;
-  long long c0 = 0;
   int second = 0;        // the first part lies in its block's second slot
+  long long c0 = 0;
   __device__ __forceinline__ void set(const Parts& P, long long start, long long nt, long long total) {
     const long long C = total < P.grid ? total : P.grid;
     c0 = block_of_tile(start, total, C);
     n = static_cast<int>(block_of_tile(start + nt - 1, total, C) - c0) + 1;
     second = start != first_tile(c0, total, C);
   }
-  __device__ __forceinline__ long long slot(const Parts& P, int i, int r) const {
-    return (2 * (c0 + i) + (i == 0 ? second : 0)) * P.slot_rows + r;
-  }
-};
-struct Row {
-  ItemParts own, sh;
-  int r_own, r_sh;
-  long long at;  // token * H + head
-  __device__ __forceinline__ int n() const { return own.n + sh.n; }
-  __device__ __forceinline__ float2 ml(const CombineParams& p, int i) const {
-    const bool mine = i < own.n;
-    const Parts& P = mine ? p.own : p.shared;
-    const ItemParts& I = mine ? own : sh;
-    return I.n == 1 ? P.row_ml[at] : P.slot_ml[I.slot(P, mine ? i : i - own.n, mine ? r_own : r_sh)];
-  }
-  __device__ __forceinline__ float4 o(const CombineParams& p, int i, int lane) const {
-    const bool mine = i < own.n;
-    const Parts& P = mine ? p.own : p.shared;
-    const ItemParts& I = mine ? own : sh;
-    const float* base =
-        I.n == 1 ? P.row_o + at * HD : P.slot_o + I.slot(P, mine ? i : i - own.n, mine ? r_own : r_sh) * HD;
-    return reinterpret_cast<const float4*>(base)[lane];
+  // the place of part i of a row: r within the item's slots, `at` among all rows
+  __device__ __forceinline__ long long place(const Parts& P, int i, int r, long long at) const {
+    return n == 1 ? at : (2 * (c0 + i) + (i == 0 ? second : 0)) * P.slot_rows + r;
   }
 };
 
@@ -579,6 +567,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// A block takes rows of one item.  SHARED: any item, blockIdx.x being its
+// number, with the parts of its own keys and of the shared ones.  Otherwise
+// the item that block blockIdx.x of the attention began and others ended.
+template <bool SHARED>
 __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__ CombineParams p) {
   __shared__ float4 s_acc[8][32];
   grid_dep_wait();
@@ -589,99 +581,134 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     p.header[2] = p.status_words;
     if (p.alone) p.header[0] = p.header[1] = 0;
   }
-  // the item: a sequence, a key/value head and, of the many-rows kernel, a
-  // row tile (sequence b's row tiles start at cu[b] G / RT + b)
-  const int h = blockIdx.x % B.Hkv, u = blockIdx.x / B.Hkv;
-  int b = u, rt = 0;
-  if (p.own.rt) {
-    int lo = 0, hi = B.B;
-    auto first = [&](int x) {
-      return min(max(B.cu[x], 0), B.n_tokens) * static_cast<long long>(B.G) / p.own.rt + x;
-    };
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first(mid) <= u) lo = mid; else hi = mid;
+  ItemParts own, sh;
+  int h, rt = 0, q0, rows;  // rows: of this row tile
+  long long nt_sh = 0, n_rt_sh = 0;
+  if (SHARED) {
+    // sequence b's row tiles start at cu[b] G / RT + b
+    h = blockIdx.x % B.Hkv;
+    const int u = blockIdx.x / B.Hkv;
+    int b = u;
+    if (p.own.rt) {
+      int lo = 0, hi = B.B;
+      auto first = [&](int x) {
+        return min(max(B.cu[x], 0), B.n_tokens) * static_cast<long long>(B.G) / p.own.rt + x;
+      };
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first(mid) <= u) lo = mid; else hi = mid;
+      }
+      b = lo;
+      rt = static_cast<int>(u - first(b));
     }
-    b = lo;
-    rt = static_cast<int>(u - first(b));
-  }
-  const Seq s = load_seq(B, b);
-  const int rows = min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
-  const int row0 = blockIdx.y * p.rows_per_block;
-  if (row0 >= rows) return;
-  Row R{};
-  {
-    const long long before = p.own.sched[b], per_head = p.own.sched[b + 1] - before;
+    const Seq s = load_seq(B, b);
+    const long long before = p.own.sched[b], per_head = p.own.sched[b + 1] - before, total = p.own.sched[B.B];
+    nt_sh = p.shared.sched[0];
+    n_rt_sh = p.shared.sched[1];
+    q0 = s.q0;
+    rows = min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
     long long nt = per_head, pre = 0;
     if (p.own.rt) {
       using C = Cut<false, 128, RT_MANY>;
-      nt = C::tiles(B, s, rt);
+      nt = rows > 0 ? C::tiles(B, s, rt) : 0;
       int sum = 0;
       for (int i = lane; i < rt; i += 32) sum += C::tiles(B, s, i);
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       pre = sum;
     }
-    if (nt > 0) R.own.set(p.own, before * B.Hkv + h * per_head + pre, nt, p.own.sched[B.B] * B.Hkv);
+    if (nt > 0) own.set(p.own, before * B.Hkv + h * per_head + pre, nt, total * B.Hkv);
+  } else {
+    const Split x = p.own.split[blockIdx.x];
+    if (x.parts == 0) return;
+    h = x.h;
+    rt = x.rt;
+    q0 = x.q0;
+    rows = min(x.rows - rt * p.own.rt, p.own.slot_rows);
+    own.n = x.parts;
+    own.c0 = blockIdx.x;
+    own.second = x.second;
   }
-  if (!p.shared.sched && R.own.n == 1) return;  // written by the block that had it whole
-  const int per_row = 8 / p.rows_per_block;     // warps
+  const int per_row = 8 / p.rows_per_pass;  // warps
   const int wr = warp / per_row, wp = warp - wr * per_row;
-  const int r = row0 + wr;
-  const bool live = r < rows;
-  float m = -INFINITY, l = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live) {
-    const int item_row = rt * p.own.rt + r, tok = s.q0 + item_row / B.G, g = item_row % B.G;
-    R.r_own = r;
-    R.at = static_cast<long long>(tok) * B.H + h * B.G + g;
-    if (p.shared.sched) {
-      const long long nt = p.shared.sched[0], n_rt = p.shared.sched[1];
-      if (nt > 0) {
+  for (int row0 = blockIdx.y * p.rows_per_pass; row0 < rows; row0 += gridDim.y * p.rows_per_pass) {
+    const int r = row0 + wr;
+    const bool live = r < rows;
+    float m = -INFINITY, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    long long at = 0;
+    if (live) {
+      const int item_row = rt * p.own.rt + r, tok = q0 + item_row / B.G, g = item_row % B.G;
+      at = static_cast<long long>(tok) * B.H + h * B.G + g;
+      int r_sh = 0;
+      if (SHARED && nt_sh > 0) {
         const int all = tok * B.G + g, srt = p.shared.rt ? all / p.shared.rt : 0;
-        R.r_sh = all - srt * p.shared.rt;
-        R.sh.set(p.shared, (h * n_rt + srt) * nt, nt, nt * n_rt * B.Hkv);
+        r_sh = all - srt * p.shared.rt;
+        sh.set(p.shared, (h * n_rt_sh + srt) * nt_sh, nt_sh, nt_sh * n_rt_sh * B.Hkv);
+      }
+      const int n = own.n + sh.n;
+      auto ml_of = [&](int i) {
+        return i < own.n ? p.own.slot_ml[own.place(p.own, i, r, 0)]
+                         : p.shared.slot_ml[sh.place(p.shared, i - own.n, r_sh, 0)];
+      };
+      auto ml = [&](int i) {
+        if (SHARED && (i < own.n ? own.n : sh.n) == 1) return (i < own.n ? p.own : p.shared).row_ml[at];
+        return ml_of(i);
+      };
+      auto o = [&](int i) {
+        const bool mine = !SHARED || i < own.n;
+        const Parts& P = mine ? p.own : p.shared;
+        const ItemParts& I = mine ? own : sh;
+        const float* base = (SHARED && I.n == 1 ? P.row_o : P.slot_o) +
+                            I.place(P, mine ? i : i - own.n, mine ? r : r_sh, at) * HD;
+        return reinterpret_cast<const float4*>(base)[lane];
+      };
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, ml(i).x);
+      m = warp_max(m);
+      if (m != -INFINITY) {
+        for (int i = lane; i < n; i += 32) {
+          const float2 v = ml(i);
+          l += v.y * ex2(v.x - m);
+        }
+        l = warp_sum(l);
+        // this warp's parts wp, wp + per_row, ..., 32 at a time
+        for (int j0 = wp; j0 < n; j0 += 32 * per_row) {
+          const int mine = j0 + lane * per_row;
+          const float f = mine < n ? ex2(ml(mine).x - m) : 0.f;
+          const int cnt = min(32, (n - j0 + per_row - 1) / per_row);
+#pragma unroll 8
+          for (int j = 0; j < cnt; ++j) {
+            const float w = __shfl_sync(0xffffffffu, f, j);
+            const float4 v = o(j0 + j * per_row);
+            a.x += w * v.x;
+            a.y += w * v.y;
+            a.z += w * v.z;
+            a.w += w * v.w;
+          }
+        }
       }
     }
-    const int n = R.n();
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, R.ml(p, i).x);
-    m = warp_max(m);
-    if (m != -INFINITY) {
-      for (int i = lane; i < n; i += 32) {
-        const float2 ml = R.ml(p, i);
-        l += ml.y * ex2(ml.x - m);
-      }
-      l = warp_sum(l);
-#pragma unroll 4
-      for (int i = wp; i < n; i += per_row) {
-        const float f = ex2(R.ml(p, i).x - m);
-        const float4 v = R.o(p, i, lane);
-        a.x += f * v.x;
-        a.y += f * v.y;
-        a.z += f * v.z;
-        a.w += f * v.w;
-      }
+    if (per_row > 1) {
+      s_acc[warp][lane] = a;
+      __syncthreads();
+      if (wp == 0)
+        for (int w = 1; w < per_row; ++w) {
+          const float4 v = s_acc[warp + w][lane];
+          a.x += v.x;
+          a.y += v.y;
+          a.z += v.z;
+          a.w += v.w;
+        }
+      __syncthreads();
     }
+    if (!live || wp) continue;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint2 w;
+    w.x = pack_bf16x2(a.x * inv, a.y * inv);
+    w.y = pack_bf16x2(a.z * inv, a.w * inv);
+    reinterpret_cast<uint2*>(p.o + at * HD)[lane] = w;
+    if (p.lse && lane == 0) p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
   }
-  if (per_row > 1) {
-    s_acc[warp][lane] = a;
-    __syncthreads();
-    if (wp) return;
-    for (int w = 1; w < per_row; ++w) {
-      const float4 v = s_acc[warp + w][lane];
-      a.x += v.x;
-      a.y += v.y;
-      a.z += v.z;
-      a.w += v.w;
-    }
-  }
-  if (!live) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint2 w;
-  w.x = pack_bf16x2(a.x * inv, a.y * inv);
-  w.y = pack_bf16x2(a.z * inv, a.w * inv);
-  reinterpret_cast<uint2*>(p.o + R.at * HD)[lane] = w;
-  if (p.lse && lane == 0) p.lse[R.at] = l > 0.f ? m + log2f(l) : -INFINITY;
 }
 
 // ================================================================ host
@@ -763,7 +790,7 @@ constexpr int kFewRows = 64;  // at most so many rows to a key/value head: the f
 struct AttendPlan {
   bool share = false;
   kv::Parts own, shared;      // the pointers as offsets from the scratch's start
-  int items = 0, item_rows = 0;
+  int items = 0;              // that the combine kernel looks at
   size_t bytes = 0;
 };
 AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
@@ -781,7 +808,10 @@ AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
     p.slot_rows = static_cast<int>(many ? kv::RT_MANY : item_rows);
     p.grid = many ? num_sms : kv::few_blocks(num_sms);
     const size_t slots = 2 * static_cast<size_t>(p.grid) * p.slot_rows;
-    p.sched = reinterpret_cast<long long*>(take(sched * 8));
+    if (P.share)
+      p.sched = reinterpret_cast<long long*>(take(sched * 8));
+    else
+      p.split = reinterpret_cast<kv::Split*>(take(p.grid * sizeof(kv::Split)));
     p.slot_o = reinterpret_cast<float*>(take(slots * kv::HD * 4));
     p.slot_ml = reinterpret_cast<float2*>(take(slots * 8));
     if (P.share) {
@@ -796,8 +826,7 @@ AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
   part(P.own, a.max_new * G, static_cast<size_t>(a.n_seqs) + 1);
   if (P.share) part(P.shared, a.n_tokens * G, 2);
   const int64_t units = P.own.rt ? a.n_tokens * G / kv::RT_MANY + a.n_seqs : a.n_seqs;
-  P.items = static_cast<int>(units * a.Hkv);
-  P.item_rows = P.own.slot_rows;
+  P.items = P.share ? static_cast<int>(units * a.Hkv) : P.own.grid;
   P.bytes = off;
   return P;
 }
@@ -837,13 +866,20 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
   c.lse = lse;
   c.header = header;
   c.alone = alone;
-  c.rows_per_block = 8;
-  while (c.rows_per_block > 1 &&
-         static_cast<int64_t>(P.items) * ((P.item_rows + c.rows_per_block - 1) / c.rows_per_block) < ctx.num_sms)
-    c.rows_per_block /= 2;
+  // All eight warps of a block at work, and few rows on more blocks than one:
+  // at most two blocks of 256 threads per SM before rows share a pass.
+  const int item_rows = P.own.slot_rows;
+  c.rows_per_pass = 8;
+  while (c.rows_per_pass > 1 &&
+         (c.rows_per_pass >= 2 * item_rows || static_cast<int64_t>(a.n_tokens) * a.H < 2 * c.rows_per_pass * ctx.num_sms))
+    c.rows_per_pass /= 2;
+  const int passes = (item_rows + c.rows_per_pass - 1) / c.rows_per_pass;
+  const dim3 grid(P.items, passes < 16 ? passes : 16);
   if (ctx.before) ctx.before(ctx.user, "kv_combine", ctx.stream);
-  kv::launch_dep(kv::kv_combine_kernel,
-                 dim3(P.items, (P.item_rows + c.rows_per_block - 1) / c.rows_per_block), 256, 0, ctx.stream, c);
+  if (P.share)
+    kv::launch_dep(kv::kv_combine_kernel<true>, grid, 256, 0, ctx.stream, c);
+  else
+    kv::launch_dep(kv::kv_combine_kernel<false>, grid, 256, 0, ctx.stream, c);
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
   return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;

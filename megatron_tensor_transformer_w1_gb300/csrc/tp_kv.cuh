@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include "tp_internal.h"
@@ -148,96 +150,121 @@ __device__ __forceinline__ void advance(const Batch& p, Cursor& c) {
 }
 
 struct SchedScratch {
-  long long sums[128];
-  int best[128], len[128];
+  long long sums[4];
+  unsigned long long longest[4];
+  int least[4];
   Cursor start;
 };
 struct Sched {
-  int n_tiles;    // of this block
-  int table_row;  // whose page table leads to the shared pages
+  int n_tiles = 0;         // of this block
+  int table_row = 0;       // whose page table leads to the shared pages
+  bool all_see = false;    // every row sees every shared key
+  bool some_empty = false; // there are rows of sequences that belong to no tile
+  long long first = 0, total = 0, blocks = 0;
 };
 
 // Called by every thread of a block (at least 128): sums the tiles of all
-// sequences, finds the block's first tile and, in block 0, leaves the prefix
-// sums for the combine kernel: `sched` [B + 1] tiles per key/value head before
-// sequence b, or for prefix items {tiles of a row tile, row tiles}.
+// sequences and finds the block's first tile.  Block 0 leaves the prefix sums
+// for the combine kernel where that asks for them: `sched` [B + 1] tiles per
+// key/value head before sequence b, or for prefix items {tiles of a row tile,
+// row tiles}.
 template <typename C, bool PREFIX>
 __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, SchedScratch* w, Cursor& c, int* err) {
-  const int tid = threadIdx.x;
-  Sched S{0, 0};
+  const int tid = threadIdx.x, lane = tid & 31;
+  Sched S;
   if constexpr (PREFIX) {
     // the longest sequence's table covers the shared pages if any does
     if (tid < 128) {
-      int best = 0, len = -1;
+      unsigned long long longest = 0;
+      int least = INT_MAX;
       for (int b = tid; b < p.B; b += 128) {
-        const int l = min(max(p.kv_len[b], 0), p.cap);
-        if (l > len) { len = l; best = b; }
+        const Seq s = load_seq(p, b);
+        const unsigned long long key = (static_cast<unsigned long long>(s.kv) << 32) | (0xffffffffu - b);
+        longest = key > longest ? key : longest;
+        if (s.qn > 0) least = min(least, s.visible(0, p.causal));
       }
-      w->best[tid] = best;
-      w->len[tid] = len;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(0xffffffffu, longest, d);
+        longest = o > longest ? o : longest;
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+      }
+      if (lane == 0) {
+        w->longest[tid >> 5] = longest;
+        w->least[tid >> 5] = least;
+      }
     }
     __syncthreads();
-    for (int d = 64; d; d >>= 1) {
-      if (tid < d) {
-        const int ol = w->len[tid + d], ob = w->best[tid + d];
-        if (ol > w->len[tid] || (ol == w->len[tid] && ob < w->best[tid])) { w->len[tid] = ol; w->best[tid] = ob; }
-      }
-      __syncthreads();
+    unsigned long long longest = w->longest[0];
+    int least = w->least[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      longest = w->longest[i] > longest ? w->longest[i] : longest;
+      least = min(least, w->least[i]);
     }
-    S.table_row = w->best[0];
+    S.table_row = static_cast<int>(0xffffffffu - static_cast<unsigned>(longest));
     c.b = 0;
     c.s.q0 = 0;
     c.s.qn = min(max(p.cu[p.B], 0), p.n_tokens);
-    c.s.kv = min(p.shared, w->len[0]);
+    c.s.kv = min(p.shared, static_cast<int>(longest >> 32));
     c.s.err = 0;
+    S.all_see = least >= c.s.kv;
     const int n_rt = C::row_tiles(p, c.s);
     c.nt = C::tiles(p, c.s, 0);
-    const long long total = static_cast<long long>(n_rt) * c.nt * p.Hkv;
+    S.total = static_cast<long long>(n_rt) * c.nt * p.Hkv;
     if (blockIdx.x == 0 && tid == 0) {
       sched[0] = c.nt;
       sched[1] = n_rt;
     }
-    const long long blocks = total < gridDim.x ? total : gridDim.x;
-    if (blockIdx.x >= blocks) return S;
-    const long long first = first_tile(blockIdx.x, total, blocks);
-    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, total, blocks) - first);
-    const long long item = first / c.nt;
-    c.t = static_cast<int>(first - item * c.nt);
+    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
+    if (blockIdx.x >= S.blocks) return S;
+    S.first = first_tile(blockIdx.x, S.total, S.blocks);
+    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, S.total, S.blocks) - S.first);
+    const long long item = S.first / c.nt;
+    c.t = static_cast<int>(S.first - item * c.nt);
     c.h = static_cast<int>(item / n_rt);
     c.rt = static_cast<int>(item - static_cast<long long>(c.h) * n_rt);
   } else {
     const int per = (p.B + 127) / 128;
     const int b0 = min(tid * per, p.B), b1 = tid < 128 ? min(b0 + per, p.B) : b0;
     long long sum = 0;
+    int empty = 0;
     for (int b = b0; b < b1; ++b) {
       const Seq s = load_seq(p, b);
       *err |= s.err;
       sum += C::tiles_per_head(p, s);
+      empty |= s.qn > 0 && C::tiles(p, s, 0) == 0;
     }
-    if (tid < 128) w->sums[tid] = sum;
-    __syncthreads();
-    for (int d = 1; d < 128; d <<= 1) {
-      const long long add = tid < 128 && tid >= d ? w->sums[tid - d] : 0;
-      __syncthreads();
-      if (tid < 128) w->sums[tid] += add;
-      __syncthreads();
+    long long before = sum;  // inclusive sums within the warp
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += o;
     }
-    const long long total = w->sums[127] * p.Hkv;
-    const long long blocks = total < gridDim.x ? total : gridDim.x;
-    const long long before = tid < 128 ? w->sums[tid] - sum : 0;
-    if (blockIdx.x == 0 && tid < 128) {
+    if (tid < 128 && lane == 31) w->sums[tid >> 5] = before;
+    S.some_empty = __syncthreads_or(empty) != 0;
+    long long total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < (tid >> 5)) before += w->sums[i];
+      total += w->sums[i];
+    }
+    before -= sum;
+    S.total = total * p.Hkv;
+    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
+    if (sched && blockIdx.x == 0 && tid < 128) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
         sched[b] = at;
         at += C::tiles_per_head(p, load_seq(p, b));
       }
-      if (tid == 127) sched[p.B] = w->sums[127];
+      if (tid == 127) sched[p.B] = total;
     }
-    if (blockIdx.x >= blocks) return S;
-    const long long first = first_tile(blockIdx.x, total, blocks);
-    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, total, blocks) - first);
-    if (tid < 128 && first >= before * p.Hkv && first < (before + sum) * p.Hkv) {
-      long long at = first - before * p.Hkv;
+    if (blockIdx.x >= S.blocks) return S;
+    S.first = first_tile(blockIdx.x, S.total, S.blocks);
+    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, S.total, S.blocks) - S.first);
+    if (tid < 128 && S.first >= before * p.Hkv && S.first < (before + sum) * p.Hkv) {
+      long long at = S.first - before * p.Hkv;
       for (int b = b0; b < b1; ++b) {
         Cursor x;
         x.b = b;
@@ -264,6 +291,13 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
   return S;
 }
 
+// An item cut between blocks, noted by the block that has its first tile.
+struct Split {
+  int h, rt, q0, rows;  // rows: of the sequence and head, all row tiles
+  int parts, second;    // 0 parts: the block's last segment is none; second: it is not the block's first
+  int pad[2];
+};
+
 // What a segment leaves for the combine kernel: the running maximum (in log2
 // units) and sum of each row, and its unnormalised output in 32 bits.  A
 // segment that is a whole item goes to its rows' own places ([token][head],
@@ -274,9 +308,25 @@ struct Parts {
   float2* slot_ml = nullptr;  // [2 blocks][slot_rows]
   float* row_o = nullptr;     // [n_tokens * H][HD]
   float2* row_ml = nullptr;
-  long long* sched = nullptr;
+  long long* sched = nullptr; // null: the splits say all
+  Split* split = nullptr;     // [blocks]
   int slot_rows = 0, grid = 0, rt = 0;  // rt: rows of a row tile, 0: all
 };
+
+// The note on a block's last segment: tile x of the list is its last one.
+__device__ __forceinline__ Split split_of(const Batch& p, const Sched& S, const Cursor& x, int seg_t, bool second) {
+  Split r{};
+  const long long end = S.first + S.n_tiles + (x.nt - x.t - 1);  // the item's
+  if (seg_t == 0 && x.t + 1 < x.nt) {
+    r.h = x.h;
+    r.rt = x.rt;
+    r.q0 = x.s.q0;
+    r.rows = x.s.qn * p.G;
+    r.parts = static_cast<int>(block_of_tile(end - 1, S.total, S.blocks) - blockIdx.x) + 1;
+    r.second = second;
+  }
+  return r;
+}
 
 struct AttendParams {
   Batch b;
@@ -292,6 +342,26 @@ struct AttendParams {
 constexpr int RT_MANY = 256;  // rows of an item of the many-rows kernel
 // The many-rows kernel (tp_kv_tc.cu).
 int launch_many(const AttendParams& p, bool prefix, LaunchCtx& ctx, const char* name);
+
+// Rows that see no key at all and belong to no tile: zeros.  By all threads;
+// block c takes the sequences c, c + grid, ...
+template <typename C>
+__device__ __forceinline__ void write_empty_rows(const AttendParams& p, int rt_rows) {
+  const Batch& B = p.b;
+  for (int b = blockIdx.x; b < B.B; b += gridDim.x) {
+    const Seq s = load_seq(B, b);
+    const int rows = s.qn * B.G, n_rt = C::row_tiles(B, s);
+    for (int rt = 0; rt < n_rt && C::tiles(B, s, rt) == 0; ++rt) {
+      const int r0 = rt * rt_rows, n = rt_rows ? min(rt_rows, rows - r0) : rows;
+      for (int i = threadIdx.x; i < n * B.Hkv * 16; i += blockDim.x) {
+        const int r = r0 + i / (16 * B.Hkv), h = (i >> 4) % B.Hkv;
+        const long long row = static_cast<long long>(s.q0 + r / B.G) * B.H + h * B.G + r % B.G;
+        reinterpret_cast<uint4*>(p.o + row * HD)[i & 15] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse && (i & 15) == 0) p.lse[row] = -INFINITY;
+      }
+    }
+  }
+}
 
 // Launch as a programmatic dependent of the stream's previous kernel.
 template <typename... KArgs, typename... Args>

@@ -21,8 +21,8 @@
 //    from.  Products run in the order of issue, so S_t of the next key tile,
 //    issued behind O_t += P_t V, finds P_t read, and when it is done that sum
 //    is too;
-//  * warp 2: gathers the query rows of the next item into the swizzled
-//    layout of the products;
+//  * warps 2 and 3: gather the query rows of the next item, a row tile each,
+//    into the swizzled layout of the products;
 //  * warps 4-7 and 8-11: the softmax of row tiles 0 and 1, a row per thread,
 //    with a maximum that moves only when it grew by more than 2^8, so that
 //    O_t is rarely rescaled; they write the rows out at the end of a segment.
@@ -64,10 +64,6 @@ static_assert(sizeof(SchedScratch) <= 8 * 4096, "the schedule's scratch lies whe
 template <bool PREFIX>
 using Many = Cut<PREFIX, BK, RT_MANY>;
 
-__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* tm, uint64_t* bar, int col, int slot,
-                                              int head, int page) {
-  tma_load_4d(dst, tm, bar, col, slot, head, page);
-}
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -80,6 +76,58 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
+}
+
+// Waits for tensor-memory loads; names their registers, so that no use of
+// them moves before the wait.
+__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
+                 "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]),
+                 "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                 "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]),
+                 "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15]), "+r"(b[16]), "+r"(b[17]), "+r"(b[18]),
+                 "+r"(b[19]), "+r"(b[20]), "+r"(b[21]), "+r"(b[22]), "+r"(b[23])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]), "+r"(b[29]), "+r"(b[30]),
+                 "+r"(b[31])
+               :
+               : "memory");
+}
+// Two 32-bit operations per instruction, and a maximum of three: with two
+// softmax warps per scheduler their instructions are what the time goes by.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 template <bool PREFIX>
@@ -128,7 +176,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   grid_dep_wait();
   grid_dep_launch();
-  if (threadIdx.x == 0) *status = 0;
+  if (threadIdx.x == 0) {
+    *status = 0;
+    if (p.part.split) p.part.split[blockIdx.x] = Split{};
+  }
   int err = 0;
   Cursor c;
   const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem + M_OUT), c, &err);
@@ -148,18 +199,26 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     const int groups = BK / box;  // at most 16
     int last_phase[SLOTS] = {-1, -1, -1, -1};
     bool ok = true;
+    // the page of this lane's group of tile x, looked up a tile ahead
+    auto look_up = [&](const Cursor& x) -> int {
+      const int key = (t0 + x.t) * BK + lane * box;
+      if (lane >= groups || key >= x.s.kv) return -1;
+      const int row = PREFIX ? S.table_row : x.b;
+      return B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
+    };
+    int next = N > 0 ? look_up(c) : -1;
     for (int n = 0; n < N && ok; ++n) {
       const int base = (t0 + c.t) * BK;
       const int live = min(groups, (c.s.kv - base + box - 1) / box);  // groups that hold keys
-      int page = static_cast<int>(B.n_pages);  // past the end: the copy fills with zeros
-      const int key = base + lane * box;
-      if (lane < live) {
-        const int row = PREFIX ? S.table_row : c.b;
-        const int at = B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
-        if (at >= 0 && at < B.n_pages)
-          page = at;
-        else
-          atomicOr(status, DEV_ERR_BATCH);
+      const int key = base + lane * box, h = c.h;
+      int page = next;
+      if (n + 1 < N) {
+        advance<C, PREFIX>(B, c);
+        next = look_up(c);
+      }
+      if (lane < live && (page < 0 || page >= B.n_pages)) {
+        page = static_cast<int>(B.n_pages);  // past the end: the copy fills with zeros
+        atomicOr(status, DEV_ERR_BATCH);
       }
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t i = 2u * n + kv;
@@ -173,11 +232,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           uint8_t* dst = ring(i) + lane * box * 128;
           const CUtensorMap* tm = kv ? &tv : &tk;
           const int at = key & (page_keys - 1);
-          tma_load_page(dst, tm, &full[slot], 0, at, c.h, page);
-          tma_load_page(dst + TILE_BYTES / 2, tm, &full[slot], 64, at, c.h, page);
+          tma_load_4d(dst, tm, &full[slot], 0, at, h, page);
+          tma_load_4d(dst + TILE_BYTES / 2, tm, &full[slot], 64, at, h, page);
         }
       }
-      if (n + 1 < N) advance<C, PREFIX>(B, c);
     }
     // every issued copy lands before the block may exit
 #pragma unroll
@@ -191,6 +249,11 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       constexpr uint32_t ID_PV = idesc(128, 0, 1);  // O += P V (V: N = hd contiguous)
       uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
       bool ok = true;
+      // descriptors: one of each kind, then steps in units of 16 bytes; one
+      // thread issues everything, and the few instructions between two
+      // products count
+      const uint64_t q_desc = kdesc(smem_u32(smem + M_Q), 128, 0), k_desc = kdesc(smem_u32(smem + M_RING), 128, 0),
+                     v_desc = mndesc(smem_u32(smem + M_RING), 128, 0);
       // S_t of tile x (the n-th of this block)
       auto issue_s = [&](int t, const Cursor& x, int n, bool new_seg, bool seg_ends) -> bool {
         if (new_seg) {
@@ -198,10 +261,13 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           ++q_uses[t];
         }
         tc_fence_after();
-        const uint32_t qa = smem_u32(smem + M_Q + t * TILE_BYTES), ka = smem_u32(ring(2u * n));
+        const uint64_t qd = q_desc + static_cast<uint64_t>(t * (TILE_BYTES >> 4));
+        const uint64_t kd = k_desc + static_cast<uint64_t>(((2u * n) & (SLOTS - 1)) * (TILE_BYTES >> 4));
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_bf16(tmem + t * 128, kdesc(qa, 128, ks), kdesc(ka, 128, ks), ID_S, ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint64_t step = ((ks >> 2) * 128 * 128 + (ks & 3) * 32) >> 4;
+          umma_bf16(tmem + t * 128, qd + step, kd + step, ID_S, ks > 0 ? 1u : 0u);
+        }
         umma_commit(&s_full[t]);
         if (seg_ends) umma_commit(&q_empty[t]);
         return true;
@@ -221,14 +287,16 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         const bool two_next = more && rows_of(x) > 128;
         ok = wait_tile(2u * n + 1) && (!more || wait_tile(2u * n + 2));
         if (!ok) break;
-        const uint32_t va = smem_u32(ring(2u * n + 1));
+        const uint64_t vd = v_desc + static_cast<uint64_t>(((2u * n + 1) & (SLOTS - 1)) * (TILE_BYTES >> 4));
         auto issue_pv = [&](int t) -> bool {
           if (!W(&p_full[t], p_uses[t] & 1u)) return false;
           ++p_uses[t];
           tc_fence_after();
-          for (int ks = 0; ks < steps; ++ks)
-            umma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, mndesc(va, 128, ks), ID_PV,
-                         (!first || ks > 0) ? 1u : 0u);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            if (ks < steps)
+              umma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, vd + static_cast<uint64_t>(ks * 128), ID_PV,
+                           (!first || ks > 0) ? 1u : 0u);
           if (last) umma_commit(&o_full[t]);
           return true;
         };
@@ -252,35 +320,41 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       W.drain(drain, 0u);
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------ query rows of each segment
-    uint32_t uses[2] = {0, 0};
-    bool ok = true, fresh = true;
-    for (int n = 0; n < N && ok; ++n) {
-      if (fresh) {
-        const int rows = rows_of(c);
-        for (int t = 0; t < 2 && rows > t * 128; ++t) {
-          if (!W.warp(&q_empty[t], (uses[t] & 1u) ^ 1u)) { ok = false; break; }
-          ++uses[t];
-          const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
-          // 16 lanes to a row: two rows of 256 bytes a time
-          for (int r = lane >> 4; r < 128; r += 2) {
-            const int item_row = c.rt * RT_MANY + t * 128 + r;
-            const bool valid = t * 128 + r < rows;
-            const int tok = valid ? item_row / B.G : 0, g = valid ? item_row - tok * B.G : 0;
-            const long long off =
-                valid ? (static_cast<long long>(c.s.q0 + tok) * B.H + c.h * B.G + g) * HD + (lane & 15) * 8 : 0;
-            cp_async16z(sw_chunk(qs, 128, r, lane & 15), p.q + off, valid);
+  } else if (warp < 4) {
+    // ------------------------------------------------ query rows of each segment, row tile t
+    const int t = warp - 2, dtok = 2 / B.G, dg = 2 - dtok * B.G;
+    const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
+    uint32_t uses = 0;
+    bool fresh = true;
+    for (int n = 0; n < N; ++n) {
+      const int rows = rows_of(c) - t * 128;
+      if (fresh && rows > 0) {
+        if (!W.warp(&q_empty[t], (uses & 1u) ^ 1u)) break;
+        ++uses;
+        // 16 lanes to a row: two rows of 256 bytes a time
+        const int r0 = lane >> 4, item_row = c.rt * RT_MANY + t * 128 + r0;
+        int tok = item_row / B.G, g = item_row - tok * B.G;
+        const __nv_bfloat16* src =
+            p.q + (static_cast<long long>(c.s.q0) * B.H + static_cast<long long>(c.h) * B.G) * HD + (lane & 15) * 8;
+#pragma unroll 8
+        for (int i = 0; i < 64; ++i) {
+          const bool valid = r0 + 2 * i < rows;
+          cp_async16z(sw_chunk(qs, 128, r0 + 2 * i, lane & 15),
+                      valid ? src + (static_cast<long long>(tok) * B.H + g) * HD : src, valid);
+          tok += dtok;
+          g += dg;
+          if (g >= B.G) {
+            g -= B.G;
+            ++tok;
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          mbar_arrive(&q_full[t]);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[t]);
       }
       fresh = c.t + 1 == c.nt;
       if (n + 1 < N) advance<C, PREFIX>(B, c);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------ softmax of row tile t
@@ -307,7 +381,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           if (r < rows) {
             const int item_row = c.rt * RT_MANY + r, tok = item_row / B.G;
             at = (c.s.q0 + tok) * B.H + c.h * B.G + (item_row - tok * B.G);
-            if (PREFIX) {
+            if (PREFIX && S.all_see) {
+              limit = c.s.kv;
+            } else if (PREFIX) {
               const int b = find_seq(B.cu, B.B, tok);
               if (b < B.B) {
                 const Seq s = load_seq(B, b);
@@ -321,24 +397,38 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         if (!W.warp(&s_full[t], s_uses & 1u)) break;
         ++s_uses;
         tc_fence_after();
-        uint32_t r[128];
+        // The scores are read twice, 64 columns at a time: for the maximum, then
+        // for the exponentials.  Holding all 128 spills registers, and the
+        // straight-line code for them misses the instruction cache.
+        const uint32_t ts = tl + t * 128;
+        const int base = (t0 + c.t) * BK, from = lo - base, to = limit - base;
+        const bool masked = __any_sync(0xffffffffu, from > 0 || to < BK);
+        auto hide = [&](uint32_t (&r)[32], int col) {
+          if (!masked) return;
+          const int a = from - col, b = to - col;  // columns [a, b) of these 32 are seen
+          const uint32_t below = b >= 32 ? 0xffffffffu : (b <= 0 ? 0u : (1u << b) - 1u);
+          const uint32_t seen = below & (a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : 0xffffffffu << a));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tmem_ld32(tl + t * 128 + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * k]));
-        tmem_wait_ld();
-        const int base = (t0 + c.t) * BK;
-        if (__any_sync(0xffffffffu, base < lo || base + BK > limit)) {
+          for (int k = 0; k < 32; ++k) r[k] = (seen >> k) & 1u ? r[k] : __float_as_uint(-INFINITY);
+        };
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto maxima = [&](const uint32_t (&r)[32]) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            r[k] = (base + k >= lo && base + k < limit) ? r[k] : __float_as_uint(-INFINITY);
+          for (int k = 0; k < 32; k += 2)
+            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+        };
+#pragma unroll 1
+        for (int col = 0; col < BK; col += 64) {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(ts + col, ra);
+          tmem_ld32(ts + col + 32, rb);
+          tmem_wait_ld2(ra, rb);
+          hide(ra, col);
+          maxima(ra);
+          hide(rb, col + 32);
+          maxima(rb);
         }
-        float m8[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m8[k] = __uint_as_float(r[k]);
-#pragma unroll
-        for (int k = 8; k < 128; ++k) m8[k & 7] = fmaxf(m8[k & 7], __uint_as_float(r[k]));
-        const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.scale_log2;
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
         float alpha = 1.f;
         bool rescale = false;
         if (m == -INFINITY) {
@@ -362,22 +452,39 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           tmem_wait_st();
         }
         const float neg_m = m == -INFINITY ? 0.f : -m;  // no key yet: every p is 0
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pack2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+        const uint64_t neg_m2 = pack2(__float_as_uint(neg_m), __float_as_uint(neg_m));
+        uint64_t l2[4] = {0, 0, 0, 0};
+        // P (two to a cell) goes over columns of S that have been read
+        auto exponentials = [&](const uint32_t (&r)[32], int col) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float e0 = ex2(fmaf(__uint_as_float(r[64 * half + 2 * k]), p.scale_log2, neg_m));
-            const float e1 = ex2(fmaf(__uint_as_float(r[64 * half + 2 * k + 1]), p.scale_log2, neg_m));
-            l4[k & 3] += e0 + e1;
+          for (int k = 0; k < 16; ++k) {
+            float e0, e1;
+            unpack2(fma2(pack2(r[2 * k], r[2 * k + 1]), scale2, neg_m2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            l2[k & 3] = add2(l2[k & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
             // rounded to bf16 for the second product; the sum is taken before
             pk[k] = pack_bf16x2(e0, e1);
           }
-          tmem_st32(tl + t * 128 + half * 32, pk);
+          tmem_st16(ts + col / 2, pk);
+        };
+#pragma unroll 1
+        for (int col = 0; col < BK; col += 64) {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(ts + col, ra);
+          tmem_ld32(ts + col + 32, rb);
+          tmem_wait_ld2(ra, rb);
+          hide(ra, col);
+          exponentials(ra, col);
+          hide(rb, col + 32);
+          exponentials(rb, col + 32);
         }
         tmem_wait_st();
-        l = l * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+        float la, lb;
+        unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), la, lb);
+        l = l * alpha + (la + lb);
         const int keys = min(BK, c.s.kv - base);  // of the sequence; V behind them may be anything
         if (t == 0 && (keys & 15)) {
           const uint32_t i = 2u * n + 1;
@@ -390,6 +497,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         tc_fence_before();
         arrive_warp(&p_full[t]);
         if (last) {
+          if (threadIdx.x == 128 && n + 1 == N && p.part.split)
+            p.part.split[blockIdx.x] = split_of(B, S, c, seg_t, seg_n > 0);
           // ---- the segment's rows: to o, to their own places, or to a slot
           if (!W.warp(&o_full[t], o_uses & 1u)) break;
           ++o_uses;
@@ -459,6 +568,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     __syncwarp();
   }
 
+  if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, RT_MANY);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
