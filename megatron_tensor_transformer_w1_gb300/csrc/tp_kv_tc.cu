@@ -16,16 +16,19 @@
 // products of the other run.  A block has
 //  * warp 0: copies K and V tiles by TMA, page by page (box: 64 columns by a
 //    page, or 128 keys of a longer one), into a ring of four 32 KB slots;
-//  * warp 1: one lane issues tcgen05.mma.  Per row tile t: S_t = Q_t K^T into
-//    tensor memory, then O_t += P_t V with P_t, in bf16, over the S_t it came
-//    from.  Products run in the order of issue, so S_t of the next key tile,
-//    issued behind O_t += P_t V, finds P_t read, and when it is done that sum
-//    is too;
-//  * warps 2 and 3: gather the query rows of the next item, a row tile each,
-//    into the swizzled layout of the products;
+//  * warps 1 and 2: a lane of each issues tcgen05.mma for row tile t = 0, 1:
+//    S_t = Q_t K^T into tensor memory, then O_t += P_t V with P_t, in bf16,
+//    over the S_t it came from.  Products run in the order of issue, so the
+//    S_t that is issued behind O_t += P_t V into the same buffer finds P_t
+//    read.  Two warps, because one spends a third of a step between products;
+//  * warp 3: gathers the query rows of the next item into the swizzled layout
+//    of the products;
 //  * warps 4-7 and 8-11: the softmax of row tiles 0 and 1, a row per thread,
 //    with a maximum that moves only when it grew by more than 2^8, so that
 //    O_t is rarely rescaled; they write the rows out at the end of a segment.
+// S_t comes in halves of 64 keys into two buffers, so that the softmax of one
+// half finds the next one's scores done: with one buffer of 128 keys a row
+// tile waits for its two products in every step.
 // Values of slots behind a sequence's last key may be anything, also NaN, and
 // 0 x NaN would spoil a row: the rows of V behind the last key are zeroed up
 // to the 16 that a product step takes, and the steps behind are left out.
@@ -52,6 +55,7 @@ using namespace tc;
 constexpr int BK = 128;                 // keys of a tile
 constexpr int TILE_BYTES = 128 * HD * 2;
 constexpr int SLOTS = 4;                // K and V tiles in flight
+constexpr int SK = 64;                  // keys of a product's half tile
 constexpr int MANY_THREADS = 384;
 constexpr int M_Q = 0;                             // two row tiles
 constexpr int M_RING = M_Q + 2 * TILE_BYTES;
@@ -64,6 +68,19 @@ static_assert(sizeof(SchedScratch) <= 8 * 4096, "the schedule's scratch lies whe
 template <bool PREFIX>
 using Many = Cut<PREFIX, BK, RT_MANY>;
 
+// A tile, to the issuing warp: product steps of 16 keys, whether it ends a
+// segment, whether the second row tile has rows.
+constexpr uint32_t I_STEPS = 15, I_LAST = 16, I_TWO = 32;
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -78,28 +95,15 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-// Waits for tensor-memory loads; names their registers, so that no use of
-// them moves before the wait.
-__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[32], uint32_t (&b)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
-                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
-                 "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]),
-                 "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27])
-               :
-               : "memory");
-  asm volatile(""
-               : "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
-                 "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]),
-                 "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15]), "+r"(b[16]), "+r"(b[17]), "+r"(b[18]),
-                 "+r"(b[19]), "+r"(b[20]), "+r"(b[21]), "+r"(b[22]), "+r"(b[23])
-               :
-               : "memory");
-  asm volatile(""
-               : "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]), "+r"(b[29]), "+r"(b[30]),
-                 "+r"(b[31])
-               :
-               : "memory");
+// Waits for tensor-memory loads; the second statement names their registers,
+// so that no use of them moves before the wait.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 // Two 32-bit operations per instruction, and a maximum of three: with two
 // softmax warps per scheduler their instructions are what the time goes by.
@@ -130,6 +134,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Hides the columns outside [from, to) of 32.
+__device__ __forceinline__ void hide(uint32_t (&r)[32], int from, int to) {
+  const uint32_t below = to >= 32 ? 0xffffffffu : (to <= 0 ? 0u : (1u << to) - 1u);
+  const uint32_t seen = below & (from <= 0 ? 0xffffffffu : (from >= 32 ? 0u : 0xffffffffu << from));
+#pragma unroll
+  for (int k = 0; k < 32; ++k) r[k] = (seen >> k) & 1u ? r[k] : __float_as_uint(-INFINITY);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 template <bool PREFIX>
 __global__ void __launch_bounds__(MANY_THREADS, 1)
     kv_many_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -142,12 +162,13 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   uint64_t* empty = bar + 4;    // [SLOTS] its products are done
   uint64_t* q_full = bar + 8;   // [2]
   uint64_t* q_empty = bar + 10; // [2] the item's last S_t is done
-  uint64_t* s_full = bar + 12;  // [2]
-  uint64_t* p_full = bar + 14;  // [2] P_t written (a warp each)
-  uint64_t* o_full = bar + 16;  // [2] the segment's last O_t is done
-  uint64_t* drain = bar + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 19);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 19) + 1;
+  uint64_t* s_full = bar + 12;  // [2][2] S_t of a half tile is done
+  uint64_t* p_full = bar + 16;  // [2][2] P_t written (a warp each)
+  uint64_t* pv_done = bar + 20; // [2][2] O_t has its product
+  uint64_t* drain = bar + 24;   // [2]
+  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(bar + 26);  // [2] of the tiles in the ring
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 27);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 27) + 1;
   const Batch& B = p.b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = p.status + blockIdx.x;
@@ -155,16 +176,18 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);  // both row tiles
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 32);
       mbar_init(&q_empty[t], 1);
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
-      mbar_init(&o_full[t], 1);
+      mbar_init(&drain[t], 1);
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -187,7 +210,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   __syncthreads();  // (also: the status word is clear, the scratch has been read)
   tc_fence_after();
   if (err) atomicOr(status, err);
-  const uint32_t tmem = *tmem_slot;  // S_0, S_1 at columns 0 and 128, O_0, O_1 at 256 and 384
+  const uint32_t tmem = *tmem_slot;  // S_t at columns 128 t and 128 t + 64, O_t at 256 + 128 t
   const Waiter W{abort_flag, status, p.timeout_ns};
   const int N = S.n_tiles, t0 = C::t0(B), lo = C::first_key(B);
   auto ring = [&](uint32_t i) { return smem + M_RING + (i & (SLOTS - 1)) * TILE_BYTES; };
@@ -211,6 +234,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const int base = (t0 + c.t) * BK;
       const int live = min(groups, (c.s.kv - base + box - 1) / box);  // groups that hold keys
       const int key = base + lane * box, h = c.h;
+      // what the issuing warp has to know of the tile; published with its K
+      const uint32_t what = static_cast<uint32_t>((min(BK, c.s.kv - base) + 15) / 16) |
+                            (c.t + 1 == c.nt || n + 1 == N ? I_LAST : 0u) | (rows_of(c) > 128 ? I_TWO : 0u);
       int page = next;
       if (n + 1 < N) {
         advance<C, PREFIX>(B, c);
@@ -225,7 +251,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         const int slot = i & (SLOTS - 1);
         const uint32_t ph = (i / SLOTS) & 1u;
         if (!W.warp(&empty[slot], ph ^ 1u)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(live * box) * HD * 2);
+        if (lane == 0) {
+          if (kv == 0) info[n & 1] = what;
+          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(live * box) * HD * 2);
+        }
         __syncwarp();
         last_phase[slot] = static_cast<int>(ph);
         if (lane < live) {
@@ -242,95 +271,120 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     for (int i = 0; i < SLOTS; ++i)
       if (last_phase[i] >= 0) W.drain(&full[i], static_cast<uint32_t>(last_phase[i]));
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------ products
-    if (lane == 0 && N > 0) {
-      constexpr uint32_t ID_S = idesc(128, 0, 0);   // S = Q K^T
+  } else if (warp < 3) {
+    // ------------------------------------------------ products of row tile t
+    if (N > 0) {
+      constexpr uint32_t ID_S = idesc(SK, 0, 0);    // S = Q K^T
       constexpr uint32_t ID_PV = idesc(128, 0, 1);  // O += P V (V: N = hd contiguous)
-      uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
-      bool ok = true;
-      // descriptors: one of each kind, then steps in units of 16 bytes; one
-      // thread issues everything, and the few instructions between two
-      // products count
-      const uint64_t q_desc = kdesc(smem_u32(smem + M_Q), 128, 0), k_desc = kdesc(smem_u32(smem + M_RING), 128, 0),
-                     v_desc = mndesc(smem_u32(smem + M_RING), 128, 0);
-      // S_t of tile x (the n-th of this block)
-      auto issue_s = [&](int t, const Cursor& x, int n, bool new_seg, bool seg_ends) -> bool {
-        if (new_seg) {
-          if (!W(&q_full[t], q_uses[t] & 1u)) return false;
-          ++q_uses[t];
-        }
-        tc_fence_after();
-        const uint64_t qd = q_desc + static_cast<uint64_t>(t * (TILE_BYTES >> 4));
-        const uint64_t kd = k_desc + static_cast<uint64_t>(((2u * n) & (SLOTS - 1)) * (TILE_BYTES >> 4));
+      const int t = warp - 1;
+      uint32_t q_uses = 0, s_cnt = 0, p_cnt = 0;    // half tiles so far: buffer and phase
+      // The warp stays together and one lane issues: what a product is told
+      // (descriptors: one of each kind, then steps in units of 16 bytes) is the
+      // same for all lanes.  The few instructions between two products count:
+      // a product takes 32 to 64 cycles.
+      const bool leader = elect_one();
+      const uint64_t q_desc = kdesc(smem_u32(smem + M_Q + t * TILE_BYTES), 128, 0),
+                     k_desc = kdesc(smem_u32(smem + M_RING), 128, 0), v_desc = mndesc(smem_u32(smem + M_RING), 128, 0);
+      // S_t of half j of the n-th tile
+      auto issue_s = [&](int n, int j, bool seg_ends) {
+        const uint32_t buf = s_cnt++ & 1u;
+        const uint64_t kd = k_desc + static_cast<uint64_t>(((2u * n) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * (SK * 128 >> 4));
+        const uint32_t sd = tmem + t * 128 + buf * SK;
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint64_t step = ((ks >> 2) * 128 * 128 + (ks & 3) * 32) >> 4;
-          umma_bf16(tmem + t * 128, qd + step, kd + step, ID_S, ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint64_t step = ((ks >> 2) * 128 * 128 + (ks & 3) * 32) >> 4;
+            umma_bf16(sd, q_desc + step, kd + step, ID_S, ks > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[2 * t + buf]);
+          if (seg_ends) umma_commit(&q_empty[t]);
         }
-        umma_commit(&s_full[t]);
-        if (seg_ends) umma_commit(&q_empty[t]);
+        __syncwarp();
+      };
+      // O_t += P_t V of half j of the n-th tile
+      auto issue_pv = [&](int n, int j, bool first, int steps) -> bool {
+        const uint32_t buf = p_cnt & 1u;
+        if (!W.warp(&p_full[2 * t + buf], (p_cnt >> 1) & 1u)) return false;
+        ++p_cnt;
+        tc_fence_after();
+        const uint64_t vd = v_desc + static_cast<uint64_t>(((2u * n + 1) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * 512);
+        const uint32_t od = tmem + 256 + t * 128, pd = tmem + t * 128 + buf * SK;
+        if (leader) {
+          if (steps == 4) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16_ta(od, pd + ks * 8, vd + static_cast<uint64_t>(ks * 128), ID_PV, ks > 0 ? 1u : (first ? 0u : 1u));
+          } else {
+#pragma unroll 1
+            for (int ks = 0; ks < steps; ++ks)
+              umma_bf16_ta(od, pd + ks * 8, vd + static_cast<uint64_t>(ks * 128), ID_PV, ks > 0 ? 1u : (first ? 0u : 1u));
+          }
+          umma_commit(&pv_done[2 * t + buf]);
+        }
+        __syncwarp();
         return true;
       };
-      auto wait_tile = [&](uint32_t i) { return W(&full[i & (SLOTS - 1)], (i / SLOTS) & 1u); };
-      auto ends = [&](const Cursor& x, int n) { return x.t + 1 == x.nt || n + 1 == N; };
-      bool two = rows_of(c) > 128;
-      ok = wait_tile(0) && issue_s(0, c, 0, true, ends(c, 0)) && (!two || issue_s(1, c, 0, true, ends(c, 0)));
-      if (ok) umma_commit(&empty[0]);
-      bool first = true;
-      for (int n = 0; n < N && ok; ++n) {
-        const int base = (t0 + c.t) * BK;
-        const int steps = (min(BK, c.s.kv - base) + 15) / 16;
-        const bool last = ends(c, n), more = n + 1 < N;
-        Cursor x = c;
-        if (more) advance<C, PREFIX>(B, x);
-        const bool two_next = more && rows_of(x) > 128;
-        ok = wait_tile(2u * n + 1) && (!more || wait_tile(2u * n + 2));
-        if (!ok) break;
-        const uint64_t vd = v_desc + static_cast<uint64_t>(((2u * n + 1) & (SLOTS - 1)) * (TILE_BYTES >> 4));
-        auto issue_pv = [&](int t) -> bool {
-          if (!W(&p_full[t], p_uses[t] & 1u)) return false;
-          ++p_uses[t];
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            if (ks < steps)
-              umma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, vd + static_cast<uint64_t>(ks * 128), ID_PV,
-                           (!first || ks > 0) ? 1u : 0u);
-          if (last) umma_commit(&o_full[t]);
-          return true;
-        };
-        if (!last) {
-          ok = issue_pv(0) && issue_s(0, x, n + 1, false, ends(x, n + 1));
-          if (ok && two) ok = issue_pv(1) && issue_s(1, x, n + 1, false, ends(x, n + 1));
-        } else {
-          // the next item's S waits for its rows: behind both tiles' products
-          ok = issue_pv(0) && (!two || issue_pv(1));
-          if (ok && more)
-            ok = issue_s(0, x, n + 1, true, ends(x, n + 1)) && (!two_next || issue_s(1, x, n + 1, true, ends(x, n + 1)));
+      // row tile t is done with ring entry i: when its products are, or at once
+      auto release = [&](uint32_t i, bool active) {
+        if (leader) {
+          if (active)
+            umma_commit(&empty[i & (SLOTS - 1)]);
+          else
+            mbar_arrive(&empty[i & (SLOTS - 1)]);
         }
-        if (!ok) break;
-        umma_commit(&empty[(2u * n + 1) & (SLOTS - 1)]);
-        if (more) umma_commit(&empty[(2u * n + 2) & (SLOTS - 1)]);
+        __syncwarp();
+      };
+      auto wait_tile = [&](uint32_t i) { return W.warp(&full[i & (SLOTS - 1)], (i / SLOTS) & 1u); };
+      auto halves = [](uint32_t what) { return (what & I_STEPS) > 4 ? 2 : 1; };
+      bool ok = true, first = true;
+      uint32_t cur = 0;
+      for (int n = 0; n < N && ok; ++n) {
+        if (first) {
+          // a segment begins: both halves of its first S
+          if (!(ok = wait_tile(2u * n))) break;
+          cur = info[n & 1];
+          const bool active = t == 0 || (cur & I_TWO);
+          if (active) {
+            if (!(ok = W.warp(&q_full[t], q_uses++ & 1u))) break;
+            tc_fence_after();
+            for (int j = 0; j < halves(cur); ++j) issue_s(n, j, (cur & I_LAST) && j + 1 == halves(cur));
+          }
+          release(2u * n, active);
+        }
+        const bool last = cur & I_LAST, active = t == 0 || (cur & I_TWO);
+        const int steps = cur & I_STEPS;
+        if (!(ok = wait_tile(2u * n + 1) && (last || wait_tile(2u * n + 2)))) break;
+        const uint32_t next = last ? 0 : info[(n + 1) & 1];
+        if (active) {
+          const int n_next = last ? 0 : halves(next);
+#pragma unroll 1
+          for (int j = 0; j < halves(cur); ++j) {
+            if (!(ok = issue_pv(n, j, first && j == 0, min(4, steps - 4 * j)))) break;
+            if (j < n_next) issue_s(n + 1, j, (next & I_LAST) && j + 1 == n_next);
+          }
+          if (!ok) break;
+        }
+        release(2u * n + 1, active);
+        if (!last) release(2u * n + 2, active);
         first = last;
-        c = x;
-        two = two_next;
+        cur = next;
       }
-      umma_commit(drain);  // all issued products complete before tensor memory is released
-      W.drain(drain, 0u);
+      // all issued products complete before tensor memory is released
+      if (leader) umma_commit(&drain[t]);
+      __syncwarp();
+      W.drain(&drain[t], 0u);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 3) {
     // ------------------------------------------------ query rows of each segment, row tile t
-    const int t = warp - 2, dtok = 2 / B.G, dg = 2 - dtok * B.G;
-    const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
-    uint32_t uses = 0;
-    bool fresh = true;
-    for (int n = 0; n < N; ++n) {
-      const int rows = rows_of(c) - t * 128;
-      if (fresh && rows > 0) {
-        if (!W.warp(&q_empty[t], (uses & 1u) ^ 1u)) break;
-        ++uses;
+    const int dtok = 2 / B.G, dg = 2 - dtok * B.G;
+    uint32_t uses[2] = {0, 0};
+    bool fresh = true, ok = true;
+    for (int n = 0; n < N && ok; ++n) {
+      for (int t = 0; fresh && t < 2 && rows_of(c) > t * 128; ++t) {
+        const int rows = rows_of(c) - t * 128;
+        const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
+        if (!(ok = W.warp(&q_empty[t], (uses[t]++ & 1u) ^ 1u))) break;
         // 16 lanes to a row: two rows of 256 bytes a time
         const int r0 = lane >> 4, item_row = c.rt * RT_MANY + t * 128 + r0;
         int tok = item_row / B.G, g = item_row - tok * B.G;
@@ -356,12 +410,13 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       if (n + 1 < N) advance<C, PREFIX>(B, c);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------ softmax of row tile t
     const int t = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = smem_u32(smem + M_OUT + (warp - 4) * 4096);
-    uint32_t s_uses = 0, o_uses = 0;
+    uint32_t cnt = 0;  // half tiles so far: buffer and phase
+    const uint64_t scale2 = pack2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
     bool fresh = true;
     int seg_t = 0, seg_n = 0, limit = 0;
     int at = -1;  // token * H + head of this thread's row, -1: none
@@ -394,170 +449,152 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             }
           }
         }
-        if (!W.warp(&s_full[t], s_uses & 1u)) break;
-        ++s_uses;
-        tc_fence_after();
-        // The scores are read twice, 64 columns at a time: for the maximum, then
-        // for the exponentials.  Holding all 128 spills registers, and the
-        // straight-line code for them misses the instruction cache.
-        const uint32_t ts = tl + t * 128;
-        const int base = (t0 + c.t) * BK, from = lo - base, to = limit - base;
-        const bool masked = __any_sync(0xffffffffu, from > 0 || to < BK);
-        auto hide = [&](uint32_t (&r)[32], int col) {
-          if (!masked) return;
-          const int a = from - col, b = to - col;  // columns [a, b) of these 32 are seen
-          const uint32_t below = b >= 32 ? 0xffffffffu : (b <= 0 ? 0u : (1u << b) - 1u);
-          const uint32_t seen = below & (a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : 0xffffffffu << a));
-#pragma unroll
-          for (int k = 0; k < 32; ++k) r[k] = (seen >> k) & 1u ? r[k] : __float_as_uint(-INFINITY);
-        };
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto maxima = [&](const uint32_t (&r)[32]) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 2)
-            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-        };
+        const int base0 = (t0 + c.t) * BK, keys = min(BK, c.s.kv - base0);  // V behind them may be anything
+        bool ok = true;
 #pragma unroll 1
-        for (int col = 0; col < BK; col += 64) {
+        for (int j = 0; j * SK < keys; ++j, ++cnt) {
+          const uint32_t buf = cnt & 1u;
+          if (!W.warp(&s_full[2 * t + buf], (cnt >> 1) & 1u)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ts = tl + t * 128 + buf * SK;
           uint32_t ra[32], rb[32];
-          tmem_ld32(ts + col, ra);
-          tmem_ld32(ts + col + 32, rb);
-          tmem_wait_ld2(ra, rb);
-          hide(ra, col);
-          maxima(ra);
-          hide(rb, col + 32);
-          maxima(rb);
-        }
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-        float alpha = 1.f;
-        bool rescale = false;
-        if (m == -INFINITY) {
-          m = mx;  // the first key that this row sees: O_t and l are still zero
-        } else if (mx > m + 8.f) {
-          alpha = ex2(m - mx);
-          m = mx;
-          rescale = true;
-        }
-        if (__any_sync(0xffffffffu, rescale)) {
-          // O_t holds the sum up to the tile before: S_t was issued behind it
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t o[32];
-            tmem_ld32(tl + 256 + t * 128 + k * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tl + 256 + t * 128 + k * 32, o);
+          tmem_ld32(ts, ra);
+          tmem_ld32(ts + 32, rb);
+          const int base = base0 + j * SK, from = lo - base, to = limit - base;
+          tmem_wait_ld32(ra);
+          tmem_wait_ld32(rb);
+          if (__any_sync(0xffffffffu, from > 0 || to < SK)) {
+            hide(ra, from, to);
+            hide(rb, from - 32, to - 32);
           }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            m4[k & 2] = max3(m4[k & 2], __uint_as_float(ra[k]), __uint_as_float(ra[k + 1]));
+            m4[(k & 2) + 1] = max3(m4[(k & 2) + 1], __uint_as_float(rb[k]), __uint_as_float(rb[k + 1]));
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          float alpha = 1.f;
+          bool rescale = false;
+          if (m == -INFINITY) {
+            m = mx;  // the first key that this row sees: O_t and l are still zero
+          } else if (mx > m + 8.f) {
+            alpha = ex2(m - mx);
+            m = mx;
+            rescale = true;
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            // O_t has to hold the sum up to the half tile before
+            const uint32_t was = cnt - 1;
+            if (!W.warp(&pv_done[2 * t + (was & 1u)], (was >> 1) & 1u)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < HD; k += 16) {
+              uint32_t o[16];
+              tmem_ld16(tl + 256 + t * 128 + k, o);
+              tmem_wait_ld();
+              asm volatile(""
+                           : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]),
+                             "+r"(o[7]), "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]),
+                             "+r"(o[13]), "+r"(o[14]), "+r"(o[15]));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tl + 256 + t * 128 + k, o);
+            }
+            tmem_wait_st();
+          }
+          const float neg_m = m == -INFINITY ? 0.f : -m;  // no key yet: every p is 0
+          const uint64_t neg_m2 = pack2(__float_as_uint(neg_m), __float_as_uint(neg_m));
+          uint64_t l2[4] = {0, 0, 0, 0};
+          // P (two to a cell) goes over the first half of the S it comes from
+          auto exponentials = [&](const uint32_t (&r)[32], uint32_t dst) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float e0, e1;
+              unpack2(fma2(pack2(r[2 * k], r[2 * k + 1]), scale2, neg_m2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              l2[k & 3] = add2(l2[k & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+              // rounded to bf16 for the second product; the sum is taken before
+              pk[k] = pack_bf16x2(e0, e1);
+            }
+            tmem_st16(dst, pk);
+          };
+          exponentials(ra, ts);
+          exponentials(rb, ts + 16);
           tmem_wait_st();
-        }
-        const float neg_m = m == -INFINITY ? 0.f : -m;  // no key yet: every p is 0
-        const uint64_t scale2 = pack2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-        const uint64_t neg_m2 = pack2(__float_as_uint(neg_m), __float_as_uint(neg_m));
-        uint64_t l2[4] = {0, 0, 0, 0};
-        // P (two to a cell) goes over columns of S that have been read
-        auto exponentials = [&](const uint32_t (&r)[32], int col) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float e0, e1;
-            unpack2(fma2(pack2(r[2 * k], r[2 * k + 1]), scale2, neg_m2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            l2[k & 3] = add2(l2[k & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
-            // rounded to bf16 for the second product; the sum is taken before
-            pk[k] = pack_bf16x2(e0, e1);
+          float la, lb;
+          unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), la, lb);
+          l = l * alpha + (la + lb);
+          if ((keys & 15) && keys - j * SK <= SK) {
+            // (both row tiles' warps: the products of neither wait for the other's)
+            const uint32_t i = 2u * n + 1;
+            if (!W.warp(&full[i & (SLOTS - 1)], (i / SLOTS) & 1u)) { ok = false; break; }
+            const uint32_t vs = smem_u32(ring(i));
+            const int tid = threadIdx.x & 127, bad = 16 - (keys & 15);
+            for (int k = tid; k < bad * 16; k += 128) st_shared_v4(sw_chunk(vs, 128, keys + (k >> 4), k & 15), 0, 0, 0, 0);
+            fence_proxy_async_smem();
           }
-          tmem_st16(ts + col / 2, pk);
-        };
-#pragma unroll 1
-        for (int col = 0; col < BK; col += 64) {
-          uint32_t ra[32], rb[32];
-          tmem_ld32(ts + col, ra);
-          tmem_ld32(ts + col + 32, rb);
-          tmem_wait_ld2(ra, rb);
-          hide(ra, col);
-          exponentials(ra, col);
-          hide(rb, col + 32);
-          exponentials(rb, col + 32);
+          tc_fence_before();
+          arrive_warp(&p_full[2 * t + buf]);
         }
-        tmem_wait_st();
-        float la, lb;
-        unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), la, lb);
-        l = l * alpha + (la + lb);
-        const int keys = min(BK, c.s.kv - base);  // of the sequence; V behind them may be anything
-        if (t == 0 && (keys & 15)) {
-          const uint32_t i = 2u * n + 1;
-          if (!W.warp(&full[i & (SLOTS - 1)], (i / SLOTS) & 1u)) break;
-          const uint32_t vs = smem_u32(ring(i));
-          const int tid = threadIdx.x - 128, bad = 16 - (keys & 15);
-          for (int k = tid; k < bad * 16; k += 128) st_shared_v4(sw_chunk(vs, 128, keys + (k >> 4), k & 15), 0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        arrive_warp(&p_full[t]);
+        if (!ok) break;
         if (last) {
           if (threadIdx.x == 128 && n + 1 == N && p.part.split)
             p.part.split[blockIdx.x] = split_of(B, S, c, seg_t, seg_n > 0);
           // ---- the segment's rows: to o, to their own places, or to a slot
-          if (!W.warp(&o_full[t], o_uses & 1u)) break;
-          ++o_uses;
+          const uint32_t was = cnt - 1;
+          if (!W.warp(&pv_done[2 * t + (was & 1u)], (was >> 1) & 1u)) break;
           tc_fence_after();
           const bool whole = seg_t == 0 && c.t + 1 == c.nt;
           const bool direct = whole && !PREFIX && B.shared == 0;
           const long long slot = (2ll * blockIdx.x + (seg_n ? 1 : 0)) * p.part.slot_rows + t * 128 + quarter * 32;
-          if (direct) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          // 128 bytes of each of the warp's 32 rows, staged so that eight lanes
+          // write a row's together: dst(row of the warp, row among all)
+          auto write_rows = [&](auto dst) {
+            __syncwarp();
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t o[32];
-                tmem_ld32(tl + 256 + t * 128 + k * 64 + half * 32, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                  st_shared_v4(sbuf + lane * 128 + (((4 * half + i) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-                }
-              }
-              __syncwarp();
-              // eight lanes write 128 bytes of a row, four rows at a time
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int rr = 4 * i + (lane >> 3), ch = lane & 7;
-                const uint4 v = ld_shared_v4(sbuf + rr * 128 + ((ch ^ (rr & 7)) << 4));
-                const int row = __shfl_sync(0xffffffffu, at, rr);
-                if (row >= 0) reinterpret_cast<uint4*>(p.o + static_cast<long long>(row) * HD + k * 64)[ch] = v;
-              }
-              __syncwarp();
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 4 * i + (lane >> 3), k = lane & 7;
+              const uint4 v = ld_shared_v4(sbuf + rr * 128 + ((k ^ (rr & 7)) << 4));
+              const int row = __shfl_sync(0xffffffffu, at, rr);
+              if (row >= 0) reinterpret_cast<uint4*>(dst(rr, row))[k] = v;
             }
-            if (at >= 0 && p.lse) p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
-          } else {
+            __syncwarp();
+          };
+          auto stage = [&](int k, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            st_shared_v4(sbuf + lane * 128 + ((k ^ (lane & 7)) << 4), a, b, c, d);
+          };
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              uint32_t o[32];
-              tmem_ld32(tl + 256 + t * 128 + k * 32, o);
-              tmem_wait_ld();
+          for (int col = 0; col < HD; col += 32) {
+            uint32_t o[32];
+            tmem_ld32(tl + 256 + t * 128 + col, o);
+            tmem_wait_ld32(o);
+            if (direct) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                st_shared_v4(sbuf + lane * 128 + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2],
-                             o[4 * i + 3]);
-              __syncwarp();
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int rr = 4 * i + (lane >> 3), ch = lane & 7;
-                const uint4 v = ld_shared_v4(sbuf + rr * 128 + ((ch ^ (rr & 7)) << 4));
-                const int row = __shfl_sync(0xffffffffu, at, rr);
-                float* dst = whole ? p.part.row_o + static_cast<long long>(row) * HD : p.part.slot_o + (slot + rr) * HD;
-                if (row >= 0) reinterpret_cast<uint4*>(dst + k * 32)[ch] = v;
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                stage((col & 32) / 8 + k, w[0], w[1], w[2], w[3]);
               }
-              __syncwarp();
+              if (col & 32) write_rows([&](int, int row) { return p.o + static_cast<long long>(row) * HD + col - 32; });
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) stage(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              write_rows([&](int rr, int row) {
+                return (whole ? p.part.row_o + static_cast<long long>(row) * HD : p.part.slot_o + (slot + rr) * HD) + col;
+              });
             }
-            if (at >= 0) (whole ? p.part.row_ml[at] : p.part.slot_ml[slot + lane]) = make_float2(m, l);
+          }
+          if (at >= 0) {
+            if (!direct)
+              (whole ? p.part.row_ml[at] : p.part.slot_ml[slot + lane]) = make_float2(m, l);
+            else if (p.lse)
+              p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
           }
           tc_fence_before();
         }
