@@ -556,23 +556,13 @@ struct ItemParts {
   }
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-
 // A block takes rows of one item.  SHARED: any item, blockIdx.x being its
 // number, with the parts of its own keys and of the shared ones.  Otherwise
 // the item that block blockIdx.x of the attention began and others ended.
 template <bool SHARED>
 __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__ CombineParams p) {
   __shared__ float4 s_acc[8][32];
+  __shared__ float2 s_ml[8];
   grid_dep_wait();
   grid_dep_launch();
   const Batch& B = p.b;
@@ -663,42 +653,60 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
                             I.place(P, mine ? i : i - own.n, mine ? r : r_sh, at) * HD;
         return reinterpret_cast<const float4*>(base)[lane];
       };
-      for (int i = lane; i < n; i += 32) m = fmaxf(m, ml(i).x);
-      m = warp_max(m);
-      if (m != -INFINITY) {
-        for (int i = lane; i < n; i += 32) {
-          const float2 v = ml(i);
-          l += v.y * ex2(v.x - m);
-        }
-        l = warp_sum(l);
-        // this warp's parts wp, wp + per_row, ..., 32 at a time
-        for (int j0 = wp; j0 < n; j0 += 32 * per_row) {
-          const int mine = j0 + lane * per_row;
-          const float f = mine < n ? ex2(ml(mine).x - m) : 0.f;
-          const int cnt = min(32, (n - j0 + per_row - 1) / per_row);
-#pragma unroll 8
-          for (int j = 0; j < cnt; ++j) {
-            const float w = __shfl_sync(0xffffffffu, f, j);
-            const float4 v = o(j0 + j * per_row);
-            a.x += w * v.x;
-            a.y += w * v.y;
-            a.z += w * v.z;
-            a.w += w * v.w;
+      // this warp's parts wp, wp + per_row, ..., four at a time: all loads of
+      // the four are on their way at once
+      for (int i0 = wp; i0 < n; i0 += 4 * per_row) {
+        float2 x[4];
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * per_row;
+          x[j] = make_float2(-INFINITY, 0.f);
+          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n) {
+            x[j] = ml(i);
+            v[j] = o(i);
           }
+        }
+        const float top = fmaxf(m, fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)));
+        if (top == -INFINITY) continue;
+        const float f = ex2(m - top);
+        m = top;
+        l *= f;
+        a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float w = ex2(x[j].x - top);
+          l += w * x[j].y;
+          a.x += w * v[j].x;
+          a.y += w * v[j].y;
+          a.z += w * v[j].z;
+          a.w += w * v[j].w;
         }
       }
     }
     if (per_row > 1) {
       s_acc[warp][lane] = a;
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
       __syncthreads();
-      if (wp == 0)
+      if (wp == 0) {
+        float top = m;
+        for (int w = 1; w < per_row; ++w) top = fmaxf(top, s_ml[warp + w].x);
+        const float f = top == -INFINITY ? 0.f : ex2(m - top);
+        m = top;
+        l *= f;
+        a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
         for (int w = 1; w < per_row; ++w) {
           const float4 v = s_acc[warp + w][lane];
-          a.x += v.x;
-          a.y += v.y;
-          a.z += v.z;
-          a.w += v.w;
+          const float2 y = s_ml[warp + w];
+          const float g = top == -INFINITY ? 0.f : ex2(y.x - top);
+          l += g * y.y;
+          a.x += g * v.x;
+          a.y += g * v.y;
+          a.z += g * v.z;
+          a.w += g * v.w;
         }
+      }
       __syncthreads();
     }
     if (!live || wp) continue;
@@ -874,7 +882,7 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
          (c.rows_per_pass >= 2 * item_rows || static_cast<int64_t>(a.n_tokens) * a.H < 2 * c.rows_per_pass * ctx.num_sms))
     c.rows_per_pass /= 2;
   const int passes = (item_rows + c.rows_per_pass - 1) / c.rows_per_pass;
-  const dim3 grid(P.items, passes < 16 ? passes : 16);
+  const dim3 grid(P.items, passes);
   if (ctx.before) ctx.before(ctx.user, "kv_combine", ctx.stream);
   if (P.share)
     kv::launch_dep(kv::kv_combine_kernel<true>, grid, 256, 0, ctx.stream, c);
