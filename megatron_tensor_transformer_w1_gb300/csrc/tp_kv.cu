@@ -32,10 +32,18 @@ using tc::smem_u32;
 // key heads by the angle t * inv_freq[j]:
 //   x' = (x cos - y sin) scale,  y' = (y cos + x sin) scale,
 // pairs (j, j + r/2) or, interleaved, (2j, 2j + 1), for the first r columns.
-// The angle is formed in turns in 64 bits and reduced to (-1/2, 1/2] turn
-// before it is rounded to 32 (a float product t * f loses the angle of far
-// positions), once per token and pair: all heads of the token share it.
-// Bound by memory: every element is read once and written once.
+// The angle is formed in turns, modulo one, in 64-bit fixed point: t times
+// the fraction inv_freq / 2 pi, which is found once per thread (a float
+// product t * f loses the angle of far positions, and 64-bit floating point is
+// slow here); what sincospi gets is rounded to 24 bits of half a turn.
+//
+// Bound by memory: every element is read once and written once.  A warp takes
+// 4 IT heads of a token, a lane 8 pairs of a head: its 8 angles are the same
+// for all heads, so four lanes find two each and pass them around.  The
+// elements are on their way before the token's sequence and page are looked
+// up.  IT = 2 makes that and the angles cheaper per head (12604 tokens of 48
+// heads, 310 MB: 53 us, IT = 4 60 us); IT = 1 spreads few tokens over more
+// warps.
 struct AppendParams {
   Batch b;
   const __nv_bfloat16* qkv;
@@ -51,97 +59,120 @@ struct AppendParams {
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t w) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
-
-__device__ __forceinline__ void turn_pair(uint32_t& wa, uint32_t& wb, const float2* cs) {
-  // two pairs: the low and the high halves of the two words
+// (x, y) = (low, high) halves of two words' pairs: the pairs (a.lo, b.lo), (a.hi, b.hi)
+__device__ __forceinline__ void turn_across(uint32_t& wa, uint32_t& wb, float2 c0, float2 c1) {
   const float2 a = unpack_bf16x2(wa), b = unpack_bf16x2(wb);
-  const float2 c0 = cs[0], c1 = cs[1];
   wa = pack_bf16x2(a.x * c0.x - b.x * c0.y, a.y * c1.x - b.y * c1.y);
   wb = pack_bf16x2(b.x * c0.x + a.x * c0.y, b.y * c1.x + a.y * c1.y);
+}
+// the pair within a word
+__device__ __forceinline__ void turn_within(uint32_t& w, float2 c) {
+  const float2 x = unpack_bf16x2(w);
+  w = pack_bf16x2(x.x * c.x - x.y * c.y, x.y * c.x + x.x * c.y);
 }
 
 constexpr int APPEND_THREADS = 256;
 
-__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendParams p) {
-  __shared__ float2 cs[HD / 2];
+template <int IT>
+__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ int s_err;
-  if (threadIdx.x == 0) s_err = 0;
-  grid_dep_wait();
-  grid_dep_launch();
   const Batch& B = p.b;
+  const int lane = threadIdx.x & 31, k = lane & 7, sub = lane >> 3;
   const int per = p.hq_per + 2 * p.hk_per, heads = B.H + 2 * B.Hkv;
   const int half = p.rot / 16;  // 16-byte chunks of half the rotated columns
+  const bool turns = k < half;  // lane k of a head has the pairs 8 k .. 8 k + 7
+  // two 16-byte chunks of a head: eight pairs' halves, or neighbours
+  const int ca = !p.interleaved && turns ? k : 2 * k, cb = !p.interleaved && turns ? k + half : 2 * k + 1;
+  if (threadIdx.x == 0) s_err = 0;
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  unsigned long long freq[2] = {0, 0};  // turns per position of pairs 8 k + 2 sub, + 1, in 2^-64
+  if (turns) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const double f = static_cast<double>(p.inv_freq[8 * k + 2 * sub + e]) * 0.15915494309189533577;  // 1 / (2 pi)
+      freq[e] = static_cast<unsigned long long>(__double2ll_rn((f - rint(f)) * 9223372036854775808.0)) << 1;
+    }
+  }
+  const int chunks = (heads + 4 * IT - 1) / (4 * IT);
+  const long long units = static_cast<long long>(B.n_tokens) * chunks;
+  const int warps = gridDim.x * (APPEND_THREADS / 32);
   int err = 0;
-  for (int row = blockIdx.x; row < B.n_tokens; row += gridDim.x) {
+  for (long long u = blockIdx.x * (APPEND_THREADS / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+    const int row = static_cast<int>(u / chunks), h0 = static_cast<int>(u - static_cast<long long>(row) * chunks) * 4 * IT;
+    const uint4* src = reinterpret_cast<const uint4*>(p.qkv + static_cast<long long>(row) * heads * HD);
+    uint4 a[IT], c[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int hh = h0 + 4 * i + sub;
+      if (hh < heads) {
+        a[i] = src[hh * 16 + ca];
+        c[i] = src[hh * 16 + cb];
+      }
+    }
     const int b = find_seq_warp(B.cu, B.B, row);
-    if (b >= B.B || B.cu[b] > row || B.cu[b] < 0) continue;  // no sequence's row: left as it is
-    const int pos = B.kv_len[b] - (B.cu[b + 1] - row);
+    if (b >= B.B) continue;
+    const int first = B.cu[b], end = B.cu[b + 1];
+    if (first > row || first < 0) continue;  // no sequence's row: left as it is
+    const int pos = B.kv_len[b] - (end - row);
     long long page = -1;
     if (pos >= 0 && pos < B.cap) {
       page = B.table[static_cast<long long>(b) * B.max_pages + (pos >> B.page_shift)];
       if (page >= B.n_pages) page = -1;
     }
-    if (page < 0 || B.cu[b + 1] > B.n_tokens) err = DEV_ERR_BATCH;
-    __syncthreads();  // the previous token's angles have been read
-    if (threadIdx.x < p.rot / 2) {
-      const double turns = static_cast<double>(pos) * static_cast<double>(p.inv_freq[threadIdx.x]) *
-                           0.15915494309189533577;  // 1 / (2 pi)
-      float s, c;
-      sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-      cs[threadIdx.x] = make_float2(c * p.scale, s * p.scale);
-    }
-    __syncthreads();
-    const uint4* src = reinterpret_cast<const uint4*>(p.qkv + static_cast<long long>(row) * heads * HD);
-    const int slot = pos & ((1 << B.page_shift) - 1);
-    // 8 units of two 16-byte chunks per head: the two chunks of 8 pairs
-    // (first half, second half), or two neighbours
-    for (int u = threadIdx.x; u < heads * 8; u += APPEND_THREADS) {
-      const int hh = u >> 3, k = u & 7;
-      const int t = hh / per, w = hh - t * per;
-      int ca = 2 * k, cb = 2 * k + 1;
-      const bool turned = w < p.hq_per + p.hk_per;
-      if (!p.interleaved) {
-        if (k < half) {
-          ca = k;
-          cb = k + half;
-        } else {
-          ca = 2 * k;  // 2 half + 2 (k - half): the columns past the rotated ones
-          cb = ca + 1;
-        }
-      }
-      uint4 a = src[hh * 16 + ca], c = src[hh * 16 + cb];
-      if (turned) {
-        if (p.interleaved) {
-          if (ca * 8 < p.rot) {
-            uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
-            uint32_t* wc = reinterpret_cast<uint32_t*>(&c);
+    if (page < 0 || end > B.n_tokens) err = DEV_ERR_BATCH;
+    float2 cs[8];
+    if (half) {
+      float2 mine[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = unpack_bf16x2(wa[i]), y = unpack_bf16x2(wc[i]);
-              const float2 f = cs[ca * 4 + i], g = cs[cb * 4 + i];
-              wa[i] = pack_bf16x2(x.x * f.x - x.y * f.y, x.y * f.x + x.x * f.y);
-              wc[i] = pack_bf16x2(y.x * g.x - y.y * g.y, y.y * g.x + y.x * g.y);
-            }
-          }
-        } else if (k < half) {
-          turn_pair(a.x, c.x, cs + 8 * k);
-          turn_pair(a.y, c.y, cs + 8 * k + 2);
-          turn_pair(a.z, c.z, cs + 8 * k + 4);
-          turn_pair(a.w, c.w, cs + 8 * k + 6);
+      for (int e = 0; e < 2; ++e) {
+        const int turn = static_cast<int>((static_cast<unsigned long long>(static_cast<long long>(pos)) * freq[e]) >> 32);
+        float s, co;
+        sincospif(static_cast<float>(turn) * 4.656612873077392578125e-10f, &s, &co);  // 2^-31: half turns
+        mine[e] = make_float2(co * p.scale, s * p.scale);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i].x = __shfl_sync(0xffffffffu, mine[i & 1].x, k + 8 * (i >> 1));
+        cs[i].y = __shfl_sync(0xffffffffu, mine[i & 1].y, k + 8 * (i >> 1));
+      }
+    }
+    const int slot = pos & ((1 << B.page_shift) - 1);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int hh = h0 + 4 * i + sub;
+      if (hh >= heads) continue;
+      const int t = hh / per, w = hh - t * per;
+      if (turns && w < p.hq_per + p.hk_per) {
+        if (p.interleaved) {
+          turn_within(a[i].x, cs[0]);
+          turn_within(a[i].y, cs[1]);
+          turn_within(a[i].z, cs[2]);
+          turn_within(a[i].w, cs[3]);
+          turn_within(c[i].x, cs[4]);
+          turn_within(c[i].y, cs[5]);
+          turn_within(c[i].z, cs[6]);
+          turn_within(c[i].w, cs[7]);
+        } else {
+          turn_across(a[i].x, c[i].x, cs[0], cs[1]);
+          turn_across(a[i].y, c[i].y, cs[2], cs[3]);
+          turn_across(a[i].z, c[i].z, cs[4], cs[5]);
+          turn_across(a[i].w, c[i].w, cs[6], cs[7]);
         }
       }
       __nv_bfloat16* dst;
       if (w < p.hq_per) {
         dst = p.q + (static_cast<long long>(row) * B.H + t * p.hq_per + w) * HD;
-        if (pos < 0) a = c = make_uint4(0u, 0u, 0u, 0u);
+        if (pos < 0) a[i] = c[i] = make_uint4(0u, 0u, 0u, 0u);
       } else {
         if (page < 0) continue;
         const bool is_k = w < p.hq_per + p.hk_per;
         const int h = t * p.hk_per + (is_k ? w - p.hq_per : w - p.hq_per - p.hk_per);
         dst = (is_k ? B.k : B.v) + ((((page * B.Hkv + h) << B.page_shift) + slot) * HD);
       }
-      reinterpret_cast<uint4*>(dst)[ca] = a;
-      reinterpret_cast<uint4*>(dst)[cb] = c;
+      reinterpret_cast<uint4*>(dst)[ca] = a[i];
+      reinterpret_cast<uint4*>(dst)[cb] = c[i];
     }
   }
   if (err) atomicOr(&s_err, err);
@@ -234,7 +265,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rg = warp / F::WK, kg = warp % F::WK;
   if (tid == 0) s_err = 0;
-  grid_dep_wait();
+  if (!p.beside) grid_dep_wait();
   grid_dep_launch();
   int err = 0;
   Cursor c;
@@ -244,6 +275,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   if (n_tiles == 0) {
     if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, 0);
     if (tid == 0 && p.part.split) p.part.split[blockIdx.x] = Split{};
+    if (p.beside) grid_dep_wait();
     if (err) atomicOr(&s_err, err);
     __syncthreads();
     if (tid == 0) p.status[blockIdx.x] = s_err;
@@ -515,6 +547,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   }
   cp_async_wait<0>();
   if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, 0);
+  if (p.beside) grid_dep_wait();
   if (err) atomicOr(&s_err, err);
   __syncthreads();
   if (tid == 0) p.status[blockIdx.x] = s_err;
@@ -782,9 +815,18 @@ int launch_kv_append(const KvSpec& a, const KvRotation& r, const void* qkv, void
   p.hk_per = a.Hkv / a.T_p;
   p.header = header;
   p.alone = alone;
-  const int most = 8 * ctx.num_sms < kKvStatusWords ? 8 * ctx.num_sms : kKvStatusWords;
+  // 8 heads to a warp where that still gives every SM 32 warps
+  const int heads = a.H + 2 * a.Hkv, warps = kv::APPEND_THREADS / 32;
+  const bool wide = static_cast<int64_t>(a.n_tokens) * ((heads + 7) / 8) >= 32 * ctx.num_sms;
+  const int64_t units = static_cast<int64_t>(a.n_tokens) * (wide ? (heads + 7) / 8 : (heads + 3) / 4);
+  const int64_t most = 8 * ctx.num_sms < kKvStatusWords ? 8 * ctx.num_sms : kKvStatusWords;
+  const int64_t blocks = (units + warps - 1) / warps;
+  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
   if (ctx.before) ctx.before(ctx.user, "kv_append", ctx.stream);
-  kv::launch_dep(kv::kv_append_kernel, dim3(a.n_tokens < most ? a.n_tokens : most), kv::APPEND_THREADS, 0, ctx.stream, p);
+  if (wide)
+    kv::launch_dep(kv::kv_append_kernel<2>, grid, kv::APPEND_THREADS, 0, ctx.stream, p);
+  else
+    kv::launch_dep(kv::kv_append_kernel<1>, grid, kv::APPEND_THREADS, 0, ctx.stream, p);
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
   return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
@@ -865,6 +907,7 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
     if (rc) return rc;
   }
   p.part = c.own = P.own;
+  p.beside = P.share;
   p.status = status + c.status_words;
   c.status_words += P.own.grid;
   rc = P.own.rt ? kv::launch_many(p, false, ctx, "kv_attend_many") : kv::launch_few<false>(p, ctx, "kv_attend_few");

@@ -336,6 +336,11 @@ struct AttendParams {
   Parts part;
   float scale_log2;
   int* status;             // a word per block
+  // The kernel before it on the stream is the shared keys' of the same call:
+  // nothing that it writes is read here, and it lets its successor start only
+  // when the call's inputs are there.  This kernel starts without waiting for
+  // it, and waits before its blocks end.
+  int beside;
   unsigned long long timeout_ns;
 };
 

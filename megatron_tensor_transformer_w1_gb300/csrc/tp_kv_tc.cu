@@ -21,11 +21,10 @@
 //    over the S_t it came from.  Products run in the order of issue, so the
 //    S_t that is issued behind O_t += P_t V into the same buffer finds P_t
 //    read.  Two warps, because one spends a third of a step between products;
-//  * warp 3: gathers the query rows of the next item into the swizzled layout
-//    of the products;
 //  * warps 4-7 and 8-11: the softmax of row tiles 0 and 1, a row per thread,
 //    with a maximum that moves only when it grew by more than 2^8, so that
-//    O_t is rarely rescaled; they write the rows out at the end of a segment.
+//    O_t is rarely rescaled; they also gather a segment's query rows and write
+//    its results.
 // S_t comes in halves of 64 keys into two buffers, so that the softmax of one
 // half finds the next one's scores done: with one buffer of 128 keys a row
 // tile waits for its two products in every step.
@@ -161,7 +160,6 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   uint64_t* full = bar;         // [SLOTS] a K or V tile has landed
   uint64_t* empty = bar + 4;    // [SLOTS] its products are done
   uint64_t* q_full = bar + 8;   // [2]
-  uint64_t* q_empty = bar + 10; // [2] the item's last S_t is done
   uint64_t* s_full = bar + 12;  // [2][2] S_t of a half tile is done
   uint64_t* p_full = bar + 16;  // [2][2] P_t written (a warp each)
   uint64_t* pv_done = bar + 20; // [2][2] O_t has its product
@@ -179,8 +177,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       mbar_init(&empty[i], 2);  // both row tiles
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&q_full[t], 32);
-      mbar_init(&q_empty[t], 1);
+      mbar_init(&q_full[t], 4);
       mbar_init(&drain[t], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -197,7 +194,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     prefetch_tmap(&tv);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
-  grid_dep_wait();
+  if (!p.beside) grid_dep_wait();
   grid_dep_launch();
   if (threadIdx.x == 0) {
     *status = 0;
@@ -286,7 +283,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const uint64_t q_desc = kdesc(smem_u32(smem + M_Q + t * TILE_BYTES), 128, 0),
                      k_desc = kdesc(smem_u32(smem + M_RING), 128, 0), v_desc = mndesc(smem_u32(smem + M_RING), 128, 0);
       // S_t of half j of the n-th tile
-      auto issue_s = [&](int n, int j, bool seg_ends) {
+      auto issue_s = [&](int n, int j) {
         const uint32_t buf = s_cnt++ & 1u;
         const uint64_t kd = k_desc + static_cast<uint64_t>(((2u * n) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * (SK * 128 >> 4));
         const uint32_t sd = tmem + t * 128 + buf * SK;
@@ -297,7 +294,6 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             umma_bf16(sd, q_desc + step, kd + step, ID_S, ks > 0 ? 1u : 0u);
           }
           umma_commit(&s_full[2 * t + buf]);
-          if (seg_ends) umma_commit(&q_empty[t]);
         }
         __syncwarp();
       };
@@ -347,7 +343,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           if (active) {
             if (!(ok = W.warp(&q_full[t], q_uses++ & 1u))) break;
             tc_fence_after();
-            for (int j = 0; j < halves(cur); ++j) issue_s(n, j, (cur & I_LAST) && j + 1 == halves(cur));
+            for (int j = 0; j < halves(cur); ++j) issue_s(n, j);
           }
           release(2u * n, active);
         }
@@ -360,7 +356,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
 #pragma unroll 1
           for (int j = 0; j < halves(cur); ++j) {
             if (!(ok = issue_pv(n, j, first && j == 0, min(4, steps - 4 * j)))) break;
-            if (j < n_next) issue_s(n + 1, j, (next & I_LAST) && j + 1 == n_next);
+            if (j < n_next) issue_s(n + 1, j);
           }
           if (!ok) break;
         }
@@ -375,47 +371,46 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       W.drain(&drain[t], 0u);
     }
     __syncwarp();
-  } else if (warp == 3) {
-    // ------------------------------------------------ query rows of each segment, row tile t
-    const int dtok = 2 / B.G, dg = 2 - dtok * B.G;
-    uint32_t uses[2] = {0, 0};
-    bool fresh = true, ok = true;
-    for (int n = 0; n < N && ok; ++n) {
-      for (int t = 0; fresh && t < 2 && rows_of(c) > t * 128; ++t) {
-        const int rows = rows_of(c) - t * 128;
-        const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
-        if (!(ok = W.warp(&q_empty[t], (uses[t]++ & 1u) ^ 1u))) break;
-        // 16 lanes to a row: two rows of 256 bytes a time
-        const int r0 = lane >> 4, item_row = c.rt * RT_MANY + t * 128 + r0;
-        int tok = item_row / B.G, g = item_row - tok * B.G;
-        const __nv_bfloat16* src =
-            p.q + (static_cast<long long>(c.s.q0) * B.H + static_cast<long long>(c.h) * B.G) * HD + (lane & 15) * 8;
-#pragma unroll 8
-        for (int i = 0; i < 64; ++i) {
-          const bool valid = r0 + 2 * i < rows;
-          cp_async16z(sw_chunk(qs, 128, r0 + 2 * i, lane & 15),
-                      valid ? src + (static_cast<long long>(tok) * B.H + g) * HD : src, valid);
-          tok += dtok;
-          g += dg;
-          if (g >= B.G) {
-            g -= B.G;
-            ++tok;
-          }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[t]);
-      }
-      fresh = c.t + 1 == c.nt;
-      if (n + 1 < N) advance<C, PREFIX>(B, c);
-    }
-    __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------ softmax of row tile t
     const int t = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = smem_u32(smem + M_OUT + (warp - 4) * 4096);
     uint32_t cnt = 0;  // half tiles so far: buffer and phase
+    // The query rows of a segment, into the swizzled layout of the products:
+    // on their way while the segment before is written out.  (Its last S_t is
+    // done, so the buffer is free.)  16 lanes to a row, two rows of 256 bytes
+    // to a warp's copy.
+    const int dtok = 2 / B.G, dg = 2 - dtok * B.G;
+    auto fetch_q = [&](const Cursor& x) {
+      const int rows = rows_of(x) - t * 128, r0 = quarter * 32 + (lane >> 4);
+      const int item_row = x.rt * RT_MANY + t * 128 + r0;
+      int tok = item_row / B.G, g = item_row - tok * B.G;
+      const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
+      const __nv_bfloat16* src =
+          p.q + (static_cast<long long>(x.s.q0) * B.H + static_cast<long long>(x.h) * B.G) * HD + (lane & 15) * 8;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const bool valid = r0 + 2 * i < rows;
+        cp_async16z(sw_chunk(qs, 128, r0 + 2 * i, lane & 15),
+                    valid ? src + (static_cast<long long>(tok) * B.H + g) * HD : src, valid);
+        tok += dtok;
+        g += dg;
+        if (g >= B.G) {
+          g -= B.G;
+          ++tok;
+        }
+      }
+    };
+    auto publish_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      arrive_warp(&q_full[t]);
+    };
+    if (N > 0 && rows_of(c) > t * 128) {
+      fetch_q(c);
+      publish_q();
+    }
     const uint64_t scale2 = pack2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
     bool fresh = true;
     int seg_t = 0, seg_n = 0, limit = 0;
@@ -424,6 +419,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     for (int n = 0; n < N; ++n) {
       const int rows = rows_of(c);
       const bool last = c.t + 1 == c.nt || n + 1 == N;
+      Cursor next = c;
+      if (n + 1 < N) advance<C, PREFIX>(B, next);
+      const bool fetch = last && n + 1 < N && rows_of(next) > t * 128;
       if (rows > t * 128) {
         if (fresh) {
           seg_t = c.t;
@@ -543,10 +541,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         if (last) {
           if (threadIdx.x == 128 && n + 1 == N && p.part.split)
             p.part.split[blockIdx.x] = split_of(B, S, c, seg_t, seg_n > 0);
+          if (fetch) fetch_q(next);
           // ---- the segment's rows: to o, to their own places, or to a slot
           const uint32_t was = cnt - 1;
           if (!W.warp(&pv_done[2 * t + (was & 1u)], (was >> 1) & 1u)) break;
           tc_fence_after();
+          if (fetch) publish_q();  // the next segment's S_t may start
           const bool whole = seg_t == 0 && c.t + 1 == c.nt;
           const bool direct = whole && !PREFIX && B.shared == 0;
           const long long slot = (2ll * blockIdx.x + (seg_n ? 1 : 0)) * p.part.slot_rows + t * 128 + quarter * 32;
@@ -598,14 +598,19 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           }
           tc_fence_before();
         }
+      } else if (fetch) {
+        fetch_q(next);
+        publish_q();
       }
       fresh = last;
-      if (n + 1 < N) advance<C, PREFIX>(B, c);
+      c = next;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   }
 
   if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, RT_MANY);
+  if (p.beside) grid_dep_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -13,7 +13,7 @@ in libtpffn.so.
 
 A call takes its workspace from PyTorch's allocator on the current stream, so
 calls on different streams, and graphs that were captured apart, do not share
-one.
+one (an append needs only status words, which the cache keeps).
 """
 from __future__ import annotations
 
@@ -45,6 +45,7 @@ class KVBatch:
         self.device = kv_len.device
         self.abi = abi.KvBatch(self.n_seqs, n_tokens, max_new, page_table.shape[1], cu_tokens.data_ptr(),
                                kv_len.data_ptr(), page_table.data_ptr())
+        self._bytes = {}  # workspace sizes of the calls made with this batch
 
 
 class PagedKVCache:
@@ -57,10 +58,12 @@ class PagedKVCache:
     def __init__(self, attn, n_pages, page_size, k=None, v=None, inv_freq=None, interleaved=False, rotary_scale=1.0):
         shape = (int(n_pages), attn.Hkv, int(page_size), attn.hd)
         self.attn, self.n_pages, self.page_size = attn, shape[0], shape[2]
+        self._width = attn.info["qkv_width"]
         self.device = attn.device if attn.device.index is not None else torch.device(
             attn.device.type, torch.cuda.current_device())
         if n_pages < 1 or page_size < 8 or page_size > 1024 or page_size & (page_size - 1):
             raise ValueError("n_pages is at least 1, page_size a power of two from 8 to 1024")
+        self._index = self.device.index
         pages = []
         for name, t in (("k", k), ("v", v)):
             if t is None:
@@ -77,27 +80,38 @@ class PagedKVCache:
             self._check("inv_freq", inv_freq, torch.float32, inv_freq.shape)
             self._rot = abi.KvRotation(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)),
                                        float(rotary_scale))
+        self._status = torch.empty(abi.tp_attn_kv_workspace_bytes(attn.plan, abi.KvBatch(), self.page_size, 0,
+                                                                  abi.TP_KV_APPEND),
+                                   dtype=torch.uint8, device=self.device)
         self._last = None  # workspace of the last call, for last_device_error
 
     def _check(self, name, t, dtype, shape):
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device} is "
                              f"needed, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
-    def _out(self, name, t, dtype, shape):
+    def _out(self, name, t, shape):
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        self._check(name, t, dtype, shape)
+            return torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        self._check(name, t, torch.bfloat16, shape)
         return t
 
-    def _call(self, batch, shared_len, call, flags):
-        """Workspace and stream of one call."""
+    def _workspace(self, batch, shared_len, call, flags):
+        key = (call, shared_len, flags, self.attn.plan, self.page_size)
+        need = batch._bytes.get(key)
+        if need is None:
+            need = abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call, flags)
+            batch._bytes[key] = need
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+
+    def _run(self, batch, call):
+        """call(stream) with the cache's device current."""
         if batch.device != self.device:
             raise ValueError(f"the batch lies on {batch.device}, the cache on {self.device}")
-        need = abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call, flags)
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
-        self._last = ws if batch.n_tokens and batch.n_seqs else None
-        return ws, torch.cuda.current_stream(self.device)
+        if torch._C._cuda_getDevice() == self._index:
+            return call(torch._C._cuda_getCurrentRawStream(self._index))
+        with torch.cuda.device(self.device):
+            return call(torch._C._cuda_getCurrentRawStream(self._index))
 
     def batch(self, cu_tokens, kv_len, page_table, n_tokens, max_new):
         return KVBatch(cu_tokens, kv_len, page_table, n_tokens, max_new)
@@ -105,37 +119,48 @@ class PagedKVCache:
     def append(self, qkv, batch, q=None, flags=0):
         """Stores the new tokens' keys (rotated) and values; returns the rotated
         queries [n_tokens, H * 128] (in `q` if given)."""
+        return self._run(batch, lambda st: self._append(qkv, batch, q, flags, st))
+
+    def _append(self, qkv, batch, q, flags, st):
         a, n = self.attn, batch.n_tokens
-        with torch.cuda.device(self.device):
-            self._check("qkv", qkv, torch.bfloat16, (n, a.info["qkv_width"]))
-            q = self._out("q", q, torch.bfloat16, (n, a.H * a.hd))
-            ws, st = self._call(batch, 0, abi.TP_KV_APPEND, flags)
-            abi.check(abi.tp_attn_kv_append(a.plan, self._abi, batch.abi, self._rot, qkv, q, ws, ws.numel(), flags,
-                                            st), "tp_attn_kv_append")
+        self._check("qkv", qkv, torch.bfloat16, (n, self._width))
+        q = self._out("q", q, (n, a.H * a.hd))
+        rc = abi.tp_attn_kv_append(a.plan, self._abi, batch.abi, self._rot, qkv, q, self._status,
+                                   self._status.numel(), flags, st)
+        abi.check(rc, "tp_attn_kv_append")
+        self._last = self._status if n and batch.n_seqs else None
         return q
 
     def attend(self, q, batch, shared_len=0, lse=False, out=None, flags=0):
         """Attention of q [n_tokens, H * 128] over the cache: o, or (o, lse) with
         the rows' log2-sum-exp [n_tokens, H] if `lse`."""
+        return self._run(batch, lambda st: self._attend(q, batch, shared_len, lse, out, flags, st))
+
+    def _attend(self, q, batch, shared_len, lse, out, flags, st):
         a, n = self.attn, batch.n_tokens
-        with torch.cuda.device(self.device):
-            self._check("q", q, torch.bfloat16, (n, a.H * a.hd))
-            o = self._out("out", out, torch.bfloat16, (n, a.H * a.hd))
-            rows = torch.empty(n, a.H, dtype=torch.float32, device=self.device) if lse else None
-            ws, st = self._call(batch, shared_len, abi.TP_KV_ATTEND, flags)
-            abi.check(abi.tp_attn_paged_fwd(a.plan, self._abi, batch.abi, shared_len, q, o, rows, ws, ws.numel(),
-                                            flags, st), "tp_attn_paged_fwd")
+        shape = (n, a.H * a.hd)
+        self._check("q", q, torch.bfloat16, shape)
+        o = self._out("out", out, shape)
+        rows = torch.empty((n, a.H), dtype=torch.float32, device=self.device) if lse else None
+        ws = self._workspace(batch, shared_len, abi.TP_KV_ATTEND, 0)
+        rc = abi.tp_attn_paged_fwd(a.plan, self._abi, batch.abi, shared_len, q, o, rows, ws, ws.numel(), flags, st)
+        abi.check(rc, "tp_attn_paged_fwd")
+        self._last = ws if n and batch.n_seqs else None
         return (o, rows) if lse else o
 
     def decode(self, x, batch, wqkv, wo, shared_len=0, out=None, flags=0):
         """The sublayer's serving pass, y [n_tokens, d] (TensorParallelAttention.decode)."""
+        return self._run(batch, lambda st: self._decode(x, batch, wqkv, wo, shared_len, out, flags, st))
+
+    def _decode(self, x, batch, wqkv, wo, shared_len, out, flags, st):
         a, n = self.attn, batch.n_tokens
-        with torch.cuda.device(self.device):
-            self._check("x", x, torch.bfloat16, (n, a.d))
-            y = self._out("out", out, torch.bfloat16, (n, a.d))
-            ws, st = self._call(batch, shared_len, abi.TP_KV_DECODE, flags)
-            abi.check(abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
-                                             ws.numel(), flags, st), "tp_attn_decode_fwd")
+        self._check("x", x, torch.bfloat16, (n, a.d))
+        y = self._out("out", out, (n, a.d))
+        ws = self._workspace(batch, shared_len, abi.TP_KV_DECODE, flags)
+        rc = abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
+                                    ws.numel(), flags, st)
+        abi.check(rc, "tp_attn_decode_fwd")
+        self._last = ws if n and batch.n_seqs else None
         return y
 
     def last_device_error(self):

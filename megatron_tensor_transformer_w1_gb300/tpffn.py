@@ -349,9 +349,7 @@ def tp_attn_last_launch_count(plan):
 
 
 # ------------------------------------------------------------ key/value cache
-def _ref(s):
-    """The address of a KvCache, KvBatch or KvRotation (or None)."""
-    return None if s is None else ctypes.addressof(s)
+_ref = lambda s: None if s is None else ctypes.addressof(s)  # of a KvCache, KvBatch or KvRotation
 
 
 def tp_attn_kv_workspace_bytes(plan, batch, page_size, shared_len, call, flags=0):
