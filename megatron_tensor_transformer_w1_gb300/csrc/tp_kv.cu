@@ -211,7 +211,7 @@ struct Few {
   static constexpr int WK = 4 / WR;           // key groups
   static constexpr int ROWS = 16 * WR;
   static constexpr int NB = WR;               // 16-key blocks of a warp per tile
-  static constexpr int STAGES = WR == 4 ? 2 : 3;
+  static constexpr int STAGES = WR == 1 ? 3 : 2;  // two blocks per SM
   static constexpr int KV_BYTES = KT * HD * 2;
   static constexpr int Q_BYTES = ROWS * HD * 2;
   static constexpr int STAGE = 2 * KV_BYTES + Q_BYTES;
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     __syncthreads();
     const bool whole = seg_t == 0 && x.t + 1 == x.nt;
     const bool direct = whole && !PREFIX && B.shared == 0;
-    const long long slot = (2ll * blockIdx.x + (seg_i ? 1 : 0)) * p.part.slot_rows;
+    const long long slot = 2ll * blockIdx.x + (seg_i ? 1 : 0);
 #pragma unroll
     for (int a = 0; a < WR; ++a) {
       const int r16 = tid >> 3, r = a * 16 + r16;
@@ -512,7 +512,6 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
         }
         const int tok = x.s.q0 + r / B.G, head = x.h * B.G + r % B.G;
         const long long row = static_cast<long long>(tok) * B.H + head;
-        float* part_o = whole ? p.part.row_o + row * HD : p.part.slot_o + (slot + r) * HD;
         const float inv = lr > 0.f ? 1.f / lr : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -533,12 +532,13 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
             w.y = pack_bf16x2(v.z * inv, v.w * inv);
             *reinterpret_cast<uint2*>(p.o + row * HD + col) = w;
           } else {
-            *reinterpret_cast<float4*>(part_o + col) = v;
+            float* dst = whole ? p.part.row_o + row * HD + col : p.part.slot_o + slot_chunk(p.part, slot, r, col >> 2);
+            *reinterpret_cast<float4*>(dst) = v;
           }
         }
         if ((tid & 7) == 0) {
           if (!direct)
-            (whole ? p.part.row_ml[row] : p.part.slot_ml[slot + r]) = make_float2(mr, lr);
+            (whole ? p.part.row_ml[row] : p.part.slot_ml[slot * p.part.slot_rows + r]) = make_float2(mr, lr);
           else if (p.lse)
             p.lse[row] = lr > 0.f ? mr + log2f(lr) : -INFINITY;
         }
@@ -558,15 +558,15 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
 // unnormalised output of part i, m = max m_i, l = sum l_i 2^(m_i - m),
 // o = sum O_i 2^(m_i - m) / l, always in the order of the parts, so that a
 // result does not change from run to run.  A row without any key gets zeros.
-// Bound by latency: the parts lie in L2.  Several warps share a row where
-// there are few rows in all, so that the many parts of a long sequence are
-// read at once.
+// Bound by latency: the parts lie in L2.  A warp takes a row, a lane
+// four columns; several warps share a row where there are few rows in all, so
+// that the many parts of a long sequence are read at once.
 struct CombineParams {
   Batch b;
   Parts own, shared;
   __nv_bfloat16* o;
   float* lse;
-  int rows_per_pass;     // of a block's eight warps: 1, 2, 4 or 8
+  int rows_per_pass;     // that a block's eight warps take: 1, 2, 4 or 8
   int* header;           // see kKvHeaderBytes
   int alone, status_words;
 };
@@ -583,11 +583,22 @@ struct ItemParts {
     n = static_cast<int>(block_of_tile(start + nt - 1, total, C) - c0) + 1;
     second = start != first_tile(c0, total, C);
   }
-  // the place of part i of a row: r within the item's slots, `at` among all rows
-  __device__ __forceinline__ long long place(const Parts& P, int i, int r, long long at) const {
-    return n == 1 ? at : (2 * (c0 + i) + (i == 0 ? second : 0)) * P.slot_rows + r;
-  }
+  // the slot of part i
+  __device__ __forceinline__ long long slot(int i) const { return 2 * (c0 + i) + (i == 0 ? second : 0); }
 };
+
+__device__ __forceinline__ void scale4(float4& a, float f) {
+  a.x *= f;
+  a.y *= f;
+  a.z *= f;
+  a.w *= f;
+}
+__device__ __forceinline__ void add4(float4& a, float f, const float4& v) {
+  a.x += f * v.x;
+  a.y += f * v.y;
+  a.z += f * v.z;
+  a.w += f * v.w;
+}
 
 // A block takes rows of one item.  SHARED: any item, blockIdx.x being its
 // number, with the parts of its own keys and of the shared ones.  Otherwise
@@ -652,15 +663,14 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     own.c0 = blockIdx.x;
     own.second = x.second;
   }
-  const int per_row = 8 / p.rows_per_pass;  // warps
-  const int wr = warp / per_row, wp = warp - wr * per_row;
+  const int share = 8 / p.rows_per_pass;  // warps to a row
+  const int wr = warp / share, wp = warp - wr * share;
   for (int row0 = blockIdx.y * p.rows_per_pass; row0 < rows; row0 += gridDim.y * p.rows_per_pass) {
     const int r = row0 + wr;
-    const bool live = r < rows;
     float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     long long at = 0;
-    if (live) {
+    if (r < rows) {
       const int item_row = rt * p.own.rt + r, tok = q0 + item_row / B.G, g = item_row % B.G;
       at = static_cast<long long>(tok) * B.H + h * B.G + g;
       int r_sh = 0;
@@ -670,35 +680,29 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         sh.set(p.shared, (h * n_rt_sh + srt) * nt_sh, nt_sh, nt_sh * n_rt_sh * B.Hkv);
       }
       const int n = own.n + sh.n;
-      auto ml_of = [&](int i) {
-        return i < own.n ? p.own.slot_ml[own.place(p.own, i, r, 0)]
-                         : p.shared.slot_ml[sh.place(p.shared, i - own.n, r_sh, 0)];
-      };
-      auto ml = [&](int i) {
-        if (SHARED && (i < own.n ? own.n : sh.n) == 1) return (i < own.n ? p.own : p.shared).row_ml[at];
-        return ml_of(i);
-      };
-      auto o = [&](int i) {
-        const bool mine = !SHARED || i < own.n;
-        const Parts& P = mine ? p.own : p.shared;
-        const ItemParts& I = mine ? own : sh;
-        const float* base = (SHARED && I.n == 1 ? P.row_o : P.slot_o) +
-                            I.place(P, mine ? i : i - own.n, mine ? r : r_sh, at) * HD;
-        return reinterpret_cast<const float4*>(base)[lane];
-      };
-      // this warp's parts wp, wp + per_row, ..., four at a time: all loads of
-      // the four are on their way at once
-      for (int i0 = wp; i0 < n; i0 += 4 * per_row) {
+      // this warp's parts wp, wp + share, ..., four at a time: all loads of the
+      // four are on their way at once
+      for (int i0 = wp; i0 < n; i0 += 4 * share) {
         float2 x[4];
         float4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int i = i0 + j * per_row;
+          const int i = i0 + j * share;
           x[j] = make_float2(-INFINITY, 0.f);
           v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (i < n) {
-            x[j] = ml(i);
-            v[j] = o(i);
+            const bool mine = !SHARED || i < own.n;
+            const Parts& P = mine ? p.own : p.shared;
+            const ItemParts& I = mine ? own : sh;
+            const int row = mine ? r : r_sh;
+            if (SHARED && I.n == 1) {
+              x[j] = P.row_ml[at];
+              v[j] = reinterpret_cast<const float4*>(P.row_o + at * HD)[lane];
+            } else {
+              const long long slot = I.slot(mine ? i : i - own.n);
+              x[j] = P.slot_ml[slot * P.slot_rows + row];
+              v[j] = *reinterpret_cast<const float4*>(P.slot_o + slot_chunk(P, slot, row, lane));
+            }
           }
         }
         const float top = fmaxf(m, fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)));
@@ -706,48 +710,39 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         const float f = ex2(m - top);
         m = top;
         l *= f;
-        a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+        scale4(a, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float w = ex2(x[j].x - top);
           l += w * x[j].y;
-          a.x += w * v[j].x;
-          a.y += w * v[j].y;
-          a.z += w * v[j].z;
-          a.w += w * v[j].w;
+          add4(a, w, v[j]);
         }
       }
     }
-    if (per_row > 1) {
+    if (share > 1) {
       s_acc[warp][lane] = a;
       if (lane == 0) s_ml[warp] = make_float2(m, l);
       __syncthreads();
       if (wp == 0) {
         float top = m;
-        for (int w = 1; w < per_row; ++w) top = fmaxf(top, s_ml[warp + w].x);
+        for (int w = 1; w < share; ++w) top = fmaxf(top, s_ml[warp + w].x);
         const float f = top == -INFINITY ? 0.f : ex2(m - top);
         m = top;
         l *= f;
-        a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
-        for (int w = 1; w < per_row; ++w) {
-          const float4 v = s_acc[warp + w][lane];
+        scale4(a, f);
+        for (int w = 1; w < share; ++w) {
           const float2 y = s_ml[warp + w];
           const float g = top == -INFINITY ? 0.f : ex2(y.x - top);
           l += g * y.y;
-          a.x += g * v.x;
-          a.y += g * v.y;
-          a.z += g * v.z;
-          a.w += g * v.w;
+          add4(a, g, s_acc[warp + w][lane]);
         }
       }
       __syncthreads();
     }
-    if (!live || wp) continue;
+    if (r >= rows || wp) continue;
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint2 w;
-    w.x = pack_bf16x2(a.x * inv, a.y * inv);
-    w.y = pack_bf16x2(a.z * inv, a.w * inv);
-    reinterpret_cast<uint2*>(p.o + at * HD)[lane] = w;
+    reinterpret_cast<uint2*>(p.o + at * HD)[lane] =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     if (p.lse && lane == 0) p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
   }
 }
@@ -790,8 +785,7 @@ int launch_few_inst(const AttendParams& p, LaunchCtx& ctx, const char* name) {
 template <bool PREFIX>
 int launch_few(const AttendParams& p, LaunchCtx& ctx, const char* name) {
   if (p.part.slot_rows <= 16) return launch_few_inst<1, PREFIX>(p, ctx, name);
-  if (p.part.slot_rows <= 32) return launch_few_inst<2, PREFIX>(p, ctx, name);
-  return launch_few_inst<4, PREFIX>(p, ctx, name);
+  return launch_few_inst<2, PREFIX>(p, ctx, name);
 }
 
 }  // namespace kv
@@ -836,7 +830,19 @@ namespace {
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // How a call's attention is launched, and its scratch.
-constexpr int kFewRows = 64;  // at most so many rows to a key/value head: the few-rows kernel
+// At most so many rows to a key/value head: the few-rows kernel.  32 sequences
+// of 4000 keys (8 heads, 531 MB): 8 rows 88 us, 32 rows 103 us against 106 us
+// of the many-rows kernel, 64 rows 140 against 107; 4 sequences of 300 keys,
+// where starting the kernel counts: 64 rows 17 against 21.
+constexpr int kFewRows = 32;
+// At most so many rows to a key/value head, on average over the sequences, for
+// the shared keys to be taken together.
+constexpr int kShareRows = 64;
+// At least so many bytes of shared keys and values that would be read again.
+// Single tokens, 8 key heads, 300 own keys each, together / each on its own: 64
+// sequences behind 1024 keys (264 MB saved) 44 / 55 us, 8 behind 4096 (117 MB)
+// 25 / 30 us, 64 behind 256 (66 MB) 37 / 30 us, 4 behind 4096 (50 MB) 25 / 20 us.
+constexpr double kShareBytes = 96 << 20;
 struct AttendPlan {
   bool share = false;
   kv::Parts own, shared;      // the pointers as offsets from the scratch's start
@@ -869,10 +875,12 @@ AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
       p.row_ml = reinterpret_cast<float2*>(take(rows * 8));
     }
   };
-  // One sequence shares with nobody; and where the sequences bring many rows
-  // each, their products bound the time, not the reads of the shared keys, and
-  // the parts to be joined would only cost.
-  P.share = a.shared_len > 0 && a.n_seqs > 1 && a.n_tokens * G <= static_cast<int64_t>(kFewRows) * a.n_seqs;
+  // Where the sequences bring many rows each, their products bound the time,
+  // not the reads of the shared keys.
+  // Taking the shared keys together pays where it saves enough reads: it costs a
+  // kernel more and the join, some 10 us.
+  const double saved = (a.n_seqs - 1.0) * a.shared_len * a.Hkv * (kv::HD * 4);
+  P.share = saved >= kShareBytes && a.n_tokens * G <= static_cast<int64_t>(kShareRows) * a.n_seqs;
   part(P.own, a.max_new * G, static_cast<size_t>(a.n_seqs) + 1);
   if (P.share) part(P.shared, a.n_tokens * G, 2);
   const int64_t units = P.own.rt ? a.n_tokens * G / kv::RT_MANY + a.n_seqs : a.n_seqs;
@@ -918,14 +926,13 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
   c.header = header;
   c.alone = alone;
   // All eight warps of a block at work, and few rows on more blocks than one:
-  // at most two blocks of 256 threads per SM before rows share a pass.
-  const int item_rows = P.own.slot_rows;
+  // at most two blocks of 256 threads per SM before a warp has a row to itself.
+  const int rows = P.own.slot_rows;
+  const int64_t all = static_cast<int64_t>(a.n_tokens) * a.H;
   c.rows_per_pass = 8;
-  while (c.rows_per_pass > 1 &&
-         (c.rows_per_pass >= 2 * item_rows || static_cast<int64_t>(a.n_tokens) * a.H < 2 * c.rows_per_pass * ctx.num_sms))
+  while (c.rows_per_pass > 1 && (c.rows_per_pass >= 2 * rows || all < 2 * c.rows_per_pass * ctx.num_sms))
     c.rows_per_pass /= 2;
-  const int passes = (item_rows + c.rows_per_pass - 1) / c.rows_per_pass;
-  const dim3 grid(P.items, passes);
+  const dim3 grid(P.items, (rows + c.rows_per_pass - 1) / c.rows_per_pass);
   if (ctx.before) ctx.before(ctx.user, "kv_combine", ctx.stream);
   if (P.share)
     kv::launch_dep(kv::kv_combine_kernel<true>, grid, 256, 0, ctx.stream, c);

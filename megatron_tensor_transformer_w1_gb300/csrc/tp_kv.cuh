@@ -94,9 +94,13 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int row) {
 // Block c of C takes the tiles [c T / C, (c + 1) T / C), whatever items they
 // belong to; a run of tiles of one item in one block is a segment.  Every
 // block gets the same number of tiles however the lengths differ.
-__host__ __device__ __forceinline__ long long first_tile(long long c, long long T, long long C) { return c * T / C; }
-__host__ __device__ __forceinline__ long long block_of_tile(long long t, long long T, long long C) {
-  return ((t + 1) * C - 1) / T;
+// (a 64-bit division takes some hundred cycles, several in a row are felt)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 31) == 0 ? static_cast<int>(a) / static_cast<int>(b) : a / b;
+}
+__device__ __forceinline__ long long first_tile(long long c, long long T, long long C) { return quotient(c * T, C); }
+__device__ __forceinline__ long long block_of_tile(long long t, long long T, long long C) {
+  return quotient((t + 1) * C - 1, T);
 }
 
 template <bool PREFIX, int KTILE, int RT>
@@ -220,9 +224,9 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
     if (blockIdx.x >= S.blocks) return S;
     S.first = first_tile(blockIdx.x, S.total, S.blocks);
     S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, S.total, S.blocks) - S.first);
-    const long long item = S.first / c.nt;
+    const long long item = quotient(S.first, c.nt);
     c.t = static_cast<int>(S.first - item * c.nt);
-    c.h = static_cast<int>(item / n_rt);
+    c.h = static_cast<int>(quotient(item, n_rt));
     c.rt = static_cast<int>(item - static_cast<long long>(c.h) * n_rt);
   } else {
     const int per = (p.B + 127) / 128;
@@ -271,7 +275,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
         x.s = load_seq(p, b);
         const long long per_head = C::tiles_per_head(p, x.s);
         if (at < per_head * p.Hkv) {
-          x.h = static_cast<int>(at / per_head);
+          x.h = static_cast<int>(quotient(at, per_head));
           at -= x.h * per_head;
           for (x.rt = 0;; ++x.rt) {
             x.nt = C::tiles(p, x.s, x.rt);
@@ -303,8 +307,13 @@ struct Split {
 // segment that is a whole item goes to its rows' own places ([token][head],
 // used only where other keys are still to be joined), the others, of which a
 // block has at most two, its first and its last, to the block's two slots.
+// A slot's outputs lie in four parts of 32 columns, [4][slot_rows][32], the
+// 16-byte chunks of a row's 128 bytes swizzled by the row (chunk k at k ^ (r &
+// 7)): so the many-rows kernel, a row to a thread, can stage a warp's 32 rows
+// free of bank conflicts and write them as they lie, 512 bytes in a row per
+// store, and the combine kernel reads whole lines.
 struct Parts {
-  float* slot_o = nullptr;    // [2 blocks][slot_rows][HD]
+  float* slot_o = nullptr;    // [2 blocks][4][slot_rows][32]
   float2* slot_ml = nullptr;  // [2 blocks][slot_rows]
   float* row_o = nullptr;     // [n_tokens * H][HD]
   float2* row_ml = nullptr;
@@ -312,6 +321,11 @@ struct Parts {
   Split* split = nullptr;     // [blocks]
   int slot_rows = 0, grid = 0, rt = 0;  // rt: rows of a row tile, 0: all
 };
+
+// Chunk c (of 32, four columns each) of row r of a slot.
+__device__ __forceinline__ long long slot_chunk(const Parts& P, long long slot, int r, int c) {
+  return ((slot * 4 + (c >> 3)) * P.slot_rows + r) * 32 + (((c & 7) ^ (r & 7)) << 2);
+}
 
 // The note on a block's last segment: tile x of the list is its last one.
 __device__ __forceinline__ Split split_of(const Batch& p, const Sched& S, const Cursor& x, int seg_t, bool second) {

@@ -23,8 +23,9 @@
 //    read.  Two warps, because one spends a third of a step between products;
 //  * warps 4-7 and 8-11: the softmax of row tiles 0 and 1, a row per thread,
 //    with a maximum that moves only when it grew by more than 2^8, so that
-//    O_t is rarely rescaled; they also gather a segment's query rows and write
-//    its results.
+//    O_t is rarely rescaled; they write the rows out at the end of a segment;
+//  * warp 3: gathers the query rows of the next segment meanwhile (of the
+//    block's first, the softmax warps do).
 // S_t comes in halves of 64 keys into two buffers, so that the softmax of one
 // half finds the next one's scores done: with one buffer of 128 keys a row
 // tile waits for its two products in every step.
@@ -104,6 +105,14 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                  : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                    "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
 // Two 32-bit operations per instruction, and a maximum of three: with two
 // softmax warps per scheduler their instructions are what the time goes by.
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -160,6 +169,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   uint64_t* full = bar;         // [SLOTS] a K or V tile has landed
   uint64_t* empty = bar + 4;    // [SLOTS] its products are done
   uint64_t* q_full = bar + 8;   // [2]
+  uint64_t* q_empty = bar + 10; // [2] a segment's last S_t is done
   uint64_t* s_full = bar + 12;  // [2][2] S_t of a half tile is done
   uint64_t* p_full = bar + 16;  // [2][2] P_t written (a warp each)
   uint64_t* pv_done = bar + 20; // [2][2] O_t has its product
@@ -178,6 +188,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 4);
+      mbar_init(&q_empty[t], 1);
       mbar_init(&drain[t], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -213,6 +224,38 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   auto ring = [&](uint32_t i) { return smem + M_RING + (i & (SLOTS - 1)) * TILE_BYTES; };
   auto rows_of = [&](const Cursor& x) { return x.s.qn * B.G - x.rt * RT_MANY; };  // > 128: both row tiles
 
+  // Query rows [first, first + n) of row tile t of a segment, into the swizzled
+  // layout of the products: 16 lanes to a row, two rows of 256 bytes to a warp's
+  // copy.
+  const int dtok = 2 / B.G, dg = 2 - dtok * B.G;
+  auto fetch_q = [&](const Cursor& x, int t, int first, int n) {
+    const int rows = rows_of(x) - t * 128, r0 = first + (lane >> 4);
+    const int item_row = x.rt * RT_MANY + t * 128 + r0, tok = item_row / B.G;
+    int g = item_row - tok * B.G;
+    const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
+    const __nv_bfloat16* src =
+        p.q + ((static_cast<long long>(x.s.q0) + tok) * B.H + static_cast<long long>(x.h) * B.G + g) * HD +
+        (lane & 15) * 8;
+    const int step = (dtok * B.H + dg) * HD, wrap = (B.H - B.G) * HD;  // two rows on; past a token's last head
+#pragma unroll 4
+    for (int i = 0; i < n; i += 2) {
+      const bool valid = r0 + i < rows;
+      cp_async16z(sw_chunk(qs, 128, r0 + i, lane & 15), valid ? src : p.q, valid);
+      src += step;
+      g += dg;
+      if (g >= B.G) {
+        g -= B.G;
+        src += wrap;
+      }
+    }
+  };
+  // `arrivals` of the four that a row tile's rows take
+  auto publish_q = [&](int t, int arrivals) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane < arrivals) mbar_arrive(&q_full[t]);
+  };
   if (warp == 0) {
     // ------------------------------------------------ copies: K_0, V_0, K_1, V_1, ...
     const int page_keys = 1 << B.page_shift, box = page_keys < BK ? page_keys : BK;
@@ -283,7 +326,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const uint64_t q_desc = kdesc(smem_u32(smem + M_Q + t * TILE_BYTES), 128, 0),
                      k_desc = kdesc(smem_u32(smem + M_RING), 128, 0), v_desc = mndesc(smem_u32(smem + M_RING), 128, 0);
       // S_t of half j of the n-th tile
-      auto issue_s = [&](int n, int j) {
+      auto issue_s = [&](int n, int j, bool seg_ends) {
         const uint32_t buf = s_cnt++ & 1u;
         const uint64_t kd = k_desc + static_cast<uint64_t>(((2u * n) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * (SK * 128 >> 4));
         const uint32_t sd = tmem + t * 128 + buf * SK;
@@ -294,6 +337,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             umma_bf16(sd, q_desc + step, kd + step, ID_S, ks > 0 ? 1u : 0u);
           }
           umma_commit(&s_full[2 * t + buf]);
+          if (seg_ends) umma_commit(&q_empty[t]);
         }
         __syncwarp();
       };
@@ -343,7 +387,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           if (active) {
             if (!(ok = W.warp(&q_full[t], q_uses++ & 1u))) break;
             tc_fence_after();
-            for (int j = 0; j < halves(cur); ++j) issue_s(n, j);
+            for (int j = 0; j < halves(cur); ++j) issue_s(n, j, (cur & I_LAST) && j + 1 == halves(cur));
           }
           release(2u * n, active);
         }
@@ -356,7 +400,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
 #pragma unroll 1
           for (int j = 0; j < halves(cur); ++j) {
             if (!(ok = issue_pv(n, j, first && j == 0, min(4, steps - 4 * j)))) break;
-            if (j < n_next) issue_s(n + 1, j);
+            if (j < n_next) issue_s(n + 1, j, (next & I_LAST) && j + 1 == n_next);
           }
           if (!ok) break;
         }
@@ -371,45 +415,33 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       W.drain(&drain[t], 0u);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // ------------------------------------------------ query rows of all segments but the first
+    uint32_t uses[2] = {0, 0};
+    bool fresh = true, ok = true;
+    for (int n = 0; n < N && ok; ++n) {
+      for (int t = 0; fresh && t < 2 && rows_of(c) > t * 128; ++t) {
+        // S_t of the segment before that had this row tile is done
+        if (n > 0) {
+          if (uses[t] && !(ok = W.warp(&q_empty[t], (uses[t] - 1) & 1u))) break;
+          fetch_q(c, t, 0, 128);
+          publish_q(t, 4);
+        }
+        ++uses[t];
+      }
+      fresh = c.t + 1 == c.nt;
+      if (n + 1 < N) advance<C, PREFIX>(B, c);
+    }
+    __syncwarp();
+  } else {
     // ------------------------------------------------ softmax of row tile t
     const int t = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = smem_u32(smem + M_OUT + (warp - 4) * 4096);
     uint32_t cnt = 0;  // half tiles so far: buffer and phase
-    // The query rows of a segment, into the swizzled layout of the products:
-    // on their way while the segment before is written out.  (Its last S_t is
-    // done, so the buffer is free.)  16 lanes to a row, two rows of 256 bytes
-    // to a warp's copy.
-    const int dtok = 2 / B.G, dg = 2 - dtok * B.G;
-    auto fetch_q = [&](const Cursor& x) {
-      const int rows = rows_of(x) - t * 128, r0 = quarter * 32 + (lane >> 4);
-      const int item_row = x.rt * RT_MANY + t * 128 + r0;
-      int tok = item_row / B.G, g = item_row - tok * B.G;
-      const uint32_t qs = smem_u32(smem + M_Q + t * TILE_BYTES);
-      const __nv_bfloat16* src =
-          p.q + (static_cast<long long>(x.s.q0) * B.H + static_cast<long long>(x.h) * B.G) * HD + (lane & 15) * 8;
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const bool valid = r0 + 2 * i < rows;
-        cp_async16z(sw_chunk(qs, 128, r0 + 2 * i, lane & 15),
-                    valid ? src + (static_cast<long long>(tok) * B.H + g) * HD : src, valid);
-        tok += dtok;
-        g += dg;
-        if (g >= B.G) {
-          g -= B.G;
-          ++tok;
-        }
-      }
-    };
-    auto publish_q = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      arrive_warp(&q_full[t]);
-    };
     if (N > 0 && rows_of(c) > t * 128) {
-      fetch_q(c);
-      publish_q();
+      fetch_q(c, t, quarter * 32, 32);
+      publish_q(t, 1);
     }
     const uint64_t scale2 = pack2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
     bool fresh = true;
@@ -419,9 +451,6 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     for (int n = 0; n < N; ++n) {
       const int rows = rows_of(c);
       const bool last = c.t + 1 == c.nt || n + 1 == N;
-      Cursor next = c;
-      if (n + 1 < N) advance<C, PREFIX>(B, next);
-      const bool fetch = last && n + 1 < N && rows_of(next) > t * 128;
       if (rows > t * 128) {
         if (fresh) {
           seg_t = c.t;
@@ -490,11 +519,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             for (int k = 0; k < HD; k += 16) {
               uint32_t o[16];
               tmem_ld16(tl + 256 + t * 128 + k, o);
-              tmem_wait_ld();
-              asm volatile(""
-                           : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]),
-                             "+r"(o[7]), "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]),
-                             "+r"(o[13]), "+r"(o[14]), "+r"(o[15]));
+              tmem_wait_ld16(o);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
               tmem_st16(tl + 256 + t * 128 + k, o);
@@ -541,21 +566,20 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         if (last) {
           if (threadIdx.x == 128 && n + 1 == N && p.part.split)
             p.part.split[blockIdx.x] = split_of(B, S, c, seg_t, seg_n > 0);
-          if (fetch) fetch_q(next);
           // ---- the segment's rows: to o, to their own places, or to a slot
           const uint32_t was = cnt - 1;
           if (!W.warp(&pv_done[2 * t + (was & 1u)], (was >> 1) & 1u)) break;
           tc_fence_after();
-          if (fetch) publish_q();  // the next segment's S_t may start
           const bool whole = seg_t == 0 && c.t + 1 == c.nt;
           const bool direct = whole && !PREFIX && B.shared == 0;
-          const long long slot = (2ll * blockIdx.x + (seg_n ? 1 : 0)) * p.part.slot_rows + t * 128 + quarter * 32;
+          const long long slot = 2ll * blockIdx.x + (seg_n ? 1 : 0);
+          const int row0 = t * 128 + quarter * 32;  // of the warp, in the item
           const float inv = l > 0.f ? 1.f / l : 0.f;
           // 128 bytes of each of the warp's 32 rows, staged so that eight lanes
           // write a row's together: dst(row of the warp, row among all)
           auto write_rows = [&](auto dst) {
             __syncwarp();
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {
               const int rr = 4 * i + (lane >> 3), k = lane & 7;
               const uint4 v = ld_shared_v4(sbuf + rr * 128 + ((k ^ (rr & 7)) << 4));
@@ -568,44 +592,49 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             st_shared_v4(sbuf + lane * 128 + ((k ^ (lane & 7)) << 4), a, b, c, d);
           };
 #pragma unroll 1
-          for (int col = 0; col < HD; col += 32) {
-            uint32_t o[32];
-            tmem_ld32(tl + 256 + t * 128 + col, o);
-            tmem_wait_ld32(o);
+          for (int col = 0; col < HD; col += 16) {
+            uint32_t o[16];
+            tmem_ld16(tl + 256 + t * 128 + col, o);
+            tmem_wait_ld16(o);
             if (direct) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (int k = 0; k < 2; ++k) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   w[e] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                stage((col & 32) / 8 + k, w[0], w[1], w[2], w[3]);
+                stage((col & 48) / 8 + k, w[0], w[1], w[2], w[3]);
               }
-              if (col & 32) write_rows([&](int, int row) { return p.o + static_cast<long long>(row) * HD + col - 32; });
+              if ((col & 48) == 48) write_rows([&](int, int row) { return p.o + static_cast<long long>(row) * HD + col - 48; });
             } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) stage(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-              write_rows([&](int rr, int row) {
-                return (whole ? p.part.row_o + static_cast<long long>(row) * HD : p.part.slot_o + (slot + rr) * HD) + col;
-              });
+              for (int k = 0; k < 4; ++k) stage((col & 16) / 4 + k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              if (col & 16) {
+                if (whole) {
+                  write_rows([&](int, int row) { return p.part.row_o + static_cast<long long>(row) * HD + col - 16; });
+                } else {
+                  __syncwarp();
+                  uint4* dst = reinterpret_cast<uint4*>(p.part.slot_o) +
+                               ((slot * 4 + (col >> 5)) * p.part.slot_rows + row0) * 8 + lane;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) dst[32 * i] = ld_shared_v4(sbuf + (32 * i + lane) * 16);
+                  __syncwarp();
+                }
+              }
             }
           }
           if (at >= 0) {
             if (!direct)
-              (whole ? p.part.row_ml[at] : p.part.slot_ml[slot + lane]) = make_float2(m, l);
+              (whole ? p.part.row_ml[at] : p.part.slot_ml[slot * p.part.slot_rows + row0 + lane]) = make_float2(m, l);
             else if (p.lse)
               p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
           }
           tc_fence_before();
         }
-      } else if (fetch) {
-        fetch_q(next);
-        publish_q();
       }
       fresh = last;
-      c = next;
+      if (n + 1 < N) advance<C, PREFIX>(B, c);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   }
 

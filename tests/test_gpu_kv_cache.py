@@ -130,6 +130,58 @@ def test_attend_many_rows(new, ctx, H, Hkv, T, page, shared, causal):
     test_attend(new, ctx, H, Hkv, T, page, shared, causal)
 
 
+SHARED = [  # shared keys worth taking together: (sequences - 1) x keys x key heads x 512 bytes from 96 MiB on
+    ([1] * 7, [5, 40, 1, 0, 300, 64, 63], 32, 16, 4, 16, 2048, True),         # 14 rows: few
+    ([1, 2, 1, 0, 1, 3, 1, 1], [5, 0, 130, 9, 0, 1, 2, 3], 32, 16, 4, 64, 1800, True),   # 20 rows, ends inside a page
+    ([2] * 8, [30] * 8, 16, 8, 2, 16, 3600, False),                           # 32 rows, all keys seen
+    ([3] * 11, [5 * i for i in range(11)], 32, 8, 8, 128, 2500, True),        # 132 rows: many
+    ([1] * 80, [(i * 29) % 200 for i in range(80)], 8, 2, 2, 16, 1301, True),  # 320 rows, two row tiles
+    ([1] * 70, [3] * 70, 10, 2, 1, 1024, 1500, False),                        # groups of five
+    ([200] + [1] * 59, [3] * 60, 2, 2, 2, 64, 1700, True),                    # a prompt among single tokens
+    ([9, 1] * 10, [0] * 20, 40, 5, 5, 8, 2100, True),                         # no own context; own rows: many
+]
+
+
+@pytest.mark.parametrize("new,ctx,H,Hkv,T,page,shared,causal", SHARED)
+def test_attend_shared_keys(new, ctx, H, Hkv, T, page, shared, causal):
+    assert (len(new) - 1) * shared * Hkv * 512 >= 96 << 20
+    test_attend(new, ctx, H, Hkv, T, page, shared, causal)
+
+
+@pytest.mark.parametrize("new", [1, 5])
+def test_attend_shared_keys_longer_than_sequences(new):
+    """Behind shared keys that some sequences do not reach the end of: cut rows, no
+    keys at all, more new tokens than keys."""
+    B, Hkv, H = 60, 2, 8
+    s = ref.make_batch([new] * B, [3] * B, Hkv, 16, shared=1700, seed=6)
+    for b, n in ((0, 1650), (1, 0), (2, 1), (3, 3), (7, 1699), (8, 1701), (59, 64)):
+        s["lens"][b] = n
+    s["kv_len"].copy_(torch.tensor(s["lens"]))
+    cache, batch = _cache(s, H, 2)
+    q = _q(s["n"], H, 2)
+    o, lse = cache.attend(q, batch, shared_len=1700, lse=True)
+    assert cache.last_device_error() == 0
+    check_attend(s, q, H, o, lse)
+
+
+def test_attend_shared_keys_of_idle_sequences():
+    """The first sequence has no keys and no table: the shared pages are found all the same."""
+    B, Hkv, H = 60, 2, 8
+    s = ref.make_batch([0] + [1] * (B - 1), [0] * B, Hkv, 16, shared=1700, seed=16)
+    s["lens"][0] = 0
+    s["kv_len"][0] = 0
+    s["table"][0] = -5
+    cache, batch = _cache(s, H, 2)
+    q = _q(s["n"], H, 2)
+    o, lse = cache.attend(q, batch, shared_len=1700, lse=True)
+    assert cache.last_device_error() == 0
+    check_attend(s, q, H, o, lse)
+    # a bad shared page is reported
+    s["table"][:, 3] = s["n_pages"]
+    o = cache.attend(q, batch, shared_len=1700)
+    assert cache.last_device_error() == _modules()[0].TP_ERR_BATCH and torch.isfinite(o).all()
+
+
 def test_attend_many_rows_that_see_nothing():
     """A prompt cut off by kv_len: its first rows see no key, whole row tiles among them."""
     s = ref.make_batch([600, 70, 80], [0, 0, 10], 1, 16, seed=15)
@@ -336,25 +388,26 @@ def test_append_then_attend_over_several_steps():
 
 def test_two_streams_and_a_graph():
     """Calls on two streams at once, and a captured step replayed on changed contents."""
-    s = ref.make_batch([1] * 6, [300, 20, 999, 0, 64, 128], 2, 16, shared=64, seed=41)
-    cache, batch = _cache(s, 16, 2, inv_freq=10000.0 ** (-torch.arange(32, device="cuda") / 32))
+    shared = 2600
+    s = ref.make_batch([1] * 6, [300, 20, 999, 0, 64, 128], 16, 16, shared=shared, seed=41)
+    cache, batch = _cache(s, 64, 2, inv_freq=10000.0 ** (-torch.arange(32, device="cuda") / 32))
     g = torch.Generator(device="cuda").manual_seed(3)
-    qkv = [torch.randn(s["n"], 20 * HD, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    qkv = [torch.randn(s["n"], 96 * HD, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
     eager = []
     for x in qkv:
-        o, lse = _step(cache, batch, x, 64)
+        o, lse = _step(cache, batch, x, shared)
         eager.append((o.clone(), lse.clone()))
     qs = [cache.append(x, batch).clone() for x in qkv]
     cache.append(qkv[0], batch)
     torch.cuda.synchronize()
-    one = [cache.attend(q, batch, shared_len=64) for q in qs]
+    one = [cache.attend(q, batch, shared_len=shared) for q in qs]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     got = [[], []]
     for _ in range(10):
         for st, q, out in zip(streams, qs, got):
             with torch.cuda.stream(st):
-                out.append(cache.attend(q, batch, shared_len=64))
+                out.append(cache.attend(q, batch, shared_len=shared))
     torch.cuda.synchronize()
     for out, want in zip(got, one):
         assert all(torch.equal(o, want) for o in out)
@@ -363,7 +416,7 @@ def test_two_streams_and_a_graph():
     for _ in range(2):  # two graphs of the same calls
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            held.append(_step(cache, batch, x, 64))
+            held.append(_step(cache, batch, x, shared))
         graphs.append(graph)
     for i in (1, 2, 0):
         x.copy_(qkv[i])
