@@ -11,15 +11,22 @@ in libtpffn.so.
     o = cache.attend(q, batch, shared_len=0)          # [n, H * 128]
     y = attn.decode(x, cache, batch, wqkv, wo)        # both, between the projections
 
-A call takes its workspace from PyTorch's allocator on the current stream, so
-calls on different streams, and graphs that were captured apart, do not share
-one (an append needs only status words, which the cache keeps).
+The cache keeps a workspace for every stream that it has been used on; a call
+that is being captured into a graph takes one of its own (from the graph's
+memory), so that no two of them can be at work in the same one.  (An append
+needs only status words, which the cache keeps.)
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
 from . import tpffn as abi
+
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 class KVBatch:
@@ -43,8 +50,10 @@ class KVBatch:
         self.cu_tokens, self.kv_len, self.page_table = cu_tokens, kv_len, page_table
         self.n_seqs, self.n_tokens, self.max_new = kv_len.numel(), n_tokens, max_new
         self.device = kv_len.device
+        self._index = kv_len.get_device()
         self.abi = abi.KvBatch(self.n_seqs, n_tokens, max_new, page_table.shape[1], cu_tokens.data_ptr(),
                                kv_len.data_ptr(), page_table.data_ptr())
+        self._at = ctypes.addressof(self.abi)
         self._bytes = {}  # workspace sizes of the calls made with this batch
 
 
@@ -58,7 +67,7 @@ class PagedKVCache:
     def __init__(self, attn, n_pages, page_size, k=None, v=None, inv_freq=None, interleaved=False, rotary_scale=1.0):
         shape = (int(n_pages), attn.Hkv, int(page_size), attn.hd)
         self.attn, self.n_pages, self.page_size = attn, shape[0], shape[2]
-        self._width = attn.info["qkv_width"]
+        self._width, self._q_width = attn.info["qkv_width"], attn.H * attn.hd
         self.device = attn.device if attn.device.index is not None else torch.device(
             attn.device.type, torch.cuda.current_device())
         if n_pages < 1 or page_size < 8 or page_size > 1024 or page_size & (page_size - 1):
@@ -80,10 +89,13 @@ class PagedKVCache:
             self._check("inv_freq", inv_freq, torch.float32, inv_freq.shape)
             self._rot = abi.KvRotation(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)),
                                        float(rotary_scale))
+        self._at = ctypes.addressof(self._abi)
+        self._rot_at = None if self._rot is None else ctypes.addressof(self._rot)
         self._status = torch.empty(abi.tp_attn_kv_workspace_bytes(attn.plan, abi.KvBatch(), self.page_size, 0,
                                                                   abi.TP_KV_APPEND),
                                    dtype=torch.uint8, device=self.device)
-        self._last = None  # workspace of the last call, for last_device_error
+        self._workspaces = {}  # by stream
+        self._last = None      # workspace of the last call, for last_device_error
 
     def _check(self, name, t, dtype, shape):
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
@@ -96,22 +108,27 @@ class PagedKVCache:
         self._check(name, t, torch.bfloat16, shape)
         return t
 
-    def _workspace(self, batch, shared_len, call, flags):
-        key = (call, shared_len, flags, self.attn.plan, self.page_size)
+    def _workspace(self, batch, shared_len, call, flags, stream):
+        key = (self.attn.plan, self.page_size, shared_len, call, flags)
         need = batch._bytes.get(key)
         if need is None:
-            need = abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call, flags)
+            need = max(16, abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call,
+                                                          flags))
             batch._bytes[key] = need
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+        if _capturing():
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        else:
+            ws = self._workspaces.get(stream)
+            if ws is None or ws.numel() < need:
+                ws = self._workspaces[stream] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self._last = ws if batch.n_tokens and batch.n_seqs else None
+        return ws, need
 
-    def _run(self, batch, call):
-        """call(stream) with the cache's device current."""
-        if batch.device != self.device:
+    def _elsewhere(self, batch):
+        """Whether the cache's device is not the current one."""
+        if batch._index != self._index:
             raise ValueError(f"the batch lies on {batch.device}, the cache on {self.device}")
-        if torch._C._cuda_getDevice() == self._index:
-            return call(torch._C._cuda_getCurrentRawStream(self._index))
-        with torch.cuda.device(self.device):
-            return call(torch._C._cuda_getCurrentRawStream(self._index))
+        return _current_device() != self._index
 
     def batch(self, cu_tokens, kv_len, page_table, n_tokens, max_new):
         return KVBatch(cu_tokens, kv_len, page_table, n_tokens, max_new)
@@ -119,48 +136,51 @@ class PagedKVCache:
     def append(self, qkv, batch, q=None, flags=0):
         """Stores the new tokens' keys (rotated) and values; returns the rotated
         queries [n_tokens, H * 128] (in `q` if given)."""
-        return self._run(batch, lambda st: self._append(qkv, batch, q, flags, st))
-
-    def _append(self, qkv, batch, q, flags, st):
-        a, n = self.attn, batch.n_tokens
+        if self._elsewhere(batch):
+            with torch.cuda.device(self.device):
+                return self.append(qkv, batch, q, flags)
+        n = batch.n_tokens
         self._check("qkv", qkv, torch.bfloat16, (n, self._width))
-        q = self._out("q", q, (n, a.H * a.hd))
-        rc = abi.tp_attn_kv_append(a.plan, self._abi, batch.abi, self._rot, qkv, q, self._status,
-                                   self._status.numel(), flags, st)
-        abi.check(rc, "tp_attn_kv_append")
+        q = self._out("q", q, (n, self._q_width))
         self._last = self._status if n and batch.n_seqs else None
+        rc = abi._lib.tp_attn_kv_append(self.attn.plan, self._at, batch._at, self._rot_at, qkv.data_ptr(),
+                                        q.data_ptr(), self._status.data_ptr(), self._status.numel(), flags,
+                                        _current_stream(self._index))
+        if rc:
+            abi.check(rc, "tp_attn_kv_append")
         return q
 
     def attend(self, q, batch, shared_len=0, lse=False, out=None, flags=0):
         """Attention of q [n_tokens, H * 128] over the cache: o, or (o, lse) with
         the rows' log2-sum-exp [n_tokens, H] if `lse`."""
-        return self._run(batch, lambda st: self._attend(q, batch, shared_len, lse, out, flags, st))
-
-    def _attend(self, q, batch, shared_len, lse, out, flags, st):
-        a, n = self.attn, batch.n_tokens
-        shape = (n, a.H * a.hd)
+        if self._elsewhere(batch):
+            with torch.cuda.device(self.device):
+                return self.attend(q, batch, shared_len, lse, out, flags)
+        n = batch.n_tokens
+        shape = (n, self._q_width)
         self._check("q", q, torch.bfloat16, shape)
-        o = self._out("out", out, shape)
-        rows = torch.empty((n, a.H), dtype=torch.float32, device=self.device) if lse else None
-        ws = self._workspace(batch, shared_len, abi.TP_KV_ATTEND, 0)
-        rc = abi.tp_attn_paged_fwd(a.plan, self._abi, batch.abi, shared_len, q, o, rows, ws, ws.numel(), flags, st)
-        abi.check(rc, "tp_attn_paged_fwd")
-        self._last = ws if n and batch.n_seqs else None
+        o = torch.empty_like(q) if out is None else self._out("out", out, shape)
+        rows = torch.empty((n, self.attn.H), dtype=torch.float32, device=self.device) if lse else None
+        st = _current_stream(self._index)
+        ws, need = self._workspace(batch, shared_len, abi.TP_KV_ATTEND, 0, st)
+        rc = abi._lib.tp_attn_paged_fwd(self.attn.plan, self._at, batch._at, shared_len, q.data_ptr(), o.data_ptr(),
+                                        rows.data_ptr() if lse else None, ws.data_ptr(), need, flags, st)
+        if rc:
+            abi.check(rc, "tp_attn_paged_fwd")
         return (o, rows) if lse else o
 
     def decode(self, x, batch, wqkv, wo, shared_len=0, out=None, flags=0):
         """The sublayer's serving pass, y [n_tokens, d] (TensorParallelAttention.decode)."""
-        return self._run(batch, lambda st: self._decode(x, batch, wqkv, wo, shared_len, out, flags, st))
-
-    def _decode(self, x, batch, wqkv, wo, shared_len, out, flags, st):
+        if self._elsewhere(batch):
+            with torch.cuda.device(self.device):
+                return self.decode(x, batch, wqkv, wo, shared_len, out, flags)
         a, n = self.attn, batch.n_tokens
         self._check("x", x, torch.bfloat16, (n, a.d))
         y = self._out("out", out, (n, a.d))
-        ws = self._workspace(batch, shared_len, abi.TP_KV_DECODE, flags)
-        rc = abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
-                                    ws.numel(), flags, st)
-        abi.check(rc, "tp_attn_decode_fwd")
-        self._last = ws if n and batch.n_seqs else None
+        st = _current_stream(self._index)
+        ws, need = self._workspace(batch, shared_len, abi.TP_KV_DECODE, flags, st)
+        abi.check(abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
+                                         need, flags, st), "tp_attn_decode_fwd")
         return y
 
     def last_device_error(self):

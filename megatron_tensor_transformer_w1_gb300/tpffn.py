@@ -349,7 +349,9 @@ def tp_attn_last_launch_count(plan):
 
 
 # ------------------------------------------------------------ key/value cache
-_ref = lambda s: None if s is None else ctypes.addressof(s)  # of a KvCache, KvBatch or KvRotation
+def _ref(s):
+    """The address of a KvCache, KvBatch or KvRotation (or None)."""
+    return None if s is None else ctypes.addressof(s)
 
 
 def tp_attn_kv_workspace_bytes(plan, batch, page_size, shared_len, call, flags=0):
