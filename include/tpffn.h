@@ -368,7 +368,8 @@ TPFFN_API int tp_attn_last_launch_count(const tp_attn_plan* plan);
  *   cu_tokens  [n_seqs + 1]  sequence b's new tokens are the rows
  *              cu_tokens[b] .. cu_tokens[b + 1] - 1 of every [n_tokens][...]
  *              buffer; ascending from 0.  Rows behind cu_tokens[n_seqs] are
- *              nobody's (padding): they are not read and left as they were.
+ *              nobody's (padding): what they hold is not used, and the
+ *              outputs' rows there are left as they were.
  *   kv_len     [n_seqs]  keys of the sequence with the new tokens, whose
  *              positions are the last ones: kv_len[b] - q .. kv_len[b] - 1
  *   page_table [n_seqs][max_pages]  key j lies in page page_table[b][j /
@@ -441,9 +442,10 @@ TPFFN_API int tp_attn_kv_append(const tp_attn_plan* plan, const tp_kv_cache* cac
  * hold anything.
  * shared_len > 0: the first shared_len keys of all sequences are the same
  * (their page table rows name the same pages, or pages of the same contents,
- * there); they are attended to once for the rows of all sequences together,
- * read through the table row of the longest sequence.  The result is that
- * of shared_len = 0 up to rounding.  0 <= shared_len <= max_pages * page_size.
+ * there).  Where that saves enough reads they are attended to once for the
+ * rows of all sequences together, read through the table row of the longest
+ * sequence.  The result is that of shared_len = 0 up to rounding.
+ * 0 <= shared_len <= max_pages * page_size.
  * Results do not change from run to run.  Errors as tp_attn_kv_append. */
 TPFFN_API int tp_attn_paged_fwd(const tp_attn_plan* plan, const tp_kv_cache* cache, const tp_kv_batch* batch,
                                 int64_t shared_len, const void* q, void* o, float* lse, void* workspace,

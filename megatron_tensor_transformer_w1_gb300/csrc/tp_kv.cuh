@@ -94,7 +94,8 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int row) {
 // Block c of C takes the tiles [c T / C, (c + 1) T / C), whatever items they
 // belong to; a run of tiles of one item in one block is a segment.  Every
 // block gets the same number of tiles however the lengths differ.
-// (a 64-bit division takes some hundred cycles, several in a row are felt)
+
+// (A 64-bit division takes some hundred cycles, and several in a row are felt.)
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 31) == 0 ? static_cast<int>(a) / static_cast<int>(b) : a / b;
 }
@@ -135,8 +136,9 @@ struct Cursor {
   Seq s;
 };
 
-// The next tile; past an item's end the next one that has tiles (the caller
-// knows that there is one).
+// The next tile; past an item's end the next one that has tiles.  The caller
+// knows that there is one; should the arrays have changed meanwhile, the walk
+// ends at the last sequence with an item of no rows and no keys.
 template <typename C, bool PREFIX>
 __device__ __forceinline__ void advance(const Batch& p, Cursor& c) {
   if (++c.t < c.nt) return;
@@ -146,7 +148,15 @@ __device__ __forceinline__ void advance(const Batch& p, Cursor& c) {
       c.rt = 0;
       if (++c.h >= p.Hkv) {
         c.h = 0;
-        if constexpr (!PREFIX) c.s = load_seq(p, ++c.b);
+        if constexpr (!PREFIX) {
+          if (++c.b >= p.B) {
+            c.b = p.B - 1;
+            c.s.qn = c.s.kv = 0;
+            c.nt = 1;
+            return;
+          }
+          c.s = load_seq(p, c.b);
+        }
       }
     }
     c.nt = C::tiles(p, c.s, c.rt);

@@ -272,10 +272,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     int next = N > 0 ? look_up(c) : -1;
     for (int n = 0; n < N && ok; ++n) {
       const int base = (t0 + c.t) * BK;
-      const int live = min(groups, (c.s.kv - base + box - 1) / box);  // groups that hold keys
+      const int live = max(min(groups, (c.s.kv - base + box - 1) / box), 0);  // groups that hold keys
       const int key = base + lane * box, h = c.h;
       // what the issuing warp has to know of the tile; published with its K
-      const uint32_t what = static_cast<uint32_t>((min(BK, c.s.kv - base) + 15) / 16) |
+      const uint32_t what = static_cast<uint32_t>((max(min(BK, c.s.kv - base), 0) + 15) / 16) |
                             (c.t + 1 == c.nt || n + 1 == N ? I_LAST : 0u) | (rows_of(c) > 128 ? I_TWO : 0u);
       int page = next;
       if (n + 1 < N) {
