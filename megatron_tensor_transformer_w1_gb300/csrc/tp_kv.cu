@@ -225,6 +225,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
   const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -285,9 +288,9 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     return;
   }
 
-  // page of 8-key group `lane` (< 8) of the cursor's tile, or -1
-  auto page_of_group = [&](const Cursor& x) -> int {
-    if (lane >= 8) return -1;
+  // The page of each 8-key group of four tiles of the cursor's item from its
+  // tile on, a lane to a group; -1: no key, or no page of the cache.
+  auto look_up = [&](const Cursor& x) -> int {
     const int key = (t0 + x.t) * KT + lane * 8;
     if (key >= x.s.kv) return -1;
     const int row = PREFIX ? S.table_row : x.b;
@@ -298,20 +301,37 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     }
     return page;
   };
-  auto issue = [&](int stage, const Cursor& x, int group_page, bool new_item) {
+  // Copies of tile x, whose groups' pages are in lanes `from` on.  What this
+  // takes to issue is felt in the stream of bytes: a whole tile within a page
+  // (pages of 64 keys or more) finds its place once.
+  const int ch = tid & 15, r0 = tid >> 4, mask = (1 << B.page_shift) - 1;
+  const long long page_stride = (static_cast<long long>(B.Hkv) << B.page_shift) * HD;
+  auto issue = [&](int stage, const Cursor& x, int pages, int from, bool new_item) {
     const uint32_t ks = smem_u32(smem + stage * F::STAGE), vs = ks + F::KV_BYTES, qs = vs + F::KV_BYTES;
-    const int ch = tid & 15, r0 = tid >> 4;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = r0 + 8 * i, key = (t0 + x.t) * KT + r;
-      const int page = __shfl_sync(0xffffffffu, group_page, i);
-      const bool ok = page >= 0 && key >= lo && key < x.s.kv;
+    const int first = (t0 + x.t) * KT;
+    const int page = __shfl_sync(0xffffffffu, pages, from);
+    if (B.page_shift >= 6 && page >= 0 && first >= lo && first + KT <= x.s.kv) {
       const long long off =
-          ok ? ((((static_cast<long long>(page) * B.Hkv + x.h) << B.page_shift) +
-                 (key & ((1 << B.page_shift) - 1))) * HD + ch * 8)
-             : 0;
-      cp_async16(tile_chunk(ks, r, ch), B.k + off, ok);
-      cp_async16(tile_chunk(vs, r, ch), B.v + off, ok);
+          (((static_cast<long long>(page) * B.Hkv + x.h) << B.page_shift) + (first & mask) + r0) * HD + ch * 8;
+      const __nv_bfloat16 *k = B.k + off, *v = B.v + off;
+      const uint32_t at = tile_chunk(0, r0, ch);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cp_async16(ks + at + i * 2048, k + i * 8 * HD);
+        cp_async16(vs + at + i * 2048, v + i * 8 * HD);
+      }
+    } else {
+      const long long head = (static_cast<long long>(x.h) << B.page_shift) * HD + ch * 8;
+      const uint32_t at = tile_chunk(0, r0, ch);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int key = first + r0 + 8 * i;
+        const int page = __shfl_sync(0xffffffffu, pages, from + i);
+        const bool ok = page >= 0 && key >= lo && key < x.s.kv;
+        const long long off = ok ? page * page_stride + head + (key & mask) * HD : 0;
+        cp_async16(ks + at + i * 2048, B.k + off, ok);
+        cp_async16(vs + at + i * 2048, B.v + off, ok);
+      }
     }
     if (new_item) {
       const int rows = x.s.qn * B.G;
@@ -328,19 +348,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     if (tid == 0) s_cur[stage] = x;
   };
 
-  int issued = 0;
-  int group_page = page_of_group(c);
-#pragma unroll
-  for (int s = 0; s < F::STAGES - 1; ++s) {
-    if (issued < n_tiles) {
-      issue(s, c, group_page, issued == 0 || c.t == 0);
-      if (++issued < n_tiles) {
-        advance<C, PREFIX>(B, c);
-        group_page = page_of_group(c);
-      }
-    }
-    cp_async_commit();
-  }
+  int issued = 0, looked_at = c.t;  // tiles copied so far; the tile that `pages` begins with
+  int pages = look_up(c);
 
   float o[16][4];
   float m[2], l[2];
@@ -348,20 +357,28 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   int limit[2] = {0, 0};
   bool fresh = true;         // the next tile starts a segment
   int seg_t = 0, seg_i = 0;  // its first tile within the item, and of the block's
-  for (int i = 0; i < n_tiles; ++i) {
-    const int stage = i % F::STAGES;
-    cp_async_wait<F::STAGES - 2>();
-    __syncthreads();  // tile i has landed for everybody; tile i - 1 has been used by everybody
-    const Cursor x = s_cur[stage];
+  // (The copies run STAGES - 1 tiles ahead.  They begin in the same loop: the
+  // code for them is long, and a second copy of it is fetched for nothing.)
+#pragma unroll 1
+  for (int i = 1 - F::STAGES; i < n_tiles; ++i) {
+    if (i >= 0) {
+      cp_async_wait<F::STAGES - 2>();
+      __syncthreads();  // tile i has landed for everybody; tile i - 1 has been used by everybody
+    }
     if (issued < n_tiles) {
-      issue((i + F::STAGES - 1) % F::STAGES, c, group_page, c.t == 0);
+      issue(issued % F::STAGES, c, pages, 8 * (c.t - looked_at), issued == 0 || c.t == 0);
       if (++issued < n_tiles) {
         advance<C, PREFIX>(B, c);
-        group_page = page_of_group(c);
+        if (c.t == 0 || c.t == looked_at + 4) {
+          looked_at = c.t;
+          pages = look_up(c);
+        }
       }
     }
     cp_async_commit();
-
+    if (i < 0) continue;
+    const int stage = i % F::STAGES;
+    const Cursor x = s_cur[stage];
     const uint32_t ks = smem_u32(smem + stage * F::STAGE), vs = ks + F::KV_BYTES, qs = vs + F::KV_BYTES;
     const int rows = x.s.qn * B.G;
     if (fresh) {

@@ -97,7 +97,7 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int row) {
 
 // (A 64-bit division takes some hundred cycles, and several in a row are felt.)
 __device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 31) == 0 ? static_cast<int>(a) / static_cast<int>(b) : a / b;
+  return ((a | b) >> 32) == 0 ? static_cast<unsigned>(a) / static_cast<unsigned>(b) : a / b;
 }
 __device__ __forceinline__ long long first_tile(long long c, long long T, long long C) { return quotient(c * T, C); }
 __device__ __forceinline__ long long block_of_tile(long long t, long long T, long long C) {
@@ -175,23 +175,48 @@ struct Sched {
   bool all_see = false;    // every row sees every shared key
   bool some_empty = false; // there are rows of sequences that belong to no tile
   long long first = 0, total = 0, blocks = 0;
+  // this block's share of `total_` tiles; false: none
+  __device__ __forceinline__ bool set(long long total_) {
+    total = total_;
+    blocks = total < gridDim.x ? total : gridDim.x;
+    if (blockIdx.x >= blocks) return false;
+    first = first_tile(blockIdx.x, total, blocks);
+    n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, total, blocks) - first);
+    return true;
+  }
 };
+
+// The place of tile `at` of a sequence's (x.b, x.s) tiles.
+template <typename C>
+__device__ __forceinline__ void locate(const Batch& p, Cursor& x, long long at, long long per_head) {
+  x.h = static_cast<int>(quotient(at, per_head));
+  at -= x.h * per_head;
+  for (x.rt = 0;; ++x.rt) {
+    x.nt = C::tiles(p, x.s, x.rt);
+    if (at < x.nt) break;
+    at -= x.nt;
+  }
+  x.t = static_cast<int>(at);
+}
 
 // Called by every thread of a block (at least 128): sums the tiles of all
 // sequences and finds the block's first tile.  Block 0 leaves the prefix sums
 // for the combine kernel where that asks for them: `sched` [B + 1] tiles per
 // key/value head before sequence b, or for prefix items {tiles of a row tile,
-// row tiles}.
+// row tiles}.  Up to 32 sequences every warp does it for itself, a lane to a
+// sequence, without meeting the others: a call of few tokens waits for this
+// before its first copy.
 template <typename C, bool PREFIX>
 __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, SchedScratch* w, Cursor& c, int* err) {
   const int tid = threadIdx.x, lane = tid & 31;
+  const bool small = p.B <= 32;
   Sched S;
   if constexpr (PREFIX) {
     // the longest sequence's table covers the shared pages if any does
-    if (tid < 128) {
-      unsigned long long longest = 0;
-      int least = INT_MAX;
-      for (int b = tid; b < p.B; b += 128) {
+    unsigned long long longest = 0;
+    int least = INT_MAX;
+    if (small || tid < 128) {
+      for (int b = small ? lane : tid; b < p.B; b += 128) {
         const Seq s = load_seq(p, b);
         const unsigned long long key = (static_cast<unsigned long long>(s.kv) << 32) | (0xffffffffu - b);
         longest = key > longest ? key : longest;
@@ -203,18 +228,18 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
         longest = o > longest ? o : longest;
         least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
       }
-      if (lane == 0) {
+    }
+    if (!small) {
+      if (tid < 128 && lane == 0) {
         w->longest[tid >> 5] = longest;
         w->least[tid >> 5] = least;
       }
-    }
-    __syncthreads();
-    unsigned long long longest = w->longest[0];
-    int least = w->least[0];
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      longest = w->longest[i] > longest ? w->longest[i] : longest;
-      least = min(least, w->least[i]);
+      __syncthreads();
+      longest = 0;
+      for (int i = 0; i < 4; ++i) {
+        longest = w->longest[i] > longest ? w->longest[i] : longest;
+        least = min(least, w->least[i]);
+      }
     }
     S.table_row = static_cast<int>(0xffffffffu - static_cast<unsigned>(longest));
     c.b = 0;
@@ -225,29 +250,26 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
     S.all_see = least >= c.s.kv;
     const int n_rt = C::row_tiles(p, c.s);
     c.nt = C::tiles(p, c.s, 0);
-    S.total = static_cast<long long>(n_rt) * c.nt * p.Hkv;
     if (blockIdx.x == 0 && tid == 0) {
       sched[0] = c.nt;
       sched[1] = n_rt;
     }
-    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
-    if (blockIdx.x >= S.blocks) return S;
-    S.first = first_tile(blockIdx.x, S.total, S.blocks);
-    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, S.total, S.blocks) - S.first);
+    if (!S.set(static_cast<long long>(n_rt) * c.nt * p.Hkv)) return S;
     const long long item = quotient(S.first, c.nt);
     c.t = static_cast<int>(S.first - item * c.nt);
     c.h = static_cast<int>(quotient(item, n_rt));
     c.rt = static_cast<int>(item - static_cast<long long>(c.h) * n_rt);
   } else {
-    const int per = (p.B + 127) / 128;
-    const int b0 = min(tid * per, p.B), b1 = tid < 128 ? min(b0 + per, p.B) : b0;
+    const int per = small ? 1 : (p.B + 127) / 128;
+    const int b0 = small ? min(lane, p.B) : min(tid * per, p.B), b1 = small || tid < 128 ? min(b0 + per, p.B) : b0;
     long long sum = 0;
     int empty = 0;
+    Cursor x{};
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(p, b);
-      *err |= s.err;
-      sum += C::tiles_per_head(p, s);
-      empty |= s.qn > 0 && C::tiles(p, s, 0) == 0;
+      x.s = load_seq(p, b);
+      *err |= x.s.err;
+      sum += C::tiles_per_head(p, x.s);
+      empty |= x.s.qn > 0 && C::tiles(p, x.s, 0) == 0;
     }
     long long before = sum;  // inclusive sums within the warp
 #pragma unroll
@@ -255,52 +277,57 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       const long long o = __shfl_up_sync(0xffffffffu, before, d);
       if (lane >= d) before += o;
     }
-    if (tid < 128 && lane == 31) w->sums[tid >> 5] = before;
-    S.some_empty = __syncthreads_or(empty) != 0;
     long long total = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < (tid >> 5)) before += w->sums[i];
-      total += w->sums[i];
+    if (small) {
+      S.some_empty = __any_sync(0xffffffffu, empty);
+      total = __shfl_sync(0xffffffffu, before, 31);
+    } else {
+      if (tid < 128 && lane == 31) w->sums[tid >> 5] = before;
+      S.some_empty = __syncthreads_or(empty) != 0;
+      for (int i = 0; i < 4; ++i) {
+        if (i < (tid >> 5)) before += w->sums[i];
+        total += w->sums[i];
+      }
     }
     before -= sum;
-    S.total = total * p.Hkv;
-    S.blocks = S.total < gridDim.x ? S.total : gridDim.x;
-    if (sched && blockIdx.x == 0 && tid < 128) {
+    if (sched && blockIdx.x == 0 && tid < (small ? 32 : 128)) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
         sched[b] = at;
         at += C::tiles_per_head(p, load_seq(p, b));
       }
-      if (tid == 127) sched[p.B] = total;
+      if (tid == 0) sched[p.B] = total;
     }
-    if (blockIdx.x >= S.blocks) return S;
-    S.first = first_tile(blockIdx.x, S.total, S.blocks);
-    S.n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, S.total, S.blocks) - S.first);
-    if (tid < 128 && S.first >= before * p.Hkv && S.first < (before + sum) * p.Hkv) {
-      long long at = S.first - before * p.Hkv;
-      for (int b = b0; b < b1; ++b) {
-        Cursor x;
-        x.b = b;
-        x.s = load_seq(p, b);
-        const long long per_head = C::tiles_per_head(p, x.s);
-        if (at < per_head * p.Hkv) {
-          x.h = static_cast<int>(quotient(at, per_head));
-          at -= x.h * per_head;
-          for (x.rt = 0;; ++x.rt) {
-            x.nt = C::tiles(p, x.s, x.rt);
-            if (at < x.nt) break;
-            at -= x.nt;
+    if (!S.set(total * p.Hkv)) return S;
+    const bool mine = (small || tid < 128) && S.first >= before * p.Hkv && S.first < (before + sum) * p.Hkv;
+    if (small) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      c.b = src;
+      c.s.q0 = __shfl_sync(0xffffffffu, x.s.q0, src);
+      c.s.qn = __shfl_sync(0xffffffffu, x.s.qn, src);
+      c.s.kv = __shfl_sync(0xffffffffu, x.s.kv, src);
+      c.s.err = 0;
+      sum = __shfl_sync(0xffffffffu, sum, src);
+      before = __shfl_sync(0xffffffffu, before, src);
+      locate<C>(p, c, S.first - before * p.Hkv, sum);
+    } else {
+      if (mine) {
+        long long at = S.first - before * p.Hkv;
+        for (int b = b0; b < b1; ++b) {
+          x.b = b;
+          x.s = load_seq(p, b);
+          const long long per_head = C::tiles_per_head(p, x.s);
+          if (at < per_head * p.Hkv) {
+            locate<C>(p, x, at, per_head);
+            w->start = x;
+            break;
           }
-          x.t = static_cast<int>(at);
-          w->start = x;
-          break;
+          at -= per_head * p.Hkv;
         }
-        at -= per_head * p.Hkv;
       }
+      __syncthreads();
+      c = w->start;
     }
-    __syncthreads();
-    c = w->start;
   }
   return S;
 }
