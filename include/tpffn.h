@@ -104,7 +104,9 @@ enum {
   TP_FLAG_DEBUG_SKIP_LOAD = 1 << 16  /* test hook: the first tensor-core GEMM
                              of the call never issues its first operand load,
                              so its consumer's bounded wait expires and the
-                             call reports TP_ERR_TIMEOUT (bf16 plans only)    */
+                             call reports TP_ERR_TIMEOUT (bf16 plans only);
+                             tp_attn_paged_fwd: its tensor-memory kernel (more
+                             than 32 query rows to a key head) does the same  */
 };
 
 /* ---------------------------------------------------------------- plans */

@@ -1504,6 +1504,7 @@ void kv_ctx(const tp_attn_plan* a, void* workspace, int flags, cudaStream_t stre
   ctx.stream = stream;
   ctx.err = static_cast<int*>(workspace);
   ctx.num_sms = num_sms_current();
+  ctx.debug_skip_load = (flags & TP_FLAG_DEBUG_SKIP_LOAD) ? 1 : 0;
   ctx.timing = (flags & TP_FLAG_TIMING) != 0;
   if (ctx.timing) {
     a->wo->timing_stream = stream;

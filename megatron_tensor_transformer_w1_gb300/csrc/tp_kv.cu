@@ -925,6 +925,7 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
   p.lse = lse;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kv::HD)));
   p.timeout_ns = ctx.timeout_ns;
+  p.skip_load = ctx.debug_skip_load;
   int rc = TP_OK;
   if (P.share) {
     p.part = c.shared = P.shared;

@@ -392,6 +392,7 @@ struct AttendParams {
   // when the call's inputs are there.  This kernel starts without waiting for
   // it, and waits before its blocks end.
   int beside;
+  int skip_load;           // test hook: block 0 never issues its first copy
   unsigned long long timeout_ns;
 };
 

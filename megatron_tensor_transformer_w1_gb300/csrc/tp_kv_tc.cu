@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         const int slot = i & (SLOTS - 1);
         const uint32_t ph = (i / SLOTS) & 1u;
         if (!W.warp(&empty[slot], ph ^ 1u)) { ok = false; break; }
+        if (p.skip_load && blockIdx.x == 0 && i == 0) continue;
         if (lane == 0) {
           if (kv == 0) info[n & 1] = what;
           mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(live * box) * HD * 2);

@@ -226,6 +226,121 @@ def test_many_rows_bad_batches():
     assert cache.last_device_error() == abi.TP_OK
 
 
+def test_many_rows_bounded_wait_expires_and_context_survives():
+    """A copy that is never issued: its waits run out, the call reports it, and the
+    next call is as ever."""
+    abi = _modules()[0]
+    s = ref.make_batch([80, 70, 200], [100, 60, 2000], 2, 16, seed=23)
+    cache, batch = _cache(s, 4, 2)
+    q = _q(s["n"], 4, 8)
+    good = cache.attend(q, batch)
+    with pytest.raises(Exception, match="TP_ERR_TIMEOUT"):
+        cache.attend(q, batch, flags=abi.TP_FLAG_DEBUG_SKIP_LOAD | abi.TP_FLAG_SYNC)
+    assert torch.equal(cache.attend(q, batch, flags=abi.TP_FLAG_SYNC), good)
+
+
+def test_calls_are_refused():
+    """Tensors of the wrong type, shape, layout or place."""
+    abi, Attention, KVBatch, Cache = _modules()
+    s = ref.make_batch([1, 2], [10, 20], 2, 16, seed=24, spare_rows=1)
+    cache, batch = _cache(s, 4, 2)
+    q, qkv = _q(s["n"], 4, 1), torch.zeros(s["n"], 8 * HD, dtype=torch.bfloat16, device="cuda")
+    wide = torch.zeros(s["n"], 1024, dtype=torch.bfloat16, device="cuda")
+    for bad in (q.float(), q[1:], q.cpu(), q.t().contiguous().t(), wide[:, :512]):
+        with pytest.raises(ValueError):
+            cache.attend(bad, batch)
+        with pytest.raises(ValueError):
+            cache.attend(q, batch, out=bad)
+        with pytest.raises(ValueError):
+            cache.append(qkv, batch, q=bad)
+    for bad in (qkv.float(), qkv[:-1], qkv.cpu(), wide[:, ::1][:, 1:]):
+        with pytest.raises(ValueError):
+            cache.append(bad, batch)
+    with pytest.raises(ValueError):
+        cache.attend(q, KVBatch(s["cu"].cpu(), s["kv_len"].cpu(), s["table"].cpu(), s["n"], 2))
+    for shared in (-1, s["table"].shape[1] * 16 + 1):
+        with pytest.raises(abi.TPFFNError):
+            cache.attend(q, batch, shared_len=shared)
+    attn = cache.attn
+    for kw in (dict(page_size=4), dict(page_size=24), dict(page_size=2048), dict(n_pages=0), dict(k=s["k"].float()),
+               dict(k=s["k"][:-1]), dict(v=s["v"].cpu()), dict(inv_freq=torch.ones(12, device="cuda")),
+               dict(inv_freq=torch.ones(72, device="cuda")), dict(inv_freq=torch.ones(64, device="cuda").double())):
+        args = dict(n_pages=s["n_pages"], page_size=16, k=s["k"], v=s["v"])
+        args.update(kw)
+        with pytest.raises(ValueError):
+            Cache(attn, **args)
+    other = Attention(256, 4, 2, HD, 2)
+    with pytest.raises(ValueError):
+        other.decode(wide[:, :256].contiguous(), cache, batch, None, None)
+
+
+def test_empty_calls():
+    """No new tokens, no sequences: no work, and the cache as it was."""
+    abi = _modules()[0]
+    s = ref.make_batch([1, 2], [10, 20], 2, 16, seed=25)
+    cache, _ = _cache(s, 4, 2)
+    k0 = s["k"].clone()
+    none = torch.zeros(0, 8 * HD, dtype=torch.bfloat16, device="cuda")
+    batch = cache.batch(torch.zeros(3, dtype=torch.int32, device="cuda"), s["kv_len"], s["table"], 0, 0)
+    q = cache.append(none, batch)
+    o, lse = cache.attend(q, batch, lse=True)
+    assert q.shape == o.shape == (0, 4 * HD) and lse.shape == (0, 4) and cache.last_device_error() == abi.TP_OK
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = cache.batch(torch.zeros(1, **i32), torch.zeros(0, **i32), torch.zeros(0, 3, **i32), 5, 1)
+    x = torch.full((5, 4 * HD), 3.0, dtype=torch.bfloat16, device="cuda")
+    cache.append(torch.zeros(5, 8 * HD, dtype=torch.bfloat16, device="cuda"), batch, q=x)
+    cache.attend(_q(5, 4, 1), batch, out=x)
+    assert (x == 3).all() and cache.last_device_error() == abi.TP_OK
+    assert torch.equal(k0.nan_to_num(), s["k"].nan_to_num())
+
+
+def test_rows_behind_the_last_sequence_in_a_replayed_graph():
+    """A graph for 8 sequences of at most 4 new tokens each, replayed with batches of fewer."""
+    s = ref.make_batch([4] * 8, [100] * 8, 2, 16, seed=26)
+    cache, batch = _cache(s, 8, 2)
+    q = _q(s["n"], 8, 9)
+    out = torch.zeros(s["n"], 8 * HD, dtype=torch.bfloat16, device="cuda")
+    cache.attend(q, batch, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(q, batch, out=out)
+    for new in ([4] * 8, [1] * 8, [0, 3, 0, 0, 1, 2, 0, 0], [0] * 8, [4, 1, 4, 1, 4, 1, 4, 1]):
+        s["new"] = new
+        s["lens"] = [50 + 7 * b + n for b, n in enumerate(new)]
+        s["cu"].copy_(torch.tensor([0] + new).cumsum(0))
+        s["kv_len"].copy_(torch.tensor(s["lens"]))
+        out.fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        rows = sum(new)
+        assert (out[rows:] == 5).all()
+        if rows:
+            check_attend(s, q, 8, out, None)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages far behind 2^31 elements of the cache."""
+    Hkv, page, H = 16, 64, 16
+    n_pages = 2 ** 31 // (Hkv * page * HD) + 40  # 4.3 GB each of keys and values
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.tensor([[n_pages - 1, 3, n_pages - 7]], **i32)
+    k, v = (torch.empty(n_pages, Hkv, page, HD, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(8)
+    for new in (1, 70):
+        s = dict(k=k, v=v, cu=torch.tensor([0, new], **i32), kv_len=torch.tensor([150], **i32), table=table, n=new,
+                 n_pages=n_pages, new=[new], lens=[150], max_new=new)
+        for p in table[0].tolist():
+            k[p].normal_(generator=g)
+            v[p].normal_(generator=g)
+        cache, batch = _cache(s, H, 4)
+        qkv = torch.randn(new, 48 * HD, generator=g, device="cuda").to(torch.bfloat16)
+        q = cache.append(qkv, batch)
+        _, kk, vv = ref.split_qkv(qkv, H, Hkv, 4)
+        assert torch.equal(k[n_pages - 7, :, 149 - 128], kk[-1]) and torch.equal(v[n_pages - 7, :, 149 - 128], vv[-1])
+        check_attend(s, q, H, *cache.attend(q, batch, lse=True))
+        assert cache.last_device_error() == 0
+
+
 def test_attend_rows_that_see_nothing():
     """More new tokens than keys (the first rows see none), and no keys at all."""
     s = ref.make_batch([3, 2, 4], [40, 0, 0], 2, 16, seed=5)
@@ -466,6 +581,30 @@ def test_decode_is_the_composition(new, ctx, shared, fused):
     assert rel <= 2 * U, rel.item()
     new_k = (c0.k.double() - c1.k.double()).nan_to_num().abs()
     assert (new_k <= 2 * U * c1.k.double().nan_to_num().abs() + 2.0 ** -16).all()
+
+
+def test_decode_in_a_graph_and_with_the_overlapped_sum():
+    abi, Attention, _, Cache = _modules()
+    H, Hkv, T, d = 8, 2, 2, 512
+    s = ref.make_batch([1, 3, 2, 40], [100, 0, 30, 7], Hkv, 16, seed=52, junk=0.0)
+    attn = Attention(d, H, Hkv, HD, T)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = lambda *sh: (torch.randn(*sh, generator=g, device="cuda") / math.sqrt(sh[1])).to(torch.bfloat16)
+    wqkv, wo = attn.pack(w(H * HD, d), w(Hkv * HD, d), w(Hkv * HD, d), w(d, H * HD))
+    x = torch.randn(s["n"], d, generator=g, device="cuda").to(torch.bfloat16)
+    cache = Cache(attn, s["n_pages"], 16, k=s["k"], v=s["v"], inv_freq=1e4 ** (-torch.arange(64, device="cuda") / 64))
+    batch = cache.batch(s["cu"], s["kv_len"], s["table"], s["n"], s["max_new"])
+    y = attn.decode(x, cache, batch, wqkv, wo)
+    assert torch.equal(attn.decode(x, cache, batch, wqkv, wo, overlap=True), y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = attn.decode(x, cache, batch, wqkv, wo)
+    for _ in range(2):
+        held.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, y)
+    assert cache.last_device_error() == abi.TP_OK
 
 
 def test_decode_matches_the_training_forward():
