@@ -394,16 +394,24 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
         const bool last = cur & I_LAST, active = t == 0 || (cur & I_TWO);
         const int steps = cur & I_STEPS;
-        if (!(ok = wait_tile(2u * n + 1) && (last || wait_tile(2u * n + 2)))) break;
-        const uint32_t next = last ? 0 : info[(n + 1) & 1];
+        if (!(ok = wait_tile(2u * n + 1))) break;
+        uint32_t next = 0;
         if (active) {
-          const int n_next = last ? 0 : halves(next);
+          int n_next = 0;
 #pragma unroll 1
           for (int j = 0; j < halves(cur); ++j) {
             if (!(ok = issue_pv(n, j, first && j == 0, min(4, steps - 4 * j)))) break;
+            if (j == 0 && !last) {
+              if (!(ok = wait_tile(2u * n + 2))) break;
+              next = info[(n + 1) & 1];
+              n_next = halves(next);
+            }
             if (j < n_next) issue_s(n + 1, j, (next & I_LAST) && j + 1 == n_next);
           }
           if (!ok) break;
+        } else if (!last) {
+          if (!(ok = wait_tile(2u * n + 2))) break;
+          next = info[(n + 1) & 1];
         }
         release(2u * n + 1, active);
         if (!last) release(2u * n + 2, active);
