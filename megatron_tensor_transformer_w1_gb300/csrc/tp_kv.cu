@@ -948,12 +948,17 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
   c.alone = alone;
   // All eight warps of a block at work, and few rows on more blocks than one:
   // at most two blocks of 256 threads per SM before a warp has a row to itself.
-  const int rows = P.own.slot_rows;
+  // A block goes through the rows of an item in strides: 16 blocks per SM are
+  // enough, and blocks that find nothing to do cost a launch each (39000 of
+  // them 30 us).
+  const int64_t item_rows = static_cast<int64_t>(a.max_new) * (a.H / a.Hkv);
+  const int rows = static_cast<int>(item_rows < P.own.slot_rows ? item_rows : P.own.slot_rows);
   const int64_t all = static_cast<int64_t>(a.n_tokens) * a.H;
   c.rows_per_pass = 8;
   while (c.rows_per_pass > 1 && (c.rows_per_pass >= 2 * rows || all < 2 * c.rows_per_pass * ctx.num_sms))
     c.rows_per_pass /= 2;
-  const dim3 grid(P.items, (rows + c.rows_per_pass - 1) / c.rows_per_pass);
+  const int passes = (rows + c.rows_per_pass - 1) / c.rows_per_pass, most = 16 * ctx.num_sms / P.items;
+  const dim3 grid(P.items, most < 1 ? 1 : (passes < most ? passes : most));
   if (ctx.before) ctx.before(ctx.user, "kv_combine", ctx.stream);
   if (P.share)
     kv::launch_dep(kv::kv_combine_kernel<true>, grid, 256, 0, ctx.stream, c);
