@@ -286,9 +286,9 @@ struct Waiter {
 // of bounds.  Returns 0 or a TP_ERR_* code.
 int encode_map_3d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[3], const uint64_t strides_bytes[2],
                        const uint32_t box[3]);
-// The same in four dimensions.
-int encode_map_4d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[4], const uint64_t strides_bytes[3],
-                       const uint32_t box[4]);
+// The same in five dimensions.
+int encode_map_5d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[5], const uint64_t strides_bytes[4],
+                       const uint32_t box[5]);
 
 }  // namespace tc
 }  // namespace tpffn

@@ -1469,7 +1469,7 @@ int kv_spec(const tp_attn_plan* a, const tp_kv_cache* c, const tp_kv_batch* b, i
   int rc = kv_sizes(a, b, c->page_size, shared_len, sp);
   if (rc || sp.n_tokens == 0 || sp.n_seqs == 0) return rc;
   if (!c->k || !c->v || c->n_pages < 1 || !b->cu_tokens || !b->kv_len || !b->page_table) return TP_ERR_INVALID;
-  if (c->n_pages > INT32_MAX) return TP_ERR_UNSUPPORTED;
+  if (c->n_pages > INT32_MAX / a->Hkv) return TP_ERR_UNSUPPORTED;  // (a coordinate of the copies)
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(b->cu_tokens) || !aligned4(b->kv_len) ||
       !aligned4(b->page_table))
     return TP_ERR_ALIGN;

@@ -1553,17 +1553,22 @@ int encode_map_3d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[3], 
   return r == CUDA_SUCCESS ? 0 : TP_ERR_CUDA;
 }
 
-int encode_map_4d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[4], const uint64_t strides_bytes[3],
-                       const uint32_t box[4]) {
+int encode_map_5d_bf16(CUtensorMap* m, const void* ptr, const uint64_t dims[5], const uint64_t strides_bytes[4],
+                       const uint32_t box[5]) {
   if (reinterpret_cast<uintptr_t>(ptr) % 16) return TP_ERR_ALIGN;
-  for (int i = 0; i < 3; ++i)
-    if (strides_bytes[i] % 16) return TP_ERR_ALIGN;
   EncodeTiledFn fn = encode_fn();
   if (!fn) return TP_ERR_CUDA;
-  cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
-  cuuint64_t st[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
-  cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]}, estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), d, st, bx, estr,
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], estr[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < 5; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i < 4) {
+      if (strides_bytes[i] % 16) return TP_ERR_ALIGN;
+      st[i] = strides_bytes[i];
+    }
+  }
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), d, st, bx, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : TP_ERR_CUDA;

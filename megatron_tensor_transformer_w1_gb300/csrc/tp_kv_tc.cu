@@ -14,8 +14,8 @@
 // products a step of two row tiles, 2048 cycles at 4096 a cycle.  The two
 // row tiles take turns: while one tile's scores go through the softmax, the
 // products of the other run.  A block has
-//  * warp 0: copies K and V tiles by TMA, page by page (box: 64 columns by a
-//    page, or 128 keys of a longer one), into a ring of four 32 KB slots;
+//  * warp 0: copies K and V tiles by TMA, a copy for each page (or 128 keys of
+//    a longer one), into a ring of four 32 KB slots;
 //  * warps 1 and 2: a lane of each issues tcgen05.mma for row tile t = 0, 1:
 //    S_t = Q_t K^T into tensor memory, then O_t += P_t V with P_t, in bf16,
 //    over the S_t it came from.  Products run in the order of issue, so the
@@ -65,6 +65,23 @@ constexpr int M_SMEM = M_BAR + 512 + 1024;
 static_assert(M_SMEM <= 232448, "shared memory per block");
 static_assert(sizeof(SchedScratch) <= 8 * 4096, "the schedule's scratch lies where the output is staged");
 
+// A K or V tile in shared memory: groups of 8 keys, 2 KB each, the columns
+// 0-63 of the group's keys and then 64-127 in 128-byte swizzled rows.  So a
+// page of any size is one box of the tensor map {64 columns, 8 keys, 2 column
+// halves, groups of a page, heads and pages}; with the column halves 16 KB
+// apart a page takes two.
+constexpr uint32_t GROUP = 2048, COL_HALF = 1024;
+// The products' operands: K, keys by columns (step ks: columns 16 ks ..), and
+// V, its columns along N (step ks: keys 16 ks ..).
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(GROUP >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// 16-byte chunk c (of 16) of key r.
+__device__ __forceinline__ uint32_t key_chunk(uint32_t tile, int r, int c) {
+  return tile + (r >> 3) * GROUP + (c >> 3) * COL_HALF + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
 template <bool PREFIX>
 using Many = Cut<PREFIX, BK, RT_MANY>;
 
@@ -84,6 +101,14 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* tm, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;
@@ -299,11 +324,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         __syncwarp();
         last_phase[slot] = static_cast<int>(ph);
         if (lane < live) {
-          uint8_t* dst = ring(i) + lane * box * 128;
-          const CUtensorMap* tm = kv ? &tv : &tk;
-          const int at = key & (page_keys - 1);
-          tma_load_4d(dst, tm, &full[slot], 0, at, h, page);
-          tma_load_4d(dst + TILE_BYTES / 2, tm, &full[slot], 64, at, h, page);
+          tma_load_5d(ring(i) + lane * box * (HD * 2), kv ? &tv : &tk, &full[slot], 0, 0, 0,
+                      (key & (page_keys - 1)) >> 3, page * B.Hkv + h);
         }
       }
     }
@@ -325,17 +347,18 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       // a product takes 32 to 64 cycles.
       const bool leader = elect_one();
       const uint64_t q_desc = kdesc(smem_u32(smem + M_Q + t * TILE_BYTES), 128, 0),
-                     k_desc = kdesc(smem_u32(smem + M_RING), 128, 0), v_desc = mndesc(smem_u32(smem + M_RING), 128, 0);
+                     k_desc = tile_desc(smem_u32(smem + M_RING), 16), v_desc = tile_desc(smem_u32(smem + M_RING), COL_HALF);
       // S_t of half j of the n-th tile
       auto issue_s = [&](int n, int j, bool seg_ends) {
         const uint32_t buf = s_cnt++ & 1u;
-        const uint64_t kd = k_desc + static_cast<uint64_t>(((2u * n) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * (SK * 128 >> 4));
+        const uint64_t kd = k_desc + static_cast<uint64_t>(((2u * n) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * (SK / 8 * GROUP >> 4));
         const uint32_t sd = tmem + t * 128 + buf * SK;
         if (leader) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
-            const uint64_t step = ((ks >> 2) * 128 * 128 + (ks & 3) * 32) >> 4;
-            umma_bf16(sd, q_desc + step, kd + step, ID_S, ks > 0 ? 1u : 0u);
+            const uint64_t q_step = ((ks >> 2) * 128 * 128 + (ks & 3) * 32) >> 4,
+                           k_step = ((ks >> 2) * COL_HALF + (ks & 3) * 32) >> 4;
+            umma_bf16(sd, q_desc + q_step, kd + k_step, ID_S, ks > 0 ? 1u : 0u);
           }
           umma_commit(&s_full[2 * t + buf]);
           if (seg_ends) umma_commit(&q_empty[t]);
@@ -348,17 +371,17 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         if (!W.warp(&p_full[2 * t + buf], (p_cnt >> 1) & 1u)) return false;
         ++p_cnt;
         tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint64_t>(((2u * n + 1) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * 512);
+        const uint64_t vd = v_desc + static_cast<uint64_t>(((2u * n + 1) & (SLOTS - 1)) * (TILE_BYTES >> 4) + j * (SK / 8 * GROUP >> 4));
         const uint32_t od = tmem + 256 + t * 128, pd = tmem + t * 128 + buf * SK;
         if (leader) {
           if (steps == 4) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_bf16_ta(od, pd + ks * 8, vd + static_cast<uint64_t>(ks * 128), ID_PV, ks > 0 ? 1u : (first ? 0u : 1u));
+              umma_bf16_ta(od, pd + ks * 8, vd + static_cast<uint64_t>(ks * (2 * GROUP >> 4)), ID_PV, ks > 0 ? 1u : (first ? 0u : 1u));
           } else {
 #pragma unroll 1
             for (int ks = 0; ks < steps; ++ks)
-              umma_bf16_ta(od, pd + ks * 8, vd + static_cast<uint64_t>(ks * 128), ID_PV, ks > 0 ? 1u : (first ? 0u : 1u));
+              umma_bf16_ta(od, pd + ks * 8, vd + static_cast<uint64_t>(ks * (2 * GROUP >> 4)), ID_PV, ks > 0 ? 1u : (first ? 0u : 1u));
           }
           umma_commit(&pv_done[2 * t + buf]);
         }
@@ -565,7 +588,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             if (!W.warp(&full[i & (SLOTS - 1)], (i / SLOTS) & 1u)) { ok = false; break; }
             const uint32_t vs = smem_u32(ring(i));
             const int tid = threadIdx.x & 127, bad = 16 - (keys & 15);
-            for (int k = tid; k < bad * 16; k += 128) st_shared_v4(sw_chunk(vs, 128, keys + (k >> 4), k & 15), 0, 0, 0, 0);
+            for (int k = tid; k < bad * 16; k += 128) st_shared_v4(key_chunk(vs, keys + (k >> 4), k & 15), 0, 0, 0, 0);
             fence_proxy_async_smem();
           }
           tc_fence_before();
@@ -660,10 +683,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
 namespace {
 int map_pages(CUtensorMap* m, const void* ptr, const Batch& b) {
   const uint64_t page = 1ull << b.page_shift;
-  const uint64_t dims[4] = {HD, page, static_cast<uint64_t>(b.Hkv), static_cast<uint64_t>(b.n_pages)};
-  const uint64_t str[3] = {HD * 2, page * HD * 2, page * HD * 2 * static_cast<uint64_t>(b.Hkv)};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(page < BK ? page : BK), 1, 1};
-  return encode_map_4d_bf16(m, ptr, dims, str, box);
+  const uint64_t dims[5] = {64, 8, 2, page / 8, static_cast<uint64_t>(b.Hkv) * static_cast<uint64_t>(b.n_pages)};
+  const uint64_t str[4] = {HD * 2, 128, 8 * HD * 2, page * HD * 2};
+  const uint32_t box[5] = {64, 8, 2, static_cast<uint32_t>((page < BK ? page : BK) / 8), 1};
+  return encode_map_5d_bf16(m, ptr, dims, str, box);
 }
 
 template <bool PREFIX>
