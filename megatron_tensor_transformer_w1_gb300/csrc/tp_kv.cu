@@ -598,6 +598,7 @@ struct ItemParts {
   int second = 0;        // the first part lies in its block's second slot
   long long c0 = 0;
   __device__ __forceinline__ void set(const Parts& P, long long start, long long nt, long long total) {
+    if (start < 0 || nt <= 0 || start + nt > total) return;  // no list that the kernels cut: no parts
     const long long C = total < P.grid ? total : P.grid;
     c0 = block_of_tile(start, total, C);
     n = static_cast<int>(block_of_tile(start + nt - 1, total, C) - c0) + 1;
@@ -644,15 +645,19 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     const int u = blockIdx.x / B.Hkv;
     int b = u;
     if (p.own.rt) {
-      int lo = 0, hi = B.B;
+      // the last b with first(b) <= u, 32 places to a round
       auto first = [&](int x) {
         return min(max(B.cu[x], 0), B.n_tokens) * static_cast<long long>(B.G) / p.own.rt + x;
       };
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first(mid) <= u) lo = mid; else hi = mid;
+      int n = B.B;  // b lies in [lo, lo + n)
+      b = 0;
+      while (n > 1) {
+        const int step = (n + 31) >> 5, at = lane * step;
+        const int cnt = __popc(__ballot_sync(0xffffffffu, at < n && first(b + at) <= u));
+        const int skip = max(cnt - 1, 0) * step;
+        b += skip;
+        n = min(step, n - skip);
       }
-      b = lo;
       rt = static_cast<int>(u - first(b));
     }
     const Seq s = load_seq(B, b);
@@ -660,7 +665,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     nt_sh = p.shared.sched[0];
     n_rt_sh = p.shared.sched[1];
     q0 = s.q0;
-    rows = min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
+    rows = rt < 0 ? 0 : min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
     long long nt = per_head, pre = 0;
     if (p.own.rt) {
       using C = Cut<false, 128, RT_MANY>;
@@ -697,6 +702,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
       if (SHARED && nt_sh > 0) {
         const int all = tok * B.G + g, srt = p.shared.rt ? all / p.shared.rt : 0;
         r_sh = all - srt * p.shared.rt;
+        sh.n = 0;
         sh.set(p.shared, (h * n_rt_sh + srt) * nt_sh, nt_sh, nt_sh * n_rt_sh * B.Hkv);
       }
       const int n = own.n + sh.n;

@@ -312,6 +312,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       locate<C>(p, c, S.first - before * p.Hkv, sum);
     } else {
       if (mine) {
+        w->start = Cursor{p.B - 1, 0, 0, 0, 1, Seq{}};  // see advance()
         long long at = S.first - before * p.Hkv;
         for (int b = b0; b < b1; ++b) {
           x.b = b;

@@ -109,7 +109,7 @@ class PagedKVCache:
         return t
 
     def _workspace(self, batch, shared_len, call, flags, stream):
-        key = (self.attn.plan, self.page_size, shared_len, call, flags)
+        key = (self.attn, self.page_size, shared_len, call, flags)
         need = batch._bytes.get(key)
         if need is None:
             need = max(16, abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call,

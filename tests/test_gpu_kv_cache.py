@@ -182,6 +182,34 @@ def test_attend_shared_keys_of_idle_sequences():
     assert cache.last_device_error() == _modules()[0].TP_ERR_BATCH and torch.isfinite(o).all()
 
 
+def test_attend_shared_keys_bad_offsets():
+    """Offsets that descend, or begin behind the first row, leave rows that the shared
+    keys' work does not cover: nothing is read for them, and the call reports it."""
+    abi = _modules()[0]
+    B, Hkv, H = 5, 8, 64
+    s = ref.make_batch([40] * B, [3] * B, Hkv, 64, shared=6400, seed=26)
+    assert (B - 1) * 6400 * Hkv * 512 >= 96 << 20
+    cache, batch = _cache(s, H, 8)
+    q = _q(s["n"], H, 12)
+    good = cache.attend(q, batch, shared_len=6400)
+    assert cache.last_device_error() == abi.TP_OK
+    check_attend(s, q, H, good, None)
+    keep = s["cu"].clone()
+    for bad in ([0, 40, 80, 120, 160, 3], [0, 40, 80, 120, 160, 0], [0, 200, 3, 120, 2, 1], [0, -7, 80, 120, 160, 200]):
+        s["cu"].copy_(torch.tensor(bad))
+        assert torch.isfinite(cache.attend(q, batch, shared_len=6400, out=torch.zeros_like(good))).all()
+        assert cache.last_device_error() == abi.TP_ERR_BATCH
+    s["cu"].copy_(keep)
+    s["cu"][0] = 33  # the first sequence's last seven rows; those before are nobody's
+    o = torch.full_like(good, 7.0)
+    cache.attend(q, batch, shared_len=6400, out=o)
+    assert (o[:33] == 7).all()
+    check_attend(dict(s, new=[7] + [40] * 4, cu=s["cu"] - 33), q[33:], H, o[33:], None)
+    s["cu"].copy_(keep)
+    assert torch.equal(cache.attend(q, batch, shared_len=6400), good)
+    assert cache.last_device_error() == abi.TP_OK
+
+
 def test_attend_many_rows_that_see_nothing():
     """A prompt cut off by kv_len: its first rows see no key, whole row tiles among them."""
     s = ref.make_batch([600, 70, 80], [0, 0, 10], 1, 16, seed=15)
