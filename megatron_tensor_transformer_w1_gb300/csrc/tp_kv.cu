@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   grid_dep_launch();
   int err = 0;
   Cursor c;
-  const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem), c, &err);
+  const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem), c, &err, p.part.early,
+                                      p.part.lead);
   __syncthreads();
   const int n_tiles = S.n_tiles, t0 = C::t0(B), lo = C::first_key(B);
   if (n_tiles == 0) {
@@ -599,10 +600,10 @@ struct ItemParts {
   long long c0 = 0;
   __device__ __forceinline__ void set(const Parts& P, long long start, long long nt, long long total) {
     if (start < 0 || nt <= 0 || start + nt > total) return;  // no list that the kernels cut: no parts
-    const long long C = total < P.grid ? total : P.grid;
-    c0 = block_of_tile(start, total, C);
-    n = static_cast<int>(block_of_tile(start + nt - 1, total, C) - c0) + 1;
-    second = start != first_tile(c0, total, C);
+    const Deal D(total, P.grid, P.early, P.lead);
+    c0 = D.block_of(start);
+    n = static_cast<int>(D.block_of(start + nt - 1) - c0) + 1;
+    second = start != D.first(c0);
   }
   // the slot of part i
   __device__ __forceinline__ long long slot(int i) const { return 2 * (c0 + i) + (i == 0 ? second : 0); }
@@ -866,8 +867,9 @@ constexpr int kFewRows = 32;
 constexpr int kShareRows = 64;
 // At least so many bytes of shared keys and values that would be read again.
 // Single tokens, 8 key heads, 300 own keys each, together / each on its own: 64
-// sequences behind 1024 keys (264 MB saved) 44 / 55 us, 8 behind 4096 (117 MB)
-// 25 / 30 us, 64 behind 256 (66 MB) 37 / 30 us, 4 behind 4096 (50 MB) 25 / 20 us.
+// sequences behind 1024 keys (264 MB saved) 31 / 48 us, 8 behind 4096 (117 MB)
+// 22 / 26 us, 64 behind 256 (66 MB) 27 / 28 us, 4 behind 4096 (50 MB) 21 / 19 us;
+// with more own rows, where the two kernels run in turn, it is even at 90 MB.
 constexpr double kShareBytes = 96 << 20;
 struct AttendPlan {
   bool share = false;
@@ -875,6 +877,32 @@ struct AttendPlan {
   int items = 0;              // that the combine kernel looks at
   size_t bytes = 0;
 };
+// The shared keys' kernel of many rows and the own keys' of few rows, side by
+// side: the first on just so many SMs that both end together, by what they were
+// measured to take.  The own keys' lengths are the device's to know: a short
+// item, of two tiles, is assumed; of longer ones the blocks that start at once
+// take what they can in the meantime (Deal).  In turn / side by side: 64
+// sequences of one token, 4 rows to a key head, 8 key heads, 8192 shared keys
+// and 16 to 1024 own ones 53 / 42 us, 4000 own 190 / 179, none 36 / 35, 1024
+// shared and 300 own 37 / 27; 128 sequences, 2048 shared and 100 own 42 / 44.
+void split_sms(const KvSpec& a, int num_sms, AttendPlan& P) {
+  const int64_t rows = static_cast<int64_t>(a.n_tokens) * (a.H / a.Hkv);
+  const int64_t tiles = a.Hkv * ((rows + kv::RT_MANY - 1) / kv::RT_MANY) * ((a.shared_len + 127) / 128);
+  const double step = rows > 128 ? 1.8 : 1.2;  // us per 128 keys, with two row tiles or one
+  auto shared_us = [&](int64_t sms) { return 9.0 + step * ((tiles + sms - 1) / sms); };
+  auto own_us = [&](int64_t sms) { return 8.0 + 5.3 * a.n_seqs * a.Hkv / kv::few_blocks(static_cast<int>(sms)); };
+  double best = shared_us(num_sms) + own_us(num_sms) - 6.0;  // in turn; the second's start is hidden
+  for (int64_t n = 1; n <= 64; ++n) {
+    const int64_t sms = (tiles + n - 1) / n;  // with n tiles each
+    if (sms >= num_sms) continue;
+    const double s = shared_us(sms), o = own_us(num_sms - sms), us = s > o ? s : o;
+    if (us >= best) continue;
+    best = us;
+    P.shared.grid = static_cast<int>(sms);
+    P.own.early = kv::few_blocks(static_cast<int>(num_sms - sms));
+    P.own.lead = static_cast<int>(s / 1.2);  // 64 keys of an item take a block that long
+  }
+}
 AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
   AttendPlan P;
   const int64_t G = a.H / a.Hkv, rows = static_cast<int64_t>(a.n_tokens) * a.H;
@@ -909,6 +937,7 @@ AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
   P.share = saved >= kShareBytes && a.n_tokens * G <= static_cast<int64_t>(kShareRows) * a.n_seqs;
   part(P.own, a.max_new * G, static_cast<size_t>(a.n_seqs) + 1);
   if (P.share) part(P.shared, a.n_tokens * G, 2);
+  if (P.share && P.shared.rt && !P.own.rt) split_sms(a, num_sms, P);
   const int64_t units = P.own.rt ? a.n_tokens * G / kv::RT_MANY + a.n_seqs : a.n_seqs;
   P.items = P.share ? static_cast<int>(units * a.Hkv) : P.own.grid;
   P.bytes = off;

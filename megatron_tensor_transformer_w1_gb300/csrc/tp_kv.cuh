@@ -93,7 +93,8 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int row) {
 //
 // Block c of C takes the tiles [c T / C, (c + 1) T / C), whatever items they
 // belong to; a run of tiles of one item in one block is a segment.  Every
-// block gets the same number of tiles however the lengths differ.
+// block gets the same number of tiles however the lengths differ (but see
+// Deal).
 
 // (A 64-bit division takes some hundred cycles, and several in a row are felt.)
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -103,6 +104,33 @@ __device__ __forceinline__ long long first_tile(long long c, long long T, long l
 __device__ __forceinline__ long long block_of_tile(long long t, long long T, long long C) {
   return quotient((t + 1) * C - 1, T);
 }
+
+// How T tiles fall to `grid` blocks: the first E share Te tiles evenly, the L
+// behind them the rest.  Where the first `early` blocks start while the SMs of
+// the others are still busy, for as long as a block takes for `lead` tiles,
+// they get so many more; otherwise (early = 0) all get the same.  No block of
+// the E + L is without a tile.
+struct Deal {
+  long long T, Te;
+  int E, L;
+  __device__ __forceinline__ Deal(long long T_, int grid, int early, int lead) : T(T_), Te(T_), L(0) {
+    const long long ahead = static_cast<long long>(early) * lead;
+    E = early && T <= ahead ? early : grid;
+    if (early && T > ahead) {
+      const long long late = quotient((T - ahead) * (grid - early), grid);
+      Te = T - late;
+      E = early;
+      L = static_cast<int>(late < grid - early ? late : grid - early);
+    }
+    if (T < E) E = static_cast<int>(T);
+  }
+  __device__ __forceinline__ long long first(long long c) const {
+    return c <= E ? first_tile(c, Te, E) : Te + first_tile(c - E, T - Te, L);
+  }
+  __device__ __forceinline__ long long block_of(long long t) const {
+    return t < Te ? block_of_tile(t, Te, E) : E + block_of_tile(t - Te, T - Te, L);
+  }
+};
 
 template <bool PREFIX, int KTILE, int RT>
 struct Cut {
@@ -176,12 +204,13 @@ struct Sched {
   bool some_empty = false; // there are rows of sequences that belong to no tile
   long long first = 0, total = 0, blocks = 0;
   // this block's share of `total_` tiles; false: none
-  __device__ __forceinline__ bool set(long long total_) {
+  __device__ __forceinline__ bool set(long long total_, int early, int lead) {
+    const Deal D(total_, gridDim.x, early, lead);
     total = total_;
-    blocks = total < gridDim.x ? total : gridDim.x;
+    blocks = D.E + D.L;
     if (blockIdx.x >= blocks) return false;
-    first = first_tile(blockIdx.x, total, blocks);
-    n_tiles = static_cast<int>(first_tile(blockIdx.x + 1, total, blocks) - first);
+    first = D.first(blockIdx.x);
+    n_tiles = static_cast<int>(D.first(blockIdx.x + 1) - first);
     return true;
   }
 };
@@ -207,7 +236,8 @@ __device__ __forceinline__ void locate(const Batch& p, Cursor& x, long long at, 
 // sequence, without meeting the others: a call of few tokens waits for this
 // before its first copy.
 template <typename C, bool PREFIX>
-__device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, SchedScratch* w, Cursor& c, int* err) {
+__device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, SchedScratch* w, Cursor& c, int* err,
+                                          int early = 0, int lead = 0) {
   const int tid = threadIdx.x, lane = tid & 31;
   const bool small = p.B <= 32;
   Sched S;
@@ -254,7 +284,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       sched[0] = c.nt;
       sched[1] = n_rt;
     }
-    if (!S.set(static_cast<long long>(n_rt) * c.nt * p.Hkv)) return S;
+    if (!S.set(static_cast<long long>(n_rt) * c.nt * p.Hkv, 0, 0)) return S;
     const long long item = quotient(S.first, c.nt);
     c.t = static_cast<int>(S.first - item * c.nt);
     c.h = static_cast<int>(quotient(item, n_rt));
@@ -298,7 +328,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       }
       if (tid == 0) sched[p.B] = total;
     }
-    if (!S.set(total * p.Hkv)) return S;
+    if (!S.set(total * p.Hkv, early, lead)) return S;
     const bool mine = (small || tid < 128) && S.first >= before * p.Hkv && S.first < (before + sum) * p.Hkv;
     if (small) {
       const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
@@ -358,6 +388,7 @@ struct Parts {
   long long* sched = nullptr; // null: the splits say all
   Split* split = nullptr;     // [blocks]
   int slot_rows = 0, grid = 0, rt = 0;  // rt: rows of a row tile, 0: all
+  int early = 0, lead = 0;              // see Deal
 };
 
 // Chunk c (of 32, four columns each) of row r of a slot.
@@ -366,6 +397,7 @@ __device__ __forceinline__ long long slot_chunk(const Parts& P, long long slot, 
 }
 
 // The note on a block's last segment: tile x of the list is its last one.
+// (Where all blocks get the same number of tiles.)
 __device__ __forceinline__ Split split_of(const Batch& p, const Sched& S, const Cursor& x, int seg_t, bool second) {
   Split r{};
   const long long end = S.first + S.n_tiles + (x.nt - x.t - 1);  // the item's

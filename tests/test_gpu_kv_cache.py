@@ -139,6 +139,9 @@ SHARED = [  # shared keys worth taking together: (sequences - 1) x keys x key he
     ([1] * 70, [3] * 70, 10, 2, 1, 1024, 1500, False),                        # groups of five
     ([200] + [1] * 59, [3] * 60, 2, 2, 2, 64, 1700, True),                    # a prompt among single tokens
     ([9, 1] * 10, [0] * 20, 40, 5, 5, 8, 2100, True),                         # no own context; own rows: many
+    ([1] * 9, [0] * 9, 32, 8, 8, 64, 4000, True),                             # fewer own tiles than blocks
+    ([1] * 20, [(701 * i) % 7000 for i in range(20)], 32, 8, 8, 32, 1300, True),  # long own keys, ragged
+    ([2] * 33, [(97 * i) % 900 for i in range(33)], 64, 16, 4, 16, 500, False),   # short shared keys
 ]
 
 
