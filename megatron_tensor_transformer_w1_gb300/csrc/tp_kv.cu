@@ -202,7 +202,11 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 // asynchronous copies, so that two blocks per SM keep some 128 KB in flight.
 // 4 / WR key groups of warps: a warp takes 16 query rows and 16 WR keys of a
 // tile with its own running maximum and sum (no exchange per tile); the groups
-// meet at the end of a segment.  The products are m16n8k16 matrix
+// meet at the end of a segment, where few instructions count: with a warp or
+// two per scheduler each takes some four cycles, and short sequences end a
+// segment every few tiles (a row to a warp, no division, rows that there are
+// not left out: 3900 -> 2000 cycles a segment; 7 sequences of 100 to 5000 keys
+// 19 -> 17 us).  The products are m16n8k16 matrix
 // instructions on registers: for so few rows they take less time than the
 // bytes do, and the 128-row tensor-memory products would be mostly empty.
 // WR = 2 has two stages: three would leave room for one block per SM (32
@@ -252,6 +256,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 // 16-byte chunk c of row r of a tile with 256-byte rows: eight rows' chunks
 // of one column fall into different banks
 __device__ __forceinline__ uint32_t tile_chunk(uint32_t tile, int r, int c) {
@@ -263,13 +278,16 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   using F = Few<WR>;
   using C = Cut<PREFIX, KT, 0>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ float2 s_ml[4][16];
   __shared__ Cursor s_cur[F::STAGES];
   __shared__ int s_err;
   const Batch& B = p.b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rg = warp / F::WK, kg = warp % F::WK;
+  // row / G for rows below 32, without a division (some thirty instructions)
+  const uint32_t g_inv = (65536u + B.G - 1) / B.G;
+  auto token_of = [&](int r) { return static_cast<int>(r * g_inv >> 16); };
   if (tid == 0) s_err = 0;
   if (!p.beside) grid_dep_wait();
   grid_dep_launch();
@@ -321,6 +339,17 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
         cp_async16(ks + at + i * 2048, k + i * 8 * HD);
         cp_async16(vs + at + i * 2048, v + i * 8 * HD);
       }
+    } else if (B.page_shift >= 6) {
+      const long long off =
+          (((static_cast<long long>(max(page, 0)) * B.Hkv + x.h) << B.page_shift) + (first & mask) + r0) * HD + ch * 8;
+      const __nv_bfloat16 *k = B.k + off, *v = B.v + off;
+      const uint32_t at = tile_chunk(0, r0, ch);
+      const int from = lo - first - r0, to = page >= 0 ? x.s.kv - first - r0 : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cp_async16(ks + at + i * 2048, k + i * 8 * HD, 8 * i >= from && 8 * i < to);
+        cp_async16(vs + at + i * 2048, v + i * 8 * HD, 8 * i >= from && 8 * i < to);
+      }
     } else {
       const long long head = (static_cast<long long>(x.h) << B.page_shift) * HD + ch * 8;
       const uint32_t at = tile_chunk(0, r0, ch);
@@ -340,7 +369,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
       for (int i = 0; i < 2 * WR; ++i) {
         const int r = r0 + 8 * i;
         const bool ok = r < rows;
-        const int tok = ok ? r / B.G : 0, g = ok ? r - tok * B.G : 0;
+        const int tok = ok ? token_of(r) : 0, g = ok ? r - tok * B.G : 0;
         const long long off =
             ok ? (static_cast<long long>(x.s.q0 + tok) * B.H + x.h * B.G + g) * HD + ch * 8 : 0;
         cp_async16(tile_chunk(qs, r, ch), p.q + off, ok);
@@ -400,7 +429,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
         const int r = rg * 16 + (lane >> 2) + 8 * e;
         limit[e] = 0;
         if (r < rows) {
-          const int tok = r / B.G;
+          const int tok = token_of(r);
           if (PREFIX && S.all_see) {
             limit[e] = x.s.kv;
           } else if (PREFIX) {
@@ -504,65 +533,56 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
       if ((lane & 3) == 0) s_ml[warp][(lane >> 2) + 8 * e] = make_float2(m[e], l[e]);
     }
     __syncthreads();  // everybody is done with this tile's K and V: they become the meeting place
-    float* meet = reinterpret_cast<float*>(smem + stage * F::STAGE);  // [4 warps][16 rows][HD]
+    const uint32_t meet = smem_u32(smem + stage * F::STAGE);  // [4 warps][16 rows][HD]
+    {
+      // a row's groups of 8 columns are exchanged by the row, so that a store's
+      // eight rows use different banks; rows behind the last are not read
+      const uint32_t at = meet + (warp * 16 + (lane >> 2)) * (HD * 4) + ((lane >> 2) << 5) + ((lane & 3) << 3);
+      if (rg * 16 < rows) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int col = j * 8 + (lane & 3) * 2, r = lane >> 2;
-      // rows are shifted against each other so that a store's eight rows use different banks
-      *reinterpret_cast<float2*>(meet + (warp * 16 + r) * HD + ((col + 8 * (r & 7)) & 127)) =
-          make_float2(o[j][0], o[j][1]);
-      *reinterpret_cast<float2*>(meet + (warp * 16 + r + 8) * HD + ((col + 8 * (r & 7)) & 127)) =
-          make_float2(o[j][2], o[j][3]);
+        for (int j = 0; j < 16; ++j) st_shared_v2(at ^ (j << 5), o[j][0], o[j][1]);
+      }
+      if (rg * 16 + 8 < rows) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st_shared_v2((at + 8 * HD * 4) ^ (j << 5), o[j][2], o[j][3]);
+      }
     }
     __syncthreads();
     const bool whole = seg_t == 0 && x.t + 1 == x.nt;
     const bool direct = whole && !PREFIX && B.shared == 0;
     const long long slot = 2ll * blockIdx.x + (seg_i ? 1 : 0);
+    // a warp takes a row, a lane four columns
+#pragma unroll 2
+    for (int r = warp; r < rows; r += 4) {
+      const int r16 = r & 15, w0 = (r >> 4) * F::WK, tok = token_of(r);
+      float2 ml[F::WK];
+      float mr = -INFINITY, lr = 0.f;
 #pragma unroll
-    for (int a = 0; a < WR; ++a) {
-      const int r16 = tid >> 3, r = a * 16 + r16;
-      if (r < rows) {
-        float mr = -INFINITY, lr = 0.f, f[F::WK];
+      for (int g = 0; g < F::WK; ++g) {
+        ml[g] = s_ml[w0 + g][r16];
+        mr = fmaxf(mr, ml[g].x);
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int g = 0; g < F::WK; ++g) mr = fmaxf(mr, s_ml[a * F::WK + g][r16].x);
-#pragma unroll
-        for (int g = 0; g < F::WK; ++g) {
-          const float2 ml = s_ml[a * F::WK + g][r16];
-          f[g] = mr == -INFINITY ? 0.f : ex2(ml.x - mr);
-          lr += ml.y * f[g];
-        }
-        const int tok = x.s.q0 + r / B.G, head = x.h * B.G + r % B.G;
-        const long long row = static_cast<long long>(tok) * B.H + head;
+      for (int g = 0; g < F::WK; ++g) {
+        const float f = mr == -INFINITY ? 0.f : ex2(ml[g].x - mr);
+        lr += ml[g].y * f;
+        const float4 w = ld_shared_f4(meet + ((w0 + g) * 16 + r16) * (HD * 4) + ((lane << 4) ^ ((r16 & 7) << 5)));
+        v.x += w.x * f;
+        v.y += w.y * f;
+        v.z += w.z * f;
+        v.w += w.w * f;
+      }
+      const long long row = static_cast<long long>(x.s.q0 + tok) * B.H + x.h * B.G + (r - tok * B.G);
+      if (direct) {
         const float inv = lr > 0.f ? 1.f / lr : 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int col = (tid & 7) * 4 + 32 * k;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int g = 0; g < F::WK; ++g) {
-            const float4 w = *reinterpret_cast<const float4*>(
-                meet + ((a * F::WK + g) * 16 + r16) * HD + ((col + 8 * (r16 & 7)) & 127));
-            v.x += w.x * f[g];
-            v.y += w.y * f[g];
-            v.z += w.z * f[g];
-            v.w += w.w * f[g];
-          }
-          if (direct) {
-            uint2 w;
-            w.x = pack_bf16x2(v.x * inv, v.y * inv);
-            w.y = pack_bf16x2(v.z * inv, v.w * inv);
-            *reinterpret_cast<uint2*>(p.o + row * HD + col) = w;
-          } else {
-            float* dst = whole ? p.part.row_o + row * HD + col : p.part.slot_o + slot_chunk(p.part, slot, r, col >> 2);
-            *reinterpret_cast<float4*>(dst) = v;
-          }
-        }
-        if ((tid & 7) == 0) {
-          if (!direct)
-            (whole ? p.part.row_ml[row] : p.part.slot_ml[slot * p.part.slot_rows + r]) = make_float2(mr, lr);
-          else if (p.lse)
-            p.lse[row] = lr > 0.f ? mr + log2f(lr) : -INFINITY;
-        }
+        reinterpret_cast<uint2*>(p.o + row * HD)[lane] =
+            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+        if (p.lse && lane == 0) p.lse[row] = lr > 0.f ? mr + log2f(lr) : -INFINITY;
+      } else {
+        float* dst = whole ? p.part.row_o + row * HD + lane * 4 : p.part.slot_o + slot_chunk(p.part, slot, r, lane);
+        *reinterpret_cast<float4*>(dst) = v;
+        if (lane == 0) (whole ? p.part.row_ml[row] : p.part.slot_ml[slot * p.part.slot_rows + r]) = make_float2(mr, lr);
       }
     }
   }
@@ -879,18 +899,18 @@ struct AttendPlan {
 };
 // The shared keys' kernel of many rows and the own keys' of few rows, side by
 // side: the first on just so many SMs that both end together, by what they were
-// measured to take.  The own keys' lengths are the device's to know: a short
-// item, of two tiles, is assumed; of longer ones the blocks that start at once
+// measured to take.  The own keys' lengths are the device's to know: short
+// items, of two tiles, are assumed; of longer ones the blocks that start at once
 // take what they can in the meantime (Deal).  In turn / side by side: 64
 // sequences of one token, 4 rows to a key head, 8 key heads, 8192 shared keys
-// and 16 to 1024 own ones 53 / 42 us, 4000 own 190 / 179, none 36 / 35, 1024
-// shared and 300 own 37 / 27; 128 sequences, 2048 shared and 100 own 42 / 44.
+// and 16 to 1024 own ones 48 / 38 us, 4000 own 188 / 178, none 34 / 35, 1024
+// shared and 300 own 35 / 26; 128 sequences, 2048 shared and 100 own 40 / 36.
 void split_sms(const KvSpec& a, int num_sms, AttendPlan& P) {
   const int64_t rows = static_cast<int64_t>(a.n_tokens) * (a.H / a.Hkv);
   const int64_t tiles = a.Hkv * ((rows + kv::RT_MANY - 1) / kv::RT_MANY) * ((a.shared_len + 127) / 128);
   const double step = rows > 128 ? 1.8 : 1.2;  // us per 128 keys, with two row tiles or one
   auto shared_us = [&](int64_t sms) { return 9.0 + step * ((tiles + sms - 1) / sms); };
-  auto own_us = [&](int64_t sms) { return 8.0 + 5.3 * a.n_seqs * a.Hkv / kv::few_blocks(static_cast<int>(sms)); };
+  auto own_us = [&](int64_t sms) { return 8.0 + 4.0 * a.n_seqs * a.Hkv / kv::few_blocks(static_cast<int>(sms)); };
   double best = shared_us(num_sms) + own_us(num_sms) - 6.0;  // in turn; the second's start is hidden
   for (int64_t n = 1; n <= 64; ++n) {
     const int64_t sms = (tiles + n - 1) / n;  // with n tiles each
