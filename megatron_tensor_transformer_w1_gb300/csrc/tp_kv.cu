@@ -213,6 +213,10 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 // sequences of 4000 keys, 32 rows, 531 MB: 150 us; with two 103 us).
 // Measured: one sequence of 131072 keys, 537 MB, 84 us with the join (6.4
 // TB/s); 32 sequences of 64 to 16384 keys, 390 MB, 73 us.
+// A segment costs about a tile's time besides its tiles, and counts for one more
+// when work is dealt (64 sequences of 16 to 1024 keys 28 -> 26 us, 32 of 64 to
+// 16384 keys 68 -> 67 us).
+constexpr int FEW_START = 1;
 template <int WR>
 struct Few {
   static constexpr int WK = 4 / WR;           // key groups
@@ -276,7 +280,7 @@ __device__ __forceinline__ uint32_t tile_chunk(uint32_t tile, int r, int c) {
 template <int WR, bool PREFIX>
 __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ AttendParams p) {
   using F = Few<WR>;
-  using C = Cut<PREFIX, KT, 0>;
+  using C = Cut<PREFIX, KT, 0, PREFIX ? 0 : FEW_START>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ float2 s_ml[4][16];
@@ -296,8 +300,14 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem), c, &err, p.part.early,
                                       p.part.lead);
   __syncthreads();
-  const int n_tiles = S.n_tiles, t0 = C::t0(B), lo = C::first_key(B);
-  if (n_tiles == 0) {
+  const int t0 = C::t0(B), lo = C::first_key(B);
+  int left = S.n_tiles;  // places of the list
+  if (left > 0 && c.t < 0) {
+    left += c.t;
+    c.t = 0;
+  }
+  int n_tiles = left;    // at most; known when the copies have come to the end
+  if (left <= 0) {
     if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, 0);
     if (tid == 0 && p.part.split) p.part.split[blockIdx.x] = Split{};
     if (p.beside) grid_dep_wait();
@@ -308,17 +318,13 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   }
 
   // The page of each 8-key group of four tiles of the cursor's item from its
-  // tile on, a lane to a group; -1: no key, or no page of the cache.
+  // tile on, a lane to a group; checked when it is used, a tile later: behind
+  // the copies under way a load takes long.
   auto look_up = [&](const Cursor& x) -> int {
     const int key = (t0 + x.t) * KT + lane * 8;
     if (key >= x.s.kv) return -1;
     const int row = PREFIX ? S.table_row : x.b;
-    const int page = B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
-    if (page < 0 || page >= B.n_pages) {
-      err = DEV_ERR_BATCH;
-      return -1;
-    }
-    return page;
+    return B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
   };
   // Copies of tile x, whose groups' pages are in lanes `from` on.  What this
   // takes to issue is felt in the stream of bytes: a whole tile within a page
@@ -326,6 +332,11 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   const int ch = tid & 15, r0 = tid >> 4, mask = (1 << B.page_shift) - 1;
   const long long page_stride = (static_cast<long long>(B.Hkv) << B.page_shift) * HD;
   auto issue = [&](int stage, const Cursor& x, int pages, int from, bool new_item) {
+    if (pages < 0 || pages >= B.n_pages) {
+      // (a lane without a key has -1)
+      if ((t0 + x.t) * KT + (lane - from) * 8 < x.s.kv && lane >= from && lane < from + 8) err = DEV_ERR_BATCH;
+      pages = -1;
+    }
     const uint32_t ks = smem_u32(smem + stage * F::STAGE), vs = ks + F::KV_BYTES, qs = vs + F::KV_BYTES;
     const int first = (t0 + x.t) * KT;
     const int page = __shfl_sync(0xffffffffu, pages, from);
@@ -397,7 +408,12 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     }
     if (issued < n_tiles) {
       issue(issued % F::STAGES, c, pages, 8 * (c.t - looked_at), issued == 0 || c.t == 0);
-      if (++issued < n_tiles) {
+      ++issued;
+      --left;
+      if (c.t + 1 == c.nt) left -= C::START;
+      if (left <= 0) {
+        n_tiles = issued;
+      } else {
         advance<C, PREFIX>(B, c);
         if (c.t == 0 || c.t == looked_at + 4) {
           looked_at = c.t;
@@ -618,12 +634,13 @@ struct ItemParts {
   int n = 0;
   int second = 0;        // the first part lies in its block's second slot
   long long c0 = 0;
-  __device__ __forceinline__ void set(const Parts& P, long long start, long long nt, long long total) {
-    if (start < 0 || nt <= 0 || start + nt > total) return;  // no list that the kernels cut: no parts
+  // its places begin at `start`, its nt tiles `skip` behind that
+  __device__ __forceinline__ void set(const Parts& P, long long start, int skip, long long nt, long long total) {
+    if (start < 0 || nt <= 0 || start + skip + nt > total) return;  // no list that the kernels cut: no parts
     const Deal D(total, P.grid, P.early, P.lead);
-    c0 = D.block_of(start);
-    n = static_cast<int>(D.block_of(start + nt - 1) - c0) + 1;
-    second = start != D.first(c0);
+    c0 = D.block_of(start + skip);
+    n = static_cast<int>(D.block_of(start + skip + nt - 1) - c0) + 1;
+    second = D.first(c0) < start;
   }
   // the slot of part i
   __device__ __forceinline__ long long slot(int i) const { return 2 * (c0 + i) + (i == 0 ? second : 0); }
@@ -688,6 +705,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     q0 = s.q0;
     rows = rt < 0 ? 0 : min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
     long long nt = per_head, pre = 0;
+    const int skip = p.own.rt ? 0 : FEW_START;
     if (p.own.rt) {
       using C = Cut<false, 128, RT_MANY>;
       nt = rows > 0 ? C::tiles(B, s, rt) : 0;
@@ -697,7 +715,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       pre = sum;
     }
-    if (nt > 0) own.set(p.own, before * B.Hkv + h * per_head + pre, nt, total * B.Hkv);
+    if (nt > skip) own.set(p.own, before * B.Hkv + h * per_head + pre, skip, nt - skip, total * B.Hkv);
   } else {
     const Split x = p.own.split[blockIdx.x];
     if (x.parts == 0) return;
@@ -724,7 +742,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         const int all = tok * B.G + g, srt = p.shared.rt ? all / p.shared.rt : 0;
         r_sh = all - srt * p.shared.rt;
         sh.n = 0;
-        sh.set(p.shared, (h * n_rt_sh + srt) * nt_sh, nt_sh, nt_sh * n_rt_sh * B.Hkv);
+        sh.set(p.shared, (h * n_rt_sh + srt) * nt_sh, 0, nt_sh, nt_sh * n_rt_sh * B.Hkv);
       }
       const int n = own.n + sh.n;
       // this warp's parts wp, wp + share, ..., four at a time: all loads of the

@@ -132,8 +132,11 @@ struct Deal {
   }
 };
 
-template <bool PREFIX, int KTILE, int RT>
+// With START > 0 an item takes START places of the list before its first tile:
+// what a block spends on a segment besides its tiles.
+template <bool PREFIX, int KTILE, int RT, int START_ = 0>
 struct Cut {
+  static constexpr int START = START_;
   static __device__ __forceinline__ int row_tiles(const Batch& p, const Seq& s) {
     const int rows = s.qn * p.G;
     return RT ? (rows + RT - 1) / (RT ? RT : 1) : (rows > 0);
@@ -149,11 +152,16 @@ struct Cut {
     }
     return (s.qn > 0 && hi > first_key(p)) ? (hi + KTILE - 1) / KTILE - t0(p) : 0;
   }
-  static __device__ __forceinline__ long long tiles_per_head(const Batch& p, const Seq& s) {
+  // places in the list
+  static __device__ __forceinline__ int places(const Batch& p, const Seq& s, int rt) {
+    const int n = tiles(p, s, rt);
+    return n + (n > 0 ? START : 0);
+  }
+  static __device__ __forceinline__ long long places_per_head(const Batch& p, const Seq& s) {
     const int n = row_tiles(p, s);
-    if (!RT || PREFIX) return static_cast<long long>(n) * tiles(p, s, 0);
+    if (!RT || PREFIX) return static_cast<long long>(n) * places(p, s, 0);
     long long sum = 0;
-    for (int rt = 0; rt < n; ++rt) sum += tiles(p, s, rt);
+    for (int rt = 0; rt < n; ++rt) sum += places(p, s, rt);
     return sum;
   }
 };
@@ -198,7 +206,7 @@ struct SchedScratch {
   Cursor start;
 };
 struct Sched {
-  int n_tiles = 0;         // of this block
+  int n_tiles = 0;         // of this block; places where items have places to start
   int table_row = 0;       // whose page table leads to the shared pages
   bool all_see = false;    // every row sees every shared key
   bool some_empty = false; // there are rows of sequences that belong to no tile
@@ -215,22 +223,24 @@ struct Sched {
   }
 };
 
-// The place of tile `at` of a sequence's (x.b, x.s) tiles.
+// The tile at place `at` of a sequence's (x.b, x.s) places; x.t below 0: before
+// the first.
 template <typename C>
 __device__ __forceinline__ void locate(const Batch& p, Cursor& x, long long at, long long per_head) {
   x.h = static_cast<int>(quotient(at, per_head));
   at -= x.h * per_head;
   for (x.rt = 0;; ++x.rt) {
     x.nt = C::tiles(p, x.s, x.rt);
-    if (at < x.nt) break;
-    at -= x.nt;
+    const int n = x.nt + (x.nt > 0 ? C::START : 0);
+    if (at < n) break;
+    at -= n;
   }
-  x.t = static_cast<int>(at);
+  x.t = static_cast<int>(at) - C::START;
 }
 
 // Called by every thread of a block (at least 128): sums the tiles of all
 // sequences and finds the block's first tile.  Block 0 leaves the prefix sums
-// for the combine kernel where that asks for them: `sched` [B + 1] tiles per
+// for the combine kernel where that asks for them: `sched` [B + 1] places per
 // key/value head before sequence b, or for prefix items {tiles of a row tile,
 // row tiles}.  Up to 32 sequences every warp does it for itself, a lane to a
 // sequence, without meeting the others: a call of few tokens waits for this
@@ -298,7 +308,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
     for (int b = b0; b < b1; ++b) {
       x.s = load_seq(p, b);
       *err |= x.s.err;
-      sum += C::tiles_per_head(p, x.s);
+      sum += C::places_per_head(p, x.s);
       empty |= x.s.qn > 0 && C::tiles(p, x.s, 0) == 0;
     }
     long long before = sum;  // inclusive sums within the warp
@@ -324,7 +334,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       long long at = before;
       for (int b = b0; b < b1; ++b) {
         sched[b] = at;
-        at += C::tiles_per_head(p, load_seq(p, b));
+        at += C::places_per_head(p, load_seq(p, b));
       }
       if (tid == 0) sched[p.B] = total;
     }
@@ -347,7 +357,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
         for (int b = b0; b < b1; ++b) {
           x.b = b;
           x.s = load_seq(p, b);
-          const long long per_head = C::tiles_per_head(p, x.s);
+          const long long per_head = C::places_per_head(p, x.s);
           if (at < per_head * p.Hkv) {
             locate<C>(p, x, at, per_head);
             w->start = x;
