@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 // WR = 2 has two stages: three would leave room for one block per SM (32
 // sequences of 4000 keys, 32 rows, 531 MB: 150 us; with two 103 us).
 // Measured: one sequence of 131072 keys, 537 MB, 84 us with the join (6.4
-// TB/s); 32 sequences of 64 to 16384 keys, 390 MB, 73 us.
+// TB/s); 32 sequences of 64 to 16384 keys, 390 MB, 67 us.
 // A segment costs about a tile's time besides its tiles, and counts for one more
 // when work is dealt (64 sequences of 16 to 1024 keys 28 -> 26 us, 32 of 64 to
 // 16384 keys 68 -> 67 us).
