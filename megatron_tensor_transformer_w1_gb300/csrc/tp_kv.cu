@@ -301,12 +301,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
                                       p.part.lead);
   __syncthreads();
   const int t0 = C::t0(B), lo = C::first_key(B);
-  int left = S.n_tiles;  // places of the list
-  if (left > 0 && c.t < 0) {
-    left += c.t;
-    c.t = 0;
-  }
-  int n_tiles = left;    // at most; known when the copies have come to the end
+  int left = S.left;
+  int n_tiles = left;  // at most; known when the copies have come to the end
   if (left <= 0) {
     if (!PREFIX && S.some_empty && B.shared == 0) write_empty_rows<C>(p, 0);
     if (tid == 0 && p.part.split) p.part.split[blockIdx.x] = Split{};
@@ -397,7 +393,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   uint32_t qf[8][4];
   int limit[2] = {0, 0};
   bool fresh = true;         // the next tile starts a segment
-  int seg_t = 0, seg_i = 0;  // its first tile within the item, and of the block's
+  int seg_t = 0;             // its first tile within the item
   // (The copies run STAGES - 1 tiles ahead.  They begin in the same loop: the
   // code for them is long, and a second copy of it is fetched for nothing.)
 #pragma unroll 1
@@ -409,8 +405,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     if (issued < n_tiles) {
       issue(issued % F::STAGES, c, pages, 8 * (c.t - looked_at), issued == 0 || c.t == 0);
       ++issued;
-      --left;
-      if (c.t + 1 == c.nt) left -= C::START;
+      left = left_behind<C>(B, c, left);
       if (left <= 0) {
         n_tiles = issued;
       } else {
@@ -429,7 +424,6 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     const int rows = x.s.qn * B.G;
     if (fresh) {
       seg_t = x.t;
-      seg_i = i;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
 #pragma unroll
@@ -541,7 +535,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     // ---- end of a segment: the key groups of the rows meet
     fresh = true;
     if (tid == 0 && i + 1 == n_tiles && p.part.split)
-      p.part.split[blockIdx.x] = split_of(B, S, x, seg_t, seg_i > 0);
+      p.part.split[blockIdx.x] = split_of<C>(B, S, x, seg_t, S.first + S.places - 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -566,7 +560,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
     __syncthreads();
     const bool whole = seg_t == 0 && x.t + 1 == x.nt;
     const bool direct = whole && !PREFIX && B.shared == 0;
-    const long long slot = 2ll * blockIdx.x + (seg_i ? 1 : 0);
+    const long long slot = 2ll * blockIdx.x + (seg_t ? 0 : 1);
     // a warp takes a row, a lane four columns
 #pragma unroll 2
     for (int r = warp; r < rows; r += 4) {
@@ -632,18 +626,16 @@ struct CombineParams {
 // or, n = 1, the rows' own places.
 struct ItemParts {
   int n = 0;
-  int second = 0;        // the first part lies in its block's second slot
   long long c0 = 0;
-  // its places begin at `start`, its nt tiles `skip` behind that
-  __device__ __forceinline__ void set(const Parts& P, long long start, int skip, long long nt, long long total) {
-    if (start < 0 || nt <= 0 || start + skip + nt > total) return;  // no list that the kernels cut: no parts
-    const Deal D(total, P.grid, P.early, P.lead);
-    c0 = D.block_of(start + skip);
-    n = static_cast<int>(D.block_of(start + skip + nt - 1) - c0) + 1;
-    second = D.first(c0) < start;
+  // its first and last tile's places
+  __device__ __forceinline__ void set(const Parts& P, long long first, long long last, long long total, int least) {
+    if (first < 0 || first > last || last >= total) return;  // no list that the kernels cut: no parts
+    const Deal D(total, P.grid, P.early, P.lead, least);
+    c0 = D.block_of(first);
+    n = static_cast<int>(D.block_of(last) - c0) + 1;
   }
-  // the slot of part i
-  __device__ __forceinline__ long long slot(int i) const { return 2 * (c0 + i) + (i == 0 ? second : 0); }
+  // the slot of part i: the first begins the item, the others go on
+  __device__ __forceinline__ long long slot(int i) const { return 2 * (c0 + i) + (i == 0); }
 };
 
 __device__ __forceinline__ void scale4(float4& a, float f) {
@@ -704,18 +696,19 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     n_rt_sh = p.shared.sched[1];
     q0 = s.q0;
     rows = rt < 0 ? 0 : min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
-    long long nt = per_head, pre = 0;
-    const int skip = p.own.rt ? 0 : FEW_START;
+    long long at = before * B.Hkv + h * per_head;  // the item's places
     if (p.own.rt) {
-      using C = Cut<false, 128, RT_MANY>;
-      nt = rows > 0 ? C::tiles(B, s, rt) : 0;
+      using C = Many<false>;
       int sum = 0;
-      for (int i = lane; i < rt; i += 32) sum += C::tiles(B, s, i);
+      for (int i = lane; i < rt; i += 32) sum += C::places(B, s, i);
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      pre = sum;
+      at += sum + C::START;
+      const int nt = rows > 0 ? C::tiles(B, s, rt) : 0;
+      if (nt > 0) own.set(p.own, at, at + (nt - 1) * C::width(B, s, rt), total * B.Hkv, C::LEAST);
+    } else if (per_head > 0) {
+      own.set(p.own, at + FEW_START, at + per_head - 1, total * B.Hkv, 1);
     }
-    if (nt > skip) own.set(p.own, before * B.Hkv + h * per_head + pre, skip, nt - skip, total * B.Hkv);
   } else {
     const Split x = p.own.split[blockIdx.x];
     if (x.parts == 0) return;
@@ -725,7 +718,6 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     rows = min(x.rows - rt * p.own.rt, p.own.slot_rows);
     own.n = x.parts;
     own.c0 = blockIdx.x;
-    own.second = x.second;
   }
   const int share = 8 / p.rows_per_pass;  // warps to a row
   const int wr = warp / share, wp = warp - wr * share;
@@ -742,7 +734,8 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         const int all = tok * B.G + g, srt = p.shared.rt ? all / p.shared.rt : 0;
         r_sh = all - srt * p.shared.rt;
         sh.n = 0;
-        sh.set(p.shared, (h * n_rt_sh + srt) * nt_sh, 0, nt_sh, nt_sh * n_rt_sh * B.Hkv);
+        const long long at_sh = (h * n_rt_sh + srt) * nt_sh;
+        sh.set(p.shared, at_sh, at_sh + nt_sh - 1, nt_sh * n_rt_sh * B.Hkv, 1);
       }
       const int n = own.n + sh.n;
       // this warp's parts wp, wp + share, ..., four at a time: all loads of the

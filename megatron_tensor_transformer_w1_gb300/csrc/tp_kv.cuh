@@ -108,12 +108,13 @@ __device__ __forceinline__ long long block_of_tile(long long t, long long T, lon
 // How T tiles fall to `grid` blocks: the first E share Te tiles evenly, the L
 // behind them the rest.  Where the first `early` blocks start while the SMs of
 // the others are still busy, for as long as a block takes for `lead` tiles,
-// they get so many more; otherwise (early = 0) all get the same.  No block of
-// the E + L is without a tile.
+// they get so many more; otherwise (early = 0) all get the same.  (Tiles are
+// places here, see Cut: a block of the E has `least` of them, the most that a
+// tile takes, so that no block inside an item is without a tile.)
 struct Deal {
   long long T, Te;
   int E, L;
-  __device__ __forceinline__ Deal(long long T_, int grid, int early, int lead) : T(T_), Te(T_), L(0) {
+  __device__ __forceinline__ Deal(long long T_, int grid, int early, int lead, int least) : T(T_), Te(T_), L(0) {
     const long long ahead = static_cast<long long>(early) * lead;
     E = early && T <= ahead ? early : grid;
     if (early && T > ahead) {
@@ -122,7 +123,8 @@ struct Deal {
       E = early;
       L = static_cast<int>(late < grid - early ? late : grid - early);
     }
-    if (T < E) E = static_cast<int>(T);
+    const long long most = least > 1 ? quotient(T, least) : T;
+    if (most < E) E = most > 1 ? static_cast<int>(most) : 1;
   }
   __device__ __forceinline__ long long first(long long c) const {
     return c <= E ? first_tile(c, Te, E) : Te + first_tile(c - E, T - Te, L);
@@ -132,11 +134,15 @@ struct Deal {
   }
 };
 
-// With START > 0 an item takes START places of the list before its first tile:
-// what a block spends on a segment besides its tiles.
-template <bool PREFIX, int KTILE, int RT, int START_ = 0>
+// An item takes START places of the list before its first tile, for what a block
+// spends on a segment besides its tiles, and a tile ONE places, or TWO if it has
+// more than half of RT rows.  A tile is the block's that has its first place.
+template <bool PREFIX, int KTILE, int RT, int START_ = 0, int ONE = 1, int TWO = 1>
 struct Cut {
-  static constexpr int START = START_;
+  static constexpr int START = START_, LEAST = TWO;
+  static __device__ __forceinline__ int width(const Batch& p, const Seq& s, int rt) {
+    return ONE == TWO || s.qn * p.G - rt * RT <= RT / 2 ? ONE : TWO;
+  }
   static __device__ __forceinline__ int row_tiles(const Batch& p, const Seq& s) {
     const int rows = s.qn * p.G;
     return RT ? (rows + RT - 1) / (RT ? RT : 1) : (rows > 0);
@@ -155,7 +161,7 @@ struct Cut {
   // places in the list
   static __device__ __forceinline__ int places(const Batch& p, const Seq& s, int rt) {
     const int n = tiles(p, s, rt);
-    return n + (n > 0 ? START : 0);
+    return n * width(p, s, rt) + (n > 0 ? START : 0);
   }
   static __device__ __forceinline__ long long places_per_head(const Batch& p, const Seq& s) {
     const int n = row_tiles(p, s);
@@ -199,43 +205,55 @@ __device__ __forceinline__ void advance(const Batch& p, Cursor& c) {
   } while (c.nt == 0);
 }
 
+// Places left behind the tile at the cursor, up to the block's last; the block
+// has another tile where they are more than none.  `left`: from the tile's first.
+template <typename C>
+__device__ __forceinline__ int left_behind(const Batch& p, const Cursor& c, int left) {
+  return left - C::width(p, c.s, c.rt) - (c.t + 1 == c.nt ? C::START : 0);
+}
+
 struct SchedScratch {
   long long sums[4];
   unsigned long long longest[4];
   int least[4];
   Cursor start;
+  int gone;
 };
 struct Sched {
-  int n_tiles = 0;         // of this block; places where items have places to start
+  int places = 0;          // of this block
+  int left = 0;            // from its first tile's on; none: no tile
   int table_row = 0;       // whose page table leads to the shared pages
   bool all_see = false;    // every row sees every shared key
   bool some_empty = false; // there are rows of sequences that belong to no tile
   long long first = 0, total = 0, blocks = 0;
   // this block's share of `total_` tiles; false: none
-  __device__ __forceinline__ bool set(long long total_, int early, int lead) {
-    const Deal D(total_, gridDim.x, early, lead);
+  __device__ __forceinline__ bool set(long long total_, int early, int lead, int least) {
+    if (total_ == 0) return false;
+    const Deal D(total_, gridDim.x, early, lead, least);
     total = total_;
     blocks = D.E + D.L;
     if (blockIdx.x >= blocks) return false;
     first = D.first(blockIdx.x);
-    n_tiles = static_cast<int>(D.first(blockIdx.x + 1) - first);
+    left = places = static_cast<int>(D.first(blockIdx.x + 1) - first);
     return true;
   }
 };
 
-// The tile at place `at` of a sequence's (x.b, x.s) places; x.t below 0: before
-// the first.
+// The first tile from place `at` of a sequence's (x.b, x.s) places on; returns how
+// many places lie before it.  x.t = x.nt: the next item's first.
 template <typename C>
-__device__ __forceinline__ void locate(const Batch& p, Cursor& x, long long at, long long per_head) {
+__device__ __forceinline__ int locate(const Batch& p, Cursor& x, long long at, long long per_head) {
   x.h = static_cast<int>(quotient(at, per_head));
   at -= x.h * per_head;
   for (x.rt = 0;; ++x.rt) {
     x.nt = C::tiles(p, x.s, x.rt);
-    const int n = x.nt + (x.nt > 0 ? C::START : 0);
+    const int n = C::places(p, x.s, x.rt);
     if (at < n) break;
     at -= n;
   }
-  x.t = static_cast<int>(at) - C::START;
+  const int w = C::width(p, x.s, x.rt), in = static_cast<int>(at) - C::START;
+  x.t = in > 0 ? (in + w - 1) / w : 0;
+  return x.t * w - in;
 }
 
 // Called by every thread of a block (at least 128): sums the tiles of all
@@ -294,7 +312,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       sched[0] = c.nt;
       sched[1] = n_rt;
     }
-    if (!S.set(static_cast<long long>(n_rt) * c.nt * p.Hkv, 0, 0)) return S;
+    if (!S.set(static_cast<long long>(n_rt) * c.nt * p.Hkv, 0, 0, 1)) return S;
     const long long item = quotient(S.first, c.nt);
     c.t = static_cast<int>(S.first - item * c.nt);
     c.h = static_cast<int>(quotient(item, n_rt));
@@ -338,7 +356,7 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       }
       if (tid == 0) sched[p.B] = total;
     }
-    if (!S.set(total * p.Hkv, early, lead)) return S;
+    if (!S.set(total * p.Hkv, early, lead, C::LEAST)) return S;
     const bool mine = (small || tid < 128) && S.first >= before * p.Hkv && S.first < (before + sum) * p.Hkv;
     if (small) {
       const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
@@ -349,17 +367,18 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       c.s.err = 0;
       sum = __shfl_sync(0xffffffffu, sum, src);
       before = __shfl_sync(0xffffffffu, before, src);
-      locate<C>(p, c, S.first - before * p.Hkv, sum);
+      S.left -= locate<C>(p, c, S.first - before * p.Hkv, sum);
     } else {
       if (mine) {
         w->start = Cursor{p.B - 1, 0, 0, 0, 1, Seq{}};  // see advance()
+        w->gone = 0;
         long long at = S.first - before * p.Hkv;
         for (int b = b0; b < b1; ++b) {
           x.b = b;
           x.s = load_seq(p, b);
           const long long per_head = C::places_per_head(p, x.s);
           if (at < per_head * p.Hkv) {
-            locate<C>(p, x, at, per_head);
+            w->gone = locate<C>(p, x, at, per_head);
             w->start = x;
             break;
           }
@@ -368,6 +387,12 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
       }
       __syncthreads();
       c = w->start;
+      S.left -= w->gone;
+    }
+    if (c.t == c.nt) {  // behind an item's last tile
+      S.left -= C::START;
+      --c.t;
+      if (S.left > 0) advance<C, PREFIX>(p, c);
     }
   }
   return S;
@@ -376,15 +401,16 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
 // An item cut between blocks, noted by the block that has its first tile.
 struct Split {
   int h, rt, q0, rows;  // rows: of the sequence and head, all row tiles
-  int parts, second;    // 0 parts: the block's last segment is none; second: it is not the block's first
-  int pad[2];
+  int parts;            // 0: the block's last segment is none
+  int pad[3];
 };
 
 // What a segment leaves for the combine kernel: the running maximum (in log2
 // units) and sum of each row, and its unnormalised output in 32 bits.  A
 // segment that is a whole item goes to its rows' own places ([token][head],
-// used only where other keys are still to be joined), the others, of which a
-// block has at most two, its first and its last, to the block's two slots.
+// used only where other keys are still to be joined); the others, of which a
+// block has at most two, go to its two slots: one that goes on with an item to
+// the first, one that begins an item to the second.
 // A slot's outputs lie in four parts of 32 columns, [4][slot_rows][32], the
 // 16-byte chunks of a row's 128 bytes swizzled by the row (chunk k at k ^ (r &
 // 7)): so the many-rows kernel, a row to a thread, can stage a warp's 32 rows
@@ -406,18 +432,18 @@ __device__ __forceinline__ long long slot_chunk(const Parts& P, long long slot, 
   return ((slot * 4 + (c >> 3)) * P.slot_rows + r) * 32 + (((c & 7) ^ (r & 7)) << 2);
 }
 
-// The note on a block's last segment: tile x of the list is its last one.
-// (Where all blocks get the same number of tiles.)
-__device__ __forceinline__ Split split_of(const Batch& p, const Sched& S, const Cursor& x, int seg_t, bool second) {
+// The note on a block's last segment, whose last tile is x at place `at` of the
+// list.  (Where all blocks get the same number of places.)
+template <typename C>
+__device__ __forceinline__ Split split_of(const Batch& p, const Sched& S, const Cursor& x, int seg_t, long long at) {
   Split r{};
-  const long long end = S.first + S.n_tiles + (x.nt - x.t - 1);  // the item's
   if (seg_t == 0 && x.t + 1 < x.nt) {
+    const long long end = at + (x.nt - 1 - x.t) * C::width(p, x.s, x.rt);  // the item's last tile
     r.h = x.h;
     r.rt = x.rt;
     r.q0 = x.s.q0;
     r.rows = x.s.qn * p.G;
-    r.parts = static_cast<int>(block_of_tile(end - 1, S.total, S.blocks) - blockIdx.x) + 1;
-    r.second = second;
+    r.parts = static_cast<int>(block_of_tile(end, S.total, S.blocks) - blockIdx.x) + 1;
   }
   return r;
 }
@@ -435,11 +461,18 @@ struct AttendParams {
   // when the call's inputs are there.  This kernel starts without waiting for
   // it, and waits before its blocks end.
   int beside;
-  int skip_load;           // test hook: block 0 never issues its first copy
+  int skip_load;           // test hook: no block issues its first copy
   unsigned long long timeout_ns;
 };
 
 constexpr int RT_MANY = 256;  // rows of an item of the many-rows kernel
+// A segment costs it about a tile, a tile of one row tile little less than one of
+// two (its softmax waits for its own products).  All tiles alike and segments for
+// nothing / these weights: 4 prompt chunks 373 / 365 us, 16 prompts behind 4096
+// shared keys 215 / 208 us, 86 sequences of 40 rows 109 / 93 us; one row tile for
+// two thirds of two 374 / 219 / 94 us.
+template <bool PREFIX>
+using Many = Cut<PREFIX, 128, RT_MANY, PREFIX ? 0 : 6, PREFIX ? 1 : 6, PREFIX ? 1 : 7>;
 // The many-rows kernel (tp_kv_tc.cu).
 int launch_many(const AttendParams& p, bool prefix, LaunchCtx& ctx, const char* name);
 

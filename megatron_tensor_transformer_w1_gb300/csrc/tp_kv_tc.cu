@@ -82,12 +82,9 @@ __device__ __forceinline__ uint32_t key_chunk(uint32_t tile, int r, int c) {
   return tile + (r >> 3) * GROUP + (c >> 3) * COL_HALF + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-template <bool PREFIX>
-using Many = Cut<PREFIX, BK, RT_MANY>;
-
 // A tile, to the issuing warp: product steps of 16 keys, whether it ends a
-// segment, whether the second row tile has rows.
-constexpr uint32_t I_STEPS = 15, I_LAST = 16, I_TWO = 32;
+// segment, whether the second row tile has rows, whether it is the block's last.
+constexpr uint32_t I_STEPS = 15, I_LAST = 16, I_TWO = 32, I_END = 64;
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -245,7 +242,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   if (err) atomicOr(status, err);
   const uint32_t tmem = *tmem_slot;  // S_t at columns 128 t and 128 t + 64, O_t at 256 + 128 t
   const Waiter W{abort_flag, status, p.timeout_ns};
-  const int N = S.n_tiles, t0 = C::t0(B), lo = C::first_key(B);
+  const int t0 = C::t0(B), lo = C::first_key(B);
+  const bool some = S.left > 0;
+  int left = S.left;  // of each role, with its cursor
   auto ring = [&](uint32_t i) { return smem + M_RING + (i & (SLOTS - 1)) * TILE_BYTES; };
   auto rows_of = [&](const Cursor& x) { return x.s.qn * B.G - x.rt * RT_MANY; };  // > 128: both row tiles
 
@@ -294,16 +293,18 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       const int row = PREFIX ? S.table_row : x.b;
       return B.table[static_cast<long long>(row) * B.max_pages + (key >> B.page_shift)];
     };
-    int next = N > 0 ? look_up(c) : -1;
-    for (int n = 0; n < N && ok; ++n) {
+    int next = some ? look_up(c) : -1;
+    for (int n = 0; left > 0 && ok; ++n) {
       const int base = (t0 + c.t) * BK;
       const int live = max(min(groups, (c.s.kv - base + box - 1) / box), 0);  // groups that hold keys
       const int key = base + lane * box, h = c.h;
       // what the issuing warp has to know of the tile; published with its K
+      left = left_behind<C>(B, c, left);
       const uint32_t what = static_cast<uint32_t>((max(min(BK, c.s.kv - base), 0) + 15) / 16) |
-                            (c.t + 1 == c.nt || n + 1 == N ? I_LAST : 0u) | (rows_of(c) > 128 ? I_TWO : 0u);
+                            (c.t + 1 == c.nt || left <= 0 ? I_LAST : 0u) | (rows_of(c) > 128 ? I_TWO : 0u) |
+                            (left <= 0 ? I_END : 0u);
       int page = next;
-      if (n + 1 < N) {
+      if (left > 0) {
         advance<C, PREFIX>(B, c);
         next = look_up(c);
       }
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         const int slot = i & (SLOTS - 1);
         const uint32_t ph = (i / SLOTS) & 1u;
         if (!W.warp(&empty[slot], ph ^ 1u)) { ok = false; break; }
-        if (p.skip_load && blockIdx.x == 0 && i == 0) continue;
+        if (p.skip_load && i == 0) continue;
         if (lane == 0) {
           if (kv == 0) info[n & 1] = what;
           mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(live * box) * HD * 2);
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     __syncwarp();
   } else if (warp < 3) {
     // ------------------------------------------------ products of row tile t
-    if (N > 0) {
+    if (some) {
       constexpr uint32_t ID_S = idesc(SK, 0, 0);    // S = Q K^T
       constexpr uint32_t ID_PV = idesc(128, 0, 1);  // O += P V (V: N = hd contiguous)
       const int t = warp - 1;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
       auto halves = [](uint32_t what) { return (what & I_STEPS) > 4 ? 2 : 1; };
       bool ok = true, first = true;
       uint32_t cur = 0;
-      for (int n = 0; n < N && ok; ++n) {
+      for (int n = 0; ok; ++n) {
         if (first) {
           // a segment begins: both halves of its first S
           if (!(ok = wait_tile(2u * n))) break;
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
         release(2u * n + 1, active);
         if (!last) release(2u * n + 2, active);
+        if (cur & I_END) break;
         first = last;
         cur = next;
       }
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     // ------------------------------------------------ query rows of all segments but the first
     uint32_t uses[2] = {0, 0};
     bool fresh = true, ok = true;
-    for (int n = 0; n < N && ok; ++n) {
+    for (int n = 0; left > 0 && ok; ++n) {
       for (int t = 0; fresh && t < 2 && rows_of(c) > t * 128; ++t) {
         // S_t of the segment before that had this row tile is done
         if (n > 0) {
@@ -462,7 +464,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         ++uses[t];
       }
       fresh = c.t + 1 == c.nt;
-      if (n + 1 < N) advance<C, PREFIX>(B, c);
+      left = left_behind<C>(B, c, left);
+      if (left > 0) advance<C, PREFIX>(B, c);
     }
     __syncwarp();
   } else {
@@ -471,22 +474,21 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t sbuf = smem_u32(smem + M_OUT + (warp - 4) * 4096);
     uint32_t cnt = 0;  // half tiles so far: buffer and phase
-    if (N > 0 && rows_of(c) > t * 128) {
+    if (some && rows_of(c) > t * 128) {
       fetch_q(c, t, quarter * 32, 32);
       publish_q(t, 1);
     }
     const uint64_t scale2 = pack2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
     bool fresh = true;
-    int seg_t = 0, seg_n = 0, limit = 0;
+    int seg_t = 0, limit = 0;
     int at = -1;  // token * H + head of this thread's row, -1: none
     float m = -INFINITY, l = 0.f;
-    for (int n = 0; n < N; ++n) {
-      const int rows = rows_of(c);
-      const bool last = c.t + 1 == c.nt || n + 1 == N;
+    for (int n = 0; left > 0; ++n) {
+      const int rows = rows_of(c), behind = left_behind<C>(B, c, left);
+      const bool last = c.t + 1 == c.nt || behind <= 0;
       if (rows > t * 128) {
         if (fresh) {
           seg_t = c.t;
-          seg_n = n;
           m = -INFINITY;
           l = 0.f;
           limit = 0;
@@ -596,15 +598,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
         if (!ok) break;
         if (last) {
-          if (threadIdx.x == 128 && n + 1 == N && p.part.split)
-            p.part.split[blockIdx.x] = split_of(B, S, c, seg_t, seg_n > 0);
+          if (threadIdx.x == 128 && behind <= 0 && p.part.split)
+            p.part.split[blockIdx.x] = split_of<C>(B, S, c, seg_t, S.first + S.places - left);
           // ---- the segment's rows: to o, to their own places, or to a slot
           const uint32_t was = cnt - 1;
           if (!W.warp(&pv_done[2 * t + (was & 1u)], (was >> 1) & 1u)) break;
           tc_fence_after();
           const bool whole = seg_t == 0 && c.t + 1 == c.nt;
           const bool direct = whole && !PREFIX && B.shared == 0;
-          const long long slot = 2ll * blockIdx.x + (seg_n ? 1 : 0);
+          const long long slot = 2ll * blockIdx.x + (seg_t ? 0 : 1);
           const int row0 = t * 128 + quarter * 32;  // of the warp, in the item
           const float inv = l > 0.f ? 1.f / l : 0.f;
           // 128 bytes of each of the warp's 32 rows, staged so that eight lanes
@@ -665,7 +667,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         }
       }
       fresh = last;
-      if (n + 1 < N) advance<C, PREFIX>(B, c);
+      left = behind;
+      if (left > 0) advance<C, PREFIX>(B, c);
     }
     __syncwarp();
   }
