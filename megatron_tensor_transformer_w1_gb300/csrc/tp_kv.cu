@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 // Its floor is the one read of K and V from memory, 512 bytes per key.
 //
 // Work is cut in tiles of 64 keys and every block takes the same number of
-// consecutive tiles of the whole batch, however the lengths differ; a block
+// consecutive ones of the whole batch (see Cut), however the lengths differ; a block
 // starts and ends inside an item, and the parts of an item (its running
 // maximum, sum and unnormalised output) are joined by kv_combine_kernel.
 //
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 // instructions on registers: for so few rows they take less time than the
 // bytes do, and the 128-row tensor-memory products would be mostly empty.
 // WR = 2 has two stages: three would leave room for one block per SM (32
-// sequences of 4000 keys, 32 rows, 531 MB: 150 us; with two 103 us).
+// sequences of 4000 keys, 32 rows, 531 MB: 150 us; with two 97 us).
 // Measured: one sequence of 131072 keys, 537 MB, 84 us with the join (6.4
 // TB/s); 32 sequences of 64 to 16384 keys, 390 MB, 67 us.
 // A segment costs about a tile's time besides its tiles, and counts for one more
@@ -889,9 +889,9 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // How a call's attention is launched, and its scratch.
 // At most so many rows to a key/value head: the few-rows kernel.  32 sequences
-// of 4000 keys (8 heads, 531 MB): 8 rows 88 us, 32 rows 103 us against 106 us
-// of the many-rows kernel, 64 rows 140 against 107; 4 sequences of 300 keys,
-// where starting the kernel counts: 64 rows 17 against 21.
+// of 4000 keys (8 heads, 531 MB): 16 rows 89 us, 32 rows 97 us against 101 us
+// of the many-rows kernel, 64 rows 140 against 103; 64 sequences of 300 keys,
+// 32 rows: 27 against 36.
 constexpr int kFewRows = 32;
 // At most so many rows to a key/value head, on average over the sequences, for
 // the shared keys to be taken together.

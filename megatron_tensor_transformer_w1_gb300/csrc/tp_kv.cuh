@@ -91,9 +91,10 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int row) {
 // token r / G, head h G + r % G.  Prefix items (PREFIX) take the rows of all
 // sequences together against the shared keys.
 //
-// Block c of C takes the tiles [c T / C, (c + 1) T / C), whatever items they
-// belong to; a run of tiles of one item in one block is a segment.  Every
-// block gets the same number of tiles however the lengths differ (but see
+// A tile takes one or more places of the list (see Cut).  Block c of C takes the
+// places [c T / C, (c + 1) T / C) and the tiles that begin there, whatever items
+// they belong to; a run of tiles of one item in one block is a segment.  Every
+// block gets the same number of places however the lengths differ (but see
 // Deal).
 
 // (A 64-bit division takes some hundred cycles, and several in a row are felt.)
@@ -105,12 +106,12 @@ __device__ __forceinline__ long long block_of_tile(long long t, long long T, lon
   return quotient((t + 1) * C - 1, T);
 }
 
-// How T tiles fall to `grid` blocks: the first E share Te tiles evenly, the L
+// How T places fall to `grid` blocks: the first E share Te of them evenly, the L
 // behind them the rest.  Where the first `early` blocks start while the SMs of
-// the others are still busy, for as long as a block takes for `lead` tiles,
-// they get so many more; otherwise (early = 0) all get the same.  (Tiles are
-// places here, see Cut: a block of the E has `least` of them, the most that a
-// tile takes, so that no block inside an item is without a tile.)
+// the others are still busy, for as long as a block takes for `lead` places,
+// they get so many more; otherwise (early = 0) all get the same.  A block has
+// `least` of them, the most that a tile takes, so that no block inside an item is
+// without a tile.  (Where blocks do not start in that order it takes longer.)
 struct Deal {
   long long T, Te;
   int E, L;

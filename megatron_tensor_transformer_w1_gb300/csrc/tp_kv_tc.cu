@@ -5,7 +5,7 @@
 // An item is a key/value head with 256 of a sequence's rows (new tokens times
 // the G query heads of the group; of all sequences' rows for the shared
 // keys), in two tiles of 128; its keys come in tiles of 128.  One persistent
-// block per SM takes an equal share of the batch's key tiles (see Cut in
+// block per SM takes an equal share of the batch's key tiles by cost (Cut in
 // tp_kv.cuh) and leaves the parts of items that it shares with its
 // neighbours to kv_combine_kernel.
 //
