@@ -122,6 +122,8 @@ MANY = [  # more than 64 rows to a key head: the tensor-memory kernel
     ([2] * 33, [5] * 33, 8, 8, 4, 128, 129, False),
     ([90, 1, 1, 1, 1, 1, 1, 1, 1], [3] * 9, 4, 2, 2, 16, 300, True),   # a prompt among single tokens
     ([100, 80], [30, 40], 8, 2, 2, 32, 640, True),                     # prompts behind a prefix
+    ([(37 * i) % 300 for i in range(24)], [(431 * i) % 2500 for i in range(24)], 16, 4, 4, 16, 0, True),  # many cut items
+    ([1 + (13 * i) % 64 for i in range(150)], [(7 * i) % 40 for i in range(150)], 4, 2, 2, 8, 0, False),  # many short ones
 ]
 
 
@@ -142,6 +144,7 @@ SHARED = [  # shared keys worth taking together: (sequences - 1) x keys x key he
     ([1] * 9, [0] * 9, 32, 8, 8, 64, 4000, True),                             # fewer own tiles than blocks
     ([1] * 20, [(701 * i) % 7000 for i in range(20)], 32, 8, 8, 32, 1300, True),  # long own keys, ragged
     ([2] * 33, [(97 * i) % 900 for i in range(33)], 64, 16, 4, 16, 500, False),   # short shared keys
+    ([9 + i % 8 for i in range(30)], [(61 * i) % 700 for i in range(30)], 32, 8, 8, 16, 1000, True),  # own rows: many, ragged
 ]
 
 
