@@ -293,12 +293,16 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
   const uint32_t g_inv = (65536u + B.G - 1) / B.G;
   auto token_of = [&](int r) { return static_cast<int>(r * g_inv >> 16); };
   if (tid == 0) s_err = 0;
-  if (!p.beside) grid_dep_wait();
-  grid_dep_launch();
+  if (!p.beside && !p.behind_append) grid_dep_wait();
+  if (!p.behind_append) grid_dep_launch();
   int err = 0;
   Cursor c;
   const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem), c, &err, p.part.early,
                                       p.part.lead);
+  if (p.behind_append) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
   __syncthreads();
   const int t0 = C::t0(B), lo = C::first_key(B);
   int left = S.left;
@@ -992,6 +996,7 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kv::HD)));
   p.timeout_ns = ctx.timeout_ns;
   p.skip_load = ctx.debug_skip_load;
+  p.behind_append = !alone;
   int rc = TP_OK;
   if (P.share) {
     p.part = c.shared = P.shared;
@@ -1003,6 +1008,7 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
   }
   p.part = c.own = P.own;
   p.beside = P.share;
+  p.behind_append = !alone && !P.share;
   p.status = status + c.status_words;
   c.status_words += P.own.grid;
   rc = P.own.rt ? kv::launch_many(p, false, ctx, "kv_attend_many") : kv::launch_few<false>(p, ctx, "kv_attend_few");

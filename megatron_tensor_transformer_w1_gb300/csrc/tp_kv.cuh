@@ -462,6 +462,10 @@ struct AttendParams {
   // when the call's inputs are there.  This kernel starts without waiting for
   // it, and waits before its blocks end.
   int beside;
+  // The kernel before it is the same call's append, which lets its successor
+  // start only when the call's inputs are there: the place in the list is looked
+  // for while that runs, and waited for before anything else is read.
+  int behind_append;
   int skip_load;           // test hook: no block issues its first copy
   unsigned long long timeout_ns;
 };

@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     prefetch_tmap(&tv);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
-  if (!p.beside) grid_dep_wait();
-  grid_dep_launch();
+  if (!p.beside && !p.behind_append) grid_dep_wait();
+  if (!p.behind_append) grid_dep_launch();
   if (threadIdx.x == 0) {
     *status = 0;
     if (p.part.split) p.part.split[blockIdx.x] = Split{};
@@ -236,6 +236,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
   int err = 0;
   Cursor c;
   const Sched S = schedule<C, PREFIX>(B, p.part.sched, reinterpret_cast<SchedScratch*>(smem + M_OUT), c, &err);
+  if (p.behind_append) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
   tc_fence_before();
   __syncthreads();  // (also: the status word is clear, the scratch has been read)
   tc_fence_after();
