@@ -671,48 +671,83 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     if (p.alone) p.header[0] = p.header[1] = 0;
   }
   ItemParts own, sh;
-  int h, rt = 0, q0, rows;  // rows: of this row tile
+  int h, rt = 0, q0 = 0, rows = 0;  // rows: of this row tile
   long long nt_sh = 0, n_rt_sh = 0;
+  int srt = 0;  // row tile of the shared keys' that `sh` is of
+  auto shared_parts = [&](int row_tile) {
+    srt = row_tile;
+    sh.n = 0;
+    const long long at = (h * n_rt_sh + srt) * nt_sh;
+    if (nt_sh > 0) sh.set(p.shared, at, at + nt_sh - 1, nt_sh * n_rt_sh * B.Hkv, 1);
+  };
+  auto shared_tile = [&](int row) { return p.shared.rt ? row / RT_MANY : 0; };
   if (SHARED) {
-    // sequence b's row tiles start at cu[b] G / RT + b
+    // The first warp looks the item up for all: eight times its divisions are
+    // most of what the kernel would issue.
+    __shared__ ItemParts s_own, s_sh;
+    __shared__ int s_item[4];
+    __shared__ long long s_tiles[2];
     h = blockIdx.x % B.Hkv;
-    const int u = blockIdx.x / B.Hkv;
-    int b = u;
-    if (p.own.rt) {
-      // the last b with first(b) <= u, 32 places to a round
-      auto first = [&](int x) {
-        return min(max(B.cu[x], 0), B.n_tokens) * static_cast<long long>(B.G) / p.own.rt + x;
-      };
-      int n = B.B;  // b lies in [lo, lo + n)
-      b = 0;
-      while (n > 1) {
-        const int step = (n + 31) >> 5, at = lane * step;
-        const int cnt = __popc(__ballot_sync(0xffffffffu, at < n && first(b + at) <= u));
-        const int skip = max(cnt - 1, 0) * step;
-        b += skip;
-        n = min(step, n - skip);
+    if (warp == 0) {
+      const int u = blockIdx.x / B.Hkv;
+      int b = u;
+      if (p.own.rt) {
+        // sequence b's row tiles start at cu[b] G / RT + b: the last b with
+        // first(b) <= u, 32 places to a round
+        auto first = [&](int x) {
+          return min(max(B.cu[x], 0), B.n_tokens) * static_cast<long long>(B.G) / RT_MANY + x;
+        };
+        int n = B.B;  // b lies in [lo, lo + n)
+        b = 0;
+        while (n > 1) {
+          const int step = (n + 31) >> 5, at = lane * step;
+          const int cnt = __popc(__ballot_sync(0xffffffffu, at < n && first(b + at) <= u));
+          const int skip = max(cnt - 1, 0) * step;
+          b += skip;
+          n = min(step, n - skip);
+        }
+        rt = static_cast<int>(u - first(b));
       }
-      rt = static_cast<int>(u - first(b));
-    }
-    const Seq s = load_seq(B, b);
-    const long long before = p.own.sched[b], per_head = p.own.sched[b + 1] - before, total = p.own.sched[B.B];
-    nt_sh = p.shared.sched[0];
-    n_rt_sh = p.shared.sched[1];
-    q0 = s.q0;
-    rows = rt < 0 ? 0 : min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
-    long long at = before * B.Hkv + h * per_head;  // the item's places
-    if (p.own.rt) {
-      using C = Many<false>;
-      int sum = 0;
-      for (int i = lane; i < rt; i += 32) sum += C::places(B, s, i);
+      const Seq s = load_seq(B, b);
+      const long long before = p.own.sched[b], per_head = p.own.sched[b + 1] - before, total = p.own.sched[B.B];
+      nt_sh = p.shared.sched[0];
+      n_rt_sh = p.shared.sched[1];
+      q0 = s.q0;
+      rows = rt < 0 ? 0 : min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
+      long long at = before * B.Hkv + h * per_head;  // the item's places
+      if (p.own.rt) {
+        using C = Many<false>;
+        int sum = 0;
+        for (int i = lane; i < rt; i += 32) sum += C::places(B, s, i);
 #pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      at += sum + C::START;
-      const int nt = rows > 0 ? C::tiles(B, s, rt) : 0;
-      if (nt > 0) own.set(p.own, at, at + (nt - 1) * C::width(B, s, rt), total * B.Hkv, C::LEAST);
-    } else if (per_head > 0) {
-      own.set(p.own, at + FEW_START, at + per_head - 1, total * B.Hkv, 1);
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        at += sum + C::START;
+        const int nt = rows > 0 ? C::tiles(B, s, rt) : 0;
+        if (nt > 0) own.set(p.own, at, at + (nt - 1) * C::width(B, s, rt), total * B.Hkv, C::LEAST);
+      } else if (per_head > 0) {
+        own.set(p.own, at + FEW_START, at + per_head - 1, total * B.Hkv, 1);
+      }
+      shared_parts(shared_tile(q0 * B.G + max(rt, 0) * p.own.rt));
+      if (lane == 0) {
+        s_own = own;
+        s_sh = sh;
+        s_item[0] = rt;
+        s_item[1] = q0;
+        s_item[2] = rows;
+        s_item[3] = srt;
+        s_tiles[0] = nt_sh;
+        s_tiles[1] = n_rt_sh;
+      }
     }
+    __syncthreads();
+    own = s_own;
+    sh = s_sh;
+    rt = s_item[0];
+    q0 = s_item[1];
+    rows = s_item[2];
+    srt = s_item[3];
+    nt_sh = s_tiles[0];
+    n_rt_sh = s_tiles[1];
   } else {
     const Split x = p.own.split[blockIdx.x];
     if (x.parts == 0) return;
@@ -731,15 +766,13 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     long long at = 0;
     if (r < rows) {
-      const int item_row = rt * p.own.rt + r, tok = q0 + item_row / B.G, g = item_row % B.G;
+      const int item_row = rt * p.own.rt + r, i_tok = item_row / B.G, tok = q0 + i_tok, g = item_row - i_tok * B.G;
       at = static_cast<long long>(tok) * B.H + h * B.G + g;
       int r_sh = 0;
-      if (SHARED && nt_sh > 0) {
-        const int all = tok * B.G + g, srt = p.shared.rt ? all / p.shared.rt : 0;
-        r_sh = all - srt * p.shared.rt;
-        sh.n = 0;
-        const long long at_sh = (h * n_rt_sh + srt) * nt_sh;
-        sh.set(p.shared, at_sh, at_sh + nt_sh - 1, nt_sh * n_rt_sh * B.Hkv, 1);
+      if (SHARED) {
+        const int all = tok * B.G + g, tile = shared_tile(all);
+        if (tile != srt) shared_parts(tile);
+        r_sh = all - tile * RT_MANY;
       }
       const int n = own.n + sh.n;
       // this warp's parts wp, wp + share, ..., four at a time: all loads of the
