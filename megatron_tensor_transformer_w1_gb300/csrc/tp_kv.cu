@@ -204,11 +204,11 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 // tile with its own running maximum and sum (no exchange per tile); the groups
 // meet at the end of a segment, where few instructions count: with a warp or
 // two per scheduler each takes some four cycles, and short sequences end a
-// segment every few tiles (a row to a warp, no division, rows that there are
-// not left out: 3900 -> 2000 cycles a segment; 7 sequences of 100 to 5000 keys
-// 19 -> 17 us).  The products are m16n8k16 matrix
-// instructions on registers: for so few rows they take less time than the
-// bytes do, and the 128-row tensor-memory products would be mostly empty.
+// segment every few tiles (a row to a warp, no division, absent rows left out:
+// 3900 -> 2000 cycles a segment; 7 sequences of 100 to 5000 keys 19 -> 17 us).
+// The products are m16n8k16 matrix instructions on registers: for so few rows
+// they take less time than the bytes do, and the 128-row tensor-memory products
+// would be mostly empty.
 // WR = 2 has two stages: three would leave room for one block per SM (32
 // sequences of 4000 keys, 32 rows, 531 MB: 150 us; with two 97 us).
 // Measured: one sequence of 131072 keys, 537 MB, 84 us with the join (6.4
