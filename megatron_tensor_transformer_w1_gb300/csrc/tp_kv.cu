@@ -589,10 +589,10 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
       }
       const long long row = static_cast<long long>(x.s.q0 + tok) * B.H + x.h * B.G + (r - tok * B.G);
       if (direct) {
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const float inv = inverse_sum(lr);
         reinterpret_cast<uint2*>(p.o + row * HD)[lane] =
             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-        if (p.lse && lane == 0) p.lse[row] = lr > 0.f ? mr + log2f(lr) : -INFINITY;
+        if (p.lse && lane == 0) p.lse[row] = log2_sum_exp(mr, lr);
       } else {
         float* dst = whole ? p.part.row_o + row * HD + lane * 4 : p.part.slot_o + slot_chunk(p.part, slot, r, lane);
         *reinterpret_cast<float4*>(dst) = v;
@@ -612,7 +612,8 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
 // Joins the parts of a row: with (m_i, l_i, O_i) the running maximum, sum and
 // unnormalised output of part i, m = max m_i, l = sum l_i 2^(m_i - m),
 // o = sum O_i 2^(m_i - m) / l, always in the order of the parts, so that a
-// result does not change from run to run.  A row without any key gets zeros.
+// result does not change from run to run.  A row without any key gets zeros; one
+// with NaN or +inf among its scores has NaN for its sum, and gets NaN.
 // Bound by latency: the parts lie in L2.  A warp takes a row, a lane
 // four columns; several warps share a row where there are few rows in all, so
 // that the many parts of a long sequence are read at once.
@@ -801,14 +802,16 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
           }
         }
         const float top = fmaxf(m, fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)));
-        if (top == -INFINITY) continue;
-        const float f = ex2(m - top);
+        // No maximum yet: the sums are 0, or NaN where scores are (a maximum drops
+        // NaN), and are added with a weight of 0.
+        const float base = top == -INFINITY ? 0.f : top;
+        const float f = ex2(m - base);
         m = top;
         l *= f;
         scale4(a, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float w = ex2(x[j].x - top);
+          const float w = ex2(x[j].x - base);
           l += w * x[j].y;
           add4(a, w, v[j]);
         }
@@ -835,10 +838,10 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
       __syncthreads();
     }
     if (r >= rows || wp) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
     reinterpret_cast<uint2*>(p.o + at * HD)[lane] =
         make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-    if (p.lse && lane == 0) p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+    if (p.lse && lane == 0) p.lse[at] = log2_sum_exp(m, l);
   }
 }
 

@@ -449,6 +449,12 @@ __device__ __forceinline__ Split split_of(const Batch& p, const Sched& S, const 
   return r;
 }
 
+// 1 / l and the log2-sum-exp of a row with running maximum m and sum l.  l is 0
+// where the row saw no key, and NaN where a score was NaN or +inf (the maximum
+// drops NaN): that is what the row gets.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log2_sum_exp(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
+
 struct AttendParams {
   Batch b;
   const __nv_bfloat16* q;  // [n_tokens][H * HD]

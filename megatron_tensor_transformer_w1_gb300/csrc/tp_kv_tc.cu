@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           float alpha = 1.f;
           bool rescale = false;
           if (m == -INFINITY) {
-            m = mx;  // the first key that this row sees: O_t and l are still zero
+            m = mx;  // the first key that this row sees: O_t and l are still zero (or NaN, from scores that are)
           } else if (mx > m + 8.f) {
             alpha = ex2(m - mx);
             m = mx;
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           const bool direct = whole && !PREFIX && B.shared == 0;
           const long long slot = 2ll * blockIdx.x + (seg_t ? 0 : 1);
           const int row0 = t * 128 + quarter * 32;  // of the warp, in the item
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = inverse_sum(l);
           // 128 bytes of each of the warp's 32 rows, staged so that eight lanes
           // write a row's together: dst(row of the warp, row among all)
           auto write_rows = [&](auto dst) {
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             if (!direct)
               (whole ? p.part.row_ml[at] : p.part.slot_ml[slot * p.part.slot_rows + row0 + lane]) = make_float2(m, l);
             else if (p.lse)
-              p.lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+              p.lse[at] = log2_sum_exp(m, l);
           }
           tc_fence_before();
         }
