@@ -439,7 +439,8 @@ TPFFN_API int tp_attn_kv_append(const tp_attn_plan* plan, const tp_kv_cache* cac
  * (position t) sees keys 0 .. t (causal plans) or all kv_len[b] keys.
  * o [n_tokens][H*hd]; lse [n_tokens][H] fp32 or NULL: log2 of
  * sum_j 2^(s_ij log2 e), as in tp_attn_core_fwd.  A row that sees no key gets
- * o = 0 and lse = -inf; one with a score of NaN or +inf gets NaN in both.
+ * o = 0 and lse = -inf; one with a score of NaN or +inf gets NaN in both, one
+ * whose scores are all -inf gets NaN in o and lse = -inf.
  * Cached values that a row does not see must still be finite where they belong
  * to its sequence or are among the shared keys (below); slots behind kv_len may
  * hold anything.

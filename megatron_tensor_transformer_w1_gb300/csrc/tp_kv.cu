@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(128, 2) kv_few_kernel(const __grid_constant__ 
       }
       const long long row = static_cast<long long>(x.s.q0 + tok) * B.H + x.h * B.G + (r - tok * B.G);
       if (direct) {
-        const float inv = inverse_sum(lr);
+        const float inv = inverse_sum(lr, x.s.visible(tok, B.causal) > 0);
         reinterpret_cast<uint2*>(p.o + row * HD)[lane] =
             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         if (p.lse && lane == 0) p.lse[row] = log2_sum_exp(mr, lr);
@@ -672,7 +672,8 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     if (p.alone) p.header[0] = p.header[1] = 0;
   }
   ItemParts own, sh;
-  int h, rt = 0, q0 = 0, rows = 0;  // rows: of this row tile
+  Seq s{};  // the item's sequence
+  int h, rt = 0, rows = 0;  // rows: of this row tile
   long long nt_sh = 0, n_rt_sh = 0;
   int srt = 0;  // row tile of the shared keys' that `sh` is of
   auto shared_parts = [&](int row_tile) {
@@ -686,7 +687,8 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     // The first warp looks the item up for all: eight times its divisions are
     // most of what the kernel would issue.
     __shared__ ItemParts s_own, s_sh;
-    __shared__ int s_item[4];
+    __shared__ int s_item[3];
+    __shared__ Seq s_seq;
     __shared__ long long s_tiles[2];
     h = blockIdx.x % B.Hkv;
     if (warp == 0) {
@@ -709,11 +711,10 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         }
         rt = static_cast<int>(u - first(b));
       }
-      const Seq s = load_seq(B, b);
+      s = load_seq(B, b);
       const long long before = p.own.sched[b], per_head = p.own.sched[b + 1] - before, total = p.own.sched[B.B];
       nt_sh = p.shared.sched[0];
       n_rt_sh = p.shared.sched[1];
-      q0 = s.q0;
       rows = rt < 0 ? 0 : min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
       long long at = before * B.Hkv + h * per_head;  // the item's places
       if (p.own.rt) {
@@ -728,14 +729,14 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
       } else if (per_head > 0) {
         own.set(p.own, at + FEW_START, at + per_head - 1, total * B.Hkv, 1);
       }
-      shared_parts(shared_tile(q0 * B.G + max(rt, 0) * p.own.rt));
+      shared_parts(shared_tile(s.q0 * B.G + max(rt, 0) * p.own.rt));
       if (lane == 0) {
         s_own = own;
         s_sh = sh;
+        s_seq = s;
         s_item[0] = rt;
-        s_item[1] = q0;
-        s_item[2] = rows;
-        s_item[3] = srt;
+        s_item[1] = rows;
+        s_item[2] = srt;
         s_tiles[0] = nt_sh;
         s_tiles[1] = n_rt_sh;
       }
@@ -743,19 +744,19 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     __syncthreads();
     own = s_own;
     sh = s_sh;
+    s = s_seq;
     rt = s_item[0];
-    q0 = s_item[1];
-    rows = s_item[2];
-    srt = s_item[3];
+    rows = s_item[1];
+    srt = s_item[2];
     nt_sh = s_tiles[0];
     n_rt_sh = s_tiles[1];
   } else {
     const Split x = p.own.split[blockIdx.x];
     if (x.parts == 0) return;
+    s = x.s;
     h = x.h;
     rt = x.rt;
-    q0 = x.q0;
-    rows = min(x.rows - rt * p.own.rt, p.own.slot_rows);
+    rows = min(s.qn * B.G - rt * p.own.rt, p.own.slot_rows);
     own.n = x.parts;
     own.c0 = blockIdx.x;
   }
@@ -766,8 +767,10 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     long long at = 0;
+    bool sees = false;
     if (r < rows) {
-      const int item_row = rt * p.own.rt + r, i_tok = item_row / B.G, tok = q0 + i_tok, g = item_row - i_tok * B.G;
+      const int item_row = rt * p.own.rt + r, i_tok = item_row / B.G, tok = s.q0 + i_tok, g = item_row - i_tok * B.G;
+      sees = s.visible(i_tok, B.causal) > 0;
       at = static_cast<long long>(tok) * B.H + h * B.G + g;
       int r_sh = 0;
       if (SHARED) {
@@ -838,7 +841,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
       __syncthreads();
     }
     if (r >= rows || wp) continue;
-    const float inv = inverse_sum(l);
+    const float inv = inverse_sum(l, sees);
     reinterpret_cast<uint2*>(p.o + at * HD)[lane] =
         make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     if (p.lse && lane == 0) p.lse[at] = log2_sum_exp(m, l);

@@ -401,9 +401,10 @@ __device__ __forceinline__ Sched schedule(const Batch& p, long long* sched, Sche
 
 // An item cut between blocks, noted by the block that has its first tile.
 struct Split {
-  int h, rt, q0, rows;  // rows: of the sequence and head, all row tiles
-  int parts;            // 0: the block's last segment is none
-  int pad[3];
+  Seq s;
+  int h, rt;
+  int parts;  // 0: the block's last segment is none
+  int pad;
 };
 
 // What a segment leaves for the combine kernel: the running maximum (in log2
@@ -440,19 +441,19 @@ __device__ __forceinline__ Split split_of(const Batch& p, const Sched& S, const 
   Split r{};
   if (seg_t == 0 && x.t + 1 < x.nt) {
     const long long end = at + (x.nt - 1 - x.t) * C::width(p, x.s, x.rt);  // the item's last tile
+    r.s = x.s;
     r.h = x.h;
     r.rt = x.rt;
-    r.q0 = x.s.q0;
-    r.rows = x.s.qn * p.G;
     r.parts = static_cast<int>(block_of_tile(end, S.total, S.blocks) - blockIdx.x) + 1;
   }
   return r;
 }
 
-// 1 / l and the log2-sum-exp of a row with running maximum m and sum l.  l is 0
-// where the row saw no key, and NaN where a score was NaN or +inf (the maximum
-// drops NaN): that is what the row gets.
-__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+// 1 / l and the log2-sum-exp of a row with running maximum m and sum l.  l is NaN
+// where a score was NaN or +inf (the maximum drops NaN): that is what the row
+// gets.  It is 0 where the row sees no key, for an output of 0, and where all
+// scores that it sees are -inf, for one of 0 / 0.
+__device__ __forceinline__ float inverse_sum(float l, bool sees) { return l == 0.f && !sees ? 0.f : 1.f / l; }
 __device__ __forceinline__ float log2_sum_exp(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
 struct AttendParams {

@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
           const bool direct = whole && !PREFIX && B.shared == 0;
           const long long slot = 2ll * blockIdx.x + (seg_t ? 0 : 1);
           const int row0 = t * 128 + quarter * 32;  // of the warp, in the item
-          const float inv = inverse_sum(l);
+          const float inv = inverse_sum(l, limit > 0);
           // 128 bytes of each of the warp's 32 rows, staged so that eight lanes
           // write a row's together: dst(row of the warp, row among all)
           auto write_rows = [&](auto dst) {

@@ -95,3 +95,55 @@ def test_a_shared_key_that_is_nan(new, ctx, H, Hkv, T, page, shared, causal):
     got, G = got.view(-1, H, HD), H // Hkv
     assert got[:, H - G:].isnan().all() and got_lse[:, H - G:].isnan().all()
     assert torch.equal(got[:, :H - G], o[:, :H - G]) and torch.equal(got_lse[:, :H - G], lse[:, :H - G])
+
+
+@pytest.mark.parametrize("new,ctx,H,Hkv,T,page,shared,causal", BATCHES)
+def test_scores_that_are_all_minus_infinity(new, ctx, H, Hkv, T, page, shared, causal):
+    """A row that sees keys, all with a weight of 2^-inf: 0 / 0, not the zeros of a
+    row that sees none; the log2 of their sum is -inf."""
+    s, cache, batch, q, _, _ = _clean(new, ctx, H, Hkv, T, page, shared, causal)
+    s["k"][..., 17] = torch.where(s["k"][..., 17].isnan(), s["k"][..., 17], 1.0)
+    o, lse = cache.attend(q, batch, shared_len=shared, lse=True)
+    o = o.view(-1, H, HD)
+    hit = torch.zeros(s["n"], H, dtype=torch.bool, device="cuda")
+    hit[::5, H // 2] = True
+    bad = q.clone().view(-1, H, HD)
+    bad[..., 17][hit] = -math.inf
+    got, got_lse = cache.attend(bad.view(-1, H * HD), batch, shared_len=shared, lse=True)
+    got = got.view(-1, H, HD)
+    assert cache.last_device_error() == 0
+    assert got[hit].isnan().all() and (got_lse[hit] == -math.inf).all()
+    assert torch.equal(got[~hit], o[~hit]) and torch.equal(got_lse[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("new,shared", [([9, 1, 5, 3], 0), ([90, 1, 50, 30], 0), ([2] * 30, 1000), ([9] * 30, 1000)])
+def test_rows_without_keys_beside_scores_of_minus_infinity(new, shared):
+    """Rows that see no key get zeros, those that see only such scores NaN."""
+    H, Hkv = 32, 8
+    s = ref.make_batch(new, [20] * len(new), Hkv, 16, shared, seed=4)
+    for b, n in ((0, new[0] - 1), (1, 0), (2, 1)):
+        s["lens"][b] = n
+    s["kv_len"].copy_(torch.tensor(s["lens"]))
+    s["k"][..., 17] = torch.where(s["k"][..., 17].isnan(), s["k"][..., 17], 1.0)
+    cache, batch = _cache(s, H, 8)
+    q = _q(s["n"], H, 3).view(-1, H, HD)
+    q[..., 17] = -math.inf
+    o, lse = cache.attend(q.view(-1, H * HD), batch, shared_len=shared, lse=True)
+    assert cache.last_device_error() == 0 and (lse == -math.inf).all()
+    seen = torch.tensor([length - rows + i + 1 > 0 for rows, length in zip(s["new"], s["lens"]) for i in range(rows)],
+                        device="cuda")
+    assert (~seen).any() and o[seen].isnan().all() and (o[~seen] == 0).all()
+
+
+@pytest.mark.parametrize("new,ctx,H,Hkv,T,page,shared,causal", [b for b in BATCHES if max(b[1]) > 50])
+def test_a_score_of_minus_infinity(new, ctx, H, Hkv, T, page, shared, causal):
+    """One key of many: its weight is 0, as that of a score of -2600."""
+    s, cache, batch, q, _, _ = _clean(new, ctx, H, Hkv, T, page, shared, causal)
+    q.view(-1, H, HD)[..., 17] = 1.0
+    out = []
+    for low in (-30000.0, -math.inf):
+        s["k"][s["table"][0, 0].item(), :, 1, 17] = low
+        out.append(cache.attend(q, batch, shared_len=shared, lse=True))
+    assert torch.isfinite(out[0][0]).all()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
