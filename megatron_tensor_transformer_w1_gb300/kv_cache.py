@@ -11,10 +11,10 @@ in libtpffn.so.
     o = cache.attend(q, batch, shared_len=0)          # [n, H * 128]
     y = attn.decode(x, cache, batch, wqkv, wo)        # both, between the projections
 
-The cache keeps a workspace for every stream that it has been used on; a call
-that is being captured into a graph takes one of its own (from the graph's
-memory), so that no two of them can be at work in the same one.  (An append
-needs only status words, which the cache keeps.)
+The cache keeps a workspace for every stream that it has been used on, and the
+status words that an append needs likewise; a call that is being captured into a
+graph takes its own (from the graph's memory).  So calls on different streams,
+and replays beside them, have nothing in common but the pages.
 """
 from __future__ import annotations
 
@@ -91,9 +91,9 @@ class PagedKVCache:
                                        float(rotary_scale))
         self._at = ctypes.addressof(self._abi)
         self._rot_at = None if self._rot is None else ctypes.addressof(self._rot)
-        self._status = torch.empty(abi.tp_attn_kv_workspace_bytes(attn.plan, abi.KvBatch(), self.page_size, 0,
-                                                                  abi.TP_KV_APPEND),
-                                   dtype=torch.uint8, device=self.device)
+        self._status_bytes = abi.tp_attn_kv_workspace_bytes(attn.plan, abi.KvBatch(), self.page_size, 0,
+                                                            abi.TP_KV_APPEND)
+        self._statuses = {}    # of the appends, by stream
         self._workspaces = {}  # by stream
         self._last = None      # workspace of the last call, for last_device_error
 
@@ -108,6 +108,14 @@ class PagedKVCache:
         self._check(name, t, torch.bfloat16, shape)
         return t
 
+    def _buffer(self, kept, need, stream):
+        if _capturing():
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        t = kept.get(stream)
+        if t is None or t.numel() < need:
+            t = kept[stream] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return t
+
     def _workspace(self, batch, shared_len, call, flags, stream):
         key = (self.attn, self.page_size, shared_len, call, flags)
         need = batch._bytes.get(key)
@@ -115,12 +123,7 @@ class PagedKVCache:
             need = max(16, abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call,
                                                           flags))
             batch._bytes[key] = need
-        if _capturing():
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        else:
-            ws = self._workspaces.get(stream)
-            if ws is None or ws.numel() < need:
-                ws = self._workspaces[stream] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        ws = self._buffer(self._workspaces, need, stream)
         self._last = ws if batch.n_tokens and batch.n_seqs else None
         return ws, need
 
@@ -142,10 +145,11 @@ class PagedKVCache:
         n = batch.n_tokens
         self._check("qkv", qkv, torch.bfloat16, (n, self._width))
         q = self._out("q", q, (n, self._q_width))
-        self._last = self._status if n and batch.n_seqs else None
+        st = _current_stream(self._index)
+        status = self._buffer(self._statuses, self._status_bytes, st)
+        self._last = status if n and batch.n_seqs else None
         rc = abi._lib.tp_attn_kv_append(self.attn.plan, self._at, batch._at, self._rot_at, qkv.data_ptr(),
-                                        q.data_ptr(), self._status.data_ptr(), self._status.numel(), flags,
-                                        _current_stream(self._index))
+                                        q.data_ptr(), status.data_ptr(), self._status_bytes, flags, st)
         if rc:
             abi.check(rc, "tp_attn_kv_append")
         return q
@@ -185,7 +189,8 @@ class PagedKVCache:
 
     def last_device_error(self):
         """Waits for the current stream and returns the status that the last call
-        on this cache left on the device (TP_OK, TP_ERR_BATCH, ...)."""
+        on this cache left on the device (TP_OK, TP_ERR_BATCH, ...): to be called
+        on that call's stream, or after a wait for it."""
         if self._last is None:
             return abi.TP_OK
         with torch.cuda.device(self.device):

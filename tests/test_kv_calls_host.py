@@ -1,0 +1,70 @@
+"""How PagedKVCache hands buffers to the library, on the CPU: the library's calls
+are replaced by recorders, the device's streams by numbers."""
+import threading
+import time
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+
+@pytest.fixture
+def host(monkeypatch):
+    from megatron_tensor_transformer_w1_gb300 import build
+    build.build()
+    from megatron_tensor_transformer_w1_gb300 import kv_cache, tpffn as abi
+
+    class HostCache(kv_cache.PagedKVCache):
+        def _elsewhere(self, batch):
+            return False
+
+        def _check(self, name, t, dtype, shape):
+            assert t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+    rc, plan = abi.tp_attn_plan_create(256, 8, 2, 128, 2, True, abi.TP_BF16)
+    assert rc == abi.TP_OK
+    attn = SimpleNamespace(plan=plan, H=8, Hkv=2, hd=128, d=256, info=abi.tp_attn_plan_info(plan),
+                           device=torch.device("cpu", 0))
+    env = SimpleNamespace(abi=abi, stream=1, capturing=False, calls=[], attn=attn, during=lambda at: None)
+    monkeypatch.setattr(kv_cache, "_current_stream", lambda index: env.stream)
+    monkeypatch.setattr(kv_cache, "_capturing", lambda: env.capturing)
+
+    def append(plan, cache, batch, rot, qkv, q, ws, ws_bytes, flags, stream):
+        env.calls.append((stream, ws, ws_bytes))
+        env.during(ws)
+        return abi.TP_OK
+
+    def attend(plan, cache, batch, shared, q, o, lse, ws, ws_bytes, flags, stream):
+        return append(plan, cache, batch, None, q, o, ws, ws_bytes, flags, stream)
+
+    def decode(plan, cache, batch, rot, shared, x, wqkv, wo, y, ws, ws_bytes, flags, stream):
+        return append(plan, cache, batch, None, x, y, ws.data_ptr(), ws_bytes, flags, stream)
+    monkeypatch.setattr(abi, "_lib", SimpleNamespace(
+        tp_attn_kv_append=append, tp_attn_paged_fwd=attend,
+        tp_attn_kv_workspace_bytes=abi._lib.tp_attn_kv_workspace_bytes))
+    monkeypatch.setattr(abi, "tp_attn_decode_fwd", decode)
+    env.cache = HostCache(attn, 10, 16)
+    i32 = lambda *sh: torch.zeros(*sh, dtype=torch.int32)
+    env.batch = env.cache.batch(i32(4), i32(3), i32(3, 5), 4, 2)
+    env.rows = lambda width: torch.zeros(4, width, dtype=torch.bfloat16)
+    yield env
+    monkeypatch.undo()
+    abi.tp_attn_plan_destroy(plan)
+
+
+def test_append_has_a_status_buffer_of_its_stream_and_of_its_capture(host):
+    qkv = host.rows(12 * 128)
+    kept = []  # what a captured call was given stays with its graph
+
+    def call(stream, capturing=False):
+        host.stream, host.capturing = stream, capturing
+        host.cache.append(qkv, host.batch)
+        kept.append(host.cache._last)
+        assert host.calls[-1][0] == stream
+        return host.calls[-1][1]
+    a, b = call(1), call(2)
+    assert a != b and call(1) == a and call(2) == b
+    c, d = call(1, True), call(1, True)
+    assert len({a, b, c, d}) == 4 and call(1) == a
+    need = host.abi.tp_attn_kv_workspace_bytes(host.attn.plan, host.batch.abi, 16, 0, host.abi.TP_KV_APPEND)
+    assert all(size == need for _, _, size in host.calls)
