@@ -14,11 +14,14 @@ in libtpffn.so.
 The cache keeps a workspace for every stream that it has been used on, and the
 status words that an append needs likewise; a call that is being captured into a
 graph takes its own (from the graph's memory).  So calls on different streams,
-and replays beside them, have nothing in common but the pages.
+and replays beside them, have nothing in common but the pages.  Host threads on
+one stream take turns: the launches of an attention call or a decode pass, which
+follow one another in the stream's workspace, are made under the cache's lock.
 """
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -96,6 +99,7 @@ class PagedKVCache:
         self._statuses = {}    # of the appends, by stream
         self._workspaces = {}  # by stream
         self._last = None      # workspace of the last call, for last_device_error
+        self._turn = threading.Lock()
 
     def _check(self, name, t, dtype, shape):
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
@@ -166,9 +170,11 @@ class PagedKVCache:
         o = torch.empty_like(q) if out is None else self._out("out", out, shape)
         rows = torch.empty((n, self.attn.H), dtype=torch.float32, device=self.device) if lse else None
         st = _current_stream(self._index)
-        ws, need = self._workspace(batch, shared_len, abi.TP_KV_ATTEND, 0, st)
-        rc = abi._lib.tp_attn_paged_fwd(self.attn.plan, self._at, batch._at, shared_len, q.data_ptr(), o.data_ptr(),
-                                        rows.data_ptr() if lse else None, ws.data_ptr(), need, flags, st)
+        with self._turn:
+            ws, need = self._workspace(batch, shared_len, abi.TP_KV_ATTEND, 0, st)
+            rc = abi._lib.tp_attn_paged_fwd(self.attn.plan, self._at, batch._at, shared_len, q.data_ptr(),
+                                            o.data_ptr(), rows.data_ptr() if lse else None, ws.data_ptr(), need,
+                                            flags, st)
         if rc:
             abi.check(rc, "tp_attn_paged_fwd")
         return (o, rows) if lse else o
@@ -182,9 +188,11 @@ class PagedKVCache:
         self._check("x", x, torch.bfloat16, (n, a.d))
         y = self._out("out", out, (n, a.d))
         st = _current_stream(self._index)
-        ws, need = self._workspace(batch, shared_len, abi.TP_KV_DECODE, flags, st)
-        abi.check(abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
-                                         need, flags, st), "tp_attn_decode_fwd")
+        with self._turn:
+            ws, need = self._workspace(batch, shared_len, abi.TP_KV_DECODE, flags, st)
+            rc = abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
+                                        need, flags, st)
+        abi.check(rc, "tp_attn_decode_fwd")
         return y
 
     def last_device_error(self):

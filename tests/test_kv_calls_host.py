@@ -23,9 +23,11 @@ def host(monkeypatch):
 
     rc, plan = abi.tp_attn_plan_create(256, 8, 2, 128, 2, True, abi.TP_BF16)
     assert rc == abi.TP_OK
-    attn = SimpleNamespace(plan=plan, H=8, Hkv=2, hd=128, d=256, info=abi.tp_attn_plan_info(plan),
-                           device=torch.device("cpu", 0))
-    env = SimpleNamespace(abi=abi, stream=1, capturing=False, calls=[], attn=attn, during=lambda at: None)
+    attn = type("Sublayer", (), dict(plan=plan, H=8, Hkv=2, hd=128, d=256, info=abi.tp_attn_plan_info(plan),
+                                     device=torch.device("cpu", 0)))()
+    weights = [torch.zeros(abi.tp_attn_packed_bytes(plan, which), dtype=torch.uint8) for which in (0, 1)]
+    env = SimpleNamespace(abi=abi, stream=1, capturing=False, calls=[], attn=attn, weights=weights,
+                          during=lambda at: None)
     monkeypatch.setattr(kv_cache, "_current_stream", lambda index: env.stream)
     monkeypatch.setattr(kv_cache, "_capturing", lambda: env.capturing)
 
@@ -68,3 +70,30 @@ def test_append_has_a_status_buffer_of_its_stream_and_of_its_capture(host):
     assert len({a, b, c, d}) == 4 and call(1) == a
     need = host.abi.tp_attn_kv_workspace_bytes(host.attn.plan, host.batch.abi, 16, 0, host.abi.TP_KV_APPEND)
     assert all(size == need for _, _, size in host.calls)
+
+
+@pytest.mark.parametrize("what", ["attend", "decode", "both"])
+def test_two_threads_on_one_stream_take_turns(host, what):
+    """A call is several launches: in one workspace, those of two calls must not mix."""
+    inside, met = [], []
+
+    def during(ws):
+        inside.append(ws)
+        time.sleep(0.002)  # the other thread's turn, as where a call into the library lets go of the interpreter
+        met.append(inside.count(ws) > 1)
+        inside.remove(ws)
+    host.during = during
+    q, x = host.rows(8 * 128), host.rows(256)
+
+    def work(decode):
+        for _ in range(20):
+            if decode:
+                host.cache.decode(x, host.batch, *host.weights)
+            else:
+                host.cache.attend(q, host.batch)
+    threads = [threading.Thread(target=work, args=(what == "decode" or (what == "both" and i),)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(met) == 40 and not any(met)
