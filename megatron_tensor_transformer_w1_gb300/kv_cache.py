@@ -100,11 +100,17 @@ class PagedKVCache:
         self._workspaces = {}  # by stream
         self._last = None      # workspace of the last call, for last_device_error
         self._turn = threading.Lock()
+        self._weight_bytes = [abi.tp_attn_packed_bytes(attn.plan, which)
+                              for which in (abi.TP_PACK_COLUMNS, abi.TP_PACK_ROWS)]
 
     def _check(self, name, t, dtype, shape):
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device} is "
                              f"needed, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _check_weights(self, name, t, nbytes):
+        if not isinstance(t, torch.Tensor) or t.device != self.k.device or not t.is_contiguous() or t.nbytes < nbytes:
+            raise ValueError(f"{name}: the packed weight of this sublayer is needed, {nbytes} bytes on {self.device}")
 
     def _out(self, name, t, shape):
         if t is None:
@@ -186,6 +192,8 @@ class PagedKVCache:
                 return self.decode(x, batch, wqkv, wo, shared_len, out, flags)
         a, n = self.attn, batch.n_tokens
         self._check("x", x, torch.bfloat16, (n, a.d))
+        self._check_weights("wqkv", wqkv, self._weight_bytes[0])
+        self._check_weights("wo", wo, self._weight_bytes[1])
         y = self._out("out", out, (n, a.d))
         st = _current_stream(self._index)
         with self._turn:

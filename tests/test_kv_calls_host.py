@@ -42,7 +42,7 @@ def host(monkeypatch):
     def decode(plan, cache, batch, rot, shared, x, wqkv, wo, y, ws, ws_bytes, flags, stream):
         return append(plan, cache, batch, None, x, y, ws.data_ptr(), ws_bytes, flags, stream)
     monkeypatch.setattr(abi, "_lib", SimpleNamespace(
-        tp_attn_kv_append=append, tp_attn_paged_fwd=attend,
+        tp_attn_kv_append=append, tp_attn_paged_fwd=attend, tp_attn_packed_bytes=abi._lib.tp_attn_packed_bytes,
         tp_attn_kv_workspace_bytes=abi._lib.tp_attn_kv_workspace_bytes))
     monkeypatch.setattr(abi, "tp_attn_decode_fwd", decode)
     env.cache = HostCache(attn, 10, 16)
@@ -97,3 +97,21 @@ def test_two_threads_on_one_stream_take_turns(host, what):
     for t in threads:
         t.join()
     assert len(met) == 40 and not any(met)
+
+
+def test_decode_checks_its_weights(host):
+    """Packed weights of another sublayer, layout or place do not reach the kernels."""
+    x = host.rows(256)
+    wqkv, wo = host.weights
+    y = host.cache.decode(x, host.batch, wqkv, wo)
+    assert y.shape == (4, 256) and len(host.calls) == 1
+    for t in (None, wqkv[:-16], torch.zeros(2 * wqkv.numel(), dtype=torch.uint8)[::2], wqkv.to("meta"),
+              wqkv.data_ptr()):
+        with pytest.raises(ValueError, match="wqkv"):
+            host.cache.decode(x, host.batch, t, wo)
+    for t in (None, wo[:-16], wo.to("meta")):
+        with pytest.raises(ValueError, match="wo"):
+            host.cache.decode(x, host.batch, wqkv, t)
+    assert len(host.calls) == 1
+    host.cache.decode(x, host.batch, wqkv.view(torch.bfloat16), wo)  # their bytes count, not their type
+    assert len(host.calls) == 2
