@@ -1442,23 +1442,24 @@ int kv_sizes(const tp_attn_plan* a, const tp_kv_batch* b, int64_t page_size, int
   if (!a || !b || b->n_seqs < 0 || b->n_tokens < 0 || shared_len < 0 || page_size < 1) return TP_ERR_INVALID;
   if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1))) return TP_ERR_UNSUPPORTED;
   if (b->n_seqs > kMaxKvTokens || b->n_tokens > kMaxKvTokens) return TP_ERR_UNSUPPORTED;
-  if (b->n_seqs > 0 && b->n_tokens > 0 && (b->max_new < 1 || b->max_pages < 1)) return TP_ERR_INVALID;
+  const bool work = b->n_seqs > 0 && b->n_tokens > 0;
+  if (work && (b->max_new < 1 || b->max_pages < 1)) return TP_ERR_INVALID;
   if (b->max_pages > (int64_t(1) << 27)) return TP_ERR_UNSUPPORTED;
   if (b->n_tokens * a->H > INT32_MAX / 2 || b->n_seqs * a->Hkv > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
   sp.H = a->H;
   sp.Hkv = a->Hkv;
   sp.T_p = a->T_p;
   sp.causal = a->causal;
-  sp.max_pages = b->max_pages;
+  sp.max_pages = work ? b->max_pages : 0;
   sp.page_size = static_cast<int>(page_size);
   sp.n_seqs = static_cast<int>(b->n_seqs);
   sp.n_tokens = static_cast<int>(b->n_tokens);
-  sp.max_new = static_cast<int>(b->max_new < b->n_tokens ? b->max_new : b->n_tokens);
+  sp.max_new = work ? static_cast<int>(b->max_new < b->n_tokens ? b->max_new : b->n_tokens) : 0;
   sp.cu = b->cu_tokens;
   sp.kv_len = b->kv_len;
   sp.table = b->page_table;
-  if (b->n_seqs > 0 && b->n_tokens > 0 && shared_len > kv_cap(sp)) return TP_ERR_INVALID;
-  sp.shared_len = static_cast<int>(shared_len);
+  if (work && shared_len > kv_cap(sp)) return TP_ERR_INVALID;
+  sp.shared_len = work ? static_cast<int>(shared_len) : 0;
   return TP_OK;
 }
 

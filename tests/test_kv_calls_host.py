@@ -115,3 +115,26 @@ def test_decode_checks_its_weights(host):
     assert len(host.calls) == 1
     host.cache.decode(x, host.batch, wqkv.view(torch.bfloat16), wo)  # their bytes count, not their type
     assert len(host.calls) == 2
+
+
+def test_workspace_of_a_batch_without_work():
+    """A batch without sequences or tokens needs no sizes: whatever its bounds say,
+    the call is made and its workspace is that of no work."""
+    from megatron_tensor_transformer_w1_gb300 import build
+    build.build()
+    from megatron_tensor_transformer_w1_gb300 import tpffn as abi
+    rc, plan = abi.tp_attn_plan_create(256, 8, 2, 128, 2, True, abi.TP_BF16)
+    assert rc == abi.TP_OK
+    cache = abi.KvCache(1 << 20, 1 << 20, 10, 16)
+    try:
+        for n_seqs, n_tokens in ((0, 4), (3, 0), (0, 0)):
+            sizes = []
+            for max_new, max_pages in ((0, 5), (-1, 5), (-(2 ** 40), 5), (0, -1), (0, -(2 ** 40)), (2 ** 40, 5)):
+                b = abi.KvBatch(n_seqs, n_tokens, max_new, max_pages, None, None, None)
+                assert abi.tp_attn_paged_fwd(plan, cache, b, 0, None, None, None, None, 0) == abi.TP_OK
+                sizes.append([abi.tp_attn_kv_workspace_bytes(plan, b, 16, 0, call)
+                              for call in (abi.TP_KV_APPEND, abi.TP_KV_ATTEND, abi.TP_KV_DECODE)])
+            assert all(s == sizes[0] for s in sizes), sizes
+            assert max(max(s) for s in sizes) < 1 << 26
+    finally:
+        abi.tp_attn_plan_destroy(plan)
