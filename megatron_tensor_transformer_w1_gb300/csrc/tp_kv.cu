@@ -114,7 +114,10 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
     const int b = find_seq_warp(B.cu, B.B, row);
     if (b >= B.B) continue;
     const int first = B.cu[b], end = B.cu[b + 1];
-    if (first > row || first < 0) continue;  // no sequence's row: left as it is
+    if (first > row || first < 0) {  // no sequence's row: left as it is
+      if (first < 0) err = DEV_ERR_BATCH;
+      continue;
+    }
     const int pos = B.kv_len[b] - (end - row);
     long long page = -1;
     if (pos >= 0 && pos < B.cap) {

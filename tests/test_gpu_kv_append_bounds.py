@@ -88,3 +88,18 @@ def test_a_bad_length_or_offset_stays_in_its_sequence(new, ctx, H, Hkv, T, page)
         assert torch.equal(s["k"][free], k[free]) and torch.equal(s["v"][free], v[free]), (name, bad)
     cache.append(qkv, batch)
     assert cache.last_device_error() == abi.TP_OK and total == s["n"] - 1
+
+
+def test_a_negative_offset_is_reported():
+    """The tokens of its sequence are not stored: the call says so."""
+    abi = _modules()[0]
+    s, cache, batch, qkv, _ = _make(*BATCHES[0])
+    for i, bad in ((0, -1), (0, -2 ** 31), (1, -3)):
+        was = s["cu"][i].item()
+        s["cu"][i] = bad
+        cache.append(qkv, batch)
+        assert cache.last_device_error() == abi.TP_ERR_BATCH, (i, bad)
+        s["cu"][i] = was
+    s["cu"][0] = 1  # rows in front of the first offset are nobody's: no fault
+    cache.append(qkv, batch)
+    assert cache.last_device_error() == abi.TP_OK
