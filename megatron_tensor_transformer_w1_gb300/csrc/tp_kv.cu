@@ -936,18 +936,27 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 // How a call's attention is launched, and its scratch.
 // At most so many rows to a key/value head: the few-rows kernel.  32 sequences
 // of 4000 keys (8 heads, 531 MB): 16 rows 89 us, 32 rows 97 us against 101 us
-// of the many-rows kernel, 64 rows 140 against 103; 64 sequences of 300 keys,
-// 32 rows: 27 against 36.
+// of the many-rows kernel; 64 sequences of 300 keys, 32 rows: 27 against 36.  A
+// form of it for 64 rows took 140 against 103 us on the long sequences; where
+// only starting the kernel counts it was the faster one (4 sequences of 300 keys,
+// 17 against 21 us), which was not worth a third form.
 constexpr int kFewRows = 32;
 // At most so many rows to a key/value head, on average over the sequences, for
 // the shared keys to be taken together.
 constexpr int kShareRows = 64;
-// At least so many bytes of shared keys and values that would be read again.
-// Single tokens, 8 key heads, 300 own keys each, together / each on its own: 64
-// sequences behind 1024 keys (264 MB saved) 31 / 48 us, 8 behind 4096 (117 MB)
-// 22 / 26 us, 64 behind 256 (66 MB) 27 / 28 us, 4 behind 4096 (50 MB) 21 / 19 us;
-// with more own rows, where the two kernels run in turn, it is even at 90 MB.
-constexpr double kShareBytes = 96 << 20;
+// At least so many bytes of shared keys and values that would be read again: what
+// a kernel and the join cost (12 us of reads), and for each row its parts.  Both
+// ways were timed for 1200 random batches (1 to 16 key heads, groups of 1 to 8, 1
+// to 32 new tokens, 2 to 256 sequences, 24 MB to 1 GB saved, no to 4096 own keys),
+// with the caches flushed and with the keys left in L2 where they fit: these two
+// numbers have the times within 1 % of the better way's on average both times, and
+// within 28 % at most; without the rows' share, from 96 MiB on, 2 % and 139 %.
+// Together / each on its own, 8 key heads, 300 own keys: 64 single tokens (4 query
+// heads to a key head) behind 512 keys (132 MB saved, 105 asked for) 30 / 32 us,
+// behind 256 (66 MB) 28 / 25 us, 16 behind 1600 (98 MB, 89) 24 / 27 us, behind 1088
+// (67 MB) 21.5 / 22.5 us; 64 of 4 tokens behind 512 (132 MB, 166) 32 / 35 us, behind
+// 384 31 - 36 / 31 us; 128 of 16 tokens behind 256 (133 MB, 740) 108 / 66 us.
+constexpr double kShareBytes = 80 << 20, kShareRowBytes = 10000;
 struct AttendPlan {
   bool share = false;
   kv::Parts own, shared;      // the pointers as offsets from the scratch's start
@@ -1008,10 +1017,9 @@ AttendPlan attend_plan(const KvSpec& a, int num_sms, char* ws) {
   };
   // Where the sequences bring many rows each, their products bound the time,
   // not the reads of the shared keys.
-  // Taking the shared keys together pays where it saves enough reads: it costs a
-  // kernel more and the join, some 10 us.
+  // Taking the shared keys together pays where it saves enough reads.
   const double saved = (a.n_seqs - 1.0) * a.shared_len * a.Hkv * (kv::HD * 4);
-  P.share = saved >= kShareBytes && a.n_tokens * G <= static_cast<int64_t>(kShareRows) * a.n_seqs;
+  P.share = saved >= kShareBytes + kShareRowBytes * rows && a.n_tokens * G <= static_cast<int64_t>(kShareRows) * a.n_seqs;
   part(P.own, a.max_new * G, static_cast<size_t>(a.n_seqs) + 1);
   if (P.share) part(P.shared, a.n_tokens * G, 2);
   if (P.share && P.shared.rt && !P.own.rt) split_sms(a, num_sms, P);

@@ -24,7 +24,7 @@ CASES = [  # new, ctx, H, Hkv, T, page, shared, kernels
     ([1] * 4, [3, 0, 200, 65], 32, 8, 8, 32, 11000, [S_FEW, FEW]),
     ([2] * 4, [3, 0, 200, 65], 32, 8, 4, 32, 11000, [S_FEW, FEW]),
     ([1] * 64, [(i * 29) % 200 for i in range(64)], 32, 8, 8, 64, 700, [S_MANY, FEW]),
-    ([9 + i % 8 for i in range(30)], [(61 * i) % 300 for i in range(30)], 32, 8, 8, 16, 1200, [S_MANY, MANY]),
+    ([9 + i % 8 for i in range(30)], [(61 * i) % 300 for i in range(30)], 32, 8, 8, 16, 1900, [S_MANY, MANY]),
     ([40, 3, 90, 0, 260], [7, 500, 0, 129, 30], 8, 2, 2, 16, 0, [MANY]),
     ([50, 60], [0, 900], 8, 2, 2, 64, 300, [MANY]),   # shared keys that are not worth it
     ([1] * 40, [50 * i for i in range(40)], 8, 2, 2, 16, 0, [FEW]),

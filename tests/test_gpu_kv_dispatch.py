@@ -43,9 +43,17 @@ CASES = [  # new, ctx, H, Hkv, T, page, shared, causal, rows behind the last seq
     # more sequences than a block has lanes to look at them
     ([1] * 200, [(i * 37) % 150 for i in range(200)], 8, 2, 2, 16, 700, True, 0, [S_MANY, FEW]),
     ([i % 3 for i in range(300)], [(i * 53) % 90 for i in range(300)], 4, 2, 2, 32, 450, True, 2, [S_MANY, FEW]),
-    ([9 + i % 8 for i in range(150)], [(i * 61) % 200 for i in range(150)], 8, 2, 2, 16, 900, True, 0, [S_MANY, MANY]),
+    ([9 + i % 8 for i in range(150)], [(i * 61) % 200 for i in range(150)], 8, 2, 2, 16, 1700, True, 0, [S_MANY, MANY]),
     ([int(i % 20 == 3) for i in range(150)], [(i * 37) % 150 for i in range(150)], 8, 2, 2, 16, 900, True, 0,
      [S_FEW, FEW]),
+    # few rows and many of single sequences behind keys that all share; ragged own rows
+    ([9, 1] * 10, [0] * 20, 40, 5, 5, 8, 2700, True, 0, [S_MANY, MANY]),
+    ([9 + i % 8 for i in range(30)], [(61 * i) % 700 for i in range(30)], 32, 8, 8, 16, 1900, True, 2, [S_MANY, MANY]),
+    # as many bytes of shared keys, but more rows to join than those reads cost
+    ([16] * 128, [i % 40 for i in range(128)], 32, 8, 8, 64, 256, True, 0, [MANY]),
+    ([16] * 4, [i for i in range(4)], 32, 8, 8, 64, 9600, True, 0, [S_MANY, MANY]),
+    ([1] * 64, [i for i in range(64)], 32, 8, 8, 64, 320, True, 0, [FEW]),
+    ([1] * 64, [i for i in range(64)], 32, 8, 8, 64, 512, True, 0, [S_MANY, FEW]),
     ([int(i % 20 == 3) for i in range(150)], [(i * 37) % 150 for i in range(150)], 8, 2, 2, 16, 0, True, 0, [FEW]),
 ]
 
@@ -67,3 +75,55 @@ def test_at_the_borders_of_the_kernels(new, ctx, H, Hkv, T, page, shared, causal
     for _ in range(2):
         again, again_lse = cache.attend(q, batch, shared_len=shared, lse=True)
         assert torch.equal(o[:rows], again[:rows]) and torch.equal(lse[:rows], again_lse[:rows])
+
+
+@pytest.mark.parametrize("new,shared", [(1, 1700), (5, 2100)])
+def test_shared_keys_longer_than_sequences(new, shared):
+    """Behind shared keys that some sequences do not reach the end of: cut rows, no
+    keys at all, more new tokens than keys."""
+    abi = _modules()[0]
+    B, Hkv, H = 60, 2, 8
+    s = ref.make_batch([new] * B, [3] * B, Hkv, 16, shared=shared, seed=6)
+    for b, n in ((0, shared - 50), (1, 0), (2, 1), (3, 3), (7, shared - 1), (8, shared + 1), (59, 64)):
+        s["lens"][b] = n
+    s["kv_len"].copy_(torch.tensor(s["lens"]))
+    cache, batch = _cache(s, H, 2)
+    q = _q(s["n"], H, 2)
+    o, lse = cache.attend(q, batch, shared_len=shared, lse=True, flags=abi.TP_FLAG_TIMING)
+    assert [name for name, _ in abi.tp_attn_kernel_times(cache.attn.plan)] == [S_MANY, FEW, "kv_combine"]
+    assert cache.last_device_error() == 0
+    check_attend(s, q, H, o, lse)
+
+
+def test_shared_keys_of_many_own_rows_bad_offsets():
+    """Offsets that descend, or begin behind the first row, leave rows that the shared
+    keys' work does not cover: what they get is unspecified, the call reports it and
+    the sequences' other rows, where there are any, are as ever."""
+    abi = _modules()[0]
+    B, new, Hkv, H, shared = 40, 8, 8, 64, 1920
+    s = ref.make_batch([new] * B, [3] * B, Hkv, 64, shared=shared, seed=26)
+    cache, batch = _cache(s, H, 8)
+    q = _q(s["n"], H, 12)
+    good = cache.attend(q, batch, shared_len=shared, flags=abi.TP_FLAG_TIMING)
+    assert [name for name, _ in abi.tp_attn_kernel_times(cache.attn.plan)] == [S_MANY, MANY, "kv_combine"]
+    assert cache.last_device_error() == abi.TP_OK
+    check_attend(s, q, H, good, None)
+    keep = s["cu"].clone()
+    for at, bad in ((B, 3), (B, 0), (B, -2 ** 31), (B // 2, 2 ** 31 - 1), (1, 300), (0, -7), (B - 1, 5)):
+        s["cu"][at] = bad
+        cache.attend(q, batch, shared_len=shared)
+        assert cache.last_device_error() == abi.TP_ERR_BATCH, (at, bad)
+        s["cu"].copy_(keep)
+    for bad in (list(range(320, -1, -8)), [0, 320] * 20 + [0], [160] * 41, [2 ** 31 - 1] * 41, [-1] * 41):
+        s["cu"].copy_(torch.tensor(bad))
+        cache.attend(q, batch, shared_len=shared)
+        assert cache.last_device_error() == (abi.TP_OK if bad[0] == 160 else abi.TP_ERR_BATCH), bad
+        s["cu"].copy_(keep)
+    s["cu"][0] = 5  # the first sequence's last three rows; those before are nobody's
+    o = torch.full_like(good, 7.0)
+    cache.attend(q, batch, shared_len=shared, out=o)
+    assert cache.last_device_error() == abi.TP_OK and (o[:5] == 7).all()
+    check_attend(dict(s, new=[3] + [new] * (B - 1), cu=s["cu"] - 5), q[5:], H, o[5:], None)
+    s["cu"].copy_(keep)
+    assert torch.equal(cache.attend(q, batch, shared_len=shared), good)
+    assert cache.last_device_error() == abi.TP_OK

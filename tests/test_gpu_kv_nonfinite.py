@@ -25,7 +25,7 @@ BATCHES = [  # new, ctx, H, Hkv, T, page, shared, causal
     ([1, 1, 1, 1], [7, 0, 130, 64], 32, 8, 8, 32, 8704, True),           # shared keys of 16 rows
     ([2, 1, 2, 1], [7, 0, 130, 64], 32, 8, 8, 32, 8704, True),           # of 24 rows
     ([1] * 64, [(i * 29) % 200 for i in range(64)], 32, 8, 8, 16, 700, True),   # of many, own rows few
-    ([9 + i % 8 for i in range(30)], [(61 * i) % 300 for i in range(30)], 32, 8, 8, 16, 1000, True),  # both many
+    ([9 + i % 8 for i in range(30)], [(61 * i) % 300 for i in range(30)], 32, 8, 8, 16, 1900, True),  # both many
 ]
 
 
@@ -116,7 +116,7 @@ def test_scores_that_are_all_minus_infinity(new, ctx, H, Hkv, T, page, shared, c
     assert torch.equal(got[~hit], o[~hit]) and torch.equal(got_lse[~hit], lse[~hit])
 
 
-@pytest.mark.parametrize("new,shared", [([9, 1, 5, 3], 0), ([90, 1, 50, 30], 0), ([2] * 30, 1000), ([9] * 30, 1000)])
+@pytest.mark.parametrize("new,shared", [([9, 1, 5, 3], 0), ([90, 1, 50, 30], 0), ([2] * 30, 1000), ([9] * 30, 1600)])
 def test_rows_without_keys_beside_scores_of_minus_infinity(new, shared):
     """Rows that see no key get zeros, those that see only such scores NaN."""
     H, Hkv = 32, 8
