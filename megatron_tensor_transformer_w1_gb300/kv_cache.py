@@ -30,6 +30,7 @@ from . import tpffn as abi
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 _capturing = torch._C._cuda_isCurrentStreamCapturing
+_REFUSED = (abi.TP_ERR_INVALID, abi.TP_ERR_UNSUPPORTED, abi.TP_ERR_ALIGN)  # without any work
 
 
 class KVBatch:
@@ -133,9 +134,15 @@ class PagedKVCache:
             need = max(16, abi.tp_attn_kv_workspace_bytes(self.attn.plan, batch.abi, self.page_size, shared_len, call,
                                                           flags))
             batch._bytes[key] = need
-        ws = self._buffer(self._workspaces, need, stream)
-        self._last = ws if batch.n_tokens and batch.n_seqs else None
-        return ws, need
+        return self._buffer(self._workspaces, need, stream), need
+
+    def _done(self, rc, where, batch, ws):
+        """After a call: what last_device_error reads is the workspace of the last
+        one that enqueued work."""
+        if rc not in _REFUSED:
+            self._last = ws if batch.n_tokens and batch.n_seqs else None
+        if rc:
+            abi.check(rc, where)
 
     def _elsewhere(self, batch):
         """Whether the cache's device is not the current one."""
@@ -157,11 +164,9 @@ class PagedKVCache:
         q = self._out("q", q, (n, self._q_width))
         st = _current_stream(self._index)
         status = self._buffer(self._statuses, self._status_bytes, st)
-        self._last = status if n and batch.n_seqs else None
         rc = abi._lib.tp_attn_kv_append(self.attn.plan, self._at, batch._at, self._rot_at, qkv.data_ptr(),
                                         q.data_ptr(), status.data_ptr(), self._status_bytes, flags, st)
-        if rc:
-            abi.check(rc, "tp_attn_kv_append")
+        self._done(rc, "tp_attn_kv_append", batch, status)
         return q
 
     def attend(self, q, batch, shared_len=0, lse=False, out=None, flags=0):
@@ -181,8 +186,7 @@ class PagedKVCache:
             rc = abi._lib.tp_attn_paged_fwd(self.attn.plan, self._at, batch._at, shared_len, q.data_ptr(),
                                             o.data_ptr(), rows.data_ptr() if lse else None, ws.data_ptr(), need,
                                             flags, st)
-        if rc:
-            abi.check(rc, "tp_attn_paged_fwd")
+        self._done(rc, "tp_attn_paged_fwd", batch, ws)
         return (o, rows) if lse else o
 
     def decode(self, x, batch, wqkv, wo, shared_len=0, out=None, flags=0):
@@ -200,7 +204,7 @@ class PagedKVCache:
             ws, need = self._workspace(batch, shared_len, abi.TP_KV_DECODE, flags, st)
             rc = abi.tp_attn_decode_fwd(a.plan, self._abi, batch.abi, self._rot, shared_len, x, wqkv, wo, y, ws,
                                         need, flags, st)
-        abi.check(rc, "tp_attn_decode_fwd")
+        self._done(rc, "tp_attn_decode_fwd", batch, ws)
         return y
 
     def last_device_error(self):

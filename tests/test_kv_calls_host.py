@@ -26,7 +26,7 @@ def host(monkeypatch):
     attn = type("Sublayer", (), dict(plan=plan, H=8, Hkv=2, hd=128, d=256, info=abi.tp_attn_plan_info(plan),
                                      device=torch.device("cpu", 0)))()
     weights = [torch.zeros(abi.tp_attn_packed_bytes(plan, which), dtype=torch.uint8) for which in (0, 1)]
-    env = SimpleNamespace(abi=abi, stream=1, capturing=False, calls=[], attn=attn, weights=weights,
+    env = SimpleNamespace(abi=abi, stream=1, capturing=False, status=abi.TP_OK, calls=[], attn=attn, weights=weights,
                           during=lambda at: None)
     monkeypatch.setattr(kv_cache, "_current_stream", lambda index: env.stream)
     monkeypatch.setattr(kv_cache, "_capturing", lambda: env.capturing)
@@ -34,7 +34,7 @@ def host(monkeypatch):
     def append(plan, cache, batch, rot, qkv, q, ws, ws_bytes, flags, stream):
         env.calls.append((stream, ws, ws_bytes))
         env.during(ws)
-        return abi.TP_OK
+        return env.status
 
     def attend(plan, cache, batch, shared, q, o, lse, ws, ws_bytes, flags, stream):
         return append(plan, cache, batch, None, q, o, ws, ws_bytes, flags, stream)
@@ -43,7 +43,8 @@ def host(monkeypatch):
         return append(plan, cache, batch, None, x, y, ws.data_ptr(), ws_bytes, flags, stream)
     monkeypatch.setattr(abi, "_lib", SimpleNamespace(
         tp_attn_kv_append=append, tp_attn_paged_fwd=attend, tp_attn_packed_bytes=abi._lib.tp_attn_packed_bytes,
-        tp_attn_kv_workspace_bytes=abi._lib.tp_attn_kv_workspace_bytes))
+        tp_attn_kv_workspace_bytes=abi._lib.tp_attn_kv_workspace_bytes,
+        tp_ffn_status_string=abi._lib.tp_ffn_status_string))
     monkeypatch.setattr(abi, "tp_attn_decode_fwd", decode)
     env.cache = HostCache(attn, 10, 16)
     i32 = lambda *sh: torch.zeros(*sh, dtype=torch.int32)
@@ -138,3 +139,35 @@ def test_workspace_of_a_batch_without_work():
             assert max(max(s) for s in sizes) < 1 << 26
     finally:
         abi.tp_attn_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("what", ["append", "attend", "decode"])
+def test_a_refused_call_leaves_the_last_status_alone(host, what):
+    """last_device_error reads what the last call wrote: one that was refused wrote nothing,
+    one that ran and failed did."""
+    def call():
+        if what == "append":
+            host.cache.append(host.rows(12 * 128), host.batch)
+        elif what == "attend":
+            host.cache.attend(host.rows(8 * 128), host.batch)
+        else:
+            host.cache.decode(host.rows(256), host.batch, *host.weights)
+        return host.cache._last
+    for status in ("INVALID", "UNSUPPORTED", "ALIGN"):
+        host.status = getattr(host.abi, "TP_ERR_" + status)
+        with pytest.raises(host.abi.TPFFNError):
+            call()
+        assert host.cache._last is None
+    host.status = host.abi.TP_OK
+    host.stream = 5
+    good = call()
+    assert good.data_ptr() == host.calls[-1][1]
+    host.stream, host.status = 6, host.abi.TP_ERR_INVALID
+    with pytest.raises(host.abi.TPFFNError):
+        call()
+    assert host.cache._last is good
+    for status in ("BATCH", "TIMEOUT"):
+        host.status = getattr(host.abi, "TP_ERR_" + status)
+        with pytest.raises(host.abi.TPFFNError):
+            call()
+        assert host.cache._last.data_ptr() == host.calls[-1][1]
