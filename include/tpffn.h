@@ -425,9 +425,12 @@ TPFFN_API size_t tp_attn_kv_workspace_bytes(const tp_attn_plan* plan, const tp_k
 /* Append: from the packed projections qkv [n_tokens][qkv_width] of the new
  * tokens, stores the rotated keys and the values in their pages and writes
  * the rotated queries to q [n_tokens][H*hd] (head h in columns
- * [h*hd, (h+1)*hd)).  rotation NULL: none.  A token whose position is
- * negative (more new tokens than kv_len) has no place: its q row is zero and
- * nothing is stored.  One launch; flags: TP_FLAG_SYNC, TP_FLAG_TIMING.
+ * [h*hd, (h+1)*hd)), which does not overlap qkv.  rotation NULL: none.  A token
+ * whose position is negative (more new tokens than kv_len) has no place: its q
+ * row is zero and nothing is stored, which is reported as TP_ERR_BATCH, since
+ * its key and value are lost (attention over such a batch has nothing to
+ * report: the rows see no key).  To leave a sequence out of a batch of a fixed
+ * size, give it no new tokens.  One launch; flags: TP_FLAG_SYNC, TP_FLAG_TIMING.
  * Errors: TP_ERR_INVALID (NULL, sizes, workspace too small, rotary_dim),
  * TP_ERR_UNSUPPORTED (page_size; n_tokens or n_seqs above 2^24),
  * TP_ERR_ALIGN.  n_tokens or n_seqs 0: TP_OK, no work. */
@@ -437,7 +440,7 @@ TPFFN_API int tp_attn_kv_append(const tp_attn_plan* plan, const tp_kv_cache* cac
 
 /* Attention of q [n_tokens][H*hd] over the cache: new token i of sequence b
  * (position t) sees keys 0 .. t (causal plans) or all kv_len[b] keys.
- * o [n_tokens][H*hd]; lse [n_tokens][H] fp32 or NULL: log2 of
+ * o [n_tokens][H*hd], which may be q itself; lse [n_tokens][H] fp32 or NULL: log2 of
  * sum_j 2^(s_ij log2 e), as in tp_attn_core_fwd.  A row that sees no key gets
  * o = 0 and lse = -inf; one with a score of NaN or +inf gets NaN in both, one
  * whose scores are all -inf gets NaN in o and lse = -inf.
