@@ -9,11 +9,13 @@
 // tp_kv.cuh) and leaves the parts of items that it shares with its
 // neighbours to kv_combine_kernel.
 //
-// With R rows a key/value head does 2 R products per byte of K and V, so from
-// some 128 rows on the tensor cores bound the time, not the memory: 4 x 128^3
-// products a step of two row tiles, 2048 cycles at 4096 a cycle.  The two
-// row tiles take turns: while one tile's scores go through the softmax, the
-// products of the other run.  A block has
+// With R rows a key takes 256 R multiply-adds for its 512 bytes, R flops a byte:
+// at 1898 TFLOP/s and 6773 GB/s the products bound the time of own keys from
+// some 280 rows on (fewer rows of a tile of 128 cost as much as a full one, and
+// keys that lie in L2 or are shared cost less to read).  A step of two row tiles
+// has 4 x 128^3 multiply-adds, 2048 cycles at 4096 a cycle.  The two row tiles
+// take turns: while one tile's scores go through the softmax, the products of
+// the other run.  A block has
 //  * warp 0: copies K and V tiles by TMA, a copy for each page (or 128 keys of
 //    a longer one), into a ring of four 32 KB slots;
 //  * warps 1 and 2: a lane of each issues tcgen05.mma for row tile t = 0, 1:
