@@ -946,11 +946,11 @@ constexpr int kFewRows = 32;
 constexpr int kShareRows = 64;
 // At least so many bytes of shared keys and values that would be read again: what
 // a kernel and the join cost (12 us of reads), and for each row its parts.  Both
-// ways were timed for 1200 random batches (1 to 16 key heads, groups of 1 to 8, 1
-// to 32 new tokens, 2 to 256 sequences, 24 MB to 1 GB saved, no to 4096 own keys),
+// ways were timed for 1400 random batches (1 to 16 key heads, groups of 1 to 8, 1
+// to 32 new tokens, 2 to 256 sequences, 14 MB to 1 GB saved, no to 4096 own keys),
 // with the caches flushed and with the keys left in L2 where they fit: these two
 // numbers have the times within 1 % of the better way's on average both times, and
-// within 28 % at most; without the rows' share, from 96 MiB on, 2 % and 139 %.
+// within 33 % at most; without the rows' share, from 96 MiB on, 2 % and 139 %.
 // Together / each on its own, 8 key heads, 300 own keys: 64 single tokens (4 query
 // heads to a key head) behind 512 keys (132 MB saved, 105 asked for) 30 / 32 us,
 // behind 256 (66 MB) 28 / 25 us, 16 behind 1600 (98 MB, 89) 24 / 27 us, behind 1088
