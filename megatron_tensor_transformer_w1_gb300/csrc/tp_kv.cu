@@ -946,8 +946,8 @@ constexpr int kFewRows = 32;
 // them take longer than their reads.  Of 300 random batches of 40 to 500 rows 38 of
 // more than 64 pass the bound below; together they are 0.67 to 2.0 times as fast
 // (median 1.07; 27 sequences of 67 tokens, 8 key heads, behind 21184 keys 181 / 366
-// us, 13 of 96 rows of one key head behind 16576, with 2000 own keys, 58 / 39 us), the faster ones
-// behind some 20000 keys and without own ones.
+// us, 13 of 96 rows of one key head behind 16576, with 2000 own keys, 58 / 39 us),
+// the faster ones behind some 20000 keys and without own ones.
 constexpr int kShareRows = 64;
 // At least so many bytes of shared keys and values that would be read again: what
 // a kernel and the join cost (12 us of reads), and for each row its parts.  Both
