@@ -415,10 +415,10 @@ typedef struct tp_kv_rotation {
 } tp_kv_rotation;
 
 /* Workspace of one call (queried on the device that runs it): `call` is
- * TP_KV_APPEND, TP_KV_ATTEND or TP_KV_DECODE; shared_len and flags as for the
- * call (0 where it has none).  0 for arguments that the call would refuse.
+ * TP_KV_APPEND, TP_KV_ATTEND, TP_KV_DECODE or TP_KV_DECODE4 (tp_attn_decode_fwd4);
+ * shared_len and flags as for the call (0 where it has none).  0 for arguments that the call would refuse.
  * Calls that may run at the same time need workspaces of their own. */
-enum { TP_KV_APPEND = 0, TP_KV_ATTEND = 1, TP_KV_DECODE = 2 };
+enum { TP_KV_APPEND = 0, TP_KV_ATTEND = 1, TP_KV_DECODE = 2, TP_KV_DECODE4 = 3 };
 TPFFN_API size_t tp_attn_kv_workspace_bytes(const tp_attn_plan* plan, const tp_kv_batch* batch, int64_t page_size,
                                             int64_t shared_len, int call, int flags);
 
@@ -471,6 +471,75 @@ TPFFN_API int tp_attn_decode_fwd(const tp_attn_plan* plan, const tp_kv_cache* ca
  * workspace reported: TP_OK, TP_ERR_BATCH, TP_ERR_TIMEOUT or TP_ERR_CUDA.
  * Only after a call that enqueued work. */
 TPFFN_API int tp_attn_kv_last_device_error(const tp_attn_plan* plan, const void* workspace, tp_stream_t stream);
+
+/* ------------------------------------------------------------ 4-bit weights
+ *
+ * Weights of the serving passes in four bits: a group of `group` (32, 64 or
+ * 128) consecutive input features of an output row has one scale s in bf16, an
+ * element is (code - 8) * s with a code of 0..15.  Every operation is bf16 only.
+ *
+ * Natural layout of a matrix [rows][cols]: codes [rows][(cols + 1) / 2] bytes,
+ * the even column in the low half; scales [rows][segments * ceil(cols /
+ * segments / group)] bf16.  `segments` equal parts of a row (it divides cols)
+ * start their groups anew: T_p for the row-sharded W2 and W_O, so that no group
+ * crosses shards, 1 for the others.  Codes from elsewhere are given in the same
+ * form.
+ */
+
+/* Quantises W [rows][cols] bf16: s = bf16(max |w| / 7) and code = rint(w / s)
+ * + 8, ties to even, so codes lie in 1..15; 8 where s is 0.  A group with an
+ * infinity or a NaN gets that for its scale.  One launch, two where cols /
+ * segments is no multiple of 16.
+ * Dequantising: W = bf16((code - 8) * s).
+ * Errors: TP_ERR_INVALID (NULL, sizes below 0, segments < 1 or not dividing
+ * cols, group), TP_ERR_UNSUPPORTED (cols above 2^30, rows * cols above 2^46),
+ * TP_ERR_ALIGN.  rows or cols 0: TP_OK, no work. */
+TPFFN_API int tp_quantize4(const void* W, int64_t rows, int64_t cols, int64_t segments, int group, void* codes,
+                           void* scales, tp_stream_t stream);
+TPFFN_API int tp_dequantize4(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t segments,
+                             int group, void* W, tp_stream_t stream);
+
+/* The layout that the products read, for all shards at once: TP_PACK_COLUMNS
+ * holds W1 (and W3), TP_PACK_ROWS W2.  Natural codes and scales as above, W2's
+ * with segments = T_p.  codes3 and scales3: SwiGLU only.  The packed buffer is
+ * good for any number of tokens; padding is part of it.
+ * tp_ffn_packed4_bytes is 0 for a NULL or fp32 plan, an unknown group or
+ * `which`, and TP_PACK_COLUMNS of act NONE; the others return TP_ERR_INVALID
+ * there, and TP_ERR_ALIGN. */
+TPFFN_API size_t tp_ffn_packed4_bytes(const tp_ffn_plan* plan, int which, int group);
+TPFFN_API int tp_ffn_shard_columns4(const tp_ffn_plan* plan, int group, const void* codes1, const void* scales1,
+                                    const void* codes3, const void* scales3, void* packed, tp_stream_t stream);
+TPFFN_API int tp_ffn_shard_rows4(const tp_ffn_plan* plan, int group, const void* codes2, const void* scales2,
+                                 void* packed, tp_stream_t stream);
+TPFFN_API int tp_ffn_unshard_columns4(const tp_ffn_plan* plan, int group, const void* packed, void* codes1,
+                                      void* scales1, void* codes3, void* scales3, tp_stream_t stream);
+TPFFN_API int tp_ffn_unshard_rows4(const tp_ffn_plan* plan, int group, const void* packed, void* codes2,
+                                   void* scales2, tp_stream_t stream);
+
+/* tp_ffn_fwd for inference from packed 4-bit weights (w13_4 NULL for act NONE;
+ * both of the same group): x, b1, b2 and y as there.  The shards are summed in
+ * the order t = 0..T_p-1; results do not change from run to run.  A product is
+ * summed in 32 bits within a group, times its scale, over the groups in 32 bits;
+ * the hidden activations are rounded to bf16.
+ * flags: TP_FLAG_SYNC, TP_FLAG_TIMING; the TP_SUM_* choices make no difference.
+ * Errors as tp_ffn_fwd; TP_ERR_UNSUPPORTED for fp32 plans. */
+TPFFN_API size_t tp_ffn_workspace4_bytes(const tp_ffn_plan* plan, int64_t n_tokens, int flags);
+TPFFN_API int tp_ffn_fwd4(const tp_ffn_plan* plan, int group, int64_t n_tokens, const void* x, const void* w13_4,
+                          const void* w2_4, const void* b1, const void* b2, void* y, void* workspace,
+                          size_t workspace_bytes, int flags, tp_stream_t stream);
+
+/* The same for the attention sublayer: Wq, Wk, Wv (segments 1) into the packed
+ * q/k/v projection, Wo (segments = T_p) into the packed W_O. */
+TPFFN_API size_t tp_attn_packed4_bytes(const tp_attn_plan* plan, int which, int group);
+TPFFN_API int tp_attn_shard_weights4(const tp_attn_plan* plan, int group, const void* const codes[4],
+                                     const void* const scales[4], void* wqkv_4, void* wo_4, tp_stream_t stream);
+TPFFN_API int tp_attn_unshard_weights4(const tp_attn_plan* plan, int group, const void* wqkv_4, const void* wo_4,
+                                       void* const codes[4], void* const scales[4], tp_stream_t stream);
+/* tp_attn_decode_fwd from packed 4-bit weights. */
+TPFFN_API int tp_attn_decode_fwd4(const tp_attn_plan* plan, const tp_kv_cache* cache, const tp_kv_batch* batch,
+                                  const tp_kv_rotation* rotation, int64_t shared_len, int group, const void* x,
+                                  const void* wqkv_4, const void* wo_4, void* y, void* workspace,
+                                  size_t workspace_bytes, int flags, tp_stream_t stream);
 
 /* ------------------------------------------------ forward without allocation */
 

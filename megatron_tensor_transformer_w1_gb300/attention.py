@@ -9,12 +9,14 @@ in libtpffn.so ("7.9 Tensor and pipeline parallelism (TP, PP)", §2.2
     y, saved = attn.forward(x, B, S, wqkv, wo)
     g = attn.backward(x, B, S, wqkv, wo, saved, dy)   # dx, dwqkv, dwo
     y = attn.decode(x, cache, batch, wqkv, wo)        # serving, over a kv_cache.PagedKVCache
+    y = attn.decode(x, cache, batch, *attn.pack4(Wq, Wk, Wv, Wo))  # the same from 4-bit weights
 """
 from __future__ import annotations
 
 import torch
 
 from . import tpffn as abi
+from . import weights4 as w4
 
 
 class TensorParallelAttention:
@@ -65,6 +67,43 @@ class TensorParallelAttention:
                   "unshard_weights")
         return Wq, Wk, Wv, Wo
 
+    def _key4(self):
+        return ("attention", self.d, self.H, self.Hkv, self.hd, self.T_p)
+
+    def _shapes4(self):
+        """(rows, columns, segments) of Wq, Wk, Wv, Wo."""
+        nq, nk = self.H * self.hd, self.Hkv * self.hd
+        return ((nq, self.d, 1), (nk, self.d, 1), (nk, self.d, 1), (self.d, nq, self.T_p))
+
+    def pack4(self, Wq, Wk, Wv, Wo, group=None):
+        """4-bit weights for decode(), (wqkv_4, wo_4).  Each weight is a bfloat16 matrix,
+        which is quantised, or a weights4.Codes4, Wo's with T_p segments.  group: 32, 64
+        or 128 (the default, or the codes' own)."""
+        dev = w4.full_device(self.device)
+        weights = (Wq, Wk, Wv, Wo)
+        group = w4.group_of(group, *weights)
+        with torch.cuda.device(dev):
+            c = [w4.as_codes(name, W, rows, cols, group, segments, dev)
+                 for name, W, (rows, cols, segments) in zip(("Wq", "Wk", "Wv", "Wo"), weights, self._shapes4())]
+            packed = [w4.Packed4(torch.empty(abi.tp_attn_packed4_bytes(self.plan, which, group), dtype=torch.uint8, device=dev),
+                                 group, which, self._key4()) for which in (abi.TP_PACK_COLUMNS, abi.TP_PACK_ROWS)]
+            abi.check(abi.tp_attn_shard_weights4(self.plan, group, [a.codes for a in c], [a.scales for a in c],
+                                                 packed[0].data, packed[1].data, torch.cuda.current_stream()),
+                      "shard_weights4")
+        return tuple(packed)
+
+    def unpack4(self, wqkv_4, wo_4):
+        """The codes of Wq, Wk, Wv and Wo."""
+        dev = w4.full_device(self.device)
+        w4.check_packed("wqkv_4", wqkv_4, abi.TP_PACK_COLUMNS, self._key4(), dev)
+        w4.check_packed("wo_4", wo_4, abi.TP_PACK_ROWS, self._key4(), dev, wqkv_4.group)
+        with torch.cuda.device(dev):
+            c = [w4.Codes4.empty(rows, cols, wo_4.group, segments, dev) for rows, cols, segments in self._shapes4()]
+            abi.check(abi.tp_attn_unshard_weights4(self.plan, wo_4.group, wqkv_4.data, wo_4.data, [a.codes for a in c],
+                                                   [a.scales for a in c], torch.cuda.current_stream()),
+                      "unshard_weights4")
+        return tuple(c)
+
     # ------------------------------------------------------------ passes
     def saved_views(self, saved, B, S):
         """(qkv [B*S, qkv_width], c [B*S, H*hd], lse [B*H, S_pad]) views of `saved`."""
@@ -98,7 +137,8 @@ class TensorParallelAttention:
     def decode(self, x, cache, batch, wqkv, wo, shared_len=0, fused=False, overlap=False, flags=0):
         """Serving pass over a PagedKVCache of this sublayer: projects the new tokens
         x [n_tokens, d] of a batch, appends their keys and values, attends to the
-        cache and projects the head outputs: y [n_tokens, d]."""
+        cache and projects the head outputs: y [n_tokens, d].  wqkv, wo: of pack() or
+        both of pack4()."""
         if cache.attn is not self:
             raise ValueError("the cache belongs to another attention sublayer")
         flags |= (abi.TP_SUM_FUSED if fused else 0) | (abi.TP_SUM_OVERLAP if overlap else 0)

@@ -1544,6 +1544,163 @@ DecodeWs decode_ws(const tp_attn_plan* a, const KvSpec& sp, int flags) {
   L.total = off;
   return L;
 }
+
+// ------------------------------------------------------------ 4-bit weights
+bool w4_group(int g) { return g == 32 || g == 64 || g == 128; }
+int64_t w4_sp(const tp_ffn_plan* p) { return (p->s + 127) / 128 * 128; }  // hidden slots of a shard
+W4Shape w4_up(const tp_ffn_plan* p, int group) {
+  W4Shape m;
+  m.rows_kind = p->act == TP_ACT_SWIGLU ? W4_GATED : W4_HIDDEN;
+  m.group = group;
+  m.T = p->T_p;
+  m.s = p->s;
+  m.sp = w4_sp(p);
+  m.seg = p->d;
+  return m;
+}
+W4Shape w4_down(const tp_ffn_plan* p, int group) {
+  W4Shape m;
+  m.group = group;
+  m.rows = p->d;
+  m.segs = p->T_p;
+  m.seg = p->s;
+  return m;
+}
+W4Shape w4_qkv(const tp_attn_plan* a, int group) {
+  W4Shape m;
+  m.rows_kind = W4_QKV;
+  m.group = group;
+  m.rows = a->W;
+  m.T = a->T_p;
+  m.sq = a->H / a->T_p * a->hd;
+  m.sk = a->Hkv / a->T_p * a->hd;
+  m.seg = a->d;
+  return m;
+}
+
+struct Ws4 {
+  size_t h = 0, total = 0;
+};
+Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
+  Ws4 L;
+  size_t off = kAlign;  // error word
+  L.h = off;
+  if (p->act != TP_ACT_NONE) off += align_up(static_cast<size_t>(n) * p->T_p * w4_sp(p) * 2);
+  L.total = off;
+  return L;
+}
+constexpr int64_t kMaxTokens4 = int64_t(1) << 18;
+
+int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n, const void* x, const void* w13, const void* w2,
+              const void* b1, const void* b2, void* y, char* ws, LaunchCtx& ctx) {
+  const Ws4 L = ws4_layout(p, n);
+  W4Product g;
+  g.n = n;
+  const void* h = x;
+  int64_t h_seg = p->s, h_rs = p->d_ff;
+  if (p->act != TP_ACT_NONE) {
+    g.name = p->act == TP_ACT_SWIGLU ? "up_swiglu4" : "up_gelu4";
+    g.m = w4_up(p, group);
+    g.packed = w13;
+    g.x = x;
+    g.x_seg = 0;
+    g.x_rs = p->d;
+    g.epi = p->act == TP_ACT_SWIGLU ? W4_SWIGLU : W4_GELU;
+    g.bias = b1;
+    g.out = ws + L.h;
+    g.out_rs = p->T_p * w4_sp(p);
+    if (int rc = launch_w4_product(g, ctx)) return rc;
+    h = ws + L.h;
+    h_seg = w4_sp(p);
+    h_rs = g.out_rs;
+  }
+  g.name = "down4";
+  g.m = w4_down(p, group);
+  g.packed = w2;
+  g.x = h;
+  g.x_seg = h_seg;
+  g.x_rs = h_rs;
+  g.epi = W4_OUT;
+  g.bias = b2;
+  g.out = y;
+  g.out_rs = p->d;
+  return launch_w4_product(g, ctx);
+}
+
+struct Decode4Ws {
+  size_t attend = 0, wo = 0, qkv = 0, q = 0, c = 0, total = 0;
+};
+Decode4Ws decode4_ws(const tp_attn_plan* a, const KvSpec& sp) {
+  Decode4Ws L;
+  const size_t n = static_cast<size_t>(sp.n_tokens);
+  size_t off = align_up(kKvHeaderBytes);
+  L.attend = off;
+  off += align_up(kv_attend_scratch_bytes(sp, num_sms_current()));
+  L.wo = off;
+  off += align_up(ws4_layout(a->wo, sp.n_tokens).total);
+  L.qkv = off;
+  off += align_up(n * a->W * 2);
+  L.q = off;
+  off += align_up(n * a->H * a->hd * 2);
+  L.c = off;
+  off += align_up(n * a->H * a->hd * 2);
+  L.total = off;
+  return L;
+}
+
+int all_aligned(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs) {
+    if (!q) return TP_ERR_INVALID;
+    if (!aligned16(q)) return TP_ERR_ALIGN;
+  }
+  return TP_OK;
+}
+int check_quant4(const void* W, int64_t rows, int64_t cols, int64_t segs, int group, const void* codes,
+                 const void* scales, bool& work) {
+  work = false;
+  if (rows < 0 || cols < 0 || segs < 1 || cols % segs || !w4_group(group)) return TP_ERR_INVALID;
+  if (cols > (int64_t(1) << 30) || rows > (int64_t(1) << 46) || (cols && rows > (int64_t(1) << 46) / cols))
+    return TP_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return TP_OK;
+  work = true;
+  return all_aligned({W, codes, scales});
+}
+int columns4(const tp_ffn_plan* p, int group, const void* c1, const void* s1, const void* c3, const void* s3,
+             const void* packed, int unpack, tp_stream_t stream) {
+  if (!tp_ffn_packed4_bytes(p, TP_PACK_COLUMNS, group)) return TP_ERR_INVALID;
+  int rc = all_aligned({c1, s1, packed});
+  if (!rc && p->act == TP_ACT_SWIGLU) rc = all_aligned({c3, s3});
+  if (rc) return rc;
+  W4Codes c;
+  c.codes[0] = const_cast<void*>(c1);
+  c.scales[0] = const_cast<void*>(s1);
+  c.codes[1] = const_cast<void*>(c3);
+  c.scales[1] = const_cast<void*>(s3);
+  return launch_w4_pack(w4_up(p, group), c, const_cast<void*>(packed), unpack, reinterpret_cast<cudaStream_t>(stream));
+}
+int rows4(const tp_ffn_plan* p, int group, const void* c2, const void* s2, const void* packed, int unpack,
+          tp_stream_t stream) {
+  if (!tp_ffn_packed4_bytes(p, TP_PACK_ROWS, group)) return TP_ERR_INVALID;
+  if (int rc = all_aligned({c2, s2, packed})) return rc;
+  W4Codes c;
+  c.codes[0] = const_cast<void*>(c2);
+  c.scales[0] = const_cast<void*>(s2);
+  return launch_w4_pack(w4_down(p, group), c, const_cast<void*>(packed), unpack, reinterpret_cast<cudaStream_t>(stream));
+}
+int attn_weights4(const tp_attn_plan* a, int group, const void* const codes[4], const void* const scales[4],
+                  const void* wqkv, const void* wo, int unpack, tp_stream_t stream) {
+  if (!a || !w4_group(group) || !codes || !scales) return TP_ERR_INVALID;
+  int rc = all_aligned({wqkv, wo});
+  for (int i = 0; i < 4 && !rc; ++i) rc = all_aligned({codes[i], scales[i]});
+  if (rc) return rc;
+  W4Codes c;
+  for (int i = 0; i < 3; ++i) {
+    c.codes[i] = const_cast<void*>(codes[i]);
+    c.scales[i] = const_cast<void*>(scales[i]);
+  }
+  rc = launch_w4_pack(w4_qkv(a, group), c, const_cast<void*>(wqkv), unpack, reinterpret_cast<cudaStream_t>(stream));
+  return rc ? rc : rows4(a->wo, group, codes[3], scales[3], wo, unpack, stream);
+}
 }  // namespace
 
 size_t tp_attn_kv_workspace_bytes(const tp_attn_plan* a, const tp_kv_batch* batch, int64_t page_size,
@@ -1554,6 +1711,7 @@ size_t tp_attn_kv_workspace_bytes(const tp_attn_plan* a, const tp_kv_batch* batc
     case TP_KV_APPEND: return align_up(kKvHeaderBytes);
     case TP_KV_ATTEND: return align_up(kKvHeaderBytes) + kv_attend_scratch_bytes(sp, num_sms_current());
     case TP_KV_DECODE: return decode_ws(a, sp, flags).total;
+    case TP_KV_DECODE4: return decode4_ws(a, sp).total;
     default: return 0;
   }
 }
@@ -1642,6 +1800,125 @@ int tp_attn_kv_last_device_error(const tp_attn_plan* a, const void* workspace, t
   if (all & DEV_ERR_TIMEOUT) return TP_ERR_TIMEOUT;
   if (all & DEV_ERR_BATCH) return TP_ERR_BATCH;
   return all ? TP_ERR_CUDA : TP_OK;
+}
+
+// ------------------------------------------------------------ 4-bit weights
+int tp_quantize4(const void* W, int64_t rows, int64_t cols, int64_t segments, int group, void* codes, void* scales,
+                 tp_stream_t stream) {
+  bool work;
+  const int rc = check_quant4(W, rows, cols, segments, group, codes, scales, work);
+  if (rc || !work) return rc;
+  return launch_w4_quantize(W, rows, cols, segments, group, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int tp_dequantize4(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t segments, int group,
+                   void* W, tp_stream_t stream) {
+  bool work;
+  const int rc = check_quant4(W, rows, cols, segments, group, codes, scales, work);
+  if (rc || !work) return rc;
+  return launch_w4_dequantize(codes, scales, rows, cols, segments, group, W, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t tp_ffn_packed4_bytes(const tp_ffn_plan* p, int which, int group) {
+  if (!p || p->dtype != TP_BF16 || !w4_group(group)) return 0;
+  if (which == TP_PACK_ROWS) return static_cast<size_t>(w4_down(p, group).bytes());
+  return which == TP_PACK_COLUMNS && p->act != TP_ACT_NONE ? static_cast<size_t>(w4_up(p, group).bytes()) : 0;
+}
+
+int tp_ffn_shard_columns4(const tp_ffn_plan* p, int group, const void* codes1, const void* scales1,
+                          const void* codes3, const void* scales3, void* packed, tp_stream_t stream) {
+  return columns4(p, group, codes1, scales1, codes3, scales3, packed, 0, stream);
+}
+int tp_ffn_unshard_columns4(const tp_ffn_plan* p, int group, const void* packed, void* codes1, void* scales1,
+                            void* codes3, void* scales3, tp_stream_t stream) {
+  return columns4(p, group, codes1, scales1, codes3, scales3, packed, 1, stream);
+}
+int tp_ffn_shard_rows4(const tp_ffn_plan* p, int group, const void* codes2, const void* scales2, void* packed,
+                       tp_stream_t stream) {
+  return rows4(p, group, codes2, scales2, packed, 0, stream);
+}
+int tp_ffn_unshard_rows4(const tp_ffn_plan* p, int group, const void* packed, void* codes2, void* scales2,
+                         tp_stream_t stream) {
+  return rows4(p, group, codes2, scales2, packed, 1, stream);
+}
+
+size_t tp_ffn_workspace4_bytes(const tp_ffn_plan* p, int64_t n, int) {
+  if (!p || n < 0 || p->dtype != TP_BF16 || n > kMaxTokens4) return 0;
+  return ws4_layout(p, n).total;
+}
+
+int tp_ffn_fwd4(const tp_ffn_plan* p, int group, int64_t n, const void* x, const void* w13_4, const void* w2_4,
+                const void* b1, const void* b2, void* y, void* workspace, size_t workspace_bytes, int flags,
+                tp_stream_t stream) {
+  if (!p || n < 0 || !w4_group(group)) return TP_ERR_INVALID;
+  if (p->dtype != TP_BF16 || n > kMaxTokens4) return TP_ERR_UNSUPPORTED;
+  if (n == 0) {
+    p->last_launches = 0;
+    return TP_OK;
+  }
+  int rc = all_aligned({x, w2_4, y, workspace});
+  if (!rc && p->act != TP_ACT_NONE) rc = all_aligned({w13_4});
+  if (rc) return rc;
+  if (b1 && p->act != TP_ACT_GELU_TANH) return TP_ERR_UNSUPPORTED;
+  if (!aligned16(b1) || !aligned16(b2)) return TP_ERR_ALIGN;
+  if (workspace_bytes < ws4_layout(p, n).total) return TP_ERR_INVALID;
+  LaunchCtx ctx;
+  rc = make_ctx(p, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
+  if (!rc) rc = fwd4_impl(p, group, n, x, w13_4, w2_4, b1, b2, y, static_cast<char*>(workspace), ctx);
+  return finish_call(p, ctx, rc, flags, workspace);
+}
+
+size_t tp_attn_packed4_bytes(const tp_attn_plan* a, int which, int group) {
+  if (!a || !w4_group(group)) return 0;
+  if (which == TP_PACK_COLUMNS) return static_cast<size_t>(w4_qkv(a, group).bytes());
+  return which == TP_PACK_ROWS ? tp_ffn_packed4_bytes(a->wo, TP_PACK_ROWS, group) : 0;
+}
+int tp_attn_shard_weights4(const tp_attn_plan* a, int group, const void* const codes[4], const void* const scales[4],
+                           void* wqkv_4, void* wo_4, tp_stream_t stream) {
+  return attn_weights4(a, group, codes, scales, wqkv_4, wo_4, 0, stream);
+}
+int tp_attn_unshard_weights4(const tp_attn_plan* a, int group, const void* wqkv_4, const void* wo_4,
+                             void* const codes[4], void* const scales[4], tp_stream_t stream) {
+  return attn_weights4(a, group, codes, scales, wqkv_4, wo_4, 1, stream);
+}
+
+int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const tp_kv_batch* batch,
+                        const tp_kv_rotation* rotation, int64_t shared_len, int group, const void* x,
+                        const void* wqkv_4, const void* wo_4, void* y, void* workspace, size_t workspace_bytes,
+                        int flags, tp_stream_t stream) {
+  KvSpec sp;
+  KvRotation rot;
+  int rc = kv_spec(a, cache, batch, shared_len, sp);
+  if (!rc) rc = kv_rotation(a, rotation, rot);
+  if (rc) return rc;
+  if (!w4_group(group)) return TP_ERR_INVALID;
+  if (sp.n_tokens > kMaxTokens4) return TP_ERR_UNSUPPORTED;
+  if (sp.n_tokens == 0 || sp.n_seqs == 0) {
+    a->wo->last_launches = 0;
+    return TP_OK;
+  }
+  const Decode4Ws L = decode4_ws(a, sp);
+  if ((rc = kv_pointers(workspace, workspace_bytes, L.total, {x, wqkv_4, wo_4, y}))) return rc;
+  LaunchCtx ctx;
+  rc = make_ctx(a->wo, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
+  if (rc) return rc;
+  const int64_t n = sp.n_tokens;
+  char* ws = static_cast<char*>(workspace);
+  W4Product g;
+  g.name = "qkv_proj4";
+  g.m = w4_qkv(a, group);
+  g.packed = wqkv_4;
+  g.n = n;
+  g.x = x;
+  g.x_rs = a->d;
+  g.out = ws + L.qkv;
+  g.out_rs = a->W;
+  rc = launch_w4_product(g, ctx);
+  if (!rc) rc = launch_kv_append(sp, rot, ws + L.qkv, ws + L.q, static_cast<int*>(workspace), false, ctx);
+  if (!rc)
+    rc = launch_kv_attend(sp, ws + L.q, ws + L.c, nullptr, static_cast<int*>(workspace), false, ws + L.attend, ctx);
+  if (!rc) rc = fwd4_impl(a->wo, group, n, ws + L.c, nullptr, wo_4, nullptr, nullptr, y, ws + L.wo, ctx);
+  return kv_finish(a, ctx, rc, flags, workspace);
 }
 
 }  // extern "C"

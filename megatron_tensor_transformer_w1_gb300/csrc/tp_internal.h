@@ -237,4 +237,98 @@ size_t kv_attend_scratch_bytes(const KvSpec& a, int num_sms);
 int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* header, bool alone, void* scratch,
                      LaunchCtx& ctx);
 
+// ------------------------------------------------------------ 4-bit weights
+// (tp_w4.cu)  A matrix of 4-bit codes with a bf16 scale for each group of
+// consecutive columns of a row: element (code - 8) * scale.
+//
+// Natural layout: codes [rows][(cols + 1) / 2], the even column in a byte's low
+// half; scales [rows][segs * ceil(seg / group)], cols = segs * seg, the groups
+// starting anew in every segment.
+//
+// Packed layout, what the products read: the rows in tiles of 128, two to a
+// unit, the columns of every segment in chunks of 128 slots (those behind the
+// segment's end hold code 8).  Block (unit, chunk) lies at unit * chunks + chunk:
+// codes [2 tiles][4][128 rows][16 bytes], piece i of a row being its slots
+// 32 i .. 32 i + 31, a 32-bit word eight of them, slot 2 j in bits 4 j and slot
+// 2 j + 1 in bits 16 + 4 j; then scales [128 / group][256 rows].
+enum W4Rows : int {
+  W4_PLAIN = 0,   // output rows as they are
+  W4_HIDDEN = 1,  // shard t's s hidden units in sp slots (a multiple of 128)
+  W4_GATED = 2,   // a unit: 128 slots of the first matrix, the same of the second
+  W4_QKV = 3,     // shard t: sq rows of the first matrix, sk of the second, sk of the third
+};
+struct W4Shape {
+  int rows_kind = W4_PLAIN, group = 128;
+  int64_t rows = 0;              // W4_PLAIN, W4_QKV: output rows
+  int T = 1;                     // W4_HIDDEN, W4_GATED, W4_QKV: shards
+  int64_t s = 0, sp = 0;         // W4_HIDDEN, W4_GATED
+  int64_t sq = 0, sk = 0;        // W4_QKV
+  int64_t segs = 1, seg = 0;     // columns
+  __host__ __device__ int64_t tiles() const {
+    return rows_kind == W4_HIDDEN ? T * sp / 128 : rows_kind == W4_GATED ? 2 * (T * sp / 128) : (rows + 127) / 128;
+  }
+  __host__ __device__ int64_t units() const { return (tiles() + 1) / 2; }
+  __host__ __device__ int64_t seg_chunks() const { return (seg + 127) / 128; }
+  __host__ __device__ int64_t chunks() const { return segs * seg_chunks(); }
+  __host__ __device__ int64_t seg_groups() const { return (seg + group - 1) / group; }
+  __host__ __device__ int64_t cols() const { return segs * seg; }
+  __host__ __device__ int block_bytes() const { return 16384 + 512 * (128 / group); }
+  __host__ __device__ int64_t bytes() const { return units() * chunks() * block_bytes(); }
+};
+// Tile `tile` of the packed layout: rows row0 .. row0 + n - 1 of matrix `mat`.
+struct W4Tile {
+  int mat = 0, n = 0;
+  int64_t row0 = 0;
+};
+__host__ __device__ inline W4Tile w4_tile(const W4Shape& m, int64_t tile) {
+  W4Tile r;
+  int64_t slot = tile * 128, left = 0;
+  if (m.rows_kind == W4_HIDDEN || m.rows_kind == W4_GATED) {
+    if (m.rows_kind == W4_GATED) {
+      r.mat = static_cast<int>(tile & 1);
+      slot = (tile >> 1) * 128;
+    }
+    const int64_t t = slot / m.sp, j = slot - t * m.sp;
+    r.row0 = t * m.s + j;
+    left = t < m.T ? m.s - j : 0;
+  } else if (m.rows_kind == W4_QKV) {
+    const int64_t slice = m.sq + 2 * m.sk, t = slot / slice, w = slot - t * slice;
+    r.mat = w < m.sq ? 0 : (w < m.sq + m.sk ? 1 : 2);
+    r.row0 = r.mat == 0 ? t * m.sq + w : t * m.sk + w - m.sq - (r.mat - 1) * m.sk;
+    left = slot < m.rows ? 128 : 0;
+  } else {
+    r.row0 = slot;
+    left = m.rows - slot;
+  }
+  r.n = static_cast<int>(left < 0 ? 0 : (left > 128 ? 128 : left));
+  return r;
+}
+
+int launch_w4_quantize(const void* W, int64_t rows, int64_t cols, int64_t segs, int group, void* codes, void* scales,
+                       cudaStream_t st);
+int launch_w4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t segs, int group,
+                         void* W, cudaStream_t st);
+// Natural to packed and back; up to three matrices (see W4Rows).
+struct W4Codes {
+  void* codes[3] = {};
+  void* scales[3] = {};
+};
+int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack, cudaStream_t st);
+
+enum W4Epi : int { W4_OUT = 0, W4_GELU = 1, W4_SWIGLU = 2 };
+// out[token][row] = epilogue(sum over the columns of x[token][column] * W[row][column] + bias[row])
+struct W4Product {
+  const char* name = "w4_product";
+  W4Shape m;
+  const void* packed = nullptr;
+  int64_t n = 0;
+  const void* x = nullptr;       // bf16; segment e's columns start at e * x_seg, rows x_rs apart
+  int64_t x_seg = 0, x_rs = 0;
+  int epi = W4_OUT;
+  const void* bias = nullptr;    // W4_OUT: by row; W4_GELU: by hidden unit
+  void* out = nullptr;           // bf16; W4_GELU and W4_SWIGLU: by hidden slot
+  int64_t out_rs = 0;
+};
+int launch_w4_product(const W4Product& p, LaunchCtx& ctx);
+
 }  // namespace tpffn

@@ -26,6 +26,7 @@ import threading
 import torch
 
 from . import tpffn as abi
+from . import weights4 as w4
 
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
@@ -196,6 +197,17 @@ class PagedKVCache:
                 return self.decode(x, batch, wqkv, wo, shared_len, out, flags)
         a, n = self.attn, batch.n_tokens
         self._check("x", x, torch.bfloat16, (n, a.d))
+        if isinstance(wqkv, w4.Packed4) or isinstance(wo, w4.Packed4):
+            w4.check_packed("wqkv", wqkv, abi.TP_PACK_COLUMNS, a._key4(), self.k.device)
+            w4.check_packed("wo", wo, abi.TP_PACK_ROWS, a._key4(), self.k.device, wqkv.group)
+            y = self._out("out", out, (n, a.d))
+            st = _current_stream(self._index)
+            with self._turn:
+                ws, need = self._workspace(batch, shared_len, abi.TP_KV_DECODE4, flags, st)
+                rc = abi.tp_attn_decode_fwd4(a.plan, self._abi, batch.abi, self._rot, shared_len, wo.group, x, wqkv.data,
+                                             wo.data, y, ws, need, flags, st)
+            self._done(rc, "tp_attn_decode_fwd4", batch, ws)
+            return y
         self._check_weights("wqkv", wqkv, self._weight_bytes[0])
         self._check_weights("wo", wo, self._weight_bytes[1])
         y = self._out("out", out, (n, a.d))

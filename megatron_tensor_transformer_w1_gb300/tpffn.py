@@ -20,7 +20,7 @@ TP_F32, TP_BF16 = 0, 1
 TP_PACK_COLUMNS, TP_PACK_ROWS = 0, 1
 TP_SUM_STANDALONE, TP_SUM_FUSED, TP_FLAG_SYNC, TP_FLAG_TIMING, TP_SUM_OVERLAP = 0, 1, 2, 4, 8
 TP_FLAG_DEBUG_SKIP_LOAD = 1 << 16
-TP_KV_APPEND, TP_KV_ATTEND, TP_KV_DECODE = 0, 1, 2
+TP_KV_APPEND, TP_KV_ATTEND, TP_KV_DECODE, TP_KV_DECODE4 = 0, 1, 2, 3
 
 ABI_FUNCTIONS = (
     "tp_ffn_plan_create", "tp_attn_out_plan_create", "tp_ffn_plan_destroy", "tp_ffn_plan_info",
@@ -35,6 +35,9 @@ ABI_FUNCTIONS = (
     "tp_attn_kernel_times", "tp_attn_last_launch_count",
     "tp_attn_kv_workspace_bytes", "tp_attn_kv_append", "tp_attn_paged_fwd", "tp_attn_decode_fwd",
     "tp_attn_kv_last_device_error",
+    "tp_quantize4", "tp_dequantize4", "tp_ffn_packed4_bytes", "tp_ffn_shard_columns4", "tp_ffn_shard_rows4",
+    "tp_ffn_unshard_columns4", "tp_ffn_unshard_rows4", "tp_ffn_workspace4_bytes", "tp_ffn_fwd4",
+    "tp_attn_packed4_bytes", "tp_attn_shard_weights4", "tp_attn_unshard_weights4", "tp_attn_decode_fwd4",
 )
 TPFFN_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -118,6 +121,19 @@ _SIGS = {
     "tp_attn_paged_fwd": (_INT, [_P, _P, _P, _I64, _P, _P, _P, _P, _SZ, _INT, _P]),
     "tp_attn_decode_fwd": (_INT, [_P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _SZ, _INT, _P]),
     "tp_attn_kv_last_device_error": (_INT, [_P, _P, _P]),
+    "tp_quantize4": (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P]),
+    "tp_dequantize4": (_INT, [_P, _P, _I64, _I64, _I64, _INT, _P, _P]),
+    "tp_ffn_packed4_bytes": (_SZ, [_P, _INT, _INT]),
+    "tp_ffn_shard_columns4": (_INT, [_P, _INT, _P, _P, _P, _P, _P, _P]),
+    "tp_ffn_shard_rows4": (_INT, [_P, _INT, _P, _P, _P, _P]),
+    "tp_ffn_unshard_columns4": (_INT, [_P, _INT, _P, _P, _P, _P, _P, _P]),
+    "tp_ffn_unshard_rows4": (_INT, [_P, _INT, _P, _P, _P, _P]),
+    "tp_ffn_workspace4_bytes": (_SZ, [_P, _I64, _INT]),
+    "tp_ffn_fwd4": (_INT, [_P, _INT, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _INT, _P]),
+    "tp_attn_packed4_bytes": (_SZ, [_P, _INT, _INT]),
+    "tp_attn_shard_weights4": (_INT, [_P, _INT, _P, _P, _P, _P, _P]),
+    "tp_attn_unshard_weights4": (_INT, [_P, _INT, _P, _P, _P, _P, _P]),
+    "tp_attn_decode_fwd4": (_INT, [_P, _P, _P, _P, _I64, _INT, _P, _P, _P, _P, _P, _SZ, _INT, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -377,6 +393,72 @@ def tp_attn_decode_fwd(plan, cache, batch, rotation, shared_len, x, wqkv, wo_pac
 
 def tp_attn_kv_last_device_error(plan, workspace, stream=None):
     return _lib.tp_attn_kv_last_device_error(plan, _ptr(workspace), _stream(stream))
+
+
+# ------------------------------------------------------------ 4-bit weights
+def tp_quantize4(W, rows, cols, segments, group, codes, scales, stream=None):
+    return _lib.tp_quantize4(_ptr(W), rows, cols, segments, group, _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def tp_dequantize4(codes, scales, rows, cols, segments, group, W, stream=None):
+    return _lib.tp_dequantize4(_ptr(codes), _ptr(scales), rows, cols, segments, group, _ptr(W), _stream(stream))
+
+
+def tp_ffn_packed4_bytes(plan, which, group):
+    return _lib.tp_ffn_packed4_bytes(plan, which, group)
+
+
+def tp_ffn_shard_columns4(plan, group, codes1, scales1, codes3, scales3, packed, stream=None):
+    return _lib.tp_ffn_shard_columns4(plan, group, _ptr(codes1), _ptr(scales1), _ptr(codes3), _ptr(scales3),
+                                      _ptr(packed), _stream(stream))
+
+
+def tp_ffn_shard_rows4(plan, group, codes2, scales2, packed, stream=None):
+    return _lib.tp_ffn_shard_rows4(plan, group, _ptr(codes2), _ptr(scales2), _ptr(packed), _stream(stream))
+
+
+def tp_ffn_unshard_columns4(plan, group, packed, codes1, scales1, codes3, scales3, stream=None):
+    return _lib.tp_ffn_unshard_columns4(plan, group, _ptr(packed), _ptr(codes1), _ptr(scales1), _ptr(codes3),
+                                        _ptr(scales3), _stream(stream))
+
+
+def tp_ffn_unshard_rows4(plan, group, packed, codes2, scales2, stream=None):
+    return _lib.tp_ffn_unshard_rows4(plan, group, _ptr(packed), _ptr(codes2), _ptr(scales2), _stream(stream))
+
+
+def tp_ffn_workspace4_bytes(plan, n_tokens, flags=0):
+    return _lib.tp_ffn_workspace4_bytes(plan, n_tokens, flags)
+
+
+def tp_ffn_fwd4(plan, group, n_tokens, x, w13_4, w2_4, b1, b2, y, workspace, workspace_bytes, flags=0, stream=None):
+    return _lib.tp_ffn_fwd4(plan, group, n_tokens, _ptr(x), _ptr(w13_4), _ptr(w2_4), _ptr(b1), _ptr(b2), _ptr(y),
+                            _ptr(workspace), workspace_bytes, flags, _stream(stream))
+
+
+def tp_attn_packed4_bytes(plan, which, group):
+    return _lib.tp_attn_packed4_bytes(plan, which, group)
+
+
+def _four(items):
+    """A host array of four device pointers."""
+    return ctypes.cast((ctypes.c_void_p * 4)(*[_ptr(a) for a in items]), ctypes.c_void_p)
+
+
+def tp_attn_shard_weights4(plan, group, codes, scales, wqkv_4, wo_4, stream=None):
+    c, s = _four(codes), _four(scales)
+    return _lib.tp_attn_shard_weights4(plan, group, c, s, _ptr(wqkv_4), _ptr(wo_4), _stream(stream))
+
+
+def tp_attn_unshard_weights4(plan, group, wqkv_4, wo_4, codes, scales, stream=None):
+    c, s = _four(codes), _four(scales)
+    return _lib.tp_attn_unshard_weights4(plan, group, _ptr(wqkv_4), _ptr(wo_4), c, s, _stream(stream))
+
+
+def tp_attn_decode_fwd4(plan, cache, batch, rotation, shared_len, group, x, wqkv_4, wo_4, y, workspace,
+                        workspace_bytes, flags=0, stream=None):
+    return _lib.tp_attn_decode_fwd4(plan, _ref(cache), _ref(batch), _ref(rotation), shared_len, group, _ptr(x),
+                                    _ptr(wqkv_4), _ptr(wo_4), _ptr(y), _ptr(workspace), workspace_bytes, flags,
+                                    _stream(stream))
 
 
 def check(status, where=""):
