@@ -1578,12 +1578,27 @@ W4Shape w4_qkv(const tp_attn_plan* a, int group) {
   return m;
 }
 
+// Workspace of a forward pass: error word, the products' counters and parts (of
+// one product at a time), hidden activations.
 struct Ws4 {
-  size_t h = 0, total = 0;
+  size_t counters = 0, parts = 0, h = 0, total = 0;
+  int64_t n_up = 0, n_down = 0;  // counters
 };
 Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
   Ws4 L;
-  size_t off = kAlign;  // error word
+  const int sms = num_sms_current();
+  const W4Shape up = w4_up(p, 128), down = w4_down(p, 128);
+  size_t parts = w4_product_scratch(down, n, sms), off = kAlign;
+  L.n_down = w4_product_counters(down, n);
+  if (p->act != TP_ACT_NONE) {
+    L.n_up = w4_product_counters(up, n);
+    const size_t u = w4_product_scratch(up, n, sms);
+    if (u > parts) parts = u;
+  }
+  L.counters = off;
+  off += align_up(static_cast<size_t>(L.n_up + L.n_down) * sizeof(int));
+  L.parts = off;
+  off += align_up(parts);
   L.h = off;
   if (p->act != TP_ACT_NONE) off += align_up(static_cast<size_t>(n) * p->T_p * w4_sp(p) * 2);
   L.total = off;
@@ -1591,11 +1606,29 @@ Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
 }
 constexpr int64_t kMaxTokens4 = int64_t(1) << 18;
 
+// The launch context of a 4-bit call, without the launch that clears the error word.
+void ctx4(const tp_ffn_plan* p, void* workspace, int flags, cudaStream_t stream, LaunchCtx& ctx) {
+  ctx.stream = stream;
+  ctx.err = static_cast<int*>(workspace);
+  ctx.num_sms = num_sms_current();
+  ctx.debug_skip_load = (flags & TP_FLAG_DEBUG_SKIP_LOAD) ? 1 : 0;
+  ctx.timing = (flags & TP_FLAG_TIMING) != 0;
+  if (ctx.timing) {
+    p->timing_stream = stream;
+    ctx.before = timing_before;
+    ctx.after = timing_after;
+    ctx.user = const_cast<tp_ffn_plan*>(p);
+  }
+}
+
+// The products of a forward pass; the counters are clear.
 int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n, const void* x, const void* w13, const void* w2,
               const void* b1, const void* b2, void* y, char* ws, LaunchCtx& ctx) {
   const Ws4 L = ws4_layout(p, n);
   W4Product g;
   g.n = n;
+  g.scratch = ws + L.parts;
+  g.counters = reinterpret_cast<int*>(ws + L.counters);
   const void* h = x;
   int64_t h_seg = p->s, h_rs = p->d_ff;
   if (p->act != TP_ACT_NONE) {
@@ -1603,7 +1636,6 @@ int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n, const void* x, const v
     g.m = w4_up(p, group);
     g.packed = w13;
     g.x = x;
-    g.x_seg = 0;
     g.x_rs = p->d;
     g.epi = p->act == TP_ACT_SWIGLU ? W4_SWIGLU : W4_GELU;
     g.bias = b1;
@@ -1624,26 +1656,36 @@ int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n, const void* x, const v
   g.bias = b2;
   g.out = y;
   g.out_rs = p->d;
+  g.counters += L.n_up;
   return launch_w4_product(g, ctx);
 }
 
+// The decode pass: its counters lie together, those of q/k/v first.
 struct Decode4Ws {
-  size_t attend = 0, wo = 0, qkv = 0, q = 0, c = 0, total = 0;
+  size_t attend = 0, counters = 0, parts = 0, qkv = 0, q = 0, c = 0, total = 0;
+  int64_t n_qkv = 0, n_wo = 0;
 };
 Decode4Ws decode4_ws(const tp_attn_plan* a, const KvSpec& sp) {
   Decode4Ws L;
-  const size_t n = static_cast<size_t>(sp.n_tokens);
+  const int64_t n = sp.n_tokens;
+  const int sms = num_sms_current();
   size_t off = align_up(kKvHeaderBytes);
   L.attend = off;
-  off += align_up(kv_attend_scratch_bytes(sp, num_sms_current()));
-  L.wo = off;
-  off += align_up(ws4_layout(a->wo, sp.n_tokens).total);
+  off += align_up(kv_attend_scratch_bytes(sp, sms));
+  const W4Shape qkv = w4_qkv(a, 128), wo = w4_down(a->wo, 128);
+  L.n_qkv = w4_product_counters(qkv, n);
+  L.n_wo = w4_product_counters(wo, n);
+  L.counters = off;
+  off += align_up(static_cast<size_t>(L.n_qkv + L.n_wo) * sizeof(int));
+  L.parts = off;
+  const size_t p1 = w4_product_scratch(qkv, n, sms), p2 = w4_product_scratch(wo, n, sms);
+  off += align_up(p1 > p2 ? p1 : p2);
   L.qkv = off;
-  off += align_up(n * a->W * 2);
+  off += align_up(static_cast<size_t>(n) * a->W * 2);
   L.q = off;
-  off += align_up(n * a->H * a->hd * 2);
+  off += align_up(static_cast<size_t>(n) * a->H * a->hd * 2);
   L.c = off;
-  off += align_up(n * a->H * a->hd * 2);
+  off += align_up(static_cast<size_t>(n) * a->H * a->hd * 2);
   L.total = off;
   return L;
 }
@@ -1863,8 +1905,11 @@ int tp_ffn_fwd4(const tp_ffn_plan* p, int group, int64_t n, const void* x, const
   if (!aligned16(b1) || !aligned16(b2)) return TP_ERR_ALIGN;
   if (workspace_bytes < ws4_layout(p, n).total) return TP_ERR_INVALID;
   LaunchCtx ctx;
-  rc = make_ctx(p, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
-  if (!rc) rc = fwd4_impl(p, group, n, x, w13_4, w2_4, b1, b2, y, static_cast<char*>(workspace), ctx);
+  ctx4(p, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
+  char* ws = static_cast<char*>(workspace);
+  const Ws4 L = ws4_layout(p, n);
+  rc = launch_w4_reset(ctx.err, reinterpret_cast<int*>(ws + L.counters), L.n_up + L.n_down, ctx);
+  if (!rc) rc = fwd4_impl(p, group, n, x, w13_4, w2_4, b1, b2, y, ws, ctx);
   return finish_call(p, ctx, rc, flags, workspace);
 }
 
@@ -1900,10 +1945,11 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
   const Decode4Ws L = decode4_ws(a, sp);
   if ((rc = kv_pointers(workspace, workspace_bytes, L.total, {x, wqkv_4, wo_4, y}))) return rc;
   LaunchCtx ctx;
-  rc = make_ctx(a->wo, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
-  if (rc) return rc;
+  ctx4(a->wo, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
   const int64_t n = sp.n_tokens;
   char* ws = static_cast<char*>(workspace);
+  int* counters = reinterpret_cast<int*>(ws + L.counters);
+  if ((rc = launch_w4_reset(ctx.err, counters, L.n_qkv + L.n_wo, ctx))) return rc;
   W4Product g;
   g.name = "qkv_proj4";
   g.m = w4_qkv(a, group);
@@ -1913,11 +1959,24 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
   g.x_rs = a->d;
   g.out = ws + L.qkv;
   g.out_rs = a->W;
+  g.scratch = ws + L.parts;
+  g.counters = counters;
   rc = launch_w4_product(g, ctx);
   if (!rc) rc = launch_kv_append(sp, rot, ws + L.qkv, ws + L.q, static_cast<int*>(workspace), false, ctx);
   if (!rc)
     rc = launch_kv_attend(sp, ws + L.q, ws + L.c, nullptr, static_cast<int*>(workspace), false, ws + L.attend, ctx);
-  if (!rc) rc = fwd4_impl(a->wo, group, n, ws + L.c, nullptr, wo_4, nullptr, nullptr, y, ws + L.wo, ctx);
+  if (!rc) {
+    g.name = "wo_proj4";
+    g.m = w4_down(a->wo, group);
+    g.packed = wo_4;
+    g.x = ws + L.c;
+    g.x_seg = a->wo->s;
+    g.x_rs = a->wo->d_ff;
+    g.out = y;
+    g.out_rs = a->d;
+    g.counters = counters + L.n_qkv;
+    rc = launch_w4_product(g, ctx);
+  }
   return kv_finish(a, ctx, rc, flags, workspace);
 }
 

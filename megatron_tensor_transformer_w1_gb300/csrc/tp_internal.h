@@ -328,7 +328,13 @@ struct W4Product {
   const void* bias = nullptr;    // W4_OUT: by row; W4_GELU: by hidden unit
   void* out = nullptr;           // bf16; W4_GELU and W4_SWIGLU: by hidden slot
   int64_t out_rs = 0;
+  void* scratch = nullptr;       // w4_product_scratch bytes
+  int* counters = nullptr;       // w4_product_counters words, 0 before the launch
 };
+size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms);
+int64_t w4_product_counters(const W4Shape& m, int64_t n);
+// The kernel before a call's first product: clears the error word and the counters.
+int launch_w4_reset(int* err, int* counters, int64_t n, LaunchCtx& ctx);
 int launch_w4_product(const W4Product& p, LaunchCtx& ctx);
 
 }  // namespace tpffn

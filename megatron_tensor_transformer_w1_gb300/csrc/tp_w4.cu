@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "tc_ptx.cuh"
@@ -232,72 +233,434 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
 }
 
 // ================================================================ products
-// The simplest form: a thread to a row of a unit, eight tokens at a time, the
-// group's sum in 32 bits times its scale.
+// y[token][row] = sum_g s[row][g] sum_{k in g} (code - 8) x[token][k], for up to
+// 64 tokens at a time.
+//
+// Bound by the one read of the codes for few tokens.  The weights are the matrix
+// unit's A operand, 128 rows at a time, the tokens its N: code - 8 is a bf16
+// number without rounding, and the product of a group is scaled in 32 bits when
+// it is read back, so a result is as exact as the sums in 32 bits.  (A scaled
+// weight would have to be rounded to bf16.)
+//
+// A block takes a run of chunks (128 columns of a unit's 256 rows) of the list of
+// all units' chunks, the same number as the others, whatever units they belong to;
+// a run of chunks of one unit is a segment.  One block has
+//  * warp 16: copies of the chunks into a ring: the packed block (codes, scales) in
+//    one piece, as it lies, the tokens' 128 columns by two TMA boxes;
+//  * warps 0-15, in four groups of 128 threads, a row to a thread: tile 0 and 1 of
+//    the unit, the even and the odd steps (a step: a group's columns).  A thread
+//    turns its row's codes into bf16 and writes them to tensor memory, where the
+//    matrix unit takes them from (shared memory would be written and read once
+//    more), then reads the step's product back, scales and adds it.  Four groups,
+//    so that one's products run while others turn codes;
+//  * warp 17: issues tcgen05.mma.
+// At a segment's end the groups' sums meet in tensor memory (all four have row r in
+// lane r).  A unit that several blocks share is joined by the last of them to
+// come, in the order of the columns.
+//
+// Every wait is bounded (abort flag and error word); after an abort the warps run
+// on without waiting, so that they meet at the block's barriers.
+using namespace tc;
+
+constexpr int GROUPS_OF_WARPS = 4, WORK_WARPS = 16, THREADS = (WORK_WARPS + 2) * 32;
+constexpr int T_COLS = 64;  // columns of tensor memory for a group's weights, and for its products
+
 struct ProductParams {
   W4Shape m;
   const uint8_t* packed;
-  const __nv_bfloat16* x;
-  long long n, x_seg, x_rs, out_rs;
+  long long total;  // chunks of all units
+  int chunks, seg_chunks, block_bytes, subs, units;
+  long long n, out_rs;
   int epi;
   const __nv_bfloat16* bias;
   __nv_bfloat16* out;
+  float* parts;   // [blocks][2][2 tiles][NT][128]
+  int* counters;  // [token tiles][units]
+  int* err;
+  int skip_load;
+  unsigned long long timeout_ns;
 };
-constexpr int TOK = 8;
 
-__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ ProductParams p) {
-  __shared__ float sx[128][TOK];
-  __shared__ float sg[128][TOK];
-  const W4Shape& m = p.m;
-  const long long unit = blockIdx.x, n0 = static_cast<long long>(blockIdx.y) * TOK;
-  const int tile = threadIdx.x >> 7, r = threadIdx.x & 127;
-  const long long chunks = m.chunks(), seg_chunks = m.seg_chunks();
-  float acc[TOK] = {};
-  for (long long chunk = 0; chunk < chunks; ++chunk) {
-    const long long e = chunk / seg_chunks, in = (chunk - e * seg_chunks) * 128;
-    __syncthreads();
-    for (int i = threadIdx.x; i < 128 * TOK; i += 256) {
-      const int k = i & 127, j = i >> 7;
-      const bool ok = n0 + j < p.n && in + k < m.seg;
-      sx[k][j] = ok ? __bfloat162float(p.x[(n0 + j) * p.x_rs + e * p.x_seg + in + k]) : 0.f;
+// NT: tokens of a product (N); NC: those that are read back.
+template <int NT>
+struct Ring {
+  static constexpr int X_BYTES = NT * 256, CODES = 18432, STAGE = X_BYTES + CODES;
+  static constexpr int STAGES = NT <= 16 ? 8 : (NT <= 32 ? 7 : 6);
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static_assert(SMEM <= 232448 - 1024, "shared memory per block");
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Two codes (bits 0-3 of each half) as bf16: 128 + code by its bits, less 136.
+__device__ __forceinline__ uint32_t two_weights(uint32_t w) {
+  uint32_t d, r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(d) : "r"(w));  // (w & mask) | bits
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x43084308u));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[N]) {
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+  }
+  tmem_wait_ld();
+  // names the registers, so that no use of them moves before the wait
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_store8(uint32_t at, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+template <int NT, int NC>
+__global__ void __launch_bounds__(THREADS, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ ProductParams p) {
+  using R = Ring<NT>;
+  constexpr int LD = NC < 16 ? NC : 16;  // columns read back at a time
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[R::STAGES], empty[R::STAGES], a_full[GROUPS_OF_WARPS], d_full[GROUPS_OF_WARPS], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_abort, s_last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], p.subs == 1 ? WORK_WARPS / 2 : WORK_WARPS);  // the warps that have a step of the chunk
     }
-    __syncthreads();
-    const uint8_t* blk = p.packed + (unit * chunks + chunk) * m.block_bytes();
-    for (int sub = 0; sub < 128 / m.group; ++sub) {
-      float part[TOK] = {};
-      for (int k = sub * m.group; k < (sub + 1) * m.group; k += 8) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + tile * 8192 + (k >> 5) * 2048 + r * 16 + ((k >> 3) & 3) * 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float q = static_cast<float>((w >> (16 * (i & 1) + 4 * (i >> 1))) & 15u) - 8.f;
-#pragma unroll
-          for (int j = 0; j < TOK; ++j) part[j] += q * sx[k + i][j];
+    for (int i = 0; i < GROUPS_OF_WARPS; ++i) {
+      mbar_init(&a_full[i], 4);
+      mbar_init(&d_full[i], 1);
+    }
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == WORK_WARPS && lane == 0) prefetch_tmap(&tx);
+  if (warp == WORK_WARPS + 1) tmem_alloc(&tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;  // group g's weights at T_COLS g, its products at 256 + T_COLS g
+  const Waiter W{&s_abort, p.err, p.timeout_ns};
+  const long long first = p.total * blockIdx.x / gridDim.x, last = p.total * (blockIdx.x + 1) / gridDim.x;
+  const int count = static_cast<int>(last - first);  // chunks
+  const int subs = p.subs, ksteps = 8 / subs;        // K = 16 steps of a group
+  const long long n0 = static_cast<long long>(blockIdx.y) * NT;
+
+  if (warp == WORK_WARPS) {
+    // ------------------------------------------------ copies
+    // The weights are not the previous kernel's to write (what wrote them is done
+    // before the call's first kernel lets others start); the tokens may be.
+    if (lane == 0) {
+      const uint64_t policy = gridDim.y == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+      const uint8_t* src = p.packed + first * p.block_bytes;
+      auto weights = [&](int i) {
+        uint8_t* st = smem + (i % R::STAGES) * R::STAGE;
+        mbar_arrive_expect_tx(&full[i % R::STAGES], static_cast<uint32_t>(p.block_bytes + R::X_BYTES));
+        if (!(p.skip_load && i == 0)) bulk_load(st + R::X_BYTES, src + static_cast<long long>(i) * p.block_bytes,
+                                                static_cast<uint32_t>(p.block_bytes), &full[i % R::STAGES], policy);
+      };
+      int c = static_cast<int>(first % p.chunks), e = c / p.seg_chunks, in = c - e * p.seg_chunks;
+      auto tokens = [&](int i) {
+        uint8_t* st = smem + (i % R::STAGES) * R::STAGE;
+        uint64_t* bar = &full[i % R::STAGES];
+        tma_load_3d(st, &tx, bar, in * 128, e, static_cast<int>(n0));
+        tma_load_3d(st + NT * 128, &tx, bar, in * 128 + 64, e, static_cast<int>(n0));
+        if (++in == p.seg_chunks) {
+          in = 0;
+          if (++e * p.seg_chunks == p.chunks) e = 0;
+        }
+      };
+      const int ahead = count < R::STAGES ? count : R::STAGES;
+      for (int i = 0; i < ahead; ++i) weights(i);
+      grid_dep_wait();
+      for (int i = 0; i < ahead; ++i) tokens(i);
+      int issued = ahead;
+      for (int i = ahead; i < count; ++i) {
+        if (!W(&empty[i % R::STAGES], ((i / R::STAGES) & 1) ^ 1)) break;
+        weights(i);
+        tokens(i);
+        ++issued;
+      }
+      // every issued copy lands before the block may exit
+      for (int i = issued > R::STAGES ? issued - R::STAGES : 0; i < issued; ++i)
+        W.drain(&full[i % R::STAGES], (i / R::STAGES) & 1);
+    }
+    __syncwarp();
+  } else if (warp == WORK_WARPS + 1) {
+    // ------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t ID = idesc(NT, 0, 0);
+      bool ok = true;
+      int step = 0;
+      for (int i = 0; i < count && ok; ++i) {
+        if (!(ok = W(&full[i % R::STAGES], (i / R::STAGES) & 1))) break;
+        const uint32_t xs = smem_u32(smem + (i % R::STAGES) * R::STAGE);
+        for (int sub = 0; sub < subs && ok; ++sub, ++step) {
+          for (int tile = 0; tile < 2; ++tile) {
+            const int g = 2 * tile + (step & 1);
+            if (!(ok = W(&a_full[g], (step >> 1) & 1))) break;
+            tc_fence_after();
+            for (int k = 0; k < ksteps; ++k)
+              umma_bf16_ta(tmem + 256 + g * T_COLS, tmem + g * T_COLS + k * 8, kdesc(xs, NT, sub * ksteps + k), ID, k > 0);
+            umma_commit(&d_full[g]);
+          }
         }
       }
-      const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + 16384)[sub * 256 + threadIdx.x]);
+      umma_commit(&drain);
+      W.drain(&drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ weights to bf16, products back, sums
+    const int g = warp >> 2, tile = g >> 1, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t at_a = tmem + lane_base + g * T_COLS, at_d = tmem + lane_base + 256 + g * T_COLS;
+    const int pieces = 4 / subs;
+    grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
+    float acc[NC];
 #pragma unroll
-      for (int j = 0; j < TOK; ++j) acc[j] += s * part[j];
+    for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+    int mine = 0;  // steps of this group so far
+    long long unit = first / p.chunks;
+    int chunk = static_cast<int>(first - unit * p.chunks);
+    for (int i = 0; i < count; ++i) {
+      const uint8_t* st = smem + (i % R::STAGES) * R::STAGE + R::X_BYTES;
+      const uint32_t codes = smem_u32(st) + tile * 8192 + r * 16;
+      bool had = false;
+      for (int sub = 0; sub < subs; ++sub) {
+        if (((i * subs + sub) & 1) != (g & 1)) continue;
+        if (!had) W.warp(&full[i % R::STAGES], (i / R::STAGES) & 1);
+        had = true;
+#pragma unroll 1
+        for (int q = 0; q < pieces; ++q) {
+          const uint4 v = ld_shared_v4(codes + (sub * pieces + q) * 2048);
+          uint32_t a[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[j] = two_weights(v.x >> (4 * j));
+            a[4 + j] = two_weights(v.y >> (4 * j));
+            a[8 + j] = two_weights(v.z >> (4 * j));
+            a[12 + j] = two_weights(v.w >> (4 * j));
+          }
+          tmem_st16(at_a + q * 16, a);
+        }
+        const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(st + 16384)[sub * 256 + tile * 128 + r]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a_full[g]);
+        W.warp(&d_full[g], mine & 1);
+        ++mine;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NC; c += LD) {
+          uint32_t d[LD];
+          tmem_load<LD>(at_d + c, d);
+#pragma unroll
+          for (int j = 0; j < LD; ++j) acc[c + j] = fmaf(s, __uint_as_float(d[j]), acc[c + j]);
+        }
+      }
+      if (had) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[i % R::STAGES]);
+      }
+      if (++chunk < p.chunks && i + 1 < count) continue;
+
+      // ---- end of a segment of `unit`: the odd steps' sums to the even ones'
+      const int odd = g & 1;
+      if (odd) {
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) tmem_store8(at_d + c, acc + c);
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      bar_sync(1 + tile, 256);
+      if (!odd) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NC; c += LD) {
+          uint32_t d[LD];
+          tmem_load<LD>(at_d + T_COLS + c, d);
+#pragma unroll
+          for (int j = 0; j < LD; ++j) acc[c + j] += __uint_as_float(d[j]);
+        }
+        tc_fence_before();
+      }
+      bar_sync(1 + tile, 256);  // read: the odd group's next products may come
+      if (!odd) {
+        const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
+        const int C = gridDim.x;
+        const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
+        bool write = true;
+        if (c0 != c1) {
+          // a part: [tile][token][row]
+          const long long slot = NT * 256;
+          float* parts = p.parts + static_cast<long long>(blockIdx.y) * C * 2 * slot + tile * (NT * 128) + r;
+          float* to = parts + (2 * blockIdx.x + (blockIdx.x == c0)) * slot;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) __stcg(to + c * 128, acc[c]);
+          __threadfence();
+          bar_sync(3, 256);
+          if (threadIdx.x == 0) {
+            int* counter = p.counters + blockIdx.y * p.units + unit;
+            s_last = atomicAdd(counter, 1) == c1 - c0;
+          }
+          bar_sync(3, 256);
+          write = s_last != 0;
+          if (write) {
+            __threadfence();
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+            for (int b = c0; b <= c1; ++b) {
+              const float* from = parts + (2 * b + (b == c0)) * slot;
+#pragma unroll
+              for (int c = 0; c < NC; ++c) acc[c] += __ldcg(from + c * 128);
+            }
+          }
+        }
+        long long row = unit * 256 + tile * 128 + r;
+        bool store = write && *W.abort_flag == 0;
+        if (p.epi == W4_SWIGLU) {
+          // tile 1 has the second matrix's rows of the same hidden slots
+          if (tile) {
+#pragma unroll
+            for (int c = 0; c < NC; c += 8) tmem_store8(at_d + c, acc + c);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          bar_sync(3, 256);
+          if (!tile) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < NC; c += LD) {
+              uint32_t d[LD];
+              tmem_load<LD>(at_d + 2 * T_COLS + c, d);
+#pragma unroll
+              for (int j = 0; j < LD; ++j) acc[c + j] = acc[c + j] * sigmoid_f(acc[c + j]) * __uint_as_float(d[j]);
+            }
+            tc_fence_before();
+          }
+          bar_sync(3, 256);
+          row = unit * 128 + r;
+          store = store && !tile && row < p.m.T * p.m.sp;
+        } else if (p.epi == W4_GELU) {
+          const long long t = row / p.m.sp, in = row - t * p.m.sp;
+          const float b = p.bias && in < p.m.s && t < p.m.T ? __bfloat162float(p.bias[t * p.m.s + in]) : 0.f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) acc[c] = gelu_tanh_f(acc[c] + b);
+          store = store && row < p.m.T * p.m.sp;
+        } else {
+          store = store && row < p.m.rows;
+          if (p.bias && store) {
+            const float b = __bfloat162float(p.bias[row]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[c] += b;
+          }
+        }
+        if (store) {
+          __nv_bfloat16* to = p.out + n0 * p.out_rs + row;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (n0 + c < p.n) to[c * p.out_rs] = __float2bfloat16_rn(acc[c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+      chunk = 0;
+      ++unit;
     }
   }
-  long long row = unit * 256 + threadIdx.x;
-  if (p.epi == W4_SWIGLU) {
-    __syncthreads();
-    if (tile == 1)
-      for (int j = 0; j < TOK; ++j) sg[r][j] = acc[j];
-    __syncthreads();
-    if (tile == 1) return;
-    row = unit * 128 + r;
-    for (int j = 0; j < TOK; ++j) acc[j] = acc[j] * sigmoid_f(acc[j]) * sg[r][j];
-  } else if (p.epi == W4_GELU) {
-    const long long t = row / m.sp, in = row - t * m.sp;
-    const float b = p.bias && in < m.s && t < m.T ? __bfloat162float(p.bias[t * m.s + in]) : 0.f;
-    for (int j = 0; j < TOK; ++j) acc[j] = gelu_tanh_f(acc[j] + b);
-  } else if (p.bias && row < m.rows) {
-    const float b = __bfloat162float(p.bias[row]);
-    for (int j = 0; j < TOK; ++j) acc[j] += b;
+  grid_dep_launch();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WORK_WARPS + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  if (row >= (p.epi == W4_OUT ? m.rows : m.T * m.sp)) return;
-  for (int j = 0; j < TOK && n0 + j < p.n; ++j) p.out[(n0 + j) * p.out_rs + row] = __float2bfloat16_rn(acc[j]);
+}
+
+// Clears what a call counts in, when everything before it on the stream is done;
+// the products behind it read their weights without a further wait.
+__global__ void __launch_bounds__(256) reset_kernel(int* err, int* counters, int n) {
+  grid_dep_wait();
+  grid_dep_launch();
+  if (threadIdx.x == 0 && blockIdx.x == 0) *err = 0;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) counters[i] = 0;
+}
+
+template <typename... KArgs, typename... Args>
+void launch_dep(void (*kern)(KArgs...), dim3 grid, int block, int smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int NT, int NC>
+int launch_product(const CUtensorMap& tx, const ProductParams& p, dim3 grid, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TP_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done.load() & bit)) {
+    if (cudaFuncSetAttribute(product_kernel<NT, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<NT>::SMEM) != cudaSuccess)
+      return TP_ERR_CUDA;
+    done.fetch_or(bit);
+  }
+  launch_dep(product_kernel<NT, NC>, grid, THREADS, Ring<NT>::SMEM, st, tx, p);
+  return TP_OK;
+}
+
+// How a product of n tokens is cut: NT tokens to a block, `tiles` of them, `blocks`
+// runs of chunks.
+struct Cut {
+  int nt, tiles, blocks;
+};
+Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
+  Cut c;
+  c.nt = n <= 16 ? 16 : (n <= 32 ? 32 : 64);
+  c.tiles = static_cast<int>((n + c.nt - 1) / c.nt);
+  const int64_t most = std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
+  c.blocks = static_cast<int>(std::min<int64_t>(most, total));
+  return c;
 }
 
 // A grid of at most 32 blocks per SM.
@@ -353,22 +716,59 @@ int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack,
   return launched();
 }
 
+size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms) {
+  const w4::Cut c = w4::cut_of(m, n, num_sms);
+  return static_cast<size_t>(c.blocks) * c.tiles * 2 * 256 * c.nt * sizeof(float);
+}
+int64_t w4_product_counters(const W4Shape& m, int64_t n) { return m.units() * ((n + 15) / 16); }
+
+int launch_w4_reset(int* err, int* counters, int64_t n, LaunchCtx& ctx) {
+  w4::launch_dep(w4::reset_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8) + (n == 0))), 256, 0,
+                 ctx.stream, err, counters, static_cast<int>(n));
+  ctx.launches++;
+  return w4::launched();
+}
+
 int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   using namespace w4;
+  const Cut c = cut_of(a.m, a.n, ctx.num_sms);
   ProductParams p{};
   p.m = a.m;
   p.packed = static_cast<const uint8_t*>(a.packed);
-  p.x = static_cast<const __nv_bfloat16*>(a.x);
+  p.chunks = static_cast<int>(a.m.chunks());
+  p.seg_chunks = static_cast<int>(a.m.seg_chunks());
+  p.total = a.m.units() * a.m.chunks();
+  p.block_bytes = a.m.block_bytes();
+  p.subs = 128 / a.m.group;
+  p.units = static_cast<int>(a.m.units());
   p.n = a.n;
-  p.x_seg = a.x_seg;
-  p.x_rs = a.x_rs;
   p.out_rs = a.out_rs;
   p.epi = a.epi;
   p.bias = static_cast<const __nv_bfloat16*>(a.bias);
   p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.parts = static_cast<float*>(a.scratch);
+  p.counters = a.counters;
+  p.err = ctx.err;
+  p.skip_load = ctx.debug_skip_load;
+  p.timeout_ns = ctx.timeout_ns;
+  ctx.debug_skip_load = 0;
+  const uint64_t dims[3] = {static_cast<uint64_t>(a.m.seg), static_cast<uint64_t>(a.m.segs), static_cast<uint64_t>(a.n)};
+  const uint64_t str[2] = {static_cast<uint64_t>(a.m.segs > 1 ? a.x_seg : a.x_rs) * 2, static_cast<uint64_t>(a.x_rs) * 2};
+  const uint32_t box[3] = {64, 1, static_cast<uint32_t>(c.nt)};
+  CUtensorMap tx;
+  if (int rc = encode_map_3d_bf16(&tx, a.x, dims, str, box)) return rc;
+  const dim3 grid(static_cast<unsigned>(c.blocks), static_cast<unsigned>(c.tiles));
   if (ctx.before) ctx.before(ctx.user, a.name, ctx.stream);
-  product_kernel<<<dim3(static_cast<unsigned>(a.m.units()), static_cast<unsigned>((a.n + TOK - 1) / TOK)), 256, 0,
-                   ctx.stream>>>(p);
+  int rc;
+  if (a.n <= 8)
+    rc = launch_product<16, 8>(tx, p, grid, ctx.stream);
+  else if (c.nt == 16)
+    rc = launch_product<16, 16>(tx, p, grid, ctx.stream);
+  else if (c.nt == 32)
+    rc = launch_product<32, 32>(tx, p, grid, ctx.stream);
+  else
+    rc = launch_product<64, 64>(tx, p, grid, ctx.stream);
+  if (rc) return rc;
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
   return launched();
