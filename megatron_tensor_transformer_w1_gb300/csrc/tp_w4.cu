@@ -269,7 +269,7 @@ struct ProductParams {
   W4Shape m;
   const uint8_t* packed;
   long long total;  // chunks of all units
-  int chunks, seg_chunks, block_bytes, subs, units;
+  int chunks, seg_chunks, block_bytes, units;
   long long n, out_rs;
   int epi;
   const __nv_bfloat16* bias;
@@ -279,6 +279,43 @@ struct ProductParams {
   int* err;
   int skip_load;
   unsigned long long timeout_ns;
+};
+
+// Bounded wait on an mbarrier phase, as tc::Waiter's, for waits that mostly last
+// some hundred cycles: the clock, which takes longer than that to read, is looked
+// at only after many tries.
+struct Wait {
+  volatile int* abort_flag;
+  int* err;
+  unsigned long long timeout_ns;
+  __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity, bool honour_abort) const {
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (n & 63u) continue;
+      if (honour_abort && *abort_flag) return false;
+      const uint64_t t = global_timer();
+      if (!t0) t0 = t;
+      if (t - t0 > timeout_ns) {
+        *abort_flag = 1;
+        atomicOr(err, DEV_ERR_TIMEOUT);
+        __threadfence();
+        return false;
+      }
+    }
+  }
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    return mbar_try_wait(bar, parity) || slow(bar, parity, true);
+  }
+  __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
+    if (!mbar_try_wait(bar, parity)) slow(bar, parity, false);
+  }
+  // of a whole warp
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) ok = slow(bar, parity, true);
+    return __all_sync(0xffffffffu, ok) != 0;
+  }
 };
 
 // NT: tokens of a product (N); NC: those that are read back.
@@ -301,6 +338,15 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -340,7 +386,8 @@ __device__ __forceinline__ void tmem_store8(uint32_t at, const float* v) {
                : "memory");
 }
 
-template <int NT, int NC>
+// SUBS: groups of a chunk.
+template <int NT, int NC, int SUBS>
 __global__ void __launch_bounds__(THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ ProductParams p) {
   using R = Ring<NT>;
@@ -354,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < R::STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], p.subs == 1 ? WORK_WARPS / 2 : WORK_WARPS);  // the warps that have a step of the chunk
+      mbar_init(&empty[i], SUBS == 1 ? WORK_WARPS / 2 : WORK_WARPS);  // the warps that have a step of the chunk
     }
     for (int i = 0; i < GROUPS_OF_WARPS; ++i) {
       mbar_init(&a_full[i], 4);
@@ -371,10 +418,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;  // group g's weights at T_COLS g, its products at 256 + T_COLS g
-  const Waiter W{&s_abort, p.err, p.timeout_ns};
+  const Wait W{&s_abort, p.err, p.timeout_ns};
   const long long first = p.total * blockIdx.x / gridDim.x, last = p.total * (blockIdx.x + 1) / gridDim.x;
   const int count = static_cast<int>(last - first);  // chunks
-  const int subs = p.subs, ksteps = 8 / subs;        // K = 16 steps of a group
+  constexpr int KSTEPS = 8 / SUBS;  // K = 16 steps of a group
   const long long n0 = static_cast<long long>(blockIdx.y) * NT;
 
   if (warp == WORK_WARPS) {
@@ -419,81 +466,106 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == WORK_WARPS + 1) {
     // ------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t ID = idesc(NT, 0, 0);
-      bool ok = true;
-      int step = 0;
-      for (int i = 0; i < count && ok; ++i) {
-        if (!(ok = W(&full[i % R::STAGES], (i / R::STAGES) & 1))) break;
-        const uint32_t xs = smem_u32(smem + (i % R::STAGES) * R::STAGE);
-        for (int sub = 0; sub < subs && ok; ++sub, ++step) {
-          for (int tile = 0; tile < 2; ++tile) {
-            const int g = 2 * tile + (step & 1);
-            if (!(ok = W(&a_full[g], (step >> 1) & 1))) break;
-            tc_fence_after();
-            for (int k = 0; k < ksteps; ++k)
-              umma_bf16_ta(tmem + 256 + g * T_COLS, tmem + g * T_COLS + k * 8, kdesc(xs, NT, sub * ksteps + k), ID, k > 0);
+    // A product takes 48 cycles, whatever N up to 64 is (measured; M 128, K 16, from
+    // tensor or shared memory): few instructions may lie between two.
+    const bool leader = elect_one();
+    constexpr uint32_t ID = idesc(NT, 0, 0);
+    const uint64_t x_desc = kdesc(smem_u32(smem), NT, 0);
+    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0, step = 0;
+#pragma unroll 1
+    for (int i = 0; i < count && ok; ++i) {
+      ok = W.warp(&full[stage], phase);
+      const uint64_t xd = x_desc + static_cast<uint64_t>(stage * (R::STAGE >> 4));
+#pragma unroll
+      for (int sub = 0; sub < SUBS; ++sub, ++step) {
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          const uint32_t g = 2 * tile + (step & 1);
+          ok = ok && W.warp(&a_full[g], (step >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ad = tmem + g * T_COLS;
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < KSTEPS; ++k) {
+              const int ks = sub * KSTEPS + k;
+              umma_bf16_ta(ad + 256, ad + k * 8, xd + static_cast<uint64_t>(((ks >> 2) * NT * 128 + (ks & 3) * 32) >> 4), ID,
+                           k > 0);
+            }
             umma_commit(&d_full[g]);
           }
+          __syncwarp();
         }
       }
-      umma_commit(&drain);
-      W.drain(&drain, 0);
+      if (++stage == R::STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
+    if (leader) umma_commit(&drain);
+    __syncwarp();
+    W.drain(&drain, 0);
     __syncwarp();
   } else {
     // ------------------------------------------------ weights to bf16, products back, sums
     const int g = warp >> 2, tile = g >> 1, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t at_a = tmem + lane_base + g * T_COLS, at_d = tmem + lane_base + 256 + g * T_COLS;
-    const int pieces = 4 / subs;
+    constexpr int PIECES = 4 / SUBS;
     grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
     float acc[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[c] = 0.f;
-    int mine = 0;  // steps of this group so far
+    uint32_t mine = 0;  // steps of this group so far
+    int stage = 0;
+    uint32_t phase = 0;
     long long unit = first / p.chunks;
     int chunk = static_cast<int>(first - unit * p.chunks);
-    for (int i = 0; i < count; ++i) {
-      const uint8_t* st = smem + (i % R::STAGES) * R::STAGE + R::X_BYTES;
-      const uint32_t codes = smem_u32(st) + tile * 8192 + r * 16;
-      bool had = false;
-      for (int sub = 0; sub < subs; ++sub) {
-        if (((i * subs + sub) & 1) != (g & 1)) continue;
-        if (!had) W.warp(&full[i % R::STAGES], (i / R::STAGES) & 1);
-        had = true;
 #pragma unroll 1
-        for (int q = 0; q < pieces; ++q) {
-          const uint4 v = ld_shared_v4(codes + (sub * pieces + q) * 2048);
-          uint32_t a[16];
+    for (int i = 0; i < count; ++i) {
+      if (SUBS > 1 || (i & 1) == (g & 1)) {
+        const uint8_t* st = smem + stage * R::STAGE + R::X_BYTES;
+        const uint32_t codes = smem_u32(st) + tile * 8192 + r * 16;
+        W.warp(&full[stage], phase);
+#pragma unroll 1
+        for (int sub = SUBS > 1 ? g & 1 : 0; sub < SUBS; sub += 2) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[j] = two_weights(v.x >> (4 * j));
-            a[4 + j] = two_weights(v.y >> (4 * j));
-            a[8 + j] = two_weights(v.z >> (4 * j));
-            a[12 + j] = two_weights(v.w >> (4 * j));
+          for (int q = 0; q < PIECES; ++q) {
+            const uint4 v = ld_shared_v4(codes + (sub * PIECES + q) * 2048);
+            uint32_t a[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              a[j] = two_weights(v.x >> (4 * j));
+              a[4 + j] = two_weights(v.y >> (4 * j));
+              a[8 + j] = two_weights(v.z >> (4 * j));
+              a[12 + j] = two_weights(v.w >> (4 * j));
+            }
+            tmem_st16(at_a + q * 16, a);
           }
-          tmem_st16(at_a + q * 16, a);
+          const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(st + 16384)[sub * 256 + tile * 128 + r]);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&a_full[g]);
+          W.warp(&d_full[g], mine & 1);
+          ++mine;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < NC; c += LD) {
+            uint32_t d[LD];
+            tmem_load<LD>(at_d + c, d);
+#pragma unroll
+            for (int j = 0; j < LD; ++j) acc[c + j] = fmaf(s, __uint_as_float(d[j]), acc[c + j]);
+          }
         }
-        const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(st + 16384)[sub * 256 + tile * 128 + r]);
-        tmem_wait_st();
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&a_full[g]);
-        W.warp(&d_full[g], mine & 1);
-        ++mine;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < NC; c += LD) {
-          uint32_t d[LD];
-          tmem_load<LD>(at_d + c, d);
-#pragma unroll
-          for (int j = 0; j < LD; ++j) acc[c + j] = fmaf(s, __uint_as_float(d[j]), acc[c + j]);
-        }
+        if (lane == 0) mbar_arrive(&empty[stage]);
       }
-      if (had) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[i % R::STAGES]);
+      if (++stage == R::STAGES) {
+        stage = 0;
+        phase ^= 1;
       }
       if (++chunk < p.chunks && i + 1 < count) continue;
 
@@ -634,19 +706,26 @@ void launch_dep(void (*kern)(KArgs...), dim3 grid, int block, int smem, cudaStre
   cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int NT, int NC>
-int launch_product(const CUtensorMap& tx, const ProductParams& p, dim3 grid, cudaStream_t st) {
+template <int NT, int NC, int SUBS>
+int launch_product_inst(const CUtensorMap& tx, const ProductParams& p, dim3 grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return TP_ERR_CUDA;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load() & bit)) {
-    if (cudaFuncSetAttribute(product_kernel<NT, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<NT>::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(product_kernel<NT, NC, SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<NT>::SMEM) != cudaSuccess)
       return TP_ERR_CUDA;
     done.fetch_or(bit);
   }
-  launch_dep(product_kernel<NT, NC>, grid, THREADS, Ring<NT>::SMEM, st, tx, p);
+  launch_dep(product_kernel<NT, NC, SUBS>, grid, THREADS, Ring<NT>::SMEM, st, tx, p);
   return TP_OK;
+}
+
+template <int NT, int NC>
+int launch_product(const CUtensorMap& tx, const ProductParams& p, dim3 grid, cudaStream_t st) {
+  if (p.m.group == 128) return launch_product_inst<NT, NC, 1>(tx, p, grid, st);
+  if (p.m.group == 64) return launch_product_inst<NT, NC, 2>(tx, p, grid, st);
+  return launch_product_inst<NT, NC, 4>(tx, p, grid, st);
 }
 
 // How a product of n tokens is cut: NT tokens to a block, `tiles` of them, `blocks`
@@ -739,7 +818,6 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   p.seg_chunks = static_cast<int>(a.m.seg_chunks());
   p.total = a.m.units() * a.m.chunks();
   p.block_bytes = a.m.block_bytes();
-  p.subs = 128 / a.m.group;
   p.units = static_cast<int>(a.m.units());
   p.n = a.n;
   p.out_rs = a.out_rs;
