@@ -520,7 +520,9 @@ TPFFN_API int tp_ffn_unshard_rows4(const tp_ffn_plan* plan, int group, const voi
  * both of the same group): x, b1, b2 and y as there.  The shards are summed in
  * the order t = 0..T_p-1; results do not change from run to run.  A product is
  * summed in 32 bits within a group, times its scale, over the groups in 32 bits;
- * the hidden activations are rounded to bf16.
+ * the hidden activations are rounded to bf16 or better.  A token with an infinity
+ * or a NaN, in x or among its hidden activations, gets those; the others are as
+ * without it.
  * flags: TP_FLAG_SYNC, TP_FLAG_TIMING; the TP_SUM_* choices make no difference.
  * Errors as tp_ffn_fwd; TP_ERR_UNSUPPORTED for fp32 plans. */
 TPFFN_API size_t tp_ffn_workspace4_bytes(const tp_ffn_plan* plan, int64_t n_tokens, int flags);

@@ -1579,9 +1579,10 @@ W4Shape w4_qkv(const tp_attn_plan* a, int group) {
 }
 
 // Workspace of a forward pass: error word, the products' counters and parts (of
-// one product at a time), hidden activations.
+// one product at a time), the tokens' blocks and the hidden activations (blocks, or
+// bf16 rows).
 struct Ws4 {
-  size_t counters = 0, parts = 0, h = 0, total = 0;
+  size_t counters = 0, parts = 0, x = 0, h = 0, total = 0;
   int64_t n_up = 0, n_down = 0;  // counters
 };
 Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
@@ -1599,8 +1600,11 @@ Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
   off += align_up(static_cast<size_t>(L.n_up + L.n_down) * sizeof(int));
   L.parts = off;
   off += align_up(parts);
+  L.x = off;
+  off += align_up(w4_image_bytes(p->act != TP_ACT_NONE ? up : down, n));
   L.h = off;
-  if (p->act != TP_ACT_NONE) off += align_up(static_cast<size_t>(n) * p->T_p * w4_sp(p) * 2);
+  if (p->act != TP_ACT_NONE)
+    off += align_up(w4_few(n) ? w4_image_bytes(down, n) : static_cast<size_t>(n) * p->T_p * w4_sp(p) * 2);
   L.total = off;
   return L;
 }
@@ -1621,48 +1625,51 @@ void ctx4(const tp_ffn_plan* p, void* workspace, int flags, cudaStream_t stream,
   }
 }
 
-// The products of a forward pass; the counters are clear.
 int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n, const void* x, const void* w13, const void* w2,
               const void* b1, const void* b2, void* y, char* ws, LaunchCtx& ctx) {
   const Ws4 L = ws4_layout(p, n);
   W4Product g;
   g.n = n;
+  g.x = x;
   g.scratch = ws + L.parts;
   g.counters = reinterpret_cast<int*>(ws + L.counters);
-  const void* h = x;
-  int64_t h_seg = p->s, h_rs = p->d_ff;
-  if (p->act != TP_ACT_NONE) {
-    g.name = p->act == TP_ACT_SWIGLU ? "up_swiglu4" : "up_gelu4";
-    g.m = w4_up(p, group);
-    g.packed = w13;
-    g.x = x;
-    g.x_rs = p->d;
-    g.epi = p->act == TP_ACT_SWIGLU ? W4_SWIGLU : W4_GELU;
-    g.bias = b1;
-    g.out = ws + L.h;
-    g.out_rs = p->T_p * w4_sp(p);
-    if (int rc = launch_w4_product(g, ctx)) return rc;
-    h = ws + L.h;
-    h_seg = w4_sp(p);
-    h_rs = g.out_rs;
+  g.image = ws + L.x;
+  W4Product down = g;
+  down.name = "down4";
+  down.m = w4_down(p, group);
+  down.packed = w2;
+  down.x_seg = p->s;
+  down.x_rs = p->d_ff;
+  down.bias = b2;
+  down.out = y;
+  down.out_rs = p->d;
+  if (p->act == TP_ACT_NONE) {
+    if (int rc = launch_w4_prepare(down, ctx.err, L.n_down, ctx)) return rc;
+    return launch_w4_product(down, ctx);
   }
-  g.name = "down4";
-  g.m = w4_down(p, group);
-  g.packed = w2;
-  g.x = h;
-  g.x_seg = h_seg;
-  g.x_rs = h_rs;
-  g.epi = W4_OUT;
-  g.bias = b2;
-  g.out = y;
-  g.out_rs = p->d;
-  g.counters += L.n_up;
-  return launch_w4_product(g, ctx);
+  g.name = p->act == TP_ACT_SWIGLU ? "up_swiglu4" : "up_gelu4";
+  g.m = w4_up(p, group);
+  g.packed = w13;
+  g.x_rs = p->d;
+  g.epi = p->act == TP_ACT_SWIGLU ? W4_SWIGLU : W4_GELU;
+  g.bias = b1;
+  g.out = ws + L.h;
+  g.out_rs = p->T_p * w4_sp(p);
+  g.image_out = ws + L.h;
+  int rc = launch_w4_prepare(g, ctx.err, L.n_up + L.n_down, ctx);
+  if (!rc) rc = launch_w4_product(g, ctx);
+  if (rc) return rc;
+  down.x = ws + L.h;
+  down.x_seg = w4_sp(p);
+  down.x_rs = g.out_rs;
+  down.image = ws + L.h;
+  down.counters += L.n_up;
+  return launch_w4_product(down, ctx);
 }
 
 // The decode pass: its counters lie together, those of q/k/v first.
 struct Decode4Ws {
-  size_t attend = 0, counters = 0, parts = 0, qkv = 0, q = 0, c = 0, total = 0;
+  size_t attend = 0, counters = 0, parts = 0, image = 0, qkv = 0, q = 0, c = 0, total = 0;
   int64_t n_qkv = 0, n_wo = 0;
 };
 Decode4Ws decode4_ws(const tp_attn_plan* a, const KvSpec& sp) {
@@ -1680,6 +1687,9 @@ Decode4Ws decode4_ws(const tp_attn_plan* a, const KvSpec& sp) {
   L.parts = off;
   const size_t p1 = w4_product_scratch(qkv, n, sms), p2 = w4_product_scratch(wo, n, sms);
   off += align_up(p1 > p2 ? p1 : p2);
+  L.image = off;
+  const size_t i1 = w4_image_bytes(qkv, n), i2 = w4_image_bytes(wo, n);
+  off += align_up(i1 > i2 ? i1 : i2);
   L.qkv = off;
   off += align_up(static_cast<size_t>(n) * a->W * 2);
   L.q = off;
@@ -1906,10 +1916,7 @@ int tp_ffn_fwd4(const tp_ffn_plan* p, int group, int64_t n, const void* x, const
   if (workspace_bytes < ws4_layout(p, n).total) return TP_ERR_INVALID;
   LaunchCtx ctx;
   ctx4(p, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
-  char* ws = static_cast<char*>(workspace);
-  const Ws4 L = ws4_layout(p, n);
-  rc = launch_w4_reset(ctx.err, reinterpret_cast<int*>(ws + L.counters), L.n_up + L.n_down, ctx);
-  if (!rc) rc = fwd4_impl(p, group, n, x, w13_4, w2_4, b1, b2, y, ws, ctx);
+  rc = fwd4_impl(p, group, n, x, w13_4, w2_4, b1, b2, y, static_cast<char*>(workspace), ctx);
   return finish_call(p, ctx, rc, flags, workspace);
 }
 
@@ -1948,8 +1955,6 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
   ctx4(a->wo, workspace, flags, reinterpret_cast<cudaStream_t>(stream), ctx);
   const int64_t n = sp.n_tokens;
   char* ws = static_cast<char*>(workspace);
-  int* counters = reinterpret_cast<int*>(ws + L.counters);
-  if ((rc = launch_w4_reset(ctx.err, counters, L.n_qkv + L.n_wo, ctx))) return rc;
   W4Product g;
   g.name = "qkv_proj4";
   g.m = w4_qkv(a, group);
@@ -1959,9 +1964,11 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
   g.x_rs = a->d;
   g.out = ws + L.qkv;
   g.out_rs = a->W;
+  g.image = ws + L.image;
   g.scratch = ws + L.parts;
-  g.counters = counters;
-  rc = launch_w4_product(g, ctx);
+  g.counters = reinterpret_cast<int*>(ws + L.counters);
+  rc = launch_w4_prepare(g, ctx.err, L.n_qkv + L.n_wo, ctx);
+  if (!rc) rc = launch_w4_product(g, ctx);
   if (!rc) rc = launch_kv_append(sp, rot, ws + L.qkv, ws + L.q, static_cast<int*>(workspace), false, ctx);
   if (!rc)
     rc = launch_kv_attend(sp, ws + L.q, ws + L.c, nullptr, static_cast<int*>(workspace), false, ws + L.attend, ctx);
@@ -1974,8 +1981,9 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
     g.x_rs = a->wo->d_ff;
     g.out = y;
     g.out_rs = a->d;
-    g.counters = counters + L.n_qkv;
-    rc = launch_w4_product(g, ctx);
+    g.counters += L.n_qkv;
+    if (w4_few(n)) rc = launch_w4_prepare(g, nullptr, 0, ctx);
+    if (!rc) rc = launch_w4_product(g, ctx);
   }
   return kv_finish(a, ctx, rc, flags, workspace);
 }

@@ -248,9 +248,9 @@ int launch_kv_attend(const KvSpec& a, const void* q, void* o, float* lse, int* h
 // Packed layout, what the products read: the rows in tiles of 128, two to a
 // unit, the columns of every segment in chunks of 128 slots (those behind the
 // segment's end hold code 8).  Block (unit, chunk) lies at unit * chunks + chunk:
-// codes [2 tiles][4][128 rows][16 bytes], piece i of a row being its slots
-// 32 i .. 32 i + 31, a 32-bit word eight of them, slot 2 j in bits 4 j and slot
-// 2 j + 1 in bits 16 + 4 j; then scales [128 / group][256 rows].
+// codes [2 tiles][128 rows][4 pieces][4 words], piece t of a row at place t ^
+// ((row >> 1) & 3), its word q the slots 32 q + 8 t .. + 7, slot 2 j of them in bits
+// 4 j and slot 2 j + 1 in bits 16 + 4 j; then scales [128 / group][256 rows].
 enum W4Rows : int {
   W4_PLAIN = 0,   // output rows as they are
   W4_HIDDEN = 1,  // shard t's s hidden units in sp slots (a multiple of 128)
@@ -328,13 +328,19 @@ struct W4Product {
   const void* bias = nullptr;    // W4_OUT: by row; W4_GELU: by hidden unit
   void* out = nullptr;           // bf16; W4_GELU and W4_SWIGLU: by hidden slot
   int64_t out_rs = 0;
+  // Up to 16 tokens (w4_few): x is read as blocks, which launch_w4_prepare makes of
+  // it or an up product has left in its image_out, and so are the hidden activations.
+  void *image = nullptr, *image_out = nullptr;  // w4_image_bytes
   void* scratch = nullptr;       // w4_product_scratch bytes
   int* counters = nullptr;       // w4_product_counters words, 0 before the launch
 };
 size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms);
 int64_t w4_product_counters(const W4Shape& m, int64_t n);
-// The kernel before a call's first product: clears the error word and the counters.
-int launch_w4_reset(int* err, int* counters, int64_t n, LaunchCtx& ctx);
+bool w4_few(int64_t n);
+size_t w4_image_bytes(const W4Shape& m, int64_t n);  // of the tokens that m multiplies
+// The kernel before a call's first product (err: the error word, else null): the
+// image of p.x if there is to be one; clears the error word and n_counters counters.
+int launch_w4_prepare(const W4Product& p, int* err, int64_t n_counters, LaunchCtx& ctx);
 int launch_w4_product(const W4Product& p, LaunchCtx& ctx);
 
 }  // namespace tpffn

@@ -5,6 +5,7 @@
 // elements are (code - 8) s with codes 0..15.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -158,18 +159,13 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restri
 }
 
 // ================================================================ packing
-// Eight codes in column order <-> a packed word (even columns in the low half).
+// Eight codes in column order as a packed word (even columns in the low half).
 __device__ __forceinline__ uint32_t half_of(uint32_t w) {  // nibbles 0, 2, 4, 6
   w &= 0x0f0f0f0fu;
   w = (w | (w >> 4)) & 0x00ff00ffu;
   return (w | (w >> 8)) & 0xffffu;
 }
-__device__ __forceinline__ uint32_t spread(uint32_t h) {
-  h = (h | (h << 8)) & 0x00ff00ffu;
-  return (h | (h << 4)) & 0x0f0f0f0fu;
-}
 __device__ __forceinline__ uint32_t to_packed(uint32_t w) { return half_of(w) | (half_of(w >> 4) << 16); }
-__device__ __forceinline__ uint32_t to_natural(uint32_t p) { return spread(p & 0xffffu) | (spread(p >> 16) << 4); }
 
 // A block of the packed layout to a thread block.
 __global__ void __launch_bounds__(256) pack_kernel(W4Shape m, W4Codes c, uint8_t* packed, int unpack) {
@@ -178,23 +174,23 @@ __global__ void __launch_bounds__(256) pack_kernel(W4Shape m, W4Codes c, uint8_t
   for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
     const long long unit = b / chunks, chunk = b - unit * chunks, e = chunk / seg_chunks, in = (chunk - e * seg_chunks) * 128;
     uint8_t* blk = packed + b * m.block_bytes();
-    for (int i = threadIdx.x; i < 1024; i += 256) {
+    for (int i = threadIdx.x; i < 1024 && !unpack; i += 256) {
       const int piece = i & 3, r = (i >> 2) & 127, tile = i >> 9;
       const W4Tile t = w4_tile(m, unit * 2 + tile);
-      const long long col0 = in + piece * 32;  // within the segment
-      const bool row_ok = r < t.n;
-      const int live = !row_ok || col0 >= m.seg ? 0 : (m.seg - col0 < 32 ? static_cast<int>(m.seg - col0) : 32);
-      uint4* at = reinterpret_cast<uint4*>(blk + tile * 8192 + piece * 2048 + r * 16);
-      uint8_t* src = static_cast<uint8_t*>(c.codes[t.mat]) + (t.row0 + r) * row_bytes;
-      const long long from = e * m.seg + col0;
-      uint32_t w[4] = {0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
-      if (!unpack) {
+      const uint8_t* src = static_cast<const uint8_t*>(c.codes[t.mat]) + (t.row0 + r) * row_bytes;
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const long long col = in + 32 * q + 8 * piece, from = e * m.seg + col;  // within the segment, the row
+        const int live = r >= t.n || col >= m.seg ? 0 : (m.seg - col < 8 ? static_cast<int>(m.seg - col) : 8);
+        uint32_t v = 0x88888888u;
         for (int j = 0; j < live; ++j) {
-          const uint32_t q = (src[(from + j) >> 1] >> (4 * ((from + j) & 1))) & 15u;
-          w[j >> 3] = (w[j >> 3] & ~(15u << (4 * (j & 7)))) | (q << (4 * (j & 7)));
+          const uint32_t code = (src[(from + j) >> 1] >> (4 * ((from + j) & 1))) & 15u;
+          v = (v & ~(15u << (4 * j))) | (code << (4 * j));
         }
-        *at = make_uint4(to_packed(w[0]), to_packed(w[1]), to_packed(w[2]), to_packed(w[3]));
+        w[q] = to_packed(v);
       }
+      *reinterpret_cast<uint4*>(blk + tile * 8192 + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     for (int i = threadIdx.x; i < 256 * (128 / m.group); i += 256) {
       const int r = i & 127, tile = (i >> 7) & 1, sub = i >> 8;
@@ -222,8 +218,8 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
       for (int h = 0; h < 2 && c0 + h < cols; ++h) {
         const long long e = (c0 + h) / m.seg, in = c0 + h - e * m.seg, chunk = e * seg_chunks + in / 128;
         const int k = static_cast<int>(in & 127);
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(from + chunk * m.block_bytes() + (k >> 5) * 2048 + r * 16 +
-                                                              ((k >> 3) & 3) * 4);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(from + chunk * m.block_bytes() + r * 64 +
+                                                              ((((k >> 3) & 3) ^ ((r >> 1) & 3)) << 4) + (k >> 5) * 4);
         const uint32_t q = (w >> (16 * (k & 1) + 4 * ((k & 7) >> 1))) & 15u;
         byte = h ? (byte & 0x0fu) | (q << 4) : (byte & 0xf0u) | q;
       }
@@ -274,7 +270,9 @@ struct ProductParams {
   int epi;
   const __nv_bfloat16* bias;
   __nv_bfloat16* out;
-  float* parts;   // [blocks][2][2 tiles][NT][128]
+  const uint8_t* image;  // few tokens: the tokens' blocks, and the hidden activations'
+  uint8_t* image_out;
+  float* parts;   // [blocks][2][2 tiles][NT][128]; few tokens: [blocks][2][NT][256]
   int* counters;  // [token tiles][units]
   int* err;
   int skip_load;
@@ -339,6 +337,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -380,6 +383,10 @@ __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[N]) {
                  : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                    "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
+__device__ __forceinline__ void tmem_store4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_store8(uint32_t at, const float* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "f"(v[0]), "f"(v[1]),
                "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
@@ -391,7 +398,7 @@ template <int NT, int NC, int SUBS>
 __global__ void __launch_bounds__(THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ ProductParams p) {
   using R = Ring<NT>;
-  constexpr int LD = NC < 16 ? NC : 16;  // columns read back at a time
+  constexpr int LD = 16;  // columns read back at a time
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[R::STAGES], empty[R::STAGES], a_full[GROUPS_OF_WARPS], d_full[GROUPS_OF_WARPS], drain;
@@ -527,22 +534,27 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < count; ++i) {
       if (SUBS > 1 || (i & 1) == (g & 1)) {
         const uint8_t* st = smem + stage * R::STAGE + R::X_BYTES;
-        const uint32_t codes = smem_u32(st) + tile * 8192 + r * 16;
+        const uint32_t codes = smem_u32(st) + tile * 8192 + r * 64;
         W.warp(&full[stage], phase);
 #pragma unroll 1
         for (int sub = SUBS > 1 ? g & 1 : 0; sub < SUBS; sub += 2) {
 #pragma unroll
-          for (int q = 0; q < PIECES; ++q) {
-            const uint4 v = ld_shared_v4(codes + (sub * PIECES + q) * 2048);
-            uint32_t a[16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              a[j] = two_weights(v.x >> (4 * j));
-              a[4 + j] = two_weights(v.y >> (4 * j));
-              a[8 + j] = two_weights(v.z >> (4 * j));
-              a[12 + j] = two_weights(v.w >> (4 * j));
+          for (int t = 0; t < 4; ++t) {
+            // the step's words of piece t
+            const uint32_t at = codes + ((t ^ ((r >> 1) & 3)) << 4) + sub * (PIECES * 4);
+            uint32_t v[PIECES];
+            if constexpr (PIECES == 4) {
+              const uint4 all = ld_shared_v4(at);
+              v[0] = all.x, v[1] = all.y, v[2] = all.z, v[3] = all.w;
+            } else if constexpr (PIECES == 2) {
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+            } else {
+              v[0] = ld_shared(at);
             }
-            tmem_st16(at_a + q * 16, a);
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q)
+              tmem_store4(at_a + q * 16 + t * 4, two_weights(v[q]), two_weights(v[q] >> 4), two_weights(v[q] >> 8),
+                          two_weights(v[q] >> 12));
           }
           const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(st + 16384)[sub * 256 + tile * 128 + r]);
           tmem_wait_st();
@@ -682,13 +694,392 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Clears what a call counts in, when everything before it on the stream is done;
-// the products behind it read their weights without a further wait.
-__global__ void __launch_bounds__(256) reset_kernel(int* err, int* counters, int n) {
+// ---------------------------------------------------------------- few tokens
+// Up to 16 tokens: m16n8k16 matrix instructions on registers.  They take 2.05 cycles
+// an SM (measured), 8 tokens of a chunk 262 of the some 720 that its bytes take, 16
+// tokens 525; the tensor-memory products take 768 whatever the number of tokens,
+// besides the way of the weights into tensor memory.
+//
+// What is left to count are the instructions that make operands of codes.  A code
+// in the low bits of an fp16 number is code * 2^-24, a subnormal, and four bits
+// higher code * 2^-20: a word's eight codes are four operand registers after one
+// shift and four masks, without an addition or a conversion.  For that
+//  * the tokens are fp16 too: a block of 128 columns of a token times a power of
+//    two that brings its largest element to 2^14..2^15 (bf16's eight bits are kept
+//    down to 2^-25 of it, what is smaller is rounded to 2^-40 of it), and columns 2, 3,
+//    6, 7 of each eight times 2^-4, for their codes' place;
+//  * the codes' offset of 8 is taken off as the block's sum: a product starts at -8
+//    times the sum of the 32, 64 or 128 columns.
+// A token with an infinity or a NaN so gets NaN throughout.
+// (With codes made into bf16 as below, 11 instructions a word, the 70B
+// feed-forward took 102 us for one token.)
+//
+// A block of tokens as the kernels keep it ("image"), for NT tokens: [2][NT][128
+// bytes], 64 columns each, 16-byte pieces swizzled by the token (piece i at i ^
+// (token & 7)); float [NT][8], -8 * 2^-24 times the sums of its four 32-column
+// parts, its two halves and the whole, and the power of two that undoes the block's.
+// The order of a product's columns is free as long as both operands have it: lane
+// t of a row's four takes the 32-bit word of codes 8 t .. 8 t + 7 of 32 columns, its
+// pairs as the halves of two k16 steps, and so reads the same 8 columns of a token
+// in one piece.  Token t of eight stands in column 2 t, token t + 4 in column 2 t +
+// 1 of the product, so that the two tokens of an eighth of a warp lie in different
+// halves of the swizzled rows.
+// 8 warps, 32 rows of the unit each, two blocks per SM.  At a segment's end the rows
+// meet in shared memory, from where they go out in order.
+__host__ __device__ constexpr int image_bytes(int nt) { return nt * 288; }
+
+// Columns 4 lane .. 4 lane + 3 of a token's block, by a warp, into an image.
+__device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, int lane, const float (&v)[4]) {
+  const float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+  // (infinities count as the largest numbers, NaN is left out: either spoils the block's sum)
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
+  const int e = min(141 - static_cast<int>(min(most >> 23, 254u)), 126);  // most * 2^e in 2^14..2^15
+  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
+  const float2 a = __half22float2(lo), b = __half22float2(hi);
+  float sum = (a.x + a.y) + 16.f * (b.x + b.y);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
+  *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  sum *= -4.76837158203125e-7f;  // -8 * 2^-24
+  const float two = sum + __shfl_xor_sync(0xffffffffu, sum, 8), all = two + __shfl_xor_sync(0xffffffffu, two, 16);
+  float* tail = reinterpret_cast<float*>(image + nt * 256) + token * 8;
+  if ((lane & 7) == 0) tail[lane >> 3] = sum;
+  if ((lane & 15) == 0) tail[4 + (lane >> 4)] = two;
+  if (lane == 0) *reinterpret_cast<float2*>(tail + 6) = make_float2(all, __uint_as_float(static_cast<uint32_t>(127 - e) << 23));
+}
+
+struct PrepareParams {
+  const __nv_bfloat16* x;
+  long long x_seg, x_rs, seg, seg_chunks, chunks, n;
+  int nt;
+  uint8_t* image;  // [chunks]
+  int *err, *counters, n_counters;
+};
+// The kernel before a call's first product: the tokens' blocks, a warp to a token's;
+// clears what the call counts in.  It lets others start when everything before it
+// on the stream is done: the products behind it read their weights without a further wait.
+__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  if (threadIdx.x == 0 && blockIdx.x == 0) *err = 0;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) counters[i] = 0;
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < p.n_counters; i += gridDim.x * 256) p.counters[i] = 0;
+  for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < p.chunks * p.nt; i += gridDim.x * 8ll) {
+    const long long chunk = i / p.nt, e = chunk / p.seg_chunks, col = (chunk - e * p.seg_chunks) * 128 + lane * 4;
+    const int token = static_cast<int>(i - chunk * p.nt);
+    float v[4] = {};
+    if (token < p.n && col < p.seg) {  // segments end at multiples of 8
+      const uint2 w = *reinterpret_cast<const uint2*>(p.x + token * p.x_rs + e * p.x_seg + col);
+      v[0] = bf16_at(w.x, 0), v[1] = bf16_at(w.x, 1), v[2] = bf16_at(w.y, 0), v[3] = bf16_at(w.y, 1);
+    }
+    store_block(p.image + chunk * image_bytes(p.nt), p.nt, token, lane, v);
+  }
+}
+
+template <int NT>
+struct Few {
+  static constexpr int X_BYTES = image_bytes(NT), CODES = 18432, STAGE = X_BYTES + CODES;
+  static constexpr int STAGES = NT == 8 ? 5 : 4;
+  static constexpr int SUM_PITCH = 256 + 8;  // floats: a token's rows
+  static constexpr int M_SUM = STAGES * STAGE;
+  static constexpr int SMEM = M_SUM + NT * SUM_PITCH * 4 + 128;
+  static_assert(2 * (SMEM + 2048) <= 233472, "two blocks per SM");
+};
+constexpr int FEW_WARPS = 8, FEW_THREADS = (FEW_WARPS + 1) * 32;
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+// Four neighbouring rows of a token, by a warp that has 128: bias or activation, and out.
+template <int NT>
+__device__ __forceinline__ void write4(const ProductParams& p, int token, long long row, int lane, float4 v) {
+  float a[4] = {v.x, v.y, v.z, v.w};
+  if (p.epi == W4_OUT) {
+    if (token >= p.n || row >= p.m.rows) return;  // rows are a multiple of 8
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] += __bfloat162float(p.bias[row + i]);
+    }
+    *reinterpret_cast<uint2*>(p.out + token * p.out_rs + row) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    return;
+  }
+  const long long chunk = row >> 7;
+  if (chunk * 128 >= p.m.T * p.m.sp) return;
+  if (p.epi == W4_GELU) {
+    const long long t = row / p.m.sp, in = row - t * p.m.sp;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = gelu_tanh_f(a[i] + (p.bias && in + i < p.m.s ? __bfloat162float(p.bias[t * p.m.s + in + i]) : 0.f));
+  }
+  store_block(p.image_out + chunk * image_bytes(NT), NT, token, lane, a);
+}
+
+template <int NT, int SUBS>
+__global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_constant__ ProductParams p) {
+  using F = Few<NT>;
+  constexpr int NB = NT / 8;  // products of eight tokens
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  __shared__ uint64_t full[F::STAGES], empty[F::STAGES];
+  __shared__ int s_abort, s_last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], FEW_WARPS);
+    }
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  grid_dep_launch();
+  const Wait W{&s_abort, p.err, p.timeout_ns};
+  const long long first = p.total * blockIdx.x / gridDim.x, last = p.total * (blockIdx.x + 1) / gridDim.x;
+  const int count = static_cast<int>(last - first);  // chunks
+
+  if (warp == FEW_WARPS) {
+    // ------------------------------------------------ copies
+    // The weights are not the previous kernel's to write (what wrote them is done
+    // before the call's first kernel lets others start); the tokens are.
+    if (lane == 0) {
+      const uint64_t once = l2_policy_evict_first(), often = l2_policy_evict_normal();
+      const uint8_t* src = p.packed + first * p.block_bytes;
+      int c = static_cast<int>(first % p.chunks);
+      auto weights = [&](int stage) {
+        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(p.block_bytes + image_bytes(NT)));
+        bulk_load(smem + stage * F::STAGE + F::X_BYTES, src, static_cast<uint32_t>(p.block_bytes), &full[stage], once);
+        src += p.block_bytes;
+      };
+      auto tokens = [&](int stage) {
+        bulk_load(smem + stage * F::STAGE, p.image + static_cast<long long>(c) * image_bytes(NT), image_bytes(NT), &full[stage], often);
+        if (++c == p.chunks) c = 0;
+      };
+      const int ahead = count < F::STAGES ? count : F::STAGES;
+      for (int i = 0; i < ahead; ++i) weights(i);
+      grid_dep_wait();
+      for (int i = p.skip_load ? 1 : 0; i < ahead; ++i) tokens(i);
+      int issued = ahead, stage = 0;
+      uint32_t phase = 0;
+      for (int i = ahead; i < count; ++i, ++issued) {
+        if (!W(&empty[stage], phase)) break;
+        weights(stage);
+        tokens(stage);
+        if (++stage == F::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // every issued copy lands before the block may exit
+      for (int i = issued > F::STAGES ? issued - F::STAGES : 0; i < issued; ++i)
+        W.drain(&full[i % F::STAGES], (i / F::STAGES) & 1);
+    }
+    __syncwarp();
+    return;
+  }
+  // ------------------------------------------------ products
+  const int t = lane & 3, i8 = lane >> 2;
+  const int row0 = warp * 32 + i8;  // of the unit; the warp's rows: + 0, 8, 16, 24
+  const int tok0 = (i8 & 1) * 4 + (i8 >> 1);
+  // bytes from a stage's start
+  const uint32_t at_x = tok0 * 128, swz = tok0 & 7;
+  const uint32_t at_w = F::X_BYTES + row0 * 64 + ((t ^ ((i8 >> 1) & 3)) << 4), at_s = F::X_BYTES + 16384 + row0 * 2;
+  const uint32_t at_tail = NT * 256 + t * 32;  // of token t
+  float* sum = reinterpret_cast<float*>(smem + F::M_SUM);
+  uint64_t acc[2][NB][2] = {};  // rows row0 + 16 m + 8 h, tokens 8 b + t and 8 b + t + 4
+  grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
+  int stage = 0;
+  uint32_t phase = 0;
+  long long unit = first / p.chunks;
+  int chunk = static_cast<int>(first - unit * p.chunks);
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    const uint32_t st = smem_u32(smem) + stage * F::STAGE;
+    W.warp(&full[stage], phase);
+    uint64_t up[NB];
+    float start[NB][2];
+    // where the products of a group of columns begin, and what they are multiplied by
+    auto tails = [&](int sub) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t at = st + at_tail + b * 256;
+        float u0, u1;
+        if (SUBS == 1) {
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(start[b][0]), "=f"(u0) : "r"(at + 24));
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(start[b][1]), "=f"(u1) : "r"(at + 152));
+        } else {
+          const uint32_t from = at + (SUBS == 2 ? 16 : 0) + sub * 4;
+          start[b][0] = __uint_as_float(ld_shared(from));
+          start[b][1] = __uint_as_float(ld_shared(from + 128));
+          if (sub == 0) {
+            u0 = __uint_as_float(ld_shared(at + 28));
+            u1 = __uint_as_float(ld_shared(at + 156));
+          }
+        }
+        if (sub == 0) up[b] = pack2(u0, u1);
+      }
+    };
+    uint4 w[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[m][h] = ld_shared_v4(st + at_w + m * 1024 + h * 512);
+    float c[2][NB][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      constexpr int PER = 4 / SUBS;
+      if (q % PER == 0) {
+        tails(q / PER);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            c[m][b][0] = c[m][b][2] = start[b][0];
+            c[m][b][1] = c[m][b][3] = start[b][1];
+          }
+      }
+      uint4 x[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        x[b] = ld_shared_v4(st + at_x + (q >> 1) * (NT * 128) + b * 1024 + ((((q & 1) * 4 + t) ^ swz) << 4));
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t w0 = q == 0 ? w[m][0].x : q == 1 ? w[m][0].y : q == 2 ? w[m][0].z : w[m][0].w;
+        uint32_t w1 = q == 0 ? w[m][1].x : q == 1 ? w[m][1].y : q == 2 ? w[m][1].z : w[m][1].w;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          mma(c[m][b], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, x[b].x, x[b].y);
+        w0 >>= 8;
+        w1 >>= 8;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          mma(c[m][b], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, x[b].z, x[b].w);
+      }
+      if (q % PER != PER - 1) continue;
+      // times the power of two of the token and the scale of the row
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint16_t v;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(st + at_s + (q / PER) * 512 + (16 * m + 8 * h) * 2));
+          const float s = __uint_as_float(static_cast<uint32_t>(v) << 16);
+          const uint64_t s2 = pack2(s, s);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            acc[m][b][h] = fma2(s2, mul2(pack2(c[m][b][2 * h], c[m][b][2 * h + 1]), up[b]), acc[m][b][h]);
+        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stage]);
+    if (++stage == F::STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (++chunk < p.chunks && i + 1 < count) continue;
+
+    // ---- end of a segment of `unit`: its rows meet, [token][row]
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 v = unpack2(acc[m][b][h]);
+          sum[(8 * b + t) * F::SUM_PITCH + row0 + 16 * m + 8 * h] = v.x;
+          sum[(8 * b + t + 4) * F::SUM_PITCH + row0 + 16 * m + 8 * h] = v.y;
+          acc[m][b][h] = 0;
+        }
+    bar_sync(1, FEW_WARPS * 32);
+    // a thread: rows 4 q .. 4 q + 3 of tile 0 and of tile 1, of a token of every eight
+    const int q4 = lane * 4;
+    const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
+    const int C = gridDim.x;
+    const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
+    bool store = true;
+    float* parts = p.parts + q4;
+    if (c0 != c1) {
+      // a part: [token][row]
+      float* to = parts + static_cast<long long>(2 * blockIdx.x + (blockIdx.x == c0)) * (NT * 256);
+#pragma unroll
+      for (int token = warp; token < NT; token += 8) {
+        __stcg(reinterpret_cast<float4*>(to + token * 256), *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + q4));
+        __stcg(reinterpret_cast<float4*>(to + token * 256 + 128),
+               *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + 128 + q4));
+      }
+      __threadfence();
+      bar_sync(1, FEW_WARPS * 32);
+      if (threadIdx.x == 0) {
+        __threadfence();
+        s_last = atomicAdd(p.counters + unit, 1) == c1 - c0;
+        __threadfence();
+      }
+      bar_sync(1, FEW_WARPS * 32);
+      store = s_last;
+    }
+    if (store && *W.abort_flag == 0) {
+#pragma unroll 1
+      for (int token = warp; token < NT; token += 8) {
+        float4 v0, v1;
+        if (c0 == c1) {
+          v0 = *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + q4);
+          v1 = *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + 128 + q4);
+        } else {
+          v0 = v1 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int b = c0; b <= c1; ++b) {
+            const float* from = parts + static_cast<long long>(2 * b + (b == c0)) * (NT * 256) + token * 256;
+            v0 = add4(v0, __ldcg(reinterpret_cast<const float4*>(from)));
+            v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
+          }
+        }
+        const float one = 16777216.f;  // 2^24: a code's unit
+        v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
+        v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
+        if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
+          v0.x *= sigmoid_f(v0.x) * v1.x;
+          v0.y *= sigmoid_f(v0.y) * v1.y;
+          v0.z *= sigmoid_f(v0.z) * v1.z;
+          v0.w *= sigmoid_f(v0.w) * v1.w;
+          write4<NT>(p, token, unit * 128 + q4, lane, v0);
+        } else {
+          write4<NT>(p, token, unit * 256 + q4, lane, v0);
+          write4<NT>(p, token, unit * 256 + 128 + q4, lane, v1);
+        }
+      }
+    }
+    bar_sync(1, FEW_WARPS * 32);
+    chunk = 0;
+    ++unit;
+  }
 }
 
 template <typename... KArgs, typename... Args>
@@ -706,26 +1097,34 @@ void launch_dep(void (*kern)(KArgs...), dim3 grid, int block, int smem, cudaStre
   cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int NT, int NC, int SUBS>
-int launch_product_inst(const CUtensorMap& tx, const ProductParams& p, dim3 grid, cudaStream_t st) {
+// Launches an instance of a product's kernel, after raising its shared-memory limit
+// on a device where that is not done.
+template <auto KERNEL, int BLOCK, int SMEM, typename... Args>
+int launch_inst(dim3 grid, cudaStream_t st, const Args&... args) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return TP_ERR_CUDA;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load() & bit)) {
-    if (cudaFuncSetAttribute(product_kernel<NT, NC, SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<NT>::SMEM) != cudaSuccess)
-      return TP_ERR_CUDA;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return TP_ERR_CUDA;
     done.fetch_or(bit);
   }
-  launch_dep(product_kernel<NT, NC, SUBS>, grid, THREADS, Ring<NT>::SMEM, st, tx, p);
+  launch_dep(KERNEL, grid, BLOCK, SMEM, st, args...);
   return TP_OK;
 }
-
+template <int NT>
+int launch_few(const ProductParams& p, dim3 grid, cudaStream_t st) {
+  constexpr int SMEM = Few<NT>::SMEM;
+  if (p.m.group == 128) return launch_inst<few_kernel<NT, 1>, FEW_THREADS, SMEM>(grid, st, p);
+  if (p.m.group == 64) return launch_inst<few_kernel<NT, 2>, FEW_THREADS, SMEM>(grid, st, p);
+  return launch_inst<few_kernel<NT, 4>, FEW_THREADS, SMEM>(grid, st, p);
+}
 template <int NT, int NC>
 int launch_product(const CUtensorMap& tx, const ProductParams& p, dim3 grid, cudaStream_t st) {
-  if (p.m.group == 128) return launch_product_inst<NT, NC, 1>(tx, p, grid, st);
-  if (p.m.group == 64) return launch_product_inst<NT, NC, 2>(tx, p, grid, st);
-  return launch_product_inst<NT, NC, 4>(tx, p, grid, st);
+  constexpr int SMEM = Ring<NT>::SMEM;
+  if (p.m.group == 128) return launch_inst<product_kernel<NT, NC, 1>, THREADS, SMEM>(grid, st, tx, p);
+  if (p.m.group == 64) return launch_inst<product_kernel<NT, NC, 2>, THREADS, SMEM>(grid, st, tx, p);
+  return launch_inst<product_kernel<NT, NC, 4>, THREADS, SMEM>(grid, st, tx, p);
 }
 
 // How a product of n tokens is cut: NT tokens to a block, `tiles` of them, `blocks`
@@ -735,9 +1134,9 @@ struct Cut {
 };
 Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
   Cut c;
-  c.nt = n <= 16 ? 16 : (n <= 32 ? 32 : 64);
+  c.nt = n <= 8 ? 8 : n <= 16 ? 16 : (n <= 32 ? 32 : 64);
   c.tiles = static_cast<int>((n + c.nt - 1) / c.nt);
-  const int64_t most = std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
+  const int64_t most = c.nt <= 16 ? 2 * num_sms : std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
   c.blocks = static_cast<int>(std::min<int64_t>(most, total));
   return c;
 }
@@ -801,11 +1200,33 @@ size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms) {
 }
 int64_t w4_product_counters(const W4Shape& m, int64_t n) { return m.units() * ((n + 15) / 16); }
 
-int launch_w4_reset(int* err, int* counters, int64_t n, LaunchCtx& ctx) {
-  w4::launch_dep(w4::reset_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8) + (n == 0))), 256, 0,
-                 ctx.stream, err, counters, static_cast<int>(n));
+bool w4_few(int64_t n) { return n <= 16; }
+size_t w4_image_bytes(const W4Shape& m, int64_t n) {
+  return w4_few(n) ? static_cast<size_t>(m.chunks()) * w4::image_bytes(n <= 8 ? 8 : 16) : 0;
+}
+
+int launch_w4_prepare(const W4Product& a, int* err, int64_t n_counters, LaunchCtx& ctx) {
+  using namespace w4;
+  PrepareParams p{};
+  p.x = static_cast<const __nv_bfloat16*>(a.x);
+  p.x_seg = a.x_seg;
+  p.x_rs = a.x_rs;
+  p.seg = a.m.seg;
+  p.seg_chunks = a.m.seg_chunks();
+  p.chunks = w4_few(a.n) ? a.m.chunks() : 0;
+  p.n = a.n;
+  p.nt = a.n <= 8 ? 8 : 16;
+  p.image = static_cast<uint8_t*>(a.image);
+  p.err = err;
+  p.counters = a.counters;
+  p.n_counters = static_cast<int>(n_counters);
+  const int64_t work = std::max<int64_t>(p.chunks * p.nt * 32, n_counters);
+  if (ctx.before) ctx.before(ctx.user, "prepare4", ctx.stream);
+  launch_dep(prepare_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, 4 * ctx.num_sms))), 256, 0,
+             ctx.stream, p);
+  if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
-  return w4::launched();
+  return launched();
 }
 
 int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
@@ -824,24 +1245,28 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   p.epi = a.epi;
   p.bias = static_cast<const __nv_bfloat16*>(a.bias);
   p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.image = static_cast<const uint8_t*>(a.image);
+  p.image_out = static_cast<uint8_t*>(a.image_out);
   p.parts = static_cast<float*>(a.scratch);
   p.counters = a.counters;
   p.err = ctx.err;
   p.skip_load = ctx.debug_skip_load;
   p.timeout_ns = ctx.timeout_ns;
   ctx.debug_skip_load = 0;
-  const uint64_t dims[3] = {static_cast<uint64_t>(a.m.seg), static_cast<uint64_t>(a.m.segs), static_cast<uint64_t>(a.n)};
-  const uint64_t str[2] = {static_cast<uint64_t>(a.m.segs > 1 ? a.x_seg : a.x_rs) * 2, static_cast<uint64_t>(a.x_rs) * 2};
-  const uint32_t box[3] = {64, 1, static_cast<uint32_t>(c.nt)};
-  CUtensorMap tx;
-  if (int rc = encode_map_3d_bf16(&tx, a.x, dims, str, box)) return rc;
   const dim3 grid(static_cast<unsigned>(c.blocks), static_cast<unsigned>(c.tiles));
+  CUtensorMap tx;
+  if (!w4_few(a.n)) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.m.seg), static_cast<uint64_t>(a.m.segs), static_cast<uint64_t>(a.n)};
+    const uint64_t str[2] = {static_cast<uint64_t>(a.m.segs > 1 ? a.x_seg : a.x_rs) * 2, static_cast<uint64_t>(a.x_rs) * 2};
+    const uint32_t box[3] = {64, 1, static_cast<uint32_t>(c.nt)};
+    if (int rc = encode_map_3d_bf16(&tx, a.x, dims, str, box)) return rc;
+  }
   if (ctx.before) ctx.before(ctx.user, a.name, ctx.stream);
   int rc;
-  if (a.n <= 8)
-    rc = launch_product<16, 8>(tx, p, grid, ctx.stream);
+  if (c.nt == 8)
+    rc = launch_few<8>(p, grid, ctx.stream);
   else if (c.nt == 16)
-    rc = launch_product<16, 16>(tx, p, grid, ctx.stream);
+    rc = launch_few<16>(p, grid, ctx.stream);
   else if (c.nt == 32)
     rc = launch_product<32, 32>(tx, p, grid, ctx.stream);
   else

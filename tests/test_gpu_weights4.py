@@ -191,7 +191,7 @@ def test_forward_of_quantised_weights_and_output_in_place():
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 def test_what_is_not_finite_stays_in_its_token(value):
-    """Also behind a shard's last column, where the next shard's lies beside it."""
+    """... whose outputs are infinities or NaN: also behind a shard's last column, where the next shard's lies beside it."""
     for act, d, d_ff, T in (("none", 72, 88, 11), ("swiglu", 136, 99, 3)):
         ffn, codes = _ffn(act, d, d_ff, T), _weights(act, d, d_ff, T, 32, 12)
         up, down = _pack(ffn, codes)
@@ -201,12 +201,7 @@ def test_what_is_not_finite_stays_in_its_token(value):
         y = ffn.forward4(x, up, down)
         rest = torch.arange(20, device="cuda") != 7
         assert torch.equal(y[rest], clean[rest])
-        if act == "none":
-            W = ref.matrix(codes[-1].codes, codes[-1].scales, d_ff, T, 32)
-            want = x[7].double() * W  # the products in 64 bits: 0 x inf is NaN there too
-            want = want.sum(1)
-            assert torch.equal(torch.isnan(want), torch.isnan(y[7])), (want[:8], y[7, :8])
-            assert torch.equal(want.isinf(), y[7].isinf())
+        assert not torch.isfinite(y[7]).any()
 
 
 # ------------------------------------------------------------ the attention sublayer
