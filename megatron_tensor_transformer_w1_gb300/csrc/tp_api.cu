@@ -1579,8 +1579,7 @@ W4Shape w4_qkv(const tp_attn_plan* a, int group) {
 }
 
 // Workspace of a forward pass: error word, the products' counters and parts (of
-// one product at a time), the tokens' blocks and the hidden activations (blocks, or
-// bf16 rows).
+// one product at a time), the blocks of the tokens and of the hidden activations.
 struct Ws4 {
   size_t counters = 0, parts = 0, x = 0, h = 0, total = 0;
   int64_t n_up = 0, n_down = 0;  // counters
@@ -1604,7 +1603,7 @@ Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
   off += align_up(w4_image_bytes(p->act != TP_ACT_NONE ? up : down, n));
   L.h = off;
   if (p->act != TP_ACT_NONE)
-    off += align_up(w4_few(n) ? w4_image_bytes(down, n) : static_cast<size_t>(n) * p->T_p * w4_sp(p) * 2);
+    off += align_up(w4_image_bytes(down, n));
   L.total = off;
   return L;
 }
@@ -1653,15 +1652,10 @@ int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n, const void* x, const v
   g.x_rs = p->d;
   g.epi = p->act == TP_ACT_SWIGLU ? W4_SWIGLU : W4_GELU;
   g.bias = b1;
-  g.out = ws + L.h;
-  g.out_rs = p->T_p * w4_sp(p);
   g.image_out = ws + L.h;
   int rc = launch_w4_prepare(g, ctx.err, L.n_up + L.n_down, ctx);
   if (!rc) rc = launch_w4_product(g, ctx);
   if (rc) return rc;
-  down.x = ws + L.h;
-  down.x_seg = w4_sp(p);
-  down.x_rs = g.out_rs;
   down.image = ws + L.h;
   down.counters += L.n_up;
   return launch_w4_product(down, ctx);
@@ -1982,7 +1976,7 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
     g.out = y;
     g.out_rs = a->d;
     g.counters += L.n_qkv;
-    if (w4_few(n)) rc = launch_w4_prepare(g, nullptr, 0, ctx);
+    rc = launch_w4_prepare(g, nullptr, 0, ctx);
     if (!rc) rc = launch_w4_product(g, ctx);
   }
   return kv_finish(a, ctx, rc, flags, workspace);

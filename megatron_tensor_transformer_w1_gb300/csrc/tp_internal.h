@@ -316,7 +316,7 @@ struct W4Codes {
 int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack, cudaStream_t st);
 
 enum W4Epi : int { W4_OUT = 0, W4_GELU = 1, W4_SWIGLU = 2 };
-// out[token][row] = epilogue(sum over the columns of x[token][column] * W[row][column] + bias[row])
+// epilogue(sum over the columns of x[token][column] * W[row][column] + bias[row])
 struct W4Product {
   const char* name = "w4_product";
   W4Shape m;
@@ -326,20 +326,19 @@ struct W4Product {
   int64_t x_seg = 0, x_rs = 0;
   int epi = W4_OUT;
   const void* bias = nullptr;    // W4_OUT: by row; W4_GELU: by hidden unit
-  void* out = nullptr;           // bf16; W4_GELU and W4_SWIGLU: by hidden slot
+  void* out = nullptr;           // bf16 (W4_OUT)
   int64_t out_rs = 0;
-  // Up to 16 tokens (w4_few): x is read as blocks, which launch_w4_prepare makes of
-  // it or an up product has left in its image_out, and so are the hidden activations.
+  // x is read as blocks, which launch_w4_prepare makes of it or an up product has
+  // left in its image_out.
   void *image = nullptr, *image_out = nullptr;  // w4_image_bytes
   void* scratch = nullptr;       // w4_product_scratch bytes
   int* counters = nullptr;       // w4_product_counters words, 0 before the launch
 };
 size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms);
 int64_t w4_product_counters(const W4Shape& m, int64_t n);
-bool w4_few(int64_t n);
 size_t w4_image_bytes(const W4Shape& m, int64_t n);  // of the tokens that m multiplies
-// The kernel before a call's first product (err: the error word, else null): the
-// image of p.x if there is to be one; clears the error word and n_counters counters.
+// The image of p.x.  Before a call's first product it also clears the error word
+// (else null) and n_counters counters.
 int launch_w4_prepare(const W4Product& p, int* err, int64_t n_counters, LaunchCtx& ctx);
 int launch_w4_product(const W4Product& p, LaunchCtx& ctx);
 

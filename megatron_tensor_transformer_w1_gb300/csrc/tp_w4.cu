@@ -230,54 +230,108 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
 
 // ================================================================ products
 // y[token][row] = sum_g s[row][g] sum_{k in g} (code - 8) x[token][k], for up to
-// 64 tokens at a time.
+// 64 tokens at a time.  Bound by the one read of the codes.
 //
-// Bound by the one read of the codes for few tokens.  The weights are the matrix
-// unit's A operand, 128 rows at a time, the tokens its N: code - 8 is a bf16
-// number without rounding, and the product of a group is scaled in 32 bits when
-// it is read back, so a result is as exact as the sums in 32 bits.  (A scaled
-// weight would have to be rounded to bf16.)
+// What is left to count are the instructions that make operands of codes.  A code
+// in the low bits of an fp16 number is code * 2^-24, a subnormal, and four bits
+// higher code * 2^-20: a word's eight codes are four operand registers after one
+// shift and four masks, without an addition or a conversion.  For that
+//  * the tokens are fp16 too: a block of 128 columns of a token times a power of
+//    two that brings its largest element to 2^14..2^15 (bf16's eight bits are kept
+//    down to 2^-25 of it, what is smaller is rounded to 2^-40 of it), and columns 2, 3,
+//    6, 7 of each eight times 2^-4, for their codes' place;
+//  * the codes' offset of 8 is taken off as the block's sum, -8 times the sum of the
+//    group's 32, 64 or 128 columns.
+// A group's product is scaled in 32 bits, so a result is as exact as the sums in 32
+// bits.  (A scaled weight would have to be rounded.)  A token with an infinity or a
+// NaN gets NaN throughout.
+// (With codes made into bf16, 11 instructions a word, the 70B feed-forward took
+// 102 us for one token.)
 //
 // A block takes a run of chunks (128 columns of a unit's 256 rows) of the list of
 // all units' chunks, the same number as the others, whatever units they belong to;
-// a run of chunks of one unit is a segment.  One block has
-//  * warp 16: copies of the chunks into a ring: the packed block (codes, scales) in
-//    one piece, as it lies, the tokens' 128 columns by two TMA boxes;
-//  * warps 0-15, in four groups of 128 threads, a row to a thread: tile 0 and 1 of
-//    the unit, the even and the odd steps (a step: a group's columns).  A thread
-//    turns its row's codes into bf16 and writes them to tensor memory, where the
-//    matrix unit takes them from (shared memory would be written and read once
-//    more), then reads the step's product back, scales and adds it.  Four groups,
-//    so that one's products run while others turn codes;
-//  * warp 17: issues tcgen05.mma.
-// At a segment's end the groups' sums meet in tensor memory (all four have row r in
-// lane r).  A unit that several blocks share is joined by the last of them to
-// come, in the order of the columns.
-//
-// Every wait is bounded (abort flag and error word); after an abort the warps run
-// on without waiting, so that they meet at the block's barriers.
+// a run of chunks of one unit is a segment.  A unit that several blocks share is
+// joined by the last of them to come, in the order of the columns.
 using namespace tc;
 
-constexpr int GROUPS_OF_WARPS = 4, WORK_WARPS = 16, THREADS = (WORK_WARPS + 2) * 32;
-constexpr int T_COLS = 64;  // columns of tensor memory for a group's weights, and for its products
+// A block of tokens as the kernels keep it ("image"), for NT tokens: [2][NT][128
+// bytes], 64 columns each, 16-byte pieces swizzled by the token (piece i at i ^
+// (token & 7)); then float [8][NT]: -8 * 2^-24 times the sums of its four 32-column
+// parts, its two halves and the whole, and the power of two that undoes the block's.
+__host__ __device__ constexpr int image_bytes(int nt) { return nt * 288; }
+constexpr int SUM_OF = 0, SUM_OF_HALF = 4, SUM_OF_ALL = 6, UP = 7;
 
 struct ProductParams {
   W4Shape m;
   const uint8_t* packed;
   long long total;  // chunks of all units
-  int chunks, seg_chunks, block_bytes, units;
+  int chunks, block_bytes, units;
   long long n, out_rs;
   int epi;
   const __nv_bfloat16* bias;
   __nv_bfloat16* out;
-  const uint8_t* image;  // few tokens: the tokens' blocks, and the hidden activations'
-  uint8_t* image_out;
-  float* parts;   // [blocks][2][2 tiles][NT][128]; few tokens: [blocks][2][NT][256]
+  const uint8_t* image;  // [token tiles][chunks]
+  uint8_t* image_out;    // the hidden activations', likewise
+  int out_chunks;
+  float* parts;   // [token tiles][blocks][2][NT][256]
   int* counters;  // [token tiles][units]
   int* err;
   int skip_load;
   unsigned long long timeout_ns;
 };
+
+// Columns 4 lane .. 4 lane + 3 of a token's block, by a warp, into an image.
+__device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, int lane, const float (&v)[4]) {
+  const float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+  // (infinities count as the largest numbers, NaN is left out: either spoils the block's sum)
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
+  const int e = min(141 - static_cast<int>(min(most >> 23, 254u)), 126);  // most * 2^e in 2^14..2^15
+  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
+  const float2 a = __half22float2(lo), b = __half22float2(hi);
+  float sum = (a.x + a.y) + 16.f * (b.x + b.y);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  sum *= -4.76837158203125e-7f;  // -8 * 2^-24
+  const float two = sum + __shfl_xor_sync(0xffffffffu, sum, 8), all = two + __shfl_xor_sync(0xffffffffu, two, 16);
+  uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
+  *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  float* tail = reinterpret_cast<float*>(image + nt * 256) + token;
+  if ((lane & 7) == 0) tail[(SUM_OF + (lane >> 3)) * nt] = sum;
+  if ((lane & 15) == 0) tail[(SUM_OF_HALF + (lane >> 4)) * nt] = two;
+  if (lane == 0) tail[SUM_OF_ALL * nt] = all;
+  if (lane == 0) tail[UP * nt] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
+struct PrepareParams {
+  const __nv_bfloat16* x;
+  long long x_seg, x_rs, seg, seg_chunks, chunks, n;
+  int nt, tiles;
+  uint8_t* image;  // [tiles][chunks]
+  int *err, *counters, n_counters;
+};
+// The kernel before a call's first product: the tokens' blocks, a warp to a token's;
+// clears what the call counts in.  It lets others start when everything before it
+// on the stream is done: the products behind it read their weights without a further wait.
+__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < p.n_counters; i += gridDim.x * 256) p.counters[i] = 0;
+  for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < p.tiles * p.chunks * p.nt; i += gridDim.x * 8ll) {
+    const long long block = i / p.nt, tile = block / p.chunks, chunk = block - tile * p.chunks;
+    const long long e = chunk / p.seg_chunks, col = (chunk - e * p.seg_chunks) * 128 + lane * 4;
+    const int in = static_cast<int>(i - block * p.nt);
+    const long long token = tile * p.nt + in;
+    float v[4] = {};
+    if (token < p.n && col < p.seg) {  // segments end at multiples of 8
+      const uint2 w = *reinterpret_cast<const uint2*>(p.x + token * p.x_rs + e * p.x_seg + col);
+      v[0] = bf16_at(w.x, 0), v[1] = bf16_at(w.x, 1), v[2] = bf16_at(w.y, 0), v[3] = bf16_at(w.y, 1);
+    }
+    store_block(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
+  }
+}
 
 // Bounded wait on an mbarrier phase, as tc::Waiter's, for waits that mostly last
 // some hundred cycles: the clock, which takes longer than that to read, is looked
@@ -316,15 +370,6 @@ struct Wait {
   }
 };
 
-// NT: tokens of a product (N); NC: those that are read back.
-template <int NT>
-struct Ring {
-  static constexpr int X_BYTES = NT * 256, CODES = 18432, STAGE = X_BYTES + CODES;
-  static constexpr int STAGES = NT <= 16 ? 8 : (NT <= 32 ? 7 : 6);
-  static constexpr int SMEM = STAGES * STAGE + 1024;
-  static_assert(SMEM <= 232448 - 1024, "shared memory per block");
-};
-
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
@@ -342,6 +387,367 @@ __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ float ld_shared_f(uint32_t addr) { return __uint_as_float(ld_shared(addr)); }
+__device__ __forceinline__ float ld_shared_scale(uint32_t addr) {  // a bf16
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// The codes at bits 0-3 and 16-19 as two fp16 numbers, and those at bits 4-7 and 20-23.
+__device__ __forceinline__ uint32_t low(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t high(uint32_t w) { return w & 0x00f000f0u; }
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+// The run of chunks of a block.
+struct Run {
+  long long first;
+  int count;
+  __device__ __forceinline__ explicit Run(const ProductParams& p) {
+    first = p.total * blockIdx.x / gridDim.x;
+    count = static_cast<int>(p.total * (blockIdx.x + 1) / gridDim.x - first);
+  }
+};
+
+// The copying thread: chunks of weights (the packed block as it lies) and of tokens
+// (the image) into a ring of stages, tokens first.
+template <typename R>
+__device__ __forceinline__ void copy_chunks(const ProductParams& p, const Run& run, uint8_t* ring, uint64_t* full,
+                                            uint64_t* empty, const Wait& W) {
+  // A single token tile reads the weights once.
+  const uint64_t often = l2_policy_evict_normal(), once = gridDim.y == 1 ? l2_policy_evict_first() : often;
+  const uint8_t* src = p.packed + run.first * p.block_bytes;
+  const uint8_t* image = p.image + static_cast<long long>(blockIdx.y) * p.chunks * image_bytes(R::NT);
+  int c = static_cast<int>(run.first % p.chunks);
+  auto weights = [&](int stage) {
+    mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(p.block_bytes + image_bytes(R::NT)));
+    bulk_load(ring + stage * R::STAGE + R::X_BYTES, src, static_cast<uint32_t>(p.block_bytes), &full[stage], once);
+    src += p.block_bytes;
+  };
+  auto tokens = [&](int stage) {
+    bulk_load(ring + stage * R::STAGE, image + static_cast<long long>(c) * image_bytes(R::NT), image_bytes(R::NT),
+              &full[stage], often);
+    if (++c == p.chunks) c = 0;
+  };
+  // The weights are not the previous kernel's to write (what wrote them is done
+  // before the call's first kernel lets others start); the tokens are.
+  const int ahead = run.count < R::STAGES ? run.count : R::STAGES;
+  for (int i = 0; i < ahead; ++i) weights(i);
+  grid_dep_wait();
+  for (int i = p.skip_load ? 1 : 0; i < ahead; ++i) tokens(i);
+  int issued = ahead, stage = 0;
+  uint32_t phase = 0;
+  for (int i = ahead; i < run.count; ++i, ++issued) {
+    if (!W(&empty[stage], phase)) break;
+    weights(stage);
+    tokens(stage);
+    if (++stage == R::STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  // every issued copy lands before the block may exit
+  for (int i = issued > R::STAGES ? issued - R::STAGES : 0; i < issued; ++i) W.drain(&full[i % R::STAGES], (i / R::STAGES) & 1);
+}
+
+// Four neighbouring rows of a token, by a warp that has 128: bias or activation, and out.
+template <int NT>
+__device__ __forceinline__ void write4(const ProductParams& p, int in_tile, long long row, int lane, float4 v) {
+  float a[4] = {v.x, v.y, v.z, v.w};
+  if (p.epi == W4_OUT) {
+    const long long token = static_cast<long long>(blockIdx.y) * NT + in_tile;
+    if (token >= p.n || row >= p.m.rows) return;  // rows are a multiple of 8
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] += __bfloat162float(p.bias[row + i]);
+    }
+    *reinterpret_cast<uint2*>(p.out + token * p.out_rs + row) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    return;
+  }
+  const int chunk = static_cast<int>(row >> 7);
+  if (chunk >= p.out_chunks) return;
+  if (p.epi == W4_GELU) {
+    const long long t = row / p.m.sp, in = row - t * p.m.sp;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = gelu_tanh_f(a[i] + (p.bias && in + i < p.m.s ? __bfloat162float(p.bias[t * p.m.s + in + i]) : 0.f));
+  }
+  store_block(p.image_out + (static_cast<long long>(blockIdx.y) * p.out_chunks + chunk) * image_bytes(NT), NT, in_tile, lane, a);
+}
+
+// The end of a segment of `unit`, whose sums lie in shared memory, [token][row], 256
+// rows and a few of padding: out if the segment is the whole unit, else as a part,
+// and the last block of the unit joins the parts.  By WARPS warps, which then may
+// write the sums anew.
+constexpr int SUM_PITCH = 256 + 8;
+template <int NT, int WARPS>
+__device__ __forceinline__ void finish_segment(const ProductParams& p, long long unit, const float* sum, int* s_last,
+                                               const Wait& W) {
+  // a thread: rows 4 q .. 4 q + 3 of tile 0 and of tile 1, of a token of every WARPS
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = lane * 4;
+  const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
+  const int C = gridDim.x;
+  const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
+  bool store = true;
+  float* parts = p.parts + static_cast<long long>(blockIdx.y) * C * 2 * (NT * 256) + q4;
+  auto slot = [&](int b) { return static_cast<long long>(2 * b + (b == c0)) * (NT * 256); };
+  if (c0 != c1) {
+    float* to = parts + slot(blockIdx.x);
+#pragma unroll
+    for (int token = warp; token < NT; token += WARPS) {
+      __stcg(reinterpret_cast<float4*>(to + token * 256), *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + q4));
+      __stcg(reinterpret_cast<float4*>(to + token * 256 + 128), *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + 128 + q4));
+    }
+    __threadfence();
+    bar_sync(1, WARPS * 32);
+    if (threadIdx.x == 0) {
+      __threadfence();
+      *s_last = atomicAdd(p.counters + static_cast<long long>(blockIdx.y) * p.units + unit, 1) == c1 - c0;
+      __threadfence();
+    }
+    bar_sync(1, WARPS * 32);
+    store = *s_last;
+  }
+  if (store && *W.abort_flag == 0) {
+#pragma unroll 1
+    for (int token = warp; token < NT; token += WARPS) {
+      float4 v0, v1;
+      if (c0 == c1) {
+        v0 = *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + q4);
+        v1 = *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + 128 + q4);
+      } else {
+        v0 = v1 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int b = c0; b <= c1; ++b) {
+          const float* from = parts + slot(b) + token * 256;
+          v0 = add4(v0, __ldcg(reinterpret_cast<const float4*>(from)));
+          v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
+        }
+      }
+      const float one = 16777216.f;  // 2^24: a code's unit
+      v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
+      v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
+      if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
+        v0.x *= sigmoid_f(v0.x) * v1.x;
+        v0.y *= sigmoid_f(v0.y) * v1.y;
+        v0.z *= sigmoid_f(v0.z) * v1.z;
+        v0.w *= sigmoid_f(v0.w) * v1.w;
+        write4<NT>(p, token, unit * 128 + q4, lane, v0);
+      } else {
+        write4<NT>(p, token, unit * 256 + q4, lane, v0);
+        write4<NT>(p, token, unit * 256 + 128 + q4, lane, v1);
+      }
+    }
+  }
+  bar_sync(1, WARPS * 32);
+}
+
+// ---------------------------------------------------------------- few tokens
+// Up to 16 tokens: m16n8k16 matrix instructions on registers.  They take 2.05 cycles
+// an SM (measured), 8 tokens of a chunk 262 of the some 720 that its bytes take, 16
+// tokens 525; the tensor-memory products take 768 whatever the number of tokens,
+// besides the way of the weights into tensor memory.
+//
+// The order of a product's columns is free as long as both operands have it: lane
+// t of a row's four takes the 32-bit words of codes 8 t .. 8 t + 7 of 32 columns, their
+// pairs as the halves of two k16 steps, and so reads the same 8 columns of a token
+// in one piece.  Token t of eight stands in column 2 t, token t + 4 in column 2 t +
+// 1 of the product, so that the two tokens of an eighth of a warp lie in different
+// halves of the swizzled rows.
+// 8 warps, 32 rows of the unit each, two blocks per SM.
+template <int NT_>
+struct Few {
+  static constexpr int NT = NT_, X_BYTES = image_bytes(NT), STAGE = X_BYTES + 18432;
+  static constexpr int STAGES = NT == 8 ? 5 : 4;
+  static constexpr int M_SUM = STAGES * STAGE, SMEM = M_SUM + NT * SUM_PITCH * 4 + 128;
+  static_assert(2 * (SMEM + 2048) <= 233472, "two blocks per SM");
+};
+constexpr int FEW_WARPS = 8, FEW_THREADS = (FEW_WARPS + 1) * 32;
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// SUBS: groups of a chunk.
+template <int NT, int SUBS>
+__global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_constant__ ProductParams p) {
+  using F = Few<NT>;
+  constexpr int NB = NT / 8;  // products of eight tokens
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  __shared__ uint64_t full[F::STAGES], empty[F::STAGES];
+  __shared__ int s_abort, s_last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], FEW_WARPS);
+    }
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  grid_dep_launch();
+  const Wait W{&s_abort, p.err, p.timeout_ns};
+  const Run run(p);
+  if (warp == FEW_WARPS) {
+    if (lane == 0) copy_chunks<F>(p, run, smem, full, empty, W);
+    return;
+  }
+  const int t = lane & 3, i8 = lane >> 2;
+  const int row0 = warp * 32 + i8;  // of the unit; the warp's rows: + 0, 8, 16, 24
+  const int tok0 = (i8 & 1) * 4 + (i8 >> 1);
+  // bytes from a stage's start
+  const uint32_t at_x = tok0 * 128, swz = tok0 & 7;
+  const uint32_t at_w = F::X_BYTES + row0 * 64 + ((t ^ ((i8 >> 1) & 3)) << 4), at_s = F::X_BYTES + 16384 + row0 * 2;
+  const uint32_t at_tail = NT * 256 + t * 4;  // of token t
+  float* sum = reinterpret_cast<float*>(smem + F::M_SUM);
+  uint64_t acc[2][NB][2] = {};  // rows row0 + 16 m + 8 h, tokens 8 b + t and 8 b + t + 4
+  grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
+  int stage = 0;
+  uint32_t phase = 0;
+  long long unit = run.first / p.chunks;
+  int chunk = static_cast<int>(run.first - unit * p.chunks);
+#pragma unroll 1
+  for (int i = 0; i < run.count; ++i) {
+    const uint32_t st = smem_u32(smem) + stage * F::STAGE;
+    W.warp(&full[stage], phase);
+    uint4 w[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[m][h] = ld_shared_v4(st + at_w + m * 1024 + h * 512);
+    uint64_t up[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t at = st + at_tail + UP * NT * 4 + b * 32;
+      up[b] = pack2(ld_shared_f(at), ld_shared_f(at + 16));
+    }
+    float c[2][NB][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      constexpr int PER = 4 / SUBS;
+      if (q % PER == 0) {
+        constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t at = st + at_tail + (FIRST + q / PER) * NT * 4 + b * 32;
+          const float c0 = ld_shared_f(at), c1 = ld_shared_f(at + 16);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            c[m][b][0] = c[m][b][2] = c0;
+            c[m][b][1] = c[m][b][3] = c1;
+          }
+        }
+      }
+      uint4 x[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        x[b] = ld_shared_v4(st + at_x + (q >> 1) * (NT * 128) + b * 1024 + ((((q & 1) * 4 + t) ^ swz) << 4));
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t w0 = q == 0 ? w[m][0].x : q == 1 ? w[m][0].y : q == 2 ? w[m][0].z : w[m][0].w;
+        uint32_t w1 = q == 0 ? w[m][1].x : q == 1 ? w[m][1].y : q == 2 ? w[m][1].z : w[m][1].w;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) mma(c[m][b], low(w0), low(w1), high(w0), high(w1), x[b].x, x[b].y);
+        w0 >>= 8;
+        w1 >>= 8;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) mma(c[m][b], low(w0), low(w1), high(w0), high(w1), x[b].z, x[b].w);
+      }
+      if (q % PER != PER - 1) continue;
+      // times the power of two of the token and the scale of the row
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float s = ld_shared_scale(st + at_s + (q / PER) * 512 + (16 * m + 8 * h) * 2);
+          const uint64_t s2 = pack2(s, s);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            acc[m][b][h] = fma2(s2, mul2(pack2(c[m][b][2 * h], c[m][b][2 * h + 1]), up[b]), acc[m][b][h]);
+        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stage]);
+    if (++stage == F::STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (++chunk < p.chunks && i + 1 < run.count) continue;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 v = unpack2(acc[m][b][h]);
+          sum[(8 * b + t) * SUM_PITCH + row0 + 16 * m + 8 * h] = v.x;
+          sum[(8 * b + t + 4) * SUM_PITCH + row0 + 16 * m + 8 * h] = v.y;
+          acc[m][b][h] = 0;
+        }
+    bar_sync(1, FEW_WARPS * 32);
+    finish_segment<NT, FEW_WARPS>(p, unit, sum, &s_last, W);
+    chunk = 0;
+    ++unit;
+  }
+}
+
+// ---------------------------------------------------------------- more tokens
+// 17 to 64 tokens: the weights are the A operand of tcgen05.mma, 128 rows at a time, in
+// tensor memory (in shared memory they would be written and read once more), the
+// tokens its N.  One block per SM:
+//  * warps 0-15, in four groups of 128 threads, a row to a thread: tile 0 and 1 of
+//    the unit, the even and the odd steps (a step: a group's columns).  A thread
+//    writes its row's codes to tensor memory as operands, then reads the step's
+//    product back, scales and adds it.  Four groups, so that one's products run
+//    while others make operands;
+//  * warp 16 copies, warp 17 issues the products.
+// Every wait is bounded (abort flag and error word); after an abort the warps run
+// on without waiting, so that they meet at the block's barriers.
+constexpr int GROUPS_OF_WARPS = 4, WORK_WARPS = 16, THREADS = (WORK_WARPS + 2) * 32;
+constexpr int T_COLS = 64;  // columns of tensor memory for a group's weights, and for its products
+
+template <int NT_>
+struct Ring {
+  static constexpr int NT = NT_, X_BYTES = (image_bytes(NT) + 1023) / 1024 * 1024, STAGE = X_BYTES + 18432;
+  static constexpr int STAGES = NT == 32 ? 6 : 4;
+  static constexpr int M_SUM = STAGES * STAGE, SMEM = M_SUM + NT * SUM_PITCH * 4 + 1024;
+  static_assert(SMEM <= 232448 - 1024, "shared memory per block");
+};
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -351,34 +757,17 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(one));
   return one != 0;
 }
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-// Two codes (bits 0-3 of each half) as bf16: 128 + code by its bits, less 136.
-__device__ __forceinline__ uint32_t two_weights(uint32_t w) {
-  uint32_t d, r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(d) : "r"(w));  // (w & mask) | bits
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x43084308u));
-  return r;
-}
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[N]) {
-  if constexpr (N == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(at));
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at));
-  }
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
   tmem_wait_ld();
   // names the registers, so that no use of them moves before the wait
 #pragma unroll
-  for (int i = 0; i < N; i += 8)
+  for (int i = 0; i < 16; i += 8)
     asm volatile(""
                  : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                    "+r"(r[i + 6]), "+r"(r[i + 7]));
@@ -387,18 +776,11 @@ __device__ __forceinline__ void tmem_store4(uint32_t at, uint32_t a, uint32_t b,
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
-__device__ __forceinline__ void tmem_store8(uint32_t at, const float* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "f"(v[0]), "f"(v[1]),
-               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
 
-// SUBS: groups of a chunk.
-template <int NT, int NC, int SUBS>
-__global__ void __launch_bounds__(THREADS, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ ProductParams p) {
+template <int NT, int SUBS>
+__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   using R = Ring<NT>;
-  constexpr int LD = 16;  // columns read back at a time
+  constexpr int KSTEPS = 8 / SUBS;  // K = 16 steps of a group
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[R::STAGES], empty[R::STAGES], a_full[GROUPS_OF_WARPS], d_full[GROUPS_OF_WARPS], drain;
@@ -419,70 +801,30 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == WORK_WARPS && lane == 0) prefetch_tmap(&tx);
   if (warp == WORK_WARPS + 1) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();
   const uint32_t tmem = tmem_slot;  // group g's weights at T_COLS g, its products at 256 + T_COLS g
   const Wait W{&s_abort, p.err, p.timeout_ns};
-  const long long first = p.total * blockIdx.x / gridDim.x, last = p.total * (blockIdx.x + 1) / gridDim.x;
-  const int count = static_cast<int>(last - first);  // chunks
-  constexpr int KSTEPS = 8 / SUBS;  // K = 16 steps of a group
-  const long long n0 = static_cast<long long>(blockIdx.y) * NT;
+  const Run run(p);
 
   if (warp == WORK_WARPS) {
-    // ------------------------------------------------ copies
-    // The weights are not the previous kernel's to write (what wrote them is done
-    // before the call's first kernel lets others start); the tokens may be.
-    if (lane == 0) {
-      const uint64_t policy = gridDim.y == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-      const uint8_t* src = p.packed + first * p.block_bytes;
-      auto weights = [&](int i) {
-        uint8_t* st = smem + (i % R::STAGES) * R::STAGE;
-        mbar_arrive_expect_tx(&full[i % R::STAGES], static_cast<uint32_t>(p.block_bytes + R::X_BYTES));
-        if (!(p.skip_load && i == 0)) bulk_load(st + R::X_BYTES, src + static_cast<long long>(i) * p.block_bytes,
-                                                static_cast<uint32_t>(p.block_bytes), &full[i % R::STAGES], policy);
-      };
-      int c = static_cast<int>(first % p.chunks), e = c / p.seg_chunks, in = c - e * p.seg_chunks;
-      auto tokens = [&](int i) {
-        uint8_t* st = smem + (i % R::STAGES) * R::STAGE;
-        uint64_t* bar = &full[i % R::STAGES];
-        tma_load_3d(st, &tx, bar, in * 128, e, static_cast<int>(n0));
-        tma_load_3d(st + NT * 128, &tx, bar, in * 128 + 64, e, static_cast<int>(n0));
-        if (++in == p.seg_chunks) {
-          in = 0;
-          if (++e * p.seg_chunks == p.chunks) e = 0;
-        }
-      };
-      const int ahead = count < R::STAGES ? count : R::STAGES;
-      for (int i = 0; i < ahead; ++i) weights(i);
-      grid_dep_wait();
-      for (int i = 0; i < ahead; ++i) tokens(i);
-      int issued = ahead;
-      for (int i = ahead; i < count; ++i) {
-        if (!W(&empty[i % R::STAGES], ((i / R::STAGES) & 1) ^ 1)) break;
-        weights(i);
-        tokens(i);
-        ++issued;
-      }
-      // every issued copy lands before the block may exit
-      for (int i = issued > R::STAGES ? issued - R::STAGES : 0; i < issued; ++i)
-        W.drain(&full[i % R::STAGES], (i / R::STAGES) & 1);
-    }
+    if (lane == 0) copy_chunks<R>(p, run, smem, full, empty, W);
     __syncwarp();
   } else if (warp == WORK_WARPS + 1) {
     // ------------------------------------------------ products
     // A product takes 48 cycles, whatever N up to 64 is (measured; M 128, K 16, from
     // tensor or shared memory): few instructions may lie between two.
     const bool leader = elect_one();
-    constexpr uint32_t ID = idesc(NT, 0, 0);
+    constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) | (8u << 24);  // fp16 x fp16 -> fp32, M = 128
     const uint64_t x_desc = kdesc(smem_u32(smem), NT, 0);
     bool ok = true;
     int stage = 0;
     uint32_t phase = 0, step = 0;
 #pragma unroll 1
-    for (int i = 0; i < count && ok; ++i) {
+    for (int i = 0; i < run.count && ok; ++i) {
       ok = W.warp(&full[stage], phase);
       const uint64_t xd = x_desc + static_cast<uint64_t>(stage * (R::STAGE >> 4));
 #pragma unroll
@@ -516,32 +858,34 @@ __global__ void __launch_bounds__(THREADS, 1)
     W.drain(&drain, 0);
     __syncwarp();
   } else {
-    // ------------------------------------------------ weights to bf16, products back, sums
+    // ------------------------------------------------ operands, products back, sums
     const int g = warp >> 2, tile = g >> 1, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t at_a = tmem + lane_base + g * T_COLS, at_d = tmem + lane_base + 256 + g * T_COLS;
+    const uint32_t at_w = R::X_BYTES + tile * 8192 + r * 64, swz = (r >> 1) & 3;
+    const uint32_t at_s = R::X_BYTES + 16384 + (tile * 128 + r) * 2;
+    float* sum = reinterpret_cast<float*>(smem + R::M_SUM) + tile * 128 + r;
     constexpr int PIECES = 4 / SUBS;
     grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
-    float acc[NC];
+    uint64_t acc[NT / 2];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+    for (int c = 0; c < NT / 2; ++c) acc[c] = 0;
     uint32_t mine = 0;  // steps of this group so far
     int stage = 0;
     uint32_t phase = 0;
-    long long unit = first / p.chunks;
-    int chunk = static_cast<int>(first - unit * p.chunks);
+    long long unit = run.first / p.chunks;
+    int chunk = static_cast<int>(run.first - unit * p.chunks);
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < run.count; ++i) {
       if (SUBS > 1 || (i & 1) == (g & 1)) {
-        const uint8_t* st = smem + stage * R::STAGE + R::X_BYTES;
-        const uint32_t codes = smem_u32(st) + tile * 8192 + r * 64;
+        const uint32_t st = smem_u32(smem) + stage * R::STAGE;
         W.warp(&full[stage], phase);
 #pragma unroll 1
         for (int sub = SUBS > 1 ? g & 1 : 0; sub < SUBS; sub += 2) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             // the step's words of piece t
-            const uint32_t at = codes + ((t ^ ((r >> 1) & 3)) << 4) + sub * (PIECES * 4);
+            const uint32_t at = st + at_w + ((t ^ swz) << 4) + sub * (PIECES * 4);
             uint32_t v[PIECES];
             if constexpr (PIECES == 4) {
               const uint4 all = ld_shared_v4(at);
@@ -553,10 +897,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
 #pragma unroll
             for (int q = 0; q < PIECES; ++q)
-              tmem_store4(at_a + q * 16 + t * 4, two_weights(v[q]), two_weights(v[q] >> 4), two_weights(v[q] >> 8),
-                          two_weights(v[q] >> 12));
+              tmem_store4(at_a + q * 16 + t * 4, low(v[q]), high(v[q]), low(v[q] >> 8), high(v[q] >> 8));
           }
-          const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(st + 16384)[sub * 256 + tile * 128 + r]);
+          const float s = ld_shared_scale(st + at_s + sub * 512);
+          const uint64_t s2 = pack2(s, s);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -564,12 +908,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           W.warp(&d_full[g], mine & 1);
           ++mine;
           tc_fence_after();
+          constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
+          const uint32_t at_c = st + NT * 256 + (FIRST + sub) * NT * 4, at_u = st + NT * 256 + UP * NT * 4;
 #pragma unroll
-          for (int c = 0; c < NC; c += LD) {
-            uint32_t d[LD];
-            tmem_load<LD>(at_d + c, d);
+          for (int c = 0; c < NT; c += 16) {
+            uint32_t d[16];
+            tmem_load16(at_d + c, d);
 #pragma unroll
-            for (int j = 0; j < LD; ++j) acc[c + j] = fmaf(s, __uint_as_float(d[j]), acc[c + j]);
+            for (int j = 0; j < 16; j += 4) {
+              uint64_t c0, c1, u0, u1;  // of four tokens
+              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(c0), "=l"(c1) : "r"(at_c + (c + j) * 4));
+              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(u0), "=l"(u1) : "r"(at_u + (c + j) * 4));
+              uint64_t* a = acc + (c + j) / 2;
+              a[0] = fma2(s2, mul2(add2(pack2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), c0), u0), a[0]);
+              a[1] = fma2(s2, mul2(add2(pack2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])), c1), u1), a[1]);
+            }
           }
         }
         __syncwarp();
@@ -579,506 +932,38 @@ __global__ void __launch_bounds__(THREADS, 1)
         stage = 0;
         phase ^= 1;
       }
-      if (++chunk < p.chunks && i + 1 < count) continue;
-
-      // ---- end of a segment of `unit`: the odd steps' sums to the even ones'
-      const int odd = g & 1;
-      if (odd) {
+      if (++chunk < p.chunks && i + 1 < run.count) continue;
+      // a segment ends: the odd steps' sums, then the even ones' to them
+      if (g & 1) {
 #pragma unroll
-        for (int c = 0; c < NC; c += 8) tmem_store8(at_d + c, acc + c);
-        tmem_wait_st();
-        tc_fence_before();
+        for (int c = 0; c < NT / 2; ++c) {
+          const float2 v = unpack2(acc[c]);
+          sum[2 * c * SUM_PITCH] = v.x;
+          sum[(2 * c + 1) * SUM_PITCH] = v.y;
+        }
       }
-      bar_sync(1 + tile, 256);
-      if (!odd) {
-        tc_fence_after();
+      bar_sync(1, WORK_WARPS * 32);
+      if (!(g & 1)) {
 #pragma unroll
-        for (int c = 0; c < NC; c += LD) {
-          uint32_t d[LD];
-          tmem_load<LD>(at_d + T_COLS + c, d);
-#pragma unroll
-          for (int j = 0; j < LD; ++j) acc[c + j] += __uint_as_float(d[j]);
-        }
-        tc_fence_before();
-      }
-      bar_sync(1 + tile, 256);  // read: the odd group's next products may come
-      if (!odd) {
-        const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
-        const int C = gridDim.x;
-        const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
-        bool write = true;
-        if (c0 != c1) {
-          // a part: [tile][token][row]
-          const long long slot = NT * 256;
-          float* parts = p.parts + static_cast<long long>(blockIdx.y) * C * 2 * slot + tile * (NT * 128) + r;
-          float* to = parts + (2 * blockIdx.x + (blockIdx.x == c0)) * slot;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) __stcg(to + c * 128, acc[c]);
-          __threadfence();
-          bar_sync(3, 256);
-          if (threadIdx.x == 0) {
-            int* counter = p.counters + blockIdx.y * p.units + unit;
-            s_last = atomicAdd(counter, 1) == c1 - c0;
-          }
-          bar_sync(3, 256);
-          write = s_last != 0;
-          if (write) {
-            __threadfence();
-#pragma unroll
-            for (int c = 0; c < NC; ++c) acc[c] = 0.f;
-            for (int b = c0; b <= c1; ++b) {
-              const float* from = parts + (2 * b + (b == c0)) * slot;
-#pragma unroll
-              for (int c = 0; c < NC; ++c) acc[c] += __ldcg(from + c * 128);
-            }
-          }
-        }
-        long long row = unit * 256 + tile * 128 + r;
-        bool store = write && *W.abort_flag == 0;
-        if (p.epi == W4_SWIGLU) {
-          // tile 1 has the second matrix's rows of the same hidden slots
-          if (tile) {
-#pragma unroll
-            for (int c = 0; c < NC; c += 8) tmem_store8(at_d + c, acc + c);
-            tmem_wait_st();
-            tc_fence_before();
-          }
-          bar_sync(3, 256);
-          if (!tile) {
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < NC; c += LD) {
-              uint32_t d[LD];
-              tmem_load<LD>(at_d + 2 * T_COLS + c, d);
-#pragma unroll
-              for (int j = 0; j < LD; ++j) acc[c + j] = acc[c + j] * sigmoid_f(acc[c + j]) * __uint_as_float(d[j]);
-            }
-            tc_fence_before();
-          }
-          bar_sync(3, 256);
-          row = unit * 128 + r;
-          store = store && !tile && row < p.m.T * p.m.sp;
-        } else if (p.epi == W4_GELU) {
-          const long long t = row / p.m.sp, in = row - t * p.m.sp;
-          const float b = p.bias && in < p.m.s && t < p.m.T ? __bfloat162float(p.bias[t * p.m.s + in]) : 0.f;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) acc[c] = gelu_tanh_f(acc[c] + b);
-          store = store && row < p.m.T * p.m.sp;
-        } else {
-          store = store && row < p.m.rows;
-          if (p.bias && store) {
-            const float b = __bfloat162float(p.bias[row]);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) acc[c] += b;
-          }
-        }
-        if (store) {
-          __nv_bfloat16* to = p.out + n0 * p.out_rs + row;
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (n0 + c < p.n) to[c * p.out_rs] = __float2bfloat16_rn(acc[c]);
+        for (int c = 0; c < NT / 2; ++c) {
+          const float2 v = unpack2(acc[c]);
+          sum[2 * c * SUM_PITCH] += v.x;
+          sum[(2 * c + 1) * SUM_PITCH] += v.y;
         }
       }
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+      for (int c = 0; c < NT / 2; ++c) acc[c] = 0;
+      bar_sync(1, WORK_WARPS * 32);
+      finish_segment<NT, WORK_WARPS>(p, unit, reinterpret_cast<const float*>(smem + R::M_SUM), &s_last, W);
       chunk = 0;
       ++unit;
     }
   }
-  grid_dep_launch();
   tc_fence_before();
   __syncthreads();
   if (warp == WORK_WARPS + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
-  }
-}
-
-// ---------------------------------------------------------------- few tokens
-// Up to 16 tokens: m16n8k16 matrix instructions on registers.  They take 2.05 cycles
-// an SM (measured), 8 tokens of a chunk 262 of the some 720 that its bytes take, 16
-// tokens 525; the tensor-memory products take 768 whatever the number of tokens,
-// besides the way of the weights into tensor memory.
-//
-// What is left to count are the instructions that make operands of codes.  A code
-// in the low bits of an fp16 number is code * 2^-24, a subnormal, and four bits
-// higher code * 2^-20: a word's eight codes are four operand registers after one
-// shift and four masks, without an addition or a conversion.  For that
-//  * the tokens are fp16 too: a block of 128 columns of a token times a power of
-//    two that brings its largest element to 2^14..2^15 (bf16's eight bits are kept
-//    down to 2^-25 of it, what is smaller is rounded to 2^-40 of it), and columns 2, 3,
-//    6, 7 of each eight times 2^-4, for their codes' place;
-//  * the codes' offset of 8 is taken off as the block's sum: a product starts at -8
-//    times the sum of the 32, 64 or 128 columns.
-// A token with an infinity or a NaN so gets NaN throughout.
-// (With codes made into bf16 as below, 11 instructions a word, the 70B
-// feed-forward took 102 us for one token.)
-//
-// A block of tokens as the kernels keep it ("image"), for NT tokens: [2][NT][128
-// bytes], 64 columns each, 16-byte pieces swizzled by the token (piece i at i ^
-// (token & 7)); float [NT][8], -8 * 2^-24 times the sums of its four 32-column
-// parts, its two halves and the whole, and the power of two that undoes the block's.
-// The order of a product's columns is free as long as both operands have it: lane
-// t of a row's four takes the 32-bit word of codes 8 t .. 8 t + 7 of 32 columns, its
-// pairs as the halves of two k16 steps, and so reads the same 8 columns of a token
-// in one piece.  Token t of eight stands in column 2 t, token t + 4 in column 2 t +
-// 1 of the product, so that the two tokens of an eighth of a warp lie in different
-// halves of the swizzled rows.
-// 8 warps, 32 rows of the unit each, two blocks per SM.  At a segment's end the rows
-// meet in shared memory, from where they go out in order.
-__host__ __device__ constexpr int image_bytes(int nt) { return nt * 288; }
-
-// Columns 4 lane .. 4 lane + 3 of a token's block, by a warp, into an image.
-__device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, int lane, const float (&v)[4]) {
-  const float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-  // (infinities count as the largest numbers, NaN is left out: either spoils the block's sum)
-  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
-  const int e = min(141 - static_cast<int>(min(most >> 23, 254u)), 126);  // most * 2^e in 2^14..2^15
-  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
-  const float2 a = __half22float2(lo), b = __half22float2(hi);
-  float sum = (a.x + a.y) + 16.f * (b.x + b.y);
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
-  *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  sum *= -4.76837158203125e-7f;  // -8 * 2^-24
-  const float two = sum + __shfl_xor_sync(0xffffffffu, sum, 8), all = two + __shfl_xor_sync(0xffffffffu, two, 16);
-  float* tail = reinterpret_cast<float*>(image + nt * 256) + token * 8;
-  if ((lane & 7) == 0) tail[lane >> 3] = sum;
-  if ((lane & 15) == 0) tail[4 + (lane >> 4)] = two;
-  if (lane == 0) *reinterpret_cast<float2*>(tail + 6) = make_float2(all, __uint_as_float(static_cast<uint32_t>(127 - e) << 23));
-}
-
-struct PrepareParams {
-  const __nv_bfloat16* x;
-  long long x_seg, x_rs, seg, seg_chunks, chunks, n;
-  int nt;
-  uint8_t* image;  // [chunks]
-  int *err, *counters, n_counters;
-};
-// The kernel before a call's first product: the tokens' blocks, a warp to a token's;
-// clears what the call counts in.  It lets others start when everything before it
-// on the stream is done: the products behind it read their weights without a further wait.
-__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < p.n_counters; i += gridDim.x * 256) p.counters[i] = 0;
-  for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < p.chunks * p.nt; i += gridDim.x * 8ll) {
-    const long long chunk = i / p.nt, e = chunk / p.seg_chunks, col = (chunk - e * p.seg_chunks) * 128 + lane * 4;
-    const int token = static_cast<int>(i - chunk * p.nt);
-    float v[4] = {};
-    if (token < p.n && col < p.seg) {  // segments end at multiples of 8
-      const uint2 w = *reinterpret_cast<const uint2*>(p.x + token * p.x_rs + e * p.x_seg + col);
-      v[0] = bf16_at(w.x, 0), v[1] = bf16_at(w.x, 1), v[2] = bf16_at(w.y, 0), v[3] = bf16_at(w.y, 1);
-    }
-    store_block(p.image + chunk * image_bytes(p.nt), p.nt, token, lane, v);
-  }
-}
-
-template <int NT>
-struct Few {
-  static constexpr int X_BYTES = image_bytes(NT), CODES = 18432, STAGE = X_BYTES + CODES;
-  static constexpr int STAGES = NT == 8 ? 5 : 4;
-  static constexpr int SUM_PITCH = 256 + 8;  // floats: a token's rows
-  static constexpr int M_SUM = STAGES * STAGE;
-  static constexpr int SMEM = M_SUM + NT * SUM_PITCH * 4 + 128;
-  static_assert(2 * (SMEM + 2048) <= 233472, "two blocks per SM");
-};
-constexpr int FEW_WARPS = 8, FEW_THREADS = (FEW_WARPS + 1) * 32;
-
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
-
-// Four neighbouring rows of a token, by a warp that has 128: bias or activation, and out.
-template <int NT>
-__device__ __forceinline__ void write4(const ProductParams& p, int token, long long row, int lane, float4 v) {
-  float a[4] = {v.x, v.y, v.z, v.w};
-  if (p.epi == W4_OUT) {
-    if (token >= p.n || row >= p.m.rows) return;  // rows are a multiple of 8
-    if (p.bias) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] += __bfloat162float(p.bias[row + i]);
-    }
-    *reinterpret_cast<uint2*>(p.out + token * p.out_rs + row) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-    return;
-  }
-  const long long chunk = row >> 7;
-  if (chunk * 128 >= p.m.T * p.m.sp) return;
-  if (p.epi == W4_GELU) {
-    const long long t = row / p.m.sp, in = row - t * p.m.sp;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      a[i] = gelu_tanh_f(a[i] + (p.bias && in + i < p.m.s ? __bfloat162float(p.bias[t * p.m.s + in + i]) : 0.f));
-  }
-  store_block(p.image_out + chunk * image_bytes(NT), NT, token, lane, a);
-}
-
-template <int NT, int SUBS>
-__global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_constant__ ProductParams p) {
-  using F = Few<NT>;
-  constexpr int NB = NT / 8;  // products of eight tokens
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  __shared__ uint64_t full[F::STAGES], empty[F::STAGES];
-  __shared__ int s_abort, s_last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < F::STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], FEW_WARPS);
-    }
-    s_abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    fence_proxy_async_smem();
-  }
-  __syncthreads();
-  grid_dep_launch();
-  const Wait W{&s_abort, p.err, p.timeout_ns};
-  const long long first = p.total * blockIdx.x / gridDim.x, last = p.total * (blockIdx.x + 1) / gridDim.x;
-  const int count = static_cast<int>(last - first);  // chunks
-
-  if (warp == FEW_WARPS) {
-    // ------------------------------------------------ copies
-    // The weights are not the previous kernel's to write (what wrote them is done
-    // before the call's first kernel lets others start); the tokens are.
-    if (lane == 0) {
-      const uint64_t once = l2_policy_evict_first(), often = l2_policy_evict_normal();
-      const uint8_t* src = p.packed + first * p.block_bytes;
-      int c = static_cast<int>(first % p.chunks);
-      auto weights = [&](int stage) {
-        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(p.block_bytes + image_bytes(NT)));
-        bulk_load(smem + stage * F::STAGE + F::X_BYTES, src, static_cast<uint32_t>(p.block_bytes), &full[stage], once);
-        src += p.block_bytes;
-      };
-      auto tokens = [&](int stage) {
-        bulk_load(smem + stage * F::STAGE, p.image + static_cast<long long>(c) * image_bytes(NT), image_bytes(NT), &full[stage], often);
-        if (++c == p.chunks) c = 0;
-      };
-      const int ahead = count < F::STAGES ? count : F::STAGES;
-      for (int i = 0; i < ahead; ++i) weights(i);
-      grid_dep_wait();
-      for (int i = p.skip_load ? 1 : 0; i < ahead; ++i) tokens(i);
-      int issued = ahead, stage = 0;
-      uint32_t phase = 0;
-      for (int i = ahead; i < count; ++i, ++issued) {
-        if (!W(&empty[stage], phase)) break;
-        weights(stage);
-        tokens(stage);
-        if (++stage == F::STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-      // every issued copy lands before the block may exit
-      for (int i = issued > F::STAGES ? issued - F::STAGES : 0; i < issued; ++i)
-        W.drain(&full[i % F::STAGES], (i / F::STAGES) & 1);
-    }
-    __syncwarp();
-    return;
-  }
-  // ------------------------------------------------ products
-  const int t = lane & 3, i8 = lane >> 2;
-  const int row0 = warp * 32 + i8;  // of the unit; the warp's rows: + 0, 8, 16, 24
-  const int tok0 = (i8 & 1) * 4 + (i8 >> 1);
-  // bytes from a stage's start
-  const uint32_t at_x = tok0 * 128, swz = tok0 & 7;
-  const uint32_t at_w = F::X_BYTES + row0 * 64 + ((t ^ ((i8 >> 1) & 3)) << 4), at_s = F::X_BYTES + 16384 + row0 * 2;
-  const uint32_t at_tail = NT * 256 + t * 32;  // of token t
-  float* sum = reinterpret_cast<float*>(smem + F::M_SUM);
-  uint64_t acc[2][NB][2] = {};  // rows row0 + 16 m + 8 h, tokens 8 b + t and 8 b + t + 4
-  grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
-  int stage = 0;
-  uint32_t phase = 0;
-  long long unit = first / p.chunks;
-  int chunk = static_cast<int>(first - unit * p.chunks);
-#pragma unroll 1
-  for (int i = 0; i < count; ++i) {
-    const uint32_t st = smem_u32(smem) + stage * F::STAGE;
-    W.warp(&full[stage], phase);
-    uint64_t up[NB];
-    float start[NB][2];
-    // where the products of a group of columns begin, and what they are multiplied by
-    auto tails = [&](int sub) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t at = st + at_tail + b * 256;
-        float u0, u1;
-        if (SUBS == 1) {
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(start[b][0]), "=f"(u0) : "r"(at + 24));
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(start[b][1]), "=f"(u1) : "r"(at + 152));
-        } else {
-          const uint32_t from = at + (SUBS == 2 ? 16 : 0) + sub * 4;
-          start[b][0] = __uint_as_float(ld_shared(from));
-          start[b][1] = __uint_as_float(ld_shared(from + 128));
-          if (sub == 0) {
-            u0 = __uint_as_float(ld_shared(at + 28));
-            u1 = __uint_as_float(ld_shared(at + 156));
-          }
-        }
-        if (sub == 0) up[b] = pack2(u0, u1);
-      }
-    };
-    uint4 w[2][2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) w[m][h] = ld_shared_v4(st + at_w + m * 1024 + h * 512);
-    float c[2][NB][4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      constexpr int PER = 4 / SUBS;
-      if (q % PER == 0) {
-        tails(q / PER);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            c[m][b][0] = c[m][b][2] = start[b][0];
-            c[m][b][1] = c[m][b][3] = start[b][1];
-          }
-      }
-      uint4 x[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        x[b] = ld_shared_v4(st + at_x + (q >> 1) * (NT * 128) + b * 1024 + ((((q & 1) * 4 + t) ^ swz) << 4));
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t w0 = q == 0 ? w[m][0].x : q == 1 ? w[m][0].y : q == 2 ? w[m][0].z : w[m][0].w;
-        uint32_t w1 = q == 0 ? w[m][1].x : q == 1 ? w[m][1].y : q == 2 ? w[m][1].z : w[m][1].w;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          mma(c[m][b], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, x[b].x, x[b].y);
-        w0 >>= 8;
-        w1 >>= 8;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          mma(c[m][b], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, x[b].z, x[b].w);
-      }
-      if (q % PER != PER - 1) continue;
-      // times the power of two of the token and the scale of the row
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint16_t v;
-          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(st + at_s + (q / PER) * 512 + (16 * m + 8 * h) * 2));
-          const float s = __uint_as_float(static_cast<uint32_t>(v) << 16);
-          const uint64_t s2 = pack2(s, s);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[m][b][h] = fma2(s2, mul2(pack2(c[m][b][2 * h], c[m][b][2 * h + 1]), up[b]), acc[m][b][h]);
-        }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stage]);
-    if (++stage == F::STAGES) {
-      stage = 0;
-      phase ^= 1;
-    }
-    if (++chunk < p.chunks && i + 1 < count) continue;
-
-    // ---- end of a segment of `unit`: its rows meet, [token][row]
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2 v = unpack2(acc[m][b][h]);
-          sum[(8 * b + t) * F::SUM_PITCH + row0 + 16 * m + 8 * h] = v.x;
-          sum[(8 * b + t + 4) * F::SUM_PITCH + row0 + 16 * m + 8 * h] = v.y;
-          acc[m][b][h] = 0;
-        }
-    bar_sync(1, FEW_WARPS * 32);
-    // a thread: rows 4 q .. 4 q + 3 of tile 0 and of tile 1, of a token of every eight
-    const int q4 = lane * 4;
-    const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
-    const int C = gridDim.x;
-    const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
-    bool store = true;
-    float* parts = p.parts + q4;
-    if (c0 != c1) {
-      // a part: [token][row]
-      float* to = parts + static_cast<long long>(2 * blockIdx.x + (blockIdx.x == c0)) * (NT * 256);
-#pragma unroll
-      for (int token = warp; token < NT; token += 8) {
-        __stcg(reinterpret_cast<float4*>(to + token * 256), *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + q4));
-        __stcg(reinterpret_cast<float4*>(to + token * 256 + 128),
-               *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + 128 + q4));
-      }
-      __threadfence();
-      bar_sync(1, FEW_WARPS * 32);
-      if (threadIdx.x == 0) {
-        __threadfence();
-        s_last = atomicAdd(p.counters + unit, 1) == c1 - c0;
-        __threadfence();
-      }
-      bar_sync(1, FEW_WARPS * 32);
-      store = s_last;
-    }
-    if (store && *W.abort_flag == 0) {
-#pragma unroll 1
-      for (int token = warp; token < NT; token += 8) {
-        float4 v0, v1;
-        if (c0 == c1) {
-          v0 = *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + q4);
-          v1 = *reinterpret_cast<const float4*>(sum + token * F::SUM_PITCH + 128 + q4);
-        } else {
-          v0 = v1 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int b = c0; b <= c1; ++b) {
-            const float* from = parts + static_cast<long long>(2 * b + (b == c0)) * (NT * 256) + token * 256;
-            v0 = add4(v0, __ldcg(reinterpret_cast<const float4*>(from)));
-            v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
-          }
-        }
-        const float one = 16777216.f;  // 2^24: a code's unit
-        v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
-        v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
-        if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
-          v0.x *= sigmoid_f(v0.x) * v1.x;
-          v0.y *= sigmoid_f(v0.y) * v1.y;
-          v0.z *= sigmoid_f(v0.z) * v1.z;
-          v0.w *= sigmoid_f(v0.w) * v1.w;
-          write4<NT>(p, token, unit * 128 + q4, lane, v0);
-        } else {
-          write4<NT>(p, token, unit * 256 + q4, lane, v0);
-          write4<NT>(p, token, unit * 256 + 128 + q4, lane, v1);
-        }
-      }
-    }
-    bar_sync(1, FEW_WARPS * 32);
-    chunk = 0;
-    ++unit;
   }
 }
 
@@ -1119,12 +1004,12 @@ int launch_few(const ProductParams& p, dim3 grid, cudaStream_t st) {
   if (p.m.group == 64) return launch_inst<few_kernel<NT, 2>, FEW_THREADS, SMEM>(grid, st, p);
   return launch_inst<few_kernel<NT, 4>, FEW_THREADS, SMEM>(grid, st, p);
 }
-template <int NT, int NC>
-int launch_product(const CUtensorMap& tx, const ProductParams& p, dim3 grid, cudaStream_t st) {
+template <int NT>
+int launch_product(const ProductParams& p, dim3 grid, cudaStream_t st) {
   constexpr int SMEM = Ring<NT>::SMEM;
-  if (p.m.group == 128) return launch_inst<product_kernel<NT, NC, 1>, THREADS, SMEM>(grid, st, tx, p);
-  if (p.m.group == 64) return launch_inst<product_kernel<NT, NC, 2>, THREADS, SMEM>(grid, st, tx, p);
-  return launch_inst<product_kernel<NT, NC, 4>, THREADS, SMEM>(grid, st, tx, p);
+  if (p.m.group == 128) return launch_inst<product_kernel<NT, 1>, THREADS, SMEM>(grid, st, p);
+  if (p.m.group == 64) return launch_inst<product_kernel<NT, 2>, THREADS, SMEM>(grid, st, p);
+  return launch_inst<product_kernel<NT, 4>, THREADS, SMEM>(grid, st, p);
 }
 
 // How a product of n tokens is cut: NT tokens to a block, `tiles` of them, `blocks`
@@ -1200,29 +1085,31 @@ size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms) {
 }
 int64_t w4_product_counters(const W4Shape& m, int64_t n) { return m.units() * ((n + 15) / 16); }
 
-bool w4_few(int64_t n) { return n <= 16; }
 size_t w4_image_bytes(const W4Shape& m, int64_t n) {
-  return w4_few(n) ? static_cast<size_t>(m.chunks()) * w4::image_bytes(n <= 8 ? 8 : 16) : 0;
+  const w4::Cut c = w4::cut_of(m, n, 1);
+  return static_cast<size_t>(m.chunks()) * c.tiles * w4::image_bytes(c.nt);
 }
 
 int launch_w4_prepare(const W4Product& a, int* err, int64_t n_counters, LaunchCtx& ctx) {
   using namespace w4;
+  const Cut c = cut_of(a.m, a.n, ctx.num_sms);
   PrepareParams p{};
   p.x = static_cast<const __nv_bfloat16*>(a.x);
   p.x_seg = a.x_seg;
   p.x_rs = a.x_rs;
   p.seg = a.m.seg;
   p.seg_chunks = a.m.seg_chunks();
-  p.chunks = w4_few(a.n) ? a.m.chunks() : 0;
+  p.chunks = a.m.chunks();
   p.n = a.n;
-  p.nt = a.n <= 8 ? 8 : 16;
+  p.nt = c.nt;
+  p.tiles = c.tiles;
   p.image = static_cast<uint8_t*>(a.image);
   p.err = err;
   p.counters = a.counters;
   p.n_counters = static_cast<int>(n_counters);
-  const int64_t work = std::max<int64_t>(p.chunks * p.nt * 32, n_counters);
+  const int64_t warps = p.tiles * p.chunks * p.nt;
   if (ctx.before) ctx.before(ctx.user, "prepare4", ctx.stream);
-  launch_dep(prepare_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((work + 255) / 256, 4 * ctx.num_sms))), 256, 0,
+  launch_dep(prepare_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, 8 * ctx.num_sms))), 256, 0,
              ctx.stream, p);
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
@@ -1236,7 +1123,6 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   p.m = a.m;
   p.packed = static_cast<const uint8_t*>(a.packed);
   p.chunks = static_cast<int>(a.m.chunks());
-  p.seg_chunks = static_cast<int>(a.m.seg_chunks());
   p.total = a.m.units() * a.m.chunks();
   p.block_bytes = a.m.block_bytes();
   p.units = static_cast<int>(a.m.units());
@@ -1247,6 +1133,7 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.image = static_cast<const uint8_t*>(a.image);
   p.image_out = static_cast<uint8_t*>(a.image_out);
+  p.out_chunks = a.epi == W4_OUT ? 0 : static_cast<int>(a.m.T * a.m.sp / 128);
   p.parts = static_cast<float*>(a.scratch);
   p.counters = a.counters;
   p.err = ctx.err;
@@ -1254,13 +1141,6 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   p.timeout_ns = ctx.timeout_ns;
   ctx.debug_skip_load = 0;
   const dim3 grid(static_cast<unsigned>(c.blocks), static_cast<unsigned>(c.tiles));
-  CUtensorMap tx;
-  if (!w4_few(a.n)) {
-    const uint64_t dims[3] = {static_cast<uint64_t>(a.m.seg), static_cast<uint64_t>(a.m.segs), static_cast<uint64_t>(a.n)};
-    const uint64_t str[2] = {static_cast<uint64_t>(a.m.segs > 1 ? a.x_seg : a.x_rs) * 2, static_cast<uint64_t>(a.x_rs) * 2};
-    const uint32_t box[3] = {64, 1, static_cast<uint32_t>(c.nt)};
-    if (int rc = encode_map_3d_bf16(&tx, a.x, dims, str, box)) return rc;
-  }
   if (ctx.before) ctx.before(ctx.user, a.name, ctx.stream);
   int rc;
   if (c.nt == 8)
@@ -1268,9 +1148,9 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   else if (c.nt == 16)
     rc = launch_few<16>(p, grid, ctx.stream);
   else if (c.nt == 32)
-    rc = launch_product<32, 32>(tx, p, grid, ctx.stream);
+    rc = launch_product<32>(p, grid, ctx.stream);
   else
-    rc = launch_product<64, 64>(tx, p, grid, ctx.stream);
+    rc = launch_product<64>(p, grid, ctx.stream);
   if (rc) return rc;
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
