@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <cstdlib>
 
 #include "tc_ptx.cuh"
 #include "tp_act.cuh"
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
 //    down to 2^-25 of it, what is smaller is rounded to 2^-40 of it), and columns 2, 3,
 //    6, 7 of each eight times 2^-4, for their codes' place;
 //  * the codes' offset of 8 is taken off as the block's sum, -8 times the sum of the
-//    group's 32, 64 or 128 columns.
+//    group's 32, 64 or 128 columns: product * down + sum, times the row's scale.
 // A group's product is scaled in 32 bits, so a result is as exact as the sums in 32
 // bits.  (A scaled weight would have to be rounded.)  A token with an infinity or a
 // NaN gets NaN throughout.
@@ -257,9 +258,10 @@ using namespace tc;
 // A block of tokens as the kernels keep it ("image"), for NT tokens: [2][NT][128
 // bytes], 64 columns each, 16-byte pieces swizzled by the token (piece i at i ^
 // (token & 7)); then float [8][NT]: -8 * 2^-24 times the sums of its four 32-column
-// parts, its two halves and the whole, and the power of two that undoes the block's.
+// parts, its two halves and the whole, and the power of two that undoes the block's
+// and is in the sums already.
 __host__ __device__ constexpr int image_bytes(int nt) { return nt * 288; }
-constexpr int SUM_OF = 0, SUM_OF_HALF = 4, SUM_OF_ALL = 6, UP = 7;
+constexpr int SUM_OF = 0, SUM_OF_HALF = 4, SUM_OF_ALL = 6, DOWN = 7;
 
 struct ProductParams {
   W4Shape m;
@@ -292,7 +294,8 @@ __device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, i
   float sum = (a.x + a.y) + 16.f * (b.x + b.y);
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  sum *= -4.76837158203125e-7f;  // -8 * 2^-24
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  sum *= -4.76837158203125e-7f * down;  // -8 * 2^-24
   const float two = sum + __shfl_xor_sync(0xffffffffu, sum, 8), all = two + __shfl_xor_sync(0xffffffffu, two, 16);
   uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
   *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -300,7 +303,7 @@ __device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, i
   if ((lane & 7) == 0) tail[(SUM_OF + (lane >> 3)) * nt] = sum;
   if ((lane & 15) == 0) tail[(SUM_OF_HALF + (lane >> 4)) * nt] = two;
   if (lane == 0) tail[SUM_OF_ALL * nt] = all;
-  if (lane == 0) tail[UP * nt] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  if (lane == 0) tail[DOWN * nt] = down;
 }
 
 struct PrepareParams {
@@ -363,10 +366,9 @@ struct Wait {
     if (!mbar_try_wait(bar, parity)) slow(bar, parity, false);
   }
   // of a whole warp
-  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) ok = slow(bar, parity, true);
-    return __all_sync(0xffffffffu, ok) != 0;
+  __device__ __forceinline__ void warp(uint64_t* bar, uint32_t parity) const {
+    if (!mbar_try_wait(bar, parity)) slow(bar, parity, true);
+    __syncwarp();
   }
 };
 
@@ -409,16 +411,6 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 // The codes at bits 0-3 and 16-19 as two fp16 numbers, and those at bits 4-7 and 20-23.
@@ -504,14 +496,14 @@ __device__ __forceinline__ void write4(const ProductParams& p, int in_tile, long
 
 // The end of a segment of `unit`, whose sums lie in shared memory, [token][row], 256
 // rows and a few of padding: out if the segment is the whole unit, else as a part,
-// and the last block of the unit joins the parts.  By WARPS warps, which then may
-// write the sums anew.
+// and the last block of the unit joins the parts.  By the WARPS warps from FIRST on,
+// which then may write the sums anew.
 constexpr int SUM_PITCH = 256 + 8;
-template <int NT, int WARPS>
+template <int NT, int WARPS, int FIRST>
 __device__ __forceinline__ void finish_segment(const ProductParams& p, long long unit, const float* sum, int* s_last,
                                                const Wait& W) {
   // a thread: rows 4 q .. 4 q + 3 of tile 0 and of tile 1, of a token of every WARPS
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = lane * 4;
+  const int warp = (threadIdx.x >> 5) - FIRST, lane = threadIdx.x & 31, q4 = lane * 4;
   const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
   const int C = gridDim.x;
   const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
@@ -527,7 +519,7 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
     }
     __threadfence();
     bar_sync(1, WARPS * 32);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == FIRST * 32) {
       __threadfence();
       *s_last = atomicAdd(p.counters + static_cast<long long>(blockIdx.y) * p.units + unit, 1) == c1 - c0;
       __threadfence();
@@ -649,11 +641,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) w[m][h] = ld_shared_v4(st + at_w + m * 1024 + h * 512);
-    uint64_t up[NB];
+    uint64_t down[NB], sums[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const uint32_t at = st + at_tail + UP * NT * 4 + b * 32;
-      up[b] = pack2(ld_shared_f(at), ld_shared_f(at + 16));
+      const uint32_t at = st + at_tail + DOWN * NT * 4 + b * 32;
+      down[b] = pack2(ld_shared_f(at), ld_shared_f(at + 16));
     }
     float c[2][NB][4];
 #pragma unroll
@@ -664,12 +656,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint32_t at = st + at_tail + (FIRST + q / PER) * NT * 4 + b * 32;
-          const float c0 = ld_shared_f(at), c1 = ld_shared_f(at + 16);
+          sums[b] = pack2(ld_shared_f(at), ld_shared_f(at + 16));
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            c[m][b][0] = c[m][b][2] = c0;
-            c[m][b][1] = c[m][b][3] = c1;
-          }
+          for (int m = 0; m < 2; ++m) c[m][b][0] = c[m][b][1] = c[m][b][2] = c[m][b][3] = 0.f;
         }
       }
       uint4 x[NB];
@@ -688,7 +677,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
         for (int b = 0; b < NB; ++b) mma(c[m][b], low(w0), low(w1), high(w0), high(w1), x[b].z, x[b].w);
       }
       if (q % PER != PER - 1) continue;
-      // times the power of two of the token and the scale of the row
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -697,7 +685,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
           const uint64_t s2 = pack2(s, s);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            acc[m][b][h] = fma2(s2, mul2(pack2(c[m][b][2 * h], c[m][b][2 * h + 1]), up[b]), acc[m][b][h]);
+            acc[m][b][h] = fma2(s2, fma2(pack2(c[m][b][2 * h], c[m][b][2 * h + 1]), down[b], sums[b]), acc[m][b][h]);
         }
     }
     __syncwarp();
@@ -719,32 +707,35 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
           acc[m][b][h] = 0;
         }
     bar_sync(1, FEW_WARPS * 32);
-    finish_segment<NT, FEW_WARPS>(p, unit, sum, &s_last, W);
+    finish_segment<NT, FEW_WARPS, 0>(p, unit, sum, &s_last, W);
     chunk = 0;
     ++unit;
   }
 }
 
 // ---------------------------------------------------------------- more tokens
-// 17 to 64 tokens: the weights are the A operand of tcgen05.mma, 128 rows at a time, in
-// tensor memory (in shared memory they would be written and read once more), the
-// tokens its N.  One block per SM:
-//  * warps 0-15, in four groups of 128 threads, a row to a thread: tile 0 and 1 of
-//    the unit, the even and the odd steps (a step: a group's columns).  A thread
-//    writes its row's codes to tensor memory as operands, then reads the step's
-//    product back, scales and adds it.  Four groups, so that one's products run
-//    while others make operands;
-//  * warp 16 copies, warp 17 issues the products.
+// The weights are the A operand of tcgen05.mma, 128 rows at a time, in tensor memory
+// (in shared memory they would be written and read once more), the tokens its N.
+// A product (M 128, K 16) takes 48 cycles whatever N up to 64 is (measured, from
+// tensor or shared memory), 16 of them a chunk: about what its bytes take, so
+// everything else runs beside them.  One block per SM, a step being a group's
+// columns:
+//  * two groups of four warps, a row of tile 0 or 1 to a thread, write the row's
+//    codes to tensor memory as operands, a step ahead of the products;
+//  * groups of four warps, a row and 32 tokens (16 of 16) to a thread, read a
+//    step's products back while the next's run, scale and add them;
+//  * a warp copies, a warp issues the products.
+// (One thread after the other making operands, waiting and reading back: 116 us
+// for 32 tokens of the 70B feed-forward.)
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
-constexpr int GROUPS_OF_WARPS = 4, WORK_WARPS = 16, THREADS = (WORK_WARPS + 2) * 32;
-constexpr int T_COLS = 64;  // columns of tensor memory for a group's weights, and for its products
-
 template <int NT_>
 struct Ring {
   static constexpr int NT = NT_, X_BYTES = (image_bytes(NT) + 1023) / 1024 * 1024, STAGE = X_BYTES + 18432;
-  static constexpr int STAGES = NT == 32 ? 6 : 4;
+  static constexpr int STAGES = NT == 64 ? 4 : 6;
   static constexpr int M_SUM = STAGES * STAGE, SMEM = M_SUM + NT * SUM_PITCH * 4 + 1024;
+  static constexpr int COLS = NT < 32 ? NT : 32;  // tokens of a reading thread
+  static constexpr int MAKERS = 8, READERS = 8 * (NT / COLS), WARPS = MAKERS + READERS + 2, THREADS = WARPS * 32;
   static_assert(SMEM <= 232448 - 1024, "shared memory per block");
 };
 
@@ -757,211 +748,225 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(one));
   return one != 0;
 }
-__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[N]) {
+  if constexpr (N == 32)
+    tmem_ld32(at, r);
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
   tmem_wait_ld();
   // names the registers, so that no use of them moves before the wait
 #pragma unroll
-  for (int i = 0; i < 16; i += 8)
+  for (int i = 0; i < N; i += 8)
     asm volatile(""
                  : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                    "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
-__device__ __forceinline__ void tmem_store4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
 
 template <int NT, int SUBS>
-__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
+__global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   using R = Ring<NT>;
-  constexpr int KSTEPS = 8 / SUBS;  // K = 16 steps of a group
+  constexpr int KSTEPS = 8 / SUBS;        // K = 16 steps of a group
+  constexpr int LD = NT == 32 ? 32 : 16;  // tokens read back at a time
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[R::STAGES], empty[R::STAGES], a_full[GROUPS_OF_WARPS], d_full[GROUPS_OF_WARPS], drain;
+  // of a buffer: operands written, products done, products read
+  __shared__ uint64_t full[R::STAGES], empty[R::STAGES], a_full[2], d_full[2], d_free[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort, s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R::STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], SUBS == 1 ? WORK_WARPS / 2 : WORK_WARPS);  // the warps that have a step of the chunk
+      mbar_init(&empty[i], R::MAKERS + R::READERS);
     }
-    for (int i = 0; i < GROUPS_OF_WARPS; ++i) {
-      mbar_init(&a_full[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&a_full[i], R::MAKERS);
       mbar_init(&d_full[i], 1);
+      mbar_init(&d_free[i], R::READERS);
     }
     mbar_init(&drain, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == WORK_WARPS + 1) tmem_alloc(&tmem_slot, 512);
+  if (warp == R::WARPS - 1) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();
-  const uint32_t tmem = tmem_slot;  // group g's weights at T_COLS g, its products at 256 + T_COLS g
+  // operands of a tile's buffer at 128 tile + 64 buffer, products 256 columns on
+  const uint32_t tmem = tmem_slot;
   const Wait W{&s_abort, p.err, p.timeout_ns};
   const Run run(p);
 
-  if (warp == WORK_WARPS) {
+  if (warp == R::WARPS - 2) {
     if (lane == 0) copy_chunks<R>(p, run, smem, full, empty, W);
     __syncwarp();
-  } else if (warp == WORK_WARPS + 1) {
+  } else if (warp == R::WARPS - 1) {
     // ------------------------------------------------ products
-    // A product takes 48 cycles, whatever N up to 64 is (measured; M 128, K 16, from
-    // tensor or shared memory): few instructions may lie between two.
+    // The warp stays together and one lane waits and issues: what a product is told is
+    // the same for all lanes, else it takes three times as long to issue.  One wait
+    // a step beside the chunk's, for both tiles: a wait takes 150 cycles even where
+    // it finds what it waits for.
     const bool leader = elect_one();
     constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) | (8u << 24);  // fp16 x fp16 -> fp32, M = 128
     const uint64_t x_desc = kdesc(smem_u32(smem), NT, 0);
-    bool ok = true;
     int stage = 0;
     uint32_t phase = 0, step = 0;
 #pragma unroll 1
-    for (int i = 0; i < run.count && ok; ++i) {
-      ok = W.warp(&full[stage], phase);
+    for (int i = 0; i < run.count; ++i) {
+      if (leader) W(&full[stage], phase);
       const uint64_t xd = x_desc + static_cast<uint64_t>(stage * (R::STAGE >> 4));
 #pragma unroll
       for (int sub = 0; sub < SUBS; ++sub, ++step) {
+        const uint32_t buf = step & 1, at = tmem + buf * 64;
+        if (leader) W(&a_full[buf], (step >> 1) & 1);
+        __syncwarp();
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          const uint32_t g = 2 * tile + (step & 1);
-          ok = ok && W.warp(&a_full[g], (step >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t ad = tmem + g * T_COLS;
-          if (leader) {
+          for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
             for (int k = 0; k < KSTEPS; ++k) {
               const int ks = sub * KSTEPS + k;
-              umma_bf16_ta(ad + 256, ad + k * 8, xd + static_cast<uint64_t>(((ks >> 2) * NT * 128 + (ks & 3) * 32) >> 4), ID,
-                           k > 0);
+              umma_bf16_ta(at + 256 + tile * 128, at + tile * 128 + k * 8,
+                           xd + static_cast<uint64_t>(((ks >> 2) * NT * 128 + (ks & 3) * 32) >> 4), ID, k > 0);
             }
-            umma_commit(&d_full[g]);
-          }
-          __syncwarp();
+          umma_commit(&d_full[buf]);
         }
+        __syncwarp();
       }
       if (++stage == R::STAGES) {
         stage = 0;
         phase ^= 1;
       }
     }
-    if (leader) umma_commit(&drain);
-    __syncwarp();
-    W.drain(&drain, 0);
+    if (leader) {
+      umma_commit(&drain);
+      W.drain(&drain, 0);
+    }
     __syncwarp();
   } else {
-    // ------------------------------------------------ operands, products back, sums
-    const int g = warp >> 2, tile = g >> 1, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t at_a = tmem + lane_base + g * T_COLS, at_d = tmem + lane_base + 256 + g * T_COLS;
-    const uint32_t at_w = R::X_BYTES + tile * 8192 + r * 64, swz = (r >> 1) & 3;
-    const uint32_t at_s = R::X_BYTES + 16384 + (tile * 128 + r) * 2;
-    float* sum = reinterpret_cast<float*>(smem + R::M_SUM) + tile * 128 + r;
-    constexpr int PIECES = 4 / SUBS;
-    grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
-    uint64_t acc[NT / 2];
-#pragma unroll
-    for (int c = 0; c < NT / 2; ++c) acc[c] = 0;
-    uint32_t mine = 0;  // steps of this group so far
+    const int tile = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + tile * 128;
     int stage = 0;
-    uint32_t phase = 0;
-    long long unit = run.first / p.chunks;
-    int chunk = static_cast<int>(run.first - unit * p.chunks);
+    uint32_t phase = 0, step = 0;
+    if (warp < R::MAKERS) {
+      // ------------------------------------------------ operands
+      const uint32_t at_w = R::X_BYTES + tile * 8192 + r * 64, swz = (r >> 1) & 3;
+      constexpr int PIECES = 4 / SUBS;
 #pragma unroll 1
-    for (int i = 0; i < run.count; ++i) {
-      if (SUBS > 1 || (i & 1) == (g & 1)) {
+      for (int i = 0; i < run.count; ++i) {
         const uint32_t st = smem_u32(smem) + stage * R::STAGE;
         W.warp(&full[stage], phase);
-#pragma unroll 1
-        for (int sub = SUBS > 1 ? g & 1 : 0; sub < SUBS; sub += 2) {
+        uint4 v[4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            // the step's words of piece t
-            const uint32_t at = st + at_w + ((t ^ swz) << 4) + sub * (PIECES * 4);
-            uint32_t v[PIECES];
-            if constexpr (PIECES == 4) {
-              const uint4 all = ld_shared_v4(at);
-              v[0] = all.x, v[1] = all.y, v[2] = all.z, v[3] = all.w;
-            } else if constexpr (PIECES == 2) {
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
-            } else {
-              v[0] = ld_shared(at);
+        for (int t = 0; t < 4; ++t) v[t] = ld_shared_v4(st + at_w + ((t ^ swz) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub, ++step) {
+          const uint32_t buf = step & 1, uses = step >> 1, at = lanes + buf * 64;
+          W.warp(&d_full[buf], (uses & 1) ^ 1);  // the products that had the buffer are done
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < PIECES; ++q) {
+            const int word = sub * PIECES + q;
+            uint32_t o[16];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t w = word == 0 ? v[t].x : word == 1 ? v[t].y : word == 2 ? v[t].z : v[t].w;
+              o[4 * t] = low(w);
+              o[4 * t + 1] = high(w);
+              o[4 * t + 2] = low(w >> 8);
+              o[4 * t + 3] = high(w >> 8);
             }
-#pragma unroll
-            for (int q = 0; q < PIECES; ++q)
-              tmem_store4(at_a + q * 16 + t * 4, low(v[q]), high(v[q]), low(v[q] >> 8), high(v[q] >> 8));
+            tmem_st16(at + q * 16, o);
           }
+          tmem_wait_st();
+          W.warp(&d_free[buf], (uses & 1) ^ 1);  // and read
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&a_full[buf]);
+        }
+        if (++stage == R::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    } else {
+      // ------------------------------------------------ products back, sums
+      const int token0 = ((warp - R::MAKERS) >> 3) * R::COLS;
+      const uint32_t at_s = R::X_BYTES + 16384 + (tile * 128 + r) * 2;
+      float* sum = reinterpret_cast<float*>(smem + R::M_SUM);
+      float* mine = sum + token0 * SUM_PITCH + tile * 128 + r;
+      grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
+      uint64_t acc[R::COLS / 2];
+#pragma unroll
+      for (int c = 0; c < R::COLS / 2; ++c) acc[c] = 0;
+      long long unit = run.first / p.chunks;
+      int chunk = static_cast<int>(run.first - unit * p.chunks);
+#pragma unroll 1
+      for (int i = 0; i < run.count; ++i) {
+        const uint32_t st = smem_u32(smem) + stage * R::STAGE;
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub, ++step) {
+          const uint32_t buf = step & 1, at = lanes + 256 + buf * 64 + token0;
+          W.warp(&d_full[buf], (step >> 1) & 1);  // (the chunk has landed, else there were no products)
+          tc_fence_after();
           const float s = ld_shared_scale(st + at_s + sub * 512);
           const uint64_t s2 = pack2(s, s);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&a_full[g]);
-          W.warp(&d_full[g], mine & 1);
-          ++mine;
-          tc_fence_after();
           constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
-          const uint32_t at_c = st + NT * 256 + (FIRST + sub) * NT * 4, at_u = st + NT * 256 + UP * NT * 4;
+          const uint32_t at_sum = st + NT * 256 + (FIRST + sub) * NT * 4 + token0 * 4, at_down = st + NT * 256 + DOWN * NT * 4 + token0 * 4;
 #pragma unroll
-          for (int c = 0; c < NT; c += 16) {
-            uint32_t d[16];
-            tmem_load16(at_d + c, d);
+          for (int c = 0; c < R::COLS; c += LD) {
+            uint32_t d[LD];
+            tmem_load<LD>(at + c, d);
+            if (c + LD == R::COLS) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&d_free[buf]);
+            }
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              uint64_t c0, c1, u0, u1;  // of four tokens
-              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(c0), "=l"(c1) : "r"(at_c + (c + j) * 4));
-              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(u0), "=l"(u1) : "r"(at_u + (c + j) * 4));
+            for (int j = 0; j < LD; j += 4) {
+              uint64_t v0, v1, u0, u1;  // of four tokens
+              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(at_sum + (c + j) * 4));
+              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(u0), "=l"(u1) : "r"(at_down + (c + j) * 4));
               uint64_t* a = acc + (c + j) / 2;
-              a[0] = fma2(s2, mul2(add2(pack2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), c0), u0), a[0]);
-              a[1] = fma2(s2, mul2(add2(pack2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])), c1), u1), a[1]);
+              a[0] = fma2(s2, fma2(pack2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), u0, v0), a[0]);
+              a[1] = fma2(s2, fma2(pack2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])), u1, v1), a[1]);
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
-      }
-      if (++stage == R::STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
-      if (++chunk < p.chunks && i + 1 < run.count) continue;
-      // a segment ends: the odd steps' sums, then the even ones' to them
-      if (g & 1) {
-#pragma unroll
-        for (int c = 0; c < NT / 2; ++c) {
-          const float2 v = unpack2(acc[c]);
-          sum[2 * c * SUM_PITCH] = v.x;
-          sum[(2 * c + 1) * SUM_PITCH] = v.y;
+        if (++stage == R::STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
-      }
-      bar_sync(1, WORK_WARPS * 32);
-      if (!(g & 1)) {
+        if (++chunk < p.chunks && i + 1 < run.count) continue;
 #pragma unroll
-        for (int c = 0; c < NT / 2; ++c) {
+        for (int c = 0; c < R::COLS / 2; ++c) {
           const float2 v = unpack2(acc[c]);
-          sum[2 * c * SUM_PITCH] += v.x;
-          sum[(2 * c + 1) * SUM_PITCH] += v.y;
+          mine[2 * c * SUM_PITCH] = v.x;
+          mine[(2 * c + 1) * SUM_PITCH] = v.y;
+          acc[c] = 0;
         }
+        bar_sync(1, R::READERS * 32);
+        finish_segment<NT, R::READERS, R::MAKERS>(p, unit, sum, &s_last, W);
+        chunk = 0;
+        ++unit;
       }
-#pragma unroll
-      for (int c = 0; c < NT / 2; ++c) acc[c] = 0;
-      bar_sync(1, WORK_WARPS * 32);
-      finish_segment<NT, WORK_WARPS>(p, unit, reinterpret_cast<const float*>(smem + R::M_SUM), &s_last, W);
-      chunk = 0;
-      ++unit;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == WORK_WARPS + 1) {
+  if (warp == R::WARPS - 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1007,9 +1012,9 @@ int launch_few(const ProductParams& p, dim3 grid, cudaStream_t st) {
 template <int NT>
 int launch_product(const ProductParams& p, dim3 grid, cudaStream_t st) {
   constexpr int SMEM = Ring<NT>::SMEM;
-  if (p.m.group == 128) return launch_inst<product_kernel<NT, 1>, THREADS, SMEM>(grid, st, p);
-  if (p.m.group == 64) return launch_inst<product_kernel<NT, 2>, THREADS, SMEM>(grid, st, p);
-  return launch_inst<product_kernel<NT, 4>, THREADS, SMEM>(grid, st, p);
+  if (p.m.group == 128) return launch_inst<product_kernel<NT, 1>, Ring<NT>::THREADS, SMEM>(grid, st, p);
+  if (p.m.group == 64) return launch_inst<product_kernel<NT, 2>, Ring<NT>::THREADS, SMEM>(grid, st, p);
+  return launch_inst<product_kernel<NT, 4>, Ring<NT>::THREADS, SMEM>(grid, st, p);
 }
 
 // How a product of n tokens is cut: NT tokens to a block, `tiles` of them, `blocks`
@@ -1021,7 +1026,7 @@ Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
   Cut c;
   c.nt = n <= 8 ? 8 : n <= 16 ? 16 : (n <= 32 ? 32 : 64);
   c.tiles = static_cast<int>((n + c.nt - 1) / c.nt);
-  const int64_t most = c.nt <= 16 ? 2 * num_sms : std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
+  const int64_t most = c.nt <= (getenv("W4_MID") ? 8 : 16) ? 2 * num_sms : std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
   c.blocks = static_cast<int>(std::min<int64_t>(most, total));
   return c;
 }
@@ -1146,7 +1151,7 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   if (c.nt == 8)
     rc = launch_few<8>(p, grid, ctx.stream);
   else if (c.nt == 16)
-    rc = launch_few<16>(p, grid, ctx.stream);
+    rc = getenv("W4_MID") ? launch_product<16>(p, grid, ctx.stream) : launch_few<16>(p, grid, ctx.stream);
   else if (c.nt == 32)
     rc = launch_product<32>(p, grid, ctx.stream);
   else
