@@ -6,12 +6,12 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
-#include <cstdlib>
 
 #include "tc_ptx.cuh"
 #include "tp_act.cuh"
@@ -234,20 +234,26 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
 // 64 tokens at a time.  Bound by the one read of the codes.
 //
 // What is left to count are the instructions that make operands of codes.  A code
-// in the low bits of an fp16 number is code * 2^-24, a subnormal, and four bits
-// higher code * 2^-20: a word's eight codes are four operand registers after one
-// shift and four masks, without an addition or a conversion.  For that
-//  * the tokens are fp16 too: a block of 128 columns of a token times a power of
-//    two that brings its largest element to 2^14..2^15 (bf16's eight bits are kept
-//    down to 2^-25 of it, what is smaller is rounded to 2^-40 of it), and columns 2, 3,
-//    6, 7 of each eight times 2^-4, for their codes' place;
+// in the low bits of a floating number with few exponent bits is a subnormal, code
+// times its least number, and takes no addition or conversion:
+//  * fp16 (up to 16 tokens): code * 2^-24, and four bits higher code * 2^-20.  A word's
+//    eight codes are four operand registers after one shift and four masks.
+//  * e4m3 (more tokens): code * 2^-9.  A word's eight codes are two registers after
+//    one shift and two masks, and a product takes 32 columns instead of 16.
+// (Codes made into bf16 take 11 instructions a word: 102 us instead of 68 for one
+// token of the 70B feed-forward.)  For that
+//  * the tokens are of the same type: a block of 128 columns of a token times a power
+//    of two.  fp16: its largest element comes to 2^14..2^15, so that bf16's eight bits
+//    are kept down to 2^-25 of it and what is smaller is rounded to 2^-40 of it; columns
+//    2, 3, 6, 7 of each eight are times 2^-4 besides, for their codes' place.  e4m3: its
+//    largest element comes to 2^7..2^8, and an element is the sum of two numbers of
+//    four bits, the second times 2^-4: eight bits as bf16 down to 2^-13 of the largest, what is
+//    smaller is rounded to 2^-21 of it.
 //  * the codes' offset of 8 is taken off as the block's sum, -8 times the sum of the
 //    group's 32, 64 or 128 columns: product * down + sum, times the row's scale.
 // A group's product is scaled in 32 bits, so a result is as exact as the sums in 32
 // bits.  (A scaled weight would have to be rounded.)  A token with an infinity or a
-// NaN gets NaN throughout.
-// (With codes made into bf16, 11 instructions a word, the 70B feed-forward took
-// 102 us for one token.)
+// NaN gets those throughout.
 //
 // A block takes a run of chunks (128 columns of a unit's 256 rows) of the list of
 // all units' chunks, the same number as the others, whatever units they belong to;
@@ -255,12 +261,15 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
 // joined by the last of them to come, in the order of the columns.
 using namespace tc;
 
-// A block of tokens as the kernels keep it ("image"), for NT tokens: [2][NT][128
-// bytes], 64 columns each, 16-byte pieces swizzled by the token (piece i at i ^
-// (token & 7)); then float [8][NT]: -8 * 2^-24 times the sums of its four 32-column
-// parts, its two halves and the whole, and the power of two that undoes the block's
-// and is in the sums already.
+// A block of tokens as the kernels keep it ("image"), for NT tokens: fp16 [2][NT][64],
+// 64 columns each, or e4m3 [2][NT][128], the elements' first and second numbers, in
+// rows of 128 bytes whose 16-byte pieces are swizzled by the token (piece i at i ^
+// (token & 7)); e4m3 columns 0, 4, 1, 5, 2, 6, 3, 7 of each eight in this order, as a
+// word's codes come apart.  Then float [8][NT]: -8 times the sums of its four 32-column
+// parts, its two halves and the whole, in units of a code's 2^-24 or 2^-9, and the power
+// of two that undoes the block's and is in the sums already.
 __host__ __device__ constexpr int image_bytes(int nt) { return nt * 288; }
+__host__ __device__ constexpr bool image_f8(int nt) { return nt > 16; }
 constexpr int SUM_OF = 0, SUM_OF_HALF = 4, SUM_OF_ALL = 6, DOWN = 7;
 
 struct ProductParams {
@@ -282,23 +291,52 @@ struct ProductParams {
   unsigned long long timeout_ns;
 };
 
-// Columns 4 lane .. 4 lane + 3 of a token's block, by a warp, into an image.
-__device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, int lane, const float (&v)[4]) {
-  const float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-  // (infinities count as the largest numbers, NaN is left out: either spoils the block's sum)
-  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
-  const int e = min(141 - static_cast<int>(min(most >> 23, 254u)), 126);  // most * 2^e in 2^14..2^15
-  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3),
+                 hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+__device__ __forceinline__ float4 from_e4m3x4(uint32_t v) {
+  const __half2 lo(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3)),
+      hi(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> 16), __NV_E4M3));
   const float2 a = __half22float2(lo), b = __half22float2(hi);
-  float sum = (a.x + a.y) + 16.f * (b.x + b.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Columns 4 lane .. 4 lane + 3 of a token's block, by a warp, into an image.
+template <bool F8>
+__device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, int lane, const float (&v)[4]) {
+  const float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));  // without NaN
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
+  // most * 2^e in 2^14..2^15, or 2^7..2^8
+  const int e = min((F8 ? 134 : 141) - static_cast<int>(min(most >> 23, 254u)), 126);
+  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  float sum;
+  if (F8) {
+    const uint32_t first = e4m3x4(v[0] * up, v[1] * up, v[2] * up, v[3] * up);
+    const float4 f = from_e4m3x4(first);
+    const uint32_t second = e4m3x4(16.f * fmaf(v[0], up, -f.x), 16.f * fmaf(v[1], up, -f.y), 16.f * fmaf(v[2], up, -f.z),
+                                   16.f * fmaf(v[3], up, -f.w));
+    const float4 g = from_e4m3x4(second);
+    sum = ((f.x + f.y) + (f.z + f.w)) + 0.0625f * ((g.x + g.y) + (g.z + g.w));
+    // (infinities are cut to the largest number: the sum tells of them, and of NaN)
+    if (most >= 0x7f800000u || !(v[0] + v[1] + v[2] + v[3] == v[0] + v[1] + v[2] + v[3])) sum = __uint_as_float(0x7fc00000u);
+    const bool odd = lane & 1;
+    const uint32_t first2 = __shfl_xor_sync(0xffffffffu, first, 1), second2 = __shfl_xor_sync(0xffffffffu, second, 1);
+    uint8_t* at = image + token * 128 + (((lane >> 2) ^ (token & 7)) << 4) + (lane & 3) * 4;
+    *reinterpret_cast<uint32_t*>(at) = odd ? __byte_perm(first2, first, 0x7362) : __byte_perm(first, first2, 0x5140);
+    *reinterpret_cast<uint32_t*>(at + nt * 128) = odd ? __byte_perm(second2, second, 0x7362) : __byte_perm(second, second2, 0x5140);
+  } else {
+    const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
+    const float2 a = __half22float2(lo), b = __half22float2(hi);
+    sum = (a.x + a.y) + 16.f * (b.x + b.y);
+    uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
+    *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  sum *= -4.76837158203125e-7f * down;  // -8 * 2^-24
+  sum *= (F8 ? -0.015625f : -4.76837158203125e-7f) * down;  // -8 * 2^-9, -8 * 2^-24
   const float two = sum + __shfl_xor_sync(0xffffffffu, sum, 8), all = two + __shfl_xor_sync(0xffffffffu, two, 16);
-  uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
-  *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   float* tail = reinterpret_cast<float*>(image + nt * 256) + token;
   if ((lane & 7) == 0) tail[(SUM_OF + (lane >> 3)) * nt] = sum;
   if ((lane & 15) == 0) tail[(SUM_OF_HALF + (lane >> 4)) * nt] = two;
@@ -332,7 +370,10 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
       const uint2 w = *reinterpret_cast<const uint2*>(p.x + token * p.x_rs + e * p.x_seg + col);
       v[0] = bf16_at(w.x, 0), v[1] = bf16_at(w.x, 1), v[2] = bf16_at(w.y, 0), v[3] = bf16_at(w.y, 1);
     }
-    store_block(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
+    if (image_f8(p.nt))
+      store_block<true>(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
+    else
+      store_block<false>(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
   }
 }
 
@@ -491,7 +532,7 @@ __device__ __forceinline__ void write4(const ProductParams& p, int in_tile, long
     for (int i = 0; i < 4; ++i)
       a[i] = gelu_tanh_f(a[i] + (p.bias && in + i < p.m.s ? __bfloat162float(p.bias[t * p.m.s + in + i]) : 0.f));
   }
-  store_block(p.image_out + (static_cast<long long>(blockIdx.y) * p.out_chunks + chunk) * image_bytes(NT), NT, in_tile, lane, a);
+  store_block<image_f8(NT)>(p.image_out + (static_cast<long long>(blockIdx.y) * p.out_chunks + chunk) * image_bytes(NT), NT, in_tile, lane, a);
 }
 
 // The end of a segment of `unit`, whose sums lie in shared memory, [token][row], 256
@@ -543,7 +584,7 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
           v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
         }
       }
-      const float one = 16777216.f;  // 2^24: a code's unit
+      const float one = image_f8(NT) ? 512.f : 16777216.f;  // 2^9, 2^24: a code's unit
       v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
       v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
       if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
@@ -714,28 +755,29 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- more tokens
-// The weights are the A operand of tcgen05.mma, 128 rows at a time, in tensor memory
-// (in shared memory they would be written and read once more), the tokens its N.
-// A product (M 128, K 16) takes 48 cycles whatever N up to 64 is (measured, from
-// tensor or shared memory), 16 of them a chunk: about what its bytes take, so
-// everything else runs beside them.  One block per SM, a step being a group's
-// columns:
+// 32 tokens to a block, several token tiles side by side (the weights come from L2
+// for all but the first).  The weights are the A operand of tcgen05.mma, 128 rows at
+// a time, in tensor memory (in shared memory they would be written and read once
+// more), the tokens its N: 64 columns, both numbers of 32 tokens.  A product (M 128, K
+// 32) takes 46 cycles whatever N up to 64 is, as one of fp16 with K 16 does (measured,
+// from tensor or shared memory).  One block per SM, a step being a group's columns:
 //  * two groups of four warps, a row of tile 0 or 1 to a thread, write the row's
 //    codes to tensor memory as operands, a step ahead of the products;
-//  * groups of four warps, a row and 32 tokens (16 of 16) to a thread, read a
-//    step's products back while the next's run, scale and add them;
+//  * two groups of four warps, a row to a thread, read a step's products back while
+//    the next's run, scale and add them;
 //  * a warp copies, a warp issues the products.
-// (One thread after the other making operands, waiting and reading back: 116 us
-// for 32 tokens of the 70B feed-forward.)
+// (With fp16 operands a step has 16 products, and the writes of the maker warps on the
+// issuing warp's scheduler wait behind them: 113 us for 32 tokens of the 70B
+// feed-forward.  One thread after the other making operands, waiting and reading
+// back: 116 us.)
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
 template <int NT_>
 struct Ring {
   static constexpr int NT = NT_, X_BYTES = (image_bytes(NT) + 1023) / 1024 * 1024, STAGE = X_BYTES + 18432;
-  static constexpr int STAGES = NT == 64 ? 4 : 6;
+  static constexpr int STAGES = 6;
   static constexpr int M_SUM = STAGES * STAGE, SMEM = M_SUM + NT * SUM_PITCH * 4 + 1024;
-  static constexpr int COLS = NT < 32 ? NT : 32;  // tokens of a reading thread
-  static constexpr int MAKERS = 8, READERS = 8 * (NT / COLS), WARPS = MAKERS + READERS + 2, THREADS = WARPS * 32;
+  static constexpr int MAKERS = 8, READERS = 8, WARPS = MAKERS + READERS + 2, THREADS = WARPS * 32;
   static_assert(SMEM <= 232448 - 1024, "shared memory per block");
 };
 
@@ -748,31 +790,43 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(one));
   return one != 0;
 }
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[N]) {
-  if constexpr (N == 32)
-    tmem_ld32(at, r);
-  else
+// 16 columns at `at` and 16 at `at2`.
+__device__ __forceinline__ void tmem_load2(uint32_t at, uint32_t at2, uint32_t (&r)[16], uint32_t (&q)[16]) {
+  auto load = [](uint32_t from, uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at));
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(from));
+  };
+  load(at, r);
+  load(at2, q);
   tmem_wait_ld();
   // names the registers, so that no use of them moves before the wait
 #pragma unroll
-  for (int i = 0; i < N; i += 8)
-    asm volatile(""
-                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                   "+r"(r[i + 6]), "+r"(r[i + 7]));
+  for (int i = 0; i < 16; i += 4)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(q[i]), "+r"(q[i + 1]), "+r"(q[i + 2]), "+r"(q[i + 3]));
+}
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// A in tensor memory, four consecutive columns of a row to a 32-bit cell.
+__device__ __forceinline__ void umma_f8_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 template <int NT, int SUBS>
 __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   using R = Ring<NT>;
-  constexpr int KSTEPS = 8 / SUBS;        // K = 16 steps of a group
-  constexpr int LD = NT == 32 ? 32 : 16;  // tokens read back at a time
+  constexpr int KSTEPS = 4 / SUBS;  // K = 32 steps of a group
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // of a buffer: operands written, products done, products read
@@ -800,7 +854,7 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();
-  // operands of a tile's buffer at 128 tile + 64 buffer, products 256 columns on
+  // operands of a tile's buffer at 128 tile + 64 buffer (32 columns), products 256 columns on
   const uint32_t tmem = tmem_slot;
   const Wait W{&s_abort, p.err, p.timeout_ns};
   const Run run(p);
@@ -815,8 +869,8 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
     // a step beside the chunk's, for both tiles: a wait takes 150 cycles even where
     // it finds what it waits for.
     const bool leader = elect_one();
-    constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) | (8u << 24);  // fp16 x fp16 -> fp32, M = 128
-    const uint64_t x_desc = kdesc(smem_u32(smem), NT, 0);
+    constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(2 * NT >> 3) << 17) | (8u << 24);  // e4m3 x e4m3 -> fp32, M = 128
+    const uint64_t x_desc = sw128_desc(smem_u32(smem), 16);
     int stage = 0;
     uint32_t phase = 0, step = 0;
 #pragma unroll 1
@@ -835,8 +889,7 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
 #pragma unroll
             for (int k = 0; k < KSTEPS; ++k) {
               const int ks = sub * KSTEPS + k;
-              umma_bf16_ta(at + 256 + tile * 128, at + tile * 128 + k * 8,
-                           xd + static_cast<uint64_t>(((ks >> 2) * NT * 128 + (ks & 3) * 32) >> 4), ID, k > 0);
+              umma_f8_ta(at + 256 + tile * 128, at + tile * 128 + k * 8, xd + static_cast<uint64_t>(ks * 32 >> 4), ID, k > 0);
             }
           umma_commit(&d_full[buf]);
         }
@@ -878,16 +931,14 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
 #pragma unroll
           for (int q = 0; q < PIECES; ++q) {
             const int word = sub * PIECES + q;
-            uint32_t o[16];
+            uint32_t o[8];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const uint32_t w = word == 0 ? v[t].x : word == 1 ? v[t].y : word == 2 ? v[t].z : v[t].w;
-              o[4 * t] = low(w);
-              o[4 * t + 1] = high(w);
-              o[4 * t + 2] = low(w >> 8);
-              o[4 * t + 3] = high(w >> 8);
+              o[2 * t] = w & 0x0f0f0f0fu;
+              o[2 * t + 1] = (w >> 4) & 0x0f0f0f0fu;
             }
-            tmem_st16(at + q * 16, o);
+            tmem_store8(at + q * 8, o);
           }
           tmem_wait_st();
           W.warp(&d_free[buf], (uses & 1) ^ 1);  // and read
@@ -901,14 +952,13 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
       }
     } else {
       // ------------------------------------------------ products back, sums
-      const int token0 = ((warp - R::MAKERS) >> 3) * R::COLS;
       const uint32_t at_s = R::X_BYTES + 16384 + (tile * 128 + r) * 2;
       float* sum = reinterpret_cast<float*>(smem + R::M_SUM);
-      float* mine = sum + token0 * SUM_PITCH + tile * 128 + r;
+      float* mine = sum + tile * 128 + r;
       grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
-      uint64_t acc[R::COLS / 2];
+      uint64_t acc[NT / 2];
 #pragma unroll
-      for (int c = 0; c < R::COLS / 2; ++c) acc[c] = 0;
+      for (int c = 0; c < NT / 2; ++c) acc[c] = 0;
       long long unit = run.first / p.chunks;
       int chunk = static_cast<int>(run.first - unit * p.chunks);
 #pragma unroll 1
@@ -916,30 +966,35 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
         const uint32_t st = smem_u32(smem) + stage * R::STAGE;
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub, ++step) {
-          const uint32_t buf = step & 1, at = lanes + 256 + buf * 64 + token0;
+          const uint32_t buf = step & 1, at = lanes + 256 + buf * 64;
           W.warp(&d_full[buf], (step >> 1) & 1);  // (the chunk has landed, else there were no products)
           tc_fence_after();
           const float s = ld_shared_scale(st + at_s + sub * 512);
           const uint64_t s2 = pack2(s, s);
           constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
-          const uint32_t at_sum = st + NT * 256 + (FIRST + sub) * NT * 4 + token0 * 4, at_down = st + NT * 256 + DOWN * NT * 4 + token0 * 4;
+          const uint32_t at_sum = st + NT * 256 + (FIRST + sub) * NT * 4, at_down = st + NT * 256 + DOWN * NT * 4;
+          const uint64_t second = pack2(0.0625f, 0.0625f);
 #pragma unroll
-          for (int c = 0; c < R::COLS; c += LD) {
-            uint32_t d[LD];
-            tmem_load<LD>(at + c, d);
-            if (c + LD == R::COLS) {
+          for (int c = 0; c < NT; c += 16) {
+            uint32_t d[16], f[16];
+            tmem_load2(at + c, at + NT + c, d, f);
+            if (c + 16 == NT) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&d_free[buf]);
             }
 #pragma unroll
-            for (int j = 0; j < LD; j += 4) {
+            for (int j = 0; j < 16; j += 4) {
               uint64_t v0, v1, u0, u1;  // of four tokens
               asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(at_sum + (c + j) * 4));
               asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(u0), "=l"(u1) : "r"(at_down + (c + j) * 4));
               uint64_t* a = acc + (c + j) / 2;
-              a[0] = fma2(s2, fma2(pack2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), u0, v0), a[0]);
-              a[1] = fma2(s2, fma2(pack2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])), u1, v1), a[1]);
+              auto both = [&](int k) {
+                return fma2(second, pack2(__uint_as_float(f[k]), __uint_as_float(f[k + 1])),
+                            pack2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])));
+              };
+              a[0] = fma2(s2, fma2(both(j), u0, v0), a[0]);
+              a[1] = fma2(s2, fma2(both(j + 2), u1, v1), a[1]);
             }
           }
         }
@@ -951,7 +1006,7 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
         }
         if (++chunk < p.chunks && i + 1 < run.count) continue;
 #pragma unroll
-        for (int c = 0; c < R::COLS / 2; ++c) {
+        for (int c = 0; c < NT / 2; ++c) {
           const float2 v = unpack2(acc[c]);
           mine[2 * c * SUM_PITCH] = v.x;
           mine[(2 * c + 1) * SUM_PITCH] = v.y;
@@ -1024,9 +1079,9 @@ struct Cut {
 };
 Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
   Cut c;
-  c.nt = n <= 8 ? 8 : n <= 16 ? 16 : (n <= 32 ? 32 : 64);
+  c.nt = n <= 8 ? 8 : n <= 16 ? 16 : 32;
   c.tiles = static_cast<int>((n + c.nt - 1) / c.nt);
-  const int64_t most = c.nt <= (getenv("W4_MID") ? 8 : 16) ? 2 * num_sms : std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
+  const int64_t most = c.nt <= 16 ? 2 * num_sms : std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
   c.blocks = static_cast<int>(std::min<int64_t>(most, total));
   return c;
 }
@@ -1151,11 +1206,9 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   if (c.nt == 8)
     rc = launch_few<8>(p, grid, ctx.stream);
   else if (c.nt == 16)
-    rc = getenv("W4_MID") ? launch_product<16>(p, grid, ctx.stream) : launch_few<16>(p, grid, ctx.stream);
-  else if (c.nt == 32)
-    rc = launch_product<32>(p, grid, ctx.stream);
+    rc = launch_few<16>(p, grid, ctx.stream);
   else
-    rc = launch_product<64>(p, grid, ctx.stream);
+    rc = launch_product<32>(p, grid, ctx.stream);
   if (rc) return rc;
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;

@@ -171,6 +171,26 @@ def test_forward_of_many_units(act, d, d_ff, T, n):
         assert torch.equal(ffn.forward4(x, up, down), y)
 
 
+@pytest.mark.parametrize("n", [3, 12, 40])
+@pytest.mark.parametrize("act,d,d_ff,T", [("swiglu", 512, 640, 2), ("none", 256, 1024, 4)])
+def test_forward_of_wide_ranges(act, d, d_ff, T, n):
+    """Tokens of very different sizes, and elements of very different sizes within a block."""
+    ffn, codes = _ffn(act, d, d_ff, T), _weights(act, d, d_ff, T, 64, 10)
+    up, down = _pack(ffn, codes)
+    Ws = [ref.matrix(c.codes, c.scales, c.cols, c.segments, 64) for c in codes]
+    g = _gen(n)
+    x = torch.randn(n, d_ff if act == "none" else d, generator=g, device="cuda")
+    x = x * torch.exp2(torch.randint(-12, 3, x.shape, generator=g, device="cuda").float())
+    size = torch.linspace(-60, 60, n, device="cuda") if act == "none" else torch.linspace(-20, 4, n, device="cuda")
+    x = (x * torch.exp2(size.round())[:, None]).to(BF)
+    x[1] = 0
+    y = ffn.forward4(x, up, down).double()
+    want, tol = ref.forward(x, act, Ws, None, None)
+    assert torch.isfinite(y).all() and ((y - want).abs() <= tol).all(), ((y - want).abs() / tol).max().item()
+    rel = (y - want).norm(dim=1) / want.norm(dim=1).clamp(min=1e-30)
+    assert (rel <= U).all(), rel
+
+
 def test_forward_of_quantised_weights_and_output_in_place():
     ffn = _ffn("swiglu", 256, 512, 2)
     g = _gen(2)

@@ -57,32 +57,38 @@ def gelu(z):
 def forward(x, act, Ws, b1, b2):
     """y in 64 bits, and how far a result may be from it.
 
-    z is off by at most e(K) sum |x w|: 32-bit sums of K products with their
+    A product takes its tokens exactly, or as blocks of 128 columns: fp16 to a power of
+    two, or e4m3 numbers in pairs, the largest element in 2^7..2^8.  bf16's eight bits
+    are kept but for elements so small that the second number is a subnormal: off by
+    at most half its 2^-9, times 2^-4, 2^-14, or 2^-21 of the block's largest.
+    z is off by at most e(K) sum |x w| besides: 32-bit sums of K products with their
     scales, e(K) = (K + 8) 2^-22 (four times the 2^-24 of each rounding, for the
-    shortened sums of the matrix unit).  |gelu'| <= 1.13, |silu'| <= 1.1; the
-    functions are within 2^-19 of the value for |value| >= 1e-3 and 2^-18 |z|
-    absolutely.  h is rounded to bf16 or better (2^-8 relative; where it is kept to
-    a power of two of its 128 neighbours instead, to 2^-11 relative and 2^-39 of
-    the largest).  Then the same sum for y and its rounding."""
-    def product(v, W):
-        return v @ W.T, (v.shape[1] + 8) * 2.0 ** -22 * (v.abs() @ W.abs().T)
+    shortened sums of the matrix unit).  (The codes are multiplied as 0..15 and the
+    offset of 8 taken off as a sum; for codes spread over 0..15 sum |code x| is below
+    twice sum |(code - 8) x|, which the factor of four covers.)
+    |gelu'| <= 1.13, |silu'| <= 1.1; the functions are within 2^-19 of the value for
+    |value| >= 1e-3 and 2^-18 |z| absolutely.  h is rounded to bf16 or better: 2^-8
+    relative (two e4m3 numbers: 2^-4 of 2^-4).  Then the same for y and its rounding."""
+    def product(v, ev, W):
+        ev = ev + 2.0 ** -21 * v.abs().amax(1, keepdim=True)
+        e = (v.shape[1] + 8) * 2.0 ** -22 * (v.abs() @ W.abs().T)
+        return v @ W.T, e + ev @ W.abs().T
     h = x.double()
     eh = torch.zeros_like(h)
     if act == "swiglu":
-        (a, ea), (g, eg) = product(h, Ws[0]), product(h, Ws[1])
+        (a, ea), (g, eg) = product(h, eh, Ws[0]), product(h, eh, Ws[1])
         s = torch.nn.functional.silu(a)
         h = s * g
         eh = 1.1 * ea * g.abs() + (s.abs() + 1.1 * ea) * eg + 2.0 ** -18 * (a.abs() * g.abs())
     elif act == "gelu_tanh":
-        z, ez = product(h, Ws[0])
+        z, ez = product(h, eh, Ws[0])
         if b1 is not None:
             z = z + b1.double()
         h = gelu(z)
         eh = 1.13 * (ez + 2.0 ** -23 * z.abs()) + 2.0 ** -18 * z.abs()
     if act != "none":
-        eh = eh + 2.0 ** -8 * h.abs() + 2.0 ** -39 * h.abs().amax(1, keepdim=True)
-    y, ey = product(h, Ws[-1])
+        eh = eh + 2.0 ** -8 * h.abs()
+    y, ey = product(h, eh, Ws[-1])
     if b2 is not None:
         y = y + b2.double()
-    tol = ey + eh @ Ws[-1].abs().T
-    return y, (1 + 2.0 ** -8) * tol + 2.0 ** -8 * y.abs() + 1e-30
+    return y, (1 + 2.0 ** -8) * ey + 2.0 ** -8 * y.abs() + 1e-30
