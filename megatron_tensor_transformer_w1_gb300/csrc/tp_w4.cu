@@ -763,8 +763,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // from tensor or shared memory).  One block per SM, a step being a group's columns:
 //  * two groups of four warps, a row of tile 0 or 1 to a thread, write the row's
 //    codes to tensor memory as operands, a step ahead of the products;
-//  * two groups of four warps, a row to a thread, read a step's products back while
-//    the next's run, scale and add them;
+//  * two groups of four warps, a row of either tile and 16 tokens to a thread, read a
+//    step's products back while the next's run, scale and add them (a token's two
+//    numbers are loaded once for both rows: shared memory's loads are what the time
+//    goes by, 109 us with a row and all tokens to a thread);
 //  * a warp copies, a warp issues the products.
 // (With fp16 operands a step has 16 products, and the writes of the maker warps on the
 // issuing warp's scheduler wait behind them: 113 us for 32 tokens of the 70B
@@ -790,23 +792,19 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(one));
   return one != 0;
 }
-// 16 columns at `at` and 16 at `at2`.
-__device__ __forceinline__ void tmem_load2(uint32_t at, uint32_t at2, uint32_t (&r)[16], uint32_t (&q)[16]) {
-  auto load = [](uint32_t from, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(from));
-  };
-  load(at, r);
-  load(at2, q);
+__device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(at));
+}
+// Waits for loads and names their registers, so that no use of them moves before the wait.
+__device__ __forceinline__ void tmem_loaded(uint32_t (&a)[8], uint32_t (&b)[8], uint32_t (&c)[8], uint32_t (&d)[8]) {
   tmem_wait_ld();
-  // names the registers, so that no use of them moves before the wait
 #pragma unroll
-  for (int i = 0; i < 16; i += 4)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(q[i]), "+r"(q[i + 1]), "+r"(q[i + 2]), "+r"(q[i + 3]));
+  for (int i = 0; i < 8; i += 4) {
+    asm volatile("" : "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(b[i]), "+r"(b[i + 1]), "+r"(b[i + 2]), "+r"(b[i + 3]));
+    asm volatile("" : "+r"(c[i]), "+r"(c[i + 1]), "+r"(c[i + 2]), "+r"(c[i + 3]), "+r"(d[i]), "+r"(d[i + 1]), "+r"(d[i + 2]), "+r"(d[i + 3]));
+  }
 }
 __device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
@@ -906,12 +904,13 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
     }
     __syncwarp();
   } else {
-    const int tile = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + tile * 128;
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     int stage = 0;
     uint32_t phase = 0, step = 0;
     if (warp < R::MAKERS) {
       // ------------------------------------------------ operands
+      const int tile = warp >> 2;
       const uint32_t at_w = R::X_BYTES + tile * 8192 + r * 64, swz = (r >> 1) & 3;
       constexpr int PIECES = 4 / SUBS;
 #pragma unroll 1
@@ -925,7 +924,7 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
         if (lane == 0) mbar_arrive(&empty[stage]);
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub, ++step) {
-          const uint32_t buf = step & 1, uses = step >> 1, at = lanes + buf * 64;
+          const uint32_t buf = step & 1, uses = step >> 1, at = lanes + tile * 128 + buf * 64;
           W.warp(&d_full[buf], (uses & 1) ^ 1);  // the products that had the buffer are done
           tc_fence_after();
 #pragma unroll
@@ -952,13 +951,12 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
       }
     } else {
       // ------------------------------------------------ products back, sums
-      const uint32_t at_s = R::X_BYTES + 16384 + (tile * 128 + r) * 2;
+      const int token0 = ((warp - R::MAKERS) >> 2) * (NT / 2);
+      const uint32_t at_s = R::X_BYTES + 16384 + r * 2;
       float* sum = reinterpret_cast<float*>(smem + R::M_SUM);
-      float* mine = sum + tile * 128 + r;
       grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
-      uint64_t acc[NT / 2];
-#pragma unroll
-      for (int c = 0; c < NT / 2; ++c) acc[c] = 0;
+      uint64_t acc[2][NT / 4] = {};  // rows r and 128 + r
+      const uint64_t second = pack2(0.0625f, 0.0625f);
       long long unit = run.first / p.chunks;
       int chunk = static_cast<int>(run.first - unit * p.chunks);
 #pragma unroll 1
@@ -966,36 +964,38 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
         const uint32_t st = smem_u32(smem) + stage * R::STAGE;
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub, ++step) {
-          const uint32_t buf = step & 1, at = lanes + 256 + buf * 64;
+          const uint32_t buf = step & 1, at = lanes + 256 + buf * 64 + token0;
           W.warp(&d_full[buf], (step >> 1) & 1);  // (the chunk has landed, else there were no products)
           tc_fence_after();
-          const float s = ld_shared_scale(st + at_s + sub * 512);
-          const uint64_t s2 = pack2(s, s);
           constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
-          const uint32_t at_sum = st + NT * 256 + (FIRST + sub) * NT * 4, at_down = st + NT * 256 + DOWN * NT * 4;
-          const uint64_t second = pack2(0.0625f, 0.0625f);
+          const uint32_t at_sum = st + NT * 256 + ((FIRST + sub) * NT + token0) * 4, at_down = st + NT * 256 + (DOWN * NT + token0) * 4;
+          const float s0 = ld_shared_scale(st + at_s + sub * 512), s1 = ld_shared_scale(st + at_s + sub * 512 + 256);
+          const uint64_t s2[2] = {pack2(s0, s0), pack2(s1, s1)};
 #pragma unroll
-          for (int c = 0; c < NT; c += 16) {
-            uint32_t d[16], f[16];
-            tmem_load2(at + c, at + NT + c, d, f);
-            if (c + 16 == NT) {
+          for (int c = 0; c < NT / 2; c += 8) {  // eight tokens
+            uint32_t d[2][2][8];  // [tile][number]
+#pragma unroll
+            for (int m = 0; m < 4; ++m) tmem_load8(at + (m >> 1) * 128 + (m & 1) * NT + c, d[m >> 1][m & 1]);
+            uint64_t sums[4], down[4];
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(sums[j]), "=l"(sums[j + 1]) : "r"(at_sum + (c + 2 * j) * 4));
+              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(down[j]), "=l"(down[j + 1]) : "r"(at_down + (c + 2 * j) * 4));
+            }
+            tmem_loaded(d[0][0], d[0][1], d[1][0], d[1][1]);
+            if (c + 8 == NT / 2) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&d_free[buf]);
             }
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              uint64_t v0, v1, u0, u1;  // of four tokens
-              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(at_sum + (c + j) * 4));
-              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(u0), "=l"(u1) : "r"(at_down + (c + j) * 4));
-              uint64_t* a = acc + (c + j) / 2;
-              auto both = [&](int k) {
-                return fma2(second, pack2(__uint_as_float(f[k]), __uint_as_float(f[k + 1])),
-                            pack2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])));
-              };
-              a[0] = fma2(s2, fma2(both(j), u0, v0), a[0]);
-              a[1] = fma2(s2, fma2(both(j + 2), u1, v1), a[1]);
-            }
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                auto two = [&](int k) { return pack2(__uint_as_float(d[m][k][2 * j]), __uint_as_float(d[m][k][2 * j + 1])); };
+                uint64_t& a = acc[m][c / 2 + j];
+                a = fma2(s2[m], fma2(fma2(second, two(1), two(0)), down[j], sums[j]), a);
+              }
           }
         }
         __syncwarp();
@@ -1006,12 +1006,15 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
         }
         if (++chunk < p.chunks && i + 1 < run.count) continue;
 #pragma unroll
-        for (int c = 0; c < NT / 2; ++c) {
-          const float2 v = unpack2(acc[c]);
-          mine[2 * c * SUM_PITCH] = v.x;
-          mine[(2 * c + 1) * SUM_PITCH] = v.y;
-          acc[c] = 0;
-        }
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < NT / 4; ++j) {
+            const float2 v = unpack2(acc[m][j]);
+            float* to = sum + (token0 + 2 * j) * SUM_PITCH + m * 128 + r;
+            to[0] = v.x;
+            to[SUM_PITCH] = v.y;
+            acc[m][j] = 0;
+          }
         bar_sync(1, R::READERS * 32);
         finish_segment<NT, R::READERS, R::MAKERS>(p, unit, sum, &s_last, W);
         chunk = 0;
