@@ -543,6 +543,64 @@ TPFFN_API int tp_attn_decode_fwd4(const tp_attn_plan* plan, const tp_kv_cache* c
                                   const void* wqkv_4, const void* wo_4, void* y, void* workspace,
                                   size_t workspace_bytes, int flags, tp_stream_t stream);
 
+/* ------------------------------------------- norms around a block's sublayers
+ *
+ * What stands between two sublayers of a block, for n tokens of width d: with the
+ * residual stream x and a sublayer's output b,
+ *     u   = after ? norm(b) * w_after + c_after : b
+ *     r   = x + scale * gate * u              (b NULL: r = x)
+ *     out = norm(r) * w_before + c_before     (with `before`)
+ * r is the residual stream behind the sublayer and out the input of the next one.
+ * norm(v) over the d columns of a token, with eps inside the root:
+ *     TP_NORM_RMS    v / sqrt(mean(v^2) + eps)
+ *     TP_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps)
+ * Any of w_after, c_after, w_before and c_before [d] may be NULL: ones, zeros.
+ * gate [n_gates][d] (n_gates 0: ones): token i has row i / (n / n_gates): 1 for
+ * a gate of each channel, the number of sequences for one of each of them, n for
+ * one of each token.  n_gates divides n.
+ * Elements are of `dtype` (TP_BF16 or TP_F32), rows of d, statistics and sums in
+ * 32 bits; `out` is formed from r before its rounding.  d is a multiple of 8 up to
+ * 8192.
+ */
+enum { TP_NORM_RMS = 0, TP_NORM_LAYER = 1 };
+typedef struct tp_norm {
+  int64_t d;
+  int32_t kind, dtype;
+  int32_t before, after;  /* 0 or 1 */
+  float eps, scale;
+} tp_norm;
+
+/* r [n][d] (it may be x itself); out [n][d] with `before`, NULL without.
+ * stats: fp32 [n][4] or NULL: mean and factor (1 / root) of the norm of b, then of
+ * r, for tp_norm_bwd; what belongs to a norm that there is not is left as it was.
+ * Buffers do not overlap otherwise, but out may be b.  One launch.
+ * Errors: TP_ERR_INVALID (NULL, sizes, n_gates not dividing n, out with before 0,
+ * a weight of a norm that there is not, gate or `after` without b),
+ * TP_ERR_UNSUPPORTED (d, n above 2^30), TP_ERR_ALIGN.  n 0: TP_OK, no work. */
+TPFFN_API int tp_norm_fwd(const tp_norm* norm, int64_t n, int64_t n_gates, const void* x, const void* b,
+                          const void* w_after, const void* c_after, const void* gate, const void* w_before,
+                          const void* c_before, void* r, void* out, float* stats, tp_stream_t stream);
+
+/* Gradients from dr [n][d], that of r (NULL: zeros), and dout [n][d], that of out
+ * (with `before`; NULL without), given the forward's b, r and stats:
+ *     g   = dr + (d out / d r)^T dout;  dx = g
+ *     db  = (d u / d b)^T (scale * gate * g);  dgate = scale * sum of g * u
+ *     dw_before = sum of dout * norm(r), dc_before = sum of dout, and alike
+ *     dw_after, dc_after of scale * gate * g.
+ * dx and db are [n][d], dgate [n_gates][d], the others [d]; each may be NULL where
+ * it is not wanted (dx may be dr, db may be dout).  r is needed with `before`, b
+ * with `after` or for dgate.  The sums run over tokens in a fixed order: results do
+ * not change from run to run on one kind of GPU.
+ * workspace: tp_norm_workspace_bytes(norm, n, n_gates) bytes (0 for arguments that
+ * the call would refuse).  Errors as tp_norm_fwd; a gradient of what there is not is
+ * TP_ERR_INVALID. */
+TPFFN_API size_t tp_norm_workspace_bytes(const tp_norm* norm, int64_t n, int64_t n_gates);
+TPFFN_API int tp_norm_bwd(const tp_norm* norm, int64_t n, int64_t n_gates, const void* b, const void* r,
+                          const float* stats, const void* w_after, const void* c_after, const void* gate,
+                          const void* w_before, const void* dr, const void* dout, void* dx, void* db,
+                          void* dw_after, void* dc_after, void* dgate, void* dw_before, void* dc_before,
+                          void* workspace, size_t workspace_bytes, tp_stream_t stream);
+
 /* ------------------------------------------------ forward without allocation */
 
 /* Size of the library's static scratch array (32 MiB).  A GPU holds this

@@ -1982,4 +1982,95 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
   return kv_finish(a, ctx, rc, flags, workspace);
 }
 
+// ------------------------------------------------------------ norms around sublayers
+namespace {
+int norm_sizes(const tp_norm* m, int64_t n, int64_t n_gates, NormSpec& a) {
+  if (!m || n < 0 || n_gates < 0 || m->d < 1) return TP_ERR_INVALID;
+  if ((m->kind != TP_NORM_RMS && m->kind != TP_NORM_LAYER) || (m->dtype != TP_BF16 && m->dtype != TP_F32) ||
+      (m->before & ~1) || (m->after & ~1))
+    return TP_ERR_INVALID;
+  if (n_gates && n % n_gates) return TP_ERR_INVALID;
+  if (m->d % 8 || m->d > 8192 || n > (int64_t(1) << 30)) return TP_ERR_UNSUPPORTED;
+  a.n = n;
+  a.d = m->d;
+  a.n_gates = n_gates;
+  a.layer = m->kind == TP_NORM_LAYER;
+  a.f32 = m->dtype == TP_F32;
+  a.before = m->before;
+  a.after = m->after;
+  a.eps = m->eps;
+  a.scale = m->scale;
+  return TP_OK;
+}
+int norm_aligned(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return TP_ERR_ALIGN;
+  return TP_OK;
+}
+}  // namespace
+
+int tp_norm_fwd(const tp_norm* norm, int64_t n, int64_t n_gates, const void* x, const void* b, const void* w_after,
+                const void* c_after, const void* gate, const void* w_before, const void* c_before, void* r, void* out,
+                float* stats, tp_stream_t stream) {
+  NormSpec a;
+  int rc = norm_sizes(norm, n, n_gates, a);
+  if (rc || n == 0) return rc;
+  if (!x || !r || (a.before != 0) != (out != nullptr) || (gate != nullptr) != (n_gates > 0)) return TP_ERR_INVALID;
+  if ((!a.after && (w_after || c_after)) || (!a.before && (w_before || c_before)) || (!b && (gate || a.after)))
+    return TP_ERR_INVALID;
+  if ((rc = norm_aligned({x, b, w_after, c_after, gate, w_before, c_before, r, out, stats}))) return rc;
+  a.x = x;
+  a.b = b;
+  a.w_after = w_after;
+  a.c_after = c_after;
+  a.gate = gate;
+  a.w_before = w_before;
+  a.c_before = c_before;
+  a.r = r;
+  a.out = out;
+  a.stats = stats;
+  return launch_norm_fwd(a, num_sms_current(), reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t tp_norm_workspace_bytes(const tp_norm* norm, int64_t n, int64_t n_gates) {
+  NormSpec a;
+  if (norm_sizes(norm, n, n_gates, a)) return 0;
+  return n ? align_up(norm_workspace_bytes(a, num_sms_current())) : kAlign;
+}
+
+int tp_norm_bwd(const tp_norm* norm, int64_t n, int64_t n_gates, const void* b, const void* r, const float* stats,
+                const void* w_after, const void* c_after, const void* gate, const void* w_before, const void* dr,
+                const void* dout, void* dx, void* db, void* dw_after, void* dc_after, void* dgate, void* dw_before,
+                void* dc_before, void* workspace, size_t workspace_bytes, tp_stream_t stream) {
+  NormSpec a;
+  int rc = norm_sizes(norm, n, n_gates, a);
+  if (rc || n == 0) return rc;
+  if ((a.before != 0) != (dout != nullptr) || (gate != nullptr) != (n_gates > 0)) return TP_ERR_INVALID;
+  if ((!a.after && (w_after || c_after || dw_after || dc_after)) || (!a.before && (w_before || dw_before || dc_before)))
+    return TP_ERR_INVALID;
+  if ((a.before && !r) || ((a.before || a.after) && !stats) || (dgate && !gate) || ((a.after || dgate) && !b) || !workspace)
+    return TP_ERR_INVALID;
+  if ((rc = norm_aligned({b, r, stats, w_after, c_after, gate, w_before, dr, dout, dx, db, dw_after, dc_after, dgate,
+                          dw_before, dc_before, workspace})))
+    return rc;
+  if (workspace_bytes < tp_norm_workspace_bytes(norm, n, n_gates)) return TP_ERR_INVALID;
+  a.b = a.after || dgate ? b : nullptr;
+  a.r_in = r;
+  a.stats = a.before || a.after ? const_cast<float*>(stats) : nullptr;
+  a.w_after = w_after;
+  a.c_after = c_after;
+  a.gate = gate;
+  a.w_before = w_before;
+  a.dr = dr;
+  a.dout = dout;
+  a.dx = dx;
+  a.db = db;
+  a.dw_after = dw_after;
+  a.dc_after = dc_after;
+  a.dgate = dgate;
+  a.dw_before = dw_before;
+  a.dc_before = dc_before;
+  return launch_norm_bwd(a, workspace, num_sms_current(), reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -342,4 +342,22 @@ size_t w4_image_bytes(const W4Shape& m, int64_t n);  // of the tokens that m mul
 int launch_w4_prepare(const W4Product& p, int* err, int64_t n_counters, LaunchCtx& ctx);
 int launch_w4_product(const W4Product& p, LaunchCtx& ctx);
 
+// ------------------------------------------------------------ norms around sublayers
+// (tp_norm.cu)  See tp_norm_fwd and tp_norm_bwd; the arguments are checked.
+struct NormSpec {
+  int64_t n = 0, d = 0, n_gates = 0;
+  int layer = 0, f32 = 0, before = 0, after = 0;
+  float eps = 0.f, scale = 1.f;
+  const void *x = nullptr, *b = nullptr, *w_after = nullptr, *c_after = nullptr, *gate = nullptr, *w_before = nullptr,
+             *c_before = nullptr;
+  void *r = nullptr, *out = nullptr;
+  float* stats = nullptr;
+  const void *r_in = nullptr, *dr = nullptr, *dout = nullptr;
+  void *dx = nullptr, *db = nullptr, *dw_after = nullptr, *dc_after = nullptr, *dgate = nullptr, *dw_before = nullptr,
+       *dc_before = nullptr;
+};
+int launch_norm_fwd(const NormSpec& a, int num_sms, cudaStream_t st);
+size_t norm_workspace_bytes(const NormSpec& a, int num_sms);
+int launch_norm_bwd(const NormSpec& a, void* workspace, int num_sms, cudaStream_t st);
+
 }  // namespace tpffn

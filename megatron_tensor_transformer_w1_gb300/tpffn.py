@@ -21,6 +21,7 @@ TP_PACK_COLUMNS, TP_PACK_ROWS = 0, 1
 TP_SUM_STANDALONE, TP_SUM_FUSED, TP_FLAG_SYNC, TP_FLAG_TIMING, TP_SUM_OVERLAP = 0, 1, 2, 4, 8
 TP_FLAG_DEBUG_SKIP_LOAD = 1 << 16
 TP_KV_APPEND, TP_KV_ATTEND, TP_KV_DECODE, TP_KV_DECODE4 = 0, 1, 2, 3
+TP_NORM_RMS, TP_NORM_LAYER = 0, 1
 
 ABI_FUNCTIONS = (
     "tp_ffn_plan_create", "tp_attn_out_plan_create", "tp_ffn_plan_destroy", "tp_ffn_plan_info",
@@ -38,6 +39,7 @@ ABI_FUNCTIONS = (
     "tp_quantize4", "tp_dequantize4", "tp_ffn_packed4_bytes", "tp_ffn_shard_columns4", "tp_ffn_shard_rows4",
     "tp_ffn_unshard_columns4", "tp_ffn_unshard_rows4", "tp_ffn_workspace4_bytes", "tp_ffn_fwd4",
     "tp_attn_packed4_bytes", "tp_attn_shard_weights4", "tp_attn_unshard_weights4", "tp_attn_decode_fwd4",
+    "tp_norm_fwd", "tp_norm_workspace_bytes", "tp_norm_bwd",
 )
 TPFFN_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -75,6 +77,12 @@ class KvRotation(ctypes.Structure):
     """tp_kv_rotation"""
     _fields_ = [("inv_freq", _P), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class Norm(ctypes.Structure):
+    """tp_norm"""
+    _fields_ = [("d", _I64), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32), ("before", ctypes.c_int32),
+                ("after", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
 _SIGS = {
@@ -134,6 +142,9 @@ _SIGS = {
     "tp_attn_shard_weights4": (_INT, [_P, _INT, _P, _P, _P, _P, _P]),
     "tp_attn_unshard_weights4": (_INT, [_P, _INT, _P, _P, _P, _P, _P]),
     "tp_attn_decode_fwd4": (_INT, [_P, _P, _P, _P, _I64, _INT, _P, _P, _P, _P, _P, _SZ, _INT, _P]),
+    "tp_norm_fwd": (_INT, [_P, _I64, _I64] + [_P] * 11),
+    "tp_norm_workspace_bytes": (_SZ, [_P, _I64, _I64]),
+    "tp_norm_bwd": (_INT, [_P, _I64, _I64] + [_P] * 17 + [_SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -459,6 +470,24 @@ def tp_attn_decode_fwd4(plan, cache, batch, rotation, shared_len, group, x, wqkv
     return _lib.tp_attn_decode_fwd4(plan, _ref(cache), _ref(batch), _ref(rotation), shared_len, group, _ptr(x),
                                     _ptr(wqkv_4), _ptr(wo_4), _ptr(y), _ptr(workspace), workspace_bytes, flags,
                                     _stream(stream))
+
+
+# ------------------------------------------------------------ norms around sublayers
+def tp_norm_fwd(norm, n, n_gates, x, b, w_after, c_after, gate, w_before, c_before, r, out, stats, stream=None):
+    return _lib.tp_norm_fwd(_ref(norm), n, n_gates, _ptr(x), _ptr(b), _ptr(w_after), _ptr(c_after), _ptr(gate),
+                            _ptr(w_before), _ptr(c_before), _ptr(r), _ptr(out), _ptr(stats), _stream(stream))
+
+
+def tp_norm_workspace_bytes(norm, n, n_gates):
+    return _lib.tp_norm_workspace_bytes(_ref(norm), n, n_gates)
+
+
+def tp_norm_bwd(norm, n, n_gates, b, r, stats, w_after, c_after, gate, w_before, dr, dout, dx, db, dw_after, dc_after,
+                dgate, dw_before, dc_before, workspace, workspace_bytes, stream=None):
+    return _lib.tp_norm_bwd(_ref(norm), n, n_gates, _ptr(b), _ptr(r), _ptr(stats), _ptr(w_after), _ptr(c_after),
+                            _ptr(gate), _ptr(w_before), _ptr(dr), _ptr(dout), _ptr(dx), _ptr(db), _ptr(dw_after),
+                            _ptr(dc_after), _ptr(dgate), _ptr(dw_before), _ptr(dc_before), _ptr(workspace),
+                            workspace_bytes, _stream(stream))
 
 
 def check(status, where=""):
