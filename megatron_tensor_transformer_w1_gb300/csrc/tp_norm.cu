@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "tc_ptx.cuh"
@@ -28,6 +29,7 @@ template <>
 struct Eight<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const void* p, long long at) { v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at); }
+  __device__ __forceinline__ void load(const uint4* slot) { v = slot[0]; }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ float operator[](int i) const {
     const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
@@ -45,6 +47,10 @@ struct Eight<float> {
     a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
     b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
   }
+  __device__ __forceinline__ void load(const uint4* slot) {
+    a = *reinterpret_cast<const float4*>(slot);
+    b = *reinterpret_cast<const float4*>(slot + blockDim.x);
+  }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ float operator[](int i) const {
     return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
@@ -56,7 +62,9 @@ struct Eight<float> {
 };
 
 // A row belongs to `tpr` threads, a multiple of 32, thread t of them having the
-// columns 8 t .. 8 t + 7; a block has blockDim / tpr rows at a time.
+// columns 8 t .. 8 t + 7; a block has blockDim / tpr row groups with R rows each.
+// A thread copies its columns of the next rows into slots of its own in shared memory
+// while it works on these: it waits for nobody, and no registers are held for them.
 struct NormParams {
   long long n, d, per;  // per: tokens of a gate
   int tpr, after, before;
@@ -75,6 +83,23 @@ struct NormParams {
   float* gate_sums;       // [gates][chunks][d]
 };
 
+template <typename T>
+__device__ __forceinline__ void fetch(uint4* slot, const void* p, long long at) {
+  const T* src = static_cast<const T*>(p) + at;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot + i * blockDim.x)),
+                 "l"(reinterpret_cast<const uint4*>(src) + i)
+                 : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// 16-byte slots of an array's row: one to a thread (bf16), or two.
+template <typename T>
+__host__ __device__ constexpr int slots(int threads) {
+  return threads * static_cast<int>(sizeof(T)) / 2;
+}
+
 // Sums of N values over a row's threads.  `turn` alternates between two buffers, so
 // that one barrier a sum is enough.
 template <int N>
@@ -91,93 +116,135 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (*s)[32][
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = 0.f;
+#pragma unroll 8
   for (int w = 0; w < warps; ++w)
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] += s[turn][first + w][k];
   turn ^= 1;
 }
 
-// The mean and factor of a row's norm.
-template <bool LAYER>
-__device__ __forceinline__ float2 row_stats(const float (&v)[8], bool ok, const NormParams& p, float (*s)[32][1], int& turn) {
-  float mean = 0.f, sum[1] = {0.f};
+// The mean and factor of R rows' norms.
+template <bool LAYER, int R>
+__device__ __forceinline__ void row_stats(const float (&v)[R][8], bool ok, const NormParams& p, float (*s)[32][R], int& turn,
+                                          float2 (&st)[R]) {
+  float sum[R] = {};
+#pragma unroll
+  for (int k = 0; k < R; ++k) st[k].x = 0.f;
   if (LAYER) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[0] += v[i];
-    row_sums<1>(sum, p.tpr, s, turn);
-    mean = sum[0] * p.inv_d;
-    sum[0] = 0.f;
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[k] += v[k][i];
+    row_sums<R>(sum, p.tpr, s, turn);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      st[k].x = sum[k] * p.inv_d;
+      sum[k] = 0.f;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = ok ? v[i] - mean : 0.f;
-    sum[0] = fmaf(a, a, sum[0]);
-  }
-  row_sums<1>(sum, p.tpr, s, turn);
-  return make_float2(mean, 1.f / sqrtf(fmaf(sum[0], p.inv_d, p.eps)));
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = ok ? v[k][i] - st[k].x : 0.f;
+      sum[k] = fmaf(a, a, sum[k]);
+    }
+  row_sums<R>(sum, p.tpr, s, turn);
+#pragma unroll
+  for (int k = 0; k < R; ++k) st[k].y = 1.f / sqrtf(fmaf(sum[k], p.inv_d, p.eps));
 }
 
-template <typename T, bool LAYER>
-__global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_sum[2][32][1];
+template <typename T, bool LAYER, int R>
+__global__ void __launch_bounds__(R == 2 ? 512 : 1024) forward_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s_sum[2][32][R];
+  extern __shared__ uint4 s_slots[];  // [2][x, b][R] of slots
   grid_dep_wait();
   grid_dep_launch();
-  const int t = threadIdx.x % p.tpr, rows = blockDim.x / p.tpr;
-  int turn = 0;
-  const long long col = 8ll * t;
+  const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
+  const long long col = 8ll * t, step = static_cast<long long>(gridDim.x) * groups * R;
   const bool ok = col < p.d;
+  int turn = 0, stage = 0;
+  auto slot = [&](int st, int array, int k) { return s_slots + ((st * 2 + array) * R + k) * slots<T>(blockDim.x) + threadIdx.x; };
+  auto fetch_rows = [&](long long row0, int st) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const long long row = row0 + group + k * groups;
+      if (!ok || row >= p.n) continue;
+      fetch<T>(slot(st, 0, k), p.x, row * p.d + col);
+      if (p.b) fetch<T>(slot(st, 1, k), p.b, row * p.d + col);
+    }
+    fetch_commit();
+  };
+  long long row0 = static_cast<long long>(blockIdx.x) * groups * R;
+  fetch_rows(row0, 0);
   Eight<T> wa, ca, wb, cb;
   if (ok && p.w_after) wa.load(p.w_after, col);
   if (ok && p.c_after) ca.load(p.c_after, col);
   if (ok && p.w_before) wb.load(p.w_before, col);
   if (ok && p.c_before) cb.load(p.c_before, col);
-  for (long long row0 = static_cast<long long>(blockIdx.x) * rows; row0 < p.n; row0 += static_cast<long long>(gridDim.x) * rows) {
-    const long long row = row0 + threadIdx.x / p.tpr, at = row * p.d + col;
-    const bool live = ok && row < p.n;
-    Eight<T> x, b, g;
-    x.zero();
-    b.zero();
-    g.zero();
-    if (live) {
-      x.load(p.x, at);
-      if (p.b) b.load(p.b, at);
-      if (p.gate) g.load(p.gate, row / p.per * p.d + col);
-    }
-    float v[8], u[8];
+  for (; row0 < p.n; row0 += step, stage ^= 1) {
+    float v[R][8], u[R][8];
+    float2 sa[R] = {}, sb[R] = {};
+    fetch_wait();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = x[i];
-      u[i] = b[i];
+    for (int k = 0; k < R; ++k) {
+      const bool live = ok && row0 + group + k * groups < p.n;
+      Eight<T> x, b;
+      x.zero();
+      b.zero();
+      if (live) {
+        x.load(slot(stage, 0, k));
+        if (p.b) b.load(slot(stage, 1, k));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[k][i] = x[i];
+        u[k][i] = b[i];
+      }
     }
-    float2 sa{}, sb{};
+    if (row0 + step < p.n) fetch_rows(row0 + step, stage ^ 1);
     if (p.after) {
-      sa = row_stats<LAYER>(u, ok, p, s_sum, turn);
+      row_stats<LAYER, R>(u, ok, p, s_sum, turn, sa);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        u[i] = (u[i] - sa.x) * sa.y;
-        if (p.w_after) u[i] *= wa[i];
-        if (p.c_after) u[i] += ca[i];
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          u[k][i] = (u[k][i] - sa[k].x) * sa[k].y;
+          if (p.w_after) u[k][i] *= wa[i];
+          if (p.c_after) u[k][i] += ca[i];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const long long row = row0 + group + k * groups;
+      if (!ok || row >= p.n) continue;  // (columns and rows that there are not stay zero)
+      if (p.b) {
+        Eight<T> g;
+        if (p.gate) g.load(p.gate, row / p.per * p.d + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = fmaf(p.gate ? p.scale * g[i] : p.scale, u[k][i], v[k][i]);
       }
+      Eight<T>::store(p.r, row * p.d + col, v[k]);
     }
-    if (live && p.b) {  // (columns that there are not stay zero)
+    if (p.before) row_stats<LAYER, R>(v, ok, p, s_sum, turn, sb);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fmaf(p.gate ? p.scale * g[i] : p.scale, u[i], v[i]);
-    }
-    if (live) Eight<T>::store(p.r, at, v);
-    if (p.before) {
-      sb = row_stats<LAYER>(v, ok, p, s_sum, turn);
+    for (int k = 0; k < R; ++k) {
+      const long long row = row0 + group + k * groups;
+      if (!ok || row >= p.n) continue;
+      if (p.before) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = (v[i] - sb.x) * sb.y;
-        if (p.w_before) v[i] *= wb[i];
-        if (p.c_before) v[i] += cb[i];
+        for (int i = 0; i < 8; ++i) {
+          v[k][i] = (v[k][i] - sb[k].x) * sb[k].y;
+          if (p.w_before) v[k][i] *= wb[i];
+          if (p.c_before) v[k][i] += cb[i];
+        }
+        Eight<T>::store(p.out, row * p.d + col, v[k]);
       }
-      if (live) Eight<T>::store(p.out, at, v);
-    }
-    if (p.stats && live && t == 0) {
-      float2* st = reinterpret_cast<float2*>(p.stats + row);
-      if (p.after) st[0] = sa;
-      if (p.before) st[1] = sb;
+      if (p.stats && t == 0) {
+        float2* st = reinterpret_cast<float2*>(p.stats + row);
+        if (p.after) st[0] = sa[k];
+        if (p.before) st[1] = sb[k];
+      }
     }
   }
 }
@@ -186,16 +253,57 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
 // and keeps the sums over its tokens of the weights' gradients, a column's in the
 // registers of the thread that has the column.  SHIFT: those of the shifts too.
 enum { S_WB = 0, S_CB = 1, S_WA = 2, S_CA = 3 };
+enum { A_DR = 0, A_DOUT = 1, A_R = 2, A_B = 3, A_GATE = 4 };  // slots; the last with a gate for each token
+// Rows of a row group at a time, and whether the next ones fit beside them.
+template <typename T, int MAX_THREADS>
+struct Back {
+  static constexpr int R = sizeof(T) == 2 && MAX_THREADS == 512 ? 2 : 1, STAGES = sizeof(T) == 4 && MAX_THREADS == 1024 ? 1 : 2;
+  static int smem(int threads, bool gate_each) { return STAGES * (gate_each ? 5 : 4) * R * slots<T>(threads) * 16; }
+};
 template <typename T, bool LAYER, bool SHIFT, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_sum[2][32][2];
-  extern __shared__ float s_cols[];  // [rows of a block][tpr * 8]
+  using B = Back<T, MAX_THREADS>;
+  constexpr int R = B::R;
+  __shared__ float s_sum[2][32][2 * R];
+  extern __shared__ uint4 s_slots[];  // [STAGES][arrays][R] of slots; at the end [threads][8] floats
   grid_dep_wait();
   grid_dep_launch();
-  const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, rows = blockDim.x / p.tpr;
-  int turn = 0;
+  const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
   const long long col = 8ll * t;
   const bool ok = col < p.d;
+  const int arrays = p.gate_each ? 5 : 4;
+  int turn = 0, stage = 0;
+  auto slot = [&](int st, int array, int k) { return s_slots + ((st * arrays + array) * R + k) * slots<T>(blockDim.x) + threadIdx.x; };
+  // Rows of the block's units, a few at a time.
+  struct Place {
+    long long unit, row, to;
+  };
+  auto enter = [&](Place& at) {
+    if (at.unit >= p.units) return;
+    const long long gi = at.unit / p.chunks, c = at.unit - gi * p.chunks;
+    at.row = gi * p.per + c * p.per / p.chunks;
+    at.to = gi * p.per + (c + 1) * p.per / p.chunks;
+  };
+  auto fetch_rows = [&](const Place& at, int st) {
+    if (at.unit < p.units) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const long long row = at.row + group + k * groups, from = row * p.d + col;
+        if (!ok || row >= at.to) continue;
+        if (p.dr) fetch<T>(slot(st, A_DR, k), p.dr, from);
+        if (p.before) {
+          fetch<T>(slot(st, A_DOUT, k), p.dout, from);
+          fetch<T>(slot(st, A_R, k), p.r, from);
+        }
+        if (p.b) fetch<T>(slot(st, A_B, k), p.b, from);
+        if (p.gate_each) fetch<T>(slot(st, A_GATE, k), p.gate, from);
+      }
+    }
+    fetch_commit();
+  };
+  Place here{blockIdx.x, 0, 0};
+  enter(here);
+  if (B::STAGES == 2) fetch_rows(here, 0);
   Eight<T> wa, ca, wb, gate;
   wa.zero();
   ca.zero();
@@ -204,113 +312,150 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
   if (ok && p.w_after) wa.load(p.w_after, col);
   if (ok && p.c_after) ca.load(p.c_after, col);
   if (ok && p.w_before) wb.load(p.w_before, col);
+  if (ok && p.gate && !p.gate_each && here.unit < p.units) gate.load(p.gate, here.unit / p.chunks * p.d + col);
   float sums[4][8] = {}, gsum[8] = {};
   // A column sum over the block's row groups, then to `write`.
-  auto flush = [&](float (&a)[8], auto&& write) {
-    if (rows > 1) {
+  auto flush = [&](float (&a)[8], float* s_cols, auto&& write) {
+    if (groups > 1) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 8; ++i) s_cols[threadIdx.x * 8 + i] = a[i];
       __syncthreads();
       if (group == 0)
-        for (int g = 1; g < rows; ++g)
+        for (int g = 1; g < groups; ++g)
 #pragma unroll
           for (int i = 0; i < 8; ++i) a[i] += s_cols[(g * p.tpr + t) * 8 + i];
     }
     if (group == 0 && ok) write(a);
   };
+  float* s_cols = reinterpret_cast<float*>(s_slots + B::STAGES * arrays * R * slots<T>(blockDim.x));
   auto to_floats = [](float* at, const float (&a)[8]) {
     reinterpret_cast<float4*>(at)[0] = make_float4(a[0], a[1], a[2], a[3]);
     reinterpret_cast<float4*>(at)[1] = make_float4(a[4], a[5], a[6], a[7]);
   };
-  for (long long unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
-    const long long gi = unit / p.chunks, c = unit - gi * p.chunks;
-    const long long from = gi * p.per + c * p.per / p.chunks, to = gi * p.per + (c + 1) * p.per / p.chunks;
-    if (ok && p.gate && !p.gate_each) gate.load(p.gate, gi * p.d + col);
-    for (long long row0 = from; row0 < to; row0 += rows) {
-      const long long row = row0 + group, at = row * p.d + col;
-      const bool live = ok && row < to;
-      Eight<T> b, r, dout, dr;
-      b.zero();
-      r.zero();
-      dout.zero();
-      dr.zero();
-      float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (live) {
-        if (p.before) {
-          dout.load(p.dout, at);
-          r.load(p.r, at);
-        }
-        if (p.b) b.load(p.b, at);
-        if (p.dr) dr.load(p.dr, at);
-        if (p.gate_each) gate.load(p.gate, at);
-        if (p.stats) st = p.stats[row];
-      }
-      float g[8];
+  while (here.unit < p.units) {
+    Place next = here;
+    next.row += groups * R;
+    const bool ends = next.row >= next.to;
+    if (ends) {
+      next.unit += gridDim.x;
+      enter(next);
+    }
+    if (B::STAGES == 1) fetch_rows(here, 0);
+    fetch_wait();
+    if (B::STAGES == 2) fetch_rows(next, stage ^ 1);
+    float g[R][8], s[2 * R];
+    float4 st[R];
+    bool live[R];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = dr[i];
-      if (p.before) {
-        float s[2] = {0.f, 0.f};
+    for (int k = 0; k < R; ++k) {
+      const long long row = here.row + group + k * groups;
+      live[k] = ok && row < here.to;
+      st[k] = live[k] && p.stats ? p.stats[row] : make_float4(0.f, 0.f, 0.f, 0.f);
+      Eight<T> dr;
+      dr.zero();
+      if (live[k] && p.dr) dr.load(slot(stage, A_DR, k));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[k][i] = dr[i];
+      s[2 * k] = s[2 * k + 1] = 0.f;
+    }
+    if (p.before) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (!live[k]) continue;
+        Eight<T> r, dout;
+        r.load(slot(stage, A_R, k));
+        dout.load(slot(stage, A_DOUT, k));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float y = (r[i] - st.z) * st.w, d = dout[i], dy = p.w_before ? d * wb[i] : d;
-          s[0] = fmaf(dy, y, s[0]);
-          s[1] += dy;
+          const float y = (r[i] - st[k].z) * st[k].w, d = dout[i], dy = p.w_before ? d * wb[i] : d;
+          s[2 * k] = fmaf(dy, y, s[2 * k]);
+          s[2 * k + 1] += dy;
           sums[S_WB][i] = fmaf(d, y, sums[S_WB][i]);
           if (SHIFT) sums[S_CB][i] += d;
         }
-        row_sums<2>(s, p.tpr, s_sum, turn);
-        const float m1 = s[0] * p.inv_d, m0 = LAYER ? s[1] * p.inv_d : 0.f;
+      }
+      row_sums<2 * R>(s, p.tpr, s_sum, turn);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (!live[k]) continue;
+        const float m1 = s[2 * k] * p.inv_d, m0 = LAYER ? s[2 * k + 1] * p.inv_d : 0.f;
+        Eight<T> r, dout;
+        r.load(slot(stage, A_R, k));
+        dout.load(slot(stage, A_DOUT, k));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float y = (r[i] - st.z) * st.w, d = dout[i], dy = p.w_before ? d * wb[i] : d;
-          g[i] = fmaf(st.w, dy - fmaf(y, m1, m0), g[i]);
+          const float y = (r[i] - st[k].z) * st[k].w, d = dout[i], dy = p.w_before ? d * wb[i] : d;
+          g[k][i] = fmaf(st[k].w, dy - fmaf(y, m1, m0), g[k][i]);
         }
       }
-      if (p.dx && live) Eight<T>::store(p.dx, at, g);
-      if (!p.b && !p.db) continue;  // (of all threads)
-      float s[2] = {0.f, 0.f};
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const long long at = (here.row + group + k * groups) * p.d + col;
+      s[2 * k] = s[2 * k + 1] = 0.f;
+      if (!live[k]) continue;
+      if (p.dx) Eight<T>::store(p.dx, at, g[k]);
+      Eight<T> b, ge = gate;
+      b.zero();
+      if (p.b) b.load(slot(stage, A_B, k));
+      if (p.gate_each) ge.load(slot(stage, A_GATE, k));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float y = p.after ? (b[i] - st.x) * st.y : b[i], sg = live ? p.scale * g[i] : 0.f;
+        const float y = p.after ? (b[i] - st[k].x) * st[k].y : b[i], sg = p.scale * g[k][i];
         if (p.dgate) {
           const float dg = sg * fmaf(y, p.w_after ? wa[i] : 1.f, ca[i]);
           gsum[i] = p.gate_each ? dg : gsum[i] + dg;
         }
-        float du = p.gate ? sg * gate[i] : sg;
+        float du = p.gate ? sg * ge[i] : sg;
         if (p.after) {
           sums[S_WA][i] = fmaf(du, y, sums[S_WA][i]);
           if (SHIFT) sums[S_CA][i] += du;
           if (p.w_after) du *= wa[i];
-          s[0] = fmaf(du, y, s[0]);
-          s[1] += du;
+          s[2 * k] = fmaf(du, y, s[2 * k]);
+          s[2 * k + 1] += du;
         }
-        g[i] = du;
+        g[k][i] = du;
       }
-      if (p.gate_each && p.dgate && live) Eight<T>::store(p.dgate, at, gsum);
-      if (p.after) {
-        row_sums<2>(s, p.tpr, s_sum, turn);
-        const float m1 = s[0] * p.inv_d, m0 = LAYER ? s[1] * p.inv_d : 0.f;
+      if (p.gate_each && p.dgate) Eight<T>::store(p.dgate, at, gsum);
+    }
+    if (p.after) {
+      row_sums<2 * R>(s, p.tpr, s_sum, turn);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = st.y * (g[i] - fmaf((b[i] - st.x) * st.y, m1, m0));
+      for (int k = 0; k < R; ++k) {
+        if (!live[k]) continue;
+        const float m1 = s[2 * k] * p.inv_d, m0 = LAYER ? s[2 * k + 1] * p.inv_d : 0.f;
+        Eight<T> b;
+        b.load(slot(stage, A_B, k));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[k][i] = st[k].y * (g[k][i] - fmaf((b[i] - st[k].x) * st[k].y, m1, m0));
       }
-      if (p.db && live) Eight<T>::store(p.db, at, g);
     }
-    if (p.dgate && !p.gate_each) {
-      flush(gsum, [&](const float (&a)[8]) {
-        if (p.chunks == 1)
-          Eight<T>::store(p.dgate, gi * p.d + col, a);
-        else
-          to_floats(p.gate_sums + unit * p.d + col, a);
-      });
+    if (p.db)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) gsum[i] = 0.f;
+      for (int k = 0; k < R; ++k)
+        if (live[k]) Eight<T>::store(p.db, (here.row + group + k * groups) * p.d + col, g[k]);
+    if (ends && p.gate && !p.gate_each) {
+      const long long gi = here.unit / p.chunks;
+      if (p.dgate) {
+        flush(gsum, s_cols, [&](const float (&a)[8]) {
+          if (p.chunks == 1)
+            Eight<T>::store(p.dgate, gi * p.d + col, a);
+          else
+            to_floats(p.gate_sums + here.unit * p.d + col, a);
+        });
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gsum[i] = 0.f;
+      }
+      if (ok && next.unit < p.units) gate.load(p.gate, next.unit / p.chunks * p.d + col);
     }
+    here = next;
+    if (B::STAGES == 2) stage ^= 1;
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     if (p.want_sums >> k & 1)
-      flush(sums[k], [&](const float (&a)[8]) {
+      flush(sums[k], s_cols, [&](const float (&a)[8]) {
         to_floats(p.sums + (static_cast<long long>(k) * gridDim.x + blockIdx.x) * p.d + col, a);
       });
 }
@@ -375,16 +520,16 @@ void launch_dep(void (*kern)(KArgs...), dim3 grid, int block, int smem, cudaStre
 }
 int launched() { return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA; }
 
-// Threads to a row, rows and threads of a block.
+// Threads to a row, row groups and threads of a block.
 struct Shape {
-  int tpr, rows, threads;
+  int tpr, groups, threads;
 };
 Shape shape_of(int64_t d, int64_t n, int num_sms) {
   Shape s;
   s.tpr = static_cast<int>((d / 8 + 31) / 32 * 32);
-  s.rows = std::max(512 / s.tpr, 1);
-  while (s.rows > 1 && (n + s.rows - 1) / s.rows < num_sms) s.rows /= 2;  // few tokens: on all SMs
-  s.threads = s.rows * s.tpr;
+  s.groups = std::max(512 / s.tpr, 1);
+  while (s.groups > 1 && (n + s.groups - 1) / s.groups < num_sms) s.groups /= 2;  // few tokens: on all SMs
+  s.threads = s.groups * s.tpr;
   return s;
 }
 
@@ -400,7 +545,7 @@ Plan plan_of(const NormSpec& a, int num_sms) {
   p.per = a.n / p.gates;
   const Shape s = shape_of(a.d, a.n, num_sms);
   const int64_t most = num_sms * std::max(1, 512 / s.threads);
-  p.chunks = std::min<int64_t>(std::max<int64_t>(most / p.gates, 1), (p.per + s.rows - 1) / s.rows);
+  p.chunks = std::min<int64_t>(std::max<int64_t>(most / p.gates, 1), (p.per + s.groups - 1) / s.groups);
   p.units = p.gates * p.chunks;
   p.blocks = std::min<int64_t>(p.units, most);
   return p;
@@ -427,25 +572,48 @@ NormParams params_of(const NormSpec& a, const Shape& s) {
   return p;
 }
 
+// Raises a kernel's shared-memory limit, once for a device.
+template <auto KERNEL>
+int allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TP_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (bytes > 48 * 1024 && !(done.load() & bit)) {
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess) return TP_ERR_CUDA;
+    done.fetch_or(bit);
+  }
+  return TP_OK;
+}
+
+template <typename T, bool LAYER, int R>
+int launch_forward_inst(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
+  const int smem = 2 * 2 * R * slots<T>(s.threads) * 16, rows = s.groups * R;
+  if (int rc = allow_smem<forward_kernel<T, LAYER, R>>(smem)) return rc;
+  const int64_t blocks = (p.n + rows - 1) / rows, most = static_cast<int64_t>(num_sms) * std::max(1, 1024 / s.threads);
+  launch_dep(forward_kernel<T, LAYER, R>, dim3(static_cast<unsigned>(std::min(blocks, most))), s.threads, smem, st, p);
+  return launched();
+}
+// Two rows to a thread at a time where there are enough for all SMs.
 template <typename T, bool LAYER>
-void launch_forward(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
-  launch_dep(forward_kernel<T, LAYER>, dim3(grid), s.threads, 0, st, p);
+int launch_forward(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
+  if (p.n >= 4ll * num_sms * s.groups && s.threads <= 512) return launch_forward_inst<T, LAYER, 2>(p, s, num_sms, st);
+  return launch_forward_inst<T, LAYER, 1>(p, s, num_sms, st);
+}
+template <typename T, bool LAYER, bool SHIFT, int MAX_THREADS>
+int launch_backward_inst(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
+  const int smem = Back<T, MAX_THREADS>::smem(s.threads, p.gate_each) + (s.groups > 1 ? s.threads * 32 : 0);
+  if (int rc = allow_smem<backward_kernel<T, LAYER, SHIFT, MAX_THREADS>>(smem)) return rc;
+  launch_dep(backward_kernel<T, LAYER, SHIFT, MAX_THREADS>, dim3(grid), s.threads, smem, st, p);
+  return launched();
 }
 // Up to 512 threads a thread may have 128 registers, which the sums need.
-template <typename T, bool LAYER, bool SHIFT>
-void launch_backward_inst(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
-  const int smem = s.rows > 1 ? s.threads * 8 * 4 : 0;
-  if (s.threads <= 512)
-    launch_dep(backward_kernel<T, LAYER, SHIFT, 512>, dim3(grid), s.threads, smem, st, p);
-  else
-    launch_dep(backward_kernel<T, LAYER, SHIFT, 1024>, dim3(grid), s.threads, smem, st, p);
-}
 template <typename T, bool LAYER>
-void launch_backward(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
-  if (p.want_sums & (1 << S_CB | 1 << S_CA))
-    launch_backward_inst<T, LAYER, true>(p, s, grid, st);
-  else
-    launch_backward_inst<T, LAYER, false>(p, s, grid, st);
+int launch_backward(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
+  const bool shift = p.want_sums & (1 << S_CB | 1 << S_CA);
+  if (s.threads <= 512)
+    return shift ? launch_backward_inst<T, LAYER, true, 512>(p, s, grid, st) : launch_backward_inst<T, LAYER, false, 512>(p, s, grid, st);
+  return shift ? launch_backward_inst<T, LAYER, true, 1024>(p, s, grid, st) : launch_backward_inst<T, LAYER, false, 1024>(p, s, grid, st);
 }
 }  // namespace norm
 
@@ -456,13 +624,8 @@ int launch_norm_fwd(const NormSpec& a, int num_sms, cudaStream_t st) {
   p.x = a.x;
   p.r = a.r;
   p.out = a.out;
-  const int64_t blocks = (a.n + s.rows - 1) / s.rows, most = static_cast<int64_t>(num_sms) * std::max(1, 2048 / s.threads);
-  const unsigned grid = static_cast<unsigned>(std::min(blocks, most));
-  if (a.f32)
-    a.layer ? launch_forward<float, true>(p, s, grid, st) : launch_forward<float, false>(p, s, grid, st);
-  else
-    a.layer ? launch_forward<__nv_bfloat16, true>(p, s, grid, st) : launch_forward<__nv_bfloat16, false>(p, s, grid, st);
-  return launched();
+  if (a.f32) return a.layer ? launch_forward<float, true>(p, s, num_sms, st) : launch_forward<float, false>(p, s, num_sms, st);
+  return a.layer ? launch_forward<__nv_bfloat16, true>(p, s, num_sms, st) : launch_forward<__nv_bfloat16, false>(p, s, num_sms, st);
 }
 
 size_t norm_workspace_bytes(const NormSpec& a, int num_sms) {
@@ -496,10 +659,10 @@ int launch_norm_bwd(const NormSpec& a, void* workspace, int num_sms, cudaStream_
     q.parts[k] = c.blocks;
   }
   const unsigned grid = static_cast<unsigned>(c.blocks);
-  if (a.f32)
-    a.layer ? launch_backward<float, true>(p, s, grid, st) : launch_backward<float, false>(p, s, grid, st);
-  else
-    a.layer ? launch_backward<__nv_bfloat16, true>(p, s, grid, st) : launch_backward<__nv_bfloat16, false>(p, s, grid, st);
+  const int rc = a.f32 ? (a.layer ? launch_backward<float, true>(p, s, grid, st) : launch_backward<float, false>(p, s, grid, st))
+                       : (a.layer ? launch_backward<__nv_bfloat16, true>(p, s, grid, st)
+                                  : launch_backward<__nv_bfloat16, false>(p, s, grid, st));
+  if (rc) return rc;
   q.d = a.d;
   if (a.dgate && !c.each && c.chunks > 1) {
     q.from[4] = p.gate_sums;
