@@ -22,49 +22,94 @@ namespace norm {
 using tc::grid_dep_launch;
 using tc::grid_dep_wait;
 
-// Eight columns of a row.
+// Pairs of 32-bit numbers, two operations to an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float total(uint64_t v) {
+  const float2 r = halves(v);
+  return r.x + r.y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Eight columns of a row, as four pairs.
+using Pairs = uint64_t[4];
+__device__ __forceinline__ void fill(Pairs& a, float v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = both(v);
+}
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const void* p, long long at) { v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at); }
-  __device__ __forceinline__ void load(const uint4* slot) { v = slot[0]; }
-  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ float operator[](int i) const {
-    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
-    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  static __device__ __forceinline__ void open(Pairs& a, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ void store(void* p, long long at, const float (&a)[8]) {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
-        make_uint4(tc::pack_bf16x2(a[0], a[1]), tc::pack_bf16x2(a[2], a[3]), tc::pack_bf16x2(a[4], a[5]), tc::pack_bf16x2(a[6], a[7]));
+  static __device__ __forceinline__ void load(Pairs& a, const void* p, long long at) {
+    open(a, *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+  }
+  static __device__ __forceinline__ void load(Pairs& a, const uint4* slot) { open(a, slot[0]); }
+  static __device__ __forceinline__ void store(void* p, long long at, const Pairs& a) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = halves(a[i]);
+      w[i] = tc::pack_bf16x2(v.x, v.y);
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
 struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p, long long at) {
-    a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
+  static __device__ __forceinline__ void open(Pairs& a, float4 v, float4 w) {
+    a[0] = pair(v.x, v.y);
+    a[1] = pair(v.z, v.w);
+    a[2] = pair(w.x, w.y);
+    a[3] = pair(w.z, w.w);
   }
-  __device__ __forceinline__ void load(const uint4* slot) {
-    a = *reinterpret_cast<const float4*>(slot);
-    b = *reinterpret_cast<const float4*>(slot + blockDim.x);
+  static __device__ __forceinline__ void load(Pairs& a, const void* p, long long at) {
+    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    open(a, src[0], src[1]);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ float operator[](int i) const {
-    return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+  static __device__ __forceinline__ void load(Pairs& a, const uint4* slot) {
+    open(a, *reinterpret_cast<const float4*>(slot), *reinterpret_cast<const float4*>(slot + blockDim.x));
   }
-  static __device__ __forceinline__ void store(void* p, long long at, const float (&v)[8]) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  static __device__ __forceinline__ void store(void* p, long long at, const Pairs& a) {
+    float4* to = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    const float2 v = halves(a[0]), w = halves(a[1]), x = halves(a[2]), y = halves(a[3]);
+    to[0] = make_float4(v.x, v.y, w.x, w.y);
+    to[1] = make_float4(x.x, x.y, y.x, y.y);
   }
 };
 
 // A row belongs to `tpr` threads, a multiple of 32, thread t of them having the
-// columns 8 t .. 8 t + 7; a block has blockDim / tpr row groups with R rows each.
-// A thread copies its columns of the next rows into slots of its own in shared memory
-// while it works on these: it waits for nobody, and no registers are held for them.
+// columns 8 t .. 8 t + 7; a block has blockDim / tpr row groups.  A thread copies its
+// columns of the next row into slots of its own in shared memory while it works on
+// this one: it waits for nobody, and no registers are held for them.
 struct NormParams {
   long long n, d, per;  // per: tokens of a gate
   int tpr, after, before;
@@ -109,142 +154,124 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (*s)[32][
 #pragma unroll
     for (int d = 16; d; d >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
   if (tpr == 32) return;
-  const int warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp / warps * warps;
-  if ((threadIdx.x & 31) == 0)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tpr >> 5, first = warp / warps * warps;
+  if (lane == 0)
 #pragma unroll
     for (int k = 0; k < N; ++k) s[turn][warp][k] = v[k];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = 0.f;
-#pragma unroll 8
-  for (int w = 0; w < warps; ++w)
+  for (int k = 0; k < N; ++k) {
+    v[k] = lane < warps ? s[turn][first + lane][k] : 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += s[turn][first + w][k];
+    for (int d = 16; d; d >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+  }
   turn ^= 1;
 }
 
-// The mean and factor of R rows' norms.
-template <bool LAYER, int R>
-__device__ __forceinline__ void row_stats(const float (&v)[R][8], bool ok, const NormParams& p, float (*s)[32][R], int& turn,
-                                          float2 (&st)[R]) {
-  float sum[R] = {};
-#pragma unroll
-  for (int k = 0; k < R; ++k) st[k].x = 0.f;
+// The mean and factor of a row's norm.
+template <bool LAYER>
+__device__ __forceinline__ float2 row_stats(const Pairs& v, bool ok, const NormParams& p, float (*s)[32][1], int& turn) {
+  float2 st = make_float2(0.f, 0.f);
+  float sum[1];
   if (LAYER) {
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[k] += v[k][i];
-    row_sums<R>(sum, p.tpr, s, turn);
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      st[k].x = sum[k] * p.inv_d;
-      sum[k] = 0.f;
-    }
+    sum[0] = total(add2(add2(v[0], v[1]), add2(v[2], v[3])));
+    row_sums<1>(sum, p.tpr, s, turn);
+    st.x = sum[0] * p.inv_d;
   }
+  uint64_t q = 0;
 #pragma unroll
-  for (int k = 0; k < R; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = ok ? v[k][i] - st[k].x : 0.f;
-      sum[k] = fmaf(a, a, sum[k]);
-    }
-  row_sums<R>(sum, p.tpr, s, turn);
-#pragma unroll
-  for (int k = 0; k < R; ++k) st[k].y = 1.f / sqrtf(fmaf(sum[k], p.inv_d, p.eps));
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t a = LAYER ? add2(v[i], both(-st.x)) : v[i];
+    q = fma2(a, a, q);
+  }
+  sum[0] = ok ? total(q) : 0.f;
+  row_sums<1>(sum, p.tpr, s, turn);
+  st.y = 1.f / sqrtf(fmaf(sum[0], p.inv_d, p.eps));
+  return st;
+}
+// (v - mean) * factor
+template <bool LAYER>
+__device__ __forceinline__ uint64_t unit(uint64_t v, uint64_t mean, uint64_t factor) {
+  return mul2(LAYER ? add2(v, mean) : v, factor);  // (mean: its negative)
 }
 
-template <typename T, bool LAYER, int R>
-__global__ void __launch_bounds__(R == 2 ? 512 : 1024) forward_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_sum[2][32][R];
-  extern __shared__ uint4 s_slots[];  // [2][x, b][R] of slots
+// SHIFT: there are shifts.
+template <typename T, bool LAYER, bool SHIFT>
+__global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s_sum[2][32][1];
+  extern __shared__ uint4 s_slots[];  // [2][x, b] of slots
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
-  const long long col = 8ll * t, step = static_cast<long long>(gridDim.x) * groups * R;
+  const long long col = 8ll * t, step = static_cast<long long>(gridDim.x) * groups;
   const bool ok = col < p.d;
   int turn = 0, stage = 0;
-  auto slot = [&](int st, int array, int k) { return s_slots + ((st * 2 + array) * R + k) * slots<T>(blockDim.x) + threadIdx.x; };
-  auto fetch_rows = [&](long long row0, int st) {
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const long long row = row0 + group + k * groups;
-      if (!ok || row >= p.n) continue;
-      fetch<T>(slot(st, 0, k), p.x, row * p.d + col);
-      if (p.b) fetch<T>(slot(st, 1, k), p.b, row * p.d + col);
+  auto slot = [&](int st, int array) { return s_slots + (st * 2 + array) * slots<T>(blockDim.x) + threadIdx.x; };
+  auto fetch_row = [&](long long row, int st) {
+    if (ok && row < p.n) {
+      fetch<T>(slot(st, 0), p.x, row * p.d + col);
+      if (p.b) fetch<T>(slot(st, 1), p.b, row * p.d + col);
     }
     fetch_commit();
   };
-  long long row0 = static_cast<long long>(blockIdx.x) * groups * R;
-  fetch_rows(row0, 0);
-  Eight<T> wa, ca, wb, cb;
-  if (ok && p.w_after) wa.load(p.w_after, col);
-  if (ok && p.c_after) ca.load(p.c_after, col);
-  if (ok && p.w_before) wb.load(p.w_before, col);
-  if (ok && p.c_before) cb.load(p.c_before, col);
-  for (; row0 < p.n; row0 += step, stage ^= 1) {
-    float v[R][8], u[R][8];
-    float2 sa[R] = {}, sb[R] = {};
+  long long row = static_cast<long long>(blockIdx.x) * groups + group, gate_at = -1;
+  fetch_row(row, 0);
+  Pairs k1, k0, w, c;  // scale gate w_after, scale gate c_after, w_before, c_before
+  fill(k1, 0.f);
+  fill(k0, 0.f);
+  fill(w, 1.f);
+  fill(c, 0.f);
+  if (ok && p.w_before) Eight<T>::load(w, p.w_before, col);
+  if (SHIFT && ok && p.c_before) Eight<T>::load(c, p.c_before, col);
+  for (long long row0 = row - group; row0 < p.n; row0 += step, row += step, stage ^= 1) {
+    const bool live = ok && row < p.n;
+    if (p.b && live && gate_at != (p.gate ? row / p.per : 0)) {
+      gate_at = p.gate ? row / p.per : 0;
+      fill(k1, 1.f);
+      if (p.gate) Eight<T>::load(k1, p.gate, gate_at * p.d + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k1[i] = mul2(k1[i], both(p.scale));
+      if (SHIFT && p.c_after) {
+        Eight<T>::load(k0, p.c_after, col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k0[i] = mul2(k0[i], k1[i]);
+      }
+      if (p.w_after) {
+        Pairs wa;
+        Eight<T>::load(wa, p.w_after, col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k1[i] = mul2(k1[i], wa[i]);
+      }
+    }
+    Pairs v, u;
+    fill(v, 0.f);
+    fill(u, 0.f);
     fetch_wait();
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const bool live = ok && row0 + group + k * groups < p.n;
-      Eight<T> x, b;
-      x.zero();
-      b.zero();
-      if (live) {
-        x.load(slot(stage, 0, k));
-        if (p.b) b.load(slot(stage, 1, k));
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[k][i] = x[i];
-        u[k][i] = b[i];
-      }
+    if (live) {
+      Eight<T>::load(v, slot(stage, 0));
+      if (p.b) Eight<T>::load(u, slot(stage, 1));
     }
-    if (row0 + step < p.n) fetch_rows(row0 + step, stage ^ 1);
-    if (p.after) {
-      row_stats<LAYER, R>(u, ok, p, s_sum, turn, sa);
+    fetch_row(row + step, stage ^ 1);
+    float2 sa = make_float2(0.f, 1.f), sb = make_float2(0.f, 0.f);
+    if (p.after) sa = row_stats<LAYER>(u, ok, p, s_sum, turn);
+    if (live && p.b) {  // (columns and rows that there are not stay zero)
 #pragma unroll
-      for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          u[k][i] = (u[k][i] - sa[k].x) * sa[k].y;
-          if (p.w_after) u[k][i] *= wa[i];
-          if (p.c_after) u[k][i] += ca[i];
-        }
+      for (int i = 0; i < 4; ++i) v[i] = fma2(unit<LAYER>(u[i], both(-sa.x), both(sa.y)), k1[i], SHIFT ? add2(v[i], k0[i]) : v[i]);
     }
+    if (live) Eight<T>::store(p.r, row * p.d + col, v);
+    if (p.before) {
+      sb = row_stats<LAYER>(v, ok, p, s_sum, turn);
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const long long row = row0 + group + k * groups;
-      if (!ok || row >= p.n) continue;  // (columns and rows that there are not stay zero)
-      if (p.b) {
-        Eight<T> g;
-        if (p.gate) g.load(p.gate, row / p.per * p.d + col);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = fmaf(p.gate ? p.scale * g[i] : p.scale, u[k][i], v[k][i]);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t y = unit<LAYER>(v[i], both(-sb.x), both(sb.y));
+        v[i] = SHIFT ? fma2(y, w[i], c[i]) : mul2(y, w[i]);
       }
-      Eight<T>::store(p.r, row * p.d + col, v[k]);
+      if (live) Eight<T>::store(p.out, row * p.d + col, v);
     }
-    if (p.before) row_stats<LAYER, R>(v, ok, p, s_sum, turn, sb);
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const long long row = row0 + group + k * groups;
-      if (!ok || row >= p.n) continue;
-      if (p.before) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[k][i] = (v[k][i] - sb[k].x) * sb[k].y;
-          if (p.w_before) v[k][i] *= wb[i];
-          if (p.c_before) v[k][i] += cb[i];
-        }
-        Eight<T>::store(p.out, row * p.d + col, v[k]);
-      }
-      if (p.stats && t == 0) {
-        float2* st = reinterpret_cast<float2*>(p.stats + row);
-        if (p.after) st[0] = sa[k];
-        if (p.before) st[1] = sb[k];
-      }
+    if (p.stats && live && t == 0) {
+      float2* st = reinterpret_cast<float2*>(p.stats + row);
+      if (p.after) st[0] = sa;
+      if (p.before) st[1] = sb;
     }
   }
 }
@@ -254,18 +281,18 @@ __global__ void __launch_bounds__(R == 2 ? 512 : 1024) forward_kernel(const __gr
 // registers of the thread that has the column.  SHIFT: those of the shifts too.
 enum { S_WB = 0, S_CB = 1, S_WA = 2, S_CA = 3 };
 enum { A_DR = 0, A_DOUT = 1, A_R = 2, A_B = 3, A_GATE = 4 };  // slots; the last with a gate for each token
-// Rows of a row group at a time, and whether the next ones fit beside them.
+// Whether the next rows' slots fit beside these.
 template <typename T, int MAX_THREADS>
 struct Back {
-  static constexpr int R = sizeof(T) == 2 && MAX_THREADS == 512 ? 2 : 1, STAGES = sizeof(T) == 4 && MAX_THREADS == 1024 ? 1 : 2;
-  static int smem(int threads, bool gate_each) { return STAGES * (gate_each ? 5 : 4) * R * slots<T>(threads) * 16; }
+  static constexpr int STAGES = sizeof(T) == 4 && MAX_THREADS == 1024 ? 1 : 2;
+  static int smem(int threads, bool gate_each) { return STAGES * (gate_each ? 5 : 4) * slots<T>(threads) * 16; }
 };
 template <typename T, bool LAYER, bool SHIFT, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_constant__ NormParams p) {
   using B = Back<T, MAX_THREADS>;
-  constexpr int R = B::R;
-  __shared__ float s_sum[2][32][2 * R];
-  extern __shared__ uint4 s_slots[];  // [STAGES][arrays][R] of slots; at the end [threads][8] floats
+  constexpr int N = LAYER ? 2 : 1;  // sums of a row
+  __shared__ float s_sum[2][32][N];
+  extern __shared__ uint4 s_slots[];  // [STAGES][arrays] of slots; at the end [threads][8] floats
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
@@ -273,8 +300,8 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
   const bool ok = col < p.d;
   const int arrays = p.gate_each ? 5 : 4;
   int turn = 0, stage = 0;
-  auto slot = [&](int st, int array, int k) { return s_slots + ((st * arrays + array) * R + k) * slots<T>(blockDim.x) + threadIdx.x; };
-  // Rows of the block's units, a few at a time.
+  auto slot = [&](int st, int array) { return s_slots + (st * arrays + array) * slots<T>(blockDim.x) + threadIdx.x; };
+  // Rows of the block's units, one to a row group at a time.
   struct Place {
     long long unit, row, to;
   };
@@ -284,170 +311,145 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
     at.row = gi * p.per + c * p.per / p.chunks;
     at.to = gi * p.per + (c + 1) * p.per / p.chunks;
   };
-  auto fetch_rows = [&](const Place& at, int st) {
-    if (at.unit < p.units) {
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const long long row = at.row + group + k * groups, from = row * p.d + col;
-        if (!ok || row >= at.to) continue;
-        if (p.dr) fetch<T>(slot(st, A_DR, k), p.dr, from);
-        if (p.before) {
-          fetch<T>(slot(st, A_DOUT, k), p.dout, from);
-          fetch<T>(slot(st, A_R, k), p.r, from);
-        }
-        if (p.b) fetch<T>(slot(st, A_B, k), p.b, from);
-        if (p.gate_each) fetch<T>(slot(st, A_GATE, k), p.gate, from);
+  auto fetch_row = [&](const Place& at, int st) {
+    if (ok && at.unit < p.units && at.row + group < at.to) {
+      const long long from = (at.row + group) * p.d + col;
+      if (p.dr) fetch<T>(slot(st, A_DR), p.dr, from);
+      if (p.before) {
+        fetch<T>(slot(st, A_DOUT), p.dout, from);
+        fetch<T>(slot(st, A_R), p.r, from);
       }
+      if (p.b) fetch<T>(slot(st, A_B), p.b, from);
+      if (p.gate_each) fetch<T>(slot(st, A_GATE), p.gate, from);
     }
     fetch_commit();
   };
   Place here{blockIdx.x, 0, 0};
   enter(here);
-  if (B::STAGES == 2) fetch_rows(here, 0);
-  Eight<T> wa, ca, wb, gate;
-  wa.zero();
-  ca.zero();
-  wb.zero();
-  gate.zero();
-  if (ok && p.w_after) wa.load(p.w_after, col);
-  if (ok && p.c_after) ca.load(p.c_after, col);
-  if (ok && p.w_before) wb.load(p.w_before, col);
-  if (ok && p.gate && !p.gate_each && here.unit < p.units) gate.load(p.gate, here.unit / p.chunks * p.d + col);
-  float sums[4][8] = {}, gsum[8] = {};
+  if (B::STAGES == 2) fetch_row(here, 0);
+  Pairs wa, ca, wb, gate;
+  fill(wa, 1.f);
+  fill(ca, 0.f);
+  fill(wb, 1.f);
+  fill(gate, 1.f);
+  if (ok && p.w_after) Eight<T>::load(wa, p.w_after, col);
+  if (ok && p.c_after) Eight<T>::load(ca, p.c_after, col);
+  if (ok && p.w_before) Eight<T>::load(wb, p.w_before, col);
+  if (ok && p.gate && !p.gate_each && here.unit < p.units) Eight<T>::load(gate, p.gate, here.unit / p.chunks * p.d + col);
+  Pairs sums[4] = {}, gsum = {};
   // A column sum over the block's row groups, then to `write`.
-  auto flush = [&](float (&a)[8], float* s_cols, auto&& write) {
+  auto flush = [&](Pairs& a, float* s_cols, auto&& write) {
     if (groups > 1) {
+      float4* mine = reinterpret_cast<float4*>(s_cols) + threadIdx.x * 2;
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s_cols[threadIdx.x * 8 + i] = a[i];
+      const float2 v = halves(a[0]), w = halves(a[1]), x = halves(a[2]), y = halves(a[3]);
+      mine[0] = make_float4(v.x, v.y, w.x, w.y);
+      mine[1] = make_float4(x.x, x.y, y.x, y.y);
       __syncthreads();
       if (group == 0)
-        for (int g = 1; g < groups; ++g)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] += s_cols[(g * p.tpr + t) * 8 + i];
+        for (int g = 1; g < groups; ++g) {
+          const float4 lo = mine[g * p.tpr * 2], hi = mine[g * p.tpr * 2 + 1];
+          a[0] = add2(a[0], pair(lo.x, lo.y));
+          a[1] = add2(a[1], pair(lo.z, lo.w));
+          a[2] = add2(a[2], pair(hi.x, hi.y));
+          a[3] = add2(a[3], pair(hi.z, hi.w));
+        }
     }
     if (group == 0 && ok) write(a);
   };
-  float* s_cols = reinterpret_cast<float*>(s_slots + B::STAGES * arrays * R * slots<T>(blockDim.x));
-  auto to_floats = [](float* at, const float (&a)[8]) {
-    reinterpret_cast<float4*>(at)[0] = make_float4(a[0], a[1], a[2], a[3]);
-    reinterpret_cast<float4*>(at)[1] = make_float4(a[4], a[5], a[6], a[7]);
-  };
+  float* s_cols = reinterpret_cast<float*>(s_slots + B::STAGES * arrays * slots<T>(blockDim.x));
   while (here.unit < p.units) {
     Place next = here;
-    next.row += groups * R;
+    next.row += groups;
     const bool ends = next.row >= next.to;
     if (ends) {
       next.unit += gridDim.x;
       enter(next);
     }
-    if (B::STAGES == 1) fetch_rows(here, 0);
+    if (B::STAGES == 1) fetch_row(here, 0);
+    const long long row = here.row + group, at = row * p.d + col;
+    const bool live = ok && row < here.to;
+    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live && p.stats) st = p.stats[row];
     fetch_wait();
-    if (B::STAGES == 2) fetch_rows(next, stage ^ 1);
-    float g[R][8], s[2 * R];
-    float4 st[R];
-    bool live[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const long long row = here.row + group + k * groups;
-      live[k] = ok && row < here.to;
-      st[k] = live[k] && p.stats ? p.stats[row] : make_float4(0.f, 0.f, 0.f, 0.f);
-      Eight<T> dr;
-      dr.zero();
-      if (live[k] && p.dr) dr.load(slot(stage, A_DR, k));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[k][i] = dr[i];
-      s[2 * k] = s[2 * k + 1] = 0.f;
-    }
+    if (B::STAGES == 2) fetch_row(next, stage ^ 1);
+    Pairs g;
+    fill(g, 0.f);
+    if (live && p.dr) Eight<T>::load(g, slot(stage, A_DR));
     if (p.before) {
+      Pairs y, dy;
+      fill(y, 0.f);
+      fill(dy, 0.f);
+      uint64_t s0 = 0, s1 = 0;
+      if (live) {
+        Eight<T>::load(y, slot(stage, A_R));
+        Eight<T>::load(dy, slot(stage, A_DOUT));
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if (!live[k]) continue;
-        Eight<T> r, dout;
-        r.load(slot(stage, A_R, k));
-        dout.load(slot(stage, A_DOUT, k));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = (r[i] - st[k].z) * st[k].w, d = dout[i], dy = p.w_before ? d * wb[i] : d;
-          s[2 * k] = fmaf(dy, y, s[2 * k]);
-          s[2 * k + 1] += dy;
-          sums[S_WB][i] = fmaf(d, y, sums[S_WB][i]);
-          if (SHIFT) sums[S_CB][i] += d;
+        for (int i = 0; i < 4; ++i) {
+          y[i] = unit<LAYER>(y[i], both(-st.z), both(st.w));
+          sums[S_WB][i] = fma2(dy[i], y[i], sums[S_WB][i]);
+          if (SHIFT) sums[S_CB][i] = add2(sums[S_CB][i], dy[i]);
+          dy[i] = mul2(dy[i], wb[i]);
+          s0 = fma2(dy[i], y[i], s0);
+          if (LAYER) s1 = add2(s1, dy[i]);
         }
       }
-      row_sums<2 * R>(s, p.tpr, s_sum, turn);
+      float s[N];
+      s[0] = total(s0);
+      if (LAYER) s[N - 1] = total(s1);
+      row_sums<N>(s, p.tpr, s_sum, turn);
+      const uint64_t m1 = both(-s[0] * p.inv_d), m0 = both(-s[N - 1] * p.inv_d);
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if (!live[k]) continue;
-        const float m1 = s[2 * k] * p.inv_d, m0 = LAYER ? s[2 * k + 1] * p.inv_d : 0.f;
-        Eight<T> r, dout;
-        r.load(slot(stage, A_R, k));
-        dout.load(slot(stage, A_DOUT, k));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = (r[i] - st[k].z) * st[k].w, d = dout[i], dy = p.w_before ? d * wb[i] : d;
-          g[k][i] = fmaf(st[k].w, dy - fmaf(y, m1, m0), g[k][i]);
-        }
-      }
+      for (int i = 0; i < 4; ++i) g[i] = fma2(fma2(y[i], m1, LAYER ? add2(dy[i], m0) : dy[i]), both(st.w), g[i]);
     }
+    if (p.dx && live) Eight<T>::store(p.dx, at, g);
+    if (p.b || p.db) {  // (of all threads)
+      Pairs y;
+      fill(y, 0.f);
+      uint64_t s0 = 0, s1 = 0;
+      if (live) {
+        if (p.b) Eight<T>::load(y, slot(stage, A_B));
+        if (p.gate_each) Eight<T>::load(gate, slot(stage, A_GATE));
+        if (p.after)
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const long long at = (here.row + group + k * groups) * p.d + col;
-      s[2 * k] = s[2 * k + 1] = 0.f;
-      if (!live[k]) continue;
-      if (p.dx) Eight<T>::store(p.dx, at, g[k]);
-      Eight<T> b, ge = gate;
-      b.zero();
-      if (p.b) b.load(slot(stage, A_B, k));
-      if (p.gate_each) ge.load(slot(stage, A_GATE, k));
+          for (int i = 0; i < 4; ++i) y[i] = unit<LAYER>(y[i], both(-st.x), both(st.y));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = p.after ? (b[i] - st[k].x) * st[k].y : b[i], sg = p.scale * g[k][i];
-        if (p.dgate) {
-          const float dg = sg * fmaf(y, p.w_after ? wa[i] : 1.f, ca[i]);
-          gsum[i] = p.gate_each ? dg : gsum[i] + dg;
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t sg = mul2(g[i], both(p.scale));
+          const uint64_t u = SHIFT ? fma2(y[i], wa[i], ca[i]) : mul2(y[i], wa[i]);
+          gsum[i] = p.gate_each ? mul2(sg, u) : fma2(sg, u, gsum[i]);
+          g[i] = mul2(sg, gate[i]);
+          sums[S_WA][i] = fma2(g[i], y[i], sums[S_WA][i]);
+          if (SHIFT) sums[S_CA][i] = add2(sums[S_CA][i], g[i]);
+          g[i] = mul2(g[i], wa[i]);
+          s0 = fma2(g[i], y[i], s0);
+          if (LAYER) s1 = add2(s1, g[i]);
         }
-        float du = p.gate ? sg * ge[i] : sg;
-        if (p.after) {
-          sums[S_WA][i] = fmaf(du, y, sums[S_WA][i]);
-          if (SHIFT) sums[S_CA][i] += du;
-          if (p.w_after) du *= wa[i];
-          s[2 * k] = fmaf(du, y, s[2 * k]);
-          s[2 * k + 1] += du;
-        }
-        g[k][i] = du;
+        if (p.gate_each && p.dgate) Eight<T>::store(p.dgate, at, gsum);
       }
-      if (p.gate_each && p.dgate) Eight<T>::store(p.dgate, at, gsum);
-    }
-    if (p.after) {
-      row_sums<2 * R>(s, p.tpr, s_sum, turn);
+      if (p.after) {
+        float s[N];
+        s[0] = total(s0);
+        if (LAYER) s[N - 1] = total(s1);
+        row_sums<N>(s, p.tpr, s_sum, turn);
+        const uint64_t m1 = both(-s[0] * p.inv_d), m0 = both(-s[N - 1] * p.inv_d);
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if (!live[k]) continue;
-        const float m1 = s[2 * k] * p.inv_d, m0 = LAYER ? s[2 * k + 1] * p.inv_d : 0.f;
-        Eight<T> b;
-        b.load(slot(stage, A_B, k));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[k][i] = st[k].y * (g[k][i] - fmaf((b[i] - st[k].x) * st[k].y, m1, m0));
+        for (int i = 0; i < 4; ++i) g[i] = mul2(fma2(y[i], m1, LAYER ? add2(g[i], m0) : g[i]), both(st.y));
       }
+      if (p.db && live) Eight<T>::store(p.db, at, g);
     }
-    if (p.db)
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-        if (live[k]) Eight<T>::store(p.db, (here.row + group + k * groups) * p.d + col, g[k]);
     if (ends && p.gate && !p.gate_each) {
       const long long gi = here.unit / p.chunks;
       if (p.dgate) {
-        flush(gsum, s_cols, [&](const float (&a)[8]) {
+        flush(gsum, s_cols, [&](const Pairs& a) {
           if (p.chunks == 1)
             Eight<T>::store(p.dgate, gi * p.d + col, a);
           else
-            to_floats(p.gate_sums + here.unit * p.d + col, a);
+            Eight<float>::store(p.gate_sums, here.unit * p.d + col, a);
         });
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gsum[i] = 0.f;
+        fill(gsum, 0.f);
       }
-      if (ok && next.unit < p.units) gate.load(p.gate, next.unit / p.chunks * p.d + col);
+      if (ok && next.unit < p.units) Eight<T>::load(gate, p.gate, next.unit / p.chunks * p.d + col);
     }
     here = next;
     if (B::STAGES == 2) stage ^= 1;
@@ -455,8 +457,8 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     if (p.want_sums >> k & 1)
-      flush(sums[k], s_cols, [&](const float (&a)[8]) {
-        to_floats(p.sums + (static_cast<long long>(k) * gridDim.x + blockIdx.x) * p.d + col, a);
+      flush(sums[k], s_cols, [&](const Pairs& a) {
+        Eight<float>::store(p.sums, (static_cast<long long>(k) * gridDim.x + blockIdx.x) * p.d + col, a);
       });
 }
 
@@ -586,19 +588,18 @@ int allow_smem(int bytes) {
   return TP_OK;
 }
 
-template <typename T, bool LAYER, int R>
+template <typename T, bool LAYER, bool SHIFT>
 int launch_forward_inst(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
-  const int smem = 2 * 2 * R * slots<T>(s.threads) * 16, rows = s.groups * R;
-  if (int rc = allow_smem<forward_kernel<T, LAYER, R>>(smem)) return rc;
-  const int64_t blocks = (p.n + rows - 1) / rows, most = static_cast<int64_t>(num_sms) * std::max(1, 1024 / s.threads);
-  launch_dep(forward_kernel<T, LAYER, R>, dim3(static_cast<unsigned>(std::min(blocks, most))), s.threads, smem, st, p);
+  const int smem = 2 * 2 * slots<T>(s.threads) * 16;
+  if (int rc = allow_smem<forward_kernel<T, LAYER, SHIFT>>(smem)) return rc;
+  const int64_t blocks = (p.n + s.groups - 1) / s.groups, most = static_cast<int64_t>(num_sms) * std::max(1, 1024 / s.threads);
+  launch_dep(forward_kernel<T, LAYER, SHIFT>, dim3(static_cast<unsigned>(std::min(blocks, most))), s.threads, smem, st, p);
   return launched();
 }
-// Two rows to a thread at a time where there are enough for all SMs.
 template <typename T, bool LAYER>
 int launch_forward(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
-  if (p.n >= 4ll * num_sms * s.groups && s.threads <= 512) return launch_forward_inst<T, LAYER, 2>(p, s, num_sms, st);
-  return launch_forward_inst<T, LAYER, 1>(p, s, num_sms, st);
+  if (p.c_after || p.c_before) return launch_forward_inst<T, LAYER, true>(p, s, num_sms, st);
+  return launch_forward_inst<T, LAYER, false>(p, s, num_sms, st);
 }
 template <typename T, bool LAYER, bool SHIFT, int MAX_THREADS>
 int launch_backward_inst(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
@@ -610,7 +611,7 @@ int launch_backward_inst(const NormParams& p, const Shape& s, unsigned grid, cud
 // Up to 512 threads a thread may have 128 registers, which the sums need.
 template <typename T, bool LAYER>
 int launch_backward(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
-  const bool shift = p.want_sums & (1 << S_CB | 1 << S_CA);
+  const bool shift = p.c_after || (p.want_sums & (1 << S_CB | 1 << S_CA));
   if (s.threads <= 512)
     return shift ? launch_backward_inst<T, LAYER, true, 512>(p, s, grid, st) : launch_backward_inst<T, LAYER, false, 512>(p, s, grid, st);
   return shift ? launch_backward_inst<T, LAYER, true, 1024>(p, s, grid, st) : launch_backward_inst<T, LAYER, false, 1024>(p, s, grid, st);
