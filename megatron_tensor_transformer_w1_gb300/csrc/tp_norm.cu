@@ -60,6 +60,11 @@ __device__ __forceinline__ void fill(Pairs& a, float v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) a[i] = both(v);
 }
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 template <typename T>
 struct Eight;
 template <>
@@ -72,15 +77,15 @@ struct Eight<__nv_bfloat16> {
   static __device__ __forceinline__ void load(Pairs& a, const void* p, long long at) {
     open(a, *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
   }
-  static __device__ __forceinline__ void load(Pairs& a, const uint4* slot) { open(a, slot[0]); }
-  static __device__ __forceinline__ void store(void* p, long long at, const Pairs& a) {
+  static __device__ __forceinline__ void load_slot(Pairs& a, uint32_t slot) { open(a, ld_shared(slot)); }
+  static __device__ __forceinline__ void store(void* p, long long bytes, const Pairs& a) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 v = halves(a[i]);
       w[i] = tc::pack_bf16x2(v.x, v.y);
     }
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(static_cast<char*>(p) + bytes) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
@@ -95,11 +100,13 @@ struct Eight<float> {
     const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
     open(a, src[0], src[1]);
   }
-  static __device__ __forceinline__ void load(Pairs& a, const uint4* slot) {
-    open(a, *reinterpret_cast<const float4*>(slot), *reinterpret_cast<const float4*>(slot + blockDim.x));
+  static __device__ __forceinline__ void load_slot(Pairs& a, uint32_t slot) {
+    const uint4 v = ld_shared(slot), w = ld_shared(slot + blockDim.x * 16);
+    open(a, make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)),
+         make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)));
   }
-  static __device__ __forceinline__ void store(void* p, long long at, const Pairs& a) {
-    float4* to = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+  static __device__ __forceinline__ void store(void* p, long long bytes, const Pairs& a) {
+    float4* to = reinterpret_cast<float4*>(static_cast<char*>(p) + bytes);
     const float2 v = halves(a[0]), w = halves(a[1]), x = halves(a[2]), y = halves(a[3]);
     to[0] = make_float4(v.x, v.y, w.x, w.y);
     to[1] = make_float4(x.x, x.y, y.x, y.y);
@@ -108,11 +115,12 @@ struct Eight<float> {
 
 // A row belongs to `tpr` threads, a multiple of 32, thread t of them having the
 // columns 8 t .. 8 t + 7; a block has blockDim / tpr row groups.  A thread copies its
-// columns of the next row into slots of its own in shared memory while it works on
-// this one: it waits for nobody, and no registers are held for them.
+// columns of the next rows into slots of its own in shared memory while it works on
+// this one (`stages` rows in all): it waits for nobody, and no registers are held for
+// them.
 struct NormParams {
-  long long n, d, per;  // per: tokens of a gate
-  int tpr, after, before;
+  int n, d, per;          // per: tokens of a gate
+  int tpr, after, before, stages;
   float eps, scale, inv_d;
   const void *x, *b, *w_after, *c_after, *gate, *w_before, *c_before;
   void *r, *out;
@@ -122,23 +130,30 @@ struct NormParams {
   void *dx, *db, *dgate;
   int want_sums;          // bit k: sums[k] is wanted: w_before, c_before, w_after, c_after
   int gate_each;          // a gate for each token: its gradient is written as it comes
-  long long chunks;       // of each gate's tokens
-  long long units;        // gates times chunks
+  int chunks;             // of each gate's tokens
+  int units;              // gates times chunks
   float* sums;            // [4][gridDim.x][d]
   float* gate_sums;       // [gates][chunks][d]
 };
 
 template <typename T>
-__device__ __forceinline__ void fetch(uint4* slot, const void* p, long long at) {
-  const T* src = static_cast<const T*>(p) + at;
+__device__ __forceinline__ void fetch(uint32_t slot, const void* p, long long bytes) {
+  const char* src = static_cast<const char*>(p) + bytes;
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot + i * blockDim.x)),
-                 "l"(reinterpret_cast<const uint4*>(src) + i)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + i * blockDim.x * 16), "l"(src + i * 16) : "memory");
 }
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// The oldest of stages - 1 groups, one for each row ahead, has landed (or, of one
+// stage, all have).
+__device__ __forceinline__ void fetch_wait(int stages) {
+  if (stages >= 4)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (stages == 3)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
 // 16-byte slots of an array's row: one to a thread (bf16), or two.
 template <typename T>
 __host__ __device__ constexpr int slots(int threads) {
@@ -161,9 +176,12 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (*s)[32][
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    v[k] = lane < warps ? s[turn][first + lane][k] : 0.f;
+    // (up to 16 warps: both halves of a warp have the same)
+    const int at = warps > 16 ? lane : lane & 15;
+    v[k] = at < warps ? s[turn][first + at][k] : 0.f;
+    if (warps > 16) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+    for (int d = 8; d; d >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
   }
   turn ^= 1;
 }
@@ -186,7 +204,7 @@ __device__ __forceinline__ float2 row_stats(const Pairs& v, bool ok, const NormP
   }
   sum[0] = ok ? total(q) : 0.f;
   row_sums<1>(sum, p.tpr, s, turn);
-  st.y = 1.f / sqrtf(fmaf(sum[0], p.inv_d, p.eps));
+  st.y = rsqrtf(fmaf(sum[0], p.inv_d, p.eps));
   return st;
 }
 // (v - mean) * factor
@@ -199,23 +217,30 @@ __device__ __forceinline__ uint64_t unit(uint64_t v, uint64_t mean, uint64_t fac
 template <typename T, bool LAYER, bool SHIFT>
 __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ NormParams p) {
   __shared__ float s_sum[2][32][1];
-  extern __shared__ uint4 s_slots[];  // [2][x, b] of slots
+  extern __shared__ uint4 s_slots[];  // [stages][x, b] of slots
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
-  const long long col = 8ll * t, step = static_cast<long long>(gridDim.x) * groups;
+  const int col = 8 * t, step = gridDim.x * groups;
   const bool ok = col < p.d;
-  int turn = 0, stage = 0;
-  auto slot = [&](int st, int array) { return s_slots + (st * 2 + array) * slots<T>(blockDim.x) + threadIdx.x; };
-  auto fetch_row = [&](long long row, int st) {
-    if (ok && row < p.n) {
-      fetch<T>(slot(st, 0), p.x, row * p.d + col);
-      if (p.b) fetch<T>(slot(st, 1), p.b, row * p.d + col);
+  const long long step_bytes = static_cast<long long>(step) * p.d * sizeof(T);
+  const uint32_t array = slots<T>(blockDim.x) * 16, ring = tc::smem_u32(s_slots) + threadIdx.x * 16;
+  int turn = 0, row = blockIdx.x * groups + group, gate_until = 0, ahead = row;
+  long long bytes = (static_cast<long long>(row) * p.d + col) * sizeof(T), ahead_bytes = bytes;
+  uint32_t stage = ring, ahead_stage = ring;
+  const uint32_t ring_end = ring + p.stages * 2 * array;
+  auto fetch_row = [&] {
+    if (ok && ahead < p.n) {
+      fetch<T>(ahead_stage, p.x, ahead_bytes);
+      if (p.b) fetch<T>(ahead_stage + array, p.b, ahead_bytes);
     }
     fetch_commit();
+    ahead += step;
+    ahead_bytes += step_bytes;
+    ahead_stage += 2 * array;
+    if (ahead_stage == ring_end) ahead_stage = ring;
   };
-  long long row = static_cast<long long>(blockIdx.x) * groups + group, gate_at = -1;
-  fetch_row(row, 0);
+  for (int i = 1; i < p.stages; ++i) fetch_row();
   Pairs k1, k0, w, c;  // scale gate w_after, scale gate c_after, w_before, c_before
   fill(k1, 0.f);
   fill(k0, 0.f);
@@ -223,12 +248,13 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
   fill(c, 0.f);
   if (ok && p.w_before) Eight<T>::load(w, p.w_before, col);
   if (SHIFT && ok && p.c_before) Eight<T>::load(c, p.c_before, col);
-  for (long long row0 = row - group; row0 < p.n; row0 += step, row += step, stage ^= 1) {
+  for (; row - group < p.n; row += step, bytes += step_bytes) {
     const bool live = ok && row < p.n;
-    if (p.b && live && gate_at != (p.gate ? row / p.per : 0)) {
-      gate_at = p.gate ? row / p.per : 0;
+    if (p.b && live && row >= gate_until) {
+      const int gate_at = p.gate ? row / p.per : 0;
+      gate_until = p.gate ? (gate_at + 1) * p.per : p.n;
       fill(k1, 1.f);
-      if (p.gate) Eight<T>::load(k1, p.gate, gate_at * p.d + col);
+      if (p.gate) Eight<T>::load(k1, p.gate, static_cast<long long>(gate_at) * p.d + col);
 #pragma unroll
       for (int i = 0; i < 4; ++i) k1[i] = mul2(k1[i], both(p.scale));
       if (SHIFT && p.c_after) {
@@ -246,19 +272,21 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
     Pairs v, u;
     fill(v, 0.f);
     fill(u, 0.f);
-    fetch_wait();
+    fetch_wait(p.stages);
     if (live) {
-      Eight<T>::load(v, slot(stage, 0));
-      if (p.b) Eight<T>::load(u, slot(stage, 1));
+      Eight<T>::load_slot(v, stage);
+      if (p.b) Eight<T>::load_slot(u, stage + array);
     }
-    fetch_row(row + step, stage ^ 1);
+    stage += 2 * array;
+    if (stage == ring_end) stage = ring;
+    fetch_row();  // (into the slots of the row before)
     float2 sa = make_float2(0.f, 1.f), sb = make_float2(0.f, 0.f);
     if (p.after) sa = row_stats<LAYER>(u, ok, p, s_sum, turn);
     if (live && p.b) {  // (columns and rows that there are not stay zero)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = fma2(unit<LAYER>(u[i], both(-sa.x), both(sa.y)), k1[i], SHIFT ? add2(v[i], k0[i]) : v[i]);
     }
-    if (live) Eight<T>::store(p.r, row * p.d + col, v);
+    if (live) Eight<T>::store(p.r, bytes, v);
     if (p.before) {
       sb = row_stats<LAYER>(v, ok, p, s_sum, turn);
 #pragma unroll
@@ -266,7 +294,7 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
         const uint64_t y = unit<LAYER>(v[i], both(-sb.x), both(sb.y));
         v[i] = SHIFT ? fma2(y, w[i], c[i]) : mul2(y, w[i]);
       }
-      if (live) Eight<T>::store(p.out, row * p.d + col, v);
+      if (live) Eight<T>::store(p.out, bytes, v);
     }
     if (p.stats && live && t == 0) {
       float2* st = reinterpret_cast<float2*>(p.stats + row);
@@ -281,52 +309,62 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
 // registers of the thread that has the column.  SHIFT: those of the shifts too.
 enum { S_WB = 0, S_CB = 1, S_WA = 2, S_CA = 3 };
 enum { A_DR = 0, A_DOUT = 1, A_R = 2, A_B = 3, A_GATE = 4 };  // slots; the last with a gate for each token
-// Whether the next rows' slots fit beside these.
-template <typename T, int MAX_THREADS>
-struct Back {
-  static constexpr int STAGES = sizeof(T) == 4 && MAX_THREADS == 1024 ? 1 : 2;
-  static int smem(int threads, bool gate_each) { return STAGES * (gate_each ? 5 : 4) * slots<T>(threads) * 16; }
-};
 template <typename T, bool LAYER, bool SHIFT, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_constant__ NormParams p) {
-  using B = Back<T, MAX_THREADS>;
   constexpr int N = LAYER ? 2 : 1;  // sums of a row
   __shared__ float s_sum[2][32][N];
-  extern __shared__ uint4 s_slots[];  // [STAGES][arrays] of slots; at the end [threads][8] floats
+  extern __shared__ uint4 s_slots[];  // [stages][arrays] of slots; at the end [threads][8] floats
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
-  const long long col = 8ll * t;
+  const int col = 8 * t;
   const bool ok = col < p.d;
-  const int arrays = p.gate_each ? 5 : 4;
-  int turn = 0, stage = 0;
-  auto slot = [&](int st, int array) { return s_slots + (st * arrays + array) * slots<T>(blockDim.x) + threadIdx.x; };
+  const long long step_bytes = static_cast<long long>(groups) * p.d * sizeof(T);
+  const uint32_t array = slots<T>(blockDim.x) * 16, row_slots = (p.gate_each ? 5 : 4) * array;
+  const uint32_t ring = tc::smem_u32(s_slots) + threadIdx.x * 16, ring_end = ring + p.stages * row_slots;
+  int turn = 0;
   // Rows of the block's units, one to a row group at a time.
   struct Place {
-    long long unit, row, to;
+    int unit, row, to;
+    long long bytes;
+    uint32_t slot;
   };
   auto enter = [&](Place& at) {
     if (at.unit >= p.units) return;
-    const long long gi = at.unit / p.chunks, c = at.unit - gi * p.chunks;
-    at.row = gi * p.per + c * p.per / p.chunks;
-    at.to = gi * p.per + (c + 1) * p.per / p.chunks;
+    const int gi = at.unit / p.chunks, c = at.unit - gi * p.chunks;
+    at.row = gi * p.per + static_cast<int>(static_cast<long long>(c) * p.per / p.chunks) + group;
+    at.to = gi * p.per + static_cast<int>(static_cast<long long>(c + 1) * p.per / p.chunks);
+    at.bytes = (static_cast<long long>(at.row) * p.d + col) * sizeof(T);
   };
-  auto fetch_row = [&](const Place& at, int st) {
-    if (ok && at.unit < p.units && at.row + group < at.to) {
-      const long long from = (at.row + group) * p.d + col;
-      if (p.dr) fetch<T>(slot(st, A_DR), p.dr, from);
+  auto go_on = [&](Place& at) {  // whether that ended a unit
+    at.slot += row_slots;
+    if (at.slot == ring_end) at.slot = ring;
+    at.row += groups;
+    at.bytes += step_bytes;
+    if (at.row - group < at.to) return false;
+    at.unit += gridDim.x;
+    enter(at);
+    return true;
+  };
+  auto fetch_row = [&](const Place& at) {
+    if (ok && at.unit < p.units && at.row < at.to) {
+      if (p.dr) fetch<T>(at.slot + A_DR * array, p.dr, at.bytes);
       if (p.before) {
-        fetch<T>(slot(st, A_DOUT), p.dout, from);
-        fetch<T>(slot(st, A_R), p.r, from);
+        fetch<T>(at.slot + A_DOUT * array, p.dout, at.bytes);
+        fetch<T>(at.slot + A_R * array, p.r, at.bytes);
       }
-      if (p.b) fetch<T>(slot(st, A_B), p.b, from);
-      if (p.gate_each) fetch<T>(slot(st, A_GATE), p.gate, from);
+      if (p.b) fetch<T>(at.slot + A_B * array, p.b, at.bytes);
+      if (p.gate_each) fetch<T>(at.slot + A_GATE * array, p.gate, at.bytes);
     }
     fetch_commit();
   };
-  Place here{blockIdx.x, 0, 0};
+  Place here{static_cast<int>(blockIdx.x), 0, 0, 0, ring};
   enter(here);
-  if (B::STAGES == 2) fetch_row(here, 0);
+  Place ahead = here;
+  for (int i = 1; i < p.stages; ++i) {
+    fetch_row(ahead);
+    if (ahead.unit < p.units) go_on(ahead);
+  }
   Pairs wa, ca, wb, gate;
   fill(wa, 1.f);
   fill(ca, 0.f);
@@ -335,7 +373,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
   if (ok && p.w_after) Eight<T>::load(wa, p.w_after, col);
   if (ok && p.c_after) Eight<T>::load(ca, p.c_after, col);
   if (ok && p.w_before) Eight<T>::load(wb, p.w_before, col);
-  if (ok && p.gate && !p.gate_each && here.unit < p.units) Eight<T>::load(gate, p.gate, here.unit / p.chunks * p.d + col);
+  if (ok && p.gate && !p.gate_each && here.unit < p.units) Eight<T>::load(gate, p.gate, static_cast<long long>(here.unit / p.chunks) * p.d + col);
   Pairs sums[4] = {}, gsum = {};
   // A column sum over the block's row groups, then to `write`.
   auto flush = [&](Pairs& a, float* s_cols, auto&& write) {
@@ -357,33 +395,30 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
     }
     if (group == 0 && ok) write(a);
   };
-  float* s_cols = reinterpret_cast<float*>(s_slots + B::STAGES * arrays * slots<T>(blockDim.x));
+  float* s_cols = reinterpret_cast<float*>(reinterpret_cast<char*>(s_slots) + p.stages * row_slots);
   while (here.unit < p.units) {
     Place next = here;
-    next.row += groups;
-    const bool ends = next.row >= next.to;
-    if (ends) {
-      next.unit += gridDim.x;
-      enter(next);
-    }
-    if (B::STAGES == 1) fetch_row(here, 0);
-    const long long row = here.row + group, at = row * p.d + col;
-    const bool live = ok && row < here.to;
+    const bool ends = go_on(next);
+    if (p.stages == 1) fetch_row(here);
+    const bool live = ok && here.row < here.to;
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live && p.stats) st = p.stats[row];
-    fetch_wait();
-    if (B::STAGES == 2) fetch_row(next, stage ^ 1);
+    if (live && p.stats) st = p.stats[here.row];
+    fetch_wait(p.stages);
+    if (p.stages > 1) {  // (into the slots of the row before)
+      fetch_row(ahead);
+      if (ahead.unit < p.units) go_on(ahead);
+    }
     Pairs g;
     fill(g, 0.f);
-    if (live && p.dr) Eight<T>::load(g, slot(stage, A_DR));
+    if (live && p.dr) Eight<T>::load_slot(g, here.slot + A_DR * array);
     if (p.before) {
       Pairs y, dy;
       fill(y, 0.f);
       fill(dy, 0.f);
       uint64_t s0 = 0, s1 = 0;
       if (live) {
-        Eight<T>::load(y, slot(stage, A_R));
-        Eight<T>::load(dy, slot(stage, A_DOUT));
+        Eight<T>::load_slot(y, here.slot + A_R * array);
+        Eight<T>::load_slot(dy, here.slot + A_DOUT * array);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           y[i] = unit<LAYER>(y[i], both(-st.z), both(st.w));
@@ -402,14 +437,14 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = fma2(fma2(y[i], m1, LAYER ? add2(dy[i], m0) : dy[i]), both(st.w), g[i]);
     }
-    if (p.dx && live) Eight<T>::store(p.dx, at, g);
+    if (p.dx && live) Eight<T>::store(p.dx, here.bytes, g);
     if (p.b || p.db) {  // (of all threads)
       Pairs y;
       fill(y, 0.f);
       uint64_t s0 = 0, s1 = 0;
       if (live) {
-        if (p.b) Eight<T>::load(y, slot(stage, A_B));
-        if (p.gate_each) Eight<T>::load(gate, slot(stage, A_GATE));
+        if (p.b) Eight<T>::load_slot(y, here.slot + A_B * array);
+        if (p.gate_each) Eight<T>::load_slot(gate, here.slot + A_GATE * array);
         if (p.after)
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[i] = unit<LAYER>(y[i], both(-st.x), both(st.y));
@@ -425,7 +460,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
           s0 = fma2(g[i], y[i], s0);
           if (LAYER) s1 = add2(s1, g[i]);
         }
-        if (p.gate_each && p.dgate) Eight<T>::store(p.dgate, at, gsum);
+        if (p.gate_each && p.dgate) Eight<T>::store(p.dgate, here.bytes, gsum);
       }
       if (p.after) {
         float s[N];
@@ -436,29 +471,28 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[i] = mul2(fma2(y[i], m1, LAYER ? add2(g[i], m0) : g[i]), both(st.y));
       }
-      if (p.db && live) Eight<T>::store(p.db, at, g);
+      if (p.db && live) Eight<T>::store(p.db, here.bytes, g);
     }
     if (ends && p.gate && !p.gate_each) {
       const long long gi = here.unit / p.chunks;
       if (p.dgate) {
         flush(gsum, s_cols, [&](const Pairs& a) {
           if (p.chunks == 1)
-            Eight<T>::store(p.dgate, gi * p.d + col, a);
+            Eight<T>::store(p.dgate, (gi * p.d + col) * sizeof(T), a);
           else
-            Eight<float>::store(p.gate_sums, here.unit * p.d + col, a);
+            Eight<float>::store(p.gate_sums, (static_cast<long long>(here.unit) * p.d + col) * 4, a);
         });
         fill(gsum, 0.f);
       }
-      if (ok && next.unit < p.units) Eight<T>::load(gate, p.gate, next.unit / p.chunks * p.d + col);
+      if (ok && next.unit < p.units) Eight<T>::load(gate, p.gate, static_cast<long long>(next.unit / p.chunks) * p.d + col);
     }
     here = next;
-    if (B::STAGES == 2) stage ^= 1;
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     if (p.want_sums >> k & 1)
       flush(sums[k], s_cols, [&](const Pairs& a) {
-        Eight<float>::store(p.sums, (static_cast<long long>(k) * gridDim.x + blockIdx.x) * p.d + col, a);
+        Eight<float>::store(p.sums, ((static_cast<long long>(k) * gridDim.x + blockIdx.x) * p.d + col) * 4, a);
       });
 }
 
@@ -555,9 +589,9 @@ Plan plan_of(const NormSpec& a, int num_sms) {
 
 NormParams params_of(const NormSpec& a, const Shape& s) {
   NormParams p{};
-  p.n = a.n;
-  p.d = a.d;
-  p.per = a.n_gates ? a.n / a.n_gates : a.n;
+  p.n = static_cast<int>(a.n);
+  p.d = static_cast<int>(a.d);
+  p.per = static_cast<int>(a.n_gates ? a.n / a.n_gates : a.n);
   p.tpr = s.tpr;
   p.after = a.after;
   p.before = a.before;
@@ -588,11 +622,16 @@ int allow_smem(int bytes) {
   return TP_OK;
 }
 
+// Up to four rows' slots in `room` bytes.
+int stages_in(int room, int row) { return std::max(1, std::min(4, room / row)); }
+
 template <typename T, bool LAYER, bool SHIFT>
-int launch_forward_inst(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
-  const int smem = 2 * 2 * slots<T>(s.threads) * 16;
-  if (int rc = allow_smem<forward_kernel<T, LAYER, SHIFT>>(smem)) return rc;
+int launch_forward_inst(NormParams p, const Shape& s, int num_sms, cudaStream_t st) {
   const int64_t blocks = (p.n + s.groups - 1) / s.groups, most = static_cast<int64_t>(num_sms) * std::max(1, 1024 / s.threads);
+  const int row = 2 * slots<T>(s.threads) * 16, per_sm = std::max(1, 1024 / s.threads);
+  p.stages = blocks <= most ? 2 : std::max(2, stages_in(200 * 1024 / per_sm, row));
+  const int smem = p.stages * row;
+  if (int rc = allow_smem<forward_kernel<T, LAYER, SHIFT>>(smem)) return rc;
   launch_dep(forward_kernel<T, LAYER, SHIFT>, dim3(static_cast<unsigned>(std::min(blocks, most))), s.threads, smem, st, p);
   return launched();
 }
@@ -602,8 +641,10 @@ int launch_forward(const NormParams& p, const Shape& s, int num_sms, cudaStream_
   return launch_forward_inst<T, LAYER, false>(p, s, num_sms, st);
 }
 template <typename T, bool LAYER, bool SHIFT, int MAX_THREADS>
-int launch_backward_inst(const NormParams& p, const Shape& s, unsigned grid, cudaStream_t st) {
-  const int smem = Back<T, MAX_THREADS>::smem(s.threads, p.gate_each) + (s.groups > 1 ? s.threads * 32 : 0);
+int launch_backward_inst(NormParams p, const Shape& s, unsigned grid, cudaStream_t st) {
+  const int row = (p.gate_each ? 5 : 4) * slots<T>(s.threads) * 16, columns = s.groups > 1 ? s.threads * 32 : 0;
+  p.stages = stages_in((200 * 1024 - columns * std::max(1, 512 / s.threads)) / std::max(1, 512 / s.threads), row);
+  const int smem = p.stages * row + columns;
   if (int rc = allow_smem<backward_kernel<T, LAYER, SHIFT, MAX_THREADS>>(smem)) return rc;
   launch_dep(backward_kernel<T, LAYER, SHIFT, MAX_THREADS>, dim3(grid), s.threads, smem, st, p);
   return launched();
@@ -640,15 +681,15 @@ int launch_norm_bwd(const NormSpec& a, void* workspace, int num_sms, cudaStream_
   const Plan c = plan_of(a, num_sms);
   NormParams p = params_of(a, s);
   p.r = const_cast<void*>(a.r_in);
-  p.per = c.per;
+  p.per = static_cast<int>(c.per);
   p.dr = a.dr;
   p.dout = a.dout;
   p.dx = a.dx;
   p.db = a.db;
   p.dgate = a.dgate;
   p.gate_each = c.each;
-  p.chunks = c.chunks;
-  p.units = c.units;
+  p.chunks = static_cast<int>(c.chunks);
+  p.units = static_cast<int>(c.units);
   p.sums = static_cast<float*>(workspace);
   p.gate_sums = p.sums + 4 * c.blocks * a.d;
   void* const to[4] = {a.dw_before, a.dc_before, a.dw_after, a.dc_after};
