@@ -136,12 +136,14 @@ struct NormParams {
   float* gate_sums;       // [gates][chunks][d]
 };
 
+// Not `valid`: the slot gets zeros, nothing is read.
 template <typename T>
-__device__ __forceinline__ void fetch(uint32_t slot, const void* p, long long bytes) {
+__device__ __forceinline__ void fetch(uint32_t slot, const void* p, long long bytes, bool valid = true) {
   const char* src = static_cast<const char*>(p) + bytes;
+  const int n = valid ? 16 : 0;
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + i * blockDim.x * 16), "l"(src + i * 16) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * blockDim.x * 16), "l"(src + i * 16), "r"(n) : "memory");
 }
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // The oldest of stages - 1 groups, one for each row ahead, has landed (or, of one
@@ -160,16 +162,48 @@ __host__ __device__ constexpr int slots(int threads) {
   return threads * static_cast<int>(sizeof(T)) / 2;
 }
 
+// Eight columns of a weight for all rows: as pairs, or, where registers are short, as
+// they lie.
+template <typename T, bool SHORT>
+struct Held {
+  Pairs a;
+  __device__ __forceinline__ void set(float v) { fill(a, v); }
+  __device__ __forceinline__ void load(const void* p, long long at) { Eight<T>::load(a, p, at); }
+  __device__ __forceinline__ void load_slot(uint32_t slot) { Eight<T>::load_slot(a, slot); }
+  __device__ __forceinline__ uint64_t operator[](int i) const { return a[i]; }
+};
+template <>
+struct Held<__nv_bfloat16, true> {
+  uint32_t w[4];
+  __device__ __forceinline__ void set(float v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = tc::pack_bf16x2(v, v);
+  }
+  __device__ __forceinline__ void put(uint4 v) {
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+  __device__ __forceinline__ void load(const void* p, long long at) { put(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at)); }
+  __device__ __forceinline__ void load_slot(uint32_t slot) { put(ld_shared(slot)); }
+  __device__ __forceinline__ uint64_t operator[](int i) const { return pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)); }
+};
+
 // Sums of N values over a row's threads.  `turn` alternates between two buffers, so
 // that one barrier a sum is enough.
+struct Group {
+  int warps, first;  // of a row, the first of this thread's row
+  __device__ __forceinline__ explicit Group(int tpr) : warps(tpr >> 5), first((threadIdx.x >> 5) / (tpr >> 5) * (tpr >> 5)) {}
+};
 template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (*s)[32][N], int& turn) {
+__device__ __forceinline__ void row_sums(float (&v)[N], const Group& G, float (*s)[32][N], int& turn) {
 #pragma unroll
   for (int k = 0; k < N; ++k)
 #pragma unroll
     for (int d = 16; d; d >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
-  if (tpr == 32) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tpr >> 5, first = warp / warps * warps;
+  if (G.warps == 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0)
 #pragma unroll
     for (int k = 0; k < N; ++k) s[turn][warp][k] = v[k];
@@ -177,9 +211,9 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (*s)[32][
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     // (up to 16 warps: both halves of a warp have the same)
-    const int at = warps > 16 ? lane : lane & 15;
-    v[k] = at < warps ? s[turn][first + at][k] : 0.f;
-    if (warps > 16) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+    const int at = G.warps > 16 ? lane : lane & 15;
+    v[k] = at < G.warps ? s[turn][G.first + at][k] : 0.f;
+    if (G.warps > 16) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
 #pragma unroll
     for (int d = 8; d; d >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
   }
@@ -188,12 +222,12 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (*s)[32][
 
 // The mean and factor of a row's norm.
 template <bool LAYER>
-__device__ __forceinline__ float2 row_stats(const Pairs& v, bool ok, const NormParams& p, float (*s)[32][1], int& turn) {
+__device__ __forceinline__ float2 row_stats(const Pairs& v, bool ok, const NormParams& p, const Group& G, float (*s)[32][1], int& turn) {
   float2 st = make_float2(0.f, 0.f);
   float sum[1];
   if (LAYER) {
     sum[0] = total(add2(add2(v[0], v[1]), add2(v[2], v[3])));
-    row_sums<1>(sum, p.tpr, s, turn);
+    row_sums<1>(sum, G, s, turn);
     st.x = sum[0] * p.inv_d;
   }
   uint64_t q = 0;
@@ -203,7 +237,7 @@ __device__ __forceinline__ float2 row_stats(const Pairs& v, bool ok, const NormP
     q = fma2(a, a, q);
   }
   sum[0] = ok ? total(q) : 0.f;
-  row_sums<1>(sum, p.tpr, s, turn);
+  row_sums<1>(sum, G, s, turn);
   st.y = rsqrtf(fmaf(sum[0], p.inv_d, p.eps));
   return st;
 }
@@ -221,6 +255,7 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
+  const Group G(p.tpr);
   const int col = 8 * t, step = gridDim.x * groups;
   const bool ok = col < p.d;
   const long long step_bytes = static_cast<long long>(step) * p.d * sizeof(T);
@@ -281,14 +316,14 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
     if (stage == ring_end) stage = ring;
     fetch_row();  // (into the slots of the row before)
     float2 sa = make_float2(0.f, 1.f), sb = make_float2(0.f, 0.f);
-    if (p.after) sa = row_stats<LAYER>(u, ok, p, s_sum, turn);
+    if (p.after) sa = row_stats<LAYER>(u, ok, p, G, s_sum, turn);
     if (live && p.b) {  // (columns and rows that there are not stay zero)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = fma2(unit<LAYER>(u[i], both(-sa.x), both(sa.y)), k1[i], SHIFT ? add2(v[i], k0[i]) : v[i]);
     }
     if (live) Eight<T>::store(p.r, bytes, v);
     if (p.before) {
-      sb = row_stats<LAYER>(v, ok, p, s_sum, turn);
+      sb = row_stats<LAYER>(v, ok, p, G, s_sum, turn);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t y = unit<LAYER>(v[i], both(-sb.x), both(sb.y));
@@ -317,6 +352,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
+  const Group G(p.tpr);
   const int col = 8 * t;
   const bool ok = col < p.d;
   const long long step_bytes = static_cast<long long>(groups) * p.d * sizeof(T);
@@ -346,16 +382,22 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
     enter(at);
     return true;
   };
+  // What there is not is zeros in the slots, columns and rows among it: they add
+  // nothing to any sum.
+  const void* some = p.r ? p.r : p.stats ? static_cast<const void*>(p.stats) : p.sums;
   auto fetch_row = [&](const Place& at) {
-    if (ok && at.unit < p.units && at.row < at.to) {
-      if (p.dr) fetch<T>(at.slot + A_DR * array, p.dr, at.bytes);
-      if (p.before) {
-        fetch<T>(at.slot + A_DOUT * array, p.dout, at.bytes);
-        fetch<T>(at.slot + A_R * array, p.r, at.bytes);
-      }
-      if (p.b) fetch<T>(at.slot + A_B * array, p.b, at.bytes);
-      if (p.gate_each) fetch<T>(at.slot + A_GATE * array, p.gate, at.bytes);
+    const bool there = ok && at.unit < p.units && at.row < at.to;
+    auto array_of = [&](int a, const void* from) {
+      const bool valid = there && from;
+      fetch<T>(at.slot + a * array, valid ? from : some, valid ? at.bytes : 0, valid);
+    };
+    array_of(A_DR, p.dr);
+    if (p.before) {
+      array_of(A_DOUT, p.dout);
+      array_of(A_R, p.r);
     }
+    array_of(A_B, p.b);
+    if (p.gate_each) array_of(A_GATE, p.gate);
     fetch_commit();
   };
   Place here{static_cast<int>(blockIdx.x), 0, 0, 0, ring};
@@ -365,15 +407,15 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
     fetch_row(ahead);
     if (ahead.unit < p.units) go_on(ahead);
   }
-  Pairs wa, ca, wb, gate;
-  fill(wa, 1.f);
-  fill(ca, 0.f);
-  fill(wb, 1.f);
-  fill(gate, 1.f);
-  if (ok && p.w_after) Eight<T>::load(wa, p.w_after, col);
-  if (ok && p.c_after) Eight<T>::load(ca, p.c_after, col);
-  if (ok && p.w_before) Eight<T>::load(wb, p.w_before, col);
-  if (ok && p.gate && !p.gate_each && here.unit < p.units) Eight<T>::load(gate, p.gate, static_cast<long long>(here.unit / p.chunks) * p.d + col);
+  Held<T, MAX_THREADS == 1024> wa, ca, wb, gate;
+  wa.set(1.f);
+  ca.set(0.f);
+  wb.set(1.f);
+  gate.set(1.f);
+  if (ok && p.w_after) wa.load(p.w_after, col);
+  if (ok && p.c_after) ca.load(p.c_after, col);
+  if (ok && p.w_before) wb.load(p.w_before, col);
+  if (ok && p.gate && !p.gate_each && here.unit < p.units) gate.load(p.gate, static_cast<long long>(here.unit / p.chunks) * p.d + col);
   Pairs sums[4] = {}, gsum = {};
   // A column sum over the block's row groups, then to `write`.
   auto flush = [&](Pairs& a, float* s_cols, auto&& write) {
@@ -396,43 +438,43 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
     if (group == 0 && ok) write(a);
   };
   float* s_cols = reinterpret_cast<float*>(reinterpret_cast<char*>(s_slots) + p.stages * row_slots);
+  // A row's statistics are on their way while the row before it is worked on.
+  auto stats_of = [&](const Place& at) {
+    return ok && p.stats && at.unit < p.units && at.row < at.to ? p.stats[at.row] : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float4 st_next = stats_of(here);
   while (here.unit < p.units) {
     Place next = here;
     const bool ends = go_on(next);
     if (p.stages == 1) fetch_row(here);
     const bool live = ok && here.row < here.to;
-    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live && p.stats) st = p.stats[here.row];
+    const float4 st = st_next;
+    st_next = stats_of(next);
     fetch_wait(p.stages);
     if (p.stages > 1) {  // (into the slots of the row before)
       fetch_row(ahead);
       if (ahead.unit < p.units) go_on(ahead);
     }
     Pairs g;
-    fill(g, 0.f);
-    if (live && p.dr) Eight<T>::load_slot(g, here.slot + A_DR * array);
+    Eight<T>::load_slot(g, here.slot + A_DR * array);
     if (p.before) {
       Pairs y, dy;
-      fill(y, 0.f);
-      fill(dy, 0.f);
+      Eight<T>::load_slot(y, here.slot + A_R * array);
+      Eight<T>::load_slot(dy, here.slot + A_DOUT * array);
       uint64_t s0 = 0, s1 = 0;
-      if (live) {
-        Eight<T>::load_slot(y, here.slot + A_R * array);
-        Eight<T>::load_slot(dy, here.slot + A_DOUT * array);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[i] = unit<LAYER>(y[i], both(-st.z), both(st.w));
-          sums[S_WB][i] = fma2(dy[i], y[i], sums[S_WB][i]);
-          if (SHIFT) sums[S_CB][i] = add2(sums[S_CB][i], dy[i]);
-          dy[i] = mul2(dy[i], wb[i]);
-          s0 = fma2(dy[i], y[i], s0);
-          if (LAYER) s1 = add2(s1, dy[i]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        y[i] = unit<LAYER>(y[i], both(-st.z), both(st.w));
+        sums[S_WB][i] = fma2(dy[i], y[i], sums[S_WB][i]);
+        if (SHIFT) sums[S_CB][i] = add2(sums[S_CB][i], dy[i]);
+        dy[i] = mul2(dy[i], wb[i]);
+        s0 = fma2(dy[i], y[i], s0);
+        if (LAYER) s1 = add2(s1, dy[i]);
       }
       float s[N];
       s[0] = total(s0);
       if (LAYER) s[N - 1] = total(s1);
-      row_sums<N>(s, p.tpr, s_sum, turn);
+      row_sums<N>(s, G, s_sum, turn);
       const uint64_t m1 = both(-s[0] * p.inv_d), m0 = both(-s[N - 1] * p.inv_d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = fma2(fma2(y[i], m1, LAYER ? add2(dy[i], m0) : dy[i]), both(st.w), g[i]);
@@ -440,33 +482,30 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
     if (p.dx && live) Eight<T>::store(p.dx, here.bytes, g);
     if (p.b || p.db) {  // (of all threads)
       Pairs y;
-      fill(y, 0.f);
+      Eight<T>::load_slot(y, here.slot + A_B * array);
+      if (p.gate_each) gate.load_slot(here.slot + A_GATE * array);
       uint64_t s0 = 0, s1 = 0;
-      if (live) {
-        if (p.b) Eight<T>::load_slot(y, here.slot + A_B * array);
-        if (p.gate_each) Eight<T>::load_slot(gate, here.slot + A_GATE * array);
-        if (p.after)
+      if (p.after)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = unit<LAYER>(y[i], both(-st.x), both(st.y));
+        for (int i = 0; i < 4; ++i) y[i] = unit<LAYER>(y[i], both(-st.x), both(st.y));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t sg = mul2(g[i], both(p.scale));
-          const uint64_t u = SHIFT ? fma2(y[i], wa[i], ca[i]) : mul2(y[i], wa[i]);
-          gsum[i] = p.gate_each ? mul2(sg, u) : fma2(sg, u, gsum[i]);
-          g[i] = mul2(sg, gate[i]);
-          sums[S_WA][i] = fma2(g[i], y[i], sums[S_WA][i]);
-          if (SHIFT) sums[S_CA][i] = add2(sums[S_CA][i], g[i]);
-          g[i] = mul2(g[i], wa[i]);
-          s0 = fma2(g[i], y[i], s0);
-          if (LAYER) s1 = add2(s1, g[i]);
-        }
-        if (p.gate_each && p.dgate) Eight<T>::store(p.dgate, here.bytes, gsum);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t sg = mul2(ok ? g[i] : 0, both(p.scale));  // (a layer norm's gradient is not zero behind the last column)
+        const uint64_t u = SHIFT ? fma2(y[i], wa[i], ca[i]) : mul2(y[i], wa[i]);
+        gsum[i] = p.gate_each ? mul2(sg, u) : fma2(sg, u, gsum[i]);
+        g[i] = mul2(sg, gate[i]);
+        sums[S_WA][i] = fma2(g[i], y[i], sums[S_WA][i]);
+        if (SHIFT) sums[S_CA][i] = add2(sums[S_CA][i], g[i]);
+        g[i] = mul2(g[i], wa[i]);
+        s0 = fma2(g[i], y[i], s0);
+        if (LAYER) s1 = add2(s1, g[i]);
       }
+      if (p.gate_each && p.dgate && live) Eight<T>::store(p.dgate, here.bytes, gsum);
       if (p.after) {
         float s[N];
         s[0] = total(s0);
         if (LAYER) s[N - 1] = total(s1);
-        row_sums<N>(s, p.tpr, s_sum, turn);
+        row_sums<N>(s, G, s_sum, turn);
         const uint64_t m1 = both(-s[0] * p.inv_d), m0 = both(-s[N - 1] * p.inv_d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[i] = mul2(fma2(y[i], m1, LAYER ? add2(g[i], m0) : g[i]), both(st.y));
@@ -484,7 +523,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
         });
         fill(gsum, 0.f);
       }
-      if (ok && next.unit < p.units) Eight<T>::load(gate, p.gate, static_cast<long long>(next.unit / p.chunks) * p.d + col);
+      if (ok && next.unit < p.units) gate.load(p.gate, static_cast<long long>(next.unit / p.chunks) * p.d + col);
     }
     here = next;
   }
