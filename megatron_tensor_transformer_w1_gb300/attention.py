@@ -79,7 +79,7 @@ class TensorParallelAttention:
         """4-bit weights for decode(), (wqkv_4, wo_4).  Each weight is a bfloat16 matrix,
         which is quantised, or a weights4.Codes4, Wo's with T_p segments.  group: 32, 64
         or 128 (the default, or the codes' own)."""
-        dev = w4.full_device(self.device)
+        dev = w4.device_index(self.device)
         weights = (Wq, Wk, Wv, Wo)
         group = w4.group_of(group, *weights)
         with torch.cuda.device(dev):
@@ -94,7 +94,7 @@ class TensorParallelAttention:
 
     def unpack4(self, wqkv_4, wo_4):
         """The codes of Wq, Wk, Wv and Wo."""
-        dev = w4.full_device(self.device)
+        dev = w4.device_index(self.device)
         w4.check_packed("wqkv_4", wqkv_4, abi.TP_PACK_COLUMNS, self._key4(), dev)
         w4.check_packed("wo_4", wo_4, abi.TP_PACK_ROWS, self._key4(), dev, wqkv_4.group)
         with torch.cuda.device(dev):

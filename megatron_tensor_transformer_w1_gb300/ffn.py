@@ -36,7 +36,9 @@ class TensorParallelFFN:
         self.info = abi.tp_ffn_plan_info(h)
         self.d, self.d_ff, self.T_p = self.info["d"], self.info["d_ff"], self.info["T_p"]
         self._ws = None
-        self._scratch4 = w4.Scratch(self.device)
+        self._scratch4 = w4.Scratch()
+        self._key4 = ("ffn", act, self.d, self.d_ff, self.T_p)
+        self._need4 = {}  # workspace bytes by device and tokens
 
     def __del__(self):
         plan = getattr(self, "plan", None)
@@ -82,9 +84,6 @@ class TensorParallelFFN:
         return W2
 
     # ------------------------------------------------------------ 4-bit weights
-    def _key4(self):
-        return ("ffn", self.act_name, self.d, self.d_ff, self.T_p)
-
     def _no_up4(self):
         if self.act_name == "none":
             raise ValueError("this sublayer has no first matrix")
@@ -96,7 +95,7 @@ class TensorParallelFFN:
         or the codes' own)."""
         if self.dtype_code != abi.TP_BF16:
             raise ValueError("4-bit weights need a bf16 sublayer")
-        dev = w4.full_device(self.device)
+        dev = w4.device_index(self.device)
         group = w4.group_of(group, W1, W2, W3)
         gated = self.act_name == "swiglu"
         if (W1 is None) != (self.act_name == "none") or (W3 is None) == gated:
@@ -110,17 +109,17 @@ class TensorParallelFFN:
                 up = torch.empty(abi.tp_ffn_packed4_bytes(self.plan, abi.TP_PACK_COLUMNS, group), dtype=torch.uint8, device=dev)
                 abi.check(abi.tp_ffn_shard_columns4(self.plan, group, c1.codes, c1.scales, c3 and c3.codes,
                                                     c3 and c3.scales, up, st), "shard_columns4")
-                up = w4.Packed4(up, group, abi.TP_PACK_COLUMNS, self._key4())
+                up = w4.Packed4(up, group, abi.TP_PACK_COLUMNS, self._key4)
             c2 = w4.as_codes("W2", W2, self.d, self.d_ff, group, self.T_p, dev)
             down = torch.empty(abi.tp_ffn_packed4_bytes(self.plan, abi.TP_PACK_ROWS, group), dtype=torch.uint8, device=dev)
             abi.check(abi.tp_ffn_shard_rows4(self.plan, group, c2.codes, c2.scales, down, st), "shard_rows4")
-        return up, w4.Packed4(down, group, abi.TP_PACK_ROWS, self._key4())
+        return up, w4.Packed4(down, group, abi.TP_PACK_ROWS, self._key4)
 
     def unpack4_columns(self, w13_4):
         """The codes of W1 and of W3 (None without it)."""
         self._no_up4()
-        dev = w4.full_device(self.device)
-        w4.check_packed("w13_4", w13_4, abi.TP_PACK_COLUMNS, self._key4(), dev)
+        dev = w4.device_index(self.device)
+        w4.check_packed("w13_4", w13_4, abi.TP_PACK_COLUMNS, self._key4, dev)
         with torch.cuda.device(dev):
             c = [w4.Codes4.empty(self.d_ff, self.d, w13_4.group, 1, dev) for _ in range(2 if self.act_name == "swiglu" else 1)]
             c1, c3 = c[0], (c[1] if len(c) > 1 else None)
@@ -131,8 +130,8 @@ class TensorParallelFFN:
 
     def unpack4_rows(self, w2_4):
         """The codes of W2, with T_p segments."""
-        dev = w4.full_device(self.device)
-        w4.check_packed("w2_4", w2_4, abi.TP_PACK_ROWS, self._key4(), dev)
+        dev = w4.device_index(self.device)
+        w4.check_packed("w2_4", w2_4, abi.TP_PACK_ROWS, self._key4, dev)
         with torch.cuda.device(dev):
             c = w4.Codes4.empty(self.d, self.d_ff, w2_4.group, self.T_p, dev)
             abi.check(abi.tp_ffn_unshard_rows4(self.plan, w2_4.group, w2_4.data, c.codes, c.scales,
@@ -142,31 +141,40 @@ class TensorParallelFFN:
     def forward4(self, x, w13_4, w2_4, b1=None, b2=None, out=None, flags=0):
         """y [n, d] of forward() for inference, from the 4-bit weights of pack4()
         (w13_4 None where the sublayer has no first matrix)."""
-        dev = w4.full_device(self.device)
+        index = w4.device_index(self.device)
+        if w4.current_device() != index:
+            with torch.cuda.device(index):
+                return self.forward4(x, w13_4, w2_4, b1, b2, out, flags)
         none = self.act_name == "none"
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x: a bfloat16 matrix [tokens, features] is needed")
         n = x.shape[0]
-        w4.check_tensor("x", x, torch.bfloat16, (n, self.d_ff if none else self.d), dev)
-        w4.check_packed("w2_4", w2_4, abi.TP_PACK_ROWS, self._key4(), dev)
+        w4.check_tensor("x", x, w4.BF16, (n, self.d_ff if none else self.d), index)
+        w4.check_packed("w2_4", w2_4, abi.TP_PACK_ROWS, self._key4, index)
         if not none:
-            w4.check_packed("w13_4", w13_4, abi.TP_PACK_COLUMNS, self._key4(), dev, w2_4.group)
+            w4.check_packed("w13_4", w13_4, abi.TP_PACK_COLUMNS, self._key4, index, w2_4.group)
         elif w13_4 is not None:
             self._no_up4()
         if b1 is not None:
-            w4.check_tensor("b1", b1, torch.bfloat16, (self.d_ff,), dev)
+            w4.check_tensor("b1", b1, w4.BF16, (self.d_ff,), index)
         if b2 is not None:
-            w4.check_tensor("b2", b2, torch.bfloat16, (self.d,), dev)
-        if out is not None:
-            w4.check_tensor("out", out, torch.bfloat16, (n, self.d), dev)
-        with torch.cuda.device(dev), self._scratch4.turn:
-            st = torch.cuda.current_stream()
-            y = torch.empty(n, self.d, dtype=torch.bfloat16, device=dev) if out is None else out
-            need = abi.tp_ffn_workspace4_bytes(self.plan, n, flags)
-            ws = self._scratch4.take(need, st)
-            abi.check(abi.tp_ffn_fwd4(self.plan, w2_4.group, n, x, None if none else w13_4.data, w2_4.data, b1, b2, y, ws,
-                                      ws.numel(), flags, st), "tp_ffn_fwd4")
-        return y
+            w4.check_tensor("b2", b2, w4.BF16, (self.d,), index)
+        if out is None:
+            out = torch.empty((n, self.d), dtype=w4.BF16, device=index)
+        else:
+            w4.check_tensor("out", out, w4.BF16, (n, self.d), index)
+        need = self._need4.get((index, n))
+        if need is None:
+            need = self._need4[index, n] = max(16, abi.tp_ffn_workspace4_bytes(self.plan, n, flags))
+        with self._scratch4.turn:
+            st = w4.current_stream(index)
+            ws = self._scratch4.take(need, index, st)
+            rc = abi._lib.tp_ffn_fwd4(self.plan, w2_4.group, n, x.data_ptr(), None if none else w13_4.data.data_ptr(),
+                                      w2_4.data.data_ptr(), None if b1 is None else b1.data_ptr(),
+                                      None if b2 is None else b2.data_ptr(), out.data_ptr(), ws.data_ptr(), need, flags, st)
+        if rc:
+            abi.check(rc, "tp_ffn_fwd4")
+        return out
 
     # ------------------------------------------------------------ passes
     def forward(self, x, w13p, w2p, b1=None, b2=None, save=True, fused=False, want_partials=False, flags=0,

@@ -198,8 +198,8 @@ class PagedKVCache:
         a, n = self.attn, batch.n_tokens
         self._check("x", x, torch.bfloat16, (n, a.d))
         if isinstance(wqkv, w4.Packed4) or isinstance(wo, w4.Packed4):
-            w4.check_packed("wqkv", wqkv, abi.TP_PACK_COLUMNS, a._key4(), self.k.device)
-            w4.check_packed("wo", wo, abi.TP_PACK_ROWS, a._key4(), self.k.device, wqkv.group)
+            w4.check_packed("wqkv", wqkv, abi.TP_PACK_COLUMNS, a._key4(), self._index)
+            w4.check_packed("wo", wo, abi.TP_PACK_ROWS, a._key4(), self._index, wqkv.group)
             y = self._out("out", out, (n, a.d))
             st = _current_stream(self._index)
             with self._turn:
