@@ -273,7 +273,17 @@ struct W4Shape {
   __host__ __device__ int64_t seg_groups() const { return (seg + group - 1) / group; }
   __host__ __device__ int64_t cols() const { return segs * seg; }
   __host__ __device__ int block_bytes() const { return 16384 + 512 * (128 / group); }
-  __host__ __device__ int64_t bytes() const { return units() * chunks() * block_bytes(); }
+  // Behind the blocks: for every row of the units a power of two (float) that brings
+  // the row's largest scale to 2^11..2^12, and the largest |scale| of the first matrix and
+  // (W4_GATED) of the second, as the bits of a float.
+  __host__ __device__ int64_t block_end() const { return units() * chunks() * block_bytes(); }
+  __host__ __device__ float* row_up(void* packed) const {
+    return reinterpret_cast<float*>(static_cast<char*>(packed) + block_end());
+  }
+  __host__ __device__ uint32_t* tops(void* packed) const {
+    return reinterpret_cast<uint32_t*>(static_cast<char*>(packed) + block_end() + units() * 1024);
+  }
+  __host__ __device__ int64_t bytes() const { return block_end() + units() * 1024 + 16; }
 };
 // Tile `tile` of the packed layout: rows row0 .. row0 + n - 1 of matrix `mat`.
 struct W4Tile {

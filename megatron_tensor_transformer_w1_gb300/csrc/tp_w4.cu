@@ -25,6 +25,11 @@ __device__ __forceinline__ float bf16_at(uint32_t w, int half) {
   return __uint_as_float(half ? w & 0xffff0000u : w << 16);
 }
 
+// 2^e, e brought into a range where 2^-e is a normal number too.
+__device__ __forceinline__ float pow2(int e) {
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 126) + 127) << 23);
+}
+
 // ================================================================ quantising
 // s = bf16(max |w| / 7), code = rint(w / s) + 8, ties to even.
 // A group with an infinity or NaN has that for its scale.  With s = 0 (all
@@ -229,48 +234,52 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
   }
 }
 
+// The factors of the rows (see w4_row_up): a block to a unit, a thread to a row.
+__global__ void __launch_bounds__(256) tops_kernel(W4Shape m, uint8_t* packed) {
+  const long long chunks = m.chunks(), unit = blockIdx.x;
+  const int r = threadIdx.x, subs = 128 / m.group;
+  uint32_t top = 0;  // the largest |scale|, as bits: infinities and NaN are largest
+  for (long long c = 0; c < chunks; ++c) {
+    const auto* at = reinterpret_cast<const uint16_t*>(packed + (unit * chunks + c) * m.block_bytes() + 16384) + r;
+    for (int i = 0; i < subs; ++i) top = max(top, at[i * 256] & 0x7fffu);
+  }
+  const int e = min(static_cast<int>(top >> 7), 254) - 127;  // top < 2^(e + 1)
+  m.row_up(packed)[unit * 256 + r] = pow2(top ? 11 - e : 0);
+  top = __reduce_max_sync(0xffffffffu, top);
+  // with gates the unit's second tile has the second matrix's rows
+  if ((r & 31) == 0) atomicMax(m.tops(packed) + (m.rows_kind == W4_GATED ? r >> 7 : 0), top << 16);
+}
+
 // ================================================================ products
-// y[token][row] = sum_g s[row][g] sum_{k in g} (code - 8) x[token][k], for up to
-// 64 tokens at a time.  Bound by the one read of the codes.
-//
-// What is left to count are the instructions that make operands of codes.  A code
-// in the low bits of a floating number with few exponent bits is a subnormal, code
-// times its least number, and takes no addition or conversion:
-//  * fp16 (up to 16 tokens): code * 2^-24, and four bits higher code * 2^-20.  A word's
-//    eight codes are four operand registers after one shift and four masks.
-//  * e4m3 (more tokens): code * 2^-9.  A word's eight codes are two registers after
-//    one shift and two masks, and a product takes 32 columns instead of 16.
-// (Codes made into bf16 take 11 instructions a word: 102 us instead of 68 for one
-// token of the 70B feed-forward.)  For that
-//  * the tokens are of the same type: a block of 128 columns of a token times a power
-//    of two.  fp16: its largest element comes to 2^14..2^15, so that bf16's eight bits
-//    are kept down to 2^-25 of it and what is smaller is rounded to 2^-40 of it; columns
-//    2, 3, 6, 7 of each eight are times 2^-4 besides, for their codes' place.  e4m3: its
-//    largest element comes to 2^7..2^8, and an element is the sum of two numbers of
-//    four bits, the second times 2^-4: eight bits as bf16 down to 2^-13 of the largest, what is
-//    smaller is rounded to 2^-21 of it.
-//  * the codes' offset of 8 is taken off as the block's sum, -8 times the sum of the
-//    group's 32, 64 or 128 columns: product * down + sum, times the row's scale.
-// A group's product is scaled in 32 bits, so a result is as exact as the sums in 32
-// bits.  (A scaled weight would have to be rounded.)  A token with an infinity or a
-// NaN gets those throughout.
+// y[token][row] = sum_g s[row][g] sum_{k in g} (code - 8) x[token][k].
 //
 // A block takes a run of chunks (128 columns of a unit's 256 rows) of the list of
 // all units' chunks, the same number as the others, whatever units they belong to;
 // a run of chunks of one unit is a segment.  A unit that several blocks share is
 // joined by the last of them to come, in the order of the columns.
+//
+// Two kernels: few tokens (up to 16) on registers, more on tensor memory.  Both are
+// as exact as sums in 32 bits: no scaled weight and no hidden activation is rounded
+// to bf16.  The tokens are fp16 numbers times a power of two.  A token with an
+// infinity or a NaN gets those throughout.
 using namespace tc;
 
 // A block of tokens as the kernels keep it ("image"), for NT tokens: fp16 [2][NT][64],
-// 64 columns each, or e4m3 [2][NT][128], the elements' first and second numbers, in
-// rows of 128 bytes whose 16-byte pieces are swizzled by the token (piece i at i ^
-// (token & 7)); e4m3 columns 0, 4, 1, 5, 2, 6, 3, 7 of each eight in this order, as a
-// word's codes come apart.  Then float [8][NT]: -8 times the sums of its four 32-column
-// parts, its two halves and the whole, in units of a code's 2^-24 or 2^-9, and the power
-// of two that undoes the block's and is in the sums already.
-__host__ __device__ constexpr int image_bytes(int nt) { return nt * 288; }
-__host__ __device__ constexpr bool image_f8(int nt) { return nt > 16; }
+// 64 columns each, in rows of 128 bytes whose 16-byte pieces are swizzled by the token
+// (piece i at i ^ (token & 7)).
+//  * Few tokens: every token's 128 columns have their own power of two, columns 2, 3,
+//    6, 7 of each eight are times 2^-4 besides, and behind them lies float [8][NT]: -8 times
+//    the sums of the four 32-column parts, the two halves and the whole, in units of
+//    a code's 2^-24, and the power of two that undoes the block's and is in the sums
+//    already.  A block's largest element comes to 2^14..2^15, so that bf16's eight
+//    bits are kept down to 2^-25 of it and what is smaller is rounded to 2^-40 of it.
+//  * More: the power of two is the token's, for all columns.  Behind the images of
+//    all tokens lies int [tokens + 1], the exponents e: |x| < 2^e, kept as x 2^(15 - e), and
+//    last the least that any of them counts for.
+constexpr int FEW = 16;  // tokens
+__host__ __device__ constexpr int image_bytes(int nt) { return nt <= FEW ? nt * 288 : nt * 256; }
 constexpr int SUM_OF = 0, SUM_OF_HALF = 4, SUM_OF_ALL = 6, DOWN = 7;
+constexpr int LEAST = -1000;  // an exponent below all
 
 struct ProductParams {
   W4Shape m;
@@ -284,58 +293,31 @@ struct ProductParams {
   const uint8_t* image;  // [token tiles][chunks]
   uint8_t* image_out;    // the hidden activations', likewise
   int out_chunks;
-  float* parts;   // [token tiles][blocks][2][NT][256]
+  int nt, stages, stage_bytes, bufs;  // more than a few tokens
+  const float* row_up;
+  const int *e_in, *e_out;  // the tokens' exponents, by token
+  int padded;               // tokens of all tiles
+  float* parts;             // [token tiles][blocks][2][NT][256]
   int* counters;  // [token tiles][units]
   int* err;
   int skip_load;
   unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3),
-                 hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
-}
-__device__ __forceinline__ float4 from_e4m3x4(uint32_t v) {
-  const __half2 lo(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3)),
-      hi(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> 16), __NV_E4M3));
-  const float2 a = __half22float2(lo), b = __half22float2(hi);
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-
-// Columns 4 lane .. 4 lane + 3 of a token's block, by a warp, into an image.
-template <bool F8>
+// Columns 4 lane .. 4 lane + 3 of a token's block, by a warp, into an image of few tokens.
 __device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, int lane, const float (&v)[4]) {
   const float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));  // without NaN
   const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
-  // most * 2^e in 2^14..2^15, or 2^7..2^8
-  const int e = min((F8 ? 134 : 141) - static_cast<int>(min(most >> 23, 254u)), 126);
-  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  float sum;
-  if (F8) {
-    const uint32_t first = e4m3x4(v[0] * up, v[1] * up, v[2] * up, v[3] * up);
-    const float4 f = from_e4m3x4(first);
-    const uint32_t second = e4m3x4(16.f * fmaf(v[0], up, -f.x), 16.f * fmaf(v[1], up, -f.y), 16.f * fmaf(v[2], up, -f.z),
-                                   16.f * fmaf(v[3], up, -f.w));
-    const float4 g = from_e4m3x4(second);
-    sum = ((f.x + f.y) + (f.z + f.w)) + 0.0625f * ((g.x + g.y) + (g.z + g.w));
-    // (infinities are cut to the largest number: the sum tells of them, and of NaN)
-    if (most >= 0x7f800000u || !(v[0] + v[1] + v[2] + v[3] == v[0] + v[1] + v[2] + v[3])) sum = __uint_as_float(0x7fc00000u);
-    const bool odd = lane & 1;
-    const uint32_t first2 = __shfl_xor_sync(0xffffffffu, first, 1), second2 = __shfl_xor_sync(0xffffffffu, second, 1);
-    uint8_t* at = image + token * 128 + (((lane >> 2) ^ (token & 7)) << 4) + (lane & 3) * 4;
-    *reinterpret_cast<uint32_t*>(at) = odd ? __byte_perm(first2, first, 0x7362) : __byte_perm(first, first2, 0x5140);
-    *reinterpret_cast<uint32_t*>(at + nt * 128) = odd ? __byte_perm(second2, second, 0x7362) : __byte_perm(second, second2, 0x5140);
-  } else {
-    const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
-    const float2 a = __half22float2(lo), b = __half22float2(hi);
-    sum = (a.x + a.y) + 16.f * (b.x + b.y);
-    uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
-    *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  }
+  const int e = min(141 - static_cast<int>(min(most >> 23, 254u)), 126);  // most * 2^e in 2^14..2^15
+  const float up = pow2(e), down = pow2(-e);
+  const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
+  const float2 a = __half22float2(lo), b = __half22float2(hi);
+  float sum = (a.x + a.y) + 16.f * (b.x + b.y);
+  uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
+  *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  sum *= (F8 ? -0.015625f : -4.76837158203125e-7f) * down;  // -8 * 2^-9, -8 * 2^-24
+  sum *= -4.76837158203125e-7f * down;  // -8 * 2^-24
   const float two = sum + __shfl_xor_sync(0xffffffffu, sum, 8), all = two + __shfl_xor_sync(0xffffffffu, two, 16);
   float* tail = reinterpret_cast<float*>(image + nt * 256) + token;
   if ((lane & 7) == 0) tail[(SUM_OF + (lane >> 3)) * nt] = sum;
@@ -350,16 +332,25 @@ struct PrepareParams {
   int nt, tiles;
   uint8_t* image;  // [tiles][chunks]
   int *err, *counters, n_counters;
+  // more than a few tokens, and hidden activations to come
+  int *e_in, *e_out;
+  const uint32_t* tops;
+  int epi;
+  const __nv_bfloat16* bias;
+  long long n_bias;
 };
 // The kernel before a call's first product: the tokens' blocks, a warp to a token's;
 // clears what the call counts in.  It lets others start when everything before it
 // on the stream is done: the products behind it read their weights without a further wait.
-__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams p) {
+__device__ __forceinline__ void prepare_call(const PrepareParams& p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < p.n_counters; i += gridDim.x * 256) p.counters[i] = 0;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.n_counters; i += gridDim.x * blockDim.x) p.counters[i] = 0;
+}
+__global__ void __launch_bounds__(256) prepare_few_kernel(const __grid_constant__ PrepareParams p) {
+  prepare_call(p);
+  const int lane = threadIdx.x & 31;
   for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < p.tiles * p.chunks * p.nt; i += gridDim.x * 8ll) {
     const long long block = i / p.nt, tile = block / p.chunks, chunk = block - tile * p.chunks;
     const long long e = chunk / p.seg_chunks, col = (chunk - e * p.seg_chunks) * 128 + lane * 4;
@@ -370,10 +361,91 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
       const uint2 w = *reinterpret_cast<const uint2*>(p.x + token * p.x_rs + e * p.x_seg + col);
       v[0] = bf16_at(w.x, 0), v[1] = bf16_at(w.x, 1), v[2] = bf16_at(w.y, 0), v[3] = bf16_at(w.y, 1);
     }
-    if (image_f8(p.nt))
-      store_block<true>(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
-    else
-      store_block<false>(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
+    store_block(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
+  }
+}
+// More tokens: a block to a token, whose largest element it needs before the first
+// is written.  The exponents of the hidden activations are bounds:
+// |a| <= sum |x| 8 max s, the largest scale of the matrix, |silu(a) g| <= |a| |g|,
+// |gelu(z)| <= |z| <= |a| + max |b1|.  A bound some 2^12 above the largest hidden value leaves it
+// 2^3 of fp16's 2^-25 .. 2^15, so that it is rounded to 2^-28 of the largest.
+constexpr int PREPARE_THREADS = 512;
+__device__ __forceinline__ int exponent(float v) { return static_cast<int>(__float_as_uint(v) >> 23 & 255u) - 126; }  // v < 2^it
+__global__ void __launch_bounds__(PREPARE_THREADS) prepare_kernel(const __grid_constant__ PrepareParams p) {
+  prepare_call(p);
+  __shared__ uint32_t s_most[PREPARE_THREADS / 32];
+  __shared__ float s_sum[PREPARE_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = static_cast<int>(p.chunks) * 16;
+  const int padded = p.tiles * p.nt;
+  auto most_of = [&](uint32_t v) {  // of the block, as bits
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0) s_most[warp] = v;
+    __syncthreads();
+    v = __reduce_max_sync(0xffffffffu, s_most[lane & (PREPARE_THREADS / 32 - 1)]);
+    __syncthreads();
+    return v;
+  };
+  for (int token = blockIdx.x; token <= padded; token += gridDim.x) {
+    if (token == padded) {  // the least exponents
+      uint32_t most = 0;
+      for (long long i = threadIdx.x; i < p.n_bias; i += PREPARE_THREADS)
+        most = max(most, __float_as_uint(fabsf(__bfloat162float(p.bias[i]))));
+      most = most_of(most);
+      if (threadIdx.x == 0) p.e_in[token] = LEAST;
+      if (threadIdx.x == 0 && p.e_out) p.e_out[token] = p.n_bias ? exponent(__uint_as_float(most)) + 1 : LEAST;
+      break;
+    }
+    const int tile = token / p.nt, in = token - tile * p.nt;
+    auto piece = [&](int i) {  // eight columns
+      const int chunk = i >> 4, e = chunk / static_cast<int>(p.seg_chunks);
+      const long long col = (chunk - e * p.seg_chunks) * 128 + (i & 15) * 8;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (token < p.n && col < p.seg) w = *reinterpret_cast<const uint4*>(p.x + token * p.x_rs + e * p.x_seg + col);
+      return w;
+    };
+    uint32_t most = 0;
+    for (int i = threadIdx.x; i < pieces; i += PREPARE_THREADS) {
+      const uint4 w = piece(i);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most = max(most, max(v[j] & 0x7fff0000u, (v[j] << 16) & 0x7fff0000u));
+    }
+    most = most_of(most);
+    const int e_x = max(exponent(__uint_as_float(most)), -111);  // 2^(15 - e_x) is a number
+    const float up = pow2(15 - e_x);
+    float sum = 0.f;
+    uint8_t* image = p.image + static_cast<long long>(tile) * p.chunks * image_bytes(p.nt) + in * 128;
+    for (int i = threadIdx.x; i < pieces; i += PREPARE_THREADS) {
+      const uint4 w = piece(i);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = bf16_at(v[j], 0) * up, b = bf16_at(v[j], 1) * up;
+        const __half2 h = __floats2half2_rn(a, b);
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+        sum += fabsf(a) + fabsf(b);
+      }
+      *reinterpret_cast<uint4*>(image + static_cast<long long>(i >> 4) * image_bytes(p.nt) + ((i >> 3) & 1) * (p.nt * 128) +
+                                (((i & 7) ^ (in & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (p.e_out) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      p.e_in[token] = e_x;
+      if (p.e_out) {
+        sum = 0.f;
+        for (int i = 0; i < PREPARE_THREADS / 32; ++i) sum += s_sum[i];
+        const int a = exponent(sum) + e_x - 15 + 3;  // times 8 max s
+        const int of0 = exponent(__uint_as_float(p.tops[0])), of1 = exponent(__uint_as_float(p.tops[1]));
+        p.e_out[token] = p.epi == W4_SWIGLU ? 2 * a + of0 + of1 : a + of0 + 1;
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -384,10 +456,11 @@ struct Wait {
   volatile int* abort_flag;
   int* err;
   unsigned long long timeout_ns;
-  __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity, bool honour_abort) const {
+  __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity, bool honour_abort, bool sleep) const {
     uint64_t t0 = 0;
     for (uint32_t n = 1;; ++n) {
       if (mbar_try_wait(bar, parity)) return true;
+      if (sleep) __nanosleep(256);
       if (n & 63u) continue;
       if (honour_abort && *abort_flag) return false;
       const uint64_t t = global_timer();
@@ -401,14 +474,19 @@ struct Wait {
     }
   }
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    return mbar_try_wait(bar, parity) || slow(bar, parity, true);
+    return mbar_try_wait(bar, parity) || slow(bar, parity, true, false);
   }
   __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
-    if (!mbar_try_wait(bar, parity)) slow(bar, parity, false);
+    if (!mbar_try_wait(bar, parity)) slow(bar, parity, false, false);
   }
   // of a whole warp
   __device__ __forceinline__ void warp(uint64_t* bar, uint32_t parity) const {
-    if (!mbar_try_wait(bar, parity)) slow(bar, parity, true);
+    if (!mbar_try_wait(bar, parity)) slow(bar, parity, true, false);
+    __syncwarp();
+  }
+  // and for what lasts some microseconds: the tries would take the others' issue slots
+  __device__ __forceinline__ void warp_long(uint64_t* bar, uint32_t parity) const {
+    if (!mbar_try_wait(bar, parity)) slow(bar, parity, true, true);
     __syncwarp();
   }
 };
@@ -423,6 +501,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
@@ -471,27 +554,28 @@ struct Run {
 
 // The copying thread: chunks of weights (the packed block as it lies) and of tokens
 // (the image) into a ring of stages, tokens first.
-template <typename R>
-__device__ __forceinline__ void copy_chunks(const ProductParams& p, const Run& run, uint8_t* ring, uint64_t* full,
-                                            uint64_t* empty, const Wait& W) {
+struct Ring {
+  int stages, x_bytes, stage_bytes;
+};
+__device__ __forceinline__ void copy_chunks(const ProductParams& p, const Run& run, const Ring& r, uint8_t* ring,
+                                            uint64_t* full, uint64_t* empty, const Wait& W) {
   // A single token tile reads the weights once.
   const uint64_t often = l2_policy_evict_normal(), once = gridDim.y == 1 ? l2_policy_evict_first() : often;
   const uint8_t* src = p.packed + run.first * p.block_bytes;
-  const uint8_t* image = p.image + static_cast<long long>(blockIdx.y) * p.chunks * image_bytes(R::NT);
+  const uint8_t* image = p.image + static_cast<long long>(blockIdx.y) * p.chunks * r.x_bytes;
   int c = static_cast<int>(run.first % p.chunks);
   auto weights = [&](int stage) {
-    mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(p.block_bytes + image_bytes(R::NT)));
-    bulk_load(ring + stage * R::STAGE + R::X_BYTES, src, static_cast<uint32_t>(p.block_bytes), &full[stage], once);
+    mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(p.block_bytes + r.x_bytes));
+    bulk_load(ring + stage * r.stage_bytes + r.x_bytes, src, static_cast<uint32_t>(p.block_bytes), &full[stage], once);
     src += p.block_bytes;
   };
   auto tokens = [&](int stage) {
-    bulk_load(ring + stage * R::STAGE, image + static_cast<long long>(c) * image_bytes(R::NT), image_bytes(R::NT),
-              &full[stage], often);
+    bulk_load(ring + stage * r.stage_bytes, image + static_cast<long long>(c) * r.x_bytes, r.x_bytes, &full[stage], often);
     if (++c == p.chunks) c = 0;
   };
   // The weights are not the previous kernel's to write (what wrote them is done
   // before the call's first kernel lets others start); the tokens are.
-  const int ahead = run.count < R::STAGES ? run.count : R::STAGES;
+  const int ahead = run.count < r.stages ? run.count : r.stages;
   for (int i = 0; i < ahead; ++i) weights(i);
   grid_dep_wait();
   for (int i = p.skip_load ? 1 : 0; i < ahead; ++i) tokens(i);
@@ -501,21 +585,22 @@ __device__ __forceinline__ void copy_chunks(const ProductParams& p, const Run& r
     if (!W(&empty[stage], phase)) break;
     weights(stage);
     tokens(stage);
-    if (++stage == R::STAGES) {
+    if (++stage == r.stages) {
       stage = 0;
       phase ^= 1;
     }
   }
   // every issued copy lands before the block may exit
-  for (int i = issued > R::STAGES ? issued - R::STAGES : 0; i < issued; ++i) W.drain(&full[i % R::STAGES], (i / R::STAGES) & 1);
+  for (int i = issued > r.stages ? issued - r.stages : 0; i < issued; ++i) W.drain(&full[i % r.stages], (i / r.stages) & 1);
 }
 
-// Four neighbouring rows of a token, by a warp that has 128: bias or activation, and out.
-template <int NT>
-__device__ __forceinline__ void write4(const ProductParams& p, int in_tile, long long row, int lane, float4 v) {
+// Four neighbouring rows of a token, by a warp that has 128: bias or activation, and
+// out.  FEW: into an image of few tokens; else `up` is the hidden activations' factor.
+template <bool FEW_TOKENS>
+__device__ __forceinline__ void write4(const ProductParams& p, int nt, int in_tile, long long row, int lane, float4 v, float up) {
   float a[4] = {v.x, v.y, v.z, v.w};
   if (p.epi == W4_OUT) {
-    const long long token = static_cast<long long>(blockIdx.y) * NT + in_tile;
+    const long long token = static_cast<long long>(blockIdx.y) * nt + in_tile;
     if (token >= p.n || row >= p.m.rows) return;  // rows are a multiple of 8
     if (p.bias) {
 #pragma unroll
@@ -532,19 +617,26 @@ __device__ __forceinline__ void write4(const ProductParams& p, int in_tile, long
     for (int i = 0; i < 4; ++i)
       a[i] = gelu_tanh_f(a[i] + (p.bias && in + i < p.m.s ? __bfloat162float(p.bias[t * p.m.s + in + i]) : 0.f));
   }
-  store_block<image_f8(NT)>(p.image_out + (static_cast<long long>(blockIdx.y) * p.out_chunks + chunk) * image_bytes(NT), NT, in_tile, lane, a);
+  uint8_t* image = p.image_out + (static_cast<long long>(blockIdx.y) * p.out_chunks + chunk) * image_bytes(nt);
+  if (FEW_TOKENS) {
+    store_block(image, nt, in_tile, lane, a);
+  } else {
+    const __half2 lo = __floats2half2_rn(a[0] * up, a[1] * up), hi = __floats2half2_rn(a[2] * up, a[3] * up);
+    uint8_t* at = image + (lane >> 4) * (nt * 128) + in_tile * 128 + ((((lane & 15) >> 1) ^ (in_tile & 7)) << 4) + (lane & 1) * 8;
+    *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
 }
 
 // The end of a segment of `unit`, whose sums lie in shared memory, [token][row], 256
 // rows and a few of padding: out if the segment is the whole unit, else as a part,
-// and the last block of the unit joins the parts.  By the WARPS warps from FIRST on,
-// which then may write the sums anew.
+// and the last block of the unit joins the parts.  By the block's first WARPS
+// warps, which then may write the sums anew.
 constexpr int SUM_PITCH = 256 + 8;
-template <int NT, int WARPS, int FIRST>
+template <int NT, int WARPS>
 __device__ __forceinline__ void finish_segment(const ProductParams& p, long long unit, const float* sum, int* s_last,
                                                const Wait& W) {
   // a thread: rows 4 q .. 4 q + 3 of tile 0 and of tile 1, of a token of every WARPS
-  const int warp = (threadIdx.x >> 5) - FIRST, lane = threadIdx.x & 31, q4 = lane * 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = lane * 4;
   const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
   const int C = gridDim.x;
   const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
@@ -560,7 +652,7 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
     }
     __threadfence();
     bar_sync(1, WARPS * 32);
-    if (threadIdx.x == FIRST * 32) {
+    if (threadIdx.x == 0) {
       __threadfence();
       *s_last = atomicAdd(p.counters + static_cast<long long>(blockIdx.y) * p.units + unit, 1) == c1 - c0;
       __threadfence();
@@ -584,7 +676,7 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
           v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
         }
       }
-      const float one = image_f8(NT) ? 512.f : 16777216.f;  // 2^9, 2^24: a code's unit
+      const float one = 16777216.f;  // 2^24: a code's unit
       v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
       v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
       if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
@@ -592,10 +684,10 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
         v0.y *= sigmoid_f(v0.y) * v1.y;
         v0.z *= sigmoid_f(v0.z) * v1.z;
         v0.w *= sigmoid_f(v0.w) * v1.w;
-        write4<NT>(p, token, unit * 128 + q4, lane, v0);
+        write4<true>(p, NT, token, unit * 128 + q4, lane, v0, 1.f);
       } else {
-        write4<NT>(p, token, unit * 256 + q4, lane, v0);
-        write4<NT>(p, token, unit * 256 + 128 + q4, lane, v1);
+        write4<true>(p, NT, token, unit * 256 + q4, lane, v0, 1.f);
+        write4<true>(p, NT, token, unit * 256 + 128 + q4, lane, v1, 1.f);
       }
     }
   }
@@ -603,7 +695,16 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
 }
 
 // ---------------------------------------------------------------- few tokens
-// Up to 16 tokens: m16n8k16 matrix instructions on registers.  They take 2.05 cycles
+// Up to 16 tokens, bound by the one read of the codes: m16n8k16 matrix instructions on
+// registers.  What is left to count are the instructions that make operands of
+// codes.  A code in the low bits of an fp16 number is a subnormal, code * 2^-24, and four
+// bits higher code * 2^-20: a word's eight codes are four operand registers after one
+// shift and four masks.  (Codes made into bf16 take 11 instructions a word: 102 us
+// instead of 68 for one token of the 70B feed-forward.)  The codes' offset of 8 is
+// taken off as the block's sum, -8 times the sum of the group's 32, 64 or 128
+// columns: product * down + sum, in 32 bits, times the row's scale.
+//
+// The matrix instructions take 2.05 cycles
 // an SM (measured), 8 tokens of a chunk 262 of the some 720 that its bytes take, 16
 // tokens 525; the tensor-memory products take 768 whatever the number of tokens,
 // besides the way of the weights into tensor memory.
@@ -656,7 +757,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   const Wait W{&s_abort, p.err, p.timeout_ns};
   const Run run(p);
   if (warp == FEW_WARPS) {
-    if (lane == 0) copy_chunks<F>(p, run, smem, full, empty, W);
+    if (lane == 0) copy_chunks(p, run, Ring{F::STAGES, F::X_BYTES, F::STAGE}, smem, full, empty, W);
     return;
   }
   const int t = lane & 3, i8 = lane >> 2;
@@ -748,40 +849,39 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
           acc[m][b][h] = 0;
         }
     bar_sync(1, FEW_WARPS * 32);
-    finish_segment<NT, FEW_WARPS, 0>(p, unit, sum, &s_last, W);
+    finish_segment<NT, FEW_WARPS>(p, unit, sum, &s_last, W);
     chunk = 0;
     ++unit;
   }
 }
 
 // ---------------------------------------------------------------- more tokens
-// 32 tokens to a block, several token tiles side by side (the weights come from L2
-// for all but the first).  The weights are the A operand of tcgen05.mma, 128 rows at
-// a time, in tensor memory (in shared memory they would be written and read once
-// more), the tokens its N: 64 columns, both numbers of 32 tokens.  A product (M 128, K
-// 32) takes 46 cycles whatever N up to 64 is, as one of fp16 with K 16 does (measured,
-// from tensor or shared memory).  One block per SM, a step being a group's columns:
-//  * two groups of four warps, a row of tile 0 or 1 to a thread, write the row's
-//    codes to tensor memory as operands, a step ahead of the products;
-//  * two groups of four warps, a row of either tile and 16 tokens to a thread, read a
-//    step's products back while the next's run, scale and add them (a token's two
-//    numbers are loaded once for both rows: shared memory's loads are what the time
-//    goes by, 109 us with a row and all tokens to a thread);
-//  * a warp copies, a warp issues the products.
-// (With fp16 operands a step has 16 products, and the writes of the maker warps on the
-// issuing warp's scheduler wait behind them: 113 us for 32 tokens of the 70B
-// feed-forward.  One thread after the other making operands, waiting and reading
-// back: 116 us.)
+// Up to 128 tokens to a block, several token tiles side by side (the weights come
+// from L2 for all but the first).  The weights are the A operand of tcgen05.mma, 128
+// rows at a time, in tensor memory (in shared memory they would be written and read
+// once more), the tokens its N.  A product (M 128, K 16) takes 47 cycles for N up to 64
+// and 65 for N = 128 (measured).
+//
+// The weights are scaled before the products, so that a product's sums run on over
+// all columns and are read back once a segment: (code - 8) s 2^k in fp16, where 2^k brings the row's
+// largest scale to 2^11..2^12.  (code - 8) s has at most 11 significant bits, as many as fp16
+// keeps: the weights are exact where s is at least 2^-28 of the row's largest, smaller ones
+// are rounded to 2^-36 of it.  One block per SM, a step being 64 columns:
+//  * two groups of four warps, a row of tile 0 or 1 to a thread, make the row's
+//    operands.  The writes of the warps on the issuing warp's scheduler wait behind the
+//    products that were issued before; so operands are written some steps ahead, and
+//    a step is given to the issuing warp only when all but a few steps before it
+//    are done.
+//  * a warp copies, a warp issues the products,
+//  * two groups of four warps, a row of either tile and half of the tokens to a thread,
+//    bring a segment's sums out and finish the units.
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
-template <int NT_>
-struct Ring {
-  static constexpr int NT = NT_, X_BYTES = (image_bytes(NT) + 1023) / 1024 * 1024, STAGE = X_BYTES + 18432;
-  static constexpr int STAGES = 6;
-  static constexpr int M_SUM = STAGES * STAGE, SMEM = M_SUM + NT * SUM_PITCH * 4 + 1024;
-  static constexpr int MAKERS = 8, READERS = 8, WARPS = MAKERS + READERS + 2, THREADS = WARPS * 32;
-  static_assert(SMEM <= 232448 - 1024, "shared memory per block");
-};
+constexpr int MOST = 128;  // tokens of a tile
+__host__ __device__ constexpr int sum_columns(int nt) { return (nt + 31) / 32 * 32; }
+constexpr int MAKERS = 16, READERS = 8, MANY_WARPS = MAKERS + READERS + 2, MANY_THREADS = MANY_WARPS * 32;
+constexpr int MANY_STAGES = 8, MANY_BUFS = 7, MANY_SMEM = 224 * 1024 + 1024;
+static_assert(MANY_SMEM + 2 * 128 * 4 + 512 <= 232448, "shared memory per block");
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -798,105 +898,180 @@ __device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t (&v)[8]) {
                : "r"(at));
 }
 // Waits for loads and names their registers, so that no use of them moves before the wait.
-__device__ __forceinline__ void tmem_loaded(uint32_t (&a)[8], uint32_t (&b)[8], uint32_t (&c)[8], uint32_t (&d)[8]) {
+__device__ __forceinline__ void tmem_loaded(uint32_t (&a)[8], uint32_t (&b)[8]) {
   tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
+  for (int i = 0; i < 8; i += 4)
     asm volatile("" : "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(b[i]), "+r"(b[i + 1]), "+r"(b[i + 2]), "+r"(b[i + 3]));
-    asm volatile("" : "+r"(c[i]), "+r"(c[i + 1]), "+r"(c[i + 2]), "+r"(c[i + 3]), "+r"(d[i]), "+r"(d[i + 1]), "+r"(d[i + 2]), "+r"(d[i + 3]));
-  }
 }
-__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
-// A in tensor memory, four consecutive columns of a row to a 32-bit cell.
-__device__ __forceinline__ void umma_f8_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// A in tensor memory, two consecutive columns of a row to a 32-bit cell.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// (code - 8) * s for the codes of two columns at bits 0-3 and 16-19 (HIGH: 4-7 and
+// 20-23): 1024 + code, or 64 + code, as fp16, less 1032 or 72, times s.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t weights_of(uint32_t w, uint32_t s) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(HIGH ? 0x00f000f0u : 0x000f000fu), "r"(HIGH ? 0x54005400u : 0x64006400u));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(HIGH ? 0x54805480u : 0x64086408u));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(s));
+  return v;
+}
+// Blocks c0 .. c1 share a unit; a block has two places for parts.
+struct Shared {
+  int c0, c1;
+  __device__ __forceinline__ Shared(const ProductParams& p, int unit) {
+    const long long u0 = static_cast<long long>(unit) * p.chunks, u1 = u0 + p.chunks - 1;
+    c0 = static_cast<int>(((u0 + 1) * gridDim.x - 1) / p.total);
+    c1 = static_cast<int>(((u1 + 1) * gridDim.x - 1) / p.total);
+  }
+  __device__ __forceinline__ long long slot(int b) const { return 2 * b + (b == c0); }
+};
+// A unit's sums from its parts and out, by WARPS warps: a thread has rows 4 q .. 4 q +
+// 3 of tile 0 and of tile 1, of two tokens at a time.
+template <int WARPS>
+__device__ __forceinline__ void join_unit(const ProductParams& p, int unit, int warp, const float* s_down, const float* s_up) {
+  const Shared u(p, unit);
+  const int lane = threadIdx.x & 31, q4 = lane * 4;
+  const float4* row_up = reinterpret_cast<const float4*>(p.row_up + unit * 256 + q4);
+  auto scaled = [](float4 v, float4 up, float down) {  // by 2^-k of the rows and the token's
+    auto one = [&](float x, float u) { return x * __uint_as_float(0x7f000000u - __float_as_uint(u)) * down; };
+    return make_float4(one(v.x, up.x), one(v.y, up.y), one(v.z, up.z), one(v.w, up.w));
+  };
+  const float* from = p.parts + static_cast<long long>(blockIdx.y) * gridDim.x * 2 * (p.nt * 256) + q4;
+#pragma unroll 1
+  for (int first = warp; first < p.nt; first += 2 * WARPS) {
+    const int second = first + WARPS < p.nt ? first + WARPS : first;
+    float4 v[2][2] = {};
+#pragma unroll 2
+    for (int b = u.c0; b <= u.c1; ++b) {
+      const float* at = from + u.slot(b) * (p.nt * 256);
+      float4 w[2][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i >> 1][i & 1] = __ldcg(reinterpret_cast<const float4*>(at + (i >> 1 ? second : first) * 256 + (i & 1) * 128));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i >> 1][i & 1] = add4(v[i >> 1][i & 1], w[i >> 1][i & 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int token = i ? second : first;
+      if (i && second == first) break;
+      const float down = s_down[token], up = s_up[token];
+      float4 v0 = scaled(v[i][0], row_up[0], down), v1 = scaled(v[i][1], row_up[32], down);
+      if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
+        v0.x *= sigmoid_f(v0.x) * v1.x;
+        v0.y *= sigmoid_f(v0.y) * v1.y;
+        v0.z *= sigmoid_f(v0.z) * v1.z;
+        v0.w *= sigmoid_f(v0.w) * v1.w;
+        write4<false>(p, p.nt, token, unit * 128ll + q4, lane, v0, up);
+      } else {
+        write4<false>(p, p.nt, token, unit * 256ll + q4, lane, v0, up);
+        write4<false>(p, p.nt, token, unit * 256ll + 128 + q4, lane, v1, up);
+      }
+    }
+  }
+}
 
-template <int NT, int SUBS>
-__global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
-  using R = Ring<NT>;
-  constexpr int KSTEPS = 4 / SUBS;  // K = 32 steps of a group
+template <int SUBS>
+__global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // of a buffer: operands written, products done, products read
-  __shared__ uint64_t full[R::STAGES], empty[R::STAGES], a_full[2], d_full[2], d_free[2], drain;
+  // of a buffer of operands: written, products done; of the sums: complete, read
+  __shared__ uint64_t full[MANY_STAGES], empty[MANY_STAGES], a_full[MANY_BUFS], a_free[MANY_BUFS], d_full, d_free, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort, s_last;
+  __shared__ float s_down[MOST], s_up[MOST];  // what undoes the tokens' powers of two; the hidden activations'
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R::STAGES; ++i) {
+    for (int i = 0; i < MANY_STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], R::MAKERS + R::READERS);
+      mbar_init(&empty[i], MAKERS + 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], R::MAKERS);
-      mbar_init(&d_full[i], 1);
-      mbar_init(&d_free[i], R::READERS);
+    for (int i = 0; i < MANY_BUFS; ++i) {
+      mbar_init(&a_full[i], MAKERS / 2);
+      mbar_init(&a_free[i], 1);
     }
+    mbar_init(&d_full, 1);
+    mbar_init(&d_free, READERS);
     mbar_init(&drain, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == R::WARPS - 1) tmem_alloc(&tmem_slot, 512);
+  if (warp == MANY_WARPS - 1) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();
-  // operands of a tile's buffer at 128 tile + 64 buffer (32 columns), products 256 columns on
-  const uint32_t tmem = tmem_slot;
+  // the sums of tile 0 and of tile 1, then the buffers, 32 columns for either tile
+  const uint32_t tmem = tmem_slot, d_cols = sum_columns(p.nt), a_tmem = tmem + 2 * d_cols;
   const Wait W{&s_abort, p.err, p.timeout_ns};
   const Run run(p);
+  const int x_bytes = p.nt * 256;
 
-  if (warp == R::WARPS - 2) {
-    if (lane == 0) copy_chunks<R>(p, run, smem, full, empty, W);
+  if (warp == MANY_WARPS - 2) {
+    if (lane == 0) copy_chunks(p, run, Ring{p.stages, x_bytes, p.stage_bytes}, smem, full, empty, W);
     __syncwarp();
-  } else if (warp == R::WARPS - 1) {
+  } else if (warp == MANY_WARPS - 1) {
     // ------------------------------------------------ products
     // The warp stays together and one lane waits and issues: what a product is told is
-    // the same for all lanes, else it takes three times as long to issue.  One wait
-    // a step beside the chunk's, for both tiles: a wait takes 150 cycles even where
-    // it finds what it waits for.
+    // the same for all lanes, else it takes three times as long to issue.
     const bool leader = elect_one();
-    constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(2 * NT >> 3) << 17) | (8u << 24);  // e4m3 x e4m3 -> fp32, M = 128
+    const uint32_t id = (1u << 4) | (static_cast<uint32_t>(p.nt >> 3) << 17) | (8u << 24);  // fp16 x fp16 -> fp32, M = 128
     const uint64_t x_desc = sw128_desc(smem_u32(smem), 16);
-    int stage = 0;
-    uint32_t phase = 0, step = 0;
+    int stage = 0, buf = 0, chunk = static_cast<int>(run.first % p.chunks);
+    uint32_t a_phase = 0, d_phase = 1;
+    bool fresh = true;  // of a unit's sums
 #pragma unroll 1
     for (int i = 0; i < run.count; ++i) {
-      if (leader) W(&full[stage], phase);
-      const uint64_t xd = x_desc + static_cast<uint64_t>(stage * (R::STAGE >> 4));
+      const uint64_t xd = x_desc + static_cast<uint64_t>(stage * (p.stage_bytes >> 4));
+      const bool last = ++chunk == p.chunks || i + 1 == run.count;
 #pragma unroll
-      for (int sub = 0; sub < SUBS; ++sub, ++step) {
-        const uint32_t buf = step & 1, at = tmem + buf * 64;
-        if (leader) W(&a_full[buf], (step >> 1) & 1);
+      for (int half = 0; half < 2; ++half) {
+        if (leader) {
+          if (half == 0 && fresh) W(&d_free, d_phase);
+          W(&a_full[buf], a_phase);  // (the tokens have landed, else there were no operands)
+        }
         __syncwarp();
         tc_fence_after();
         if (leader) {
+          const uint64_t xh = xd + static_cast<uint64_t>(half * (p.nt * 128 >> 4));
 #pragma unroll
-          for (int tile = 0; tile < 2; ++tile)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int k = 0; k < KSTEPS; ++k) {
-              const int ks = sub * KSTEPS + k;
-              umma_f8_ta(at + 256 + tile * 128, at + tile * 128 + k * 8, xd + static_cast<uint64_t>(ks * 32 >> 4), ID, k > 0);
-            }
-          umma_commit(&d_full[buf]);
+            for (int tile = 0; tile < 2; ++tile)
+              umma_f16_ta(tmem + tile * d_cols, a_tmem + buf * 64 + tile * 32 + k * 8, xh + static_cast<uint64_t>(k * 32 >> 4), id,
+                          !(fresh && half == 0 && k == 0));
+          umma_commit(&a_free[buf]);
+          if (half == 1) {
+            umma_commit(&empty[stage]);
+            if (last) umma_commit(&d_full);
+          }
         }
         __syncwarp();
+        if (++buf == p.bufs) {
+          buf = 0;
+          a_phase ^= 1;
+        }
       }
-      if (++stage == R::STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
+      if (fresh) d_phase ^= 1;
+      fresh = last;
+      if (last) chunk = 0;
+      if (++stage == p.stages) stage = 0;
     }
     if (leader) {
       umma_commit(&drain);
@@ -905,126 +1080,132 @@ __global__ void __launch_bounds__(Ring<NT>::THREADS, 1) product_kernel(const __g
     __syncwarp();
   } else {
     const int quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    int stage = 0;
-    uint32_t phase = 0, step = 0;
-    if (warp < R::MAKERS) {
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    if (warp < MAKERS) {
       // ------------------------------------------------ operands
-      const int tile = warp >> 2;
-      const uint32_t at_w = R::X_BYTES + tile * 8192 + r * 64, swz = (r >> 1) & 3;
-      constexpr int PIECES = 4 / SUBS;
-#pragma unroll 1
-      for (int i = 0; i < run.count; ++i) {
-        const uint32_t st = smem_u32(smem) + stage * R::STAGE;
-        W.warp(&full[stage], phase);
-        uint4 v[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] = ld_shared_v4(st + at_w + ((t ^ swz) << 4));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
-#pragma unroll
-        for (int sub = 0; sub < SUBS; ++sub, ++step) {
-          const uint32_t buf = step & 1, uses = step >> 1, at = lanes + tile * 128 + buf * 64;
-          W.warp(&d_full[buf], (uses & 1) ^ 1);  // the products that had the buffer are done
-          tc_fence_after();
-#pragma unroll
-          for (int q = 0; q < PIECES; ++q) {
-            const int word = sub * PIECES + q;
-            uint32_t o[8];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const uint32_t w = word == 0 ? v[t].x : word == 1 ? v[t].y : word == 2 ? v[t].z : v[t].w;
-              o[2 * t] = w & 0x0f0f0f0fu;
-              o[2 * t + 1] = (w >> 4) & 0x0f0f0f0fu;
-            }
-            tmem_store8(at + q * 8, o);
-          }
-          tmem_wait_st();
-          W.warp(&d_free[buf], (uses & 1) ^ 1);  // and read
-          tc_fence_before();
-          if (lane == 0) mbar_arrive(&a_full[buf]);
-        }
-        if (++stage == R::STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-    } else {
-      // ------------------------------------------------ products back, sums
-      const int token0 = ((warp - R::MAKERS) >> 2) * (NT / 2);
-      const uint32_t at_s = R::X_BYTES + 16384 + r * 2;
-      float* sum = reinterpret_cast<float*>(smem + R::M_SUM);
-      grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
-      uint64_t acc[2][NT / 4] = {};  // rows r and 128 + r
-      const uint64_t second = pack2(0.0625f, 0.0625f);
+      const int tile = (warp >> 2) & 1, half = warp >> 3;
+      const uint32_t at_w = x_bytes + tile * 8192 + r * 64 + half * 8, swz = (r >> 1) & 3;
+      const uint32_t at_s = x_bytes + 16384 + (tile * 128 + r) * 2;
+      int stage = 0, buf = half;
+      uint32_t phase = 0, a_phase = 1;
       long long unit = run.first / p.chunks;
       int chunk = static_cast<int>(run.first - unit * p.chunks);
+      const float* up_at = p.row_up + unit * 256 + tile * 128 + r;
+      float up = *up_at, next = unit + 1 < p.units ? up_at[256] : 0.f;
 #pragma unroll 1
       for (int i = 0; i < run.count; ++i) {
-        const uint32_t st = smem_u32(smem) + stage * R::STAGE;
+        const uint32_t st = smem_u32(smem) + stage * p.stage_bytes;
+        W.warp(&full[stage], phase);
+        uint2 v[4];
 #pragma unroll
-        for (int sub = 0; sub < SUBS; ++sub, ++step) {
-          const uint32_t buf = step & 1, at = lanes + 256 + buf * 64 + token0;
-          W.warp(&d_full[buf], (step >> 1) & 1);  // (the chunk has landed, else there were no products)
-          tc_fence_after();
-          constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
-          const uint32_t at_sum = st + NT * 256 + ((FIRST + sub) * NT + token0) * 4, at_down = st + NT * 256 + (DOWN * NT + token0) * 4;
-          const float s0 = ld_shared_scale(st + at_s + sub * 512), s1 = ld_shared_scale(st + at_s + sub * 512 + 256);
-          const uint64_t s2[2] = {pack2(s0, s0), pack2(s1, s1)};
+        for (int t = 0; t < 4; ++t) v[t] = ld_shared_v2(st + at_w + ((t ^ swz) << 4));
+        uint32_t s[2];
 #pragma unroll
-          for (int c = 0; c < NT / 2; c += 8) {  // eight tokens
-            uint32_t d[2][2][8];  // [tile][number]
-#pragma unroll
-            for (int m = 0; m < 4; ++m) tmem_load8(at + (m >> 1) * 128 + (m & 1) * NT + c, d[m >> 1][m & 1]);
-            uint64_t sums[4], down[4];
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(sums[j]), "=l"(sums[j + 1]) : "r"(at_sum + (c + 2 * j) * 4));
-              asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(down[j]), "=l"(down[j + 1]) : "r"(at_down + (c + 2 * j) * 4));
-            }
-            tmem_loaded(d[0][0], d[0][1], d[1][0], d[1][1]);
-            if (c + 8 == NT / 2) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&d_free[buf]);
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                auto two = [&](int k) { return pack2(__uint_as_float(d[m][k][2 * j]), __uint_as_float(d[m][k][2 * j + 1])); };
-                uint64_t& a = acc[m][c / 2 + j];
-                a = fma2(s2[m], fma2(fma2(second, two(1), two(0)), down[j], sums[j]), a);
-              }
-          }
+        for (int q = 0; q < 2; ++q) {
+          const float scale = ld_shared_scale(st + at_s + (SUBS == 4 ? 2 * half + q : SUBS == 2 ? half : 0) * 512) * up;
+          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(s[q]) : "f"(scale));
         }
-        __syncwarp();
+        W.warp(&a_free[buf], a_phase);  // the products that had the buffer are done
+        tc_fence_after();
+        const uint32_t at = a_tmem + lanes + buf * 64 + tile * 32;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[16];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t w = q == 0 ? v[t].x : v[t].y, w8 = w >> 8;
+            o[4 * t] = weights_of<false>(w, s[q]);
+            o[4 * t + 1] = weights_of<true>(w, s[q]);
+            o[4 * t + 2] = weights_of<false>(w8, s[q]);
+            o[4 * t + 3] = weights_of<true>(w8, s[q]);
+          }
+          tmem_store16(at + q * 16, o);
+        }
         if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == R::STAGES) {
+        if (++stage == p.stages) {
           stage = 0;
           phase ^= 1;
         }
-        if (++chunk < p.chunks && i + 1 < run.count) continue;
+        if (++chunk == p.chunks) {
+          chunk = 0;
+          up = next;
+          up_at += 256;
+          if (++unit + 1 < p.units) next = up_at[256];
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a_full[buf]);
+        buf += 2;
+        if (buf >= p.bufs) {
+          buf -= p.bufs;
+          a_phase ^= 1;
+        }
+      }
+      bar_sync(2, (MAKERS + READERS) * 32);
+      if (s_last) join_unit<MAKERS + READERS>(p, static_cast<int>((run.first + run.count - 1) / p.chunks), warp, s_down, s_up);
+    } else {
+      // ------------------------------------------------ sums, units
+      const int half = (warp - MAKERS) >> 2, token0 = half * (p.nt / 2), tokens = p.nt / 2;
+      grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
+      float* parts = p.parts + static_cast<long long>(blockIdx.y) * gridDim.x * 2 * (p.nt * 256) + token0 * 256 + r;
+      {
+        const long long at = static_cast<long long>(blockIdx.y) * p.nt + threadIdx.x - MAKERS * 32;
+        if (threadIdx.x - MAKERS * 32 < p.nt) {
+          s_down[threadIdx.x - MAKERS * 32] = pow2(max(p.e_in[at], p.e_in[p.padded]) - 15);
+          s_up[threadIdx.x - MAKERS * 32] = p.e_out ? pow2(15 - max(p.e_out[at], p.e_out[p.padded])) : 1.f;
+        }
+      }
+      const int end = static_cast<int>((run.first + run.count - 1) / p.chunks);
+      uint32_t phase = 0;
+#pragma unroll 1
+      for (int unit = static_cast<int>(run.first / p.chunks); unit <= end; ++unit) {
+        const Shared u(p, unit);
+        W.warp_long(&d_full, phase);
+        phase ^= 1;
+        tc_fence_after();
+        float* to = parts + u.slot(blockIdx.x) * (p.nt * 256);
+#pragma unroll 1
+        for (int c = 0; c < tokens; c += 8) {
+          uint32_t a[8], b[8];
+          tmem_load8(tmem + lanes + token0 + c, a);
+          tmem_load8(tmem + lanes + d_cols + token0 + c, b);
+          tmem_loaded(a, b);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int j = 0; j < NT / 4; ++j) {
-            const float2 v = unpack2(acc[m][j]);
-            float* to = sum + (token0 + 2 * j) * SUM_PITCH + m * 128 + r;
-            to[0] = v.x;
-            to[SUM_PITCH] = v.y;
-            acc[m][j] = 0;
+          for (int j = 0; j < 8; ++j) {
+            __stcg(to + (c + j) * 256, __uint_as_float(a[j]));
+            __stcg(to + (c + j) * 256 + 128, __uint_as_float(b[j]));
           }
-        bar_sync(1, R::READERS * 32);
-        finish_segment<NT, R::READERS, R::MAKERS>(p, unit, sum, &s_last, W);
-        chunk = 0;
-        ++unit;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_free);
+        if (u.c0 != u.c1) __threadfence();
+        bar_sync(1, READERS * 32);
+        if (threadIdx.x == MAKERS * 32) {
+          bool last = true;
+          if (u.c0 != u.c1) {
+            __threadfence();
+            last = atomicAdd(p.counters + static_cast<long long>(blockIdx.y) * p.units + unit, 1) == u.c1 - u.c0;
+            __threadfence();
+          }
+          s_last = last && *W.abort_flag == 0;
+        }
+        // the operands' warps help with the block's last
+        if (unit == end) {
+          bar_sync(2, (MAKERS + READERS) * 32);
+          if (s_last) join_unit<MAKERS + READERS>(p, unit, warp, s_down, s_up);
+        } else {
+          bar_sync(1, READERS * 32);
+          if (s_last) join_unit<READERS>(p, unit, warp - MAKERS, s_down, s_up);
+          bar_sync(1, READERS * 32);  // the block's parts and s_last have been read
+        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == R::WARPS - 1) {
+  if (warp == MANY_WARPS - 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1067,12 +1248,10 @@ int launch_few(const ProductParams& p, dim3 grid, cudaStream_t st) {
   if (p.m.group == 64) return launch_inst<few_kernel<NT, 2>, FEW_THREADS, SMEM>(grid, st, p);
   return launch_inst<few_kernel<NT, 4>, FEW_THREADS, SMEM>(grid, st, p);
 }
-template <int NT>
 int launch_product(const ProductParams& p, dim3 grid, cudaStream_t st) {
-  constexpr int SMEM = Ring<NT>::SMEM;
-  if (p.m.group == 128) return launch_inst<product_kernel<NT, 1>, Ring<NT>::THREADS, SMEM>(grid, st, p);
-  if (p.m.group == 64) return launch_inst<product_kernel<NT, 2>, Ring<NT>::THREADS, SMEM>(grid, st, p);
-  return launch_inst<product_kernel<NT, 4>, Ring<NT>::THREADS, SMEM>(grid, st, p);
+  if (p.m.group == 128) return launch_inst<product_kernel<1>, MANY_THREADS, MANY_SMEM>(grid, st, p);
+  if (p.m.group == 64) return launch_inst<product_kernel<2>, MANY_THREADS, MANY_SMEM>(grid, st, p);
+  return launch_inst<product_kernel<4>, MANY_THREADS, MANY_SMEM>(grid, st, p);
 }
 
 // How a product of n tokens is cut: NT tokens to a block, `tiles` of them, `blocks`
@@ -1082,13 +1261,28 @@ struct Cut {
 };
 Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
   Cut c;
-  c.nt = n <= 8 ? 8 : n <= 16 ? 16 : 32;
-  c.tiles = static_cast<int>((n + c.nt - 1) / c.nt);
-  const int64_t most = c.nt <= 16 ? 2 * num_sms : std::max(num_sms / c.tiles, 1), total = m.units() * m.chunks();
-  c.blocks = static_cast<int>(std::min<int64_t>(most, total));
+  if (n <= FEW) {
+    c.nt = n <= 8 ? 8 : 16;
+    c.tiles = 1;
+    c.blocks = 2 * num_sms;
+  } else {
+    c.tiles = static_cast<int>((n + MOST - 1) / MOST);
+    c.nt = static_cast<int>(((n + c.tiles - 1) / c.tiles + 15) / 16 * 16);
+    // up to four waves of blocks, the fewest that leave little of the last empty
+    double best = 0;
+    for (int waves = 1; waves <= 4 && best < 0.92; ++waves) {
+      const int per = std::max(waves * num_sms / c.tiles, 1), all = per * c.tiles;
+      const double used = static_cast<double>(all) / ((all + num_sms - 1) / num_sms * num_sms);
+      if (used > best) best = used, c.blocks = per;
+    }
+  }
+  c.blocks = static_cast<int>(std::min<int64_t>(c.blocks, m.units() * m.chunks()));
   return c;
 }
+// Where the exponents of an image of n tokens lie.
+int64_t image_end(const W4Shape& m, const Cut& c) { return m.chunks() * c.tiles * image_bytes(c.nt); }
 
+int64_t hidden_chunks(const W4Shape& m) { return m.T * m.sp / 128; }
 // A grid of at most 32 blocks per SM.
 unsigned grid_of(long long blocks) { return static_cast<unsigned>(std::min<long long>(std::max<long long>(blocks, 1), 32 * 152)); }
 int launched() { return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA; }
@@ -1136,9 +1330,14 @@ int launch_w4_dequantize(const void* codes, const void* scales, int64_t rows, in
 
 int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack, cudaStream_t st) {
   using namespace w4;
-  pack_kernel<<<grid_of(m.units() * m.chunks()), 256, 0, st>>>(m, c, static_cast<uint8_t*>(packed), unpack);
-  if (unpack)
-    unpack_codes_kernel<<<grid_of(m.tiles()), 256, 0, st>>>(m, c, static_cast<const uint8_t*>(packed));
+  auto* to = static_cast<uint8_t*>(packed);
+  pack_kernel<<<grid_of(m.units() * m.chunks()), 256, 0, st>>>(m, c, to, unpack);
+  if (unpack) {
+    unpack_codes_kernel<<<grid_of(m.tiles()), 256, 0, st>>>(m, c, to);
+  } else {
+    if (cudaMemsetAsync(m.tops(to), 0, 16, st) != cudaSuccess) return TP_ERR_CUDA;
+    tops_kernel<<<static_cast<unsigned>(m.units()), 256, 0, st>>>(m, to);
+  }
   return launched();
 }
 
@@ -1150,7 +1349,7 @@ int64_t w4_product_counters(const W4Shape& m, int64_t n) { return m.units() * ((
 
 size_t w4_image_bytes(const W4Shape& m, int64_t n) {
   const w4::Cut c = w4::cut_of(m, n, 1);
-  return static_cast<size_t>(m.chunks()) * c.tiles * w4::image_bytes(c.nt);
+  return static_cast<size_t>(w4::image_end(m, c)) + (static_cast<size_t>(c.tiles) * c.nt + 1) * sizeof(int);
 }
 
 int launch_w4_prepare(const W4Product& a, int* err, int64_t n_counters, LaunchCtx& ctx) {
@@ -1170,10 +1369,28 @@ int launch_w4_prepare(const W4Product& a, int* err, int64_t n_counters, LaunchCt
   p.err = err;
   p.counters = a.counters;
   p.n_counters = static_cast<int>(n_counters);
-  const int64_t warps = p.tiles * p.chunks * p.nt;
+  const bool few = c.nt <= FEW;
+  unsigned blocks;
+  if (few) {
+    blocks = static_cast<unsigned>(std::min<int64_t>((p.tiles * p.chunks * p.nt + 7) / 8, 8 * ctx.num_sms));
+  } else {
+    p.e_in = reinterpret_cast<int*>(p.image + image_end(a.m, c));
+    if (a.epi != W4_OUT) {
+      p.e_out = reinterpret_cast<int*>(static_cast<uint8_t*>(a.image_out) + hidden_chunks(a.m) * c.tiles * image_bytes(c.nt));
+      p.tops = a.m.tops(const_cast<void*>(a.packed));
+      p.epi = a.epi;
+      if (a.epi == W4_GELU && a.bias) {
+        p.bias = static_cast<const __nv_bfloat16*>(a.bias);
+        p.n_bias = a.m.T * a.m.s;
+      }
+    }
+    blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.nt + 1, 4 * ctx.num_sms));
+  }
   if (ctx.before) ctx.before(ctx.user, "prepare4", ctx.stream);
-  launch_dep(prepare_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, 8 * ctx.num_sms))), 256, 0,
-             ctx.stream, p);
+  if (few)
+    launch_dep(prepare_few_kernel, dim3(blocks), 256, 0, ctx.stream, p);
+  else
+    launch_dep(prepare_kernel, dim3(blocks), PREPARE_THREADS, 0, ctx.stream, p);
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
   return launched();
@@ -1196,7 +1413,7 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.image = static_cast<const uint8_t*>(a.image);
   p.image_out = static_cast<uint8_t*>(a.image_out);
-  p.out_chunks = a.epi == W4_OUT ? 0 : static_cast<int>(a.m.T * a.m.sp / 128);
+  p.out_chunks = a.epi == W4_OUT ? 0 : static_cast<int>(hidden_chunks(a.m));
   p.parts = static_cast<float*>(a.scratch);
   p.counters = a.counters;
   p.err = ctx.err;
@@ -1210,8 +1427,18 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
     rc = launch_few<8>(p, grid, ctx.stream);
   else if (c.nt == 16)
     rc = launch_few<16>(p, grid, ctx.stream);
-  else
-    rc = launch_product<32>(p, grid, ctx.stream);
+  else {
+    p.nt = c.nt;
+    p.stage_bytes = image_bytes(c.nt) + (p.block_bytes + 1023) / 1024 * 1024;
+    p.stages = std::min((MANY_SMEM - 1024) / p.stage_bytes, MANY_STAGES);
+    p.bufs = (512 - 2 * sum_columns(c.nt)) / 64;
+    p.row_up = a.m.row_up(const_cast<void*>(a.packed));
+    p.padded = c.tiles * c.nt;
+    p.e_in = reinterpret_cast<const int*>(p.image + image_end(a.m, c));
+    if (a.epi != W4_OUT)
+      p.e_out = reinterpret_cast<const int*>(p.image_out + static_cast<int64_t>(p.out_chunks) * c.tiles * image_bytes(c.nt));
+    rc = launch_product(p, grid, ctx.stream);
+  }
   if (rc) return rc;
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
