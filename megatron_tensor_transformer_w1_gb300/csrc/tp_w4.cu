@@ -297,8 +297,10 @@ struct ProductParams {
   const float* row_up;
   const int *e_in, *e_out;  // the tokens' exponents, by token
   int padded;               // tokens of all tiles
-  float* parts;             // [token tiles][blocks][2][NT][256]
-  int* counters;  // [token tiles][units]
+  int blocks;               // runs of chunks
+  // few tokens: [blocks][2][NT][256], else [token tiles][blocks + units - 1][NT][256]
+  float* parts;
+  int* counters;  // few tokens: [units]
   int* err;
   int skip_load;
   unsigned long long timeout_ns;
@@ -597,10 +599,10 @@ __device__ __forceinline__ void copy_chunks(const ProductParams& p, const Run& r
 // Four neighbouring rows of a token, by a warp that has 128: bias or activation, and
 // out.  FEW: into an image of few tokens; else `up` is the hidden activations' factor.
 template <bool FEW_TOKENS>
-__device__ __forceinline__ void write4(const ProductParams& p, int nt, int in_tile, long long row, int lane, float4 v, float up) {
+__device__ __forceinline__ void write4(const ProductParams& p, int nt, int tile, int in_tile, long long row, int lane, float4 v, float up) {
   float a[4] = {v.x, v.y, v.z, v.w};
   if (p.epi == W4_OUT) {
-    const long long token = static_cast<long long>(blockIdx.y) * nt + in_tile;
+    const long long token = static_cast<long long>(tile) * nt + in_tile;
     if (token >= p.n || row >= p.m.rows) return;  // rows are a multiple of 8
     if (p.bias) {
 #pragma unroll
@@ -617,7 +619,7 @@ __device__ __forceinline__ void write4(const ProductParams& p, int nt, int in_ti
     for (int i = 0; i < 4; ++i)
       a[i] = gelu_tanh_f(a[i] + (p.bias && in + i < p.m.s ? __bfloat162float(p.bias[t * p.m.s + in + i]) : 0.f));
   }
-  uint8_t* image = p.image_out + (static_cast<long long>(blockIdx.y) * p.out_chunks + chunk) * image_bytes(nt);
+  uint8_t* image = p.image_out + (static_cast<long long>(tile) * p.out_chunks + chunk) * image_bytes(nt);
   if (FEW_TOKENS) {
     store_block(image, nt, in_tile, lane, a);
   } else {
@@ -641,7 +643,7 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
   const int C = gridDim.x;
   const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
   bool store = true;
-  float* parts = p.parts + static_cast<long long>(blockIdx.y) * C * 2 * (NT * 256) + q4;
+  float* parts = p.parts + q4;
   auto slot = [&](int b) { return static_cast<long long>(2 * b + (b == c0)) * (NT * 256); };
   if (c0 != c1) {
     float* to = parts + slot(blockIdx.x);
@@ -654,7 +656,7 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
     bar_sync(1, WARPS * 32);
     if (threadIdx.x == 0) {
       __threadfence();
-      *s_last = atomicAdd(p.counters + static_cast<long long>(blockIdx.y) * p.units + unit, 1) == c1 - c0;
+      *s_last = atomicAdd(p.counters + unit, 1) == c1 - c0;
       __threadfence();
     }
     bar_sync(1, WARPS * 32);
@@ -684,10 +686,10 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
         v0.y *= sigmoid_f(v0.y) * v1.y;
         v0.z *= sigmoid_f(v0.z) * v1.z;
         v0.w *= sigmoid_f(v0.w) * v1.w;
-        write4<true>(p, NT, token, unit * 128 + q4, lane, v0, 1.f);
+        write4<true>(p, NT, 0, token, unit * 128 + q4, lane, v0, 1.f);
       } else {
-        write4<true>(p, NT, token, unit * 256 + q4, lane, v0, 1.f);
-        write4<true>(p, NT, token, unit * 256 + 128 + q4, lane, v1, 1.f);
+        write4<true>(p, NT, 0, token, unit * 256 + q4, lane, v0, 1.f);
+        write4<true>(p, NT, 0, token, unit * 256 + 128 + q4, lane, v1, 1.f);
       }
     }
   }
@@ -874,7 +876,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 //    are done.
 //  * a warp copies, a warp issues the products,
 //  * two groups of four warps, a row of either tile and half of the tokens to a thread,
-//    bring a segment's sums out and finish the units.
+//    bring a segment's sums out.
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
 constexpr int MOST = 128;  // tokens of a tile
@@ -930,62 +932,6 @@ __device__ __forceinline__ uint32_t weights_of(uint32_t w, uint32_t s) {
   asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(s));
   return v;
 }
-// Blocks c0 .. c1 share a unit; a block has two places for parts.
-struct Shared {
-  int c0, c1;
-  __device__ __forceinline__ Shared(const ProductParams& p, int unit) {
-    const long long u0 = static_cast<long long>(unit) * p.chunks, u1 = u0 + p.chunks - 1;
-    c0 = static_cast<int>(((u0 + 1) * gridDim.x - 1) / p.total);
-    c1 = static_cast<int>(((u1 + 1) * gridDim.x - 1) / p.total);
-  }
-  __device__ __forceinline__ long long slot(int b) const { return 2 * b + (b == c0); }
-};
-// A unit's sums from its parts and out, by WARPS warps: a thread has rows 4 q .. 4 q +
-// 3 of tile 0 and of tile 1, of two tokens at a time.
-template <int WARPS>
-__device__ __forceinline__ void join_unit(const ProductParams& p, int unit, int warp, const float* s_down, const float* s_up) {
-  const Shared u(p, unit);
-  const int lane = threadIdx.x & 31, q4 = lane * 4;
-  const float4* row_up = reinterpret_cast<const float4*>(p.row_up + unit * 256 + q4);
-  auto scaled = [](float4 v, float4 up, float down) {  // by 2^-k of the rows and the token's
-    auto one = [&](float x, float u) { return x * __uint_as_float(0x7f000000u - __float_as_uint(u)) * down; };
-    return make_float4(one(v.x, up.x), one(v.y, up.y), one(v.z, up.z), one(v.w, up.w));
-  };
-  const float* from = p.parts + static_cast<long long>(blockIdx.y) * gridDim.x * 2 * (p.nt * 256) + q4;
-#pragma unroll 1
-  for (int first = warp; first < p.nt; first += 2 * WARPS) {
-    const int second = first + WARPS < p.nt ? first + WARPS : first;
-    float4 v[2][2] = {};
-#pragma unroll 2
-    for (int b = u.c0; b <= u.c1; ++b) {
-      const float* at = from + u.slot(b) * (p.nt * 256);
-      float4 w[2][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i >> 1][i & 1] = __ldcg(reinterpret_cast<const float4*>(at + (i >> 1 ? second : first) * 256 + (i & 1) * 128));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i >> 1][i & 1] = add4(v[i >> 1][i & 1], w[i >> 1][i & 1]);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int token = i ? second : first;
-      if (i && second == first) break;
-      const float down = s_down[token], up = s_up[token];
-      float4 v0 = scaled(v[i][0], row_up[0], down), v1 = scaled(v[i][1], row_up[32], down);
-      if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
-        v0.x *= sigmoid_f(v0.x) * v1.x;
-        v0.y *= sigmoid_f(v0.y) * v1.y;
-        v0.z *= sigmoid_f(v0.z) * v1.z;
-        v0.w *= sigmoid_f(v0.w) * v1.w;
-        write4<false>(p, p.nt, token, unit * 128ll + q4, lane, v0, up);
-      } else {
-        write4<false>(p, p.nt, token, unit * 256ll + q4, lane, v0, up);
-        write4<false>(p, p.nt, token, unit * 256ll + 128 + q4, lane, v1, up);
-      }
-    }
-  }
-}
-
 template <int SUBS>
 __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -993,13 +939,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   // of a buffer of operands: written, products done; of the sums: complete, read
   __shared__ uint64_t full[MANY_STAGES], empty[MANY_STAGES], a_full[MANY_BUFS], a_free[MANY_BUFS], d_full, d_free, drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort, s_last;
-  __shared__ float s_down[MOST], s_up[MOST];  // what undoes the tokens' powers of two; the hidden activations'
+  __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MANY_STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], MAKERS + 1);
+      mbar_init(&empty[i], MAKERS / 2 + 1);
     }
     for (int i = 0; i < MANY_BUFS; ++i) {
       mbar_init(&a_full[i], MAKERS / 2);
@@ -1083,90 +1028,97 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     if (warp < MAKERS) {
       // ------------------------------------------------ operands
-      const int tile = (warp >> 2) & 1, half = warp >> 3;
-      const uint32_t at_w = x_bytes + tile * 8192 + r * 64 + half * 8, swz = (r >> 1) & 3;
+      // of every other chunk
+      const int tile = (warp >> 2) & 1, odd = warp >> 3;
+      const uint32_t at_w = x_bytes + tile * 8192 + r * 64, swz = (r >> 1) & 3;
       const uint32_t at_s = x_bytes + 16384 + (tile * 128 + r) * 2;
-      int stage = 0, buf = half;
+      int stage = odd, buf = 2 * odd;
       uint32_t phase = 0, a_phase = 1;
-      long long unit = run.first / p.chunks;
-      int chunk = static_cast<int>(run.first - unit * p.chunks);
-      const float* up_at = p.row_up + unit * 256 + tile * 128 + r;
-      float up = *up_at, next = unit + 1 < p.units ? up_at[256] : 0.f;
+      auto next_buf = [&] {
+        if (++buf == p.bufs) {
+          buf = 0;
+          a_phase ^= 1;
+        }
+      };
+      long long unit = (run.first + odd) / p.chunks;
+      int chunk = static_cast<int>(run.first + odd - unit * p.chunks);
+      const float* up_at = p.row_up + tile * 128 + r;
+      float up = unit < p.units ? up_at[unit * 256] : 0.f, next = unit + 1 < p.units ? up_at[(unit + 1) * 256] : 0.f;
 #pragma unroll 1
-      for (int i = 0; i < run.count; ++i) {
+      for (int i = odd; i < run.count; i += 2) {
         const uint32_t st = smem_u32(smem) + stage * p.stage_bytes;
         W.warp(&full[stage], phase);
-        uint2 v[4];
+        uint4 v[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] = ld_shared_v2(st + at_w + ((t ^ swz) << 4));
-        uint32_t s[2];
+        for (int t = 0; t < 4; ++t) v[t] = ld_shared_v4(st + at_w + ((t ^ swz) << 4));
+        uint32_t s[SUBS];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float scale = ld_shared_scale(st + at_s + (SUBS == 4 ? 2 * half + q : SUBS == 2 ? half : 0) * 512) * up;
-          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(s[q]) : "f"(scale));
+        for (int j = 0; j < SUBS; ++j) {
+          const float scale = ld_shared_scale(st + at_s + j * 512) * up;
+          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(s[j]) : "f"(scale));
         }
-        W.warp(&a_free[buf], a_phase);  // the products that had the buffer are done
-        tc_fence_after();
-        const uint32_t at = a_tmem + lanes + buf * 64 + tile * 32;
+        int given = buf;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < 4; ++q) {  // 32 columns
+          if (q == 0 || q == 2) {
+            W.warp(&a_free[buf], a_phase);  // the products that had the buffer are done
+            tc_fence_after();
+          }
           uint32_t o[16];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const uint32_t w = q == 0 ? v[t].x : v[t].y, w8 = w >> 8;
-            o[4 * t] = weights_of<false>(w, s[q]);
-            o[4 * t + 1] = weights_of<true>(w, s[q]);
-            o[4 * t + 2] = weights_of<false>(w8, s[q]);
-            o[4 * t + 3] = weights_of<true>(w8, s[q]);
+            const uint32_t w = q == 0 ? v[t].x : q == 1 ? v[t].y : q == 2 ? v[t].z : v[t].w, w8 = w >> 8;
+            const uint32_t sq = s[q * SUBS / 4];
+            o[4 * t] = weights_of<false>(w, sq);
+            o[4 * t + 1] = weights_of<true>(w, sq);
+            o[4 * t + 2] = weights_of<false>(w8, sq);
+            o[4 * t + 3] = weights_of<true>(w8, sq);
           }
-          tmem_store16(at + q * 16, o);
+          if (q == 2) {  // the first half is written by now
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&a_full[given]);
+            given = buf;
+          }
+          tmem_store16(a_tmem + lanes + buf * 64 + tile * 32 + (q & 1) * 16, o);
+          if (q & 1) next_buf();
         }
         if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == p.stages) {
-          stage = 0;
+        stage += 2;
+        if (stage >= p.stages) {
+          stage -= p.stages;
           phase ^= 1;
         }
-        if (++chunk == p.chunks) {
-          chunk = 0;
-          up = next;
-          up_at += 256;
-          if (++unit + 1 < p.units) next = up_at[256];
+        chunk += 2;
+        if (chunk >= p.chunks) {  // (a unit of one chunk: the next but one)
+          const int units = chunk / p.chunks;
+          chunk -= units * p.chunks;
+          unit += units;
+          up = units == 1 ? next : unit < p.units ? up_at[unit * 256] : 0.f;
+          next = unit + 1 < p.units ? up_at[(unit + 1) * 256] : 0.f;
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&a_full[buf]);
-        buf += 2;
-        if (buf >= p.bufs) {
-          buf -= p.bufs;
-          a_phase ^= 1;
-        }
+        if (lane == 0) mbar_arrive(&a_full[given]);
+        next_buf();  // the other warps' two
+        next_buf();
       }
-      bar_sync(2, (MAKERS + READERS) * 32);
-      if (s_last) join_unit<MAKERS + READERS>(p, static_cast<int>((run.first + run.count - 1) / p.chunks), warp, s_down, s_up);
     } else {
-      // ------------------------------------------------ sums, units
-      const int half = (warp - MAKERS) >> 2, token0 = half * (p.nt / 2), tokens = p.nt / 2;
-      grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
-      float* parts = p.parts + static_cast<long long>(blockIdx.y) * gridDim.x * 2 * (p.nt * 256) + token0 * 256 + r;
-      {
-        const long long at = static_cast<long long>(blockIdx.y) * p.nt + threadIdx.x - MAKERS * 32;
-        if (threadIdx.x - MAKERS * 32 < p.nt) {
-          s_down[threadIdx.x - MAKERS * 32] = pow2(max(p.e_in[at], p.e_in[p.padded]) - 15);
-          s_up[threadIdx.x - MAKERS * 32] = p.e_out ? pow2(15 - max(p.e_out[at], p.e_out[p.padded])) : 1.f;
-        }
-      }
+      // ------------------------------------------------ sums
+      const int token0 = ((warp - MAKERS) >> 2) * (p.nt / 2);
+      grid_dep_wait();  // nobody reads the parts of before
+      float* parts = p.parts + (static_cast<long long>(blockIdx.y) * (p.blocks + p.units - 1) + blockIdx.x) * (p.nt * 256) + token0 * 256 + r;
       const int end = static_cast<int>((run.first + run.count - 1) / p.chunks);
       uint32_t phase = 0;
 #pragma unroll 1
-      for (int unit = static_cast<int>(run.first / p.chunks); unit <= end; ++unit) {
-        const Shared u(p, unit);
+      for (int unit = static_cast<int>(run.first / p.chunks); unit <= end; ++unit, phase ^= 1) {
         W.warp_long(&d_full, phase);
-        phase ^= 1;
         tc_fence_after();
-        float* to = parts + u.slot(blockIdx.x) * (p.nt * 256);
+        float* to = parts + static_cast<long long>(unit) * (p.nt * 256);
 #pragma unroll 1
-        for (int c = 0; c < tokens; c += 8) {
+        for (int c = 0; c < p.nt / 2; c += 8) {
           uint32_t a[8], b[8];
           tmem_load8(tmem + lanes + token0 + c, a);
           tmem_load8(tmem + lanes + d_cols + token0 + c, b);
@@ -1180,26 +1132,6 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_free);
-        if (u.c0 != u.c1) __threadfence();
-        bar_sync(1, READERS * 32);
-        if (threadIdx.x == MAKERS * 32) {
-          bool last = true;
-          if (u.c0 != u.c1) {
-            __threadfence();
-            last = atomicAdd(p.counters + static_cast<long long>(blockIdx.y) * p.units + unit, 1) == u.c1 - u.c0;
-            __threadfence();
-          }
-          s_last = last && *W.abort_flag == 0;
-        }
-        // the operands' warps help with the block's last
-        if (unit == end) {
-          bar_sync(2, (MAKERS + READERS) * 32);
-          if (s_last) join_unit<MAKERS + READERS>(p, unit, warp, s_down, s_up);
-        } else {
-          bar_sync(1, READERS * 32);
-          if (s_last) join_unit<READERS>(p, unit, warp - MAKERS, s_down, s_up);
-          bar_sync(1, READERS * 32);  // the block's parts and s_last have been read
-        }
       }
     }
   }
@@ -1208,6 +1140,50 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   if (warp == MANY_WARPS - 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// The parts of a unit's sums, in the order of the columns, to outputs or hidden
+// activations: a warp to a token, four rows of tile 0 and four of tile 1 to a thread.
+// Its own kernel, as then all of the device takes part; the block that came last
+// doing it cost 8 us for 64 tokens of an output projection and 14 for 128 of the 70B
+// feed-forward, this costs some 3.
+constexpr int FINISH_TOKENS = 8;
+__global__ void __launch_bounds__(FINISH_TOKENS * 32) finish_kernel(const __grid_constant__ ProductParams p) {
+  grid_dep_launch();
+  const int unit = blockIdx.x, tile = blockIdx.z, in_tile = blockIdx.y * FINISH_TOKENS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, q4 = lane * 4;
+  const long long token = static_cast<long long>(tile) * p.nt + in_tile;
+  const long long u0 = static_cast<long long>(unit) * p.chunks, u1 = u0 + p.chunks - 1;
+  const int c0 = static_cast<int>(((u0 + 1) * p.blocks - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * p.blocks - 1) / p.total);
+  const float* from = p.parts + ((static_cast<long long>(tile) * (p.blocks + p.units - 1) + c0 + unit) * p.nt + in_tile) * 256 + q4;
+  const float4 up0 = *reinterpret_cast<const float4*>(p.row_up + unit * 256 + q4),
+               up1 = *reinterpret_cast<const float4*>(p.row_up + unit * 256 + 128 + q4);
+  grid_dep_wait();
+  if (token >= p.n) return;
+  const float down = pow2(max(p.e_in[token], p.e_in[p.padded]) - 15);
+  const float up = p.e_out ? pow2(15 - max(p.e_out[token], p.e_out[p.padded])) : 1.f;
+  float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+#pragma unroll 4
+  for (int b = c0; b <= c1; ++b, from += p.nt * 256) {
+    v0 = add4(v0, __ldcg(reinterpret_cast<const float4*>(from)));
+    v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
+  }
+  auto scaled = [&](float4 v, float4 u) {  // by 2^-k of the rows and the token's
+    auto one = [&](float x, float k) { return x * __uint_as_float(0x7f000000u - __float_as_uint(k)) * down; };
+    return make_float4(one(v.x, u.x), one(v.y, u.y), one(v.z, u.z), one(v.w, u.w));
+  };
+  v0 = scaled(v0, up0);
+  v1 = scaled(v1, up1);
+  if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
+    v0.x *= sigmoid_f(v0.x) * v1.x;
+    v0.y *= sigmoid_f(v0.y) * v1.y;
+    v0.z *= sigmoid_f(v0.z) * v1.z;
+    v0.w *= sigmoid_f(v0.w) * v1.w;
+    write4<false>(p, p.nt, tile, in_tile, unit * 128ll + q4, lane, v0, up);
+  } else {
+    write4<false>(p, p.nt, tile, in_tile, unit * 256ll + q4, lane, v0, up);
+    write4<false>(p, p.nt, tile, in_tile, unit * 256ll + 128 + q4, lane, v1, up);
   }
 }
 
@@ -1343,9 +1319,10 @@ int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack,
 
 size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms) {
   const w4::Cut c = w4::cut_of(m, n, num_sms);
-  return static_cast<size_t>(c.blocks) * c.tiles * 2 * 256 * c.nt * sizeof(float);
+  const size_t places = c.nt <= w4::FEW ? 2 * c.blocks : c.tiles * (c.blocks + m.units() - 1);
+  return places * 256 * c.nt * sizeof(float);
 }
-int64_t w4_product_counters(const W4Shape& m, int64_t n) { return m.units() * ((n + 15) / 16); }
+int64_t w4_product_counters(const W4Shape& m, int64_t n) { return n <= w4::FEW ? m.units() : 0; }
 
 size_t w4_image_bytes(const W4Shape& m, int64_t n) {
   const w4::Cut c = w4::cut_of(m, n, 1);
@@ -1437,11 +1414,19 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
     p.e_in = reinterpret_cast<const int*>(p.image + image_end(a.m, c));
     if (a.epi != W4_OUT)
       p.e_out = reinterpret_cast<const int*>(p.image_out + static_cast<int64_t>(p.out_chunks) * c.tiles * image_bytes(c.nt));
+    p.blocks = c.blocks;
     rc = launch_product(p, grid, ctx.stream);
   }
   if (rc) return rc;
   if (ctx.after) ctx.after(ctx.user, ctx.stream);
   ctx.launches++;
+  if (c.nt > FEW) {
+    if (ctx.before) ctx.before(ctx.user, "finish4", ctx.stream);
+    launch_dep(finish_kernel, dim3(static_cast<unsigned>(p.units), static_cast<unsigned>(c.nt / FINISH_TOKENS), static_cast<unsigned>(c.tiles)),
+               FINISH_TOKENS * 32, 0, ctx.stream, p);
+    if (ctx.after) ctx.after(ctx.user, ctx.stream);
+    ctx.launches++;
+  }
   return launched();
 }
 
