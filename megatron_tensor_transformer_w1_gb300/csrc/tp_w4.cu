@@ -869,20 +869,19 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // largest scale to 2^11..2^12.  (code - 8) s has at most 11 significant bits, as many as fp16
 // keeps: the weights are exact where s is at least 2^-28 of the row's largest, smaller ones
 // are rounded to 2^-36 of it.  One block per SM, a step being 64 columns:
-//  * two groups of four warps, a row of tile 0 or 1 to a thread, make the row's
-//    operands.  The writes of the warps on the issuing warp's scheduler wait behind the
-//    products that were issued before; so operands are written some steps ahead, and
-//    a step is given to the issuing warp only when all but a few steps before it
-//    are done.
-//  * a warp copies, a warp issues the products,
-//  * two groups of four warps, a row of either tile and half of the tokens to a thread,
-//    bring a segment's sums out.
+//  * three groups of eight warps, each for every third chunk, a row of tile 0 or 1 to
+//    a thread, make the row's operands, and bring a segment's sums out behind its last
+//    chunk.  What a group does for a chunk takes some 2400 cycles, most of them waiting
+//    (for the chunk, for a free buffer, for the operands to be written), which is why there
+//    are three; the writes of the warps on the issuing warp's scheduler moreover wait
+//    behind the products that were issued before.
+//  * a warp copies, a warp issues the products.
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
 constexpr int MOST = 128;  // tokens of a tile
 __host__ __device__ constexpr int sum_columns(int nt) { return (nt + 31) / 32 * 32; }
-constexpr int MAKERS = 16, READERS = 8, MANY_WARPS = MAKERS + READERS + 2, MANY_THREADS = MANY_WARPS * 32;
-constexpr int MANY_STAGES = 8, MANY_BUFS = 7, MANY_SMEM = 224 * 1024 + 1024;
+constexpr int GROUP = 8, GROUPS = 2, MANY_WARPS = GROUP * GROUPS + 2, MANY_THREADS = MANY_WARPS * 32;
+constexpr int MANY_STAGES = 8, MANY_BUFS = 3, MANY_SMEM = 224 * 1024 + 1024;
 static_assert(MANY_SMEM + 2 * 128 * 4 + 512 <= 232448, "shared memory per block");
 
 __device__ __forceinline__ bool elect_one() {
@@ -936,22 +935,21 @@ template <int SUBS>
 __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // of a buffer of operands: written, products done; of the sums: complete, read
-  __shared__ uint64_t full[MANY_STAGES], empty[MANY_STAGES], a_full[MANY_BUFS], a_free[MANY_BUFS], d_full, d_free, drain;
+  // of a buffer of operands: written, products done; of the sums: read
+  __shared__ uint64_t full[MANY_STAGES], empty[MANY_STAGES], a_full[MANY_BUFS], a_free[MANY_BUFS], d_free, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MANY_STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], MAKERS / 2 + 1);
+      mbar_init(&empty[i], GROUP + 1);
     }
     for (int i = 0; i < MANY_BUFS; ++i) {
-      mbar_init(&a_full[i], MAKERS / 2);
+      mbar_init(&a_full[i], GROUP);
       mbar_init(&a_free[i], 1);
     }
-    mbar_init(&d_full, 1);
-    mbar_init(&d_free, READERS);
+    mbar_init(&d_free, GROUP);
     mbar_init(&drain, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -962,8 +960,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();
-  // the sums of tile 0 and of tile 1, then the buffers, 32 columns for either tile
-  const uint32_t tmem = tmem_slot, d_cols = sum_columns(p.nt), a_tmem = tmem + 2 * d_cols;
+  // the sums of tile 0 and of tile 1, then the buffers, 64 columns for either tile.  All of
+  // tensor memory is the block's: it starts at 0 (and that the compiler knows it makes
+  // issuing products cheaper).
+  const uint32_t d_cols = sum_columns(p.nt), a_tmem = 2 * d_cols;
   const Wait W{&s_abort, p.err, p.timeout_ns};
   const Run run(p);
   const int x_bytes = p.nt * 256;
@@ -984,38 +984,32 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
 #pragma unroll 1
     for (int i = 0; i < run.count; ++i) {
       const uint64_t xd = x_desc + static_cast<uint64_t>(stage * (p.stage_bytes >> 4));
-      const bool last = ++chunk == p.chunks || i + 1 == run.count;
+      if (leader) {
+        if (fresh) W(&d_free, d_phase);
+        W(&a_full[buf], a_phase);  // (the tokens have landed, else there were no operands)
+      }
+      __syncwarp();
+      tc_fence_after();
+      if (leader) {
+        const uint32_t at = a_tmem + buf * 128;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (leader) {
-          if (half == 0 && fresh) W(&d_free, d_phase);
-          W(&a_full[buf], a_phase);  // (the tokens have landed, else there were no operands)
-        }
-        __syncwarp();
-        tc_fence_after();
-        if (leader) {
-          const uint64_t xh = xd + static_cast<uint64_t>(half * (p.nt * 128 >> 4));
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t xk = xd + static_cast<uint64_t>((k >> 2) * (p.nt * 128 >> 4) + ((k & 3) * 32 >> 4));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int tile = 0; tile < 2; ++tile)
-              umma_f16_ta(tmem + tile * d_cols, a_tmem + buf * 64 + tile * 32 + k * 8, xh + static_cast<uint64_t>(k * 32 >> 4), id,
-                          !(fresh && half == 0 && k == 0));
-          umma_commit(&a_free[buf]);
-          if (half == 1) {
-            umma_commit(&empty[stage]);
-            if (last) umma_commit(&d_full);
-          }
+          for (int tile = 0; tile < 2; ++tile)
+            umma_f16_ta(tile * d_cols, at + tile * 64 + k * 8, xk, id, k > 0 || !fresh);
         }
-        __syncwarp();
-        if (++buf == p.bufs) {
-          buf = 0;
-          a_phase ^= 1;
-        }
+        umma_commit(&a_free[buf]);
+        umma_commit(&empty[stage]);
+      }
+      __syncwarp();
+      if (++buf == p.bufs) {
+        buf = 0;
+        a_phase ^= 1;
       }
       if (fresh) d_phase ^= 1;
-      fresh = last;
-      if (last) chunk = 0;
+      fresh = ++chunk == p.chunks;
+      if (fresh) chunk = 0;
       if (++stage == p.stages) stage = 0;
     }
     if (leader) {
@@ -1026,112 +1020,95 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   } else {
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    if (warp < MAKERS) {
-      // ------------------------------------------------ operands
-      // of every other chunk
-      const int tile = (warp >> 2) & 1, odd = warp >> 3;
-      const uint32_t at_w = x_bytes + tile * 8192 + r * 64, swz = (r >> 1) & 3;
-      const uint32_t at_s = x_bytes + 16384 + (tile * 128 + r) * 2;
-      int stage = odd, buf = 2 * odd;
-      uint32_t phase = 0, a_phase = 1;
-      auto next_buf = [&] {
-        if (++buf == p.bufs) {
-          buf = 0;
-          a_phase ^= 1;
-        }
-      };
-      long long unit = (run.first + odd) / p.chunks;
-      int chunk = static_cast<int>(run.first + odd - unit * p.chunks);
-      const float* up_at = p.row_up + tile * 128 + r;
-      float up = unit < p.units ? up_at[unit * 256] : 0.f, next = unit + 1 < p.units ? up_at[(unit + 1) * 256] : 0.f;
+    // ------------------------------------------------ operands, and the sums back
+    const int tile = (warp >> 2) & 1, group = warp / GROUP;
+    const uint32_t at_w = x_bytes + tile * 8192 + r * 64, swz = (r >> 1) & 3;
+    const uint32_t at_s = x_bytes + 16384 + (tile * 128 + r) * 2;
+    int stage = group, buf = group;
+    uint32_t phase = 0, a_phase = 1;
+    if (buf >= p.bufs) {
+      buf -= p.bufs;
+      a_phase ^= 1;
+    }
+    int unit = static_cast<int>(run.first / p.chunks), chunk = static_cast<int>(run.first - static_cast<long long>(unit) * p.chunks) + group;
+    for (; chunk >= p.chunks; chunk -= p.chunks) ++unit;
+    const float* up_at = p.row_up + tile * 128 + r;
+    float up = unit < p.units ? up_at[unit * 256] : 0.f, next = unit + 1 < p.units ? up_at[(unit + 1) * 256] : 0.f;
+    float* parts = p.parts + (static_cast<long long>(blockIdx.y) * (p.blocks + p.units - 1) + blockIdx.x) * (p.nt * 256) + tile * 128 + r;
+    bool waited = false;
 #pragma unroll 1
-      for (int i = odd; i < run.count; i += 2) {
-        const uint32_t st = smem_u32(smem) + stage * p.stage_bytes;
-        W.warp(&full[stage], phase);
-        uint4 v[4];
+    for (int i = group; i < run.count; i += GROUPS) {
+      const uint32_t st = smem_u32(smem) + stage * p.stage_bytes;
+      W.warp(&full[stage], phase);
+      uint4 v[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] = ld_shared_v4(st + at_w + ((t ^ swz) << 4));
-        uint32_t s[SUBS];
+      for (int t = 0; t < 4; ++t) v[t] = ld_shared_v4(st + at_w + ((t ^ swz) << 4));
+      uint32_t s[SUBS];
 #pragma unroll
-        for (int j = 0; j < SUBS; ++j) {
-          const float scale = ld_shared_scale(st + at_s + j * 512) * up;
-          asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(s[j]) : "f"(scale));
-        }
-        int given = buf;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // 32 columns
-          if (q == 0 || q == 2) {
-            W.warp(&a_free[buf], a_phase);  // the products that had the buffer are done
-            tc_fence_after();
-          }
-          uint32_t o[16];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t w = q == 0 ? v[t].x : q == 1 ? v[t].y : q == 2 ? v[t].z : v[t].w, w8 = w >> 8;
-            const uint32_t sq = s[q * SUBS / 4];
-            o[4 * t] = weights_of<false>(w, sq);
-            o[4 * t + 1] = weights_of<true>(w, sq);
-            o[4 * t + 2] = weights_of<false>(w8, sq);
-            o[4 * t + 3] = weights_of<true>(w8, sq);
-          }
-          if (q == 2) {  // the first half is written by now
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[given]);
-            given = buf;
-          }
-          tmem_store16(a_tmem + lanes + buf * 64 + tile * 32 + (q & 1) * 16, o);
-          if (q & 1) next_buf();
-        }
-        if (lane == 0) mbar_arrive(&empty[stage]);
-        stage += 2;
-        if (stage >= p.stages) {
-          stage -= p.stages;
-          phase ^= 1;
-        }
-        chunk += 2;
-        if (chunk >= p.chunks) {  // (a unit of one chunk: the next but one)
-          const int units = chunk / p.chunks;
-          chunk -= units * p.chunks;
-          unit += units;
-          up = units == 1 ? next : unit < p.units ? up_at[unit * 256] : 0.f;
-          next = unit + 1 < p.units ? up_at[(unit + 1) * 256] : 0.f;
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a_full[given]);
-        next_buf();  // the other warps' two
-        next_buf();
+      for (int j = 0; j < SUBS; ++j) {
+        const float scale = ld_shared_scale(st + at_s + j * 512) * up;
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(s[j]) : "f"(scale));
       }
-    } else {
-      // ------------------------------------------------ sums
-      const int token0 = ((warp - MAKERS) >> 2) * (p.nt / 2);
-      grid_dep_wait();  // nobody reads the parts of before
-      float* parts = p.parts + (static_cast<long long>(blockIdx.y) * (p.blocks + p.units - 1) + blockIdx.x) * (p.nt * 256) + token0 * 256 + r;
-      const int end = static_cast<int>((run.first + run.count - 1) / p.chunks);
-      uint32_t phase = 0;
-#pragma unroll 1
-      for (int unit = static_cast<int>(run.first / p.chunks); unit <= end; ++unit, phase ^= 1) {
-        W.warp_long(&d_full, phase);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // 32 columns
+        uint32_t o[16];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t w = q == 0 ? v[t].x : q == 1 ? v[t].y : q == 2 ? v[t].z : v[t].w, w8 = w >> 8;
+          const uint32_t sq = s[q * SUBS / 4];
+          o[4 * t] = weights_of<false>(w, sq);
+          o[4 * t + 1] = weights_of<true>(w, sq);
+          o[4 * t + 2] = weights_of<false>(w8, sq);
+          o[4 * t + 3] = weights_of<true>(w8, sq);
+        }
+        if (q == 0) {
+          W.warp(&a_free[buf], a_phase);  // the products that had the buffer are done
+          tc_fence_after();
+        }
+        tmem_store16(a_tmem + lanes + buf * 128 + tile * 64 + q * 16, o);
+      }
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      stage += GROUPS;
+      if (stage >= p.stages) {
+        stage -= p.stages;
+        phase ^= 1;
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[buf]);
+      if (chunk + 1 == p.chunks || i + 1 == run.count) {
+        // a segment's last chunk: the sums back, a row of one tile to a thread
+        W.warp_long(&a_free[buf], a_phase ^ 1);  // its products are done, so all are
         tc_fence_after();
+        if (!waited) grid_dep_wait();  // nobody reads the parts of before
+        waited = true;
         float* to = parts + static_cast<long long>(unit) * (p.nt * 256);
+        const uint32_t from = lanes + tile * d_cols;
 #pragma unroll 1
-        for (int c = 0; c < p.nt / 2; c += 8) {
+        for (int c = 0; c < p.nt; c += 16) {
           uint32_t a[8], b[8];
-          tmem_load8(tmem + lanes + token0 + c, a);
-          tmem_load8(tmem + lanes + d_cols + token0 + c, b);
+          tmem_load8(from + c, a);
+          tmem_load8(from + c + 8, b);
           tmem_loaded(a, b);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             __stcg(to + (c + j) * 256, __uint_as_float(a[j]));
-            __stcg(to + (c + j) * 256 + 128, __uint_as_float(b[j]));
+            __stcg(to + (c + j + 8) * 256, __uint_as_float(b[j]));
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_free);
+      }
+      for (buf += GROUPS; buf >= p.bufs; buf -= p.bufs) a_phase ^= 1;
+      chunk += GROUPS;
+      if (chunk >= p.chunks) {
+        const int units = chunk / p.chunks;  // more than one where units are short
+        chunk -= units * p.chunks;
+        unit += units;
+        up = units == 1 ? next : unit < p.units ? up_at[unit * 256] : 0.f;
+        next = unit + 1 < p.units ? up_at[(unit + 1) * 256] : 0.f;
       }
     }
   }
@@ -1139,7 +1116,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   __syncthreads();
   if (warp == MANY_WARPS - 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem_slot, 512);
   }
 }
 
@@ -1408,7 +1385,7 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
     p.nt = c.nt;
     p.stage_bytes = image_bytes(c.nt) + (p.block_bytes + 1023) / 1024 * 1024;
     p.stages = std::min((MANY_SMEM - 1024) / p.stage_bytes, MANY_STAGES);
-    p.bufs = (512 - 2 * sum_columns(c.nt)) / 64;
+    p.bufs = (512 - 2 * sum_columns(c.nt)) / 128;
     p.row_up = a.m.row_up(const_cast<void*>(a.packed));
     p.padded = c.tiles * c.nt;
     p.e_in = reinterpret_cast<const int*>(p.image + image_end(a.m, c));
