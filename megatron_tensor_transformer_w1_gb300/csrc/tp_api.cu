@@ -1578,6 +1578,31 @@ W4Shape w4_qkv(const tp_attn_plan* a, int group) {
   return m;
 }
 
+// A product's tokens go through it in parts of some hundred, equal but for the last,
+// so that the sums, which lie in the workspace in 32 bits, stay in L2 and the workspace
+// stays small.  512: the weights are read once for what takes them seven times as
+// long in products.
+constexpr int64_t kTokens4 = 512;
+int64_t part4(int64_t n) {
+  const int64_t parts = (n + kTokens4 - 1) / kTokens4;
+  return parts ? (n + parts - 1) / parts : 0;
+}
+struct Need4 {
+  size_t parts = 0, image = 0;
+  int64_t counters = 0;
+};
+Need4 need4(const W4Shape& m, int64_t n) {
+  Need4 r;
+  const int64_t per = part4(n), last = per ? (n - 1) % per + 1 : 0;
+  for (const int64_t k : {per, last}) {
+    if (k == 0) continue;
+    r.parts = std::max(r.parts, w4_product_scratch(m, k, num_sms_current()));
+    r.image = std::max(r.image, w4_image_bytes(m, k));
+    r.counters = std::max(r.counters, w4_product_counters(m, k));
+  }
+  return r;
+}
+
 // Workspace of a forward pass: error word, the products' counters and parts (of
 // one product at a time), the blocks of the tokens and of the hidden activations.
 struct Ws4 {
@@ -1586,28 +1611,17 @@ struct Ws4 {
 };
 Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
   Ws4 L;
-  const int sms = num_sms_current();
-  const W4Shape up = w4_up(p, 128), down = w4_down(p, 128);
-  size_t parts = w4_product_scratch(down, n, sms), off = kAlign;
-  L.n_down = w4_product_counters(down, n);
-  if (p->act != TP_ACT_NONE) {
-    L.n_up = w4_product_counters(up, n);
-    const size_t u = w4_product_scratch(up, n, sms);
-    if (u > parts) parts = u;
-  }
-  L.counters = off;
-  off += align_up(static_cast<size_t>(L.n_up + L.n_down) * sizeof(int));
-  L.parts = off;
-  off += align_up(parts);
-  L.x = off;
-  off += align_up(w4_image_bytes(p->act != TP_ACT_NONE ? up : down, n));
-  L.h = off;
-  if (p->act != TP_ACT_NONE)
-    off += align_up(w4_image_bytes(down, n));
-  L.total = off;
+  const bool none = p->act == TP_ACT_NONE;
+  const Need4 down = need4(w4_down(p, 128), n), up = none ? Need4() : need4(w4_up(p, 128), n);
+  L.n_up = up.counters;
+  L.n_down = down.counters;
+  L.counters = kAlign;
+  L.parts = L.counters + align_up(static_cast<size_t>(L.n_up + L.n_down) * sizeof(int));
+  L.x = L.parts + align_up(std::max(up.parts, down.parts));
+  L.h = L.x + align_up(none ? down.image : up.image);
+  L.total = L.h + (none ? 0 : align_up(down.image));
   return L;
 }
-constexpr int64_t kMaxTokens4 = int64_t(1) << 18;
 
 // The launch context of a 4-bit call, without the launch that clears the error word.
 void ctx4(const tp_ffn_plan* p, void* workspace, int flags, cudaStream_t stream, LaunchCtx& ctx) {
@@ -1624,41 +1638,62 @@ void ctx4(const tp_ffn_plan* p, void* workspace, int flags, cudaStream_t stream,
   }
 }
 
-int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n, const void* x, const void* w13, const void* w2,
+int fwd4_impl(const tp_ffn_plan* p, int group, int64_t n_all, const void* x, const void* w13, const void* w2,
               const void* b1, const void* b2, void* y, char* ws, LaunchCtx& ctx) {
-  const Ws4 L = ws4_layout(p, n);
-  W4Product g;
-  g.n = n;
-  g.x = x;
-  g.scratch = ws + L.parts;
-  g.counters = reinterpret_cast<int*>(ws + L.counters);
-  g.image = ws + L.x;
-  W4Product down = g;
-  down.name = "down4";
-  down.m = w4_down(p, group);
-  down.packed = w2;
-  down.x_seg = p->s;
-  down.x_rs = p->d_ff;
-  down.bias = b2;
-  down.out = y;
-  down.out_rs = p->d;
-  if (p->act == TP_ACT_NONE) {
-    if (int rc = launch_w4_prepare(down, ctx.err, L.n_down, ctx)) return rc;
-    return launch_w4_product(down, ctx);
+  const Ws4 L = ws4_layout(p, n_all);
+  const bool none = p->act == TP_ACT_NONE;
+  const int64_t per = part4(n_all), x_rs = none ? p->d_ff : p->d;
+  int* err = ctx.err;
+  for (int64_t at = 0; at < n_all; at += per, err = nullptr) {
+    W4Product g;
+    g.n = std::min(per, n_all - at);
+    g.x = static_cast<const char*>(x) + at * x_rs * 2;
+    g.x_rs = x_rs;
+    g.scratch = ws + L.parts;
+    g.counters = reinterpret_cast<int*>(ws + L.counters);
+    g.image = ws + L.x;
+    W4Product down = g;
+    down.name = "down4";
+    down.m = w4_down(p, group);
+    down.packed = w2;
+    down.x_seg = p->s;
+    down.bias = b2;
+    down.out = static_cast<char*>(y) + at * p->d * 2;
+    down.out_rs = p->d;
+    if (none) {
+      int rc = launch_w4_prepare(down, err, L.n_down, ctx);
+      if (!rc) rc = launch_w4_product(down, ctx);
+      if (rc) return rc;
+      continue;
+    }
+    g.name = p->act == TP_ACT_SWIGLU ? "up_swiglu4" : "up_gelu4";
+    g.m = w4_up(p, group);
+    g.packed = w13;
+    g.epi = p->act == TP_ACT_SWIGLU ? W4_SWIGLU : W4_GELU;
+    g.bias = b1;
+    g.image_out = ws + L.h;
+    down.image = ws + L.h;
+    down.counters += L.n_up;
+    int rc = launch_w4_prepare(g, err, L.n_up + L.n_down, ctx);
+    if (!rc) rc = launch_w4_product(g, ctx);
+    if (!rc) rc = launch_w4_product(down, ctx);
+    if (rc) return rc;
   }
-  g.name = p->act == TP_ACT_SWIGLU ? "up_swiglu4" : "up_gelu4";
-  g.m = w4_up(p, group);
-  g.packed = w13;
-  g.x_rs = p->d;
-  g.epi = p->act == TP_ACT_SWIGLU ? W4_SWIGLU : W4_GELU;
-  g.bias = b1;
-  g.image_out = ws + L.h;
-  int rc = launch_w4_prepare(g, ctx.err, L.n_up + L.n_down, ctx);
-  if (!rc) rc = launch_w4_product(g, ctx);
-  if (rc) return rc;
-  down.image = ws + L.h;
-  down.counters += L.n_up;
-  return launch_w4_product(down, ctx);
+  return TP_OK;
+}
+// A product of all its tokens, with what makes their blocks.
+int product4(const W4Product& all, int* err, int64_t n_counters, LaunchCtx& ctx) {
+  const int64_t per = part4(all.n);
+  for (int64_t at = 0; at < all.n; at += per, err = nullptr, n_counters = 0) {
+    W4Product g = all;
+    g.n = std::min(per, all.n - at);
+    g.x = static_cast<const char*>(all.x) + at * all.x_rs * 2;
+    g.out = static_cast<char*>(all.out) + at * all.out_rs * 2;
+    int rc = launch_w4_prepare(g, err, n_counters, ctx);
+    if (!rc) rc = launch_w4_product(g, ctx);
+    if (rc) return rc;
+  }
+  return TP_OK;
 }
 
 // The decode pass: its counters lie together, those of q/k/v first.
@@ -1669,21 +1704,18 @@ struct Decode4Ws {
 Decode4Ws decode4_ws(const tp_attn_plan* a, const KvSpec& sp) {
   Decode4Ws L;
   const int64_t n = sp.n_tokens;
-  const int sms = num_sms_current();
   size_t off = align_up(kKvHeaderBytes);
   L.attend = off;
-  off += align_up(kv_attend_scratch_bytes(sp, sms));
-  const W4Shape qkv = w4_qkv(a, 128), wo = w4_down(a->wo, 128);
-  L.n_qkv = w4_product_counters(qkv, n);
-  L.n_wo = w4_product_counters(wo, n);
+  off += align_up(kv_attend_scratch_bytes(sp, num_sms_current()));
+  const Need4 qkv = need4(w4_qkv(a, 128), n), wo = need4(w4_down(a->wo, 128), n);
+  L.n_qkv = qkv.counters;
+  L.n_wo = wo.counters;
   L.counters = off;
   off += align_up(static_cast<size_t>(L.n_qkv + L.n_wo) * sizeof(int));
   L.parts = off;
-  const size_t p1 = w4_product_scratch(qkv, n, sms), p2 = w4_product_scratch(wo, n, sms);
-  off += align_up(p1 > p2 ? p1 : p2);
+  off += align_up(std::max(qkv.parts, wo.parts));
   L.image = off;
-  const size_t i1 = w4_image_bytes(qkv, n), i2 = w4_image_bytes(wo, n);
-  off += align_up(i1 > i2 ? i1 : i2);
+  off += align_up(std::max(qkv.image, wo.image));
   L.qkv = off;
   off += align_up(static_cast<size_t>(n) * a->W * 2);
   L.q = off;
@@ -1889,7 +1921,7 @@ int tp_ffn_unshard_rows4(const tp_ffn_plan* p, int group, const void* packed, vo
 }
 
 size_t tp_ffn_workspace4_bytes(const tp_ffn_plan* p, int64_t n, int) {
-  if (!p || n < 0 || p->dtype != TP_BF16 || n > kMaxTokens4) return 0;
+  if (!p || n < 0 || p->dtype != TP_BF16 || n > (int64_t(1) << 30)) return 0;
   return ws4_layout(p, n).total;
 }
 
@@ -1897,7 +1929,7 @@ int tp_ffn_fwd4(const tp_ffn_plan* p, int group, int64_t n, const void* x, const
                 const void* b1, const void* b2, void* y, void* workspace, size_t workspace_bytes, int flags,
                 tp_stream_t stream) {
   if (!p || n < 0 || !w4_group(group)) return TP_ERR_INVALID;
-  if (p->dtype != TP_BF16 || n > kMaxTokens4) return TP_ERR_UNSUPPORTED;
+  if (p->dtype != TP_BF16 || n > (int64_t(1) << 30)) return TP_ERR_UNSUPPORTED;
   if (n == 0) {
     p->last_launches = 0;
     return TP_OK;
@@ -1938,7 +1970,6 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
   if (!rc) rc = kv_rotation(a, rotation, rot);
   if (rc) return rc;
   if (!w4_group(group)) return TP_ERR_INVALID;
-  if (sp.n_tokens > kMaxTokens4) return TP_ERR_UNSUPPORTED;
   if (sp.n_tokens == 0 || sp.n_seqs == 0) {
     a->wo->last_launches = 0;
     return TP_OK;
@@ -1961,8 +1992,7 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
   g.image = ws + L.image;
   g.scratch = ws + L.parts;
   g.counters = reinterpret_cast<int*>(ws + L.counters);
-  rc = launch_w4_prepare(g, ctx.err, L.n_qkv + L.n_wo, ctx);
-  if (!rc) rc = launch_w4_product(g, ctx);
+  rc = product4(g, ctx.err, L.n_qkv + L.n_wo, ctx);
   if (!rc) rc = launch_kv_append(sp, rot, ws + L.qkv, ws + L.q, static_cast<int*>(workspace), false, ctx);
   if (!rc)
     rc = launch_kv_attend(sp, ws + L.q, ws + L.c, nullptr, static_cast<int*>(workspace), false, ws + L.attend, ctx);
@@ -1976,8 +2006,7 @@ int tp_attn_decode_fwd4(const tp_attn_plan* a, const tp_kv_cache* cache, const t
     g.out = y;
     g.out_rs = a->d;
     g.counters += L.n_qkv;
-    rc = launch_w4_prepare(g, nullptr, 0, ctx);
-    if (!rc) rc = launch_w4_product(g, ctx);
+    rc = product4(g, nullptr, 0, ctx);
   }
   return kv_finish(a, ctx, rc, flags, workspace);
 }

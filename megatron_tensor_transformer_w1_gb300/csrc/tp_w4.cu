@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // largest scale to 2^11..2^12.  (code - 8) s has at most 11 significant bits, as many as fp16
 // keeps: the weights are exact where s is at least 2^-28 of the row's largest, smaller ones
 // are rounded to 2^-36 of it.  One block per SM, a step being 64 columns:
-//  * three groups of eight warps, each for every third chunk, a row of tile 0 or 1 to
+//  * up to three groups of eight warps, each for every second or third chunk, a row of tile 0 or 1 to
 //    a thread, make the row's operands, and bring a segment's sums out behind its last
 //    chunk.  What a group does for a chunk takes some 2400 cycles, most of them waiting
 //    (for the chunk, for a free buffer, for the operands to be written), which is why there
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // on without waiting, so that they meet at the block's barriers.
 constexpr int MOST = 128;  // tokens of a tile
 __host__ __device__ constexpr int sum_columns(int nt) { return (nt + 31) / 32 * 32; }
-constexpr int GROUP = 8, GROUPS = 2, MANY_WARPS = GROUP * GROUPS + 2, MANY_THREADS = MANY_WARPS * 32;
+constexpr int GROUP = 8, GROUPS = 3, MANY_WARPS = GROUP * GROUPS + 2, MANY_THREADS = MANY_WARPS * 32;
 constexpr int MANY_STAGES = 8, MANY_BUFS = 3, MANY_SMEM = 224 * 1024 + 1024;
 static_assert(MANY_SMEM + 2 * 128 * 4 + 512 <= 232448, "shared memory per block");
 
@@ -935,20 +935,17 @@ template <int SUBS>
 __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // of a buffer of operands: written, products done; of the sums: read
-  __shared__ uint64_t full[MANY_STAGES], empty[MANY_STAGES], a_full[MANY_BUFS], a_free[MANY_BUFS], d_free, drain;
+  // of a chunk: copied, its products done; of a buffer of operands: written; of the sums: read
+  __shared__ uint64_t full[MANY_STAGES], done[MANY_STAGES], a_full[MANY_BUFS], d_free, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MANY_STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], GROUP + 1);
+      mbar_init(&done[i], 1);
     }
-    for (int i = 0; i < MANY_BUFS; ++i) {
-      mbar_init(&a_full[i], GROUP);
-      mbar_init(&a_free[i], 1);
-    }
+    for (int i = 0; i < MANY_BUFS; ++i) mbar_init(&a_full[i], GROUP);
     mbar_init(&d_free, GROUP);
     mbar_init(&drain, 1);
     s_abort = 0;
@@ -969,7 +966,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   const int x_bytes = p.nt * 256;
 
   if (warp == MANY_WARPS - 2) {
-    if (lane == 0) copy_chunks(p, run, Ring{p.stages, x_bytes, p.stage_bytes}, smem, full, empty, W);
+    if (lane == 0) copy_chunks(p, run, Ring{p.stages, x_bytes, p.stage_bytes}, smem, full, done, W);
     __syncwarp();
   } else if (warp == MANY_WARPS - 1) {
     // ------------------------------------------------ products
@@ -999,8 +996,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
           for (int tile = 0; tile < 2; ++tile)
             umma_f16_ta(tile * d_cols, at + tile * 64 + k * 8, xk, id, k > 0 || !fresh);
         }
-        umma_commit(&a_free[buf]);
-        umma_commit(&empty[stage]);
+        umma_commit(&done[stage]);
       }
       __syncwarp();
       if (++buf == p.bufs) {
@@ -1024,12 +1020,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
     const int tile = (warp >> 2) & 1, group = warp / GROUP;
     const uint32_t at_w = x_bytes + tile * 8192 + r * 64, swz = (r >> 1) & 3;
     const uint32_t at_s = x_bytes + 16384 + (tile * 128 + r) * 2;
-    int stage = group, buf = group;
-    uint32_t phase = 0, a_phase = 1;
-    if (buf >= p.bufs) {
-      buf -= p.bufs;
-      a_phase ^= 1;
-    }
+    // Chunk i goes to buffer i mod bufs, whose products before are chunk i - bufs's.  As
+    // many groups as buffers at most: a group that comes to chunk i knows chunk i -
+    // groups - bufs done, so that no wait here is two phases behind.
+    const int groups = p.bufs < GROUPS ? p.bufs : GROUPS;
+    int stage = group, buf = group, before = group - p.bufs;  // of chunk i - bufs
+    uint32_t phase = 0, before_phase = 0;
     int unit = static_cast<int>(run.first / p.chunks), chunk = static_cast<int>(run.first - static_cast<long long>(unit) * p.chunks) + group;
     for (; chunk >= p.chunks; chunk -= p.chunks) ++unit;
     const float* up_at = p.row_up + tile * 128 + r;
@@ -1037,7 +1033,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
     float* parts = p.parts + (static_cast<long long>(blockIdx.y) * (p.blocks + p.units - 1) + blockIdx.x) * (p.nt * 256) + tile * 128 + r;
     bool waited = false;
 #pragma unroll 1
-    for (int i = group; i < run.count; i += GROUPS) {
+    for (int i = group < groups ? group : run.count; i < run.count; i += groups) {
       const uint32_t st = smem_u32(smem) + stage * p.stage_bytes;
       W.warp(&full[stage], phase);
       uint4 v[4];
@@ -1062,16 +1058,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
           o[4 * t + 3] = weights_of<true>(w8, sq);
         }
         if (q == 0) {
-          W.warp(&a_free[buf], a_phase);  // the products that had the buffer are done
+          if (i >= p.bufs) W.warp(&done[before], before_phase);
           tc_fence_after();
         }
         tmem_store16(a_tmem + lanes + buf * 128 + tile * 64 + q * 16, o);
-      }
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      stage += GROUPS;
-      if (stage >= p.stages) {
-        stage -= p.stages;
-        phase ^= 1;
       }
       tmem_wait_st();
       tc_fence_before();
@@ -1079,7 +1069,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&a_full[buf]);
       if (chunk + 1 == p.chunks || i + 1 == run.count) {
         // a segment's last chunk: the sums back, a row of one tile to a thread
-        W.warp_long(&a_free[buf], a_phase ^ 1);  // its products are done, so all are
+        W.warp_long(&done[stage], phase);  // its products are done, so all are
         tc_fence_after();
         if (!waited) grid_dep_wait();  // nobody reads the parts of before
         waited = true;
@@ -1101,8 +1091,19 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_free);
       }
-      for (buf += GROUPS; buf >= p.bufs; buf -= p.bufs) a_phase ^= 1;
-      chunk += GROUPS;
+      buf += groups;
+      if (buf >= p.bufs) buf -= p.bufs;
+      stage += groups;
+      if (stage >= p.stages) {
+        stage -= p.stages;
+        phase ^= 1;
+      }
+      before += groups;
+      if (before >= p.stages) {
+        before -= p.stages;
+        before_phase ^= 1;
+      }
+      chunk += groups;
       if (chunk >= p.chunks) {
         const int units = chunk / p.chunks;  // more than one where units are short
         chunk -= units * p.chunks;

@@ -43,10 +43,11 @@ def test_quantize_refusals(abi, name):
 
 
 def test_packed_bytes(abi, plans):
-    # 128-slot tiles in pairs, 128-column chunks: codes 16384 bytes and 512 for each group of a chunk
-    assert abi.tp_ffn_packed4_bytes(plans["swiglu"], 0, 128) == 8 * 4 * (16384 + 512)
-    assert abi.tp_ffn_packed4_bytes(plans["gelu"], 0, 64) == 4 * 4 * (16384 + 1024)
-    assert abi.tp_ffn_packed4_bytes(plans["gelu"], 1, 32) == 2 * 8 * (16384 + 2048)
+    # 128-slot tiles in pairs, 128-column chunks: codes 16384 bytes and 512 for each group of a chunk; a factor of
+    # 4 bytes for each of a pair's 256 rows and 16 bytes for the whole
+    assert abi.tp_ffn_packed4_bytes(plans["swiglu"], 0, 128) == 8 * 4 * (16384 + 512) + 8 * 1024 + 16
+    assert abi.tp_ffn_packed4_bytes(plans["gelu"], 0, 64) == 4 * 4 * (16384 + 1024) + 4 * 1024 + 16
+    assert abi.tp_ffn_packed4_bytes(plans["gelu"], 1, 32) == 2 * 8 * (16384 + 2048) + 2 * 1024 + 16
     assert abi.tp_ffn_packed4_bytes(plans["none"], 0, 64) == 0
     for args in ((None, 0, 64), (plans["f32"], 0, 64), (plans["gelu"], 2, 64), (plans["gelu"], 0, 48)):
         assert abi.tp_ffn_packed4_bytes(*args) == 0
@@ -85,7 +86,7 @@ def test_forward_refusals(abi, plans):
 def test_attention_refusals(abi):
     rc, plan = abi.tp_attn_plan_create(256, 8, 2, 128, 2, True, abi.TP_BF16)
     assert rc == abi.TP_OK
-    assert abi.tp_attn_packed4_bytes(plan, 0, 64) == 6 * 2 * (16384 + 1024)
+    assert abi.tp_attn_packed4_bytes(plan, 0, 64) == 6 * 2 * (16384 + 1024) + 6 * 1024 + 16
     assert abi.tp_attn_packed4_bytes(plan, 0, 60) == 0 == abi.tp_attn_packed4_bytes(None, 0, 64)
     four = [A] * 4
     assert abi.tp_attn_shard_weights4(plan, 64, [A, A, None, A], four, A, A) == abi.TP_ERR_INVALID

@@ -57,18 +57,20 @@ def gelu(z):
 def forward(x, act, Ws, b1, b2):
     """y in 64 bits, and how far a result may be from it.
 
-    A product takes its tokens exactly, or as blocks of 128 columns: fp16 to a power of
-    two, or e4m3 numbers in pairs, the largest element in 2^7..2^8.  bf16's eight bits
-    are kept but for elements so small that the second number is a subnormal: off by
-    at most half its 2^-9, times 2^-4, 2^-14, or 2^-21 of the block's largest.
+    A product takes its tokens as fp16 numbers times a power of two, of 128 columns or
+    of the whole token: bf16's eight bits are kept down to 2^-25 of the largest, and what
+    is smaller is rounded to 2^-40 of it.  Hidden activations that are kept under a bound
+    instead of their largest are rounded to half of fp16's least, 2^-25, where the bound
+    is 2^15: below 2^-21 of the largest for bounds up to 2^19 too high, which
+    sum |x| 8 max s is for K of some thousand and random codes.
     z is off by at most e(K) sum |x w| besides: 32-bit sums of K products with their
     scales, e(K) = (K + 8) 2^-22 (four times the 2^-24 of each rounding, for the
     shortened sums of the matrix unit).  (The codes are multiplied as 0..15 and the
     offset of 8 taken off as a sum; for codes spread over 0..15 sum |code x| is below
     twice sum |(code - 8) x|, which the factor of four covers.)
     |gelu'| <= 1.13, |silu'| <= 1.1; the functions are within 2^-19 of the value for
-    |value| >= 1e-3 and 2^-18 |z| absolutely.  h is rounded to bf16 or better: 2^-8
-    relative (two e4m3 numbers: 2^-4 of 2^-4).  Then the same for y and its rounding."""
+    |value| >= 1e-3 and 2^-18 |z| absolutely.  h is rounded to fp16: 2^-8
+    relative covers it.  Then the same for y and its rounding."""
     def product(v, ev, W):
         ev = ev + 2.0 ** -21 * v.abs().amax(1, keepdim=True)
         e = (v.shape[1] + 8) * 2.0 ** -22 * (v.abs() @ W.abs().T)
