@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256) tops_kernel(W4Shape m, uint8_t* packed) {
 // a run of chunks of one unit is a segment.  A unit that several blocks share is
 // joined by the last of them to come, in the order of the columns.
 //
-// Two kernels: few tokens (up to 16) on registers, more on tensor memory.  Both are
+// Two kernels: few tokens (up to 8) on registers, more on tensor memory.  Both are
 // as exact as sums in 32 bits: no scaled weight and no hidden activation is rounded
 // to bf16.  The tokens are fp16 numbers times a power of two.  A token with an
 // infinity or a NaN gets those throughout.
@@ -276,7 +276,7 @@ using namespace tc;
 //  * More: the power of two is the token's, for all columns.  Behind the images of
 //    all tokens lies int [tokens + 1], the exponents e: |x| < 2^e, kept as x 2^(15 - e), and
 //    last the least that any of them counts for.
-constexpr int FEW = 16;  // tokens
+constexpr int FEW = 8;  // tokens
 __host__ __device__ constexpr int image_bytes(int nt) { return nt <= FEW ? nt * 288 : nt * 256; }
 constexpr int SUM_OF = 0, SUM_OF_HALF = 4, SUM_OF_ALL = 6, DOWN = 7;
 constexpr int LEAST = -1000;  // an exponent below all
@@ -631,73 +631,64 @@ __device__ __forceinline__ void write4(const ProductParams& p, int nt, int tile,
 
 // The end of a segment of `unit`, whose sums lie in shared memory, [token][row], 256
 // rows and a few of padding: out if the segment is the whole unit, else as a part,
-// and the last block of the unit joins the parts.  By the block's first WARPS
-// warps, which then may write the sums anew.
-constexpr int SUM_PITCH = 256 + 8;
-template <int NT, int WARPS>
+// and the last block of the unit joins the parts.  By the block's first
+// FEW_WARPS warps, which then may write the sums anew.
+constexpr int SUM_PITCH = 256 + 8, FEW_WARPS = 8;
 __device__ __forceinline__ void finish_segment(const ProductParams& p, long long unit, const float* sum, int* s_last,
                                                const Wait& W) {
-  // a thread: rows 4 q .. 4 q + 3 of tile 0 and of tile 1, of a token of every WARPS
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = lane * 4;
+  // a thread: rows 4 q .. 4 q + 3 of tile 0 and of tile 1, of a warp's token
+  static_assert(FEW == FEW_WARPS, "a token to a warp");
+  const int token = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = lane * 4;
   const long long u0 = unit * p.chunks, u1 = u0 + p.chunks - 1;
   const int C = gridDim.x;
   const int c0 = static_cast<int>(((u0 + 1) * C - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * C - 1) / p.total);
+  float4 v0 = *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + q4), v1 = *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + 128 + q4);
   bool store = true;
-  float* parts = p.parts + q4;
-  auto slot = [&](int b) { return static_cast<long long>(2 * b + (b == c0)) * (NT * 256); };
   if (c0 != c1) {
+    float* parts = p.parts + token * 256 + q4;
+    auto slot = [&](int b) { return static_cast<long long>(2 * b + (b == c0)) * (FEW * 256); };
     float* to = parts + slot(blockIdx.x);
-#pragma unroll
-    for (int token = warp; token < NT; token += WARPS) {
-      __stcg(reinterpret_cast<float4*>(to + token * 256), *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + q4));
-      __stcg(reinterpret_cast<float4*>(to + token * 256 + 128), *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + 128 + q4));
-    }
+    __stcg(reinterpret_cast<float4*>(to), v0);
+    __stcg(reinterpret_cast<float4*>(to + 128), v1);
     __threadfence();
-    bar_sync(1, WARPS * 32);
+    bar_sync(1, FEW_WARPS * 32);
     if (threadIdx.x == 0) {
       __threadfence();
       *s_last = atomicAdd(p.counters + unit, 1) == c1 - c0;
       __threadfence();
     }
-    bar_sync(1, WARPS * 32);
+    bar_sync(1, FEW_WARPS * 32);
     store = *s_last;
-  }
-  if (store && *W.abort_flag == 0) {
-#pragma unroll 1
-    for (int token = warp; token < NT; token += WARPS) {
-      float4 v0, v1;
-      if (c0 == c1) {
-        v0 = *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + q4);
-        v1 = *reinterpret_cast<const float4*>(sum + token * SUM_PITCH + 128 + q4);
-      } else {
-        v0 = v1 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (store) {
+      v0 = v1 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int b = c0; b <= c1; ++b) {
-          const float* from = parts + slot(b) + token * 256;
-          v0 = add4(v0, __ldcg(reinterpret_cast<const float4*>(from)));
-          v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
-        }
-      }
-      const float one = 16777216.f;  // 2^24: a code's unit
-      v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
-      v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
-      if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
-        v0.x *= sigmoid_f(v0.x) * v1.x;
-        v0.y *= sigmoid_f(v0.y) * v1.y;
-        v0.z *= sigmoid_f(v0.z) * v1.z;
-        v0.w *= sigmoid_f(v0.w) * v1.w;
-        write4<true>(p, NT, 0, token, unit * 128 + q4, lane, v0, 1.f);
-      } else {
-        write4<true>(p, NT, 0, token, unit * 256 + q4, lane, v0, 1.f);
-        write4<true>(p, NT, 0, token, unit * 256 + 128 + q4, lane, v1, 1.f);
+      for (int b = c0; b <= c1; ++b) {
+        const float* from = parts + slot(b);
+        v0 = add4(v0, __ldcg(reinterpret_cast<const float4*>(from)));
+        v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
       }
     }
   }
-  bar_sync(1, WARPS * 32);
+  if (store && *W.abort_flag == 0) {
+    const float one = 16777216.f;  // 2^24: a code's unit
+    v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
+    v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
+    if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
+      v0.x *= sigmoid_f(v0.x) * v1.x;
+      v0.y *= sigmoid_f(v0.y) * v1.y;
+      v0.z *= sigmoid_f(v0.z) * v1.z;
+      v0.w *= sigmoid_f(v0.w) * v1.w;
+      write4<true>(p, FEW, 0, token, unit * 128 + q4, lane, v0, 1.f);
+    } else {
+      write4<true>(p, FEW, 0, token, unit * 256 + q4, lane, v0, 1.f);
+      write4<true>(p, FEW, 0, token, unit * 256 + 128 + q4, lane, v1, 1.f);
+    }
+  }
+  bar_sync(1, FEW_WARPS * 32);
 }
 
 // ---------------------------------------------------------------- few tokens
-// Up to 16 tokens, bound by the one read of the codes: m16n8k16 matrix instructions on
+// Up to 8 tokens, bound by the one read of the codes: m16n8k16 matrix instructions on
 // registers.  What is left to count are the instructions that make operands of
 // codes.  A code in the low bits of an fp16 number is a subnormal, code * 2^-24, and four
 // bits higher code * 2^-20: a word's eight codes are four operand registers after one
@@ -706,26 +697,25 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
 // taken off as the block's sum, -8 times the sum of the group's 32, 64 or 128
 // columns: product * down + sum, in 32 bits, times the row's scale.
 //
-// The matrix instructions take 2.05 cycles
-// an SM (measured), 8 tokens of a chunk 262 of the some 720 that its bytes take, 16
-// tokens 525; the tensor-memory products take 768 whatever the number of tokens,
-// besides the way of the weights into tensor memory.
+// The matrix instructions take 2.05 cycles an SM (measured), those of a chunk 262 of
+// the some 720 that its bytes take; the tensor-memory products take 768 whatever the
+// number of tokens.  (Two of them for 9 to 16 tokens: 88.5 us for the 70B feed-forward
+// as the other kernel, but 26 us against 19 for a block of d 768 and 16 against 14 for
+// an output projection of d 4096.)
 //
 // The order of a product's columns is free as long as both operands have it: lane
 // t of a row's four takes the 32-bit words of codes 8 t .. 8 t + 7 of 32 columns, their
 // pairs as the halves of two k16 steps, and so reads the same 8 columns of a token
-// in one piece.  Token t of eight stands in column 2 t, token t + 4 in column 2 t +
+// in one piece.  Token t stands in column 2 t, token t + 4 in column 2 t +
 // 1 of the product, so that the two tokens of an eighth of a warp lie in different
 // halves of the swizzled rows.
 // 8 warps, 32 rows of the unit each, two blocks per SM.
-template <int NT_>
 struct Few {
-  static constexpr int NT = NT_, X_BYTES = image_bytes(NT), STAGE = X_BYTES + 18432;
-  static constexpr int STAGES = NT == 8 ? 5 : 4;
-  static constexpr int M_SUM = STAGES * STAGE, SMEM = M_SUM + NT * SUM_PITCH * 4 + 128;
+  static constexpr int X_BYTES = image_bytes(FEW), STAGE = X_BYTES + 18432, STAGES = 5;
+  static constexpr int M_SUM = STAGES * STAGE, SMEM = M_SUM + FEW * SUM_PITCH * 4 + 128;
   static_assert(2 * (SMEM + 2048) <= 233472, "two blocks per SM");
 };
-constexpr int FEW_WARPS = 8, FEW_THREADS = (FEW_WARPS + 1) * 32;
+constexpr int FEW_THREADS = (FEW_WARPS + 1) * 32;
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -736,10 +726,9 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // SUBS: groups of a chunk.
-template <int NT, int SUBS>
+template <int SUBS>
 __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_constant__ ProductParams p) {
-  using F = Few<NT>;
-  constexpr int NB = NT / 8;  // products of eight tokens
+  using F = Few;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   __shared__ uint64_t full[F::STAGES], empty[F::STAGES];
@@ -768,9 +757,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   // bytes from a stage's start
   const uint32_t at_x = tok0 * 128, swz = tok0 & 7;
   const uint32_t at_w = F::X_BYTES + row0 * 64 + ((t ^ ((i8 >> 1) & 3)) << 4), at_s = F::X_BYTES + 16384 + row0 * 2;
-  const uint32_t at_tail = NT * 256 + t * 4;  // of token t
+  const uint32_t at_tail = FEW * 256 + t * 4;  // of token t
   float* sum = reinterpret_cast<float*>(smem + F::M_SUM);
-  uint64_t acc[2][NB][2] = {};  // rows row0 + 16 m + 8 h, tokens 8 b + t and 8 b + t + 4
+  uint64_t acc[2][2] = {};  // rows row0 + 16 m + 8 h, tokens t and t + 4
   grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
   int stage = 0;
   uint32_t phase = 0;
@@ -785,40 +774,29 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) w[m][h] = ld_shared_v4(st + at_w + m * 1024 + h * 512);
-    uint64_t down[NB], sums[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t at = st + at_tail + DOWN * NT * 4 + b * 32;
-      down[b] = pack2(ld_shared_f(at), ld_shared_f(at + 16));
-    }
-    float c[2][NB][4];
+    auto two = [&](int what) {  // of tokens t and t + 4
+      const uint32_t at = st + at_tail + what * FEW * 4;
+      return pack2(ld_shared_f(at), ld_shared_f(at + 16));
+    };
+    const uint64_t down = two(DOWN);
+    uint64_t sums = 0;
+    float c[2][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       constexpr int PER = 4 / SUBS;
       if (q % PER == 0) {
         constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
+        sums = two(FIRST + q / PER);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t at = st + at_tail + (FIRST + q / PER) * NT * 4 + b * 32;
-          sums[b] = pack2(ld_shared_f(at), ld_shared_f(at + 16));
-#pragma unroll
-          for (int m = 0; m < 2; ++m) c[m][b][0] = c[m][b][1] = c[m][b][2] = c[m][b][3] = 0.f;
-        }
+        for (int m = 0; m < 2; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
       }
-      uint4 x[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        x[b] = ld_shared_v4(st + at_x + (q >> 1) * (NT * 128) + b * 1024 + ((((q & 1) * 4 + t) ^ swz) << 4));
+      const uint4 x = ld_shared_v4(st + at_x + (q >> 1) * (FEW * 128) + ((((q & 1) * 4 + t) ^ swz) << 4));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        uint32_t w0 = q == 0 ? w[m][0].x : q == 1 ? w[m][0].y : q == 2 ? w[m][0].z : w[m][0].w;
-        uint32_t w1 = q == 0 ? w[m][1].x : q == 1 ? w[m][1].y : q == 2 ? w[m][1].z : w[m][1].w;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) mma(c[m][b], low(w0), low(w1), high(w0), high(w1), x[b].x, x[b].y);
-        w0 >>= 8;
-        w1 >>= 8;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) mma(c[m][b], low(w0), low(w1), high(w0), high(w1), x[b].z, x[b].w);
+        const uint32_t w0 = q == 0 ? w[m][0].x : q == 1 ? w[m][0].y : q == 2 ? w[m][0].z : w[m][0].w;
+        const uint32_t w1 = q == 0 ? w[m][1].x : q == 1 ? w[m][1].y : q == 2 ? w[m][1].z : w[m][1].w;
+        mma(c[m], low(w0), low(w1), high(w0), high(w1), x.x, x.y);
+        mma(c[m], low(w0 >> 8), low(w1 >> 8), high(w0 >> 8), high(w1 >> 8), x.z, x.w);
       }
       if (q % PER != PER - 1) continue;
 #pragma unroll
@@ -826,10 +804,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float s = ld_shared_scale(st + at_s + (q / PER) * 512 + (16 * m + 8 * h) * 2);
-          const uint64_t s2 = pack2(s, s);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[m][b][h] = fma2(s2, fma2(pack2(c[m][b][2 * h], c[m][b][2 * h + 1]), down[b], sums[b]), acc[m][b][h]);
+          acc[m][h] = fma2(pack2(s, s), fma2(pack2(c[m][2 * h], c[m][2 * h + 1]), down, sums), acc[m][h]);
         }
     }
     __syncwarp();
@@ -842,16 +817,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2 v = unpack2(acc[m][b][h]);
-          sum[(8 * b + t) * SUM_PITCH + row0 + 16 * m + 8 * h] = v.x;
-          sum[(8 * b + t + 4) * SUM_PITCH + row0 + 16 * m + 8 * h] = v.y;
-          acc[m][b][h] = 0;
-        }
+      for (int h = 0; h < 2; ++h) {
+        const float2 v = unpack2(acc[m][h]);
+        sum[t * SUM_PITCH + row0 + 16 * m + 8 * h] = v.x;
+        sum[(t + 4) * SUM_PITCH + row0 + 16 * m + 8 * h] = v.y;
+        acc[m][h] = 0;
+      }
     bar_sync(1, FEW_WARPS * 32);
-    finish_segment<NT, FEW_WARPS>(p, unit, sum, &s_last, W);
+    finish_segment(p, unit, sum, &s_last, W);
     chunk = 0;
     ++unit;
   }
@@ -1195,12 +1168,10 @@ int launch_inst(dim3 grid, cudaStream_t st, const Args&... args) {
   launch_dep(KERNEL, grid, BLOCK, SMEM, st, args...);
   return TP_OK;
 }
-template <int NT>
 int launch_few(const ProductParams& p, dim3 grid, cudaStream_t st) {
-  constexpr int SMEM = Few<NT>::SMEM;
-  if (p.m.group == 128) return launch_inst<few_kernel<NT, 1>, FEW_THREADS, SMEM>(grid, st, p);
-  if (p.m.group == 64) return launch_inst<few_kernel<NT, 2>, FEW_THREADS, SMEM>(grid, st, p);
-  return launch_inst<few_kernel<NT, 4>, FEW_THREADS, SMEM>(grid, st, p);
+  if (p.m.group == 128) return launch_inst<few_kernel<1>, FEW_THREADS, Few::SMEM>(grid, st, p);
+  if (p.m.group == 64) return launch_inst<few_kernel<2>, FEW_THREADS, Few::SMEM>(grid, st, p);
+  return launch_inst<few_kernel<4>, FEW_THREADS, Few::SMEM>(grid, st, p);
 }
 int launch_product(const ProductParams& p, dim3 grid, cudaStream_t st) {
   if (p.m.group == 128) return launch_inst<product_kernel<1>, MANY_THREADS, MANY_SMEM>(grid, st, p);
@@ -1216,7 +1187,7 @@ struct Cut {
 Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
   Cut c;
   if (n <= FEW) {
-    c.nt = n <= 8 ? 8 : 16;
+    c.nt = FEW;
     c.tiles = 1;
     c.blocks = 2 * num_sms;
   } else {
@@ -1378,11 +1349,9 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   const dim3 grid(static_cast<unsigned>(c.blocks), static_cast<unsigned>(c.tiles));
   if (ctx.before) ctx.before(ctx.user, a.name, ctx.stream);
   int rc;
-  if (c.nt == 8)
-    rc = launch_few<8>(p, grid, ctx.stream);
-  else if (c.nt == 16)
-    rc = launch_few<16>(p, grid, ctx.stream);
-  else {
+  if (c.nt == FEW) {
+    rc = launch_few(p, grid, ctx.stream);
+  } else {
     p.nt = c.nt;
     p.stage_bytes = image_bytes(c.nt) + (p.block_bytes + 1023) / 1024 * 1024;
     p.stages = std::min((MANY_SMEM - 1024) / p.stage_bytes, MANY_STAGES);
