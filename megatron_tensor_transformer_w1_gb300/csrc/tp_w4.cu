@@ -25,6 +25,32 @@ __device__ __forceinline__ float bf16_at(uint32_t w, int half) {
   return __uint_as_float(half ? w & 0xffff0000u : w << 16);
 }
 
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // 2^e, e brought into a range where 2^-e is a normal number too.
 __device__ __forceinline__ float pow2(int e) {
   return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 126) + 127) << 23);
@@ -36,28 +62,23 @@ __device__ __forceinline__ float pow2(int e) {
 // zero, or too small for bf16) every code is 8.
 __device__ __forceinline__ float group_scale(float amax) { return __bfloat162float(__float2bfloat16_rn(amax / 7.f)); }
 
-// code - 8 as a float: w / s rounded to a whole number, ties to even, for w of
-// eight bits and finite s > 0 with |w| <= 7.03 s.  w * inv is within 2^-22 of the
-// quotient, which lies at least 2^-18 from a tie unless it is one; ties are told
-// by the remainder, which is exact.
-__device__ __forceinline__ float steps_of(float w, float s, float inv) {
-  const float magic = 12582912.f;  // 1.5 2^23: the sum's last bit is worth 1
-  const float u = fmaf(w, inv, magic);
-  float q = u - magic;
-  const float r = fmaf(-q, s, w);
-  if (fabsf(r + r) == s && (__float_as_uint(u) & 1u)) q += copysignf(1.f, r);
-  return q;
-}
-__device__ __forceinline__ uint32_t code_of(float w, float s, float inv) {
-  if (!(s > 0.f) || !(s < INFINITY)) return 8u;
-  return static_cast<uint32_t>(static_cast<int>(steps_of(w, s, inv)) + 8);
-}
 // 1 / s overflows for the smallest scales: s and w are brought up by 2^64 first.
 __device__ __forceinline__ void ready(float& s, float& inv, float& up) {
   up = s < 1e-30f ? 18446744073709551616.f : 1.f;
   s *= up;
   inv = 1.f / s;
 }
+// The codes of two elements, in the low bytes, for finite s > 0 and |w| <= 7.03 s.  The
+// quotient in two steps: q = w inv, then q + (w - q s) inv, whose remainder is exact and
+// which is the quotient to 2^-46 before its last rounding: a tie, which 32 bits hold,
+// comes out exactly, and others lie at least 2^-18 from one.  The sum with 1.5 2^23 + 8
+// has a last bit worth 1: ties go to the even code.
+__device__ __forceinline__ uint2 codes_of(uint64_t w, uint64_t less_s, uint64_t inv) {
+  const uint64_t q = mul2(w, inv), magic = pack2(12582920.f, 12582920.f);
+  const float2 u = unpack2(add2(fma2(fma2(q, less_s, w), inv, q), magic));
+  return make_uint2(__float_as_uint(u.x), __float_as_uint(u.y));
+}
+__device__ __forceinline__ bool has_codes(float s) { return s > 0.f && s < INFINITY; }
 
 // 16 elements to a lane, group / 16 lanes to a group.
 __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict__ W, long long pieces, int row_pieces,
@@ -87,11 +108,23 @@ __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict
     const __nv_bfloat16 top = __hmax_nan(m.x, m.y);
     float s = group_scale(__bfloat162float(top)), inv, up;
     if (ok && in % lanes == 0) scales[(row * segs + seg) * seg_groups + in / lanes] = __float2bfloat16_rn(s);
+    const bool any = has_codes(s);
     ready(s, inv, up);
-    uint32_t word[2] = {};
+    const uint64_t less2 = pack2(-s, -s), inv2 = pack2(inv, inv), up2 = pack2(up, up);
+    uint32_t word[2];
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      word[j >> 3] |= code_of(bf16_at(v[j >> 1], j & 1) * up, s, inv) << (4 * (j & 7));
+    for (int h = 0; h < 2; ++h) {
+      uint2 c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint64_t w = pack2(bf16_at(v[4 * h + j], 0), bf16_at(v[4 * h + j], 1));
+        if (up != 1.f) w = mul2(w, up2);
+        c[j] = codes_of(w, less2, inv2);
+      }
+      const uint32_t even = __byte_perm(__byte_perm(c[0].x, c[1].x, 0x0040), __byte_perm(c[2].x, c[3].x, 0x0040), 0x5410),
+                     odd = __byte_perm(__byte_perm(c[0].y, c[1].y, 0x0040), __byte_perm(c[2].y, c[3].y, 0x0040), 0x5410);
+      word[h] = any ? even + 16 * odd : 0x88888888u;
+    }
     if (ok) codes[at] = make_uint2(word[0], word[1]);
   }
 }
@@ -123,8 +156,10 @@ __global__ void __launch_bounds__(256) codes_kernel(const __nv_bfloat16* __restr
     for (int h = 0; h < 2 && c0 + h < cols; ++h) {
       const long long c = c0 + h, e = c / seg, g = (c - e * seg) / group;
       float s = __bfloat162float(scales[(row * segs + e) * seg_groups + g]), inv, up;
+      const bool any = has_codes(s);
       ready(s, inv, up);
-      const uint32_t q = code_of(__bfloat162float(W[row * cols + c]) * up, s, inv);
+      const float w = __bfloat162float(W[row * cols + c]) * up;
+      const uint32_t q = any ? codes_of(pack2(w, w), pack2(-s, -s), pack2(inv, inv)).x & 15u : 8u;
       byte = h ? (byte & 0x0fu) | (q << 4) : (byte & 0xf0u) | q;
     }
     codes[i] = static_cast<uint8_t>(byte);
@@ -133,6 +168,15 @@ __global__ void __launch_bounds__(256) codes_kernel(const __nv_bfloat16* __restr
 
 __device__ __forceinline__ float value_of(uint32_t word, int j, float s) {
   return (static_cast<float>((word >> (4 * j)) & 15u) - 8.f) * s;
+}
+// (code - 8) s as bf16, for the codes at bits 0-3 and 16-19: 128 + code less 136 is exact,
+// and the product is rounded once.
+__device__ __forceinline__ uint32_t two_values(uint32_t c, uint32_t s) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(c), "r"(0x000f000fu), "r"(0x43004300u));
+  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x43084308u));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(s));
+  return v;
 }
 __global__ void __launch_bounds__(256) dequantize16_kernel(const uint2* __restrict__ codes,
                                                            const __nv_bfloat16* __restrict__ scales, long long pieces,
@@ -143,11 +187,15 @@ __global__ void __launch_bounds__(256) dequantize16_kernel(const uint2* __restri
     const long long row = i / row_pieces;
     const int in_row = static_cast<int>(i - row * row_pieces), e = in_row / seg_pieces, in = in_row - e * seg_pieces;
     const uint2 q = codes[i];
-    const float s = __bfloat162float(scales[(row * segs + e) * seg_groups + in / lanes]);
+    const uint32_t s = reinterpret_cast<const uint16_t*>(scales)[(row * segs + e) * seg_groups + in / lanes] * 0x10001u;
     uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      w[j] = tc::pack_bf16x2(value_of(j < 4 ? q.x : q.y, 2 * (j & 3), s), value_of(j < 4 ? q.x : q.y, 2 * (j & 3) + 1, s));
+    for (int j = 0; j < 8; j += 2) {
+      // four codes: the second of either pair 12 bits up, in the upper half
+      const uint32_t four = (j < 4 ? q.x : q.y) >> (16 * ((j >> 1) & 1)) & 0xffffu, c = four | four << 12;
+      w[j] = two_values(c, s);
+      w[j + 1] = two_values(c >> 8, s);
+    }
     W[2 * i] = make_uint4(w[0], w[1], w[2], w[3]);
     W[2 * i + 1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
@@ -523,21 +571,6 @@ __device__ __forceinline__ float ld_shared_scale(uint32_t addr) {  // a bf16
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
 }
 // The codes at bits 0-3 and 16-19 as two fp16 numbers, and those at bits 4-7 and 20-23.
 __device__ __forceinline__ uint32_t low(uint32_t w) { return w & 0x000f000fu; }
