@@ -80,20 +80,39 @@ __device__ __forceinline__ uint2 codes_of(uint64_t w, uint64_t less_s, uint64_t 
 }
 __device__ __forceinline__ bool has_codes(float s) { return s > 0.f && s < INFINITY; }
 
-// 16 elements to a lane, group / 16 lanes to a group.
+// A thread's row and place in it, of `width` places each, over a grid's strides: the
+// division of 64 bits once.
+struct Walk {
+  long long row, rows_on;
+  unsigned place, places_on, width;
+  __device__ __forceinline__ Walk(long long first, long long stride, unsigned w) : width(w) {
+    row = first / w;
+    place = static_cast<unsigned>(first - row * w);
+    rows_on = stride / w;
+    places_on = static_cast<unsigned>(stride - rows_on * w);
+  }
+  __device__ __forceinline__ void next() {
+    row += rows_on;
+    place += places_on;
+    if (place >= width) {
+      place -= width;
+      ++row;
+    }
+  }
+};
+// 16 elements to a lane, 1 << lanes of them to a group.
 __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict__ W, long long pieces, int row_pieces,
                                                          int seg_pieces, int lanes, int seg_groups, int segs,
                                                          uint2* __restrict__ codes, __nv_bfloat16* __restrict__ scales) {
   // places: the pieces of a row, each segment's rounded up to whole groups
-  const long long row_places = static_cast<long long>(segs) * seg_groups * lanes;
-  const long long rows = pieces / row_pieces, total = rows * row_places;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i0 = static_cast<long long>(blockIdx.x) * blockDim.x; i0 < total; i0 += stride) {
-    const long long i = i0 + threadIdx.x;
-    const long long row = i / row_places;
-    const int place = static_cast<int>(i - row * row_places), per = seg_groups * lanes;
-    const int seg = place / per, in = place - seg * per;
-    const bool ok = i < total && in < seg_pieces;
+  const unsigned per = static_cast<unsigned>(seg_groups) << lanes;
+  const long long rows = pieces / row_pieces, total = rows * (static_cast<long long>(segs) * per);
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x, first = static_cast<long long>(blockIdx.x) * blockDim.x;
+  Walk at_row(first + threadIdx.x, stride, segs * per);
+  for (long long i0 = first; i0 < total; i0 += stride, at_row.next()) {
+    const long long row = at_row.row;
+    const int seg = segs == 1 ? 0 : static_cast<int>(at_row.place / per), in = static_cast<int>(at_row.place - seg * per);
+    const bool ok = row < rows && in < seg_pieces;
     const long long at = row * row_pieces + static_cast<long long>(seg) * seg_pieces + in;
     uint32_t v[8] = {};
     if (ok) {
@@ -104,23 +123,24 @@ __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict
     __nv_bfloat162 m = __habs2(*reinterpret_cast<__nv_bfloat162*>(&v[0]));
 #pragma unroll
     for (int j = 1; j < 8; ++j) m = __hmax2_nan(m, __habs2(*reinterpret_cast<__nv_bfloat162*>(&v[j])));
-    for (int d = 1; d < lanes; d <<= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = 1; d < 1 << lanes; d <<= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
     const __nv_bfloat16 top = __hmax_nan(m.x, m.y);
     float s = group_scale(__bfloat162float(top)), inv, up;
-    if (ok && in % lanes == 0) scales[(row * segs + seg) * seg_groups + in / lanes] = __float2bfloat16_rn(s);
+    if (ok && (in & ((1 << lanes) - 1)) == 0) scales[(row * segs + seg) * seg_groups + (in >> lanes)] = __float2bfloat16_rn(s);
     const bool any = has_codes(s);
     ready(s, inv, up);
-    const uint64_t less2 = pack2(-s, -s), inv2 = pack2(inv, inv), up2 = pack2(up, up);
+    if (up != 1.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[j]) : "r"(0x5f805f80u));  // 2^64
+    }
+    const uint64_t less2 = pack2(-s, -s), inv2 = pack2(inv, inv);
     uint32_t word[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint2 c[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint64_t w = pack2(bf16_at(v[4 * h + j], 0), bf16_at(v[4 * h + j], 1));
-        if (up != 1.f) w = mul2(w, up2);
-        c[j] = codes_of(w, less2, inv2);
-      }
+      for (int j = 0; j < 4; ++j)
+        c[j] = codes_of(pack2(bf16_at(v[4 * h + j], 0), bf16_at(v[4 * h + j], 1)), less2, inv2);
       const uint32_t even = __byte_perm(__byte_perm(c[0].x, c[1].x, 0x0040), __byte_perm(c[2].x, c[3].x, 0x0040), 0x5410),
                      odd = __byte_perm(__byte_perm(c[0].y, c[1].y, 0x0040), __byte_perm(c[2].y, c[3].y, 0x0040), 0x5410);
       word[h] = any ? even + 16 * odd : 0x88888888u;
@@ -183,11 +203,13 @@ __global__ void __launch_bounds__(256) dequantize16_kernel(const uint2* __restri
                                                            int row_pieces, int seg_pieces, int lanes, int seg_groups,
                                                            int segs, uint4* __restrict__ W) {
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += stride) {
-    const long long row = i / row_pieces;
-    const int in_row = static_cast<int>(i - row * row_pieces), e = in_row / seg_pieces, in = in_row - e * seg_pieces;
-    const uint2 q = codes[i];
-    const uint32_t s = reinterpret_cast<const uint16_t*>(scales)[(row * segs + e) * seg_groups + in / lanes] * 0x10001u;
+  long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  Walk at_row(i, stride, row_pieces);
+  auto scale_of = [&] {
+    const int e = segs == 1 ? 0 : static_cast<int>(at_row.place) / seg_pieces, in = static_cast<int>(at_row.place) - e * seg_pieces;
+    return reinterpret_cast<const uint16_t*>(scales)[(at_row.row * segs + e) * seg_groups + (in >> lanes)];
+  };
+  auto write = [&](uint4* to, uint2 q, uint32_t s) {
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -196,8 +218,18 @@ __global__ void __launch_bounds__(256) dequantize16_kernel(const uint2* __restri
       w[j] = two_values(c, s);
       w[j + 1] = two_values(c >> 8, s);
     }
-    W[2 * i] = make_uint4(w[0], w[1], w[2], w[3]);
-    W[2 * i + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  };
+  for (; i < pieces; i += 2 * stride) {  // two at a time, both loads on their way
+    const bool more = i + stride < pieces;
+    const uint2 q0 = codes[i], q1 = more ? codes[i + stride] : q0;
+    const uint32_t s0 = scale_of();
+    at_row.next();
+    const uint32_t s1 = more ? scale_of() : s0;
+    at_row.next();
+    write(W + 2 * i, q0, s0 * 0x10001u);
+    if (more) write(W + 2 * (i + stride), q1, s1 * 0x10001u);
   }
 }
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restrict__ codes,
@@ -1253,8 +1285,8 @@ int launch_w4_quantize(const void* W, int64_t rows, int64_t cols, int64_t segs, 
   const int64_t seg = cols / segs, seg_groups = (seg + group - 1) / group;
   auto* sc = static_cast<__nv_bfloat16*>(scales);
   if (seg % 16 == 0) {
-    const int lanes = group / 16;
-    const long long places = rows * segs * seg_groups * lanes;
+    const int lanes = group == 32 ? 1 : group == 64 ? 2 : 3;
+    const long long places = rows * segs * (seg_groups << lanes);
     quantize16_kernel<<<grid_of((places + 255) / 256), 256, 0, st>>>(
         static_cast<const uint4*>(W), rows * (cols / 16), static_cast<int>(cols / 16), static_cast<int>(seg / 16), lanes,
         static_cast<int>(seg_groups), static_cast<int>(segs), static_cast<uint2*>(codes), sc);
@@ -1276,8 +1308,8 @@ int launch_w4_dequantize(const void* codes, const void* scales, int64_t rows, in
   if (seg % 16 == 0) {
     const long long pieces = rows * (cols / 16);
     dequantize16_kernel<<<grid_of((pieces + 255) / 256), 256, 0, st>>>(
-        static_cast<const uint2*>(codes), sc, pieces, static_cast<int>(cols / 16), static_cast<int>(seg / 16), group / 16,
-        static_cast<int>(seg_groups), static_cast<int>(segs), static_cast<uint4*>(W));
+        static_cast<const uint2*>(codes), sc, pieces, static_cast<int>(cols / 16), static_cast<int>(seg / 16),
+        group == 32 ? 1 : group == 64 ? 2 : 3, static_cast<int>(seg_groups), static_cast<int>(segs), static_cast<uint4*>(W));
   } else {
     dequantize_kernel<<<grid_of((rows * cols + 255) / 256), 256, 0, st>>>(
         static_cast<const uint8_t*>(codes), sc, rows, cols, static_cast<int>(segs), seg, group, seg_groups,
