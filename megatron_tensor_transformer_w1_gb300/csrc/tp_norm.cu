@@ -542,9 +542,10 @@ struct SumParams {
   void* to[5];
   long long parts[5], d, gates;
 };
+constexpr int SUM_WARPS = 32;
 template <typename T>
-__global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ SumParams p) {
-  __shared__ float4 s[8][32];
+__global__ void __launch_bounds__(SUM_WARPS * 32) sum_parts_kernel(const __grid_constant__ SumParams p) {
+  __shared__ float4 s[SUM_WARPS][32];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
   if (at < p.d) {
     const float* from = p.from[which] + gate * parts * p.d + at;
 #pragma unroll 4
-    for (long long i = warp; i < parts; i += 8) {
+    for (long long i = warp; i < parts; i += SUM_WARPS) {
       const float4 v = *reinterpret_cast<const float4*>(from + i * p.d);
       a.x += v.x;
       a.y += v.y;
@@ -565,18 +566,16 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
   }
   s[warp][lane] = a;
   __syncthreads();
-  if (warp || at >= p.d) return;
-  for (int w = 1; w < 8; ++w) {
-    a.x += s[w][lane].x;
-    a.y += s[w][lane].y;
-    a.z += s[w][lane].z;
-    a.w += s[w][lane].w;
-  }
-  T* to = static_cast<T*>(p.to[which]) + gate * p.d + at;
+  const long long col = static_cast<long long>(blockIdx.x) * 128 + threadIdx.x;
+  if (threadIdx.x >= 128 || col >= p.d) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < SUM_WARPS; ++w) sum += reinterpret_cast<const float*>(s[w])[threadIdx.x];
+  T* to = static_cast<T*>(p.to[which]) + gate * p.d + col;
   if constexpr (sizeof(T) == 2)
-    *reinterpret_cast<uint2*>(to) = make_uint2(tc::pack_bf16x2(a.x, a.y), tc::pack_bf16x2(a.z, a.w));
+    *to = __float2bfloat16_rn(sum);
   else
-    *reinterpret_cast<float4*>(to) = a;
+    *to = sum;
 }
 
 template <typename... KArgs, typename... Args>
@@ -754,9 +753,9 @@ int launch_norm_bwd(const NormSpec& a, void* workspace, int num_sms, cudaStream_
   if (p.want_sums || q.gates) {
     const dim3 blocks(static_cast<unsigned>((a.d + 127) / 128), static_cast<unsigned>(4 + q.gates));
     if (a.f32)
-      launch_dep(sum_parts_kernel<float>, blocks, 256, 0, st, q);
+      launch_dep(sum_parts_kernel<float>, blocks, SUM_WARPS * 32, 0, st, q);
     else
-      launch_dep(sum_parts_kernel<__nv_bfloat16>, blocks, 256, 0, st, q);
+      launch_dep(sum_parts_kernel<__nv_bfloat16>, blocks, SUM_WARPS * 32, 0, st, q);
   }
   return launched();
 }
