@@ -74,11 +74,11 @@ struct Eight<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ void load(Pairs& a, const void* p, long long at) {
+  static __device__ __forceinline__ void load(Pairs& a, const void* p, long long at, int) {
     open(a, *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
   }
   static __device__ __forceinline__ void load_slot(Pairs& a, uint32_t slot) { open(a, ld_shared(slot)); }
-  static __device__ __forceinline__ void store(void* p, long long bytes, const Pairs& a) {
+  static __device__ __forceinline__ void store(void* p, long long bytes, const Pairs& a, int) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -96,28 +96,40 @@ struct Eight<float> {
     a[2] = pair(w.x, w.y);
     a[3] = pair(w.z, w.w);
   }
-  static __device__ __forceinline__ void load(Pairs& a, const void* p, long long at) {
-    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    open(a, src[0], src[1]);
+  static __device__ __forceinline__ void load(Pairs& a, const void* p, long long at, int apart) {
+    const float* src = static_cast<const float*>(p) + at;
+    open(a, *reinterpret_cast<const float4*>(src), *reinterpret_cast<const float4*>(src + apart));
   }
   static __device__ __forceinline__ void load_slot(Pairs& a, uint32_t slot) {
     const uint4 v = ld_shared(slot), w = ld_shared(slot + blockDim.x * 16);
     open(a, make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)),
          make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)));
   }
-  static __device__ __forceinline__ void store(void* p, long long bytes, const Pairs& a) {
-    float4* to = reinterpret_cast<float4*>(static_cast<char*>(p) + bytes);
+  static __device__ __forceinline__ void store(void* p, long long bytes, const Pairs& a, int apart) {
+    float* to = reinterpret_cast<float*>(static_cast<char*>(p) + bytes);
     const float2 v = halves(a[0]), w = halves(a[1]), x = halves(a[2]), y = halves(a[3]);
-    to[0] = make_float4(v.x, v.y, w.x, w.y);
-    to[1] = make_float4(x.x, x.y, y.x, y.y);
+    *reinterpret_cast<float4*>(to) = make_float4(v.x, v.y, w.x, w.y);
+    *reinterpret_cast<float4*>(to + apart) = make_float4(x.x, x.y, y.x, y.y);
   }
 };
 
-// A row belongs to `tpr` threads, a multiple of 32, thread t of them having the
-// columns 8 t .. 8 t + 7; a block has blockDim / tpr row groups.  A thread copies its
+// A row belongs to `tpr` threads, a multiple of 32, a thread having eight of the
+// 256 columns of its warp: in bf16 one behind the other, in 32 bits two fours of which a
+// warp's lie one behind the other (a warp's 16-byte pieces side by side: with eight
+// columns in a row a store fills half of every sector, and the backward pass of 4104
+// tokens of 1160 took 44 us); a block has blockDim / tpr row groups.  A thread copies its
 // columns of the next rows into slots of its own in shared memory while it works on
 // this one (`stages` rows in all): it waits for nobody, and no registers are held for
 // them.
+template <typename T>
+__device__ __forceinline__ int columns_apart(int t, int d) {  // from a thread's first four to its second
+  const int left = d - (t >> 5) * 256;
+  return sizeof(T) == 2 || left <= 0 ? 4 : min(left, 256) / 2;
+}
+template <typename T>
+__device__ __forceinline__ int first_column(int t) {
+  return sizeof(T) == 2 ? 8 * t : (t >> 5) * 256 + (t & 31) * 4;
+}
 struct NormParams {
   int n, d, per;          // per: tokens of a gate
   int tpr, after, before, stages;
@@ -138,12 +150,12 @@ struct NormParams {
 
 // Not `valid`: the slot gets zeros, nothing is read.
 template <typename T>
-__device__ __forceinline__ void fetch(uint32_t slot, const void* p, long long bytes, bool valid = true) {
+__device__ __forceinline__ void fetch(uint32_t slot, const void* p, long long bytes, int apart, bool valid = true) {
   const char* src = static_cast<const char*>(p) + bytes;
   const int n = valid ? 16 : 0;
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * blockDim.x * 16), "l"(src + i * 16), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * blockDim.x * 16), "l"(src + i * apart * 4), "r"(n) : "memory");
 }
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // The oldest of stages - 1 groups, one for each row ahead, has landed (or, of one
@@ -168,7 +180,7 @@ template <typename T, bool SHORT>
 struct Held {
   Pairs a;
   __device__ __forceinline__ void set(float v) { fill(a, v); }
-  __device__ __forceinline__ void load(const void* p, long long at) { Eight<T>::load(a, p, at); }
+  __device__ __forceinline__ void load(const void* p, long long at, int apart) { Eight<T>::load(a, p, at, apart); }
   __device__ __forceinline__ void load_slot(uint32_t slot) { Eight<T>::load_slot(a, slot); }
   __device__ __forceinline__ uint64_t operator[](int i) const { return a[i]; }
 };
@@ -185,7 +197,7 @@ struct Held<__nv_bfloat16, true> {
     w[2] = v.z;
     w[3] = v.w;
   }
-  __device__ __forceinline__ void load(const void* p, long long at) { put(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at)); }
+  __device__ __forceinline__ void load(const void* p, long long at, int) { put(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at)); }
   __device__ __forceinline__ void load_slot(uint32_t slot) { put(ld_shared(slot)); }
   __device__ __forceinline__ uint64_t operator[](int i) const { return pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)); }
 };
@@ -256,8 +268,8 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
   const Group G(p.tpr);
-  const int col = 8 * t, step = gridDim.x * groups;
-  const bool ok = col < p.d;
+  const bool ok = 8 * t < p.d;
+  const int apart = columns_apart<T>(t, p.d), col = first_column<T>(t), step = gridDim.x * groups;
   const long long step_bytes = static_cast<long long>(step) * p.d * sizeof(T);
   const uint32_t array = slots<T>(blockDim.x) * 16, ring = tc::smem_u32(s_slots) + threadIdx.x * 16;
   int turn = 0, row = blockIdx.x * groups + group, gate_until = 0, ahead = row;
@@ -266,8 +278,8 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
   const uint32_t ring_end = ring + p.stages * 2 * array;
   auto fetch_row = [&] {
     if (ok && ahead < p.n) {
-      fetch<T>(ahead_stage, p.x, ahead_bytes);
-      if (p.b) fetch<T>(ahead_stage + array, p.b, ahead_bytes);
+      fetch<T>(ahead_stage, p.x, ahead_bytes, apart);
+      if (p.b) fetch<T>(ahead_stage + array, p.b, ahead_bytes, apart);
     }
     fetch_commit();
     ahead += step;
@@ -281,25 +293,25 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
   fill(k0, 0.f);
   fill(w, 1.f);
   fill(c, 0.f);
-  if (ok && p.w_before) Eight<T>::load(w, p.w_before, col);
-  if (SHIFT && ok && p.c_before) Eight<T>::load(c, p.c_before, col);
+  if (ok && p.w_before) Eight<T>::load(w, p.w_before, col, apart);
+  if (SHIFT && ok && p.c_before) Eight<T>::load(c, p.c_before, col, apart);
   for (; row - group < p.n; row += step, bytes += step_bytes) {
     const bool live = ok && row < p.n;
     if (p.b && live && row >= gate_until) {
       const int gate_at = p.gate ? row / p.per : 0;
       gate_until = p.gate ? (gate_at + 1) * p.per : p.n;
       fill(k1, 1.f);
-      if (p.gate) Eight<T>::load(k1, p.gate, static_cast<long long>(gate_at) * p.d + col);
+      if (p.gate) Eight<T>::load(k1, p.gate, static_cast<long long>(gate_at) * p.d + col, apart);
 #pragma unroll
       for (int i = 0; i < 4; ++i) k1[i] = mul2(k1[i], both(p.scale));
       if (SHIFT && p.c_after) {
-        Eight<T>::load(k0, p.c_after, col);
+        Eight<T>::load(k0, p.c_after, col, apart);
 #pragma unroll
         for (int i = 0; i < 4; ++i) k0[i] = mul2(k0[i], k1[i]);
       }
       if (p.w_after) {
         Pairs wa;
-        Eight<T>::load(wa, p.w_after, col);
+        Eight<T>::load(wa, p.w_after, col, apart);
 #pragma unroll
         for (int i = 0; i < 4; ++i) k1[i] = mul2(k1[i], wa[i]);
       }
@@ -321,7 +333,7 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = fma2(unit<LAYER>(u[i], both(-sa.x), both(sa.y)), k1[i], SHIFT ? add2(v[i], k0[i]) : v[i]);
     }
-    if (live) Eight<T>::store(p.r, bytes, v);
+    if (live) Eight<T>::store(p.r, bytes, v, apart);
     if (p.before) {
       sb = row_stats<LAYER>(v, ok, p, G, s_sum, turn);
 #pragma unroll
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
         const uint64_t y = unit<LAYER>(v[i], both(-sb.x), both(sb.y));
         v[i] = SHIFT ? fma2(y, w[i], c[i]) : mul2(y, w[i]);
       }
-      if (live) Eight<T>::store(p.out, bytes, v);
+      if (live) Eight<T>::store(p.out, bytes, v, apart);
     }
     if (p.stats && live && t == 0) {
       float2* st = reinterpret_cast<float2*>(p.stats + row);
@@ -353,8 +365,8 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
   grid_dep_launch();
   const int t = threadIdx.x % p.tpr, group = threadIdx.x / p.tpr, groups = blockDim.x / p.tpr;
   const Group G(p.tpr);
-  const int col = 8 * t;
-  const bool ok = col < p.d;
+  const bool ok = 8 * t < p.d;
+  const int apart = columns_apart<T>(t, p.d), col = first_column<T>(t);
   const long long step_bytes = static_cast<long long>(groups) * p.d * sizeof(T);
   const uint32_t array = slots<T>(blockDim.x) * 16, row_slots = (p.gate_each ? 5 : 4) * array;
   const uint32_t ring = tc::smem_u32(s_slots) + threadIdx.x * 16, ring_end = ring + p.stages * row_slots;
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
     const bool there = ok && at.unit < p.units && at.row < at.to;
     auto array_of = [&](int a, const void* from) {
       const bool valid = there && from;
-      fetch<T>(at.slot + a * array, valid ? from : some, valid ? at.bytes : 0, valid);
+      fetch<T>(at.slot + a * array, valid ? from : some, valid ? at.bytes : 0, apart, valid);
     };
     array_of(A_DR, p.dr);
     if (p.before) {
@@ -412,10 +424,10 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
   ca.set(0.f);
   wb.set(1.f);
   gate.set(1.f);
-  if (ok && p.w_after) wa.load(p.w_after, col);
-  if (ok && p.c_after) ca.load(p.c_after, col);
-  if (ok && p.w_before) wb.load(p.w_before, col);
-  if (ok && p.gate && !p.gate_each && here.unit < p.units) gate.load(p.gate, static_cast<long long>(here.unit / p.chunks) * p.d + col);
+  if (ok && p.w_after) wa.load(p.w_after, col, apart);
+  if (ok && p.c_after) ca.load(p.c_after, col, apart);
+  if (ok && p.w_before) wb.load(p.w_before, col, apart);
+  if (ok && p.gate && !p.gate_each && here.unit < p.units) gate.load(p.gate, static_cast<long long>(here.unit / p.chunks) * p.d + col, apart);
   Pairs sums[4] = {}, gsum = {};
   // A column sum over the block's row groups, then to `write`.
   auto flush = [&](Pairs& a, float* s_cols, auto&& write) {
@@ -479,7 +491,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = fma2(fma2(y[i], m1, LAYER ? add2(dy[i], m0) : dy[i]), both(st.w), g[i]);
     }
-    if (p.dx && live) Eight<T>::store(p.dx, here.bytes, g);
+    if (p.dx && live) Eight<T>::store(p.dx, here.bytes, g, apart);
     if (p.b || p.db) {  // (of all threads)
       Pairs y;
       Eight<T>::load_slot(y, here.slot + A_B * array);
@@ -500,7 +512,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
         s0 = fma2(g[i], y[i], s0);
         if (LAYER) s1 = add2(s1, g[i]);
       }
-      if (p.gate_each && p.dgate && live) Eight<T>::store(p.dgate, here.bytes, gsum);
+      if (p.gate_each && p.dgate && live) Eight<T>::store(p.dgate, here.bytes, gsum, apart);
       if (p.after) {
         float s[N];
         s[0] = total(s0);
@@ -510,20 +522,20 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[i] = mul2(fma2(y[i], m1, LAYER ? add2(g[i], m0) : g[i]), both(st.y));
       }
-      if (p.db && live) Eight<T>::store(p.db, here.bytes, g);
+      if (p.db && live) Eight<T>::store(p.db, here.bytes, g, apart);
     }
     if (ends && p.gate && !p.gate_each) {
       const long long gi = here.unit / p.chunks;
       if (p.dgate) {
         flush(gsum, s_cols, [&](const Pairs& a) {
           if (p.chunks == 1)
-            Eight<T>::store(p.dgate, (gi * p.d + col) * sizeof(T), a);
+            Eight<T>::store(p.dgate, (gi * p.d + col) * sizeof(T), a, apart);
           else
-            Eight<float>::store(p.gate_sums, (static_cast<long long>(here.unit) * p.d + col) * 4, a);
+            Eight<float>::store(p.gate_sums, (static_cast<long long>(here.unit) * p.d + col) * 4, a, apart);
         });
         fill(gsum, 0.f);
       }
-      if (ok && next.unit < p.units) gate.load(p.gate, static_cast<long long>(next.unit / p.chunks) * p.d + col);
+      if (ok && next.unit < p.units) gate.load(p.gate, static_cast<long long>(next.unit / p.chunks) * p.d + col, apart);
     }
     here = next;
   }
@@ -531,7 +543,7 @@ __global__ void __launch_bounds__(MAX_THREADS) backward_kernel(const __grid_cons
   for (int k = 0; k < 4; ++k)
     if (p.want_sums >> k & 1)
       flush(sums[k], s_cols, [&](const Pairs& a) {
-        Eight<float>::store(p.sums, ((static_cast<long long>(k) * gridDim.x + blockIdx.x) * p.d + col) * 4, a);
+        Eight<float>::store(p.sums, ((static_cast<long long>(k) * gridDim.x + blockIdx.x) * p.d + col) * 4, a, apart);
       });
 }
 
