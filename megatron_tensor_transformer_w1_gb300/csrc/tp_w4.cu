@@ -149,21 +149,111 @@ __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict
   }
 }
 
-// Widths that 16-element pieces do not fit: the scales, a warp to a group, then
-// the codes, a thread to a byte (whose two columns may belong to two segments).
+// Widths that 16-element pieces do not fit: the scales, eight threads to a group, then
+// the codes, a thread to eight columns (or, with segments of less than eight, to a byte,
+// whose two columns may belong to two segments).
 __global__ void __launch_bounds__(256) scales_kernel(const __nv_bfloat16* __restrict__ W, long long rows, long long cols,
-                                                     int segs, long long seg, int group, long long seg_groups,
+                                                     int segs, int seg, int group, int seg_groups,
                                                      __nv_bfloat16* __restrict__ scales) {
-  const long long row_groups = segs * seg_groups, total = rows * row_groups;
-  const int lane = threadIdx.x & 31;
-  for (long long g = blockIdx.x * 8ll + (threadIdx.x >> 5); g < total; g += gridDim.x * 8ll) {
-    const long long row = g / row_groups, in = g - row * row_groups, e = in / seg_groups, first = (in - e * seg_groups) * group;
-    const __nv_bfloat16* src = W + row * cols + e * seg;
+  const long long stride = gridDim.x * 32ll, first = blockIdx.x * 32ll;
+  const int lane = threadIdx.x & 7;
+  Walk at(first + (threadIdx.x >> 3), stride, static_cast<unsigned>(segs) * seg_groups);
+  for (long long g0 = first; g0 < rows * (static_cast<long long>(segs) * seg_groups); g0 += stride, at.next()) {
+    const int e = segs == 1 ? 0 : static_cast<int>(at.place) / seg_groups, in = (static_cast<int>(at.place) - e * seg_groups) * group;
+    const __nv_bfloat16* src = W + at.row * cols + static_cast<long long>(e) * seg + in;
+    const int live = at.row < rows ? min(group, seg - in) : 0;
     __nv_bfloat16 m = __float2bfloat16_rn(0.f);
-    for (int j = lane; j < group && first + j < seg; j += 32) m = __hmax_nan(m, __habs(src[first + j]));
+#pragma unroll 4
+    for (int j = lane; j < live; j += 8) m = __hmax_nan(m, __habs(src[j]));
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = __hmax_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (lane == 0) scales[g] = __float2bfloat16_rn(group_scale(__bfloat162float(m)));
+    for (int d = 4; d; d >>= 1) m = __hmax_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0 && live) scales[at.row * at.width + at.place] = __float2bfloat16_rn(group_scale(__bfloat162float(m)));
+  }
+}
+// The groups of eight columns from c on, of segments of at least eight: up to `first` the
+// scale at `at`, up to `second` the next (a segment's last group may be of one column),
+// then the one behind it.
+struct Groups {
+  int at, first, second;
+  __device__ __forceinline__ Groups(int c, int segs, int seg, int group, int seg_groups) {
+    const int e = segs == 1 ? 0 : c / seg, in = c - e * seg, g = group == 32 ? in >> 5 : group == 64 ? in >> 6 : in >> 7;
+    const int end = min((g + 1) * group, seg);
+    at = e * seg_groups + g;
+    first = end - in;
+    second = first + (end == seg ? 8 : min(group, seg - end));
+  }
+  template <typename V>
+  __device__ __forceinline__ V of(int j, V a, V b, V c) const {
+    return j < first ? a : j < second ? b : c;
+  }
+};
+// Eight columns of a row, where it may begin at any even address.  Columns behind
+// `live` are zeros, or are not written.
+__device__ __forceinline__ void load8(uint32_t (&v)[4], const __nv_bfloat16* src, int live, long long cols) {
+  v[0] = v[1] = v[2] = v[3] = 0;
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+  if (live == 8 && cols % 8 == 0) {
+    const uint4 a = *reinterpret_cast<const uint4*>(src);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  } else if (live == 8 && cols % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = reinterpret_cast<const uint32_t*>(src)[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < live) v[j >> 1] |= static_cast<uint32_t>(h[j]) << (16 * (j & 1));
+  }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* to, const uint32_t (&v)[4], int live, long long cols) {
+  uint16_t* h = reinterpret_cast<uint16_t*>(to);
+  if (live == 8 && cols % 8 == 0) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+  } else if (live == 8 && cols % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(to)[j] = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < live) h[j] = static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1)));
+  }
+}
+__global__ void __launch_bounds__(256) codes8_kernel(const __nv_bfloat16* __restrict__ W, long long rows, int cols, int segs,
+                                                     int seg, int group, int seg_groups,
+                                                     const __nv_bfloat16* __restrict__ scales, uint8_t* __restrict__ codes) {
+  const long long row_bytes = (cols + 1) / 2, stride = gridDim.x * 256ll;
+  for (Walk at(blockIdx.x * 256ll + threadIdx.x, stride, (cols + 7) / 8); at.row < rows; at.next()) {
+    const int c = static_cast<int>(at.place) * 8, live = min(cols - c, 8);
+    const Groups of(c, segs, seg, group, seg_groups);
+    const __nv_bfloat16* sc = scales + at.row * (static_cast<long long>(segs) * seg_groups) + of.at;
+    uint32_t v[4];
+    load8(v, W + at.row * cols + c, live, cols);
+    float sg[3], inv[3], up[3];
+    uint32_t any[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      sg[k] = k == 0 || (k == 1 ? of.first : of.second) < live ? __bfloat162float(sc[k]) : sg[0];
+      any[k] = has_codes(sg[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) ready(sg[k], inv[k], up[k]);
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      auto pick = [&](int i, auto& v) { return of.of(i, v[0], v[1], v[2]); };
+      const int a = 2 * j, b = a + 1;
+      const uint2 q = codes_of(pack2(bf16_at(v[j], 0) * pick(a, up), bf16_at(v[j], 1) * pick(b, up)), pack2(-pick(a, sg), -pick(b, sg)),
+                               pack2(pick(a, inv), pick(b, inv)));
+      const uint32_t lo = pick(a, any) ? q.x & 15u : 8u, hi = pick(b, any) && b < live ? q.y & 15u : 8u;
+      word |= (lo | hi << 4) << (8 * j);
+    }
+    uint8_t* to = codes + at.row * row_bytes + c / 2;
+    if (row_bytes % 4 == 0 && live == 8) {
+      *reinterpret_cast<uint32_t*>(to) = word;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (2 * j < live) to[j] = static_cast<uint8_t>(word >> (8 * j));
+    }
   }
 }
 __global__ void __launch_bounds__(256) codes_kernel(const __nv_bfloat16* __restrict__ W, long long rows, long long cols,
@@ -230,6 +320,34 @@ __global__ void __launch_bounds__(256) dequantize16_kernel(const uint2* __restri
     at_row.next();
     write(W + 2 * i, q0, s0 * 0x10001u);
     if (more) write(W + 2 * (i + stride), q1, s1 * 0x10001u);
+  }
+}
+__global__ void __launch_bounds__(256) dequantize8_kernel(const uint8_t* __restrict__ codes,
+                                                          const __nv_bfloat16* __restrict__ scales, long long rows, int cols,
+                                                          int segs, int seg, int group, int seg_groups,
+                                                          __nv_bfloat16* __restrict__ W) {
+  const long long row_bytes = (cols + 1) / 2, stride = gridDim.x * 256ll;
+  for (Walk at(blockIdx.x * 256ll + threadIdx.x, stride, (cols + 7) / 8); at.row < rows; at.next()) {
+    const int c = static_cast<int>(at.place) * 8, live = min(cols - c, 8);
+    const Groups of(c, segs, seg, group, seg_groups);
+    const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales) + at.row * (static_cast<long long>(segs) * seg_groups) + of.at;
+    const uint8_t* from = codes + at.row * row_bytes + c / 2;
+    uint32_t word = 0;
+    if (row_bytes % 4 == 0 && live == 8) {
+      word = *reinterpret_cast<const uint32_t*>(from);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (2 * j < live) word |= static_cast<uint32_t>(from[j]) << (8 * j);
+    }
+    const uint32_t s0 = sc[0], s1 = of.first < live ? sc[1] : s0, s2 = of.second < live ? sc[2] : s0;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t byte = word >> (8 * j) & 0xffu;
+      w[j] = two_values(byte | byte << 12, of.of(2 * j, s0, s1, s2) | of.of(2 * j + 1, s0, s1, s2) << 16);
+    }
+    store8(W + at.row * cols + c, w, live, cols);
   }
 }
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restrict__ codes,
@@ -1293,9 +1411,13 @@ int launch_w4_quantize(const void* W, int64_t rows, int64_t cols, int64_t segs, 
     return launched();
   }
   const auto* w = static_cast<const __nv_bfloat16*>(W);
-  scales_kernel<<<grid_of((rows * segs * seg_groups + 7) / 8), 256, 0, st>>>(w, rows, cols, static_cast<int>(segs), seg,
-                                                                             group, seg_groups, sc);
-  codes_kernel<<<grid_of((rows * ((cols + 1) / 2) + 255) / 256), 256, 0, st>>>(
+  const int n_segs = static_cast<int>(segs), width = static_cast<int>(seg), groups = static_cast<int>(seg_groups);
+  scales_kernel<<<grid_of((rows * segs * seg_groups + 31) / 32), 256, 0, st>>>(w, rows, cols, n_segs, width, group, groups, sc);
+  if (seg >= 8)
+    codes8_kernel<<<grid_of((rows * ((cols + 7) / 8) + 255) / 256), 256, 0, st>>>(
+        w, rows, static_cast<int>(cols), n_segs, width, group, groups, sc, static_cast<uint8_t*>(codes));
+  else
+    codes_kernel<<<grid_of((rows * ((cols + 1) / 2) + 255) / 256), 256, 0, st>>>(
       w, rows, cols, static_cast<int>(segs), seg, group, seg_groups, sc, static_cast<uint8_t*>(codes));
   return launched();
 }
@@ -1310,6 +1432,10 @@ int launch_w4_dequantize(const void* codes, const void* scales, int64_t rows, in
     dequantize16_kernel<<<grid_of((pieces + 255) / 256), 256, 0, st>>>(
         static_cast<const uint2*>(codes), sc, pieces, static_cast<int>(cols / 16), static_cast<int>(seg / 16),
         group == 32 ? 1 : group == 64 ? 2 : 3, static_cast<int>(seg_groups), static_cast<int>(segs), static_cast<uint4*>(W));
+  } else if (seg >= 8) {
+    dequantize8_kernel<<<grid_of((rows * ((cols + 7) / 8) + 255) / 256), 256, 0, st>>>(
+        static_cast<const uint8_t*>(codes), sc, rows, static_cast<int>(cols), static_cast<int>(segs), static_cast<int>(seg),
+        group, static_cast<int>(seg_groups), static_cast<__nv_bfloat16*>(W));
   } else {
     dequantize_kernel<<<grid_of((rows * cols + 255) / 256), 256, 0, st>>>(
         static_cast<const uint8_t*>(codes), sc, rows, cols, static_cast<int>(segs), seg, group, seg_groups,
