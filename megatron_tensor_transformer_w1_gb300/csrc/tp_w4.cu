@@ -60,17 +60,21 @@ __device__ __forceinline__ float pow2(int e) {
 // s = bf16(max |w| / 7), code = rint(w / s) + 8, ties to even.
 // A group with an infinity or NaN has that for its scale.  With s = 0 (all
 // zero, or too small for bf16) every code is 8.
-__device__ __forceinline__ float group_scale(float amax) { return __bfloat162float(__float2bfloat16_rn(amax / 7.f)); }
+// The quotient by a product with 1 / 7 and its remainder, which is exact.
+__device__ __forceinline__ float group_scale(float amax) {
+  const float seventh = 1.f / 7.f, q = amax * seventh;
+  return __bfloat162float(__float2bfloat16_rn(amax < INFINITY ? fmaf(fmaf(-7.f, q, amax), seventh, q) : amax));
+}
 
 // 1 / s overflows for the smallest scales: s and w are brought up by 2^64 first.
 __device__ __forceinline__ void ready(float& s, float& inv, float& up) {
   up = s < 1e-30f ? 18446744073709551616.f : 1.f;
   s *= up;
-  inv = 1.f / s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // (to 2^-22; s is below 2^126)
 }
 // The codes of two elements, in the low bytes, for finite s > 0 and |w| <= 7.03 s.  The
 // quotient in two steps: q = w inv, then q + (w - q s) inv, whose remainder is exact and
-// which is the quotient to 2^-46 before its last rounding: a tie, which 32 bits hold,
+// which is the quotient to 2^-43 before its last rounding: a tie, which 32 bits hold,
 // comes out exactly, and others lie at least 2^-18 from one.  The sum with 1.5 2^23 + 8
 // has a last bit worth 1: ties go to the even code.
 __device__ __forceinline__ uint2 codes_of(uint64_t w, uint64_t less_s, uint64_t inv) {
@@ -149,27 +153,6 @@ __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict
   }
 }
 
-// Widths that 16-element pieces do not fit: the scales, eight threads to a group, then
-// the codes, a thread to eight columns (or, with segments of less than eight, to a byte,
-// whose two columns may belong to two segments).
-__global__ void __launch_bounds__(256) scales_kernel(const __nv_bfloat16* __restrict__ W, long long rows, long long cols,
-                                                     int segs, int seg, int group, int seg_groups,
-                                                     __nv_bfloat16* __restrict__ scales) {
-  const long long stride = gridDim.x * 32ll, first = blockIdx.x * 32ll;
-  const int lane = threadIdx.x & 7;
-  Walk at(first + (threadIdx.x >> 3), stride, static_cast<unsigned>(segs) * seg_groups);
-  for (long long g0 = first; g0 < rows * (static_cast<long long>(segs) * seg_groups); g0 += stride, at.next()) {
-    const int e = segs == 1 ? 0 : static_cast<int>(at.place) / seg_groups, in = (static_cast<int>(at.place) - e * seg_groups) * group;
-    const __nv_bfloat16* src = W + at.row * cols + static_cast<long long>(e) * seg + in;
-    const int live = at.row < rows ? min(group, seg - in) : 0;
-    __nv_bfloat16 m = __float2bfloat16_rn(0.f);
-#pragma unroll 4
-    for (int j = lane; j < live; j += 8) m = __hmax_nan(m, __habs(src[j]));
-#pragma unroll
-    for (int d = 4; d; d >>= 1) m = __hmax_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (lane == 0 && live) scales[at.row * at.width + at.place] = __float2bfloat16_rn(group_scale(__bfloat162float(m)));
-  }
-}
 // The groups of eight columns from c on, of segments of at least eight: up to `first` the
 // scale at `at`, up to `second` the next (a segment's last group may be of one column),
 // then the one behind it.
@@ -187,34 +170,102 @@ struct Groups {
     return j < first ? a : j < second ? b : c;
   }
 };
-// Eight columns of a row, where it may begin at any even address.  Columns behind
-// `live` are zeros, or are not written.
-__device__ __forceinline__ void load8(uint32_t (&v)[4], const __nv_bfloat16* src, int live, long long cols) {
-  v[0] = v[1] = v[2] = v[3] = 0;
+// Eight columns from any even address on, in the largest pieces that it allows.  Columns
+// behind `live` are zeros, or are not written.
+__device__ __forceinline__ void load8(uint32_t (&v)[4], const __nv_bfloat16* src, int live) {
   const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
-  if (live == 8 && cols % 8 == 0) {
+  const int low = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+  if (live < 8) {
+    v[0] = v[1] = v[2] = v[3] = 0;
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < live) v[j >> 1] |= static_cast<uint32_t>(h[j]) << (16 * (j & 1));
+  } else if (low == 0) {
     const uint4 a = *reinterpret_cast<const uint4*>(src);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  } else if (live == 8 && cols % 2 == 0) {
+  } else if ((low & 3) == 0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = reinterpret_cast<const uint32_t*>(src)[j];
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < live) v[j >> 1] |= static_cast<uint32_t>(h[j]) << (16 * (j & 1));
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(h + 1);
+    const uint32_t a = h[0], b = w[0], c = w[1], d = w[2], e = h[7];
+    v[0] = a | b << 16, v[1] = b >> 16 | c << 16, v[2] = c >> 16 | d << 16, v[3] = d >> 16 | e << 16;
   }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* to, const uint32_t (&v)[4], int live, long long cols) {
+__device__ __forceinline__ void store8(__nv_bfloat16* to, const uint32_t (&v)[4], int live) {
   uint16_t* h = reinterpret_cast<uint16_t*>(to);
-  if (live == 8 && cols % 8 == 0) {
+  const int low = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 15);
+  if (live < 8) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < live) h[j] = static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1)));
+  } else if (low == 0) {
     *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
-  } else if (live == 8 && cols % 2 == 0) {
+  } else if ((low & 3) == 0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(to)[j] = v[j];
   } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(h + 1);
+    h[0] = static_cast<uint16_t>(v[0]);
+    w[0] = v[0] >> 16 | v[1] << 16, w[1] = v[1] >> 16 | v[2] << 16, w[2] = v[2] >> 16 | v[3] << 16;
+    h[7] = static_cast<uint16_t>(v[3] >> 16);
+  }
+}
+// Four bytes from any address on, of which `live` are there.
+__device__ __forceinline__ uint32_t load4(const uint8_t* src, int live) {
+  const int low = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 3);
+  uint32_t w = 0;
+  if (live < 4) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < live) h[j] = static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < 3; ++j)
+      if (j < live) w |= static_cast<uint32_t>(src[j]) << (8 * j);
+  } else if (low == 0) {
+    w = *reinterpret_cast<const uint32_t*>(src);
+  } else if (low == 2) {
+    w = reinterpret_cast<const uint16_t*>(src)[0] | static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[1]) << 16;
+  } else {
+    w = src[0] | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + 1)) << 8 | static_cast<uint32_t>(src[3]) << 24;
+  }
+  return w;
+}
+__device__ __forceinline__ void store4(uint8_t* to, uint32_t w, int live) {
+  const int low = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 3);
+  if (live < 4) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < live) to[j] = static_cast<uint8_t>(w >> (8 * j));
+  } else if (low == 0) {
+    *reinterpret_cast<uint32_t*>(to) = w;
+  } else if (low == 2) {
+    reinterpret_cast<uint16_t*>(to)[0] = static_cast<uint16_t>(w);
+    reinterpret_cast<uint16_t*>(to)[1] = static_cast<uint16_t>(w >> 16);
+  } else {
+    to[0] = static_cast<uint8_t>(w);
+    *reinterpret_cast<uint16_t*>(to + 1) = static_cast<uint16_t>(w >> 8);
+    to[3] = static_cast<uint8_t>(w >> 24);
+  }
+}
+// Widths that 16-element pieces do not fit: the scales, a thread to eight columns of a
+// group, then the codes, a thread to eight columns of a row (or, with segments of less
+// than eight, to a byte, whose two columns may belong to two segments).
+// 8 << lanes columns to a group.
+__global__ void __launch_bounds__(256) scales_kernel(const __nv_bfloat16* __restrict__ W, long long rows, long long cols,
+                                                     int segs, int seg, int lanes, int seg_groups,
+                                                     __nv_bfloat16* __restrict__ scales) {
+  const int per = 256 >> lanes, lane = threadIdx.x & ((1 << lanes) - 1), group = 8 << lanes;
+  const long long stride = static_cast<long long>(gridDim.x) * per, first = static_cast<long long>(blockIdx.x) * per;
+  Walk at(first + (threadIdx.x >> lanes), stride, static_cast<unsigned>(segs) * seg_groups);
+  for (long long g0 = first; g0 < rows * (static_cast<long long>(segs) * seg_groups); g0 += stride, at.next()) {
+    const int e = segs == 1 ? 0 : static_cast<int>(at.place) / seg_groups, g = static_cast<int>(at.place) - e * seg_groups;
+    const int in = g * group + lane * 8, live = at.row < rows ? min(seg - in, 8) : 0;
+    uint32_t v[4] = {};
+    if (live > 0) load8(v, W + at.row * cols + static_cast<long long>(e) * seg + in, live);
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<__nv_bfloat162*>(&v[0]));
+#pragma unroll
+    for (int j = 1; j < 4; ++j) m = __hmax2_nan(m, __habs2(*reinterpret_cast<__nv_bfloat162*>(&v[j])));
+    for (int d = 1; d < 1 << lanes; d <<= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0 && live > 0)
+      scales[at.row * at.width + at.place] = __float2bfloat16_rn(group_scale(__bfloat162float(__hmax_nan(m.x, m.y))));
   }
 }
 __global__ void __launch_bounds__(256) codes8_kernel(const __nv_bfloat16* __restrict__ W, long long rows, int cols, int segs,
@@ -226,7 +277,7 @@ __global__ void __launch_bounds__(256) codes8_kernel(const __nv_bfloat16* __rest
     const Groups of(c, segs, seg, group, seg_groups);
     const __nv_bfloat16* sc = scales + at.row * (static_cast<long long>(segs) * seg_groups) + of.at;
     uint32_t v[4];
-    load8(v, W + at.row * cols + c, live, cols);
+    load8(v, W + at.row * cols + c, live);
     float sg[3], inv[3], up[3];
     uint32_t any[3];
 #pragma unroll
@@ -246,14 +297,7 @@ __global__ void __launch_bounds__(256) codes8_kernel(const __nv_bfloat16* __rest
       const uint32_t lo = pick(a, any) ? q.x & 15u : 8u, hi = pick(b, any) && b < live ? q.y & 15u : 8u;
       word |= (lo | hi << 4) << (8 * j);
     }
-    uint8_t* to = codes + at.row * row_bytes + c / 2;
-    if (row_bytes % 4 == 0 && live == 8) {
-      *reinterpret_cast<uint32_t*>(to) = word;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (2 * j < live) to[j] = static_cast<uint8_t>(word >> (8 * j));
-    }
+    store4(codes + at.row * row_bytes + c / 2, word, (live + 1) / 2);
   }
 }
 __global__ void __launch_bounds__(256) codes_kernel(const __nv_bfloat16* __restrict__ W, long long rows, long long cols,
@@ -331,15 +375,7 @@ __global__ void __launch_bounds__(256) dequantize8_kernel(const uint8_t* __restr
     const int c = static_cast<int>(at.place) * 8, live = min(cols - c, 8);
     const Groups of(c, segs, seg, group, seg_groups);
     const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales) + at.row * (static_cast<long long>(segs) * seg_groups) + of.at;
-    const uint8_t* from = codes + at.row * row_bytes + c / 2;
-    uint32_t word = 0;
-    if (row_bytes % 4 == 0 && live == 8) {
-      word = *reinterpret_cast<const uint32_t*>(from);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (2 * j < live) word |= static_cast<uint32_t>(from[j]) << (8 * j);
-    }
+    const uint32_t word = load4(codes + at.row * row_bytes + c / 2, (live + 1) / 2);
     const uint32_t s0 = sc[0], s1 = of.first < live ? sc[1] : s0, s2 = of.second < live ? sc[2] : s0;
     uint32_t w[4];
 #pragma unroll
@@ -347,7 +383,7 @@ __global__ void __launch_bounds__(256) dequantize8_kernel(const uint8_t* __restr
       const uint32_t byte = word >> (8 * j) & 0xffu;
       w[j] = two_values(byte | byte << 12, of.of(2 * j, s0, s1, s2) | of.of(2 * j + 1, s0, s1, s2) << 16);
     }
-    store8(W + at.row * cols + c, w, live, cols);
+    store8(W + at.row * cols + c, w, live);
   }
 }
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restrict__ codes,
@@ -1412,7 +1448,9 @@ int launch_w4_quantize(const void* W, int64_t rows, int64_t cols, int64_t segs, 
   }
   const auto* w = static_cast<const __nv_bfloat16*>(W);
   const int n_segs = static_cast<int>(segs), width = static_cast<int>(seg), groups = static_cast<int>(seg_groups);
-  scales_kernel<<<grid_of((rows * segs * seg_groups + 31) / 32), 256, 0, st>>>(w, rows, cols, n_segs, width, group, groups, sc);
+  const int lanes = group == 32 ? 2 : group == 64 ? 3 : 4;
+  scales_kernel<<<grid_of((((rows * segs * seg_groups) << lanes) + 255) / 256), 256, 0, st>>>(w, rows, cols, n_segs, width,
+                                                                                              lanes, groups, sc);
   if (seg >= 8)
     codes8_kernel<<<grid_of((rows * ((cols + 7) / 8) + 255) / 256), 256, 0, st>>>(
         w, rows, static_cast<int>(cols), n_segs, width, group, groups, sc, static_cast<uint8_t*>(codes));
