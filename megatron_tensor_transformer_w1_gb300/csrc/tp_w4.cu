@@ -283,19 +283,25 @@ __global__ void __launch_bounds__(256) codes8_kernel(const __nv_bfloat16* __rest
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       sg[k] = k == 0 || (k == 1 ? of.first : of.second) < live ? __bfloat162float(sc[k]) : sg[0];
-      any[k] = has_codes(sg[k]);
+      any[k] = has_codes(sg[k]) ? 15u : 0u;
+      ready(sg[k], inv[k], up[k]);
     }
+    auto pick = [&](int i, auto& a) { return of.of(i, a[0], a[1], a[2]); };
+    if (up[0] != 1.f || up[1] != 1.f || up[2] != 1.f) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) ready(sg[k], inv[k], up[k]);
+      for (int j = 0; j < 4; ++j) v[j] = tc::pack_bf16x2(bf16_at(v[j], 0) * pick(2 * j, up), bf16_at(v[j], 1) * pick(2 * j + 1, up));
+    }
     uint32_t word = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      auto pick = [&](int i, auto& v) { return of.of(i, v[0], v[1], v[2]); };
       const int a = 2 * j, b = a + 1;
-      const uint2 q = codes_of(pack2(bf16_at(v[j], 0) * pick(a, up), bf16_at(v[j], 1) * pick(b, up)), pack2(-pick(a, sg), -pick(b, sg)),
-                               pack2(pick(a, inv), pick(b, inv)));
-      const uint32_t lo = pick(a, any) ? q.x & 15u : 8u, hi = pick(b, any) && b < live ? q.y & 15u : 8u;
-      word |= (lo | hi << 4) << (8 * j);
+      const uint2 q = codes_of(pack2(bf16_at(v[j], 0), bf16_at(v[j], 1)), pack2(-pick(a, sg), -pick(b, sg)), pack2(pick(a, inv), pick(b, inv)));
+      word |= (q.x & 15u) << (8 * j) | (q.y & 15u) << (8 * j + 4);
+    }
+    if (!(any[0] & any[1] & any[2]) || live < 8) {  // codes of 8 in the place of some
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!pick(j, any) || j >= live) word = (word & ~(15u << (4 * j))) | 8u << (4 * j);
     }
     store4(codes + at.row * row_bytes + c / 2, word, (live + 1) / 2);
   }
