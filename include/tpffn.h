@@ -518,13 +518,17 @@ TPFFN_API int tp_ffn_unshard_rows4(const tp_ffn_plan* plan, int group, const voi
 
 /* tp_ffn_fwd for inference from packed 4-bit weights (w13_4 NULL for act NONE;
  * both of the same group): x, b1, b2 and y as there.  The shards are summed in
- * the order t = 0..T_p-1; results do not change from run to run.  A product is
- * summed in 32 bits within a group, times its scale, over the groups in 32 bits;
- * the hidden activations are rounded to bf16 or better.  A token with an infinity
- * or a NaN, in x or among its hidden activations, gets those; the others are as
- * without it.
+ * the order t = 0..T_p-1; results do not change from run to run (those of a token
+ * may in their last bit with the number of tokens beside it).  Products are summed
+ * in 32 bits; neither the scaled weights nor the hidden activations are rounded to
+ * bf16: they are kept to 11 bits, what is below 2^-28 of the largest of its row or
+ * 2^-25 of a bound of its token with fewer.  A token with an infinity or a NaN, in x
+ * or among its hidden activations, gets those, as does a row of W2 with such a scale;
+ * the others are as without it.
+ * More than 512 tokens go through it in equal parts of at most 512, and the
+ * workspace is that of one part.
  * flags: TP_FLAG_SYNC, TP_FLAG_TIMING; the TP_SUM_* choices make no difference.
- * Errors as tp_ffn_fwd; TP_ERR_UNSUPPORTED for fp32 plans. */
+ * Errors as tp_ffn_fwd; TP_ERR_UNSUPPORTED for fp32 plans and n_tokens above 2^30. */
 TPFFN_API size_t tp_ffn_workspace4_bytes(const tp_ffn_plan* plan, int64_t n_tokens, int flags);
 TPFFN_API int tp_ffn_fwd4(const tp_ffn_plan* plan, int group, int64_t n_tokens, const void* x, const void* w13_4,
                           const void* w2_4, const void* b1, const void* b2, void* y, void* workspace,

@@ -1,12 +1,11 @@
 // tp_w4.cu -- 4-bit weights with group scales: quantising, the layout that the
-// products read, and the products of few tokens with such weights.
+// products read, and the products with such weights.
 //
 // A group of `group` consecutive columns of a row has the scale s (bf16), its
 // elements are (code - 8) s with codes 0..15.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -104,7 +103,8 @@ struct Walk {
     }
   }
 };
-// 16 elements to a lane, 1 << lanes of them to a group.
+// 16 elements to a lane, 1 << lanes of them to a group.  Bound by memory and, nearly as
+// much, by its instructions (76 % of the issue slots): 28672 x 8192 in 104 us, 5.8 TB/s.
 __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict__ W, long long pieces, int row_pieces,
                                                          int seg_pieces, int lanes, int seg_groups, int segs,
                                                          uint2* __restrict__ codes, __nv_bfloat16* __restrict__ scales) {
@@ -247,7 +247,10 @@ __device__ __forceinline__ void store4(uint8_t* to, uint32_t w, int live) {
 }
 // Widths that 16-element pieces do not fit: the scales, a thread to eight columns of a
 // group, then the codes, a thread to eight columns of a row (or, with segments of less
-// than eight, to a byte, whose two columns may belong to two segments).
+// than eight, to a byte, whose two columns may belong to two segments).  Pieces of 16
+// are the faster way (28672 x 8192: 104 us), but rows that begin at any even address and
+// groups that begin in any column do not have them.  Bound by instructions, 270 to
+// eight columns: 28672 x 8190 in 416 us (the scales 129 of it), back in 174.
 // 8 << lanes columns to a group.
 __global__ void __launch_bounds__(256) scales_kernel(const __nv_bfloat16* __restrict__ W, long long rows, long long cols,
                                                      int segs, int seg, int lanes, int seg_groups,
@@ -338,6 +341,8 @@ __device__ __forceinline__ uint32_t two_values(uint32_t c, uint32_t s) {
   asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(s));
   return v;
 }
+// Bound by memory: 28672 x 8192 in 104 us, 5.7 TB/s, two pieces to a thread on their way
+// (one: 123 us).
 __global__ void __launch_bounds__(256) dequantize16_kernel(const uint2* __restrict__ codes,
                                                            const __nv_bfloat16* __restrict__ scales, long long pieces,
                                                            int row_pieces, int seg_pieces, int lanes, int seg_groups,
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(256) prepare_few_kernel(const __grid_constant_
     store_block(p.image + block * image_bytes(p.nt), p.nt, in, lane, v);
   }
 }
-// More tokens: a block to a token, whose largest element it needs before the first
+// More tokens: a block to a token (some 4 us, most of it its start), whose largest element it needs before the first
 // is written.  The exponents of the hidden activations are bounds:
 // |a| <= sum |x| 8 max s, the largest scale of the matrix, |silu(a) g| <= |a| |g|,
 // |gelu(z)| <= |z| <= |a| + max |b1|.  A bound some 2^12 above the largest hidden value leaves it
@@ -924,7 +929,9 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
 //
 // The matrix instructions take 2.05 cycles an SM (measured), those of a chunk 262 of
 // the some 720 that its bytes take; the tensor-memory products take 768 whatever the
-// number of tokens.  (Two of them for 9 to 16 tokens: 88.5 us for the 70B feed-forward
+// number of tokens.  One token of the 70B feed-forward (368 MB)
+// takes 67 us, 5.5 TB/s; what is beyond the copy rate is the start and the end of its two
+// products and the kernel before them.  (Two instructions for 9 to 16 tokens: 88.5 us for the 70B feed-forward
 // as the other kernel, but 26 us against 19 for a block of d 768 and 16 against 14 for
 // an output projection of d 4096.)
 //
@@ -1076,6 +1083,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 //  * a warp copies, a warp issues the products.
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
+//
+// 70B feed-forward: 32 tokens 91 us, 64 tokens 102, 128 tokens 140; 389 tokens of the 8B
+// one 139 us, 0.99 PFLOP/s.  Up to 64 tokens a chunk takes some 1150 cycles, of which
+// its bytes take 720 and its products 750: the issuing warp spends 330 waiting for the
+// operands and 400 giving out 16 products, a group of operand warps 1700 on its chunk.
+// Tried:
+//  * e4m3 operands as subnormals, group sums read back and scaled in 32 bits: 32 tokens
+//    100 us, 64 tokens (two tiles) 170;
+//  * half a chunk to a step: 107 us for 32 tokens, the issuing warp waits twice as often;
+//  * two groups instead of three where there are three buffers: 95 us.
+// Operands in shared memory would be written and read once more there, some 1500 cycles
+// a chunk.
 constexpr int MOST = 128;  // tokens of a tile
 __host__ __device__ constexpr int sum_columns(int nt) { return (nt + 31) / 32 * 32; }
 constexpr int GROUP = 8, GROUPS = 3, MANY_WARPS = GROUP * GROUPS + 2, MANY_THREADS = MANY_WARPS * 32;
@@ -1418,13 +1437,7 @@ Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
   } else {
     c.tiles = static_cast<int>((n + MOST - 1) / MOST);
     c.nt = static_cast<int>(((n + c.tiles - 1) / c.tiles + 15) / 16 * 16);
-    // up to four waves of blocks, the fewest that leave little of the last empty
-    double best = 0;
-    for (int waves = 1; waves <= 4 && best < 0.92; ++waves) {
-      const int per = std::max(waves * num_sms / c.tiles, 1), all = per * c.tiles;
-      const double used = static_cast<double>(all) / ((all + num_sms - 1) / num_sms * num_sms);
-      if (used > best) best = used, c.blocks = per;
-    }
+    c.blocks = std::max(num_sms / c.tiles, 1);  // a wave: a call has four tiles at most
   }
   c.blocks = static_cast<int>(std::min<int64_t>(c.blocks, m.units() * m.chunks()));
   return c;
