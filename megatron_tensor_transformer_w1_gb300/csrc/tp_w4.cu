@@ -1097,7 +1097,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // a chunk.
 constexpr int MOST = 128;  // tokens of a tile
 __host__ __device__ constexpr int sum_columns(int nt) { return (nt + 31) / 32 * 32; }
-constexpr int GROUP = 8, GROUPS = 3, MANY_WARPS = GROUP * GROUPS + 2, MANY_THREADS = MANY_WARPS * 32;
+constexpr int GROUP = 8, GROUPS = 3, MANY_WARPS = GROUP * GROUPS + 3, COPIER = GROUP * GROUPS, ISSUERS = COPIER + 1, MANY_THREADS = MANY_WARPS * 32;
 constexpr int MANY_STAGES = 8, MANY_BUFS = 3, MANY_SMEM = 224 * 1024 + 1024;
 static_assert(MANY_SMEM + 2 * 128 * 4 + 512 <= 232448, "shared memory per block");
 
@@ -1153,23 +1153,24 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // of a chunk: copied, its products done; of a buffer of operands: written; of the sums: read
-  __shared__ uint64_t full[MANY_STAGES], done[MANY_STAGES], a_full[MANY_BUFS], d_free, drain;
+  __shared__ uint64_t full[MANY_STAGES], done[MANY_STAGES], a_full[2][MANY_BUFS], d_free, drain[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MANY_STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&done[i], 1);
+      mbar_init(&done[i], 2);
     }
-    for (int i = 0; i < MANY_BUFS; ++i) mbar_init(&a_full[i], GROUP);
+    for (int i = 0; i < 2 * MANY_BUFS; ++i) mbar_init(&a_full[0][i], GROUP / 2);
     mbar_init(&d_free, GROUP);
-    mbar_init(&drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == MANY_WARPS - 1) tmem_alloc(&tmem_slot, 512);
+  if (warp == COPIER) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1182,12 +1183,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   const Run run(p);
   const int x_bytes = p.nt * 256;
 
-  if (warp == MANY_WARPS - 2) {
+  if (warp == COPIER) {
     if (lane == 0) copy_chunks(p, run, Ring{p.stages, x_bytes, p.stage_bytes}, smem, full, done, W);
     __syncwarp();
-  } else if (warp == MANY_WARPS - 1) {
+  } else if (warp >= ISSUERS) {
+    const int tile = warp - ISSUERS;
     // ------------------------------------------------ products
-    // The warp stays together and one lane waits and issues: what a product is told is
+    // A warp to a tile (one for both: 91 us for 32 tokens of the 70B feed-forward).  It
+    // stays together and one lane waits and issues: what a product is told is
     // the same for all lanes, else it takes three times as long to issue.
     const bool leader = elect_one();
     const uint32_t id = (1u << 4) | (static_cast<uint32_t>(p.nt >> 3) << 17) | (8u << 24);  // fp16 x fp16 -> fp32, M = 128
@@ -1200,19 +1203,16 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
       const uint64_t xd = x_desc + static_cast<uint64_t>(stage * (p.stage_bytes >> 4));
       if (leader) {
         if (fresh) W(&d_free, d_phase);
-        W(&a_full[buf], a_phase);  // (the tokens have landed, else there were no operands)
+        W(&a_full[tile][buf], a_phase);  // (the tokens have landed, else there were no operands)
       }
       __syncwarp();
       tc_fence_after();
       if (leader) {
-        const uint32_t at = a_tmem + buf * 128;
+        const uint32_t at = a_tmem + buf * 128 + tile * 64;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t xk = xd + static_cast<uint64_t>((k >> 2) * (p.nt * 128 >> 4) + ((k & 3) * 32 >> 4));
-#pragma unroll
-          for (int tile = 0; tile < 2; ++tile)
-            umma_f16_ta(tile * d_cols, at + tile * 64 + k * 8, xk, id, k > 0 || !fresh);
-        }
+        for (int k = 0; k < 8; ++k)
+          umma_f16_ta(tile * d_cols, at + k * 8, xd + static_cast<uint64_t>((k >> 2) * (p.nt * 128 >> 4) + ((k & 3) * 32 >> 4)), id,
+                      k > 0 || !fresh);
         umma_commit(&done[stage]);
       }
       __syncwarp();
@@ -1226,8 +1226,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
       if (++stage == p.stages) stage = 0;
     }
     if (leader) {
-      umma_commit(&drain);
-      W.drain(&drain, 0);
+      umma_commit(&drain[tile]);
+      W.drain(&drain[tile], 0);
     }
     __syncwarp();
   } else {
@@ -1283,7 +1283,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&a_full[buf]);
+      if (lane == 0) mbar_arrive(&a_full[tile][buf]);
       if (chunk + 1 == p.chunks || i + 1 == run.count) {
         // a segment's last chunk: the sums back, a row of one tile to a thread
         W.warp_long(&done[stage], phase);  // its products are done, so all are
@@ -1332,7 +1332,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == MANY_WARPS - 1) {
+  if (warp == COPIER) {
     tc_fence_after();
     tmem_dealloc(tmem_slot, 512);
   }
