@@ -274,7 +274,7 @@ struct W4Shape {
   __host__ __device__ int64_t cols() const { return segs * seg; }
   __host__ __device__ int block_bytes() const { return 16384 + 512 * (128 / group); }
   // Behind the blocks: for every row of the units a power of two (float) that brings
-  // the row's largest scale to 2^11..2^12, and the largest |scale| of the first matrix and
+  // the row's largest scale to 2^11..2^12 (a number with an inverse for every scale), and the largest |scale| of the first matrix and
   // (W4_GATED) of the second, as the bits of a float.
   __host__ __device__ int64_t block_end() const { return units() * chunks() * block_bytes(); }
   __host__ __device__ float* row_up(void* packed) const {

@@ -1070,25 +1070,23 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // and 65 for N = 128 (measured).
 //
 // The weights are scaled before the products, so that a product's sums run on over
-// all columns and are read back once a segment: (code - 8) s 2^k in fp16, where 2^k brings the row's
-// largest scale to 2^11..2^12.  (code - 8) s has at most 11 significant bits, as many as fp16
-// keeps: the weights are exact where s is at least 2^-28 of the row's largest, smaller ones
-// are rounded to 2^-36 of it.  One block per SM, a step being 64 columns:
-//  * up to three groups of eight warps, each for every second or third chunk, a row of tile 0 or 1 to
-//    a thread, make the row's operands, and bring a segment's sums out behind its last
-//    chunk.  What a group does for a chunk takes some 2400 cycles, most of them waiting
-//    (for the chunk, for a free buffer, for the operands to be written), which is why there
-//    are three; the writes of the warps on the issuing warp's scheduler moreover wait
-//    behind the products that were issued before.
-//  * a warp copies, a warp issues the products.
+// all columns and are read back once a segment: (code - 8) s in fp16, the row's largest
+// scale brought to 2^-5..2^-4.  It has at most 11 significant bits, as many as fp16 keeps:
+// the weights are exact where s is at least 2^-12 of the row's largest, smaller ones are
+// rounded to 2^-19 of it.  One block per SM:
+//  * up to three groups of eight warps, each for every second or third chunk, a row of
+//    tile 0 or 1 to a thread, make the row's operands, and bring a segment's sums out
+//    behind its last chunk.  A group takes some 2200 cycles to a chunk: 330 instructions a
+//    warp, the six warps of a scheduler in turn, which is what the time goes by.  The
+//    writes of the warps on an issuing warp's scheduler moreover wait behind the
+//    products that were issued before.
+//  * a warp copies, two warps issue the products, one a tile's.
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
 //
-// 70B feed-forward: 32 tokens 91 us, 64 tokens 102, 128 tokens 140; 389 tokens of the 8B
-// one 139 us, 0.99 PFLOP/s.  Up to 64 tokens a chunk takes some 1150 cycles, of which
-// its bytes take 720 and its products 750: the issuing warp spends 330 waiting for the
-// operands and 400 giving out 16 products, a group of operand warps 1700 on its chunk.
-// Tried:
+// 70B feed-forward: 32 tokens 82 us, 64 tokens 96, 128 tokens 137; 389 tokens of the 8B
+// one 131 us, 1.04 PFLOP/s.  Up to 64 tokens a chunk takes some 1000 cycles, of which
+// its bytes take 720 and its products 750.  Tried:
 //  * e4m3 operands as subnormals, group sums read back and scaled in 32 bits: 32 tokens
 //    100 us, 64 tokens (two tiles) 170;
 //  * half a chunk to a step: 107 us for 32 tokens, the issuing warp waits twice as often;
@@ -1138,16 +1136,15 @@ __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// (code - 8) * s for the codes of two columns at bits 0-3 and 16-19 (HIGH: 4-7 and
-// 20-23): 1024 + code, or 64 + code, as fp16, less 1032 or 72, times s.
-template <bool HIGH>
-__device__ __forceinline__ uint32_t weights_of(uint32_t w, uint32_t s) {
-  uint32_t v;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(HIGH ? 0x00f000f0u : 0x000f000fu), "r"(HIGH ? 0x54005400u : 0x64006400u));
-  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(HIGH ? 0x54805480u : 0x64086408u));
-  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(s));
+// (code - 8) * s for the codes of two columns at bits 4-7 and 20-23, which are code * 2^-20
+// as fp16 subnormals, with m = s 2^20 and c = -8 s.  (Codes made into numbers of ordinary
+// size, less 8, times s: two instructions for this one, 87 us for 82.)
+__device__ __forceinline__ uint32_t weights_of(uint32_t w, uint32_t m, uint32_t c) {
+  uint32_t v = w & 0x00f000f0u;
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(m), "r"(c));
   return v;
 }
+
 template <int SUBS>
 __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -1256,23 +1253,24 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
       uint4 v[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) v[t] = ld_shared_v4(st + at_w + ((t ^ swz) << 4));
-      uint32_t s[SUBS];
+      uint32_t m[SUBS], c[SUBS];
 #pragma unroll
       for (int j = 0; j < SUBS; ++j) {
-        const float scale = ld_shared_scale(st + at_s + j * 512) * up;
-        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(s[j]) : "f"(scale));
+        const float s = ld_shared_scale(st + at_s + j * 512) * up;
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(m[j]) : "f"(s * 16.f));
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(c[j]) : "f"(s * -1.220703125e-4f));
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // 32 columns
         uint32_t o[16];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const uint32_t w = q == 0 ? v[t].x : q == 1 ? v[t].y : q == 2 ? v[t].z : v[t].w, w8 = w >> 8;
-          const uint32_t sq = s[q * SUBS / 4];
-          o[4 * t] = weights_of<false>(w, sq);
-          o[4 * t + 1] = weights_of<true>(w, sq);
-          o[4 * t + 2] = weights_of<false>(w8, sq);
-          o[4 * t + 3] = weights_of<true>(w8, sq);
+          const uint32_t w = q == 0 ? v[t].x : q == 1 ? v[t].y : q == 2 ? v[t].z : v[t].w;
+          const uint32_t mq = m[q * SUBS / 4], cq = c[q * SUBS / 4];
+          o[4 * t] = weights_of(w << 4, mq, cq);
+          o[4 * t + 1] = weights_of(w, mq, cq);
+          o[4 * t + 2] = weights_of(w >> 4, mq, cq);
+          o[4 * t + 3] = weights_of(w >> 8, mq, cq);
         }
         if (q == 0) {
           if (i >= p.bufs) W.warp(&done[before], before_phase);
@@ -1356,7 +1354,7 @@ __global__ void __launch_bounds__(FINISH_TOKENS * 32) finish_kernel(const __grid
                up1 = *reinterpret_cast<const float4*>(p.row_up + unit * 256 + 128 + q4);
   grid_dep_wait();
   if (token >= p.n) return;
-  const float down = pow2(max(p.e_in[token], p.e_in[p.padded]) - 15);
+  const int down = -min(max(15 - max(p.e_in[token], p.e_in[p.padded]), -126), 126);  // as pow2 has it
   const float up = p.e_out ? pow2(15 - max(p.e_out[token], p.e_out[p.padded])) : 1.f;
   float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
 #pragma unroll 4
@@ -1364,8 +1362,12 @@ __global__ void __launch_bounds__(FINISH_TOKENS * 32) finish_kernel(const __grid
     v0 = add4(v0, __ldcg(reinterpret_cast<const float4*>(from)));
     v1 = add4(v1, __ldcg(reinterpret_cast<const float4*>(from + 128)));
   }
-  auto scaled = [&](float4 v, float4 u) {  // by 2^-k of the rows and the token's
-    auto one = [&](float x, float k) { return x * __uint_as_float(0x7f000000u - __float_as_uint(k)) * down; };
+  auto scaled = [&](float4 v, float4 u) {  // by 2^(16 + down) over the row's factor
+    auto one = [&](float x, float f) {
+      const int e = down + 16 + 127 - static_cast<int>(__float_as_uint(f) >> 23);
+      if (e >= -126 && e <= 127) return x * __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      return x * pow2(e / 2) * pow2(e - e / 2);  // (a tiny token and a huge row, or the other way round)
+    };
     return make_float4(one(v.x, u.x), one(v.y, u.y), one(v.z, u.z), one(v.w, u.w));
   };
   v0 = scaled(v0, up0);

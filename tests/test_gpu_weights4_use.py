@@ -43,6 +43,19 @@ def test_scales_of_a_row_far_apart(act, d, d_ff, T, n):
     _check(ffn.forward4(x, up, down), *ref.forward(x, act, _matrices(codes, 32), None, None))
 
 
+@pytest.mark.parametrize("n", [5, 40])
+def test_the_largest_and_smallest_scales(n):
+    """Rows whose scales are all as large or as small as a bf16 weight's can be."""
+    ffn, codes = _ffn("none", 256, 512, 2), _weights("none", 256, 512, 2, 64, 30)
+    sizes = torch.tensor([2.0 ** 125, 2.0 ** 120, 2.0 ** -126, 2.0 ** -60], device="cuda").repeat(64)
+    g = _gen(33)
+    codes[0].scales.copy_((0.5 + 0.5 * torch.rand(codes[0].scales.shape, generator=g, device="cuda")) * sizes[:, None])
+    x = (torch.randn(n, 512, generator=g, device="cuda") * 2.0 ** -30).to(BF)
+    want, tol = ref.forward(x, "none", _matrices(codes, 64), None, None)
+    # what is below 2^-126 may be lost, a product's and the result's
+    _check(ffn.forward4(x, *_pack(ffn, codes)), want, tol + 2.0 ** -116)
+
+
 @pytest.mark.parametrize("act,d,d_ff,T,n", [("swiglu", 256, 384, 2, 513), ("gelu_tanh", 264, 640, 4, 1030), ("none", 128, 512, 2, 1537)])
 def test_many_tokens(act, d, d_ff, T, n):
     """More tokens than go through the products at once."""
