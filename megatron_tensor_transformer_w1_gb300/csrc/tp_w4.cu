@@ -1450,7 +1450,7 @@ int64_t image_end(const W4Shape& m, const Cut& c) { return m.chunks() * c.tiles 
 int64_t hidden_chunks(const W4Shape& m) { return m.T * m.sp / 128; }
 // A grid of at most 32 blocks per SM.
 unsigned grid_of(long long blocks) { return static_cast<unsigned>(std::min<long long>(std::max<long long>(blocks, 1), 32 * 152)); }
-int launched() { return cudaPeekAtLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA; }
+int launched() { return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA; }  // (an error is not left for the next call)
 
 }  // namespace w4
 

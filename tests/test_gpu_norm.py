@@ -273,3 +273,10 @@ def test_empty():
     assert r.shape == out.shape == (0, 64)
     g = norm.backward(e, r, stats, e, e, w_after=w, w_before=w)
     assert (g["dw_after"] == 0).all() and (g["dw_before"] == 0).all()
+
+
+@pytest.mark.parametrize("kind,dtype,d", [("layer", "bf16", 3000), ("rms", "bf16", 1400), ("layer", "f32", 1504), ("rms", "f32", 3000)])
+def test_slots_of_48_kib(monkeypatch, kind, dtype, d):
+    """Rows whose slots take all of the shared memory that a kernel may have unasked."""
+    monkeypatch.setitem(globals(), "CASES", [(n, d, gates) for n, gates in ((451, 451), (800, 1), (200, 0))])
+    test_norm(kind, True, True, kind == "layer", dtype)
