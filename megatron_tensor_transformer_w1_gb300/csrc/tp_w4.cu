@@ -1084,13 +1084,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
 //
-// 70B feed-forward: 32 tokens 82 us, 64 tokens 96, 128 tokens 137; 389 tokens of the 8B
-// one 131 us, 1.04 PFLOP/s.  Up to 64 tokens a chunk takes some 1000 cycles, of which
+// 70B feed-forward: 32 tokens 81 us, 64 tokens 95, 128 tokens 136; 389 tokens of the 8B
+// one 133 us, 1.03 PFLOP/s.  Up to 64 tokens a chunk takes some 1000 cycles, of which
 // its bytes take 720 and its products 750.  Tried:
 //  * e4m3 operands as subnormals, group sums read back and scaled in 32 bits: 32 tokens
 //    100 us, 64 tokens (two tiles) 170;
-//  * half a chunk to a step: 107 us for 32 tokens, the issuing warp waits twice as often;
-//  * two groups instead of three where there are three buffers: 95 us.
+//  * half a chunk to a step: 107 us (for 97), an issuing warp waits twice as often;
+//  * two groups instead of three where there are three buffers: 95 us (for 91).
 // Operands in shared memory would be written and read once more there, some 1500 cycles
 // a chunk.
 constexpr int MOST = 128;  // tokens of a tile
@@ -1347,8 +1347,12 @@ __global__ void __launch_bounds__(FINISH_TOKENS * 32) finish_kernel(const __grid
   const int unit = blockIdx.x, tile = blockIdx.z, in_tile = blockIdx.y * FINISH_TOKENS + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, q4 = lane * 4;
   const long long token = static_cast<long long>(tile) * p.nt + in_tile;
-  const long long u0 = static_cast<long long>(unit) * p.chunks, u1 = u0 + p.chunks - 1;
-  const int c0 = static_cast<int>(((u0 + 1) * p.blocks - 1) / p.total), c1 = static_cast<int>(((u1 + 1) * p.blocks - 1) / p.total);
+  auto block_of = [&](long long chunk) {  // (a division of 64 bits takes as long as the rest)
+    const long long a = (chunk + 1) * p.blocks - 1;
+    return a >> 32 ? static_cast<int>(a / p.total) : static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(p.total));
+  };
+  const long long u0 = static_cast<long long>(unit) * p.chunks;
+  const int c0 = block_of(u0), c1 = block_of(u0 + p.chunks - 1);
   const float* from = p.parts + ((static_cast<long long>(tile) * (p.blocks + p.units - 1) + c0 + unit) * p.nt + in_tile) * 256 + q4;
   const float4 up0 = *reinterpret_cast<const float4*>(p.row_up + unit * 256 + q4),
                up1 = *reinterpret_cast<const float4*>(p.row_up + unit * 256 + 128 + q4);
