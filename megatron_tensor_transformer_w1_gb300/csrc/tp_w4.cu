@@ -750,11 +750,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
 __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -1097,7 +1092,7 @@ constexpr int MOST = 128;  // tokens of a tile
 __host__ __device__ constexpr int sum_columns(int nt) { return (nt + 31) / 32 * 32; }
 constexpr int GROUP = 8, GROUPS = 3, MANY_WARPS = GROUP * GROUPS + 3, COPIER = GROUP * GROUPS, ISSUERS = COPIER + 1, MANY_THREADS = MANY_WARPS * 32;
 constexpr int MANY_STAGES = 8, MANY_BUFS = 3, MANY_SMEM = 224 * 1024 + 1024;
-static_assert(MANY_SMEM + 2 * 128 * 4 + 512 <= 232448, "shared memory per block");
+static_assert(MANY_SMEM + 1024 <= 232448, "shared memory per block, what the kernel declares itself counted in");
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -1234,9 +1229,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) product_kernel(const __grid_c
     const int tile = (warp >> 2) & 1, group = warp / GROUP;
     const uint32_t at_w = x_bytes + tile * 8192 + r * 64, swz = (r >> 1) & 3;
     const uint32_t at_s = x_bytes + 16384 + (tile * 128 + r) * 2;
-    // Chunk i goes to buffer i mod bufs, whose products before are chunk i - bufs's.  As
-    // many groups as buffers at most: a group that comes to chunk i knows chunk i -
-    // groups - bufs done, so that no wait here is two phases behind.
+    // Chunk i goes to buffer i mod bufs, whose products before are chunk i - bufs's.  A
+    // group that comes to chunk i knows chunk i - groups - bufs done.  So no wait here
+    // may pass for a phase two before the one it means: there are as many groups as
+    // buffers at most, and stages for both together (see launch_w4_product).
     const int groups = p.bufs < GROUPS ? p.bufs : GROUPS;
     int stage = group, buf = group, before = group - p.bufs;  // of chunk i - bufs
     uint32_t phase = 0, before_phase = 0;
@@ -1608,8 +1604,10 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
   } else {
     p.nt = c.nt;
     p.stage_bytes = image_bytes(c.nt) + (p.block_bytes + 1023) / 1024 * 1024;
+    // bufs + groups <= stages: 3 + 3 of at least 6 up to 64 tokens, 2 + 2 of at least 4 above
     p.stages = std::min((MANY_SMEM - 1024) / p.stage_bytes, MANY_STAGES);
-    p.bufs = (512 - 2 * sum_columns(c.nt)) / 128;
+    p.bufs = std::min((512 - 2 * sum_columns(c.nt)) / 128, MANY_BUFS);
+    if (p.stages < p.bufs + std::min(p.bufs, GROUPS)) return TP_ERR_INVALID;
     p.row_up = a.m.row_up(const_cast<void*>(a.packed));
     p.padded = c.tiles * c.nt;
     p.e_in = reinterpret_cast<const int*>(p.image + image_end(a.m, c));
