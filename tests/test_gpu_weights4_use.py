@@ -254,3 +254,45 @@ def test_a_blocks_decode_step():
     torch.cuda.synchronize()
     for got, want in zip(captured, step()):
         assert torch.equal(got, want)
+
+
+def test_decode_of_more_tokens_than_go_through_at_once():
+    """Prompts of 650 tokens beside the bf16 pass from the same weights (scales that are powers of two), and rows
+    behind the last sequence, whose numbers reach nobody."""
+    from megatron_tensor_transformer_w1_gb300.attention import TensorParallelAttention
+    from megatron_tensor_transformer_w1_gb300.kv_cache import PagedKVCache
+    w4 = _lib()
+    d, H, Hkv, T, group = 264, 4, 2, 2, 32
+    attn = TensorParallelAttention(d, H, Hkv, 128, T)
+    g = _gen(41)
+    codes = [w4.Codes4(*ref.random_codes(r, c, s, group, g, True), c, group, s) for r, c, s in attn._shapes4()]
+    plain, packed = attn.pack(*[w4.dequantize4(c) for c in codes]), attn.pack4(*codes)
+    new, ctx, page = [300, 1, 349], [0, 70, 33], 16
+    n, spare = sum(new), 5
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 300, 301, 650], **i32)
+    kv_len = torch.tensor([a + b for a, b in zip(new, ctx)], **i32)
+    table = torch.arange(3 * 24, **i32).view(3, 24)
+    k, v = (torch.randn(72, Hkv, page, 128, generator=g, device="cuda").to(BF) for _ in range(2))
+    x = torch.randn(n + spare, d, generator=g, device="cuda").to(BF)
+    got = []
+    for weights in (plain, packed):
+        cache = PagedKVCache(attn, 72, page, k=k.clone(), v=v.clone(), inv_freq=torch.rand(64, generator=_gen(0), device="cuda"))
+        for last in (0.0, float("nan")):
+            x[n:] = last
+            y = attn.decode(x, cache, cache.batch(cu, kv_len, table, n + spare, 349), *weights)[:n]
+            assert cache.last_device_error() == 0
+            got.append(y.double())
+    assert torch.equal(got[0], got[1]) and torch.equal(got[2], got[3])
+    rel = ((got[2] - got[0]).square().mean() / got[0].square().mean()).sqrt().item()
+    assert rel <= 2 * U, rel
+
+
+def test_kernel_times_name_the_launches():
+    abi = _abi()
+    ffn, codes = _ffn("swiglu", 256, 384, 2), _weights("swiglu", 256, 384, 2, 64, 42)
+    up, down = _pack(ffn, codes)
+    for n, names in ((3, ["prepare4", "up_swiglu4", "down4"]), (20, ["prepare4", "up_swiglu4", "finish4", "down4", "finish4"])):
+        x = torch.randn(n, 256, generator=_gen(n), device="cuda").to(BF)
+        ffn.forward4(x, up, down, flags=abi.TP_FLAG_TIMING | abi.TP_FLAG_SYNC)
+        assert [name for name, _ in abi.tp_ffn_kernel_times(ffn.plan)] == names
