@@ -924,8 +924,8 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
 //
 // The matrix instructions take 2.05 cycles an SM (measured), those of a chunk 262 of
 // the some 720 that its bytes take; the tensor-memory products take 768 whatever the
-// number of tokens.  One token of the 70B feed-forward (368 MB)
-// takes 67 us, 5.5 TB/s; what is beyond the copy rate is the start and the end of its two
+// number of tokens.  One token of the 70B feed-forward (363 MB)
+// takes 67 us, 5.4 TB/s; what is beyond the copy rate is the start and the end of its two
 // products and the kernel before them.  (Two instructions for 9 to 16 tokens: 88.5 us for the 70B feed-forward
 // as the other kernel, but 26 us against 19 for a block of d 768 and 16 against 14 for
 // an output projection of d 4096.)
