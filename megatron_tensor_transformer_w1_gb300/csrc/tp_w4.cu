@@ -512,18 +512,15 @@ using namespace tc;
 // A block of tokens as the kernels keep it ("image"), for NT tokens: fp16 [2][NT][64],
 // 64 columns each, in rows of 128 bytes whose 16-byte pieces are swizzled by the token
 // (piece i at i ^ (token & 7)).
-//  * Few tokens: every token's 128 columns have their own power of two, columns 2, 3,
-//    6, 7 of each eight are times 2^-4 besides, and behind them lies float [8][NT]: -8 times
-//    the sums of the four 32-column parts, the two halves and the whole, in units of
-//    a code's 2^-24, and the power of two that undoes the block's and is in the sums
-//    already.  A block's largest element comes to 2^14..2^15, so that bf16's eight
-//    bits are kept down to 2^-25 of it and what is smaller is rounded to 2^-40 of it.
+//  * Few tokens: every token's 128 columns have their own power of two, and behind
+//    them lies float [NT], the powers that undo it.  A block's largest element comes to
+//    2^14..2^15, so that bf16's eight bits are kept down to 2^-31 of it and what is
+//    smaller is rounded to 2^-39 of it.
 //  * More: the power of two is the token's, for all columns.  Behind the images of
 //    all tokens lies int [tokens + 1], the exponents e: |x| < 2^e, kept as x 2^(15 - e), and
 //    last the least that any of them counts for.
 constexpr int FEW = 8;  // tokens
-__host__ __device__ constexpr int image_bytes(int nt) { return nt <= FEW ? nt * 288 : nt * 256; }
-constexpr int SUM_OF = 0, SUM_OF_HALF = 4, SUM_OF_ALL = 6, DOWN = 7;
+__host__ __device__ constexpr int image_bytes(int nt) { return nt * 256 + (nt <= FEW ? 128 : 0); }  // (copied to multiples of 128)
 constexpr int LEAST = -1000;  // an exponent below all
 
 struct ProductParams {
@@ -557,20 +554,10 @@ __device__ __forceinline__ void store_block(uint8_t* image, int nt, int token, i
   const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
   const int e = min(141 - static_cast<int>(min(most >> 23, 254u)), 126);  // most * 2^e in 2^14..2^15
   const float up = pow2(e), down = pow2(-e);
-  const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up * 0.0625f, v[3] * up * 0.0625f);
-  const float2 a = __half22float2(lo), b = __half22float2(hi);
-  float sum = (a.x + a.y) + 16.f * (b.x + b.y);
+  const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up), hi = __floats2half2_rn(v[2] * up, v[3] * up);
   uint8_t* at = image + (lane >> 4) * (nt * 128) + token * 128 + ((((lane & 15) >> 1) ^ (token & 7)) << 4) + (lane & 1) * 8;
   *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  sum *= -4.76837158203125e-7f * down;  // -8 * 2^-24
-  const float two = sum + __shfl_xor_sync(0xffffffffu, sum, 8), all = two + __shfl_xor_sync(0xffffffffu, two, 16);
-  float* tail = reinterpret_cast<float*>(image + nt * 256) + token;
-  if ((lane & 7) == 0) tail[(SUM_OF + (lane >> 3)) * nt] = sum;
-  if ((lane & 15) == 0) tail[(SUM_OF_HALF + (lane >> 4)) * nt] = two;
-  if (lane == 0) tail[SUM_OF_ALL * nt] = all;
-  if (lane == 0) tail[DOWN * nt] = down;
+  if (lane == 0) reinterpret_cast<float*>(image + nt * 256)[token] = down;
 }
 
 struct PrepareParams {
@@ -764,9 +751,19 @@ __device__ __forceinline__ float ld_shared_scale(uint32_t addr) {  // a bf16
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// The codes at bits 0-3 and 16-19 as two fp16 numbers, and those at bits 4-7 and 20-23.
-__device__ __forceinline__ uint32_t low(uint32_t w) { return w & 0x000f000fu; }
-__device__ __forceinline__ uint32_t high(uint32_t w) { return w & 0x00f000f0u; }
+// (code - 8) 2^-14 for the codes at bits 0-3 and 16-19, which are code * 2^-24 as fp16 subnormals,
+// and for those at bits 4-7 and 20-23, code * 2^-20: times 2^10 or 2^6, less 2^-11.  Exact
+// and no subnormals (but 0); with larger ones, sums times a token's largest power overflow.
+__device__ __forceinline__ uint32_t low(uint32_t w) {
+  uint32_t v = w & 0x000f000fu;
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(0x64006400u), "r"(0x90009000u));
+  return v;
+}
+__device__ __forceinline__ uint32_t high(uint32_t w) {
+  uint32_t v = w & 0x00f000f0u;
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(0x54005400u), "r"(0x90009000u));
+  return v;
+}
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
 // The run of chunks of a block.
@@ -895,7 +892,7 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
     }
   }
   if (store && *W.abort_flag == 0) {
-    const float one = 16777216.f;  // 2^24: a code's unit
+    const float one = 16384.f;  // 2^14: a code's unit
     v0 = make_float4(v0.x * one, v0.y * one, v0.z * one, v0.w * one);
     v1 = make_float4(v1.x * one, v1.y * one, v1.z * one, v1.w * one);
     if (p.epi == W4_SWIGLU) {  // tile 1 has the second matrix's rows of the same hidden slots
@@ -917,15 +914,19 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
 // registers.  What is left to count are the instructions that make operands of
 // codes.  A code in the low bits of an fp16 number is a subnormal, code * 2^-24, and four
 // bits higher code * 2^-20: a word's eight codes are four operand registers after one
-// shift and four masks.  (Codes made into bf16 take 11 instructions a word: 102 us
-// instead of 68 for one token of the 70B feed-forward.)  The codes' offset of 8 is
-// taken off as the block's sum, -8 times the sum of the group's 32, 64 or 128
-// columns: product * down + sum, in 32 bits, times the row's scale.
+// shift, four masks and four multiply-adds, which take the offset of 8 off.  (Codes made into
+// bf16 take 11 instructions a word: 102 us for one token of the 70B feed-forward, for 72.
+// The codes as they lie and the offset taken off as -8 times the columns' sum: 68 us, but
+// an infinity less an infinity, and sums short by some 2^-17 of 8 times the block's
+// largest element, as the unit aligns products by exponents that a subnormal does not
+// fill: an element 2^12 above the others left them an error of 2^-9.  The codes
+// shifted to the top of the mantissa, with that sum: 73 to 76 us and still short.)
+// Sums are products times the block's power of two and the row's scale, in 32 bits.
 //
 // The matrix instructions take 2.05 cycles an SM (measured), those of a chunk 262 of
 // the some 720 that its bytes take; the tensor-memory products take 768 whatever the
 // number of tokens.  One token of the 70B feed-forward (363 MB)
-// takes 67 us, 5.4 TB/s; what is beyond the copy rate is the start and the end of its two
+// takes 72 us, 5.0 TB/s; what is beyond the copy rate is the start and the end of its two
 // products and the kernel before them.  (Two instructions for 9 to 16 tokens: 88.5 us for the 70B feed-forward
 // as the other kernel, but 26 us against 19 for a block of d 768 and 16 against 14 for
 // an output projection of d 4096.)
@@ -984,7 +985,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
   // bytes from a stage's start
   const uint32_t at_x = tok0 * 128, swz = tok0 & 7;
   const uint32_t at_w = F::X_BYTES + row0 * 64 + ((t ^ ((i8 >> 1) & 3)) << 4), at_s = F::X_BYTES + 16384 + row0 * 2;
-  const uint32_t at_tail = FEW * 256 + t * 4;  // of token t
+  const uint32_t at_down = FEW * 256 + t * 4;  // of token t
   float* sum = reinterpret_cast<float*>(smem + F::M_SUM);
   uint64_t acc[2][2] = {};  // rows row0 + 16 m + 8 h, tokens t and t + 4
   grid_dep_wait();  // the counters are clear, and nobody reads the outputs or parts of before
@@ -1001,19 +1002,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) w[m][h] = ld_shared_v4(st + at_w + m * 1024 + h * 512);
-    auto two = [&](int what) {  // of tokens t and t + 4
-      const uint32_t at = st + at_tail + what * FEW * 4;
-      return pack2(ld_shared_f(at), ld_shared_f(at + 16));
-    };
-    const uint64_t down = two(DOWN);
-    uint64_t sums = 0;
+    const uint64_t down = pack2(ld_shared_f(st + at_down), ld_shared_f(st + at_down + 16));  // of tokens t and t + 4
     float c[2][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       constexpr int PER = 4 / SUBS;
       if (q % PER == 0) {
-        constexpr int FIRST = SUBS == 1 ? SUM_OF_ALL : SUBS == 2 ? SUM_OF_HALF : SUM_OF;
-        sums = two(FIRST + q / PER);
 #pragma unroll
         for (int m = 0; m < 2; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
       }
@@ -1031,7 +1025,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float s = ld_shared_scale(st + at_s + (q / PER) * 512 + (16 * m + 8 * h) * 2);
-          acc[m][h] = fma2(pack2(s, s), fma2(pack2(c[m][2 * h], c[m][2 * h + 1]), down, sums), acc[m][h]);
+          acc[m][h] = fma2(pack2(s, s), mul2(pack2(c[m][2 * h], c[m][2 * h + 1]), down), acc[m][h]);
         }
     }
     __syncwarp();
