@@ -521,11 +521,11 @@ TPFFN_API int tp_ffn_unshard_rows4(const tp_ffn_plan* plan, int group, const voi
  * the order t = 0..T_p-1; results do not change from run to run (those of a token
  * may in their last bit with the number of tokens beside it).  Products are summed
  * in 32 bits; neither the scaled weights nor the hidden activations are rounded to
- * bf16: weights are exact down to scales 2^-12 of their row's largest and off by
- * 2^-19 of that scale below, hidden activations are kept to 11 bits, and to 2^-40 of
- * a bound of their token below (sum |x| times the largest weight there can be).  A token with an infinity or a NaN, in x
- * or among its hidden activations, gets those, as does a row of W2 with such a scale;
- * the others are as without it.
+ * bf16.  Weights are exact; with more than 8 tokens down to scales 2^-12 of their row's
+ * largest, and off by 2^-19 of that scale below.  x is kept to 2^-39 of its token's
+ * largest element, hidden activations to 11 bits and to 2^-39 of their token's largest.
+ * A token with an infinity or a NaN, in x or among its hidden activations, gets
+ * infinities or NaN, as does a row of W2 with such a scale; the others are as without it.
  * More than 512 tokens go through it in equal parts of at most 512, and the
  * workspace is that of one part.
  * flags: TP_FLAG_SYNC, TP_FLAG_TIMING; the TP_SUM_* choices make no difference.

@@ -1591,13 +1591,13 @@ struct Need4 {
   size_t parts = 0, image = 0;
   int64_t counters = 0;
 };
-Need4 need4(const W4Shape& m, int64_t n) {
+Need4 need4(const W4Shape& m, int64_t n, bool hidden = false) {
   Need4 r;
   const int64_t per = part4(n), last = per ? (n - 1) % per + 1 : 0;
   for (const int64_t k : {per, last}) {
     if (k == 0) continue;
     r.parts = std::max(r.parts, w4_product_scratch(m, k, num_sms_current()));
-    r.image = std::max(r.image, w4_image_bytes(m, k));
+    r.image = std::max(r.image, w4_image_bytes(m, k, hidden));
     r.counters = std::max(r.counters, w4_product_counters(m, k));
   }
   return r;
@@ -1612,7 +1612,7 @@ struct Ws4 {
 Ws4 ws4_layout(const tp_ffn_plan* p, int64_t n) {
   Ws4 L;
   const bool none = p->act == TP_ACT_NONE;
-  const Need4 down = need4(w4_down(p, 128), n), up = none ? Need4() : need4(w4_up(p, 128), n);
+  const Need4 down = need4(w4_down(p, 128), n, !none), up = none ? Need4() : need4(w4_up(p, 128), n);
   L.n_up = up.counters;
   L.n_down = down.counters;
   L.counters = kAlign;

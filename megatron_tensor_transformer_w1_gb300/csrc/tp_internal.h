@@ -274,14 +274,11 @@ struct W4Shape {
   __host__ __device__ int64_t cols() const { return segs * seg; }
   __host__ __device__ int block_bytes() const { return 16384 + 512 * (128 / group); }
   // Behind the blocks: for every row of the units a power of two (float) that brings
-  // the row's largest scale to 2^11..2^12 (a number with an inverse for every scale), and the largest |scale| of the first matrix and
-  // (W4_GATED) of the second, as the bits of a float.
+  // the row's largest scale to 2^11..2^12 (a number with an inverse for every scale).
+  // The last 16 bytes are not used.
   __host__ __device__ int64_t block_end() const { return units() * chunks() * block_bytes(); }
   __host__ __device__ float* row_up(void* packed) const {
     return reinterpret_cast<float*>(static_cast<char*>(packed) + block_end());
-  }
-  __host__ __device__ uint32_t* tops(void* packed) const {
-    return reinterpret_cast<uint32_t*>(static_cast<char*>(packed) + block_end() + units() * 1024);
   }
   __host__ __device__ int64_t bytes() const { return block_end() + units() * 1024 + 16; }
 };
@@ -340,13 +337,13 @@ struct W4Product {
   int64_t out_rs = 0;
   // x is read as blocks, which launch_w4_prepare makes of it or an up product has
   // left in its image_out.
-  void *image = nullptr, *image_out = nullptr;  // w4_image_bytes
+  void *image = nullptr, *image_out = nullptr;  // w4_image_bytes; `hidden` for an image_out
   void* scratch = nullptr;       // w4_product_scratch bytes
   int* counters = nullptr;       // w4_product_counters words, 0 before the launch
 };
 size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms);
 int64_t w4_product_counters(const W4Shape& m, int64_t n);
-size_t w4_image_bytes(const W4Shape& m, int64_t n);  // of the tokens that m multiplies
+size_t w4_image_bytes(const W4Shape& m, int64_t n, bool hidden);  // of the tokens that m multiplies
 // The image of p.x.  Before a call's first product it also clears the error word
 // (else null) and n_counters counters.
 int launch_w4_prepare(const W4Product& p, int* err, int64_t n_counters, LaunchCtx& ctx);

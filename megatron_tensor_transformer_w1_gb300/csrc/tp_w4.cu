@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(256) unpack_codes_kernel(W4Shape m, W4Codes c,
   }
 }
 
-// The factors of the rows (see w4_row_up): a block to a unit, a thread to a row.
-__global__ void __launch_bounds__(256) tops_kernel(W4Shape m, uint8_t* packed) {
+// The factors of the rows (see W4Shape::row_up): a block to a unit, a thread to a row.
+__global__ void __launch_bounds__(256) row_up_kernel(W4Shape m, uint8_t* packed) {
   const long long chunks = m.chunks(), unit = blockIdx.x;
   const int r = threadIdx.x, subs = 128 / m.group;
   uint32_t top = 0;  // the largest |scale|, as bits: infinities and NaN are largest
@@ -490,9 +490,6 @@ __global__ void __launch_bounds__(256) tops_kernel(W4Shape m, uint8_t* packed) {
   }
   const int e = min(static_cast<int>(top >> 7), 254) - 127;  // top < 2^(e + 1)
   m.row_up(packed)[unit * 256 + r] = pow2(top ? 11 - e : 0);
-  top = __reduce_max_sync(0xffffffffu, top);
-  // with gates the unit's second tile has the second matrix's rows
-  if ((r & 31) == 0) atomicMax(m.tops(packed) + (m.rows_kind == W4_GATED ? r >> 7 : 0), top << 16);
 }
 
 // ================================================================ products
@@ -503,10 +500,12 @@ __global__ void __launch_bounds__(256) tops_kernel(W4Shape m, uint8_t* packed) {
 // a run of chunks of one unit is a segment.  A unit that several blocks share is
 // joined by the last of them to come, in the order of the columns.
 //
-// Two kernels: few tokens (up to 8) on registers, more on tensor memory.  Both are
-// as exact as sums in 32 bits: no scaled weight and no hidden activation is rounded
-// to bf16.  The tokens are fp16 numbers times a power of two.  A token with an
-// infinity or a NaN gets those throughout.
+// Two kernels: few tokens (up to 8) on registers, more on tensor memory.  Both sum in 32
+// bits.  Tokens are fp16 numbers times a power of two, which bf16 inputs are too;
+// hidden activations are rounded to it, to 11 bits (to bf16 they would be rounded to 8;
+// in two fp16 numbers each, 22 bits, the second product of a prompt, whose time is that of its
+// matrix instructions, would take twice as long).  The scaled weights of the second
+// kernel are rounded where a scale is below 2^-12 of its row's largest.
 using namespace tc;
 
 // A block of tokens as the kernels keep it ("image"), for NT tokens: fp16 [2][NT][64],
@@ -517,11 +516,17 @@ using namespace tc;
 //    2^14..2^15, so that bf16's eight bits are kept down to 2^-31 of it and what is
 //    smaller is rounded to 2^-39 of it.
 //  * More: the power of two is the token's, for all columns.  Behind the images of
-//    all tokens lies int [tokens + 1], the exponents e: |x| < 2^e, kept as x 2^(15 - e), and
-//    last the least that any of them counts for.
+//    all tokens lies int [tokens][APART], in the first the exponent e: |x| < 2^e, kept as
+//    x 2^(15 - e) (every block's maximum for a token goes there: thousands that
+//    met in a line took 4 us for 32 tokens of the 70B feed-forward).  For hidden activations int [chunks][tokens] behind that, those of each block of columns,
+//    with which they are written before the token's is known (see fit_kernel).
 constexpr int FEW = 8;  // tokens
 __host__ __device__ constexpr int image_bytes(int nt) { return nt * 256 + (nt <= FEW ? 128 : 0); }  // (copied to multiples of 128)
-constexpr int LEAST = -1000;  // an exponent below all
+constexpr int APART = 32;
+constexpr int LEAST = -111;  // an exponent: 2^(15 - e) is a number
+__device__ __forceinline__ int exponent(uint32_t bits) {  // |v| < 2^it, from v's bits (infinities, NaN: the largest)
+  return max(static_cast<int>(bits >> 23 & 255u) - 126, LEAST);
+}
 
 struct ProductParams {
   W4Shape m;
@@ -537,7 +542,8 @@ struct ProductParams {
   int out_chunks;
   int nt, stages, stage_bytes, bufs;  // more than a few tokens
   const float* row_up;
-  const int *e_in, *e_out;  // the tokens' exponents, by token
+  const int* e_in;          // the tokens' exponents, by token
+  int *e_out, *e_chunk;     // those of the hidden activations, of all columns and by chunk and token
   int padded;               // tokens of all tiles
   int blocks;               // runs of chunks
   // few tokens: [blocks][2][NT][256], else [token tiles][blocks + units - 1][NT][256]
@@ -566,12 +572,7 @@ struct PrepareParams {
   int nt, tiles;
   uint8_t* image;  // [tiles][chunks]
   int *err, *counters, n_counters;
-  // more than a few tokens, and hidden activations to come
-  int *e_in, *e_out;
-  const uint32_t* tops;
-  int epi;
-  const __nv_bfloat16* bias;
-  long long n_bias;
+  int *e_in, *e_out;  // more than a few tokens: exponents; those of hidden activations to come are cleared
 };
 // The kernel before a call's first product: the tokens' blocks, a warp to a token's;
 // clears what the call counts in.  It lets others start when everything before it
@@ -599,36 +600,14 @@ __global__ void __launch_bounds__(256) prepare_few_kernel(const __grid_constant_
   }
 }
 // More tokens: a block to a token (some 4 us, most of it its start), whose largest element it needs before the first
-// is written.  The exponents of the hidden activations are bounds:
-// |a| <= sum |x| 8 max s, the largest scale of the matrix, |silu(a) g| <= |a| |g|,
-// |gelu(z)| <= |z| <= |a| + max |b1|.  A bound some 2^12 above the largest hidden value leaves it
-// 2^3 of fp16's 2^-25 .. 2^15, so that it is rounded to 2^-28 of the largest.
+// is written.
 constexpr int PREPARE_THREADS = 512;
-__device__ __forceinline__ int exponent(float v) { return static_cast<int>(__float_as_uint(v) >> 23 & 255u) - 126; }  // v < 2^it
 __global__ void __launch_bounds__(PREPARE_THREADS) prepare_kernel(const __grid_constant__ PrepareParams p) {
   prepare_call(p);
   __shared__ uint32_t s_most[PREPARE_THREADS / 32];
-  __shared__ float s_sum[PREPARE_THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = static_cast<int>(p.chunks) * 16;
   const int padded = p.tiles * p.nt;
-  auto most_of = [&](uint32_t v) {  // of the block, as bits
-    v = __reduce_max_sync(0xffffffffu, v);
-    if (lane == 0) s_most[warp] = v;
-    __syncthreads();
-    v = __reduce_max_sync(0xffffffffu, s_most[lane & (PREPARE_THREADS / 32 - 1)]);
-    __syncthreads();
-    return v;
-  };
-  for (int token = blockIdx.x; token <= padded; token += gridDim.x) {
-    if (token == padded) {  // the least exponents
-      uint32_t most = 0;
-      for (long long i = threadIdx.x; i < p.n_bias; i += PREPARE_THREADS)
-        most = max(most, __float_as_uint(fabsf(__bfloat162float(p.bias[i]))));
-      most = most_of(most);
-      if (threadIdx.x == 0) p.e_in[token] = LEAST;
-      if (threadIdx.x == 0 && p.e_out) p.e_out[token] = p.n_bias ? exponent(__uint_as_float(most)) + 1 : LEAST;
-      break;
-    }
+  for (int token = blockIdx.x; token < padded; token += gridDim.x) {
     const int tile = token / p.nt, in = token - tile * p.nt;
     auto piece = [&](int i) {  // eight columns
       const int chunk = i >> 4, e = chunk / static_cast<int>(p.seg_chunks);
@@ -644,10 +623,13 @@ __global__ void __launch_bounds__(PREPARE_THREADS) prepare_kernel(const __grid_c
 #pragma unroll
       for (int j = 0; j < 4; ++j) most = max(most, max(v[j] & 0x7fff0000u, (v[j] << 16) & 0x7fff0000u));
     }
-    most = most_of(most);
-    const int e_x = max(exponent(__uint_as_float(most)), -111);  // 2^(15 - e_x) is a number
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_most[warp] = most;
+    __syncthreads();
+    most = __reduce_max_sync(0xffffffffu, s_most[lane & (PREPARE_THREADS / 32 - 1)]);
+    __syncthreads();
+    const int e_x = exponent(most);
     const float up = pow2(15 - e_x);
-    float sum = 0.f;
     uint8_t* image = p.image + static_cast<long long>(tile) * p.chunks * image_bytes(p.nt) + in * 128;
     for (int i = threadIdx.x; i < pieces; i += PREPARE_THREADS) {
       const uint4 w = piece(i);
@@ -655,31 +637,16 @@ __global__ void __launch_bounds__(PREPARE_THREADS) prepare_kernel(const __grid_c
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = bf16_at(v[j], 0) * up, b = bf16_at(v[j], 1) * up;
-        const __half2 h = __floats2half2_rn(a, b);
+        const __half2 h = __floats2half2_rn(bf16_at(v[j], 0) * up, bf16_at(v[j], 1) * up);
         o[j] = *reinterpret_cast<const uint32_t*>(&h);
-        sum += fabsf(a) + fabsf(b);
       }
       *reinterpret_cast<uint4*>(image + static_cast<long long>(i >> 4) * image_bytes(p.nt) + ((i >> 3) & 1) * (p.nt * 128) +
                                 (((i & 7) ^ (in & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    if (p.e_out) {
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == 0) s_sum[warp] = sum;
-      __syncthreads();
-    }
     if (threadIdx.x == 0) {
-      p.e_in[token] = e_x;
-      if (p.e_out) {
-        sum = 0.f;
-        for (int i = 0; i < PREPARE_THREADS / 32; ++i) sum += s_sum[i];
-        const int a = exponent(sum) + e_x - 15 + 3;  // times 8 max s
-        const int of0 = exponent(__uint_as_float(p.tops[0])), of1 = exponent(__uint_as_float(p.tops[1]));
-        p.e_out[token] = p.epi == W4_SWIGLU ? 2 * a + of0 + of1 : a + of0 + 1;
-      }
+      p.e_in[token * APART] = e_x;
+      if (p.e_out) p.e_out[token * APART] = LEAST;
     }
-    __syncthreads();
   }
 }
 
@@ -819,9 +786,9 @@ __device__ __forceinline__ void copy_chunks(const ProductParams& p, const Run& r
 }
 
 // Four neighbouring rows of a token, by a warp that has 128: bias or activation, and
-// out.  FEW: into an image of few tokens; else `up` is the hidden activations' factor.
+// out.  FEW_TOKENS: into an image of few tokens.
 template <bool FEW_TOKENS>
-__device__ __forceinline__ void write4(const ProductParams& p, int nt, int tile, int in_tile, long long row, int lane, float4 v, float up) {
+__device__ __forceinline__ void write4(const ProductParams& p, int nt, int tile, int in_tile, long long row, int lane, float4 v) {
   float a[4] = {v.x, v.y, v.z, v.w};
   if (p.epi == W4_OUT) {
     const long long token = static_cast<long long>(tile) * nt + in_tile;
@@ -845,6 +812,16 @@ __device__ __forceinline__ void write4(const ProductParams& p, int nt, int tile,
   if (FEW_TOKENS) {
     store_block(image, nt, in_tile, lane, a);
   } else {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = max(most, __float_as_uint(a[i]) & 0x7fffffffu);
+    const int e = exponent(__reduce_max_sync(0xffffffffu, most));
+    const float up = pow2(15 - e);
+    if (lane == 0) {
+      const int token = tile * nt + in_tile;
+      p.e_chunk[static_cast<long long>(chunk) * p.padded + token] = e;
+      atomicMax(p.e_out + token * APART, e);
+    }
     const __half2 lo = __floats2half2_rn(a[0] * up, a[1] * up), hi = __floats2half2_rn(a[2] * up, a[3] * up);
     uint8_t* at = image + (lane >> 4) * (nt * 128) + in_tile * 128 + ((((lane & 15) >> 1) ^ (in_tile & 7)) << 4) + (lane & 1) * 8;
     *reinterpret_cast<uint2*>(at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -900,10 +877,10 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
       v0.y *= sigmoid_f(v0.y) * v1.y;
       v0.z *= sigmoid_f(v0.z) * v1.z;
       v0.w *= sigmoid_f(v0.w) * v1.w;
-      write4<true>(p, FEW, 0, token, unit * 128 + q4, lane, v0, 1.f);
+      write4<true>(p, FEW, 0, token, unit * 128 + q4, lane, v0);
     } else {
-      write4<true>(p, FEW, 0, token, unit * 256 + q4, lane, v0, 1.f);
-      write4<true>(p, FEW, 0, token, unit * 256 + 128 + q4, lane, v1, 1.f);
+      write4<true>(p, FEW, 0, token, unit * 256 + q4, lane, v0);
+      write4<true>(p, FEW, 0, token, unit * 256 + 128 + q4, lane, v1);
     }
   }
   bar_sync(1, FEW_WARPS * 32);
@@ -1073,8 +1050,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_kernel(const __grid_consta
 // Every wait is bounded (abort flag and error word); after an abort the warps run
 // on without waiting, so that they meet at the block's barriers.
 //
-// 70B feed-forward: 32 tokens 81 us, 64 tokens 95, 128 tokens 136; 389 tokens of the 8B
-// one 133 us, 1.03 PFLOP/s.  Up to 64 tokens a chunk takes some 1000 cycles, of which
+// 70B feed-forward: 32 tokens 82 us, 64 tokens 98, 128 tokens 140; 389 tokens of the 8B
+// one 139 us, 0.99 PFLOP/s.  Up to 64 tokens a chunk takes some 1000 cycles, of which
 // its bytes take 720 and its products 750.  Tried:
 //  * e4m3 operands as subnormals, group sums read back and scaled in 32 bits: 32 tokens
 //    100 us, 64 tokens (two tiles) 170;
@@ -1348,8 +1325,7 @@ __global__ void __launch_bounds__(FINISH_TOKENS * 32) finish_kernel(const __grid
                up1 = *reinterpret_cast<const float4*>(p.row_up + unit * 256 + 128 + q4);
   grid_dep_wait();
   if (token >= p.n) return;
-  const int down = -min(max(15 - max(p.e_in[token], p.e_in[p.padded]), -126), 126);  // as pow2 has it
-  const float up = p.e_out ? pow2(15 - max(p.e_out[token], p.e_out[p.padded])) : 1.f;
+  const int down = p.e_in[token * APART] - 15;
   float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
 #pragma unroll 4
   for (int b = c0; b <= c1; ++b, from += p.nt * 256) {
@@ -1371,11 +1347,40 @@ __global__ void __launch_bounds__(FINISH_TOKENS * 32) finish_kernel(const __grid
     v0.y *= sigmoid_f(v0.y) * v1.y;
     v0.z *= sigmoid_f(v0.z) * v1.z;
     v0.w *= sigmoid_f(v0.w) * v1.w;
-    write4<false>(p, p.nt, tile, in_tile, unit * 128ll + q4, lane, v0, up);
+    write4<false>(p, p.nt, tile, in_tile, unit * 128ll + q4, lane, v0);
   } else {
-    write4<false>(p, p.nt, tile, in_tile, unit * 256ll + q4, lane, v0, up);
-    write4<false>(p, p.nt, tile, in_tile, unit * 256ll + 128 + q4, lane, v1, up);
+    write4<false>(p, p.nt, tile, in_tile, unit * 256ll + q4, lane, v0);
+    write4<false>(p, p.nt, tile, in_tile, unit * 256ll + 128 + q4, lane, v1);
   }
+}
+
+// The hidden activations of a token, whose blocks of 128 columns finish_kernel has written
+// with powers of two of their own, brought to the token's: its largest is known when all
+// of them are written.  What it rounds are elements below 2^-28 of that, by 2^-39 of it.  (A bound
+// from the token's absolute sum and the largest scales needs no kernel, but lies as far
+// above the hidden activations as one scale lies above the others: with one group in either matrix 2^10
+// times the others, results were off by up to 0.016 for 0.0017.)
+// A block to 16 tokens of a block of columns, a thread to eight columns: 2 us of the pass for 32
+// tokens of the 70B feed-forward, 5 for 128.
+constexpr int FIT_TOKENS = 16;
+__global__ void __launch_bounds__(FIT_TOKENS * 16) fit_kernel(const __grid_constant__ ProductParams p) {
+  grid_dep_launch();
+  const int chunk = blockIdx.x, tile = blockIdx.z, i = threadIdx.x & 127, in = blockIdx.y * FIT_TOKENS + (i >> 3);
+  const int token = tile * p.nt + in;
+  uint4* at = reinterpret_cast<uint4*>(p.image_out + (static_cast<long long>(tile) * p.out_chunks + chunk) * image_bytes(p.nt)) +
+              (threadIdx.x >> 7) * (p.nt * 8) + in * 8 + (i & 7);
+  grid_dep_wait();
+  if (token >= p.n) return;
+  const uint4 v = *at;
+  const float f = pow2(p.e_chunk[static_cast<long long>(chunk) * p.padded + token] - p.e_out[token * APART]);
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    const __half2 h = __floats2half2_rn(a.x * f, a.y * f);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *at = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename... KArgs, typename... Args>
@@ -1442,6 +1447,9 @@ Cut cut_of(const W4Shape& m, int64_t n, int num_sms) {
 int64_t image_end(const W4Shape& m, const Cut& c) { return m.chunks() * c.tiles * image_bytes(c.nt); }
 
 int64_t hidden_chunks(const W4Shape& m) { return m.T * m.sp / 128; }
+int* hidden_exponents(const W4Product& a, const Cut& c) {
+  return reinterpret_cast<int*>(static_cast<uint8_t*>(a.image_out) + hidden_chunks(a.m) * c.tiles * image_bytes(c.nt));
+}
 // A grid of at most 32 blocks per SM.
 unsigned grid_of(long long blocks) { return static_cast<unsigned>(std::min<long long>(std::max<long long>(blocks, 1), 32 * 152)); }
 int launched() { return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA; }  // (an error is not left for the next call)
@@ -1504,8 +1512,7 @@ int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack,
   if (unpack) {
     unpack_codes_kernel<<<grid_of(m.tiles()), 256, 0, st>>>(m, c, to);
   } else {
-    if (cudaMemsetAsync(m.tops(to), 0, 16, st) != cudaSuccess) return TP_ERR_CUDA;
-    tops_kernel<<<static_cast<unsigned>(m.units()), 256, 0, st>>>(m, to);
+    row_up_kernel<<<static_cast<unsigned>(m.units()), 256, 0, st>>>(m, to);
   }
   return launched();
 }
@@ -1517,9 +1524,10 @@ size_t w4_product_scratch(const W4Shape& m, int64_t n, int num_sms) {
 }
 int64_t w4_product_counters(const W4Shape& m, int64_t n) { return n <= w4::FEW ? m.units() : 0; }
 
-size_t w4_image_bytes(const W4Shape& m, int64_t n) {
+size_t w4_image_bytes(const W4Shape& m, int64_t n, bool hidden) {
   const w4::Cut c = w4::cut_of(m, n, 1);
-  return static_cast<size_t>(w4::image_end(m, c)) + (static_cast<size_t>(c.tiles) * c.nt + 1) * sizeof(int);
+  const int64_t exponents = c.nt <= w4::FEW ? 0 : c.tiles * c.nt * (w4::APART + (hidden ? m.chunks() : 0));
+  return static_cast<size_t>(w4::image_end(m, c)) + static_cast<size_t>(exponents) * sizeof(int);
 }
 
 int launch_w4_prepare(const W4Product& a, int* err, int64_t n_counters, LaunchCtx& ctx) {
@@ -1545,16 +1553,8 @@ int launch_w4_prepare(const W4Product& a, int* err, int64_t n_counters, LaunchCt
     blocks = static_cast<unsigned>(std::min<int64_t>((p.tiles * p.chunks * p.nt + 7) / 8, 8 * ctx.num_sms));
   } else {
     p.e_in = reinterpret_cast<int*>(p.image + image_end(a.m, c));
-    if (a.epi != W4_OUT) {
-      p.e_out = reinterpret_cast<int*>(static_cast<uint8_t*>(a.image_out) + hidden_chunks(a.m) * c.tiles * image_bytes(c.nt));
-      p.tops = a.m.tops(const_cast<void*>(a.packed));
-      p.epi = a.epi;
-      if (a.epi == W4_GELU && a.bias) {
-        p.bias = static_cast<const __nv_bfloat16*>(a.bias);
-        p.n_bias = a.m.T * a.m.s;
-      }
-    }
-    blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.nt + 1, 4 * ctx.num_sms));
+    if (a.epi != W4_OUT) p.e_out = hidden_exponents(a, c);
+    blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.nt, 4 * ctx.num_sms));
   }
   if (ctx.before) ctx.before(ctx.user, "prepare4", ctx.stream);
   if (few)
@@ -1605,8 +1605,10 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
     p.row_up = a.m.row_up(const_cast<void*>(a.packed));
     p.padded = c.tiles * c.nt;
     p.e_in = reinterpret_cast<const int*>(p.image + image_end(a.m, c));
-    if (a.epi != W4_OUT)
-      p.e_out = reinterpret_cast<const int*>(p.image_out + static_cast<int64_t>(p.out_chunks) * c.tiles * image_bytes(c.nt));
+    if (a.epi != W4_OUT) {
+      p.e_out = hidden_exponents(a, c);
+      p.e_chunk = p.e_out + p.padded * APART;
+    }
     p.blocks = c.blocks;
     rc = launch_product(p, grid, ctx.stream);
   }
@@ -1617,8 +1619,13 @@ int launch_w4_product(const W4Product& a, LaunchCtx& ctx) {
     if (ctx.before) ctx.before(ctx.user, "finish4", ctx.stream);
     launch_dep(finish_kernel, dim3(static_cast<unsigned>(p.units), static_cast<unsigned>(c.nt / FINISH_TOKENS), static_cast<unsigned>(c.tiles)),
                FINISH_TOKENS * 32, 0, ctx.stream, p);
-    if (ctx.after) ctx.after(ctx.user, ctx.stream);
     ctx.launches++;
+    if (a.epi != W4_OUT) {  // (timed as one with it)
+      launch_dep(fit_kernel, dim3(static_cast<unsigned>(p.out_chunks), static_cast<unsigned>(c.nt / FIT_TOKENS), static_cast<unsigned>(c.tiles)),
+                 FIT_TOKENS * 16, 0, ctx.stream, p);
+      ctx.launches++;
+    }
+    if (ctx.after) ctx.after(ctx.user, ctx.stream);
   }
   return launched();
 }

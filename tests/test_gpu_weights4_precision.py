@@ -104,3 +104,71 @@ def test_an_infinity_gives_what_its_weights_say(n):
     assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.isinf(), want.isinf())
     assert torch.equal(y[y.isinf()], want[want.isinf()])
     assert y[0].isinf().any() and y[0].isnan().any() and y[2].isinf().any() and y[3].isnan().all()
+
+
+@pytest.mark.parametrize("n", [1, 8, 9, 40, 130])
+@pytest.mark.parametrize("act,d,d_ff,T", [("swiglu", 1024, 1536, 4), ("gelu_tanh", 768, 2048, 2), ("none", 1024, 1000, 5)])
+def test_only_the_result_is_rounded_to_bf16(act, d, d_ff, T, n):
+    ffn, codes = _ffn(act, d, d_ff, T), _weights(act, d, d_ff, T, 64, 51)
+    x = torch.randn(n, d_ff if act == "none" else d, generator=_gen(52), device="cuda").to(BF)
+    _check(ffn.forward4(x, *_pack(ffn, codes)), *_forward(x, act, codes, 64))
+
+
+@pytest.mark.parametrize("n", [8, 9, 64, 130])
+@pytest.mark.parametrize("rows", [(5, 900), (5, 5)])
+@pytest.mark.parametrize("far", [8, 10, 12, 20])
+def test_one_large_group_in_either_matrix(far, rows, n):
+    """A group of one hidden unit in each of W1 and W3 with a scale far above the others, in different units
+    (whose hidden values stay near the others') and in the same (one unit above all others, where it is not
+    shut): each token's error stays what it is without them."""
+    d, d_ff, T = 1024, 1024, 2
+    ffn, codes = _ffn("swiglu", d, d_ff, T), _weights("swiglu", d, d_ff, T, 128, 53)
+    for c, row in zip(codes, rows):
+        c.scales[row, 3] *= 2.0 ** far
+    x = torch.randn(n, d, generator=_gen(54), device="cuda").to(BF)
+    _check(ffn.forward4(x, *_pack(ffn, codes)), *_forward(x, "swiglu", codes, 128), dim=1)
+
+
+@pytest.mark.parametrize("n", [8, 9, 40])
+def test_one_large_group_before_gelu(n):
+    d, d_ff, T = 512, 1024, 2
+    ffn, codes = _ffn("gelu_tanh", d, d_ff, T), _weights("gelu_tanh", d, d_ff, T, 64, 55)
+    codes[0].scales[700, 1] *= 2.0 ** 20
+    x = torch.randn(n, d, generator=_gen(56), device="cuda").to(BF)
+    _check(ffn.forward4(x, *_pack(ffn, codes)), *_forward(x, "gelu_tanh", codes, 64), dim=1)
+
+
+@pytest.mark.parametrize("n", [3, 8, 9, 40, 150])
+@pytest.mark.parametrize("act", ["swiglu", "gelu_tanh"])
+def test_hidden_activations_keep_eleven_bits(act, n):
+    """Hidden activations that are whole numbers of 1024..2047, times a power of two that the token has: y, the
+    difference of two of them, is a bf16 number and comes out as it is (of eight bits, they would be off by up to
+    four).  silu(64) and gelu of such numbers are their argument in 32 bits."""
+    d, d_ff, T, group = 64, 256, 2, 32
+    g = _gen(57)
+    base = torch.randint(1024, 1793, (d_ff // 2, 1), generator=g, device="cuda")
+    h = (base + torch.randint(0, 256, (d_ff // 2, 2), generator=g, device="cuda")).flatten()
+
+    def codes_of(q, segments):
+        groups = segments * -(-(q.shape[1] // segments) // group)
+        return _lib().Codes4(ref.bytes_of(q + 8), torch.ones(q.shape[0], groups, dtype=BF, device="cuda"), q.shape[1], group, segments)
+    digits, left = torch.zeros(d_ff, d, dtype=torch.long, device="cuda"), h.clone()
+    for k in range(3):  # h = sum digit 8^k with digits -4..3, the last up to 4
+        digits[:, k] = (left + 4) % 8 - 4
+        left = (left - digits[:, k]) // 8
+    digits[:, 3] = left
+    gate = torch.zeros(d_ff, d, dtype=torch.long, device="cuda")
+    gate[:, 4] = 1
+    down = torch.zeros(d, d_ff, dtype=torch.long, device="cuda")
+    at = torch.arange(d, device="cuda")
+    down[at, 4 * at], down[at, 4 * at + 1] = 1, -1  # of both shards
+    up = [codes_of(gate, 1), codes_of(digits, 1)] if act == "swiglu" else [codes_of(digits, 1)]
+    size = torch.exp2((torch.arange(n, device="cuda") % 4).float())[:, None]
+    x = torch.zeros(n, d, device="cuda")
+    x[:, :4] = 8.0 ** torch.arange(4, device="cuda")
+    x[:, 4] = 64
+    x = (x * size).to(BF)
+    want = (h[0::4] - h[1::4]) * (64 * size.square() if act == "swiglu" else size)
+    ffn = _ffn(act, d, d_ff, T)
+    y = ffn.forward4(x, *_pack(ffn, up + [codes_of(down, T)]))
+    assert torch.equal(y.double(), want.double())
