@@ -487,7 +487,8 @@ TPFFN_API int tp_attn_kv_last_device_error(const tp_attn_plan* plan, const void*
  */
 
 /* Quantises W [rows][cols] bf16: s = bf16(max |w| / 7) and code = rint(w / s)
- * + 8, ties to even, so codes lie in 1..15; 8 where s is 0.  A group with an
+ * + 8, ties to even, limited to 0..15 (codes lie in 1..15 but where s is a subnormal,
+ * below 2^-126); 8 where s is 0.  A group with an
  * infinity or a NaN gets that for its scale.  One launch, two where cols /
  * segments is no multiple of 16.
  * Dequantising: W = bf16((code - 8) * s).

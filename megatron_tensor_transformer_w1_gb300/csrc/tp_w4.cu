@@ -56,7 +56,8 @@ __device__ __forceinline__ float pow2(int e) {
 }
 
 // ================================================================ quantising
-// s = bf16(max |w| / 7), code = rint(w / s) + 8, ties to even.
+// s = bf16(max |w| / 7), code = rint(w / s) + 8, ties to even, limited to 0..15: only a scale
+// that is a subnormal is more than 2^-9 off max |w| / 7, so that |w| > 7.03 s.
 // A group with an infinity or NaN has that for its scale.  With s = 0 (all
 // zero, or too small for bf16) every code is 8.
 // The quotient by a product with 1 / 7 and its remainder, which is exact.
@@ -71,7 +72,10 @@ __device__ __forceinline__ void ready(float& s, float& inv, float& up) {
   s *= up;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // (to 2^-22; s is below 2^126)
 }
-// The codes of two elements, in the low bytes, for finite s > 0 and |w| <= 7.03 s.  The
+// What `ready` asks for besides, which is where |w| may be above 7.03 s: w between -8 s and 7 s, for
+// the same codes.
+__device__ __forceinline__ float limited(float w, float s) { return fminf(fmaxf(w, -8.f * s), 7.f * s); }
+// The codes of two elements, in the low bytes, for finite s > 0 and w in -8 s .. 7.03 s.  The
 // quotient in two steps: q = w inv, then q + (w - q s) inv, whose remainder is exact and
 // which is the quotient to 2^-43 before its last rounding: a tie, which 32 bits hold,
 // comes out exactly, and others lie at least 2^-18 from one.  The sum with 1.5 2^23 + 8
@@ -134,8 +138,13 @@ __global__ void __launch_bounds__(256) quantize16_kernel(const uint4* __restrict
     const bool any = has_codes(s);
     ready(s, inv, up);
     if (up != 1.f) {
+      const uint32_t most = tc::pack_bf16x2(7.f * s, 7.f * s), least = tc::pack_bf16x2(-8.f * s, -8.f * s);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[j]) : "r"(0x5f805f80u));  // 2^64
+      for (int j = 0; j < 8; ++j) {  // limited(w 2^64, s)
+        asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[j]) : "r"(0x5f805f80u));
+        asm("min.bf16x2 %0, %0, %1;" : "+r"(v[j]) : "r"(most));
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(v[j]) : "r"(least));
+      }
     }
     const uint64_t less2 = pack2(-s, -s), inv2 = pack2(inv, inv);
     uint32_t word[2];
@@ -292,7 +301,9 @@ __global__ void __launch_bounds__(256) codes8_kernel(const __nv_bfloat16* __rest
     auto pick = [&](int i, auto& a) { return of.of(i, a[0], a[1], a[2]); };
     if (up[0] != 1.f || up[1] != 1.f || up[2] != 1.f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = tc::pack_bf16x2(bf16_at(v[j], 0) * pick(2 * j, up), bf16_at(v[j], 1) * pick(2 * j + 1, up));
+      for (int j = 0; j < 4; ++j)
+        v[j] = tc::pack_bf16x2(limited(bf16_at(v[j], 0) * pick(2 * j, up), pick(2 * j, sg)),
+                               limited(bf16_at(v[j], 1) * pick(2 * j + 1, up), pick(2 * j + 1, sg)));
     }
     uint32_t word = 0;
 #pragma unroll
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(256) codes_kernel(const __nv_bfloat16* __restr
       float s = __bfloat162float(scales[(row * segs + e) * seg_groups + g]), inv, up;
       const bool any = has_codes(s);
       ready(s, inv, up);
-      const float w = __bfloat162float(W[row * cols + c]) * up;
+      const float w = limited(__bfloat162float(W[row * cols + c]) * up, s);
       const uint32_t q = any ? codes_of(pack2(w, w), pack2(-s, -s), pack2(inv, inv)).x & 15u : 8u;
       byte = h ? (byte & 0x0fu) | (q << 4) : (byte & 0xf0u) | q;
     }
