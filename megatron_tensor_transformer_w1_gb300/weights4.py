@@ -118,6 +118,8 @@ def quantize4(W, group=128, segments=1):
 
 def dequantize4(c):
     """The matrix that a Codes4 stands for, bfloat16 [rows, cols]."""
+    if not isinstance(c, Codes4) or not c.codes.is_cuda:
+        raise ValueError("c: a Codes4 on a CUDA device is needed")
     index = c.codes.get_device()
     if current_device() != index:
         with torch.cuda.device(index):
