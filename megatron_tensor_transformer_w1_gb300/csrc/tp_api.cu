@@ -1754,7 +1754,8 @@ int columns4(const tp_ffn_plan* p, int group, const void* c1, const void* s1, co
   c.scales[0] = const_cast<void*>(s1);
   c.codes[1] = const_cast<void*>(c3);
   c.scales[1] = const_cast<void*>(s3);
-  return launch_w4_pack(w4_up(p, group), c, const_cast<void*>(packed), unpack, reinterpret_cast<cudaStream_t>(stream));
+  return launch_w4_pack(w4_up(p, group), c, const_cast<void*>(packed), unpack, num_sms_current(),
+                        reinterpret_cast<cudaStream_t>(stream));
 }
 int rows4(const tp_ffn_plan* p, int group, const void* c2, const void* s2, const void* packed, int unpack,
           tp_stream_t stream) {
@@ -1763,7 +1764,8 @@ int rows4(const tp_ffn_plan* p, int group, const void* c2, const void* s2, const
   W4Codes c;
   c.codes[0] = const_cast<void*>(c2);
   c.scales[0] = const_cast<void*>(s2);
-  return launch_w4_pack(w4_down(p, group), c, const_cast<void*>(packed), unpack, reinterpret_cast<cudaStream_t>(stream));
+  return launch_w4_pack(w4_down(p, group), c, const_cast<void*>(packed), unpack, num_sms_current(),
+                        reinterpret_cast<cudaStream_t>(stream));
 }
 int attn_weights4(const tp_attn_plan* a, int group, const void* const codes[4], const void* const scales[4],
                   const void* wqkv, const void* wo, int unpack, tp_stream_t stream) {
@@ -1776,7 +1778,8 @@ int attn_weights4(const tp_attn_plan* a, int group, const void* const codes[4], 
     c.codes[i] = const_cast<void*>(codes[i]);
     c.scales[i] = const_cast<void*>(scales[i]);
   }
-  rc = launch_w4_pack(w4_qkv(a, group), c, const_cast<void*>(wqkv), unpack, reinterpret_cast<cudaStream_t>(stream));
+  rc = launch_w4_pack(w4_qkv(a, group), c, const_cast<void*>(wqkv), unpack, num_sms_current(),
+                      reinterpret_cast<cudaStream_t>(stream));
   return rc ? rc : rows4(a->wo, group, codes[3], scales[3], wo, unpack, stream);
 }
 }  // namespace
@@ -1886,7 +1889,8 @@ int tp_quantize4(const void* W, int64_t rows, int64_t cols, int64_t segments, in
   bool work;
   const int rc = check_quant4(W, rows, cols, segments, group, codes, scales, work);
   if (rc || !work) return rc;
-  return launch_w4_quantize(W, rows, cols, segments, group, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+  return launch_w4_quantize(W, rows, cols, segments, group, codes, scales, num_sms_current(),
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 int tp_dequantize4(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t segments, int group,
@@ -1894,7 +1898,8 @@ int tp_dequantize4(const void* codes, const void* scales, int64_t rows, int64_t 
   bool work;
   const int rc = check_quant4(W, rows, cols, segments, group, codes, scales, work);
   if (rc || !work) return rc;
-  return launch_w4_dequantize(codes, scales, rows, cols, segments, group, W, reinterpret_cast<cudaStream_t>(stream));
+  return launch_w4_dequantize(codes, scales, rows, cols, segments, group, W, num_sms_current(),
+                              reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t tp_ffn_packed4_bytes(const tp_ffn_plan* p, int which, int group) {

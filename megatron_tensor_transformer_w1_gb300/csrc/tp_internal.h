@@ -312,15 +312,15 @@ __host__ __device__ inline W4Tile w4_tile(const W4Shape& m, int64_t tile) {
 }
 
 int launch_w4_quantize(const void* W, int64_t rows, int64_t cols, int64_t segs, int group, void* codes, void* scales,
-                       cudaStream_t st);
+                       int num_sms, cudaStream_t st);
 int launch_w4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t segs, int group,
-                         void* W, cudaStream_t st);
+                         void* W, int num_sms, cudaStream_t st);
 // Natural to packed and back; up to three matrices (see W4Rows).
 struct W4Codes {
   void* codes[3] = {};
   void* scales[3] = {};
 };
-int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack, cudaStream_t st);
+int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack, int num_sms, cudaStream_t st);
 
 enum W4Epi : int { W4_OUT = 0, W4_GELU = 1, W4_SWIGLU = 2 };
 // epilogue(sum over the columns of x[token][column] * W[row][column] + bias[row])

@@ -1462,20 +1462,20 @@ int* hidden_exponents(const W4Product& a, const Cut& c) {
   return reinterpret_cast<int*>(static_cast<uint8_t*>(a.image_out) + hidden_chunks(a.m) * c.tiles * image_bytes(c.nt));
 }
 // A grid of at most 32 blocks per SM.
-unsigned grid_of(long long blocks) { return static_cast<unsigned>(std::min<long long>(std::max<long long>(blocks, 1), 32 * 152)); }
+unsigned grid_of(long long blocks, int num_sms) { return static_cast<unsigned>(std::min<long long>(std::max<long long>(blocks, 1), 32 * num_sms)); }
 int launched() { return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA; }  // (an error is not left for the next call)
 
 }  // namespace w4
 
 int launch_w4_quantize(const void* W, int64_t rows, int64_t cols, int64_t segs, int group, void* codes, void* scales,
-                       cudaStream_t st) {
+                       int num_sms, cudaStream_t st) {
   using namespace w4;
   const int64_t seg = cols / segs, seg_groups = (seg + group - 1) / group;
   auto* sc = static_cast<__nv_bfloat16*>(scales);
   if (seg % 16 == 0) {
     const int lanes = group == 32 ? 1 : group == 64 ? 2 : 3;
     const long long places = rows * segs * (seg_groups << lanes);
-    quantize16_kernel<<<grid_of((places + 255) / 256), 256, 0, st>>>(
+    quantize16_kernel<<<grid_of((places + 255) / 256, num_sms), 256, 0, st>>>(
         static_cast<const uint4*>(W), rows * (cols / 16), static_cast<int>(cols / 16), static_cast<int>(seg / 16), lanes,
         static_cast<int>(seg_groups), static_cast<int>(segs), static_cast<uint2*>(codes), sc);
     return launched();
@@ -1483,45 +1483,45 @@ int launch_w4_quantize(const void* W, int64_t rows, int64_t cols, int64_t segs, 
   const auto* w = static_cast<const __nv_bfloat16*>(W);
   const int n_segs = static_cast<int>(segs), width = static_cast<int>(seg), groups = static_cast<int>(seg_groups);
   const int lanes = group == 32 ? 2 : group == 64 ? 3 : 4;
-  scales_kernel<<<grid_of((((rows * segs * seg_groups) << lanes) + 255) / 256), 256, 0, st>>>(w, rows, cols, n_segs, width,
+  scales_kernel<<<grid_of((((rows * segs * seg_groups) << lanes) + 255) / 256, num_sms), 256, 0, st>>>(w, rows, cols, n_segs, width,
                                                                                               lanes, groups, sc);
   if (seg >= 8)
-    codes8_kernel<<<grid_of((rows * ((cols + 7) / 8) + 255) / 256), 256, 0, st>>>(
+    codes8_kernel<<<grid_of((rows * ((cols + 7) / 8) + 255) / 256, num_sms), 256, 0, st>>>(
         w, rows, static_cast<int>(cols), n_segs, width, group, groups, sc, static_cast<uint8_t*>(codes));
   else
-    codes_kernel<<<grid_of((rows * ((cols + 1) / 2) + 255) / 256), 256, 0, st>>>(
+    codes_kernel<<<grid_of((rows * ((cols + 1) / 2) + 255) / 256, num_sms), 256, 0, st>>>(
       w, rows, cols, static_cast<int>(segs), seg, group, seg_groups, sc, static_cast<uint8_t*>(codes));
   return launched();
 }
 
 int launch_w4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t segs, int group,
-                         void* W, cudaStream_t st) {
+                         void* W, int num_sms, cudaStream_t st) {
   using namespace w4;
   const int64_t seg = cols / segs, seg_groups = (seg + group - 1) / group;
   const auto* sc = static_cast<const __nv_bfloat16*>(scales);
   if (seg % 16 == 0) {
     const long long pieces = rows * (cols / 16);
-    dequantize16_kernel<<<grid_of((pieces + 255) / 256), 256, 0, st>>>(
+    dequantize16_kernel<<<grid_of((pieces + 255) / 256, num_sms), 256, 0, st>>>(
         static_cast<const uint2*>(codes), sc, pieces, static_cast<int>(cols / 16), static_cast<int>(seg / 16),
         group == 32 ? 1 : group == 64 ? 2 : 3, static_cast<int>(seg_groups), static_cast<int>(segs), static_cast<uint4*>(W));
   } else if (seg >= 8) {
-    dequantize8_kernel<<<grid_of((rows * ((cols + 7) / 8) + 255) / 256), 256, 0, st>>>(
+    dequantize8_kernel<<<grid_of((rows * ((cols + 7) / 8) + 255) / 256, num_sms), 256, 0, st>>>(
         static_cast<const uint8_t*>(codes), sc, rows, static_cast<int>(cols), static_cast<int>(segs), static_cast<int>(seg),
         group, static_cast<int>(seg_groups), static_cast<__nv_bfloat16*>(W));
   } else {
-    dequantize_kernel<<<grid_of((rows * cols + 255) / 256), 256, 0, st>>>(
+    dequantize_kernel<<<grid_of((rows * cols + 255) / 256, num_sms), 256, 0, st>>>(
         static_cast<const uint8_t*>(codes), sc, rows, cols, static_cast<int>(segs), seg, group, seg_groups,
         static_cast<__nv_bfloat16*>(W));
   }
   return launched();
 }
 
-int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack, cudaStream_t st) {
+int launch_w4_pack(const W4Shape& m, const W4Codes& c, void* packed, int unpack, int num_sms, cudaStream_t st) {
   using namespace w4;
   auto* to = static_cast<uint8_t*>(packed);
-  pack_kernel<<<grid_of(m.units() * m.chunks()), 256, 0, st>>>(m, c, to, unpack);
+  pack_kernel<<<grid_of(m.units() * m.chunks(), num_sms), 256, 0, st>>>(m, c, to, unpack);
   if (unpack) {
-    unpack_codes_kernel<<<grid_of(m.tiles()), 256, 0, st>>>(m, c, to);
+    unpack_codes_kernel<<<grid_of(m.tiles(), num_sms), 256, 0, st>>>(m, c, to);
   } else {
     row_up_kernel<<<static_cast<unsigned>(m.units()), 256, 0, st>>>(m, to);
   }
