@@ -360,6 +360,10 @@ __global__ void __launch_bounds__(1024) forward_kernel(const __grid_constant__ N
 // full, a row's two sums over its threads one behind the other; 4104 tokens of 1160 in
 // 32 bits with layer norms, 114 MB, 40 us.  (Two columns to a thread more: spills, 145 us; its
 // own instance for every combination of norms and gates: no faster.)
+// Rows of more than 4096 columns need more than 512 threads and have 64 registers
+// each, so that sums, weights and values are spilled (590 to 1380 bytes a thread; the other
+// instances with shifts 20 to 40): 8192 tokens of 5120 in bf16, 503 MB, 263 us, of 8192, 805 MB,
+// 334 us, 2.4 TB/s.
 enum { S_WB = 0, S_CB = 1, S_WA = 2, S_CA = 3 };
 enum { A_DR = 0, A_DOUT = 1, A_R = 2, A_B = 3, A_GATE = 4 };  // slots; the last with a gate for each token
 template <typename T, bool LAYER, bool SHIFT, int MAX_THREADS>

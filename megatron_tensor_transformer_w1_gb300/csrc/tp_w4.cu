@@ -512,11 +512,12 @@ __global__ void __launch_bounds__(256) row_up_kernel(W4Shape m, uint8_t* packed)
 // joined by the last of them to come, in the order of the columns.
 //
 // Two kernels: few tokens (up to 8) on registers, more on tensor memory.  Both sum in 32
-// bits.  Tokens are fp16 numbers times a power of two, which bf16 inputs are too;
-// hidden activations are rounded to it, to 11 bits (to bf16 they would be rounded to 8;
-// in two fp16 numbers each, 22 bits, the second product of a prompt, whose time is that of its
-// matrix instructions, would take twice as long).  The scaled weights of the second
-// kernel are rounded where a scale is below 2^-12 of its row's largest.
+// bits.  Tokens are fp16 numbers times a power of two, which holds bf16's eight bits.
+// Hidden activations are rounded to it, to 11 bits: beside y's own rounding to bf16, 2^-9, that
+// is 2^-12 (0.00167 -> 0.00168 in root mean square against 64 bits for the 70B
+// feed-forward).  In two fp16 numbers each they would have 22, and the second
+// product twice the matrix instructions, whose time a prompt's is.  The scaled weights
+// of the second kernel are rounded where a scale is below 2^-12 of its row's largest.
 using namespace tc;
 
 // A block of tokens as the kernels keep it ("image"), for NT tokens: fp16 [2][NT][64],
@@ -529,8 +530,9 @@ using namespace tc;
 //  * More: the power of two is the token's, for all columns.  Behind the images of
 //    all tokens lies int [tokens][APART], in the first the exponent e: |x| < 2^e, kept as
 //    x 2^(15 - e) (every block's maximum for a token goes there: thousands that
-//    met in a line took 4 us for 32 tokens of the 70B feed-forward).  For hidden activations int [chunks][tokens] behind that, those of each block of columns,
-//    with which they are written before the token's is known (see fit_kernel).
+//    met in a line took 4 us for 32 tokens of the 70B feed-forward).  For hidden
+//    activations int [chunks][tokens] behind that, those of each block of columns, with
+//    which they are written before the token's is known (see fit_kernel).
 constexpr int FEW = 8;  // tokens
 __host__ __device__ constexpr int image_bytes(int nt) { return nt * 256 + (nt <= FEW ? 128 : 0); }  // (copied to multiples of 128)
 constexpr int APART = 32;
@@ -902,8 +904,8 @@ __device__ __forceinline__ void finish_segment(const ProductParams& p, long long
 // registers.  What is left to count are the instructions that make operands of
 // codes.  A code in the low bits of an fp16 number is a subnormal, code * 2^-24, and four
 // bits higher code * 2^-20: a word's eight codes are four operand registers after one
-// shift, four masks and four multiply-adds, which take the offset of 8 off.  (Codes made into
-// bf16 take 11 instructions a word: 102 us for one token of the 70B feed-forward, for 72.
+// shift, four masks and four multiply-adds, which take the offset of 8 off.  (Codes made
+// into bf16 take 11 instructions a word: 102 us for one token of the 70B feed-forward, for 72.
 // The codes as they lie and the offset taken off as -8 times the columns' sum: 68 us, but
 // an infinity less an infinity, and sums short by some 2^-17 of 8 times the block's
 // largest element, as the unit aligns products by exponents that a subnormal does not
@@ -1367,12 +1369,12 @@ __global__ void __launch_bounds__(FINISH_TOKENS * 32) finish_kernel(const __grid
 
 // The hidden activations of a token, whose blocks of 128 columns finish_kernel has written
 // with powers of two of their own, brought to the token's: its largest is known when all
-// of them are written.  What it rounds are elements below 2^-28 of that, by 2^-39 of it.  (A bound
-// from the token's absolute sum and the largest scales needs no kernel, but lies as far
-// above the hidden activations as one scale lies above the others: with one group in either matrix 2^10
-// times the others, results were off by up to 0.016 for 0.0017.)
-// A block to 16 tokens of a block of columns, a thread to eight columns: 2 us of the pass for 32
-// tokens of the 70B feed-forward, 5 for 128.
+// of them are written.  What it rounds are elements below 2^-28 of that, by 2^-39 of it.
+// (A bound from the token's absolute sum and the largest scales needs no kernel, but lies
+// as far above the hidden activations as one scale lies above the others: with one
+// group in either matrix 2^10 times the others, results were off by up to 0.016 for 0.0017.)
+// A block to 16 tokens of a block of columns, a thread to eight columns: 2 us of the
+// pass for 32 tokens of the 70B feed-forward, 5 for 128.
 constexpr int FIT_TOKENS = 16;
 __global__ void __launch_bounds__(FIT_TOKENS * 16) fit_kernel(const __grid_constant__ ProductParams p) {
   grid_dep_launch();
